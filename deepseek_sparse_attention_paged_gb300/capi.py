@@ -29,11 +29,13 @@ DSA_DEVERR_PAGE_RANGE = 0x2
 DSA_DEVERR_INDEX_RANGE = 0x4
 DSA_DEVERR_TIMEOUT = 0x8
 DSA_DEVERR_POSITION = 0x10
+DSA_DEVERR_PROB = 0x20
 DSA_Q_ROTATE = 0x1
 DSA_NORM_RMS = 0x2
 DSA_ROPE_INTERLEAVED = 0x4
 DSA_K_NO_ROTATE = 0x8
 DSA_SCALE_UE8M0 = 0x10
+DSA_CAUSAL = 0x40
 DSA_KEYS_CMP4 = 0x20          # the index cache holds compressed keys, one per 4 tokens
 PAGE_SIZE = 64
 INDEX_PAGE_BYTES = 64 * 132
@@ -108,6 +110,14 @@ def load(path: str = LIB_PATH):
                                                  P, P]),
         "dsa_sparse_mla_decode_fp8": (ctypes.c_int, [P, ctypes.c_float, P, ctypes.c_float, i64, P, i32, P, P, i32, P,
                                                      i32, i32, i32, ctypes.c_float, P, P, P, sz, P, P]),
+        "dsa_store_latent_prologue": (ctypes.c_int, [P, i64, P, ctypes.c_float, P, i64, P, P, i64, P, i64, P, i64, u32,
+                                                     P, P]),
+        "dsa_dense_mla_prefill": (ctypes.c_int, [P, i64, i64, P, i64, i64, P, i64, P, i64, i64, P, P, i32, i32, i32,
+                                                 i32, ctypes.c_float, u32, P, i64, i64, P, P, P]),
+        "dsa_dense_mla_decode_workspace_size": (sz, [i32, i32]),
+        "dsa_dense_mla_decode": (ctypes.c_int, [P, P, i64, P, i32, P, P, i32, i32, i32, ctypes.c_float, P, P, P, sz,
+                                                P, P]),
+        "dsa_verify_drafts": (ctypes.c_int, [P, i64, P, i64, i32, P, P, i32, i32, P, P, P, P, P, P]),
     }
     for name, (res, args) in sigs.items():
         fn = getattr(lib, name)
@@ -571,6 +581,171 @@ def dsa_sparse_mla_decode_noalloc(q_bf16: torch.Tensor, kv_pool: torch.Tensor, b
         _ptr(cu_q), B, _ptr(idx), idx.shape[1], T, H, float(scale), _ptr(out), _ptr(lse), _ptr(dev_err),
         _stream(stream)))
     _count(2 if T > 0 else 0)
+
+
+def _one_device(**tensors) -> None:
+    """The tensors of a call live on one device, the current one (whose stream it is enqueued on)."""
+    for name, t in tensors.items():
+        if t is not None:
+            _need(t.is_cuda and t.device.index == torch.cuda.current_device(),
+                  f"{name} must be on the current CUDA device")
+
+
+def _err_word(dev_err: Optional[torch.Tensor]) -> None:
+    if dev_err is not None:
+        _cuda(dev_err, torch.int32, "dev_err")
+        _need(dev_err.numel() >= 1, "dev_err must hold one int32")
+
+
+def dsa_store_latent_prologue(kv_a: torch.Tensor, norm_weight: torch.Tensor, eps: float, cos_sin_cache: torch.Tensor,
+                              positions: torch.Tensor, slot_mapping: torch.Tensor, kv_pool: torch.Tensor,
+                              latent_out: Optional[torch.Tensor] = None, flags: int = 0,
+                              dev_err: Optional[torch.Tensor] = None, stream=None) -> None:
+    """RMSNorm of the 512 latent dims and rotary embedding of the 64 rope dims of kv_a [n, 576] (rows may
+    be strided), stored by slot into the bf16 latent cache; also written to latent_out [n, 576]."""
+    lib = load()
+    _rows(kv_a, torch.bfloat16, "kv_a")
+    _cuda(norm_weight, torch.float32, "norm_weight")
+    _cuda(cos_sin_cache, torch.float32, "cos_sin_cache")
+    _cuda(positions, torch.int64, "positions")
+    _cuda(slot_mapping, torch.int64, "slot_mapping")
+    _cuda(kv_pool, torch.bfloat16, "kv_pool")
+    _err_word(dev_err)
+    _one_device(kv_a=kv_a, norm_weight=norm_weight, cos_sin_cache=cos_sin_cache, positions=positions,
+                slot_mapping=slot_mapping, kv_pool=kv_pool, latent_out=latent_out, dev_err=dev_err)
+    n = kv_a.shape[0]
+    _need(kv_a.shape[1] == LATENT_DIM, "kv_a must be [n, 576]")
+    _need(norm_weight.numel() == VALUE_DIM, "norm_weight must have 512 entries")
+    _need(cos_sin_cache.dim() == 2 and cos_sin_cache.shape[1] == 64, "cos_sin_cache must be [max_position, 64]")
+    _need(positions.numel() == n and slot_mapping.numel() == n, "positions / slot_mapping must have n entries")
+    _need(kv_pool.dim() == 3 and tuple(kv_pool.shape[1:]) == (64, LATENT_DIM), "kv_pool must be [pages, 64, 576]")
+    if latent_out is not None:
+        _rows(latent_out, torch.bfloat16, "latent_out")
+        _need(tuple(latent_out.shape) == (n, LATENT_DIM), "latent_out must be [n, 576]")
+    _check("dsa_store_latent_prologue", lib.dsa_store_latent_prologue(
+        _ptr(kv_a), _row_stride(kv_a), _ptr(norm_weight), float(eps), _ptr(cos_sin_cache), cos_sin_cache.shape[0],
+        _ptr(positions), _ptr(slot_mapping), n, _ptr(kv_pool), kv_pool.shape[0], _ptr(latent_out),
+        LATENT_DIM if latent_out is None else _row_stride(latent_out), int(flags), _ptr(dev_err), _stream(stream)))
+    _count(1 if n > 0 else 0)
+
+
+def _row_stride(t: torch.Tensor) -> int:
+    """Row stride in elements; a single row's stride is never used, so its width stands in for it."""
+    return t.stride(0) if t.shape[0] > 1 else t.shape[-1]
+
+
+def _th_strides(t: torch.Tensor, inner: int, name: str):
+    """(row stride, head stride) of a [rows, H, inner] bf16 CUDA view whose last dim is dense; the stride
+    of an axis of length 1 is never used and a dense one stands in for it."""
+    _need(t.is_cuda and t.dtype == torch.bfloat16, f"{name} must be a bf16 CUDA tensor")
+    _need(t.dim() == 3 and t.shape[2] == inner and t.stride(2) == 1, f"{name} must be [rows, H, {inner}], last dim dense")
+    head = t.stride(1) if t.shape[1] > 1 else inner
+    return (t.stride(0) if t.shape[0] > 1 else max(inner, head * t.shape[1])), head
+
+
+def dsa_dense_mla_prefill(q: torch.Tensor, k_nope: torch.Tensor, k_pe: torch.Tensor, v: torch.Tensor,
+                          cu_q: torch.Tensor, cu_k: torch.Tensor, scale: float, out: torch.Tensor,
+                          lse: Optional[torch.Tensor] = None, causal: bool = True,
+                          dev_err: Optional[torch.Tensor] = None, stream=None) -> None:
+    """Expanded latent attention of ragged prompts: q [T, H, 192], k_nope / v [S, H, 128], k_pe [S, 64]
+    (all may be strided views, e.g. of one [S, H, 256] up-projection), out [T, H, 128], lse [T, H]."""
+    lib = load()
+    qs = _th_strides(q, 192, "q")
+    ks = _th_strides(k_nope, 128, "k_nope")
+    vs = _th_strides(v, 128, "v")
+    os_ = _th_strides(out, 128, "out")
+    _rows(k_pe, torch.bfloat16, "k_pe")
+    _cuda(cu_q, torch.int32, "cu_q")
+    _cuda(cu_k, torch.int32, "cu_k")
+    T, H = q.shape[0], q.shape[1]
+    S, B = k_nope.shape[0], cu_q.numel() - 1
+    _need(B >= 0 and cu_k.numel() == B + 1, "cu_q and cu_k must have B + 1 entries")
+    _need(k_nope.shape[1] == H and tuple(v.shape[:2]) == (S, H), "k_nope and v must be [S, H, 128]")
+    _need(tuple(k_pe.shape) == (S, 64), "k_pe must be [S, 64]")
+    _need(tuple(out.shape[:2]) == (T, H), "out must be [T, H, 128]")
+    if lse is not None:
+        _cuda(lse, torch.float32, "lse")
+        _need(tuple(lse.shape) == (T, H), "lse must be [T, H]")
+    _err_word(dev_err)
+    _one_device(q=q, k_nope=k_nope, k_pe=k_pe, v=v, cu_q=cu_q, cu_k=cu_k, out=out, lse=lse, dev_err=dev_err)
+    _check("dsa_dense_mla_prefill", lib.dsa_dense_mla_prefill(
+        _ptr(q), *qs, _ptr(k_nope), *ks, _ptr(k_pe), _row_stride(k_pe), _ptr(v), *vs, _ptr(cu_q), _ptr(cu_k), B, T, S,
+        H, float(scale), DSA_CAUSAL if causal else 0, _ptr(out), *os_, _ptr(lse), _ptr(dev_err), _stream(stream)))
+    _count(1 if T > 0 and B > 0 and H > 0 else 0)
+
+
+def dsa_dense_mla_decode_workspace_size(T: int, H: int) -> int:
+    return int(load().dsa_dense_mla_decode_workspace_size(int(T), int(H)))
+
+
+def dsa_dense_mla_decode(q_bf16: torch.Tensor, kv_pool: torch.Tensor, block_table: torch.Tensor,
+                         seq_lens: torch.Tensor, cu_q: torch.Tensor, scale: float, out: torch.Tensor,
+                         workspace: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None,
+                         dev_err: Optional[torch.Tensor] = None, stream=None) -> None:
+    """Absorbed latent attention of the query rows over every visible row of the paged cache.  `workspace`
+    holds at least dsa_dense_mla_decode_workspace_size(T, H) bytes; when it is None a buffer of that size
+    is taken from torch's allocator for this call."""
+    lib = load()
+    _cuda(q_bf16, torch.bfloat16, "q_bf16")
+    _cuda(kv_pool, torch.bfloat16, "kv_pool")
+    _cuda(block_table, torch.int32, "block_table")
+    _cuda(seq_lens, torch.int32, "seq_lens")
+    _cuda(cu_q, torch.int32, "cu_q")
+    _cuda(out, torch.bfloat16, "out")
+    _need(q_bf16.dim() == 3 and q_bf16.shape[2] == LATENT_DIM, "q_bf16 must be [T, H, 576]")
+    T, H, _ = q_bf16.shape
+    B = seq_lens.numel()
+    _need(kv_pool.dim() == 3 and tuple(kv_pool.shape[1:]) == (64, LATENT_DIM), "kv_pool must be [pages, 64, 576]")
+    _need(cu_q.numel() == B + 1 and block_table.dim() == 2 and block_table.shape[0] == B, "metadata shapes")
+    _need(tuple(out.shape) == (T, H, VALUE_DIM), "out must be [T, H, 512]")
+    if lse is not None:
+        _cuda(lse, torch.float32, "lse")
+        _need(tuple(lse.shape) == (T, H), "lse must be [T, H]")
+    if workspace is None:
+        _need(stream is None, "a call on an explicit stream brings its own workspace")
+        workspace = torch.empty(max(16, dsa_dense_mla_decode_workspace_size(T, H)), dtype=torch.uint8,
+                                device=q_bf16.device)
+    _need(workspace.is_cuda and workspace.is_contiguous(), "workspace must be a contiguous CUDA tensor")
+    _err_word(dev_err)
+    _one_device(q_bf16=q_bf16, kv_pool=kv_pool, block_table=block_table, seq_lens=seq_lens, cu_q=cu_q, out=out,
+                lse=lse, workspace=workspace, dev_err=dev_err)
+    _check("dsa_dense_mla_decode", lib.dsa_dense_mla_decode(
+        _ptr(q_bf16), _ptr(kv_pool), kv_pool.shape[0], _ptr(block_table), block_table.shape[1], _ptr(seq_lens),
+        _ptr(cu_q), B, T, H, float(scale), _ptr(out), _ptr(lse), _ptr(workspace),
+        workspace.numel() * workspace.element_size(), _ptr(dev_err), _stream(stream)))
+    _count((1 + (1 if dsa_dense_mla_decode_workspace_size(T, H) > 0 else 0)) if T > 0 and B > 0 else 0)
+
+
+def dsa_verify_drafts(target_probs: torch.Tensor, draft_tokens: torch.Tensor, cu_q: torch.Tensor,
+                      accept_u: torch.Tensor, sample_u: torch.Tensor, out_tokens: torch.Tensor,
+                      accepted: torch.Tensor, draft_probs: Optional[torch.Tensor] = None,
+                      dev_err: Optional[torch.Tensor] = None, stream=None) -> None:
+    """Accepts drafted tokens against target_probs [T, V] and draws the token after the last accepted one
+    (from max(p - q, 0) after a rejection); draft_probs None: certain (greedy) drafts."""
+    lib = load()
+    _rows(target_probs, torch.float32, "target_probs")
+    _cuda(draft_tokens, torch.int32, "draft_tokens")
+    _cuda(cu_q, torch.int32, "cu_q")
+    _cuda(accept_u, torch.float32, "accept_u")
+    _cuda(sample_u, torch.float32, "sample_u")
+    _cuda(out_tokens, torch.int32, "out_tokens")
+    _cuda(accepted, torch.int32, "accepted")
+    T, V = target_probs.shape
+    B = cu_q.numel() - 1
+    _need(B >= 0 and sample_u.numel() == B and accepted.numel() == B, "cu_q [B + 1], sample_u [B], accepted [B]")
+    _need(draft_tokens.numel() == T and accept_u.numel() == T and out_tokens.numel() == T,
+          "draft_tokens, accept_u and out_tokens must have T entries")
+    if draft_probs is not None:
+        _rows(draft_probs, torch.float32, "draft_probs")
+        _need(tuple(draft_probs.shape) == (T, V), "draft_probs must be [T, V]")
+    _err_word(dev_err)
+    _one_device(target_probs=target_probs, draft_probs=draft_probs, draft_tokens=draft_tokens, cu_q=cu_q,
+                accept_u=accept_u, sample_u=sample_u, out_tokens=out_tokens, accepted=accepted, dev_err=dev_err)
+    _check("dsa_verify_drafts", lib.dsa_verify_drafts(
+        _ptr(target_probs), _row_stride(target_probs), _ptr(draft_probs),
+        0 if draft_probs is None else _row_stride(draft_probs), V, _ptr(draft_tokens), _ptr(cu_q), B, T,
+        _ptr(accept_u), _ptr(sample_u), _ptr(out_tokens), _ptr(accepted), _ptr(dev_err), _stream(stream)))
+    _count(1 if B > 0 else 0)
 
 
 def dsa_selftest_wait_timeout(dev_err: torch.Tensor, cycles: int, stream=None) -> None:

@@ -1,0 +1,149 @@
+// store_latent.cu -- latent prologue and paged store: RMSNorm of the 512 latent dims, rotary
+// embedding of the 64 rope dims, one bf16 row of 576 written into the paged latent cache (and,
+// optionally, into a dense array the key / value up-projection and the prompt attention read).
+//
+// Follows vllm mla/common.py, MLACommonImpl.forward (concat_and_cache_mla(k_c_normed, k_pe,
+// kv_cache, slot_mapping)) with the kv_a_layernorm and rotary embedding that precede it.
+//
+// Mathematics, per token: rstd = 1 / sqrt(sum x_d^2 / 512 + eps); y_d = bf16((x_d rstd) w_d) for
+// d < 512; rope pairs a' = bf16(a c - b s), b' = bf16(b c + a s).  The sum of squares and the
+// statistics are fp32; the only rounding to bf16 is the output's.
+//
+// One warp per token: lane l holds dims 8 l .. 8 l + 7 and 256 + 8 l .. 256 + 8 l + 7 (two 16-byte
+// loads) and rope dims 2 l, 2 l + 1, so the norm is one warp reduction and nothing passes through
+// shared memory.  HBM-bound: 1152 bytes read, 256 of the cos/sin table, 1152 or 2304 written.
+#include <cuda_bf16.h>
+
+#include "dsa_common.cuh"
+
+namespace dsa {
+namespace {
+
+constexpr int kStoreThreads = 256;
+
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+    const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&v);
+}
+
+__device__ __forceinline__ void unpack8(const uint4& r, float (&x)[8]) {
+    const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        x[2 * i] = bf16_lo(w[i]);
+        x[2 * i + 1] = bf16_hi(w[i]);
+    }
+}
+
+// raw and latent_out may be the same array: a warp reads its whole row before it writes it.
+__global__ void __launch_bounds__(kStoreThreads)
+store_latent_prologue_kernel(const uint16_t* raw, int64_t raw_stride, const float* __restrict__ weight, float eps,
+                             const float* __restrict__ cos_sin, int64_t max_position,
+                             const int64_t* __restrict__ positions, const int64_t* __restrict__ slots, int64_t n,
+                             uint16_t* __restrict__ pool, int64_t num_pages, uint16_t* latent_out,
+                             int64_t out_stride, int interleaved, int32_t* err) {
+    const int64_t token = (static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x) >> 5;
+    const int lane = threadIdx.x & 31;
+    if (token >= n) return;                      // warp-uniform
+    // every load that does not depend on another is in flight before anything is examined
+    const int64_t slot = __ldg(slots + token);
+    const int64_t pos = __ldg(positions + token);
+    const uint16_t* row = raw + token * raw_stride;
+    const uint4 r0 = *reinterpret_cast<const uint4*>(row + 8 * lane);
+    const uint4 r1 = *reinterpret_cast<const uint4*>(row + 256 + 8 * lane);
+    const uint32_t rr = *reinterpret_cast<const uint32_t*>(row + kValueDim + 2 * lane);
+    if (pos < 0 || pos >= max_position) {
+        if (lane == 0 && (slot >= 0 || latent_out != nullptr)) raise_error(err, DSA_DEVERR_POSITION);
+        return;
+    }
+    const float* cs = cos_sin + pos * 64;
+    const int i0 = interleaved ? lane : 2 * (lane & 15);
+    const float c0 = __ldg(cs + i0), s0 = __ldg(cs + 32 + i0);
+    const float c1 = interleaved ? 0.0f : __ldg(cs + i0 + 1);
+    const float s1 = interleaved ? 0.0f : __ldg(cs + 32 + i0 + 1);
+    float x[16];
+    {
+        float a[8];
+        unpack8(r0, a);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[i] = a[i];
+        unpack8(r1, a);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[8 + i] = a[i];
+    }
+    float ss = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) ss = fmaf(x[i], x[i], ss);
+    ss = warp_sum(ss);
+    const float rstd = __fdiv_rn(1.0f, __fsqrt_rn(__fadd_rn(__fmul_rn(ss, 1.0f / kValueDim), eps)));
+    uint4 y[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        const float4 wa = __ldg(reinterpret_cast<const float4*>(weight + 256 * h + 8 * lane));
+        const float4 wb = __ldg(reinterpret_cast<const float4*>(weight + 256 * h + 8 * lane + 4));
+        const float* v = x + 8 * h;
+        y[h] = make_uint4(pack2(v[0] * rstd * wa.x, v[1] * rstd * wa.y), pack2(v[2] * rstd * wa.z, v[3] * rstd * wa.w),
+                          pack2(v[4] * rstd * wb.x, v[5] * rstd * wb.y), pack2(v[6] * rstd * wb.z, v[7] * rstd * wb.w));
+    }
+    const float a = bf16_lo(rr), b = bf16_hi(rr);
+    float ya, yb;
+    if (interleaved) {                           // the lane's two dims are one pair
+        ya = __fsub_rn(__fmul_rn(a, c0), __fmul_rn(b, s0));
+        yb = __fadd_rn(__fmul_rn(b, c0), __fmul_rn(a, s0));
+    } else {                                     // dim i of lane l < 16 pairs with dim i + 32 of lane l + 16
+        const float oa = __shfl_xor_sync(0xffffffffu, a, 16);
+        const float ob = __shfl_xor_sync(0xffffffffu, b, 16);
+        if (lane < 16) {
+            ya = __fsub_rn(__fmul_rn(a, c0), __fmul_rn(oa, s0));
+            yb = __fsub_rn(__fmul_rn(b, c1), __fmul_rn(ob, s1));
+        } else {
+            ya = __fadd_rn(__fmul_rn(a, c0), __fmul_rn(oa, s0));
+            yb = __fadd_rn(__fmul_rn(b, c1), __fmul_rn(ob, s1));
+        }
+    }
+    const uint32_t yr = pack2(ya, yb);
+    auto put = [&](uint16_t* dst) {
+        *reinterpret_cast<uint4*>(dst + 8 * lane) = y[0];
+        *reinterpret_cast<uint4*>(dst + 256 + 8 * lane) = y[1];
+        *reinterpret_cast<uint32_t*>(dst + kValueDim + 2 * lane) = yr;
+    };
+    if (latent_out != nullptr) put(latent_out + token * out_stride);
+    if (slot < 0) return;                        // padding token: not cached
+    if ((slot >> 6) >= num_pages) {
+        if (lane == 0) raise_error(err, DSA_DEVERR_SLOT_RANGE);
+        return;
+    }
+    put(pool + slot * kLatentDim);
+}
+
+}  // namespace
+}  // namespace dsa
+
+extern "C" dsa_status dsa_store_latent_prologue(const void* kv_a_bf16, int64_t row_stride, const float* norm_weight,
+                                                float eps, const float* cos_sin_cache, int64_t max_position,
+                                                const int64_t* positions, const int64_t* slot_mapping, int64_t n,
+                                                void* kv_pool, int64_t num_pages, void* latent_out,
+                                                int64_t out_row_stride, uint32_t flags, int32_t* dev_err,
+                                                void* stream) {
+    using namespace dsa;
+    if (n < 0 || num_pages < 0 || max_position < 0) return DSA_ERR_INVALID_ARG;
+    if (flags & ~static_cast<uint32_t>(DSA_ROPE_INTERLEAVED)) return DSA_ERR_INVALID_ARG;
+    if (!(eps >= 0.0f)) return DSA_ERR_INVALID_ARG;
+    if (n == 0) return DSA_OK;
+    if (!kv_a_bf16 || !norm_weight || !cos_sin_cache || !positions || !slot_mapping || !kv_pool)
+        return DSA_ERR_INVALID_ARG;
+    if (!aligned16(kv_a_bf16) || !aligned16(norm_weight) || !aligned16(kv_pool) ||
+        (latent_out != nullptr && !aligned16(latent_out)))
+        return DSA_ERR_INVALID_ARG;
+    if (row_stride < kLatentDim || row_stride % 8 != 0) return DSA_ERR_INVALID_ARG;
+    if (latent_out != nullptr && (out_row_stride < kLatentDim || out_row_stride % 8 != 0)) return DSA_ERR_INVALID_ARG;
+    if (num_pages > 0x7fffffffffffLL / (kPage * kLatentDim)) return DSA_ERR_UNSUPPORTED;
+    const int64_t blocks = (n + kStoreThreads / 32 - 1) / (kStoreThreads / 32);
+    if (blocks > 0x7fffffffLL) return DSA_ERR_INVALID_ARG;
+    store_latent_prologue_kernel<<<static_cast<unsigned>(blocks), kStoreThreads, 0,
+                                   static_cast<cudaStream_t>(stream)>>>(
+        static_cast<const uint16_t*>(kv_a_bf16), row_stride, norm_weight, eps, cos_sin_cache, max_position, positions,
+        slot_mapping, n, static_cast<uint16_t*>(kv_pool), num_pages, static_cast<uint16_t*>(latent_out),
+        out_row_stride, (flags & DSA_ROPE_INTERLEAVED) ? 1 : 0, dev_err);
+    return launch_status();
+}

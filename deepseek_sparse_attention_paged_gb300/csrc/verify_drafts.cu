@@ -1,0 +1,329 @@
+// verify_drafts.cu -- acceptance of drafted tokens against the target's probabilities, and the draw
+// of the token that follows the last accepted one, from given random numbers.
+//
+// Mathematics (rejection sampling of speculative decoding; Leviathan et al. 2023): row j of a
+// request holds the target distribution p after its j-th token, x_j the token drafted there and q
+// the draft's distribution.  x_j is accepted while u_j q(x_j) < p(x_j); at the first row where it is
+// not, the next token is drawn from w = max(p - q, 0) (after the last draft: w = p) by inverting its
+// cumulative sum: the least v with sum_{i <= v} w_i > u_s sum_i w_i.
+//
+// Sums: the drawn token must not depend on how the sum is split, so sums are carried in about 48
+// bits: a thread adds its 16 values of a group of 512 as fp32 pairs (high word, error word) -- the
+// difference p - q included, exactly -- and group sums are added in fp64.  fp64 throughout would
+// be bound by the fp64 unit (two conversions, a subtraction and an addition per entry), the pairs
+// keep it on HBM.  Adding in fp32 would move the borders by about 2^-24 of the sum each.
+//
+// One cluster of 8 CTAs per request, each with an eighth of the vocabulary: only the one row of p
+// and of q that the draw needs is read, once, with all group sums kept in shared memory; the CTAs
+// swap their totals through distributed shared memory, and the CTA whose range holds the border
+// re-reads one group of 512 entries.
+#include "dsa_common.cuh"
+
+namespace dsa {
+namespace {
+
+constexpr int kVerifyThreads = 256;
+constexpr int kVerifyWarps = kVerifyThreads / 32;
+constexpr int kVerifyCtas = 8;                 // cluster size: CTAs per request
+constexpr int kGroup = 512;                    // entries per recorded sum: 4 steps x 32 lanes x 4
+constexpr int kMaxVocab = 1 << 24;
+
+__device__ __forceinline__ uint32_t cluster_rank() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+
+// The two halves of a cluster barrier: what comes between needs no peer.
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+// Store a double at the same shared-memory offset in CTA `rank` of the cluster.
+__device__ __forceinline__ void store_remote(double* p, uint32_t rank, double v) {
+    uint32_t a;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;"
+                 : "=r"(a) : "r"(static_cast<uint32_t>(__cvta_generic_to_shared(p))), "r"(rank));
+    asm volatile("st.shared::cluster.f64 [%0], %1;" ::"r"(a), "d"(v) : "memory");
+}
+
+// How the row's weights are formed from p and q.
+enum Mode { kPlain = 0, kResidual = 1, kWithout = 2 };   // w = p; w = max(p - q, 0); w = p with entry x zeroed
+
+// An entry counts when it is positive and finite.
+__device__ __forceinline__ double weight_of(float p, float q) {
+    const double w = static_cast<double>(p) - static_cast<double>(q);
+    return (w > 0.0 && w < static_cast<double>(INFINITY)) ? w : 0.0;
+}
+
+// Four consecutive entries v .. v + 3 of the row (entries past V are 0); for kWithout q = p at x.
+template <bool VEC>
+__device__ __forceinline__ void load4(const float* __restrict__ p_row, const float* __restrict__ q_row, int mode, int x,
+                                      int v, int V, float (&p)[4], float (&q)[4]) {
+    if (VEC && v + 4 <= V) {
+        const float4 a = __ldg(reinterpret_cast<const float4*>(p_row + v));
+        p[0] = a.x; p[1] = a.y; p[2] = a.z; p[3] = a.w;
+        if (mode == kResidual) {
+            const float4 b = __ldg(reinterpret_cast<const float4*>(q_row + v));
+            q[0] = b.x; q[1] = b.y; q[2] = b.z; q[3] = b.w;
+        } else {
+            q[0] = q[1] = q[2] = q[3] = 0.0f;
+        }
+    } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            p[e] = v + e < V ? __ldg(p_row + v + e) : 0.0f;
+            q[e] = (mode == kResidual && v + e < V) ? __ldg(q_row + v + e) : 0.0f;
+        }
+    }
+    if (mode == kWithout) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            if (v + e == x) p[e] = 0.0f;
+    }
+}
+
+// (hi, lo) += max(p - q, 0), the difference exact (two_sum_err), the sum to about 48 bits.
+__device__ __forceinline__ void add_pair(float& hi, float& lo, float p, float q) {
+    const float d = __fsub_rn(p, q);
+    const float de = two_sum_err(p, -q, d);
+    if (d > 0.0f && d < INFINITY) {              // NaN and infinite entries count as 0
+        const float s = __fadd_rn(hi, d);
+        lo = __fadd_rn(lo, __fadd_rn(two_sum_err(hi, d, s), de));
+        hi = s;
+    }
+}
+
+__device__ __forceinline__ double shfl_up_f64(double v, int d) { return __shfl_up_sync(0xffffffffu, v, d); }
+
+template <bool VEC>
+__global__ void __launch_bounds__(kVerifyThreads) __cluster_dims__(kVerifyCtas, 1, 1)
+verify_drafts_kernel(const float* __restrict__ target, int64_t ld_t, const float* __restrict__ draft, int64_t ld_d,
+                     int V, const int32_t* __restrict__ tokens, const int32_t* __restrict__ cu_q, int T,
+                     const float* __restrict__ u_accept, const float* __restrict__ u_sample,
+                     int32_t* __restrict__ out_tokens, int32_t* __restrict__ accepted, int32_t* err) {
+    extern __shared__ double group_sum[];        // [groups of this CTA]: sums, then inclusive prefix sums
+    __shared__ double totals[kVerifyCtas];
+    __shared__ int s_first, s_x;
+    const int b = blockIdx.x / kVerifyCtas;
+    const int rank = static_cast<int>(cluster_rank());
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int r0 = max(0, min(T, __ldg(cu_q + b)));
+    const int r1 = max(r0, min(T, __ldg(cu_q + b + 1)));
+    const int n_draft = r1 - r0 - 1;
+    if (rank == 0 && threadIdx.x == 0 && (r0 != __ldg(cu_q + b) || r1 != __ldg(cu_q + b + 1)))
+        raise_error(err, DSA_DEVERR_INDEX_RANGE);
+    if (n_draft < 0) {                           // no row: nothing to verify (uniform over the cluster)
+        if (rank == 0 && threadIdx.x == 0) accepted[b] = 0;
+        return;
+    }
+    cluster_arrive();                            // every CTA runs before any writes into its shared memory
+    // ---- acceptance: the first row whose draft is missing or rejected (every CTA finds it for itself)
+    if (warp == 0) {
+        int first = n_draft, x_first = -1;
+        for (int j0 = 0; j0 < n_draft; j0 += 32) {
+            const int j = j0 + lane;
+            bool stop = false;
+            int x = -1;
+            if (j < n_draft) {
+                x = __ldg(tokens + r0 + j);
+                if (x >= V) {
+                    if (rank == 0) raise_error(err, DSA_DEVERR_INDEX_RANGE);
+                    x = -1;
+                }
+                stop = true;
+                if (x >= 0) {
+                    const float p = __ldg(target + static_cast<int64_t>(r0 + j) * ld_t + x);
+                    const float q = draft != nullptr ? __ldg(draft + static_cast<int64_t>(r0 + j) * ld_d + x) : 1.0f;
+                    // 24 x 24 bits: the product is exact
+                    stop = !(static_cast<double>(__ldg(u_accept + r0 + j)) * static_cast<double>(q) <
+                             static_cast<double>(p));
+                }
+            }
+            const uint32_t m = __ballot_sync(0xffffffffu, stop);
+            if (m != 0u) {
+                first = j0 + __ffs(m) - 1;
+                x_first = __shfl_sync(0xffffffffu, x, __ffs(m) - 1);
+                break;
+            }
+        }
+        if (lane == 0) {
+            s_first = first;
+            s_x = x_first;
+        }
+    }
+    __syncthreads();
+    const int first = s_first, x = s_x;
+    if (rank == 0) {
+        for (int j = threadIdx.x; j < r1 - r0; j += kVerifyThreads)
+            if (j != first) out_tokens[r0 + j] = j < first ? __ldg(tokens + r0 + j) : -1;
+        if (threadIdx.x == 0) accepted[b] = first;
+    }
+    // ---- the draw
+    const float* p_row = target + static_cast<int64_t>(r0 + first) * ld_t;
+    const float* q_row = draft != nullptr ? draft + static_cast<int64_t>(r0 + first) * ld_d : nullptr;
+    const int groups_all = (V + kGroup - 1) / kGroup;
+    const int per_cta = (groups_all + kVerifyCtas - 1) / kVerifyCtas;
+    const int g_begin = min(groups_all, rank * per_cta), g_end = min(groups_all, g_begin + per_cta);
+    const int ng = g_end - g_begin;
+    int mode = x < 0 ? kPlain : (q_row != nullptr ? kResidual : kWithout);
+    double base = 0.0, all = 0.0;
+    bool peers_run = false;
+    int owner = -1;
+    const double u = static_cast<double>(__ldg(u_sample + b));
+    for (;;) {
+        for (int g = warp; g < ng; g += kVerifyWarps) {
+            float hi = 0.0f, lo = 0.0f;
+            float p[4][4], q[4][4];
+            const int v0 = (g_begin + g) * kGroup + lane * 4;
+#pragma unroll
+            for (int s = 0; s < 4; ++s) load4<VEC>(p_row, q_row, mode, x, v0 + s * 128, V, p[s], q[s]);
+#pragma unroll
+            for (int s = 0; s < 4; ++s)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) add_pair(hi, lo, p[s][e], q[s][e]);
+            double sum = static_cast<double>(hi) + static_cast<double>(lo);
+#pragma unroll
+            for (int m = 16; m > 0; m >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, m);
+            if (lane == 0) group_sum[g] = sum;
+        }
+        __syncthreads();
+        if (!peers_run) {
+            __syncwarp();
+            cluster_wait();
+            peers_run = true;
+        }
+        if (warp == 0) {                         // inclusive prefix sums of this CTA's groups
+            double carry = 0.0;
+            for (int g0 = 0; g0 < ng; g0 += 32) {
+                double v = g0 + lane < ng ? group_sum[g0 + lane] : 0.0;
+#pragma unroll
+                for (int d = 1; d < 32; d <<= 1) {
+                    const double o = shfl_up_f64(v, d);
+                    if (lane >= d) v += o;
+                }
+                v += carry;
+                if (g0 + lane < ng) group_sum[g0 + lane] = v;
+                carry = __shfl_sync(0xffffffffu, v, 31);
+            }
+            if (lane < kVerifyCtas) store_remote(&totals[rank], lane, carry);
+        }
+        cluster_sync();
+        // the same sums in the same order in every CTA: base of this CTA, total, owner of the border
+        all = 0.0;
+        for (int c = 0; c < kVerifyCtas; ++c) {
+            if (c == rank) base = all;
+            all += totals[c];
+        }
+        const double t = u * all;
+        double run = 0.0;
+        owner = -1;
+        int last = -1;
+        for (int c = 0; c < kVerifyCtas; ++c) {
+            run += totals[c];
+            if (totals[c] > 0.0) last = c;
+            if (owner < 0 && totals[c] > 0.0 && run > t) owner = c;
+        }
+        if (owner < 0) owner = last;             // u outside [0, 1): the last entry with mass
+        cluster_sync();                          // totals read by every CTA before they may be written again
+        if (all > 0.0 || mode == kPlain) break;
+        mode = kPlain;                           // p <= q everywhere: draw from p itself
+    }
+    if (owner < 0) {                             // a row without mass
+        if (rank == 0 && threadIdx.x == 0) {
+            out_tokens[r0 + first] = -1;
+            raise_error(err, DSA_DEVERR_PROB);
+        }
+        return;
+    }
+    if (rank != owner || warp != 0) return;
+    const double t = u * all;
+    // the first group whose prefix passes t (the last with mass if none does)
+    int g_hit = -1, g_last = -1;
+    for (int g0 = 0; g0 < ng; g0 += 32) {
+        const int g = g0 + lane;
+        const double inc = g < ng ? group_sum[g] : 0.0;
+        const double exc = (g < ng && g > 0) ? group_sum[g - 1] : 0.0;
+        const bool mass = g < ng && inc > exc;
+        const uint32_t hit = __ballot_sync(0xffffffffu, mass && base + inc > t);
+        const uint32_t any = __ballot_sync(0xffffffffu, mass);
+        if (any != 0u) g_last = g0 + 31 - __clz(any);
+        if (hit != 0u) {
+            g_hit = g0 + __ffs(hit) - 1;
+            break;
+        }
+    }
+    if (g_hit < 0) g_hit = g_last;
+    if (g_hit < 0) g_hit = 0;                    // unreachable: the owner has mass
+    double run = base + (g_hit > 0 ? group_sum[g_hit - 1] : 0.0);
+    const int v0 = (g_begin + g_hit) * kGroup + lane * 4;
+    float p[4][4], q[4][4];
+#pragma unroll
+    for (int s = 0; s < 4; ++s) load4<VEC>(p_row, q_row, mode, x, v0 + s * 128, V, p[s], q[s]);
+    int token = -1, last_pos = -1;
+#pragma unroll
+    for (int s = 0; s < 4; ++s) {
+        double w[4], pre = 0.0;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            w[e] = weight_of(p[s][e], q[s][e]);
+            pre += w[e];
+        }
+        double inc = pre;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const double o = shfl_up_f64(inc, d);
+            if (lane >= d) inc += o;
+        }
+        double at = run + (inc - pre);
+        int found = -1, pos = -1;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            at += w[e];
+            if (w[e] > 0.0) {
+                pos = v0 + s * 128 + e;
+                if (found < 0 && at > t) found = pos;
+            }
+        }
+        const uint32_t hit = __ballot_sync(0xffffffffu, found >= 0);
+        const uint32_t any = __ballot_sync(0xffffffffu, pos >= 0);
+        if (any != 0u) last_pos = __shfl_sync(0xffffffffu, pos, 31 - __clz(any));
+        if (hit != 0u && token < 0) token = __shfl_sync(0xffffffffu, found, __ffs(hit) - 1);
+        run += __shfl_sync(0xffffffffu, inc, 31);
+    }
+    if (token < 0) token = last_pos;             // the border lies within the rounding of the group's sum
+    if (lane == 0) out_tokens[r0 + first] = token;
+}
+
+}  // namespace
+}  // namespace dsa
+
+extern "C" dsa_status dsa_verify_drafts(const float* target_probs, int64_t target_ld, const float* draft_probs,
+                                        int64_t draft_ld, int32_t V, const int32_t* draft_tokens, const int32_t* cu_q,
+                                        int32_t B, int32_t T, const float* accept_u, const float* sample_u,
+                                        int32_t* out_tokens, int32_t* accepted, int32_t* dev_err, void* stream) {
+    using namespace dsa;
+    if (B < 0 || T < 0 || V < 1) return DSA_ERR_INVALID_ARG;
+    if (V > kMaxVocab || B > 0x7fffffff / kVerifyCtas) return DSA_ERR_UNSUPPORTED;
+    if (B == 0) return DSA_OK;
+    if (!cu_q || !accepted) return DSA_ERR_INVALID_ARG;
+    if (T > 0 && (!target_probs || !draft_tokens || !accept_u || !sample_u || !out_tokens)) return DSA_ERR_INVALID_ARG;
+    if (T > 0 && (target_ld < V || (draft_probs != nullptr && draft_ld < V))) return DSA_ERR_INVALID_ARG;
+    const bool vec = aligned16(target_probs) && target_ld % 4 == 0 &&
+                     (draft_probs == nullptr || (aligned16(draft_probs) && draft_ld % 4 == 0));
+    const int groups = (V + kGroup - 1) / kGroup;
+    const size_t smem = static_cast<size_t>((groups + kVerifyCtas - 1) / kVerifyCtas) * sizeof(double);   // <= 32 KB
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    const unsigned grid = static_cast<unsigned>(B) * kVerifyCtas;
+    if (vec)
+        verify_drafts_kernel<true><<<grid, kVerifyThreads, smem, s>>>(target_probs, target_ld, draft_probs, draft_ld, V,
+                                                                      draft_tokens, cu_q, T, accept_u, sample_u,
+                                                                      out_tokens, accepted, dev_err);
+    else
+        verify_drafts_kernel<false><<<grid, kVerifyThreads, smem, s>>>(target_probs, target_ld, draft_probs, draft_ld,
+                                                                       V, draft_tokens, cu_q, T, accept_u, sample_u,
+                                                                       out_tokens, accepted, dev_err);
+    return launch_status();
+}

@@ -14,6 +14,9 @@
  * Variants: the top-k with forced initial / local tokens, power-of-two (ue8m0) quantisation
  * scales, a one-call indexer that returns top-k indices, and a sparse MLA call that needs no
  * workspace.
+ * Dense latent attention (contexts and layers without a selection): the latent row's norm, rotary
+ * embedding and paged store, the prompt's attention in expanded form, the attention of new tokens
+ * over the whole paged cache in absorbed form, and the verification of drafted tokens.
  *
  * Conventions shared by every call
  * --------------------------------
@@ -74,6 +77,7 @@ typedef enum {
 #define DSA_DEVERR_INDEX_RANGE 0x4 /* a top-k index outside [0, v_r) (entry skipped) */
 #define DSA_DEVERR_TIMEOUT 0x8     /* a bounded spin-wait gave up */
 #define DSA_DEVERR_POSITION 0x10   /* a rotary position outside [0, max_position) */
+#define DSA_DEVERR_PROB 0x20       /* verify: a distribution without a positive finite entry */
 
 /* Flags of dsa_indexer_logits. */
 #define DSA_Q_ROTATE 0x1u          /* Hadamard-rotate each query head before quantising it */
@@ -93,6 +97,9 @@ typedef enum {
  * [4s, 4s + 4), visible once all four are); seq_lens stay the token counts, and max_seq_len bounds
  * the entries (>= every v_r / 4).  The top-k of dsa_lightning_indexer uses the same rule. */
 #define DSA_KEYS_CMP4 0x20u
+
+/* Flag of dsa_dense_mla_prefill: a query sees the keys up to its own position only. */
+#define DSA_CAUSAL 0x40u
 
 /* Fixed shape constants of the path. */
 #define DSA_PAGE_SIZE 64
@@ -549,6 +556,135 @@ dsa_status dsa_mla_absorb_q(const void* q_nope_bf16, int64_t q_row_stride, int64
 dsa_status dsa_mla_v_up(const void* o_lat_bf16, int64_t o_row_stride, int64_t o_head_stride,
                         const void* w_uv_bf16, int32_t T, int32_t H, void* out_bf16,
                         int64_t out_row_stride, int64_t out_head_stride, int32_t* dev_err, void* stream);
+
+/*
+ * dsa_store_latent_prologue -- norm and rotary embedding of the latent rows, written into the paged
+ * bf16 latent cache (the one dsa_sparse_mla_decode and dsa_dense_mla_decode read).
+ * Source: vllm mla/common.py, MLACommonImpl.forward: concat_and_cache_mla(k_c_normed, k_pe,
+ * kv_cache, slot_mapping), with the kv_a_layernorm and rotary embedding in front of it.
+ * Per token t, x = kv_a[t, 0:576]:
+ *   rstd = 1 / sqrt(sum_{d < 512} x_d^2 / 512 + eps);  y_d = bf16_rn(x_d rstd w_d), d < 512;
+ *   c, s = cos_sin_cache[positions[t], 0:32], [32:64]; neox pairs (a, b) = (x_{512+i}, x_{544+i})
+ *   (DSA_ROPE_INTERLEAVED: (x_{512+2i}, x_{513+2i})), i < 32: a' = bf16_rn(a c_i - b s_i),
+ *   b' = bf16_rn(b c_i + a s_i) in the same places of y.  Statistics in fp32.
+ *   y goes to row slot & 63 of page slot >> 6 (slot >= 0) and to latent_out[t] (if given).
+ * Arguments:
+ *   kv_a_bf16      row t at kv_a_bf16[t * row_stride]; 16-byte aligned, row_stride >= 576 elements
+ *                  and a multiple of 8 (e.g. the tail columns of a wider projection output).
+ *   norm_weight    fp32 [512] (16-byte aligned).   eps >= 0.
+ *   cos_sin_cache  fp32 [max_position, 64].   positions int64 [n].
+ *   slot_mapping   int64 [n]; slot < 0: a padding token, not cached (its latent_out row is written).
+ *                  Two tokens with the same slot: one of the two rows, unspecified which (a row may
+ *                  mix 16-byte pieces of both).
+ *   kv_pool        bf16 [num_pages, 64, 576] (16-byte aligned), written in place.
+ *   latent_out     nullable; row t at latent_out[t * out_row_stride], 16-byte aligned, stride >= 576
+ *                  and a multiple of 8.  May be kv_a_bf16 itself with the same stride.
+ *   flags          0 or DSA_ROPE_INTERLEAVED.
+ *   dev_err        nullable; DSA_DEVERR_POSITION for a position outside [0, max_position) (the token
+ *                  is skipped, latent_out included), DSA_DEVERR_SLOT_RANGE for a slot past the pool
+ *                  (not cached).
+ */
+dsa_status dsa_store_latent_prologue(const void* kv_a_bf16, int64_t row_stride, const float* norm_weight, float eps,
+                                     const float* cos_sin_cache, int64_t max_position, const int64_t* positions,
+                                     const int64_t* slot_mapping, int64_t n, void* kv_pool, int64_t num_pages,
+                                     void* latent_out, int64_t out_row_stride, uint32_t flags, int32_t* dev_err,
+                                     void* stream);
+
+/*
+ * dsa_dense_mla_prefill -- attention of ragged prompts in expanded form: per-head keys and values
+ * (the up-projected latent rows), one rope key per token shared by all heads.
+ * Source: vllm mla/common.py, MLACommonImpl._forward_prefill (kv_b_proj(c) split into k_nope and v,
+ * k = [k_nope, k_pe], causal attention over ragged requests) and _compute_prefill_context (the
+ * queries of a chunk over earlier keys, not causal; returns lse).
+ *   Request b has the query rows [cu_q[b], cu_q[b+1]) and the key rows [cu_k[b], cu_k[b+1]), nq and
+ *   nk of them.  Query i sees the request's first vis_i keys: nk, or with DSA_CAUSAL
+ *   nk - nq + i + 1 (the queries are the last nq tokens; <= 0: none).
+ *   S_ij = scale (<q_i[0:128], k_nope_j> + <q_i[128:192], k_pe_j>), j < vis_i; P = softmax(S);
+ *   out_i = bf16_rn(sum_j P_ij v_j);  lse_i = ln sum_j exp(S_ij).  vis_i = 0: out = 0, lse = -inf.
+ *   bf16 operands, fp32 accumulation, P rounded to bf16 for the product with v.
+ *   Query rows >= cu_q[B] are left as they were; key rows >= cu_k[B] are not used (they may hold
+ *   anything).  Within a request, an infinite or NaN value in v at a position that a query does not
+ *   see may reach that query when it lies in the same 128-key tile as one that it does see.
+ * Arguments:
+ *   q_bf16         element (t, h, d), d < 192, at q_bf16[t * q_row_stride + h * q_head_stride + d].
+ *   k_nope_bf16    [S, H, 128] with its strides; v_bf16 [S, H, 128] with its strides (both may be
+ *                  views of one [S, H, 256] up-projection output).
+ *   k_pe_bf16      [S, 64] with its row stride (e.g. the last 64 columns of 576-wide latent rows).
+ *   out_bf16       [T, H, 128] with its strides; must not overlap the inputs.
+ *                  All bases 16-byte aligned, all strides multiples of 8 elements.
+ *   cu_q, cu_k     int32 [B + 1] (device), ascending.   T, S: rows of q / out and of the keys.
+ *   H              >= 1.   scale > 0, finite.   flags: 0 or DSA_CAUSAL.
+ *   lse            fp32 [T, H], nullable.
+ *   dev_err        nullable; DSA_DEVERR_INDEX_RANGE for a cu_q / cu_k range outside [0, T] / [0, S]
+ *                  (cut to it), DSA_DEVERR_TIMEOUT if a bounded wait gave up.
+ */
+dsa_status dsa_dense_mla_prefill(const void* q_bf16, int64_t q_row_stride, int64_t q_head_stride,
+                                 const void* k_nope_bf16, int64_t k_row_stride, int64_t k_head_stride,
+                                 const void* k_pe_bf16, int64_t pe_row_stride, const void* v_bf16,
+                                 int64_t v_row_stride, int64_t v_head_stride, const int32_t* cu_q,
+                                 const int32_t* cu_k, int32_t B, int32_t T, int32_t S, int32_t H, float scale,
+                                 uint32_t flags, void* out_bf16, int64_t out_row_stride, int64_t out_head_stride,
+                                 float* lse, int32_t* dev_err, void* stream);
+
+/*
+ * dsa_dense_mla_decode -- absorbed latent attention over every visible row of the paged latent cache
+ * (dsa_sparse_mla_decode without a selection).
+ * Source: vllm mla/common.py, MLACommonImpl.forward decode branch (_forward_decode on the absorbed
+ * query and the paged cache; returns (out, lse)), merge_attn_states for the split over the length.
+ *   For row r and head h, over positions i < v_r: g(i) = block_table[b][i >> 6] * 64 + (i & 63);
+ *   S_i = scale * <q[r,h,0:576], C[g(i),0:576]>; P = softmax(S);
+ *   out[r,h,0:512] = bf16_rn(sum_i P_i * C[g(i),0:512]);  lse[r,h] = ln sum exp(S).
+ *   v_r <= 0: out = 0, lse = -inf.  bf16 operands, fp32 accumulation, P rounded to bf16 for the
+ *   product; the work is split over the cache's length and joined by log-sum-exp.  Rows >= cu_q[B]
+ *   are left as they were.  Cache rows past the last visible position of a request may hold
+ *   anything.
+ * Arguments: as dsa_sparse_mla_decode, without idx and k.  H in {16, 32, 64, 128}.
+ *   workspace      device scratch of dsa_dense_mla_decode_workspace_size(T, H) bytes, 16-byte
+ *                  aligned, nullable when that is 0.  No initialisation needed; its contents are
+ *                  dead after the call, but two calls in flight at the same time must not share it.
+ *   dev_err        nullable; DSA_DEVERR_PAGE_RANGE for a needed page id outside [0, num_pages)
+ *                  (its 64 positions are skipped), DSA_DEVERR_INDEX_RANGE for a visible length past
+ *                  max_pages * 64 or a cu_q range outside [0, T] (cut to it), DSA_DEVERR_TIMEOUT.
+ */
+size_t dsa_dense_mla_decode_workspace_size(int32_t T, int32_t H);
+dsa_status dsa_dense_mla_decode(const void* q_bf16, const void* kv_pool, int64_t num_pages,
+                                const int32_t* block_table, int32_t max_pages, const int32_t* seq_lens,
+                                const int32_t* cu_q, int32_t B, int32_t T, int32_t H, float scale, void* out_bf16,
+                                float* lse, void* workspace, size_t workspace_bytes, int32_t* dev_err, void* stream);
+
+/*
+ * dsa_verify_drafts -- verification of drafted tokens (target-verify of the q_len >= 2 rows) from
+ * given random numbers.
+ *   The source pages score the drafted tokens' rows (sglang dsa_indexer.py, next_n >= 2 target
+ *   verify) and leave the acceptance to the engine; this is the standard rejection rule, which
+ *   keeps the target's distribution.
+ *   Request b has the rows [cu_q[b], cu_q[b+1]); target_probs[r] is the target's distribution of the
+ *   token after row r's, and draft_tokens[r] = x_r the token drafted there with probability
+ *   draft_probs[r, x_r] (draft_probs NULL: the drafts were certain, q = 1 at x_r).  The request's
+ *   last row has no draft (its entry is not read); x_r < 0 elsewhere: no draft either, the drafts
+ *   end there.
+ *   From the first row on, x_r is accepted while accept_u[r] * q(x_r) < p(x_r).  At the first row r*
+ *   that is not accepted or has no draft, one token is drawn from the weights w: max(p - q, 0) after
+ *   a rejection (p with entry x zeroed when draft_probs is NULL; p when that leaves no mass), p
+ *   otherwise: the least v with w_0 + .. + w_v > sample_u[b] * sum w.
+ *   out_tokens[cu_q[b] ..]: the accepted drafts, then the drawn token, then -1 up to the request's
+ *   rows.  accepted[b]: the number of accepted drafts (r* - cu_q[b]).  A request without rows: 0.
+ *   The differences are exact and the sums carry at least 48 bits.  Entries that are not positive
+ *   and finite count as 0 in w.
+ * Arguments:
+ *   target_probs  fp32 rows of V entries, stride target_ld >= V.   draft_probs: nullable, likewise.
+ *   V             1 .. 2^24.   draft_tokens int32 [T].   cu_q int32 [B + 1].
+ *   accept_u      fp32 [T], sample_u fp32 [B]: uniform numbers in [0, 1).
+ *   out_tokens    int32 [T].   accepted int32 [B].  Rows >= cu_q[B] of out_tokens are left as they
+ *                 were.
+ *   dev_err       nullable; DSA_DEVERR_INDEX_RANGE for a draft token >= V (no draft) or a cu_q range
+ *                 outside [0, T] (cut to it), DSA_DEVERR_PROB for a row to draw from without mass
+ *                 (the drawn token is -1).
+ */
+dsa_status dsa_verify_drafts(const float* target_probs, int64_t target_ld, const float* draft_probs,
+                             int64_t draft_ld, int32_t V, const int32_t* draft_tokens, const int32_t* cu_q, int32_t B,
+                             int32_t T, const float* accept_u, const float* sample_u, int32_t* out_tokens,
+                             int32_t* accepted, int32_t* dev_err, void* stream);
 
 /*
  * dsa_read_device_error -- synchronise `stream`, copy the device error word to the host
