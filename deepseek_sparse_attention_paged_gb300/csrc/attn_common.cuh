@@ -64,6 +64,26 @@ __device__ __forceinline__ void tmem_st_x16(uint32_t taddr, const uint32_t (&r)[
 
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
+// A value that is the same in every lane, told to the compiler as such: it then lives in a uniform
+// register, where tcgen05.mma wants its descriptors.  Without it each descriptor word is moved there
+// lane by lane before every MMA (measured: about 130 cycles per MMA of 64).
+template <typename T>
+__device__ __forceinline__ T uniform(T v) { return __shfl_sync(0xffffffffu, v, 0); }
+
+// One lane of a converged warp.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\tselp.u32 %0, 1, 0, q;\n\t}" : "=r"(p));
+    return p != 0;
+}
+
+// Whole warpgroup: take up to, or give back down to, N registers a thread.  The shares of all
+// warpgroups together may not pass what the block was launched with.
+template <int N>
+__device__ __forceinline__ void set_regs_inc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
+template <int N>
+__device__ __forceinline__ void set_regs_dec() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
+
 // 2^x on the special-function unit (PTX ex2.approx; relative error about 2^-22, ample for P in bf16).
 __device__ __forceinline__ float fast_exp2(float x) {
     float y;

@@ -17,7 +17,7 @@
 // one head and one request: while the softmax warps of one work, the tensor cores run the other's
 // products.
 //
-// CTA: block qb of 256 query rows of request b, head h.  Roles (320 threads):
+// CTA: block qb of 256 query rows of request b, head h.  Roles (384 threads):
 //   warps 0-3, 4-7  softmax of query tile 0 / 1: one thread per query (TMEM lane), 128 scores in
 //                   registers, P written back over the scores as bf16; O / l at the end;
 //   warp 8          TMA: the query tiles, then K (two 64-dim slabs of k_nope, one of k_pe) and V
@@ -42,7 +42,8 @@ constexpr int kSlabBytes = 128 * 128;                     // 128 rows x 64 bf16,
 constexpr int kRing = 8;
 constexpr int kQSlabs = 3, kKSlabs = 3, kVSlabs = 2;
 constexpr int kTmaWarp = 8, kMmaWarp = 9;
-constexpr int kPreThreads = 320;
+constexpr int kPreThreads = 384;                          // three warpgroups; warps 10 and 11 only fill the third
+constexpr int kSoftmaxRegs = 192, kOtherRegs = 112;       // 2 x 128 x 192 + 128 x 112 <= 384 x 168 at launch
 constexpr uint32_t kColS = 0, kColO = 256;                // + 128 * tile
 constexpr size_t kPreSmem = 1024 + size_t(2 * kQSlabs + kRing) * kSlabBytes + 512;
 static_assert(kPreSmem <= 232448, "shared-memory budget");
@@ -107,7 +108,7 @@ dense_mla_prefill_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_
     unsigned char* ring = base + 2 * kQSlabs * kSlabBytes;     // [8]
     PreBars& bar = *reinterpret_cast<PreBars*>(ring + kRing * kSlabBytes);
 
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = uniform(static_cast<int>(threadIdx.x >> 5)), lane = threadIdx.x & 31;
     const int h = blockIdx.y;
     if (warp == 0) {
         if (lane == 0) bar.item[0] = -1;
@@ -127,14 +128,14 @@ dense_mla_prefill_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_
         ptx::fence_barrier_init();
     }
     __syncthreads();
-    const int b = bar.item[0];
+    const int b = uniform(bar.item[0]);
     if (b < 0) return;                                         // past the last block (uniform)
     if (warp == kMmaWarp) {
         ptx::tmem_alloc(&bar.tmem_slot, 512);
         ptx::tmem_relinquish();
     }
-    const int qb = bar.item[1], q0 = bar.item[2], nq = bar.item[3];
-    const int k_lo = __ldg(cu_k + b), k_hi = __ldg(cu_k + b + 1);
+    const int qb = uniform(bar.item[1]), q0 = uniform(bar.item[2]), nq = uniform(bar.item[3]);
+    const int k_lo = uniform(__ldg(cu_k + b)), k_hi = uniform(__ldg(cu_k + b + 1));
     const int k0 = max(0, min(S, k_lo));
     const int nk = max(0, min(S, k_hi) - k0);
     if (threadIdx.x == 0 && (k_lo < 0 || k_hi > S)) raise_error(err, DSA_DEVERR_INDEX_RANGE);
@@ -152,158 +153,164 @@ dense_mla_prefill_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_
     ptx::tc_fence_before_sync();
     __syncthreads();
     ptx::tc_fence_after_sync();
-    const uint32_t tmem = bar.tmem_slot;
+    const uint32_t tmem = uniform(bar.tmem_slot);
     const uint64_t deadline = ptx::wait_deadline();
     bool timed_out = false;
 
-    if (warp == kTmaWarp) {
-        // ---------------------------------------------------------------- TMA
-        if (lane == 0 && n > 0) {
-            uint32_t c = 0;                                    // slabs issued
-            auto next = [&]() -> unsigned char* {              // the ring's next slab, once it is free
-                const int s = static_cast<int>(c % kRing);
-                if (!ptx::mbar_wait(&bar.empty[s], ((c / kRing) & 1u) ^ 1u, deadline)) timed_out = true;
-                if (timed_out) return nullptr;
-                ptx::mbar_arrive_expect_tx(&bar.full[s], kSlabBytes);
-                ++c;
-                return ring + s * kSlabBytes;
-            };
-            auto bar_of_last = [&]() { return &bar.full[(c - 1) % kRing]; };
-            auto load_q = [&](int i) {
-                if (n_tiles[i] == 0) return;
-                ptx::mbar_arrive_expect_tx(&bar.q_full[i], kQSlabs * kSlabBytes);
-                for (int j = 0; j < kQSlabs; ++j)
-                    ptx::tma_load_3d(qs + (i * kQSlabs + j) * kSlabBytes, &qmap, &bar.q_full[i], 64 * j, h,
-                                     q0 + qb * kBlockQ + i * kTileQ);
-            };
-            auto load_k = [&](int t) {
-                for (int j = 0; j < kKSlabs && !timed_out; ++j)
-                    if (unsigned char* dst = next()) {
-                        if (j < 2) ptx::tma_load_3d(dst, &kmap, bar_of_last(), 64 * j, h, k0 + t * kTileK);
-                        else ptx::tma_load_3d(dst, &pmap, bar_of_last(), 0, 0, k0 + t * kTileK);
-                    }
-            };
-            load_q(0);
-            load_k(0);
-            load_q(1);
-            for (int t = 0; t < n && !timed_out; ++t) {
-                for (int j = 0; j < kVSlabs && !timed_out; ++j)
-                    if (unsigned char* dst = next())
-                        ptx::tma_load_3d(dst, &vmap, bar_of_last(), 64 * j, h, k0 + t * kTileK);
-                if (t + 1 < n) load_k(t + 1);
-            }
-            // copies still in flight land before the CTA may leave (bounded)
-            for (int i = 0; i < 2; ++i)
-                if (n_tiles[i] > 0 && !ptx::mbar_wait(&bar.q_full[i], 0, ptx::wait_deadline(20000000ull))) timed_out = true;
-            for (uint32_t j = c > kRing ? c - kRing : 0; j < c; ++j)
-                if (!ptx::mbar_wait(&bar.full[j % kRing], (j / kRing) & 1u, ptx::wait_deadline(20000000ull)))
-                    timed_out = true;
-        }
-    } else if (warp == kMmaWarp) {
-        // ---------------------------------------------------------------- MMA
-        constexpr uint32_t idesc_qk = ptx::instr_desc(1, 1, kTileQ, kTileK);
-        constexpr uint32_t idesc_pv = ptx::instr_desc(1, 1, kTileQ, 128) | (1u << 16);   // B MN-major
-        constexpr uint32_t idesc_pv_half = ptx::instr_desc(1, 1, kTileQ, 64) | (1u << 16);
-        const uint32_t q_addr = ptx::smem_addr(qs), ring_addr = ptx::smem_addr(ring);
-        auto wait_slabs = [&](uint32_t c0, int cnt) {          // slabs c0 .. have landed (whole warp)
-            for (int j = 0; j < cnt && !timed_out; ++j)
-                if (!ptx::mbar_wait(&bar.full[(c0 + j) % kRing], ((c0 + j) / kRing) & 1u, deadline)) timed_out = true;
-            timed_out = __any_sync(0xffffffffu, timed_out);
-            ptx::tc_fence_after_sync();
-        };
-        auto release = [&](uint32_t c0, int cnt) {             // ... and are free once the MMAs so far completed
-            if (lane == 0)
-                for (int j = 0; j < cnt; ++j) ptx::umma_commit(&bar.empty[(c0 + j) % kRing]);
-            __syncwarp();
-        };
-        auto slab = [&](uint32_t cc) { return ring_addr + (cc % kRing) * kSlabBytes; };
-        auto issue_s = [&](int i, uint32_t c0) {               // S_i = Q_i K^T from the slabs at c0
-            if (lane == 0) {
-#pragma unroll 1
-                for (int j = 0; j < kKSlabs; ++j)
-#pragma unroll
-                    for (int kk = 0; kk < 4; ++kk)
-                        ptx::umma_f16(tmem + kColS + 128 * i,
-                                      desc_sw128(q_addr + (i * kQSlabs + j) * kSlabBytes + kk * 32, 16, 1024),
-                                      desc_sw128(slab(c0 + j) + kk * 32, 16, 1024), idesc_qk, (j | kk) != 0 ? 1u : 0u);
-                ptx::umma_commit(&bar.s_full[i]);
-            }
-            __syncwarp();
-        };
-        if (n > 0) {
-            wait_slabs(0, kKSlabs);
-            for (int i = 0; i < 2 && !timed_out; ++i) {
-                if (n_tiles[i] == 0) continue;
-                if (!ptx::mbar_wait(&bar.q_full[i], 0, deadline)) timed_out = true;
-                timed_out = __any_sync(0xffffffffu, timed_out);
-                if (!timed_out) issue_s(i, 0);
-            }
-            if (!timed_out) release(0, kKSlabs);
-        }
-        for (int t = 0; t < n && !timed_out; ++t) {
-            // ring order: K(0), V(0), K(1), V(1), ...; this step uses V(t) and K(t + 1)
-            const uint32_t c_v = static_cast<uint32_t>(t) * (kKSlabs + kVSlabs) + kKSlabs, c_k = c_v + kVSlabs;
-            const int last = t < n_tiles[1] ? 1 : 0;           // the last tile that uses V(t)
-            bool v_ready = false, k_ready = false;
-            for (int i = 0; i < 2 && !timed_out; ++i) {
-                if (t >= n_tiles[i]) continue;
-                if (!ptx::mbar_wait(&bar.p_full[i], t & 1, deadline)) timed_out = true;
-                timed_out = __any_sync(0xffffffffu, timed_out);
-                if (timed_out) break;
-                if (!v_ready) {
-                    wait_slabs(c_v, kVSlabs);
-                    if (timed_out) break;
-                    v_ready = true;
-                    const int valid = nk - t * kTileK;
-                    if (valid < kTileK) {
-                        // rows past the request's last key are another request's, or anything: their
-                        // P is 0, but 0 times NaN or infinity is not
-                        for (int e = lane; e < (kTileK - valid) * 8; e += 32) {
-                            const int row = valid + (e >> 3);
-#pragma unroll
-                            for (int j = 0; j < kVSlabs; ++j)
-                                *reinterpret_cast<uint4*>(ring + ((c_v + j) % kRing) * kSlabBytes + row * 128 +
-                                                          (e & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
+    if (warp >= kTmaWarp) {
+        set_regs_dec<kOtherRegs>();
+        if (warp == kTmaWarp) {
+            // ---------------------------------------------------------------- TMA
+            if (lane == 0 && n > 0) {
+                uint32_t c = 0;                                    // slabs issued
+                auto next = [&]() -> unsigned char* {              // the ring's next slab, once it is free
+                    const int s = static_cast<int>(c % kRing);
+                    if (!ptx::mbar_wait(&bar.empty[s], ((c / kRing) & 1u) ^ 1u, deadline)) timed_out = true;
+                    if (timed_out) return nullptr;
+                    ptx::mbar_arrive_expect_tx(&bar.full[s], kSlabBytes);
+                    ++c;
+                    return ring + s * kSlabBytes;
+                };
+                auto bar_of_last = [&]() { return &bar.full[(c - 1) % kRing]; };
+                auto load_q = [&](int i) {
+                    if (n_tiles[i] == 0) return;
+                    ptx::mbar_arrive_expect_tx(&bar.q_full[i], kQSlabs * kSlabBytes);
+                    for (int j = 0; j < kQSlabs; ++j)
+                        ptx::tma_load_3d(qs + (i * kQSlabs + j) * kSlabBytes, &qmap, &bar.q_full[i], 64 * j, h,
+                                         q0 + qb * kBlockQ + i * kTileQ);
+                };
+                auto load_k = [&](int t) {
+                    for (int j = 0; j < kKSlabs && !timed_out; ++j)
+                        if (unsigned char* dst = next()) {
+                            if (j < 2) ptx::tma_load_3d(dst, &kmap, bar_of_last(), 64 * j, h, k0 + t * kTileK);
+                            else ptx::tma_load_3d(dst, &pmap, bar_of_last(), 0, 0, k0 + t * kTileK);
                         }
-                        ptx::fence_proxy_async_smem();
-                        __syncwarp();
-                    }
+                };
+                load_q(0);
+                load_k(0);
+                load_q(1);
+                for (int t = 0; t < n && !timed_out; ++t) {
+                    for (int j = 0; j < kVSlabs && !timed_out; ++j)
+                        if (unsigned char* dst = next())
+                            ptx::tma_load_3d(dst, &vmap, bar_of_last(), 64 * j, h, k0 + t * kTileK);
+                    if (t + 1 < n) load_k(t + 1);
                 }
+                // copies still in flight land before the CTA may leave (bounded)
+                for (int i = 0; i < 2; ++i)
+                    if (n_tiles[i] > 0 && !ptx::mbar_wait(&bar.q_full[i], 0, ptx::wait_deadline(20000000ull))) timed_out = true;
+                for (uint32_t j = c > kRing ? c - kRing : 0; j < c; ++j)
+                    if (!ptx::mbar_wait(&bar.full[j % kRing], (j / kRing) & 1u, ptx::wait_deadline(20000000ull)))
+                        timed_out = true;
+            }
+        } else if (warp == kMmaWarp) {
+            // ---------------------------------------------------------------- MMA
+            constexpr uint32_t idesc_qk = ptx::instr_desc(1, 1, kTileQ, kTileK);
+            constexpr uint32_t idesc_pv = ptx::instr_desc(1, 1, kTileQ, 128) | (1u << 16);   // B MN-major
+            constexpr uint32_t idesc_pv_half = ptx::instr_desc(1, 1, kTileQ, 64) | (1u << 16);
+            const uint32_t q_addr = ptx::smem_addr(qs), ring_addr = ptx::smem_addr(ring);
+            auto wait_slabs = [&](uint32_t c0, int cnt) {          // slabs c0 .. have landed (whole warp)
+                for (int j = 0; j < cnt && !timed_out; ++j)
+                    if (!ptx::mbar_wait(&bar.full[(c0 + j) % kRing], ((c0 + j) / kRing) & 1u, deadline)) timed_out = true;
+                timed_out = __any_sync(0xffffffffu, timed_out);
                 ptx::tc_fence_after_sync();
-                if (lane == 0) {
-                    const uint32_t v0 = slab(c_v), v1 = slab(c_v + 1);
-                    const uint32_t o = tmem + kColO + 128 * i, p = tmem + kColS + 128 * i;
-                    if (v1 > v0) {
+            };
+            auto release = [&](uint32_t c0, int cnt) {             // ... and are free once the MMAs so far completed
+                if (elect_one())
+                    for (int j = 0; j < cnt; ++j) ptx::umma_commit(&bar.empty[(c0 + j) % kRing]);
+                __syncwarp();
+            };
+            // descriptors differ in their start address only (low word, 16-byte units): one add each
+            const uint64_t q_desc = desc_sw128(q_addr, 16, 1024);
+            const uint64_t k_desc = desc_sw128(ring_addr, 16, 1024), v_desc = desc_sw128(ring_addr, kSlabBytes, 1024);
+            auto slab = [&](uint32_t cc) { return (cc % kRing) * (kSlabBytes / 16); };
+            auto issue_s = [&](int i, uint32_t c0) {               // S_i = Q_i K^T from the slabs at c0
+                if (elect_one()) {
+                    const uint64_t a = q_desc + i * (kQSlabs * kSlabBytes / 16);
 #pragma unroll
-                        for (int ks = 0; ks < kTileK / 16; ++ks)
-                            umma_f16_ts(o, p + ks * 8, desc_sw128(v0 + ks * 2048, kSlabBytes, 1024), idesc_pv,
-                                        (t | ks) != 0 ? 1u : 0u);
-                    } else {                                   // the ring wraps between the two slabs
+                    for (int j = 0; j < kKSlabs; ++j) {
+                        const uint64_t bk = k_desc + slab(c0 + j);
 #pragma unroll
-                        for (int ks = 0; ks < kTileK / 16; ++ks) {
-                            umma_f16_ts(o, p + ks * 8, desc_sw128(v0 + ks * 2048, kSlabBytes, 1024), idesc_pv_half,
-                                        (t | ks) != 0 ? 1u : 0u);
-                            umma_f16_ts(o + 64, p + ks * 8, desc_sw128(v1 + ks * 2048, kSlabBytes, 1024),
-                                        idesc_pv_half, (t | ks) != 0 ? 1u : 0u);
-                        }
+                        for (int kk = 0; kk < 4; ++kk)
+                            ptx::umma_f16(tmem + kColS + 128 * i, a + (j * (kSlabBytes / 16) + kk * 2), bk + kk * 2, idesc_qk,
+                                          (j | kk) != 0 ? 1u : 0u);
                     }
+                    ptx::umma_commit(&bar.s_full[i]);
                 }
                 __syncwarp();
-                if (i == last) release(c_v, kVSlabs);
-                if (t + 1 < n_tiles[i]) {
-                    if (!k_ready) {
-                        wait_slabs(c_k, kKSlabs);
-                        if (timed_out) break;
-                        k_ready = true;
-                    }
-                    issue_s(i, c_k);
-                } else if (lane == 0) {
-                    ptx::umma_commit(&bar.o_full[i]);
+            };
+            if (n > 0) {
+                wait_slabs(0, kKSlabs);
+                for (int i = 0; i < 2 && !timed_out; ++i) {
+                    if (n_tiles[i] == 0) continue;
+                    if (!ptx::mbar_wait(&bar.q_full[i], 0, deadline)) timed_out = true;
+                    timed_out = __any_sync(0xffffffffu, timed_out);
+                    if (!timed_out) issue_s(i, 0);
                 }
+                if (!timed_out) release(0, kKSlabs);
             }
-            if (t + 1 < n && !timed_out) release(c_k, kKSlabs);
+            for (int t = 0; t < n && !timed_out; ++t) {
+                // ring order: K(0), V(0), K(1), V(1), ...; this step uses V(t) and K(t + 1)
+                const uint32_t c_v = static_cast<uint32_t>(t) * (kKSlabs + kVSlabs) + kKSlabs, c_k = c_v + kVSlabs;
+                const int last = t < n_tiles[1] ? 1 : 0;           // the last tile that uses V(t)
+                bool v_ready = false, k_ready = false;
+                for (int i = 0; i < 2 && !timed_out; ++i) {
+                    if (t >= n_tiles[i]) continue;
+                    if (!ptx::mbar_wait(&bar.p_full[i], t & 1, deadline)) timed_out = true;
+                    timed_out = __any_sync(0xffffffffu, timed_out);
+                    if (timed_out) break;
+                    if (!v_ready) {
+                        wait_slabs(c_v, kVSlabs);
+                        if (timed_out) break;
+                        v_ready = true;
+                        const int valid = nk - t * kTileK;
+                        if (valid < kTileK) {
+                            // rows past the request's last key are another request's, or anything: their
+                            // P is 0, but 0 times NaN or infinity is not
+                            for (int e = lane; e < (kTileK - valid) * 8; e += 32) {
+                                const int row = valid + (e >> 3);
+#pragma unroll
+                                for (int j = 0; j < kVSlabs; ++j)
+                                    *reinterpret_cast<uint4*>(ring + ((c_v + j) % kRing) * kSlabBytes + row * 128 +
+                                                              (e & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
+                            }
+                            ptx::fence_proxy_async_smem();
+                            __syncwarp();
+                        }
+                    }
+                    ptx::tc_fence_after_sync();
+                    if (elect_one()) {
+                        const uint64_t v0 = v_desc + slab(c_v), v1 = v_desc + slab(c_v + 1);
+                        const uint32_t o = tmem + kColO + 128 * i, p = tmem + kColS + 128 * i;
+                        if (v1 > v0) {
+#pragma unroll
+                            for (int ks = 0; ks < kTileK / 16; ++ks)
+                                umma_f16_ts(o, p + ks * 8, v0 + ks * 128, idesc_pv, (t | ks) != 0 ? 1u : 0u);
+                        } else {                                   // the ring wraps between the two slabs
+#pragma unroll
+                            for (int ks = 0; ks < kTileK / 16; ++ks) {
+                                umma_f16_ts(o, p + ks * 8, v0 + ks * 128, idesc_pv_half, (t | ks) != 0 ? 1u : 0u);
+                                umma_f16_ts(o + 64, p + ks * 8, v1 + ks * 128, idesc_pv_half, (t | ks) != 0 ? 1u : 0u);
+                            }
+                        }
+                    }
+                    __syncwarp();
+                    if (i == last) release(c_v, kVSlabs);
+                    if (t + 1 < n_tiles[i]) {
+                        if (!k_ready) {
+                            wait_slabs(c_k, kKSlabs);
+                            if (timed_out) break;
+                            k_ready = true;
+                        }
+                        issue_s(i, c_k);
+                    } else if (elect_one()) {
+                        ptx::umma_commit(&bar.o_full[i]);
+                    }
+                }
+                if (t + 1 < n && !timed_out) release(c_k, kKSlabs);
+            }
         }
     } else {
+        set_regs_inc<kSoftmaxRegs>();
         // ---------------------------------------------------------------- softmax, epilogue
         const int i = warp >> 2;                               // query tile
         const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;
