@@ -208,64 +208,86 @@ dense_mla_prefill_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_
             constexpr uint32_t idesc_pv = ptx::instr_desc(1, 1, kTileQ, 128) | (1u << 16);   // B MN-major
             constexpr uint32_t idesc_pv_half = ptx::instr_desc(1, 1, kTileQ, 64) | (1u << 16);
             const uint32_t q_addr = ptx::smem_addr(qs), ring_addr = ptx::smem_addr(ring);
-            auto wait_slabs = [&](uint32_t c0, int cnt) {          // slabs c0 .. have landed (whole warp)
-                for (int j = 0; j < cnt && !timed_out; ++j)
-                    if (!ptx::mbar_wait(&bar.full[(c0 + j) % kRing], ((c0 + j) / kRing) & 1u, deadline)) timed_out = true;
-                timed_out = __any_sync(0xffffffffu, timed_out);
-                ptx::tc_fence_after_sync();
+            // A wait that ran out only marks the step: the warp leaves together at the step's end.  What it
+            // issues until then reads shared and tensor memory of this CTA only.
+            bool late = false;
+            auto wait = [&](uint64_t* b, uint32_t parity) {
+                if (!ptx::mbar_wait(b, parity, deadline)) late = true;
             };
-            auto release = [&](uint32_t c0, int cnt) {             // ... and are free once the MMAs so far completed
+            auto wait_slab = [&](uint32_t cc) { wait(&bar.full[cc % kRing], (cc / kRing) & 1u); };
+            auto release = [&](uint32_t c0, int cnt) {         // free once the MMAs issued so far completed
                 if (elect_one())
                     for (int j = 0; j < cnt; ++j) ptx::umma_commit(&bar.empty[(c0 + j) % kRing]);
-                __syncwarp();
             };
             // descriptors differ in their start address only (low word, 16-byte units): one add each
             const uint64_t q_desc = desc_sw128(q_addr, 16, 1024);
             const uint64_t k_desc = desc_sw128(ring_addr, 16, 1024), v_desc = desc_sw128(ring_addr, kSlabBytes, 1024);
             auto slab = [&](uint32_t cc) { return (cc % kRing) * (kSlabBytes / 16); };
-            auto issue_s = [&](int i, uint32_t c0) {               // S_i = Q_i K^T from the slabs at c0
-                if (elect_one()) {
-                    const uint64_t a = q_desc + i * (kQSlabs * kSlabBytes / 16);
+            // S_i = Q_i K^T from the slabs at c0; the first user of a key tile waits for each slab in turn
+            auto issue_s = [&](int i, uint32_t c0, bool first) {
+                const uint64_t a = q_desc + i * (kQSlabs * kSlabBytes / 16);
 #pragma unroll
-                    for (int j = 0; j < kKSlabs; ++j) {
+                for (int j = 0; j < kKSlabs; ++j) {
+                    if (first) {
+                        wait_slab(c0 + j);
+                        __syncwarp();
+                        ptx::tc_fence_after_sync();
+                    }
+                    if (elect_one()) {
                         const uint64_t bk = k_desc + slab(c0 + j);
 #pragma unroll
                         for (int kk = 0; kk < 4; ++kk)
-                            ptx::umma_f16(tmem + kColS + 128 * i, a + (j * (kSlabBytes / 16) + kk * 2), bk + kk * 2, idesc_qk,
-                                          (j | kk) != 0 ? 1u : 0u);
+                            ptx::umma_f16(tmem + kColS + 128 * i, a + (j * (kSlabBytes / 16) + kk * 2), bk + kk * 2,
+                                          idesc_qk, (j | kk) != 0 ? 1u : 0u);
+                        if (j == kKSlabs - 1) ptx::umma_commit(&bar.s_full[i]);
                     }
-                    ptx::umma_commit(&bar.s_full[i]);
                 }
-                __syncwarp();
+            };
+            // O_i += P_i V from the two slabs at c0
+            auto issue_pv = [&](int i, uint32_t c0, uint32_t accumulate) {
+                if (elect_one()) {
+                    const uint64_t v0 = v_desc + slab(c0), v1 = v_desc + slab(c0 + 1);
+                    const uint32_t o = tmem + kColO + 128 * i, p = tmem + kColS + 128 * i;
+                    if (v1 > v0) {
+#pragma unroll
+                        for (int ks = 0; ks < kTileK / 16; ++ks)
+                            umma_f16_ts(o, p + ks * 8, v0 + ks * 128, idesc_pv, ks != 0 ? 1u : accumulate);
+                    } else {                                   // the ring wraps between the two slabs
+#pragma unroll
+                        for (int ks = 0; ks < kTileK / 16; ++ks) {
+                            umma_f16_ts(o, p + ks * 8, v0 + ks * 128, idesc_pv_half, ks != 0 ? 1u : accumulate);
+                            umma_f16_ts(o + 64, p + ks * 8, v1 + ks * 128, idesc_pv_half, ks != 0 ? 1u : accumulate);
+                        }
+                    }
+                }
             };
             if (n > 0) {
-                wait_slabs(0, kKSlabs);
-                for (int i = 0; i < 2 && !timed_out; ++i) {
+                bool first = true;
+                for (int i = 0; i < 2; ++i) {
                     if (n_tiles[i] == 0) continue;
-                    if (!ptx::mbar_wait(&bar.q_full[i], 0, deadline)) timed_out = true;
-                    timed_out = __any_sync(0xffffffffu, timed_out);
-                    if (!timed_out) issue_s(i, 0);
+                    wait(&bar.q_full[i], 0);
+                    issue_s(i, 0, first);
+                    first = false;
                 }
-                if (!timed_out) release(0, kKSlabs);
+                release(0, kKSlabs);
             }
-            for (int t = 0; t < n && !timed_out; ++t) {
+            for (int t = 0; t < n; ++t) {
                 // ring order: K(0), V(0), K(1), V(1), ...; this step uses V(t) and K(t + 1)
                 const uint32_t c_v = static_cast<uint32_t>(t) * (kKSlabs + kVSlabs) + kKSlabs, c_k = c_v + kVSlabs;
-                const int last = t < n_tiles[1] ? 1 : 0;           // the last tile that uses V(t)
-                bool v_ready = false, k_ready = false;
-                for (int i = 0; i < 2 && !timed_out; ++i) {
+                const int last = t < n_tiles[1] ? 1 : 0;       // the last tile that uses V(t)
+                bool first_v = true, first_k = true;
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
                     if (t >= n_tiles[i]) continue;
-                    if (!ptx::mbar_wait(&bar.p_full[i], t & 1, deadline)) timed_out = true;
-                    timed_out = __any_sync(0xffffffffu, timed_out);
-                    if (timed_out) break;
-                    if (!v_ready) {
-                        wait_slabs(c_v, kVSlabs);
-                        if (timed_out) break;
-                        v_ready = true;
+                    if (first_v) {
+                        first_v = false;
+                        wait_slab(c_v);
+                        wait_slab(c_v + 1);
                         const int valid = nk - t * kTileK;
                         if (valid < kTileK) {
                             // rows past the request's last key are another request's, or anything: their
                             // P is 0, but 0 times NaN or infinity is not
+                            __syncwarp();
                             for (int e = lane; e < (kTileK - valid) * 8; e += 32) {
                                 const int row = valid + (e >> 3);
 #pragma unroll
@@ -274,40 +296,24 @@ dense_mla_prefill_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_
                                                               (e & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
                             }
                             ptx::fence_proxy_async_smem();
-                            __syncwarp();
                         }
                     }
-                    ptx::tc_fence_after_sync();
-                    if (elect_one()) {
-                        const uint64_t v0 = v_desc + slab(c_v), v1 = v_desc + slab(c_v + 1);
-                        const uint32_t o = tmem + kColO + 128 * i, p = tmem + kColS + 128 * i;
-                        if (v1 > v0) {
-#pragma unroll
-                            for (int ks = 0; ks < kTileK / 16; ++ks)
-                                umma_f16_ts(o, p + ks * 8, v0 + ks * 128, idesc_pv, (t | ks) != 0 ? 1u : 0u);
-                        } else {                                   // the ring wraps between the two slabs
-#pragma unroll
-                            for (int ks = 0; ks < kTileK / 16; ++ks) {
-                                umma_f16_ts(o, p + ks * 8, v0 + ks * 128, idesc_pv_half, (t | ks) != 0 ? 1u : 0u);
-                                umma_f16_ts(o + 64, p + ks * 8, v1 + ks * 128, idesc_pv_half, (t | ks) != 0 ? 1u : 0u);
-                            }
-                        }
-                    }
+                    wait(&bar.p_full[i], t & 1);
                     __syncwarp();
+                    ptx::tc_fence_after_sync();
+                    issue_pv(i, c_v, t != 0 ? 1u : 0u);
                     if (i == last) release(c_v, kVSlabs);
                     if (t + 1 < n_tiles[i]) {
-                        if (!k_ready) {
-                            wait_slabs(c_k, kKSlabs);
-                            if (timed_out) break;
-                            k_ready = true;
-                        }
-                        issue_s(i, c_k);
+                        issue_s(i, c_k, first_k);
+                        first_k = false;
                     } else if (elect_one()) {
                         ptx::umma_commit(&bar.o_full[i]);
                     }
                 }
-                if (t + 1 < n && !timed_out) release(c_k, kKSlabs);
+                if (t + 1 < n) release(c_k, kKSlabs);
+                if (__any_sync(0xffffffffu, late)) break;
             }
+            if (late) timed_out = true;
         }
     } else {
         set_regs_inc<kSoftmaxRegs>();
