@@ -250,8 +250,10 @@ __device__ __forceinline__ void st_async_v4(uint32_t addr, uint32_t a, uint32_t 
                  "r"(a), "r"(b), "r"(c), "r"(d), "r"(bar)
                  : "memory");
 }
+// Arrive on a barrier of the peer without ordering anything before it: used for buffers this thread has
+// only read (the values are in registers).  A release at cluster scope costs about 2000 cycles here.
 __device__ __forceinline__ void arrive_remote(uint32_t bar) {
-    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+    asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 // mbar_wait that also orders what threads of the peer CTA did before they arrived.
 __device__ __forceinline__ bool mbar_wait_cluster(uint64_t* bar, uint32_t parity, uint64_t deadline) {
@@ -564,8 +566,6 @@ dense_mla_decode_kernel(const __grid_constant__ CUtensorMap vmap, const __grid_c
                             sc[4 * k4 + 2] = __uint_as_float(p[2]) + x[k4].z;
                             sc[4 * k4 + 3] = __uint_as_float(p[3]) + x[k4].w;
                         }
-                        __syncwarp();
-                        if (lane == 0) arrive_remote(map_to_rank(ptx::smem_addr(&bar.x_free[bb]), peer));
                         const int lim = bar.page_ok[s] ? vis - t * kKeys : 0;
                         if (lim < kKeys) {
 #pragma unroll
@@ -576,6 +576,9 @@ dense_mla_decode_kernel(const __grid_constant__ CUtensorMap vmap, const __grid_c
 #pragma unroll
                         for (int e = 4; e < 64; ++e) mx4[e & 3] = fmaxf(mx4[e & 3], sc[e]);
                         const float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3]));
+                        // every lane's scores have been read (the maximum needs them): the peer may send again
+                        __syncwarp();
+                        if (lane == 0) arrive_remote(map_to_rank(ptx::smem_addr(&bar.x_free[bb]), peer));
                         const bool grow = (mx - m_run) * cs > kRescaleThreshold || (m_run == -INFINITY && mx > -INFINITY);
                         if (__any_sync(0xffffffffu, grow)) {
                             const float alpha = grow ? (m_run == -INFINITY ? 0.0f : exp2f((m_run - mx) * cs)) : 1.0f;
