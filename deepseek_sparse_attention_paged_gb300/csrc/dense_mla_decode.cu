@@ -16,20 +16,24 @@
 // the key takes, and its output accumulator (128 x 512 fp32) alone would fill the tensor memory.  So
 // two CTAs of a cluster share a row tile: rank c owns the value dims 256 c .. 256 c + 255 and the rope
 // dims 512 + 32 c .. 512 + 32 c + 31, reads only those of every cached row, forms the partial scores
-// over them, and the two swap their partial scores (fp32, st.async into the peer's shared memory).
-// Both then hold the full scores, take the same softmax and accumulate their own 256 output dims.
+// over them and accumulates its own 256 output dims.  The softmax is split by rows: rank c owns the
+// 32-row groups c and c + 2; it receives the peer's partial scores of them (fp32, st.async into its
+// shared memory), and sends P (bf16) and the rescaling factors back.  That is 24 KB a tile and
+// direction over the cluster network (about 32 bytes a cycle), where a swap of all partial scores
+// took 32 KB and the whole softmax in both CTAs.
 //
 // Work: the key tiles (64 positions = one page) of all row tiles in one sequence, cut into equal shares,
 // one per cluster (at least kMinShare tiles).  A row tile that lies within one share is written
 // directly; the pieces of the others go to the workspace and the combine kernel joins them.
 //
 // Roles (384 threads):
-//   warps 0-3  softmax: one thread per query row; partial scores from tensor memory, the peer's from
-//              shared memory, P over its score tile as bf16; rescaling; O / l at a row tile's end;
-//   warps 4-7  senders: queries of the next row tile into tensor memory, partial scores to the peer;
-//              apart from the softmax so that a tile's swap runs during the previous tile's softmax;
+//   warps 0-7  rows: warp w has the rows (tensor-memory lanes) 32 (w % 4) .. + 31 and key half w / 4.
+//              Owned rows: own scores + the peer's, softmax, P to both CTAs' shared memory.  Other
+//              rows: partial scores to the peer, O rescaled by the peer's factors.  Queries into
+//              tensor memory; output of 128 of the 256 dims at a row tile's end;
 //   warp 8     TMA: the CTA's dims of each page, 4 chunks of 64 value dims and 32 rope dims, 4-deep ring;
-//   warp 9     MMA: S = Q K^T (A in tensor memory, rope part in shared memory), O += P V; warps 10, 11 idle.
+//   warp 9     MMA: S = Q K^T (A in tensor memory, rope part in shared memory), two tiles ahead, and
+//              O += P V (P in shared memory), whichever is ready; warps 10 and 11 idle.
 // Tensor memory: O (columns 0-255), two score tiles (256-383), the CTA's 4 query chunks (384-511).
 #include <cuda_bf16.h>
 
@@ -49,35 +53,44 @@ constexpr int kChunkBytes = kKeys * 128;                        // 8192, 128-byt
 constexpr int kRopeBytes = kKeys * 64;                          // 4096, 64-byte swizzle
 constexpr int kStageBytes = kChunks * kChunkBytes + kRopeBytes; // 36864
 constexpr int kStages = 4;
-constexpr int kXBytes = kRows * kKeys * 4;                      // 32768: the peer's partial scores
+constexpr int kOwnRows = kRows / 2;                             // rows whose softmax a CTA takes
+constexpr int kXBytes = kOwnRows * kKeys * 4;                   // 16384: the peer's partial scores of them
+constexpr int kPBytes = kRows * kKeys * 2;                      // 16384: P, K-major, 128-byte swizzle
 constexpr int kQRopeBytes = kRows * 64;                         // 8192
-constexpr int kSendWarp = 4, kTmaWarp = 8, kMmaWarp = 9;
+constexpr int kTmaWarp = 8, kMmaWarp = 9;
 constexpr int kDecThreads = 384;
 constexpr uint32_t kColS = 256, kColQ = 384;
 constexpr int kHalf = kValueDim / 2;
 constexpr int kMaxRequests = 16384;                             // prefix sums of the schedule fit the ring
 constexpr int kMinShare = 4;
-constexpr size_t kDecSmem = 1024 + size_t(kStages) * kStageBytes + 2 * size_t(kXBytes) + kQRopeBytes + 1024;
+constexpr size_t kDecSmem = 1024 + size_t(kStages) * kStageBytes + 2 * size_t(kXBytes + kPBytes) + kQRopeBytes + 4096;
 static_assert(kDecSmem <= 232448, "shared-memory budget");
 static_assert(kMaxRequests * 4 <= kStages * kStageBytes, "schedule scratch");
 
 struct DecBars {
-    uint64_t q_full;                        // queries in place (4 sender warps), per row tile
+    uint64_t q_full;                        // queries in place (8 row warps), per row tile
     uint64_t kv_full[kStages], kv_empty[kStages];
     uint64_t s_full[2];                     // partial scores complete
-    uint64_t s_read[2];                     // ... and read by the senders (4 warps)
-    uint64_t x_full[2];                     // the peer's partial scores arrived (armed + bytes)
-    uint64_t x_free[2];                     // the peer has read the ones sent to it (its 4 softmax warps)
-    uint64_t p_full[2];                     // P written (4 softmax warps)
-    uint64_t pv_done[2];                    // P V of the tile complete
-    uint64_t o_free;                        // O read out (4 softmax warps), per row tile
+    uint64_t s_read[2];                     // ... and read (8 row warps)
+    uint64_t x_full[2];                     // the peer's partial scores of the owned rows arrived (armed + bytes)
+    uint64_t x_free[2];                     // the peer has read the ones sent to it (its 4 owning warps)
+    uint64_t pair[2];                       // both key halves of an owned row group have written (2 warps)
+    uint64_t p_full[2];                     // P in place: 4 owning warps here, armed + bytes from the peer
+    uint64_t a_full[2];                     // the peer's rescaling factors arrived (armed + bytes)
+    uint64_t scaled[2];                     // O of the other rows rescaled by them (4 warps)
+    uint64_t pv_done[2];                    // P V of the tile complete in both CTAs
+    uint64_t o_free;                        // O read out (8 row warps), per row tile
+    uint64_t fin_full;                      // the peer's 1 / l arrived (armed + bytes), per row tile
     uint32_t tmem_slot;
     int page_ok[kStages];                   // the stage's page id was valid
     int start[4];                           // first request, first row tile of it, first key tile, tiles of the share
-    int share;
     int first_cluster;                      // cluster that holds the first piece of the first row tile
+    float tmax[2][2][kOwnRows];             // [tile parity][key half][owned row]: maximum of the tile
+    float lsum[2][kOwnRows];                // [key half]: sums at a row tile's end
+    float alpha[2][kOwnRows];               // [tile parity]: the peer's factors of the other rows
+    float fin[kOwnRows];                    // the peer's 1 / l of the other rows; -1: nothing visible
 };
-static_assert(sizeof(DecBars) <= 1024, "barrier block");
+static_assert(sizeof(DecBars) <= 4096, "barrier block");
 
 struct Batch {
     const int32_t* seq_lens;
@@ -112,7 +125,7 @@ __device__ __forceinline__ RowTile row_tile(const Batch& bt, int L, int q0, int 
 
 // A share's pieces, one row tile after the other; every role walks them by itself.
 struct Walk {
-    const Batch bt;
+    Batch bt;
     int b, g, q0, nq, L, left;
     RowTile rt;
     int t0, t1;            // key tiles [t0, t1) of the piece (t0 == t1: a row tile that sees nothing)
@@ -159,6 +172,11 @@ struct Walk {
     }
 };
 
+// Workspace slot of a part: 2 c for the one that starts share c but not its row tile, else 2 c + 1.
+__device__ __forceinline__ int64_t piece_slot(int cluster, const Walk& w) {
+    return 2 * static_cast<int64_t>(cluster) + ((w.first && w.t0 > 0) ? 0 : 1);
+}
+
 // Key tiles of request b over all its row tiles (a row tile that sees nothing counts as one).
 __device__ __forceinline__ int request_tiles(const Batch& bt, int b, int32_t* err) {
     int q0;
@@ -189,7 +207,6 @@ __device__ __forceinline__ void find_share(const Batch& bt, int c, int clusters,
         const int64_t w0 = static_cast<int64_t>(c) * share;
         if (lane == 0) {
             bar.start[3] = w0 < total ? static_cast<int>(min(static_cast<int64_t>(share), total - w0)) : 0;
-            bar.share = share;
         }
         if (w0 < total) {
             int carry = 0;
@@ -245,6 +262,11 @@ __device__ __forceinline__ uint32_t map_to_rank(uint32_t smem_addr, uint32_t ran
 }
 // 16-byte store into another CTA's shared memory, counted as transaction bytes on that CTA's
 // mbarrier (the receiver's wait on it orders the data).
+__device__ __forceinline__ void st_async_f32(uint32_t addr, float v, uint32_t bar) {
+    asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.b32 [%0], %1, [%2];" ::"r"(addr),
+                 "r"(__float_as_uint(v)), "r"(bar)
+                 : "memory");
+}
 __device__ __forceinline__ void st_async_v4(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d, uint32_t bar) {
     asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.v4.b32 [%0], {%1, %2, %3, %4}, [%5];" ::"r"(addr),
                  "r"(a), "r"(b), "r"(c), "r"(d), "r"(bar)
@@ -255,20 +277,13 @@ __device__ __forceinline__ void st_async_v4(uint32_t addr, uint32_t a, uint32_t 
 __device__ __forceinline__ void arrive_remote(uint32_t bar) {
     asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
-// mbar_wait that also orders what threads of the peer CTA did before they arrived.
-__device__ __forceinline__ bool mbar_wait_cluster(uint64_t* bar, uint32_t parity, uint64_t deadline) {
-    for (;;) {
-        uint32_t done;
-        asm volatile(
-            "{\n\t.reg .pred p;\n\t"
-            "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
-            "selp.u32 %0, 1, 0, p;\n\t}"
-            : "=r"(done)
-            : "r"(ptx::smem_addr(bar)), "r"(parity)
-            : "memory");
-        if (done) return true;
-        if (static_cast<uint64_t>(clock64()) > deadline) return false;
-    }
+// Arrive on the barrier at this offset in both CTAs once the MMAs issued so far have completed.
+__device__ __forceinline__ void umma_commit_both(uint64_t* bar) {
+    asm volatile(
+        "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+            ptx::smem_addr(bar)),
+        "h"(static_cast<uint16_t>(3))
+        : "memory");
 }
 
 // Descriptor of a K-major operand with the 64-byte swizzle: rows of 64 bytes, 8-row groups 512 apart.
@@ -299,7 +314,8 @@ dense_mla_decode_kernel(const __grid_constant__ CUtensorMap vmap, const __grid_c
     const uint32_t raw_addr = ptx::smem_addr(smem_raw);
     unsigned char* base = smem_raw + (((raw_addr + 1023u) & ~1023u) - raw_addr);
     unsigned char* ring = base;
-    float* xs = reinterpret_cast<float*>(ring + kStages * kStageBytes);            // [2][16 key quads][128 rows][4]
+    unsigned char* ps = ring + kStages * kStageBytes;                              // [2][128 rows][64 keys], 128-byte swizzle
+    float* xs = reinterpret_cast<float*>(ps + 2 * kPBytes);                        // [2][16 key quads][64 rows][4]
     unsigned char* qrope = reinterpret_cast<unsigned char*>(xs) + 2 * kXBytes;     // [128 rows][32 dims], 64-byte swizzle
     DecBars& bar = *reinterpret_cast<DecBars*>(qrope + kQRopeBytes);
 
@@ -309,20 +325,24 @@ dense_mla_decode_kernel(const __grid_constant__ CUtensorMap vmap, const __grid_c
     const int cluster = blockIdx.x >> 1, clusters = gridDim.x >> 1;
 
     if (threadIdx.x == 0) {
-        ptx::mbar_init(&bar.q_full, 4);
+        ptx::mbar_init(&bar.q_full, 8);
         for (int s = 0; s < kStages; ++s) {
             ptx::mbar_init(&bar.kv_full[s], 1);
             ptx::mbar_init(&bar.kv_empty[s], 1);
         }
         for (int a = 0; a < 2; ++a) {
             ptx::mbar_init(&bar.s_full[a], 1);
-            ptx::mbar_init(&bar.s_read[a], 4);
+            ptx::mbar_init(&bar.s_read[a], 8);
             ptx::mbar_init(&bar.x_full[a], 1);
             ptx::mbar_init(&bar.x_free[a], 4);
-            ptx::mbar_init(&bar.p_full[a], 4);
-            ptx::mbar_init(&bar.pv_done[a], 1);
+            ptx::mbar_init(&bar.pair[a], 2);
+            ptx::mbar_init(&bar.p_full[a], 5);
+            ptx::mbar_init(&bar.a_full[a], 1);
+            ptx::mbar_init(&bar.scaled[a], 4);
+            ptx::mbar_init(&bar.pv_done[a], 2);
         }
-        ptx::mbar_init(&bar.o_free, 4);
+        ptx::mbar_init(&bar.o_free, 8);
+        ptx::mbar_init(&bar.fin_full, 1);
         ptx::fence_barrier_init();
     }
     if (warp == kMmaWarp) {
@@ -390,63 +410,83 @@ dense_mla_decode_kernel(const __grid_constant__ CUtensorMap vmap, const __grid_c
             auto wait = [&](uint64_t* b, uint32_t parity) {
                 if (!ptx::mbar_wait(b, parity, deadline)) late = true;
             };
+            const uint64_t p_desc = desc_sw128(ptx::smem_addr(ps), 16, 1024);
             Walk w(bt, bar.start);
-            uint32_t it = 0, seg = 0;
+            uint32_t it = 0, seg = 0;                                // tiles of the pieces before; pieces with tiles
             do {
                 if (w.t0 >= w.t1) continue;
-                auto issue_s = [&](uint32_t u, int t) {              // partial scores of the walk's tile t, ring tile u
-                    const uint32_t s = u % kStages;
-                    wait(&bar.kv_full[s], (u / kStages) & 1u);
-                    const int valid = w.rt.vis0 + w.rt.tokens - 1 - t * kKeys;
-                    if (valid < kKeys) {
-                        // rows past the last visible position may hold anything: their P is 0, but 0 times
-                        // NaN or infinity is not
-                        __syncwarp();
-                        unsigned char* st = ring + s * kStageBytes;
-                        for (int e = lane; e < (kKeys - valid) * 8; e += 32)
-#pragma unroll
-                            for (int j = 0; j < kChunks; ++j)
-                                *reinterpret_cast<uint4*>(st + j * kChunkBytes + (valid + (e >> 3)) * 128 + (e & 7) * 16) =
-                                    make_uint4(0u, 0u, 0u, 0u);
-                        ptx::fence_proxy_async_smem();
-                    }
-                    __syncwarp();
-                    ptx::tc_fence_after_sync();
-                    if (elect_one()) {
-                        const uint64_t so = s * (kStageBytes / 16);
-                        const uint32_t d = tmem + kColS + (u & 1) * kKeys;
-#pragma unroll
-                        for (int j = 0; j < kChunks; ++j)
-#pragma unroll
-                            for (int kk = 0; kk < 4; ++kk)
-                                umma_f16_ts(d, tmem + kColQ + j * 32 + kk * 8, k_desc + so + j * (kChunkBytes / 16) + kk * 2,
-                                            idesc_qk, (j | kk) != 0 ? 1u : 0u);
-#pragma unroll
-                        for (int kk = 0; kk < 2; ++kk)
-                            ptx::umma_f16(d, qr_desc + kk * 2, r_desc + so + kk * 2, idesc_qk, 1u);
-                        ptx::umma_commit(&bar.s_full[u & 1]);
-                    }
-                };
-                wait(&bar.q_full, seg & 1u);
-                issue_s(it, w.t0);
+                const int live = w.rt.tokens * bt.H;
+                const uint32_t peer_quads = (static_cast<int>(peer) * 32 < live ? 1u : 0u) +
+                                            (static_cast<int>(peer + 2) * 32 < live ? 1u : 0u);
                 const uint32_t n = static_cast<uint32_t>(w.t1 - w.t0);
-                for (uint32_t i = 0; i < n; ++i) {
-                    const uint32_t u = it + i;
-                    // its buffer's previous P is read by a P V issued before it
-                    if (i + 1 < n) issue_s(u + 1, w.t0 + static_cast<int>(i) + 1);
-                    if (i == 0 && seg > 0) wait(&bar.o_free, (seg - 1) & 1u);
-                    wait(&bar.p_full[u & 1], (u >> 1) & 1u);
-                    __syncwarp();
-                    ptx::tc_fence_after_sync();
-                    if (elect_one()) {
-                        const uint64_t vb = v_desc + (u % kStages) * (kStageBytes / 16);
-                        const uint32_t p = tmem + kColS + (u & 1) * kKeys;
+                uint32_t iq = 0, ip = 0;                             // next score tile, next P V tile of the piece
+                wait(&bar.q_full, seg & 1u);
+                while (ip < n) {
+                    bool issued = false;
+                    // scores of tile iq: keys landed, the score buffer read
+                    if (iq < n && iq < ip + 2) {
+                        const uint32_t u = it + iq, s = u % kStages;
+                        const bool ready = ptx::mbar_test_wait(&bar.kv_full[s], (u / kStages) & 1u) &&
+                                           (u < 2 || ptx::mbar_test_wait(&bar.s_read[u & 1], ((u >> 1) & 1u) ^ 1u));
+                        if (__all_sync(0xffffffffu, ready)) {
+                            const int valid = w.rt.vis0 + w.rt.tokens - 1 - (w.t0 + static_cast<int>(iq)) * kKeys;
+                            if (valid < kKeys) {
+                                // rows past the last visible position may hold anything: their P is 0, but
+                                // 0 times NaN or infinity is not
+                                unsigned char* st = ring + s * kStageBytes;
+                                for (int e = lane; e < (kKeys - valid) * 8; e += 32)
 #pragma unroll
-                        for (int ks = 0; ks < kKeys / 16; ++ks)
-                            umma_f16_ts(tmem, p + ks * 8, vb + ks * 128, idesc_pv, (i | ks) != 0 ? 1u : 0u);
-                        ptx::umma_commit(&bar.kv_empty[u % kStages]);
-                        ptx::umma_commit(&bar.pv_done[u & 1]);
+                                    for (int j = 0; j < kChunks; ++j)
+                                        *reinterpret_cast<uint4*>(st + j * kChunkBytes + (valid + (e >> 3)) * 128 + (e & 7) * 16) =
+                                            make_uint4(0u, 0u, 0u, 0u);
+                                ptx::fence_proxy_async_smem();
+                                __syncwarp();
+                            }
+                            ptx::tc_fence_after_sync();
+                            if (elect_one()) {
+                                // the previous phase is over: the P V of tile u - 2 has been issued
+                                ptx::mbar_arrive_expect_tx(&bar.p_full[u & 1], peer_quads * (32 * kKeys * 2));
+                                const uint64_t so = s * (kStageBytes / 16);
+                                const uint32_t d = tmem + kColS + (u & 1) * kKeys;
+#pragma unroll
+                                for (int j = 0; j < kChunks; ++j)
+#pragma unroll
+                                    for (int kk = 0; kk < 4; ++kk)
+                                        umma_f16_ts(d, tmem + kColQ + j * 32 + kk * 8, k_desc + so + j * (kChunkBytes / 16) + kk * 2,
+                                                    idesc_qk, (j | kk) != 0 ? 1u : 0u);
+#pragma unroll
+                                for (int kk = 0; kk < 2; ++kk)
+                                    ptx::umma_f16(d, qr_desc + kk * 2, r_desc + so + kk * 2, idesc_qk, 1u);
+                                ptx::umma_commit(&bar.s_full[u & 1]);
+                            }
+                            __syncwarp();
+                            ++iq;
+                            issued = true;
+                        }
                     }
+                    // O += P V of tile ip: P in place, the other rows rescaled, O of the previous row tile read out
+                    if (ip < iq) {
+                        const uint32_t u = it + ip, ph = (u >> 1) & 1u;
+                        const bool ready = ptx::mbar_test_wait(&bar.p_full[u & 1], ph) && ptx::mbar_test_wait(&bar.scaled[u & 1], ph) &&
+                                           (ip > 0 || seg == 0 || ptx::mbar_test_wait(&bar.o_free, (seg - 1) & 1u));
+                        if (__all_sync(0xffffffffu, ready)) {
+                            ptx::fence_proxy_async_smem();           // P comes from ordinary and st.async stores
+                            ptx::tc_fence_after_sync();
+                            if (elect_one()) {
+                                const uint64_t vb = v_desc + (u % kStages) * (kStageBytes / 16);
+                                const uint64_t pb = p_desc + (u & 1) * (kPBytes / 16);
+#pragma unroll
+                                for (int ks = 0; ks < kKeys / 16; ++ks)
+                                    ptx::umma_f16(tmem, pb + ks * 2, vb + ks * 128, idesc_pv, (ip | ks) != 0 ? 1u : 0u);
+                                ptx::umma_commit(&bar.kv_empty[u % kStages]);
+                                umma_commit_both(&bar.pv_done[u & 1]);
+                            }
+                            __syncwarp();
+                            ++ip;
+                            issued = true;
+                        }
+                    }
+                    if (!issued && static_cast<uint64_t>(clock64()) > deadline) late = true;
                     if (__any_sync(0xffffffffu, late)) break;
                 }
                 it += n;
@@ -454,210 +494,280 @@ dense_mla_decode_kernel(const __grid_constant__ CUtensorMap vmap, const __grid_c
             } while (!__any_sync(0xffffffffu, late) && w.next());
             if (late) timed_out = true;
         }
-    } else if (warp >= kSendWarp && warp < kTmaWarp) {
-        // ---------------------------------------------------------------- senders
+    } else if (warp < kTmaWarp) {
+        // ---------------------------------------------------------------- rows
+        if (threadIdx.x == 0 && half == 0) meta[cluster].rows = 0;
         if (work) {
-            const int quad = warp & 3, row = quad * 32 + lane;
+            const int quad = warp & 3, kh = warp >> 2;
+            const int row = quad * 32 + lane;                        // query row of the row tile = tensor-memory lane
+            const bool own = (quad & 1) == half;
+            const int place = (quad >> 1) * 32 + lane;               // among the owned / the other rows
+            const bool lead = (quad >> 1) == 0 && kh == 0 && lane == 0;   // arms this side's barriers
             const uint32_t lane_base = static_cast<uint32_t>(quad * 32) << 16;
-            const uint32_t x_peer = map_to_rank(ptx::smem_addr(xs), peer) + row * 16;
-            Walk w(bt, bar.start);
-            uint32_t it = 0;
-            do {
-                if (w.t0 >= w.t1) continue;
-                const int live = w.rt.tokens * bt.H;
-                const bool quad_live = quad * 32 < live;
-                // the previous row tile's score MMAs are complete: its last s_full has been waited for
-                if (quad_live) {
+            const uint32_t o_addr = tmem + lane_base + kh * 128;     // this warp's 128 of the CTA's 256 output dims
+            const float cs = scale * kLog2e;
+            const uint64_t cs2 = f32x2(cs, cs);
+            const int token = row / bt.H;
+            const uint32_t peer_p = map_to_rank(ptx::smem_addr(ps), peer);
+            const uint32_t peer_x = map_to_rank(ptx::smem_addr(xs), peer) + place * 16 + kh * 8 * (kOwnRows * 16);
+            uint32_t p_off[4];                                       // the row's 16-byte pieces of this key half
+#pragma unroll
+            for (int i = 0; i < 4; ++i) p_off[i] = row * 128 + (((kh * 4 + i) ^ (row & 7)) << 4);
+            uint32_t it = 0, seg = 0, meets = 0;                     // meets: uses of the pair barrier
+            bool q_loaded = false;
+
+            auto wait = [&](uint64_t* b, uint32_t parity) {
+                if (!ptx::mbar_wait(b, parity, deadline)) timed_out = true;
+            };
+            // a row tile's queries: value chunks 2 kh, 2 kh + 1 into tensor memory, rope pieces 2 kh, 2 kh + 1
+            // into shared memory (the score MMAs before are complete: their s_full has been waited for)
+            auto load_q = [&](const RowTile& rt) {
+                const int n = rt.tokens * bt.H;
+                if (quad * 32 < n) {
                     const uint4* src = reinterpret_cast<const uint4*>(
-                        q + (static_cast<int64_t>(w.rt.row0) * bt.H + row) * kLatentDim);
+                        q + (static_cast<int64_t>(rt.row0) * bt.H + row) * kLatentDim);
                     const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
-#pragma unroll 2
-                    for (int j = 0; j < kChunks; ++j) {
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
                         uint32_t v[32];
 #pragma unroll
                         for (int i = 0; i < 8; ++i) {
-                            const uint4 r = row < live ? __ldg(src + half * (kHalf / 8) + j * 8 + i) : zero;
+                            const uint4 r = row < n ? __ldg(src + half * (kHalf / 8) + (2 * kh + j) * 8 + i) : zero;
                             v[4 * i] = r.x; v[4 * i + 1] = r.y; v[4 * i + 2] = r.z; v[4 * i + 3] = r.w;
                         }
-                        tmem_st_x32(tmem + lane_base + kColQ + j * 32, v);
+                        tmem_st_x32(tmem + lane_base + kColQ + (2 * kh + j) * 32, v);
                     }
 #pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        *reinterpret_cast<uint4*>(qrope + row * 64 + ((i ^ ((row >> 1) & 3)) << 4)) =
-                            row < live ? __ldg(src + (kValueDim + half * 32) / 8 + i) : zero;
+                    for (int j = 0; j < 2; ++j)
+                        *reinterpret_cast<uint4*>(qrope + row * 64 + (((2 * kh + j) ^ ((row >> 1) & 3)) << 4)) =
+                            row < n ? __ldg(src + (kValueDim + half * 32) / 8 + 2 * kh + j) : zero;
                     ptx::fence_proxy_async_smem();
                     tmem_wait_st();
                 }
                 ptx::tc_fence_before_sync();
                 __syncwarp();
                 if (lane == 0) ptx::mbar_arrive(&bar.q_full);
-                for (int t = w.t0; t < w.t1 && !timed_out; ++t, ++it) {
-                    const uint32_t bb = it & 1u, ph = (it >> 1) & 1u;
-                    if (!ptx::mbar_wait(&bar.s_full[bb], ph, deadline)) timed_out = true;
-                    if (it >= 2 && !mbar_wait_cluster(&bar.x_free[bb], ph ^ 1u, deadline)) timed_out = true;
-                    timed_out = __any_sync(0xffffffffu, timed_out);
-                    if (timed_out) break;
-                    ptx::tc_fence_after_sync();
-                    if (quad_live) {
-                        uint32_t v[2][32];
-                        const uint32_t s = tmem + lane_base + kColS + bb * kKeys;
-                        ptx::tmem_ld_32x32b_x32(s, v[0]);
-                        ptx::tmem_ld_32x32b_x32(s + 32, v[1]);
-                        ptx::tmem_wait_ld();
-                        const uint32_t dst = x_peer + bb * kXBytes;
-                        const uint32_t xb = map_to_rank(ptx::smem_addr(&bar.x_full[bb]), peer);
+            };
+            // this warp's part of O times alpha, before tile u is added, once the tiles before are
+            auto rescale = [&](float alpha, uint32_t u) {
+                wait(&bar.pv_done[(u - 1) & 1u], ((u - 1) >> 1) & 1u);
+                __syncwarp();
+                ptx::tc_fence_after_sync();
+#pragma unroll 1
+                for (int cc = 0; cc < 128; cc += 32) {
+                    uint32_t o[32];
+                    ptx::tmem_ld_32x32b_x32(o_addr + cc, o);
+                    ptx::tmem_wait_ld();
 #pragma unroll
-                        for (int k4 = 0; k4 < 16; ++k4)
-                            st_async_v4(dst + k4 * (kRows * 16), v[k4 >> 3][(k4 & 7) * 4], v[k4 >> 3][(k4 & 7) * 4 + 1],
-                                        v[k4 >> 3][(k4 & 7) * 4 + 2], v[k4 >> 3][(k4 & 7) * 4 + 3], xb);
-                    }
-                    ptx::tc_fence_before_sync();
-                    __syncwarp();
-                    if (lane == 0) ptx::mbar_arrive(&bar.s_read[bb]);
+                    for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+                    tmem_st_x32(o_addr + cc, o);
                 }
-            } while (!timed_out && w.next());
-        }
-    } else if (warp < kSendWarp) {
-        // ---------------------------------------------------------------- softmax, output
-        if (!work) {
-            if (threadIdx.x == 0 && half == 0 && meta != nullptr) meta[cluster].rows = 0;
-        } else {
-            const int row = warp * 32 + lane;
-            const uint32_t lane_base = static_cast<uint32_t>(warp * 32) << 16;
-            const float cs = scale * kLog2e;
-            const uint64_t cs2 = f32x2(cs, cs);
-            const int token = row / bt.H;                        // of the row tile
-            uint32_t it = 0;
+                tmem_wait_st();
+            };
+            // other rows: tile u's partial scores to the peer
+            auto send = [&](uint32_t u, bool live) {
+                const uint32_t bb = u & 1u, ph = (u >> 1) & 1u;
+                wait(&bar.s_full[bb], ph);
+                if (live) {
+                    __syncwarp();
+                    ptx::tc_fence_after_sync();
+                    uint32_t v[32];
+                    ptx::tmem_ld_32x32b_x32(tmem + lane_base + kColS + bb * kKeys + kh * 32, v);
+                    if (u >= 2) wait(&bar.x_free[bb], ph ^ 1u);
+                    ptx::tmem_wait_ld();
+                    const uint32_t dst = peer_x + bb * kXBytes, xb = map_to_rank(ptx::smem_addr(&bar.x_full[bb]), peer);
+#pragma unroll
+                    for (int k4 = 0; k4 < 8; ++k4)
+                        st_async_v4(dst + k4 * (kOwnRows * 16), v[4 * k4], v[4 * k4 + 1], v[4 * k4 + 2], v[4 * k4 + 3], xb);
+                }
+                ptx::tc_fence_before_sync();
+                __syncwarp();
+                if (lane == 0) ptx::mbar_arrive(&bar.s_read[bb]);
+            };
+
             Walk w(bt, bar.start);
-            if (threadIdx.x == 0 && half == 0 && meta != nullptr) meta[cluster].rows = 0;
-            do {
+            for (;;) {
                 const int live = w.rt.tokens * bt.H;
-                const bool warp_live = warp * 32 < live;
+                const bool quad_live = quad * 32 < live;
+                const uint32_t my_quads = (half * 32 < live ? 1u : 0u) + ((half + 2) * 32 < live ? 1u : 0u);
+                const uint32_t peer_quads = (static_cast<int>(peer) * 32 < live ? 1u : 0u) +
+                                            (static_cast<int>(peer + 2) * 32 < live ? 1u : 0u);
                 const int vis = min(w.rt.vis0 + token, bt.max_pages * kPage);
                 const bool has_tiles = w.t0 < w.t1;
                 float m_run = -INFINITY, l_run = 0.0f;
-                for (int t = w.t0; t < w.t1 && !timed_out; ++t, ++it) {
-                    const uint32_t bb = it & 1u, ph = (it >> 1) & 1u;
-                    const int s = static_cast<int>(it % kStages);
-                    if (threadIdx.x == 0) ptx::mbar_arrive_expect_tx(&bar.x_full[bb], ((live + 31) / 32) * 32 * kKeys * 4);
-                    if (!ptx::mbar_wait(&bar.s_full[bb], ph, deadline)) timed_out = true;
-                    if (!ptx::mbar_wait(&bar.kv_full[s], (it / kStages) & 1u, deadline)) timed_out = true;   // orders page_ok
-                    if (!ptx::mbar_wait(&bar.s_read[bb], ph, deadline)) timed_out = true;
-                    if (!mbar_wait_cluster(&bar.x_full[bb], ph, deadline)) timed_out = true;
-                    timed_out = __any_sync(0xffffffffu, timed_out);
-                    if (timed_out) break;
-                    ptx::tc_fence_after_sync();
-                    if (warp_live) {
-                        const uint32_t sa = tmem + lane_base + kColS + bb * kKeys;
-                        uint32_t v[2][32];
-                        ptx::tmem_ld_32x32b_x32(sa, v[0]);
-                        ptx::tmem_ld_32x32b_x32(sa + 32, v[1]);
-                        const float* xr = xs + bb * (kXBytes / 4) + row * 4;
-                        float4 x[16];
-#pragma unroll
-                        for (int k4 = 0; k4 < 16; ++k4) x[k4] = *reinterpret_cast<const float4*>(xr + k4 * (kRows * 4));
-                        ptx::tmem_wait_ld();
-                        float sc[64];
-#pragma unroll
-                        for (int k4 = 0; k4 < 16; ++k4) {
-                            const uint32_t* p = &v[k4 >> 3][(k4 & 7) * 4];
-                            sc[4 * k4] = __uint_as_float(p[0]) + x[k4].x;
-                            sc[4 * k4 + 1] = __uint_as_float(p[1]) + x[k4].y;
-                            sc[4 * k4 + 2] = __uint_as_float(p[2]) + x[k4].z;
-                            sc[4 * k4 + 3] = __uint_as_float(p[3]) + x[k4].w;
+                if (has_tiles && !q_loaded) load_q(w.rt);
+                if (!own) {
+                    const int n = w.t1 - w.t0;
+                    if (n > 0) send(it, quad_live);
+                    for (int i = 0; i < n; ++i, ++it) {
+                        const uint32_t bb = it & 1u, ph = (it >> 1) & 1u;
+                        if (i + 1 < n) send(it + 1, quad_live);
+                        if (lead) ptx::mbar_arrive_expect_tx(&bar.a_full[bb], peer_quads * 128);
+                        wait(&bar.a_full[bb], ph);
+                        if (quad_live && i > 0) {
+                            const float alpha = bar.alpha[bb][place];
+                            if (__any_sync(0xffffffffu, alpha != 1.0f)) rescale(alpha, it);
                         }
-                        const int lim = bar.page_ok[s] ? vis - t * kKeys : 0;
-                        if (lim < kKeys) {
-#pragma unroll
-                            for (int e = 0; e < 64; ++e)
-                                if (e >= lim) sc[e] = -INFINITY;
-                        }
-                        float mx4[4] = {sc[0], sc[1], sc[2], sc[3]};
-#pragma unroll
-                        for (int e = 4; e < 64; ++e) mx4[e & 3] = fmaxf(mx4[e & 3], sc[e]);
-                        const float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3]));
-                        // every lane's scores have been read (the maximum needs them): the peer may send again
+                        ptx::tc_fence_before_sync();
                         __syncwarp();
-                        if (lane == 0) arrive_remote(map_to_rank(ptx::smem_addr(&bar.x_free[bb]), peer));
-                        const bool grow = (mx - m_run) * cs > kRescaleThreshold || (m_run == -INFINITY && mx > -INFINITY);
-                        if (__any_sync(0xffffffffu, grow)) {
-                            const float alpha = grow ? (m_run == -INFINITY ? 0.0f : exp2f((m_run - mx) * cs)) : 1.0f;
-                            if (grow) m_run = mx;
-                            l_run *= alpha;
-                            if (t > w.t0) {
-                                // O may be rescaled once the previous tile's P V is complete
-                                const uint32_t pb = (it - 1) & 1u;
-                                if (!ptx::mbar_wait(&bar.pv_done[pb], ((it - 1) >> 1) & 1u, deadline)) timed_out = true;
-                                __syncwarp();
-                                ptx::tc_fence_after_sync();
-#pragma unroll 1
-                                for (int cc = 0; cc < kHalf; cc += 32) {
-                                    uint32_t o[32];
-                                    ptx::tmem_ld_32x32b_x32(tmem + lane_base + cc, o);
-                                    ptx::tmem_wait_ld();
+                        if (lane == 0) ptx::mbar_arrive(&bar.scaled[bb]);
+                        timed_out = __any_sync(0xffffffffu, timed_out);
+                        if (timed_out) break;
+                    }
+                } else {
+                    for (int t = w.t0; t < w.t1; ++t, ++it) {
+                        const uint32_t bb = it & 1u, ph = (it >> 1) & 1u;
+                        const int s = static_cast<int>(it % kStages);
+                        if (lead) ptx::mbar_arrive_expect_tx(&bar.x_full[bb], my_quads * (32 * kKeys * 4));
+                        wait(&bar.s_full[bb], ph);
+                        if (quad_live) {
+                            __syncwarp();
+                            ptx::tc_fence_after_sync();
+                            uint32_t v[32];
+                            ptx::tmem_ld_32x32b_x32(tmem + lane_base + kColS + bb * kKeys + kh * 32, v);
+                            wait(&bar.kv_full[s], (it / kStages) & 1u);            // orders page_ok
+                            wait(&bar.x_full[bb], ph);
+                            const float* xr = xs + bb * (kXBytes / 4) + (kh * 8 * kOwnRows + place) * 4;
+                            float4 x[8];
 #pragma unroll
-                                    for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
-                                    tmem_st_x32(tmem + lane_base + cc, o);
-                                }
+                            for (int k4 = 0; k4 < 8; ++k4) x[k4] = *reinterpret_cast<const float4*>(xr + k4 * (kOwnRows * 4));
+                            ptx::tmem_wait_ld();
+                            ptx::tc_fence_before_sync();
+                            __syncwarp();
+                            if (lane == 0) ptx::mbar_arrive(&bar.s_read[bb]);
+                            float sc[32];
+#pragma unroll
+                            for (int k4 = 0; k4 < 8; ++k4) {
+                                sc[4 * k4] = __uint_as_float(v[4 * k4]) + x[k4].x;
+                                sc[4 * k4 + 1] = __uint_as_float(v[4 * k4 + 1]) + x[k4].y;
+                                sc[4 * k4 + 2] = __uint_as_float(v[4 * k4 + 2]) + x[k4].z;
+                                sc[4 * k4 + 3] = __uint_as_float(v[4 * k4 + 3]) + x[k4].w;
                             }
-                        }
-                        const float neg = m_run == -INFINITY ? 0.0f : -m_run * cs;
-                        const uint64_t neg2 = f32x2(neg, neg);
-                        uint64_t sum2 = f32x2(0.0f, 0.0f);
+                            const int lim = (bar.page_ok[s] ? vis - t * kKeys : 0) - kh * 32;
+                            if (lim < 32) {
 #pragma unroll
-                        for (int hh = 0; hh < 2; ++hh) {
+                                for (int e = 0; e < 32; ++e)
+                                    if (e >= lim) sc[e] = -INFINITY;
+                            }
+                            float mx4[4] = {sc[0], sc[1], sc[2], sc[3]};
+#pragma unroll
+                            for (int e = 4; e < 32; ++e) mx4[e & 3] = fmaxf(mx4[e & 3], sc[e]);
+                            float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3]));
+                            // the tile's maximum over both key halves (values double-buffered by tile parity)
+                            bar.tmax[bb][kh][place] = mx;
+                            // every lane's scores have been read (the maximum needs them): the peer may send again
+                            __syncwarp();
+                            if (lane == 0) {
+                                ptx::mbar_arrive(&bar.pair[quad >> 1]);
+                                arrive_remote(map_to_rank(ptx::smem_addr(&bar.x_free[bb]), peer));
+                            }
+                            wait(&bar.pair[quad >> 1], meets & 1u);
+                            ++meets;
+                            mx = fmaxf(mx, bar.tmax[bb][kh ^ 1][place]);
+                            const bool grow = (mx - m_run) * cs > kRescaleThreshold || (m_run == -INFINITY && mx > -INFINITY);
+                            float alpha = 1.0f;
+                            if (__any_sync(0xffffffffu, grow)) {
+                                if (grow) {
+                                    alpha = m_run == -INFINITY ? 0.0f : exp2f((m_run - mx) * cs);
+                                    m_run = mx;
+                                }
+                                l_run *= alpha;
+                                if (t > w.t0) rescale(alpha, it);
+                            }
+                            const float neg = m_run == -INFINITY ? 0.0f : -m_run * cs;
+                            const uint64_t neg2 = f32x2(neg, neg);
+                            uint64_t sum2 = f32x2(0.0f, 0.0f);
                             uint32_t pk[16];
 #pragma unroll
                             for (int e = 0; e < 32; e += 2) {
                                 float a, b;
-                                unpack_f32x2(fma_f32x2(f32x2(sc[32 * hh + e], sc[32 * hh + e + 1]), cs2, neg2), a, b);
+                                unpack_f32x2(fma_f32x2(f32x2(sc[e], sc[e + 1]), cs2, neg2), a, b);
                                 a = fast_exp2(a);
                                 b = fast_exp2(b);
                                 sum2 = add_f32x2(sum2, f32x2(a, b));
                                 pk[e / 2] = pack_bf16x2(a, b);
                             }
-                            tmem_st_x16(sa + 16 * hh, pk);
+                            // the P V that read the buffer's previous P is complete in both CTAs
+                            if (it >= 2) wait(&bar.pv_done[bb], ph ^ 1u);
+                            const uint32_t pb = map_to_rank(ptx::smem_addr(&bar.p_full[bb]), peer);
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) {
+                                st_async_v4(peer_p + bb * kPBytes + p_off[i], pk[4 * i], pk[4 * i + 1], pk[4 * i + 2], pk[4 * i + 3], pb);
+                                *reinterpret_cast<uint4*>(ps + bb * kPBytes + p_off[i]) =
+                                    make_uint4(pk[4 * i], pk[4 * i + 1], pk[4 * i + 2], pk[4 * i + 3]);
+                            }
+                            if (kh == 0)
+                                st_async_f32(map_to_rank(ptx::smem_addr(&bar.alpha[bb][place]), peer), alpha,
+                                             map_to_rank(ptx::smem_addr(&bar.a_full[bb]), peer));
+                            ptx::fence_proxy_async_smem();
+                            float a, b;
+                            unpack_f32x2(sum2, a, b);
+                            l_run += a + b;
+                        } else if (lane == 0) {
+                            ptx::mbar_arrive(&bar.s_read[bb]);
+                            arrive_remote(map_to_rank(ptx::smem_addr(&bar.x_free[bb]), peer));
                         }
-                        tmem_wait_st();
-                        float a, b;
-                        unpack_f32x2(sum2, a, b);
-                        l_run += a + b;
-                    } else if (lane == 0) {
-                        arrive_remote(map_to_rank(ptx::smem_addr(&bar.x_free[bb]), peer));
+                        ptx::tc_fence_before_sync();
+                        __syncwarp();
+                        if (lane == 0) ptx::mbar_arrive(&bar.p_full[bb]);
+                        timed_out = __any_sync(0xffffffffu, timed_out);
+                        if (timed_out) break;
                     }
-                    ptx::tc_fence_before_sync();
-                    __syncwarp();
-                    if (lane == 0) ptx::mbar_arrive(&bar.p_full[bb]);
                 }
+                if (timed_out) break;
+                // ---- the next row tile's queries, so that its first scores run during this one's output
+                Walk nxt = w;
+                const bool more = nxt.next();
+                q_loaded = more && nxt.t0 < nxt.t1;
+                if (q_loaded) load_q(nxt.rt);
                 // ---- the piece's output: O / l and its log-sum-exp (log2 units for a part)
-                bool have_o = has_tiles && !timed_out;
-                if (have_o) {
-                    const bool got = ptx::mbar_wait(&bar.pv_done[(it - 1) & 1u], ((it - 1) >> 1) & 1u, deadline);
-                    have_o = __all_sync(0xffffffffu, got);
-                    if (!have_o) timed_out = true;
+                float inv = -1.0f;                                   // -1: nothing visible (O may hold 0 x NaN)
+                if (own && quad_live) {
+                    float l_tot = 0.0f;
+                    if (has_tiles) {
+                        bar.lsum[kh][place] = l_run;
+                        __syncwarp();
+                        if (lane == 0) ptx::mbar_arrive(&bar.pair[quad >> 1]);
+                        wait(&bar.pair[quad >> 1], meets & 1u);
+                        ++meets;
+                        l_tot = l_run + bar.lsum[kh ^ 1][place];
+                        if (l_tot != 0.0f) inv = 1.0f / l_tot;
+                    }
+                    if (kh == 0) {
+                        if (has_tiles)
+                            st_async_f32(map_to_rank(ptx::smem_addr(&bar.fin[place]), peer), inv,
+                                         map_to_rank(ptx::smem_addr(&bar.fin_full), peer));
+                        if (row < live) {
+                            const float lse2 = l_tot == 0.0f ? -INFINITY : m_run * cs + log2f(l_tot);
+                            if (!w.whole) part_lse[piece_slot(cluster, w) * slot_rows + row] = lse2;
+                            else if (lse_out != nullptr) lse_out[static_cast<int64_t>(w.rt.row0) * bt.H + row] = lse2 * kLn2;
+                        }
+                    }
+                } else if (!own && has_tiles) {
+                    if (lead) ptx::mbar_arrive_expect_tx(&bar.fin_full, peer_quads * 128);
+                    wait(&bar.fin_full, seg & 1u);
+                    inv = bar.fin[place];
+                }
+                if (has_tiles) {
+                    wait(&bar.pv_done[(it - 1) & 1u], ((it - 1) >> 1) & 1u);
+                    timed_out = __any_sync(0xffffffffu, timed_out);
+                    if (timed_out) break;
                     ptx::tc_fence_after_sync();
                 }
-                if (warp_live) {
-                    const float inv = l_run == 0.0f ? 0.0f : 1.0f / l_run;
-                    const bool none = l_run == 0.0f;             // nothing visible: O may hold 0 x NaN
-                    const float lse2 = none ? -INFINITY : m_run * cs + log2f(l_run);
-                    const int64_t orow = static_cast<int64_t>(w.rt.row0) * bt.H + row;
-                    // the piece that starts the share and not its row tile: slot 2 c; any other part: 2 c + 1
-                    const int64_t slot = 2 * static_cast<int64_t>(cluster) + ((w.first && w.t0 > 0) ? 0 : 1);
-                    uint16_t* dst = out + orow * kValueDim + half * kHalf;
-                    float* pdst = part_o + (slot * slot_rows + row) * kValueDim + half * kHalf;
+                if (quad_live) {
+                    const int dim = half * kHalf + kh * 128;
+                    uint16_t* dst = out + (static_cast<int64_t>(w.rt.row0) * bt.H + row) * kValueDim + dim;
+                    float* pdst = part_o + (piece_slot(cluster, w) * slot_rows + row) * kValueDim + dim;
 #pragma unroll 1
-                    for (int cc = 0; cc < kHalf; cc += 32) {
+                    for (int cc = 0; cc < 128; cc += 32) {
                         uint32_t o[32];
-                        if (have_o) {
-                            ptx::tmem_ld_32x32b_x32(tmem + lane_base + cc, o);
+                        if (has_tiles) {
+                            ptx::tmem_ld_32x32b_x32(o_addr + cc, o);
                             ptx::tmem_wait_ld();
                         }
 #pragma unroll
-                        for (int e = 0; e < 32; ++e) {
-                            if (!have_o || none) o[e] = 0u;
-                            o[e] = __float_as_uint(__uint_as_float(o[e]) * inv);
-                        }
+                        for (int e = 0; e < 32; ++e)
+                            o[e] = inv < 0.0f ? 0u : __float_as_uint(__uint_as_float(o[e]) * inv);
                         if (row < live) {
                             if (w.whole) {
 #pragma unroll
@@ -674,20 +784,19 @@ dense_mla_decode_kernel(const __grid_constant__ CUtensorMap vmap, const __grid_c
                             }
                         }
                     }
-                    if (row < live && half == 0) {
-                        if (!w.whole) part_lse[slot * slot_rows + row] = lse2;
-                        else if (lse_out != nullptr) lse_out[orow] = lse2 * kLn2;
-                    }
                 }
                 if (has_tiles) {
                     ptx::tc_fence_before_sync();
                     __syncwarp();
                     if (lane == 0) ptx::mbar_arrive(&bar.o_free);
+                    ++seg;
                 }
                 // the last piece of a split row tile: the combine kernel finds it here
                 if (threadIdx.x == 0 && half == 0 && w.first && w.t0 > 0 && w.t1 == w.rt.tiles)
                     meta[cluster] = Meta{static_cast<int64_t>(w.rt.row0) * bt.H, live, bar.first_cluster};
-            } while (!timed_out && w.next());
+                if (!more) break;
+                w = nxt;
+            }
         }
     }
     if (timed_out) raise_error(err, DSA_DEVERR_TIMEOUT);
