@@ -13,28 +13,29 @@
 //
 // Bound: HBM, 1152 bytes per cached token and request.  A tile of up to 128 query rows (heads x new
 // tokens of one request) needs 2176 FLOP per row and key, 70 % of the tensor time that the copy of
-// the key takes, and its output accumulator (128 x 512 fp32) alone would fill the tensor memory.  So
-// two CTAs of a cluster share a row tile: rank c owns the value dims 256 c .. 256 c + 255 and the rope
-// dims 512 + 32 c .. 512 + 32 c + 31, reads only those of every cached row, forms the partial scores
-// over them and accumulates its own 256 output dims.  The softmax is split by rows: rank c owns the
-// 32-row groups c and c + 2; it receives the peer's partial scores of them (fp32, st.async into its
-// shared memory), and sends P (bf16) and the rescaling factors back.  That is 24 KB a tile and
-// direction over the cluster network (about 32 bytes a cycle), where a swap of all partial scores
-// took 32 KB and the whole softmax in both CTAs.
+// the key takes, and its output accumulator (128 x 512 fp32) fills the tensor memory of an SM.  So a
+// row tile is a pipeline over the two CTAs of a cluster: rank 0 forms the scores and the softmax and
+// sends P (bf16, 16 KB a tile of 64 keys) and the rescaling factors into rank 1's shared memory
+// (st.async); rank 1 accumulates all 512 output dims and writes them.  Nothing flows back but
+// "buffer free", so latencies overlap; the products are 1152 cycles a tile in rank 0 and 1024 in rank
+// 1, where the copy of a tile's keys from HBM takes about 1560.  Both ranks read a page (rank 1 its 512
+// value dims), the second time from L2.  Splitting the dims instead, half of the scores' inner
+// dimension and of the outputs each, reads every byte once but swaps partial scores every tile: two
+// trips over the cluster network in every tile's chain, measured at 3200 cycles a tile.
 //
 // Work: the key tiles (64 positions = one page) of all row tiles in one sequence, cut into equal shares,
 // one per cluster (at least kMinShare tiles).  A row tile that lies within one share is written
 // directly; the pieces of the others go to the workspace and the combine kernel joins them.
 //
-// Roles (384 threads):
-//   warps 0-7  rows: warp w has the rows (tensor-memory lanes) 32 (w % 4) .. + 31 and key half w / 4.
-//              Owned rows: own scores + the peer's, softmax, P to both CTAs' shared memory.  Other
-//              rows: partial scores to the peer, O rescaled by the peer's factors.  Queries into
-//              tensor memory; output of 128 of the 256 dims at a row tile's end;
-//   warp 8     TMA: the CTA's dims of each page, 4 chunks of 64 value dims and 32 rope dims, 4-deep ring;
-//   warp 9     MMA: S = Q K^T (A in tensor memory, rope part in shared memory), two tiles ahead, and
-//              O += P V (P in shared memory), whichever is ready; warps 10 and 11 idle.
-// Tensor memory: O (columns 0-255), two score tiles (256-383), the CTA's 4 query chunks (384-511).
+// Roles (384 threads), warps 10 and 11 idle:
+//   rank 0  warps 0-7  softmax: rows (tensor-memory lanes) 32 (w % 4) .. + 31, key half w / 4; queries
+//                      into tensor memory (value dims) and shared memory (rope dims);
+//           warp 8     TMA: pages as 9 chunks of 64 dims, ring of 8 stages of 3 chunks;
+//           warp 9     MMA: S = Q K^T into a ring of 4 score tiles.
+//   rank 1  warps 0-7  O rescaled where a factor is not 1; O / l to the output, 256 dims a warp;
+//           warp 8     TMA: value chunks, ring of 5 stages of 4 chunks (half of the value dims);
+//           warp 9     MMA: O += P V, one N = 256 half per stage.
+// Tensor memory: rank 0 query chunks (columns 0-255) and score tiles (256-511), rank 1 O (0-511).
 #include <cuda_bf16.h>
 
 #include <algorithm>
@@ -48,49 +49,48 @@ using namespace attn;
 
 constexpr int kRows = 128;                                      // query rows of a row tile (MMA M)
 constexpr int kKeys = 64;                                       // keys of a tile: one page
-constexpr int kChunks = 4;                                      // value chunks (64 dims) per CTA
-constexpr int kChunkBytes = kKeys * 128;                        // 8192, 128-byte swizzle
-constexpr int kRopeBytes = kKeys * 64;                          // 4096, 64-byte swizzle
-constexpr int kStageBytes = kChunks * kChunkBytes + kRopeBytes; // 36864
-constexpr int kStages = 4;
-constexpr int kOwnRows = kRows / 2;                             // rows whose softmax a CTA takes
-constexpr int kXBytes = kOwnRows * kKeys * 4;                   // 16384: the peer's partial scores of them
+constexpr int kChunkBytes = kKeys * 128;                        // 64 keys x 64 dims, 128-byte swizzle
+constexpr int kKStageChunks = 3, kKStages = 8;                  // rank 0: a tile is 3 stages
+constexpr int kVStageChunks = 4, kVStages = 5;                  // rank 1: a tile is 2 stages
+constexpr int kPBufs = 3, kSBufs = 4;
 constexpr int kPBytes = kRows * kKeys * 2;                      // 16384: P, K-major, 128-byte swizzle
-constexpr int kQRopeBytes = kRows * 64;                         // 8192
+constexpr int kQRopeBytes = kRows * 128;                        // 16384
+constexpr int kDataBytes = kKStages * kKStageChunks * kChunkBytes + kQRopeBytes;
+static_assert(kVStages * kVStageChunks * kChunkBytes + kPBufs * kPBytes <= kDataBytes, "rank 1 fits rank 0's layout");
 constexpr int kTmaWarp = 8, kMmaWarp = 9;
 constexpr int kDecThreads = 384;
-constexpr uint32_t kColS = 256, kColQ = 384;
-constexpr int kHalf = kValueDim / 2;
+constexpr uint32_t kColS = 256;                                 // rank 0: score tiles, behind the query chunks
 constexpr int kMaxRequests = 16384;                             // prefix sums of the schedule fit the ring
 constexpr int kMinShare = 4;
-constexpr size_t kDecSmem = 1024 + size_t(kStages) * kStageBytes + 2 * size_t(kXBytes + kPBytes) + kQRopeBytes + 4096;
+constexpr size_t kDecSmem = 1024 + size_t(kDataBytes) + 5120;
 static_assert(kDecSmem <= 232448, "shared-memory budget");
-static_assert(kMaxRequests * 4 <= kStages * kStageBytes, "schedule scratch");
+static_assert(kMaxRequests * 4 <= kDataBytes, "schedule scratch");
 
 struct DecBars {
-    uint64_t q_full;                        // queries in place (8 row warps), per row tile
-    uint64_t kv_full[kStages], kv_empty[kStages];
-    uint64_t s_full[2];                     // partial scores complete
-    uint64_t s_read[2];                     // ... and read (8 row warps)
-    uint64_t x_full[2];                     // the peer's partial scores of the owned rows arrived (armed + bytes)
-    uint64_t x_free[2];                     // the peer has read the ones sent to it (its 4 owning warps)
-    uint64_t pair[2];                       // both key halves of an owned row group have written (2 warps)
-    uint64_t p_full[2];                     // P in place: 4 owning warps here, armed + bytes from the peer
-    uint64_t a_full[2];                     // the peer's rescaling factors arrived (armed + bytes)
-    uint64_t scaled[2];                     // O of the other rows rescaled by them (4 warps)
-    uint64_t pv_done[2];                    // P V of the tile complete in both CTAs
+    uint64_t kv_full[kKStages], kv_empty[kKStages];
+    // rank 0
+    uint64_t q_full;                        // queries in place (8 softmax warps), per row tile
+    uint64_t s_full[kSBufs];                // scores complete; tile_ok written
+    uint64_t s_read[kSBufs];                // ... and read (8 warps)
+    uint64_t pair[4];                       // both key halves of a row group have written (2 warps)
+    uint64_t p_free[kPBufs];                // rank 1's P V that read the buffer is complete
+    uint64_t fin_free;                      // rank 1 has read 1 / l (its 8 row warps), per row tile
+    // rank 1
+    uint64_t p_full[kPBufs];                // P and the factors arrived (armed + bytes)
+    uint64_t scaled[kPBufs];                // O rescaled by them (8 row warps)
+    uint64_t pv_done[kPBufs];               // P V of the tile complete (as many as tiles the row warps may be ahead)
     uint64_t o_free;                        // O read out (8 row warps), per row tile
-    uint64_t fin_full;                      // the peer's 1 / l arrived (armed + bytes), per row tile
+    uint64_t fin_full;                      // 1 / l arrived (armed + bytes), per row tile
     uint32_t tmem_slot;
-    int page_ok[kStages];                   // the stage's page id was valid
+    int page_ok[kKStages];                  // the stage's page id was valid
+    int tile_ok[kSBufs];                    // ... of the score tile's page
     int start[4];                           // first request, first row tile of it, first key tile, tiles of the share
     int first_cluster;                      // cluster that holds the first piece of the first row tile
-    float tmax[2][2][kOwnRows];             // [tile parity][key half][owned row]: maximum of the tile
-    float lsum[2][kOwnRows];                // [key half]: sums at a row tile's end
-    float alpha[2][kOwnRows];               // [tile parity]: the peer's factors of the other rows
-    float fin[kOwnRows];                    // the peer's 1 / l of the other rows; -1: nothing visible
+    float tmax[2][2][kRows];                // rank 0: [tile parity][key half][row]: maximum of the tile
+    float alpha[kPBufs][kRows];             // rank 1: the factors of the tile
+    float fin[kRows];                       // rank 1: 1 / l; -1: nothing visible
 };
-static_assert(sizeof(DecBars) <= 4096, "barrier block");
+static_assert(sizeof(DecBars) <= 5120, "barrier block");
 
 struct Batch {
     const int32_t* seq_lens;
@@ -277,24 +277,13 @@ __device__ __forceinline__ void st_async_v4(uint32_t addr, uint32_t a, uint32_t 
 __device__ __forceinline__ void arrive_remote(uint32_t bar) {
     asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
-// Arrive on the barrier at this offset in both CTAs once the MMAs issued so far have completed.
-__device__ __forceinline__ void umma_commit_both(uint64_t* bar) {
+// Arrive on the barrier at this offset in rank 0 once the MMAs issued so far have completed.
+__device__ __forceinline__ void umma_commit_rank0(uint64_t* bar) {
     asm volatile(
         "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
             ptx::smem_addr(bar)),
-        "h"(static_cast<uint16_t>(3))
+        "h"(static_cast<uint16_t>(1))
         : "memory");
-}
-
-// Descriptor of a K-major operand with the 64-byte swizzle: rows of 64 bytes, 8-row groups 512 apart.
-__device__ __forceinline__ uint64_t desc_sw64(uint32_t addr) {
-    uint64_t d = 0;
-    d |= static_cast<uint64_t>((addr >> 4) & 0x3FFFu);
-    d |= static_cast<uint64_t>(1u) << 16;
-    d |= static_cast<uint64_t>(512u >> 4) << 32;
-    d |= static_cast<uint64_t>(1u) << 46;
-    d |= static_cast<uint64_t>(4u) << 61;
-    return d;
 }
 
 // What a cluster leaves for the combine kernel: the split row tile whose last piece it computed.
@@ -305,51 +294,49 @@ struct Meta {
 };
 
 __global__ void __launch_bounds__(kDecThreads, 1) __cluster_dims__(2, 1, 1)
-dense_mla_decode_kernel(const __grid_constant__ CUtensorMap vmap, const __grid_constant__ CUtensorMap rmap,
-                        const uint16_t* __restrict__ q, int num_pages, const int32_t* __restrict__ block_table,
-                        Batch bt, float scale, uint16_t* __restrict__ out, float* __restrict__ lse_out,
-                        float* __restrict__ part_o, float* __restrict__ part_lse, Meta* __restrict__ meta, int slot_rows,
-                        int32_t* err) {
+dense_mla_decode_kernel(const __grid_constant__ CUtensorMap kvmap, const uint16_t* __restrict__ q, int num_pages,
+                        const int32_t* __restrict__ block_table, Batch bt, float scale, uint16_t* __restrict__ out,
+                        float* __restrict__ lse_out, float* __restrict__ part_o, float* __restrict__ part_lse,
+                        Meta* __restrict__ meta, int slot_rows, int32_t* err) {
     extern __shared__ unsigned char smem_raw[];
     const uint32_t raw_addr = ptx::smem_addr(smem_raw);
     unsigned char* base = smem_raw + (((raw_addr + 1023u) & ~1023u) - raw_addr);
-    unsigned char* ring = base;
-    unsigned char* ps = ring + kStages * kStageBytes;                              // [2][128 rows][64 keys], 128-byte swizzle
-    float* xs = reinterpret_cast<float*>(ps + 2 * kPBytes);                        // [2][16 key quads][64 rows][4]
-    unsigned char* qrope = reinterpret_cast<unsigned char*>(xs) + 2 * kXBytes;     // [128 rows][32 dims], 64-byte swizzle
-    DecBars& bar = *reinterpret_cast<DecBars*>(qrope + kQRopeBytes);
+    unsigned char* ring = base;                                                   // both ranks: key / value stages
+    unsigned char* qrope = base + kKStages * kKStageChunks * kChunkBytes;         // rank 0: [128 rows][64 dims]
+    unsigned char* ps = base + kVStages * kVStageChunks * kChunkBytes;            // rank 1: [3][128 rows][64 keys]
+    DecBars& bar = *reinterpret_cast<DecBars*>(base + kDataBytes);
 
     const int warp = uniform(static_cast<int>(threadIdx.x >> 5)), lane = threadIdx.x & 31;
-    const uint32_t crank = cluster_ctarank(), peer = crank ^ 1u;
-    const int half = static_cast<int>(crank);
+    const uint32_t rank = cluster_ctarank();
     const int cluster = blockIdx.x >> 1, clusters = gridDim.x >> 1;
 
     if (threadIdx.x == 0) {
-        ptx::mbar_init(&bar.q_full, 8);
-        for (int s = 0; s < kStages; ++s) {
+        for (int s = 0; s < kKStages; ++s) {
             ptx::mbar_init(&bar.kv_full[s], 1);
             ptx::mbar_init(&bar.kv_empty[s], 1);
         }
-        for (int a = 0; a < 2; ++a) {
-            ptx::mbar_init(&bar.s_full[a], 1);
-            ptx::mbar_init(&bar.s_read[a], 8);
-            ptx::mbar_init(&bar.x_full[a], 1);
-            ptx::mbar_init(&bar.x_free[a], 4);
-            ptx::mbar_init(&bar.pair[a], 2);
-            ptx::mbar_init(&bar.p_full[a], 5);
-            ptx::mbar_init(&bar.a_full[a], 1);
-            ptx::mbar_init(&bar.scaled[a], 4);
-            ptx::mbar_init(&bar.pv_done[a], 2);
+        ptx::mbar_init(&bar.q_full, 8);
+        for (int i = 0; i < kSBufs; ++i) {
+            ptx::mbar_init(&bar.s_full[i], 2);
+            ptx::mbar_init(&bar.s_read[i], 8);
+        }
+        for (int i = 0; i < 4; ++i) ptx::mbar_init(&bar.pair[i], 2);
+        for (int i = 0; i < kPBufs; ++i) {
+            ptx::mbar_init(&bar.p_free[i], 1);
+            ptx::mbar_init(&bar.p_full[i], 1);
+            ptx::mbar_init(&bar.scaled[i], 8);
+            ptx::mbar_init(&bar.pv_done[i], 1);
         }
         ptx::mbar_init(&bar.o_free, 8);
         ptx::mbar_init(&bar.fin_full, 1);
+        ptx::mbar_init(&bar.fin_free, 8);
         ptx::fence_barrier_init();
     }
     if (warp == kMmaWarp) {
         ptx::tmem_alloc(&bar.tmem_slot, 512);
         ptx::tmem_relinquish();
     }
-    find_share(bt, cluster, clusters, reinterpret_cast<int*>(ring), bar, half == 0 ? err : nullptr);
+    find_share(bt, cluster, clusters, reinterpret_cast<int*>(ring), bar, rank == 0 ? err : nullptr);
     ptx::fence_proxy_async_smem();   // the schedule's scratch lies where copies will land
     ptx::tc_fence_before_sync();
     cluster_sync_all();              // both CTAs' barriers exist before the peer signals or writes into them
@@ -358,446 +345,414 @@ dense_mla_decode_kernel(const __grid_constant__ CUtensorMap vmap, const __grid_c
     const uint64_t deadline = ptx::wait_deadline();
     bool timed_out = false;
     const bool work = uniform(bar.start[3]) > 0;
+    const uint32_t ring_addr = ptx::smem_addr(ring);
+    if (threadIdx.x == 0 && rank == 1) meta[cluster].rows = 0;
 
-    if (warp == kTmaWarp) {
-        // ---------------------------------------------------------------- TMA
-        if (work) {
-            Walk w(bt, bar.start);
-            uint32_t it = 0;
-            do {
-                int page = -1;
-                for (int t = w.t0; t < w.t1 && !timed_out; ++t, ++it) {
-                    if (((t - w.t0) & 31) == 0)                      // page ids of the next 32 tiles
-                        page = t + lane < w.t1 ? __ldg(block_table + static_cast<int64_t>(w.b) * bt.max_pages + t + lane) : 0;
-                    const int pg = __shfl_sync(0xffffffffu, page, (t - w.t0) & 31);
-                    const int s = static_cast<int>(it % kStages);
-                    if (lane == 0) {
-                        const bool ok = pg >= 0 && pg < num_pages;
-                        // a page outside the pool: a box past the end reads zeros, and nothing of it counts
-                        const int row = (ok ? pg : num_pages) * kPage;
-                        if (!ok) raise_error(err, DSA_DEVERR_PAGE_RANGE);
-                        if (!ptx::mbar_wait(&bar.kv_empty[s], ((it / kStages) & 1u) ^ 1u, deadline)) {
-                            timed_out = true;
-                        } else {
-                            bar.page_ok[s] = ok ? 1 : 0;
-                            ptx::mbar_arrive_expect_tx(&bar.kv_full[s], kStageBytes);
-                            unsigned char* st = ring + s * kStageBytes;
-#pragma unroll
-                            for (int j = 0; j < kChunks; ++j)
-                                ptx::tma_load_3d(st + j * kChunkBytes, &vmap, &bar.kv_full[s], half * kHalf + 64 * j, 0, row);
-                            ptx::tma_load_3d(st + kChunks * kChunkBytes, &rmap, &bar.kv_full[s], kValueDim + half * 32, 0, row);
-                        }
-                    }
+    if (work && warp == kTmaWarp) {
+        // ---------------------------------------------------------------- TMA (both ranks)
+        const int chunks = rank == 0 ? kKStageChunks : kVStageChunks, per_tile = rank == 0 ? 3 : 2;
+        const uint32_t stages = rank == 0 ? kKStages : kVStages;
+        Walk w(bt, bar.start);
+        uint32_t s = 0, ph = 0, used = 0;                            // stage, its phase, stages used so far
+        do {
+            int page = -1;
+            for (int t = w.t0; t < w.t1 && !timed_out; ++t) {
+                if (((t - w.t0) & 31) == 0)                          // page ids of the next 32 tiles
+                    page = t + lane < w.t1 ? __ldg(block_table + static_cast<int64_t>(w.b) * bt.max_pages + t + lane) : 0;
+                const int pg = __shfl_sync(0xffffffffu, page, (t - w.t0) & 31);
+                const bool ok = pg >= 0 && pg < num_pages;
+                // a page outside the pool: a box past the end reads zeros, and rank 0 masks its keys
+                const int row = (ok ? pg : num_pages) * kPage;
+                if (!ok && lane == 0 && rank == 0) raise_error(err, DSA_DEVERR_PAGE_RANGE);
+                for (int i = 0; i < per_tile; ++i) {
+                    if (!ptx::mbar_wait(&bar.kv_empty[s], ph ^ 1u, deadline)) timed_out = true;
                     timed_out = __any_sync(0xffffffffu, timed_out);
+                    if (timed_out) break;
+                    if (elect_one()) {
+                        if (rank == 0) bar.page_ok[s] = ok ? 1 : 0;
+                        ptx::mbar_arrive_expect_tx(&bar.kv_full[s], chunks * kChunkBytes);
+                        unsigned char* st = ring + s * chunks * kChunkBytes;
+                        for (int j = 0; j < chunks; ++j)
+                            ptx::tma_load_3d(st + j * kChunkBytes, &kvmap, &bar.kv_full[s], (i * chunks + j) * 64, 0, row);
+                    }
+                    __syncwarp();
+                    ++used;
+                    if (++s == stages) {
+                        s = 0;
+                        ph ^= 1u;
+                    }
                 }
-            } while (!timed_out && w.next());
-            // copies still in flight land before the CTA may leave (bounded)
-            if (lane == 0)
-                for (uint32_t j = it > kStages ? it - kStages : 0; j < it; ++j)
-                    if (!ptx::mbar_wait(&bar.kv_full[j % kStages], (j / kStages) & 1u, ptx::wait_deadline(20000000ull)))
-                        timed_out = true;
-        }
-    } else if (warp == kMmaWarp) {
-        // ---------------------------------------------------------------- MMA
-        if (work) {
-            constexpr uint32_t idesc_qk = ptx::instr_desc(1, 1, kRows, kKeys);
-            constexpr uint32_t idesc_pv = ptx::instr_desc(1, 1, kRows, kHalf) | (1u << 16);   // B MN-major
-            const uint32_t ring_addr = ptx::smem_addr(ring);
-            const uint64_t k_desc = desc_sw128(ring_addr, 16, 1024), v_desc = desc_sw128(ring_addr, kChunkBytes, 1024);
-            const uint64_t r_desc = desc_sw64(ring_addr + kChunks * kChunkBytes), qr_desc = desc_sw64(ptx::smem_addr(qrope));
-            // a wait that ran out only marks the step; the warp leaves at the step's end
-            bool late = false;
-            auto wait = [&](uint64_t* b, uint32_t parity) {
-                if (!ptx::mbar_wait(b, parity, deadline)) late = true;
-            };
-            const uint64_t p_desc = desc_sw128(ptx::smem_addr(ps), 16, 1024);
-            Walk w(bt, bar.start);
-            uint32_t it = 0, seg = 0;                                // tiles of the pieces before; pieces with tiles
-            do {
-                if (w.t0 >= w.t1) continue;
-                const int live = w.rt.tokens * bt.H;
-                const uint32_t peer_quads = (static_cast<int>(peer) * 32 < live ? 1u : 0u) +
-                                            (static_cast<int>(peer + 2) * 32 < live ? 1u : 0u);
-                const uint32_t n = static_cast<uint32_t>(w.t1 - w.t0);
-                uint32_t iq = 0, ip = 0;                             // next score tile, next P V tile of the piece
-                wait(&bar.q_full, seg & 1u);
-                while (ip < n) {
-                    bool issued = false;
-                    // scores of tile iq: keys landed, the score buffer read
-                    if (iq < n && iq < ip + 2) {
-                        const uint32_t u = it + iq, s = u % kStages;
-                        const bool ready = ptx::mbar_test_wait(&bar.kv_full[s], (u / kStages) & 1u) &&
-                                           (u < 2 || ptx::mbar_test_wait(&bar.s_read[u & 1], ((u >> 1) & 1u) ^ 1u));
-                        if (__all_sync(0xffffffffu, ready)) {
-                            const int valid = w.rt.vis0 + w.rt.tokens - 1 - (w.t0 + static_cast<int>(iq)) * kKeys;
-                            if (valid < kKeys) {
-                                // rows past the last visible position may hold anything: their P is 0, but
-                                // 0 times NaN or infinity is not
-                                unsigned char* st = ring + s * kStageBytes;
-                                for (int e = lane; e < (kKeys - valid) * 8; e += 32)
+            }
+        } while (!timed_out && w.next());
+        // copies still in flight land before the CTA may leave (bounded)
+        for (uint32_t j = used > stages ? used - stages : 0; j < used; ++j)
+            if (!ptx::mbar_wait(&bar.kv_full[j % stages], (j / stages) & 1u, ptx::wait_deadline(20000000ull))) timed_out = true;
+    } else if (work && warp == kMmaWarp && rank == 0) {
+        // ---------------------------------------------------------------- MMA: S = Q K^T
+        constexpr uint32_t idesc = ptx::instr_desc(1, 1, kRows, kKeys);
+        const uint64_t k_desc = desc_sw128(ring_addr, 16, 1024), qr_desc = desc_sw128(ptx::smem_addr(qrope), 16, 1024);
+        // a wait that ran out only marks the step; the warp leaves at its end
+        bool late = false;
+        auto wait = [&](uint64_t* b, uint32_t parity) {
+            if (!ptx::mbar_wait(b, parity, deadline)) late = true;
+        };
+        Walk w(bt, bar.start);
+        uint32_t u = 0, seg = 0, s = 0, ph = 0;
+        do {
+            if (w.t0 >= w.t1) continue;
+            wait(&bar.q_full, seg & 1u);
+            ++seg;
+            for (int t = w.t0; t < w.t1; ++t, ++u) {
+                const uint32_t sb = u % kSBufs;
+                if (u >= kSBufs) wait(&bar.s_read[sb], ((u / kSBufs) & 1u) ^ 1u);
+                const uint32_t d = tmem + kColS + sb * kKeys;
 #pragma unroll
-                                    for (int j = 0; j < kChunks; ++j)
-                                        *reinterpret_cast<uint4*>(st + j * kChunkBytes + (valid + (e >> 3)) * 128 + (e & 7) * 16) =
-                                            make_uint4(0u, 0u, 0u, 0u);
-                                ptx::fence_proxy_async_smem();
-                                __syncwarp();
+                for (int i = 0; i < 3; ++i) {
+                    wait(&bar.kv_full[s], ph);
+                    __syncwarp();
+                    ptx::tc_fence_after_sync();
+                    if (elect_one()) {
+                        const uint64_t so = k_desc + s * (kKStageChunks * kChunkBytes / 16);
+                        if (i == 0) {
+                            bar.tile_ok[sb] = bar.page_ok[s];
+                            ptx::mbar_arrive(&bar.s_full[sb]);       // orders tile_ok for the softmax
+                        }
+#pragma unroll
+                        for (int j = 0; j < kKStageChunks; ++j)
+#pragma unroll
+                            for (int kk = 0; kk < 4; ++kk) {
+                                const int c = i * kKStageChunks + j;
+                                if (c < 8)
+                                    umma_f16_ts(d, tmem + c * 32 + kk * 8, so + j * (kChunkBytes / 16) + kk * 2, idesc,
+                                                (c | kk) != 0 ? 1u : 0u);
+                                else
+                                    ptx::umma_f16(d, qr_desc + kk * 2, so + j * (kChunkBytes / 16) + kk * 2, idesc, 1u);
                             }
-                            ptx::tc_fence_after_sync();
-                            if (elect_one()) {
-                                // the previous phase is over: the P V of tile u - 2 has been issued
-                                ptx::mbar_arrive_expect_tx(&bar.p_full[u & 1], peer_quads * (32 * kKeys * 2));
-                                const uint64_t so = s * (kStageBytes / 16);
-                                const uint32_t d = tmem + kColS + (u & 1) * kKeys;
+                        ptx::umma_commit(&bar.kv_empty[s]);
+                        if (i == 2) ptx::umma_commit(&bar.s_full[sb]);
+                    }
+                    __syncwarp();
+                    if (++s == kKStages) {
+                        s = 0;
+                        ph ^= 1u;
+                    }
+                }
+                if (__any_sync(0xffffffffu, late)) break;
+            }
+        } while (!__any_sync(0xffffffffu, late) && w.next());
+        if (late) timed_out = true;
+    } else if (work && warp == kMmaWarp) {
+        // ---------------------------------------------------------------- MMA: O += P V
+        constexpr uint32_t idesc = ptx::instr_desc(1, 1, kRows, 256) | (1u << 16);   // B MN-major
+        const uint64_t v_desc = desc_sw128(ring_addr, kChunkBytes, 1024), p_desc = desc_sw128(ptx::smem_addr(ps), 16, 1024);
+        bool late = false;
+        auto wait = [&](uint64_t* b, uint32_t parity) {
+            if (!ptx::mbar_wait(b, parity, deadline)) late = true;
+        };
+        Walk w(bt, bar.start);
+        uint32_t u = 0, seg = 0, s = 0, ph = 0, pb = 0, pph = 0;
+        do {
+            if (w.t0 >= w.t1) continue;
+            for (int t = w.t0; t < w.t1; ++t, ++u) {
+                const int valid = w.rt.vis0 + w.rt.tokens - 1 - t * kKeys;
 #pragma unroll
-                                for (int j = 0; j < kChunks; ++j)
+                for (int i = 0; i < 2; ++i) {
+                    wait(&bar.kv_full[s], ph);
+                    if (valid < kKeys) {
+                        // rows past the last visible position may hold anything: their P is 0, but 0 times NaN
+                        // or infinity is not
+                        __syncwarp();
+                        unsigned char* st = ring + s * (kVStageChunks * kChunkBytes);
+                        for (int e = lane; e < (kKeys - valid) * 8; e += 32)
 #pragma unroll
-                                    for (int kk = 0; kk < 4; ++kk)
-                                        umma_f16_ts(d, tmem + kColQ + j * 32 + kk * 8, k_desc + so + j * (kChunkBytes / 16) + kk * 2,
-                                                    idesc_qk, (j | kk) != 0 ? 1u : 0u);
+                            for (int j = 0; j < kVStageChunks; ++j)
+                                *reinterpret_cast<uint4*>(st + j * kChunkBytes + (valid + (e >> 3)) * 128 + (e & 7) * 16) =
+                                    make_uint4(0u, 0u, 0u, 0u);
+                        ptx::fence_proxy_async_smem();
+                    }
+                    if (i == 0) {
+                        if (t == w.t0 && seg > 0) wait(&bar.o_free, (seg - 1) & 1u);
+                        wait(&bar.p_full[pb], pph);
+                        wait(&bar.scaled[pb], pph);
+                        ptx::fence_proxy_async_smem();               // P comes from st.async stores
+                    }
+                    __syncwarp();
+                    ptx::tc_fence_after_sync();
+                    if (elect_one()) {
+                        const uint64_t vb = v_desc + s * (kVStageChunks * kChunkBytes / 16);
+                        const uint64_t pd = p_desc + pb * (kPBytes / 16);
 #pragma unroll
-                                for (int kk = 0; kk < 2; ++kk)
-                                    ptx::umma_f16(d, qr_desc + kk * 2, r_desc + so + kk * 2, idesc_qk, 1u);
-                                ptx::umma_commit(&bar.s_full[u & 1]);
-                            }
-                            __syncwarp();
-                            ++iq;
-                            issued = true;
+                        for (int ks = 0; ks < kKeys / 16; ++ks)
+                            ptx::umma_f16(tmem + i * 256, pd + ks * 2, vb + ks * 128, idesc, (t > w.t0 || ks != 0) ? 1u : 0u);
+                        ptx::umma_commit(&bar.kv_empty[s]);
+                        if (i == 1) {
+                            umma_commit_rank0(&bar.p_free[pb]);
+                            ptx::umma_commit(&bar.pv_done[pb]);
                         }
                     }
-                    // O += P V of tile ip: P in place, the other rows rescaled, O of the previous row tile read out
-                    if (ip < iq) {
-                        const uint32_t u = it + ip, ph = (u >> 1) & 1u;
-                        const bool ready = ptx::mbar_test_wait(&bar.p_full[u & 1], ph) && ptx::mbar_test_wait(&bar.scaled[u & 1], ph) &&
-                                           (ip > 0 || seg == 0 || ptx::mbar_test_wait(&bar.o_free, (seg - 1) & 1u));
-                        if (__all_sync(0xffffffffu, ready)) {
-                            ptx::fence_proxy_async_smem();           // P comes from ordinary and st.async stores
-                            ptx::tc_fence_after_sync();
-                            if (elect_one()) {
-                                const uint64_t vb = v_desc + (u % kStages) * (kStageBytes / 16);
-                                const uint64_t pb = p_desc + (u & 1) * (kPBytes / 16);
-#pragma unroll
-                                for (int ks = 0; ks < kKeys / 16; ++ks)
-                                    ptx::umma_f16(tmem, pb + ks * 2, vb + ks * 128, idesc_pv, (ip | ks) != 0 ? 1u : 0u);
-                                ptx::umma_commit(&bar.kv_empty[u % kStages]);
-                                umma_commit_both(&bar.pv_done[u & 1]);
-                            }
-                            __syncwarp();
-                            ++ip;
-                            issued = true;
-                        }
+                    __syncwarp();
+                    if (++s == kVStages) {
+                        s = 0;
+                        ph ^= 1u;
                     }
-                    if (!issued && static_cast<uint64_t>(clock64()) > deadline) late = true;
-                    if (__any_sync(0xffffffffu, late)) break;
                 }
-                it += n;
-                ++seg;
-            } while (!__any_sync(0xffffffffu, late) && w.next());
-            if (late) timed_out = true;
-        }
-    } else if (warp < kTmaWarp) {
-        // ---------------------------------------------------------------- rows
-        if (threadIdx.x == 0 && half == 0) meta[cluster].rows = 0;
-        if (work) {
-            const int quad = warp & 3, kh = warp >> 2;
-            const int row = quad * 32 + lane;                        // query row of the row tile = tensor-memory lane
-            const bool own = (quad & 1) == half;
-            const int place = (quad >> 1) * 32 + lane;               // among the owned / the other rows
-            const bool lead = (quad >> 1) == 0 && kh == 0 && lane == 0;   // arms this side's barriers
-            const uint32_t lane_base = static_cast<uint32_t>(quad * 32) << 16;
-            const uint32_t o_addr = tmem + lane_base + kh * 128;     // this warp's 128 of the CTA's 256 output dims
-            const float cs = scale * kLog2e;
-            const uint64_t cs2 = f32x2(cs, cs);
-            const int token = row / bt.H;
-            const uint32_t peer_p = map_to_rank(ptx::smem_addr(ps), peer);
-            const uint32_t peer_x = map_to_rank(ptx::smem_addr(xs), peer) + place * 16 + kh * 8 * (kOwnRows * 16);
-            uint32_t p_off[4];                                       // the row's 16-byte pieces of this key half
+                if (++pb == kPBufs) {
+                    pb = 0;
+                    pph ^= 1u;
+                }
+                if (__any_sync(0xffffffffu, late)) break;
+            }
+            ++seg;
+        } while (!__any_sync(0xffffffffu, late) && w.next());
+        if (late) timed_out = true;
+    } else if (work && warp < kTmaWarp && rank == 0) {
+        // ---------------------------------------------------------------- softmax (rank 0)
+        const int quad = warp & 3, kh = warp >> 2;
+        const int row = quad * 32 + lane;                            // query row of the row tile = tensor-memory lane
+        const uint32_t lane_base = static_cast<uint32_t>(quad * 32) << 16;
+        const float cs = scale * kLog2e;
+        const uint64_t cs2 = f32x2(cs, cs);
+        const int token = row / bt.H;
+        uint32_t p_addr[4];                                          // rank 1's places of the row's pieces of this key half
 #pragma unroll
-            for (int i = 0; i < 4; ++i) p_off[i] = row * 128 + (((kh * 4 + i) ^ (row & 7)) << 4);
-            uint32_t it = 0, seg = 0, meets = 0;                     // meets: uses of the pair barrier
-            bool q_loaded = false;
-
-            auto wait = [&](uint64_t* b, uint32_t parity) {
-                if (!ptx::mbar_wait(b, parity, deadline)) timed_out = true;
-            };
-            // a row tile's queries: value chunks 2 kh, 2 kh + 1 into tensor memory, rope pieces 2 kh, 2 kh + 1
-            // into shared memory (the score MMAs before are complete: their s_full has been waited for)
-            auto load_q = [&](const RowTile& rt) {
-                const int n = rt.tokens * bt.H;
-                if (quad * 32 < n) {
+        for (int i = 0; i < 4; ++i)
+            p_addr[i] = map_to_rank(ptx::smem_addr(ps), 1) + row * 128 + (((kh * 4 + i) ^ (row & 7)) << 4);
+        const uint32_t alpha_addr = map_to_rank(ptx::smem_addr(&bar.alpha[0][row]), 1);
+        const uint32_t p_full_addr = map_to_rank(ptx::smem_addr(&bar.p_full[0]), 1);
+        auto wait = [&](uint64_t* b, uint32_t parity) {
+            if (!ptx::mbar_wait(b, parity, deadline)) timed_out = true;
+        };
+        uint32_t u = 0, seg = 0, meets = 0, pb = 0, pph = 0;         // meets: uses of the pair barrier
+        Walk w(bt, bar.start);
+        do {
+            const int live = w.rt.tokens * bt.H;
+            const bool quad_live = quad * 32 < live;
+            const int vis = min(w.rt.vis0 + token, bt.max_pages * kPage);
+            float m_run = -INFINITY, l_run = 0.0f;
+            if (w.t0 < w.t1) {
+                // the row tile's queries: value chunks 4 kh .. + 3 into tensor memory, half of the rope dims into
+                // shared memory (the score MMAs before are complete: their s_full has been waited for)
+                if (quad_live) {
                     const uint4* src = reinterpret_cast<const uint4*>(
-                        q + (static_cast<int64_t>(rt.row0) * bt.H + row) * kLatentDim);
+                        q + (static_cast<int64_t>(w.rt.row0) * bt.H + row) * kLatentDim);
                     const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
-#pragma unroll
-                    for (int j = 0; j < 2; ++j) {
+#pragma unroll 2
+                    for (int j = 4 * kh; j < 4 * kh + 4; ++j) {
                         uint32_t v[32];
 #pragma unroll
                         for (int i = 0; i < 8; ++i) {
-                            const uint4 r = row < n ? __ldg(src + half * (kHalf / 8) + (2 * kh + j) * 8 + i) : zero;
+                            const uint4 r = row < live ? __ldg(src + j * 8 + i) : zero;
                             v[4 * i] = r.x; v[4 * i + 1] = r.y; v[4 * i + 2] = r.z; v[4 * i + 3] = r.w;
                         }
-                        tmem_st_x32(tmem + lane_base + kColQ + (2 * kh + j) * 32, v);
+                        tmem_st_x32(tmem + lane_base + j * 32, v);
                     }
 #pragma unroll
-                    for (int j = 0; j < 2; ++j)
-                        *reinterpret_cast<uint4*>(qrope + row * 64 + (((2 * kh + j) ^ ((row >> 1) & 3)) << 4)) =
-                            row < n ? __ldg(src + (kValueDim + half * 32) / 8 + 2 * kh + j) : zero;
+                    for (int i = 4 * kh; i < 4 * kh + 4; ++i)
+                        *reinterpret_cast<uint4*>(qrope + row * 128 + ((i ^ (row & 7)) << 4)) =
+                            row < live ? __ldg(src + kValueDim / 8 + i) : zero;
                     ptx::fence_proxy_async_smem();
                     tmem_wait_st();
                 }
                 ptx::tc_fence_before_sync();
                 __syncwarp();
                 if (lane == 0) ptx::mbar_arrive(&bar.q_full);
-            };
-            // this warp's part of O times alpha, before tile u is added, once the tiles before are
-            auto rescale = [&](float alpha, uint32_t u) {
-                wait(&bar.pv_done[(u - 1) & 1u], ((u - 1) >> 1) & 1u);
-                __syncwarp();
-                ptx::tc_fence_after_sync();
-#pragma unroll 1
-                for (int cc = 0; cc < 128; cc += 32) {
-                    uint32_t o[32];
-                    ptx::tmem_ld_32x32b_x32(o_addr + cc, o);
-                    ptx::tmem_wait_ld();
-#pragma unroll
-                    for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
-                    tmem_st_x32(o_addr + cc, o);
-                }
-                tmem_wait_st();
-            };
-            // other rows: tile u's partial scores to the peer
-            auto send = [&](uint32_t u, bool live) {
-                const uint32_t bb = u & 1u, ph = (u >> 1) & 1u;
-                wait(&bar.s_full[bb], ph);
-                if (live) {
+            }
+            for (int t = w.t0; t < w.t1; ++t, ++u) {
+                const uint32_t sb = u % kSBufs;
+                wait(&bar.s_full[sb], (u / kSBufs) & 1u);
+                if (quad_live) {
                     __syncwarp();
                     ptx::tc_fence_after_sync();
                     uint32_t v[32];
-                    ptx::tmem_ld_32x32b_x32(tmem + lane_base + kColS + bb * kKeys + kh * 32, v);
-                    if (u >= 2) wait(&bar.x_free[bb], ph ^ 1u);
+                    ptx::tmem_ld_32x32b_x32(tmem + lane_base + kColS + sb * kKeys + kh * 32, v);
+                    const int lim = (bar.tile_ok[sb] ? vis - t * kKeys : 0) - kh * 32;
                     ptx::tmem_wait_ld();
-                    const uint32_t dst = peer_x + bb * kXBytes, xb = map_to_rank(ptx::smem_addr(&bar.x_full[bb]), peer);
-#pragma unroll
-                    for (int k4 = 0; k4 < 8; ++k4)
-                        st_async_v4(dst + k4 * (kOwnRows * 16), v[4 * k4], v[4 * k4 + 1], v[4 * k4 + 2], v[4 * k4 + 3], xb);
-                }
-                ptx::tc_fence_before_sync();
-                __syncwarp();
-                if (lane == 0) ptx::mbar_arrive(&bar.s_read[bb]);
-            };
-
-            Walk w(bt, bar.start);
-            for (;;) {
-                const int live = w.rt.tokens * bt.H;
-                const bool quad_live = quad * 32 < live;
-                const uint32_t my_quads = (half * 32 < live ? 1u : 0u) + ((half + 2) * 32 < live ? 1u : 0u);
-                const uint32_t peer_quads = (static_cast<int>(peer) * 32 < live ? 1u : 0u) +
-                                            (static_cast<int>(peer + 2) * 32 < live ? 1u : 0u);
-                const int vis = min(w.rt.vis0 + token, bt.max_pages * kPage);
-                const bool has_tiles = w.t0 < w.t1;
-                float m_run = -INFINITY, l_run = 0.0f;
-                if (has_tiles && !q_loaded) load_q(w.rt);
-                if (!own) {
-                    const int n = w.t1 - w.t0;
-                    if (n > 0) send(it, quad_live);
-                    for (int i = 0; i < n; ++i, ++it) {
-                        const uint32_t bb = it & 1u, ph = (it >> 1) & 1u;
-                        if (i + 1 < n) send(it + 1, quad_live);
-                        if (lead) ptx::mbar_arrive_expect_tx(&bar.a_full[bb], peer_quads * 128);
-                        wait(&bar.a_full[bb], ph);
-                        if (quad_live && i > 0) {
-                            const float alpha = bar.alpha[bb][place];
-                            if (__any_sync(0xffffffffu, alpha != 1.0f)) rescale(alpha, it);
-                        }
-                        ptx::tc_fence_before_sync();
-                        __syncwarp();
-                        if (lane == 0) ptx::mbar_arrive(&bar.scaled[bb]);
-                        timed_out = __any_sync(0xffffffffu, timed_out);
-                        if (timed_out) break;
-                    }
-                } else {
-                    for (int t = w.t0; t < w.t1; ++t, ++it) {
-                        const uint32_t bb = it & 1u, ph = (it >> 1) & 1u;
-                        const int s = static_cast<int>(it % kStages);
-                        if (lead) ptx::mbar_arrive_expect_tx(&bar.x_full[bb], my_quads * (32 * kKeys * 4));
-                        wait(&bar.s_full[bb], ph);
-                        if (quad_live) {
-                            __syncwarp();
-                            ptx::tc_fence_after_sync();
-                            uint32_t v[32];
-                            ptx::tmem_ld_32x32b_x32(tmem + lane_base + kColS + bb * kKeys + kh * 32, v);
-                            wait(&bar.kv_full[s], (it / kStages) & 1u);            // orders page_ok
-                            wait(&bar.x_full[bb], ph);
-                            const float* xr = xs + bb * (kXBytes / 4) + (kh * 8 * kOwnRows + place) * 4;
-                            float4 x[8];
-#pragma unroll
-                            for (int k4 = 0; k4 < 8; ++k4) x[k4] = *reinterpret_cast<const float4*>(xr + k4 * (kOwnRows * 4));
-                            ptx::tmem_wait_ld();
-                            ptx::tc_fence_before_sync();
-                            __syncwarp();
-                            if (lane == 0) ptx::mbar_arrive(&bar.s_read[bb]);
-                            float sc[32];
-#pragma unroll
-                            for (int k4 = 0; k4 < 8; ++k4) {
-                                sc[4 * k4] = __uint_as_float(v[4 * k4]) + x[k4].x;
-                                sc[4 * k4 + 1] = __uint_as_float(v[4 * k4 + 1]) + x[k4].y;
-                                sc[4 * k4 + 2] = __uint_as_float(v[4 * k4 + 2]) + x[k4].z;
-                                sc[4 * k4 + 3] = __uint_as_float(v[4 * k4 + 3]) + x[k4].w;
-                            }
-                            const int lim = (bar.page_ok[s] ? vis - t * kKeys : 0) - kh * 32;
-                            if (lim < 32) {
-#pragma unroll
-                                for (int e = 0; e < 32; ++e)
-                                    if (e >= lim) sc[e] = -INFINITY;
-                            }
-                            float mx4[4] = {sc[0], sc[1], sc[2], sc[3]};
-#pragma unroll
-                            for (int e = 4; e < 32; ++e) mx4[e & 3] = fmaxf(mx4[e & 3], sc[e]);
-                            float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3]));
-                            // the tile's maximum over both key halves (values double-buffered by tile parity)
-                            bar.tmax[bb][kh][place] = mx;
-                            // every lane's scores have been read (the maximum needs them): the peer may send again
-                            __syncwarp();
-                            if (lane == 0) {
-                                ptx::mbar_arrive(&bar.pair[quad >> 1]);
-                                arrive_remote(map_to_rank(ptx::smem_addr(&bar.x_free[bb]), peer));
-                            }
-                            wait(&bar.pair[quad >> 1], meets & 1u);
-                            ++meets;
-                            mx = fmaxf(mx, bar.tmax[bb][kh ^ 1][place]);
-                            const bool grow = (mx - m_run) * cs > kRescaleThreshold || (m_run == -INFINITY && mx > -INFINITY);
-                            float alpha = 1.0f;
-                            if (__any_sync(0xffffffffu, grow)) {
-                                if (grow) {
-                                    alpha = m_run == -INFINITY ? 0.0f : exp2f((m_run - mx) * cs);
-                                    m_run = mx;
-                                }
-                                l_run *= alpha;
-                                if (t > w.t0) rescale(alpha, it);
-                            }
-                            const float neg = m_run == -INFINITY ? 0.0f : -m_run * cs;
-                            const uint64_t neg2 = f32x2(neg, neg);
-                            uint64_t sum2 = f32x2(0.0f, 0.0f);
-                            uint32_t pk[16];
-#pragma unroll
-                            for (int e = 0; e < 32; e += 2) {
-                                float a, b;
-                                unpack_f32x2(fma_f32x2(f32x2(sc[e], sc[e + 1]), cs2, neg2), a, b);
-                                a = fast_exp2(a);
-                                b = fast_exp2(b);
-                                sum2 = add_f32x2(sum2, f32x2(a, b));
-                                pk[e / 2] = pack_bf16x2(a, b);
-                            }
-                            // the P V that read the buffer's previous P is complete in both CTAs
-                            if (it >= 2) wait(&bar.pv_done[bb], ph ^ 1u);
-                            const uint32_t pb = map_to_rank(ptx::smem_addr(&bar.p_full[bb]), peer);
-#pragma unroll
-                            for (int i = 0; i < 4; ++i) {
-                                st_async_v4(peer_p + bb * kPBytes + p_off[i], pk[4 * i], pk[4 * i + 1], pk[4 * i + 2], pk[4 * i + 3], pb);
-                                *reinterpret_cast<uint4*>(ps + bb * kPBytes + p_off[i]) =
-                                    make_uint4(pk[4 * i], pk[4 * i + 1], pk[4 * i + 2], pk[4 * i + 3]);
-                            }
-                            if (kh == 0)
-                                st_async_f32(map_to_rank(ptx::smem_addr(&bar.alpha[bb][place]), peer), alpha,
-                                             map_to_rank(ptx::smem_addr(&bar.a_full[bb]), peer));
-                            ptx::fence_proxy_async_smem();
-                            float a, b;
-                            unpack_f32x2(sum2, a, b);
-                            l_run += a + b;
-                        } else if (lane == 0) {
-                            ptx::mbar_arrive(&bar.s_read[bb]);
-                            arrive_remote(map_to_rank(ptx::smem_addr(&bar.x_free[bb]), peer));
-                        }
-                        ptx::tc_fence_before_sync();
-                        __syncwarp();
-                        if (lane == 0) ptx::mbar_arrive(&bar.p_full[bb]);
-                        timed_out = __any_sync(0xffffffffu, timed_out);
-                        if (timed_out) break;
-                    }
-                }
-                if (timed_out) break;
-                // ---- the next row tile's queries, so that its first scores run during this one's output
-                Walk nxt = w;
-                const bool more = nxt.next();
-                q_loaded = more && nxt.t0 < nxt.t1;
-                if (q_loaded) load_q(nxt.rt);
-                // ---- the piece's output: O / l and its log-sum-exp (log2 units for a part)
-                float inv = -1.0f;                                   // -1: nothing visible (O may hold 0 x NaN)
-                if (own && quad_live) {
-                    float l_tot = 0.0f;
-                    if (has_tiles) {
-                        bar.lsum[kh][place] = l_run;
-                        __syncwarp();
-                        if (lane == 0) ptx::mbar_arrive(&bar.pair[quad >> 1]);
-                        wait(&bar.pair[quad >> 1], meets & 1u);
-                        ++meets;
-                        l_tot = l_run + bar.lsum[kh ^ 1][place];
-                        if (l_tot != 0.0f) inv = 1.0f / l_tot;
-                    }
-                    if (kh == 0) {
-                        if (has_tiles)
-                            st_async_f32(map_to_rank(ptx::smem_addr(&bar.fin[place]), peer), inv,
-                                         map_to_rank(ptx::smem_addr(&bar.fin_full), peer));
-                        if (row < live) {
-                            const float lse2 = l_tot == 0.0f ? -INFINITY : m_run * cs + log2f(l_tot);
-                            if (!w.whole) part_lse[piece_slot(cluster, w) * slot_rows + row] = lse2;
-                            else if (lse_out != nullptr) lse_out[static_cast<int64_t>(w.rt.row0) * bt.H + row] = lse2 * kLn2;
-                        }
-                    }
-                } else if (!own && has_tiles) {
-                    if (lead) ptx::mbar_arrive_expect_tx(&bar.fin_full, peer_quads * 128);
-                    wait(&bar.fin_full, seg & 1u);
-                    inv = bar.fin[place];
-                }
-                if (has_tiles) {
-                    wait(&bar.pv_done[(it - 1) & 1u], ((it - 1) >> 1) & 1u);
-                    timed_out = __any_sync(0xffffffffu, timed_out);
-                    if (timed_out) break;
-                    ptx::tc_fence_after_sync();
-                }
-                if (quad_live) {
-                    const int dim = half * kHalf + kh * 128;
-                    uint16_t* dst = out + (static_cast<int64_t>(w.rt.row0) * bt.H + row) * kValueDim + dim;
-                    float* pdst = part_o + (piece_slot(cluster, w) * slot_rows + row) * kValueDim + dim;
-#pragma unroll 1
-                    for (int cc = 0; cc < 128; cc += 32) {
-                        uint32_t o[32];
-                        if (has_tiles) {
-                            ptx::tmem_ld_32x32b_x32(o_addr + cc, o);
-                            ptx::tmem_wait_ld();
-                        }
-#pragma unroll
-                        for (int e = 0; e < 32; ++e)
-                            o[e] = inv < 0.0f ? 0u : __float_as_uint(__uint_as_float(o[e]) * inv);
-                        if (row < live) {
-                            if (w.whole) {
-#pragma unroll
-                                for (int e = 0; e < 32; e += 8)
-                                    *reinterpret_cast<uint4*>(dst + cc + e) = make_uint4(
-                                        pack_bf16x2(__uint_as_float(o[e]), __uint_as_float(o[e + 1])),
-                                        pack_bf16x2(__uint_as_float(o[e + 2]), __uint_as_float(o[e + 3])),
-                                        pack_bf16x2(__uint_as_float(o[e + 4]), __uint_as_float(o[e + 5])),
-                                        pack_bf16x2(__uint_as_float(o[e + 6]), __uint_as_float(o[e + 7])));
-                            } else {
-#pragma unroll
-                                for (int e = 0; e < 32; e += 4)
-                                    *reinterpret_cast<uint4*>(pdst + cc + e) = make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]);
-                            }
-                        }
-                    }
-                }
-                if (has_tiles) {
                     ptx::tc_fence_before_sync();
                     __syncwarp();
-                    if (lane == 0) ptx::mbar_arrive(&bar.o_free);
-                    ++seg;
+                    if (lane == 0) ptx::mbar_arrive(&bar.s_read[sb]);
+                    if (lim < 32) {
+#pragma unroll
+                        for (int e = 0; e < 32; ++e)
+                            if (e >= lim) v[e] = 0xff800000u;        // -inf
+                    }
+                    float mx4[4];
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) mx4[e & 3] = e < 4 ? __uint_as_float(v[e]) : fmaxf(mx4[e & 3], __uint_as_float(v[e]));
+                    float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3]));
+                    // the tile's maximum over both key halves (values double-buffered by tile parity)
+                    bar.tmax[u & 1][kh][row] = mx;
+                    __syncwarp();
+                    if (lane == 0) ptx::mbar_arrive(&bar.pair[quad]);
+                    wait(&bar.pair[quad], meets & 1u);
+                    ++meets;
+                    mx = fmaxf(mx, bar.tmax[u & 1][kh ^ 1][row]);
+                    const bool grow = (mx - m_run) * cs > kRescaleThreshold || (m_run == -INFINITY && mx > -INFINITY);
+                    float alpha = 1.0f;
+                    if (grow) {
+                        alpha = m_run == -INFINITY ? 0.0f : exp2f((m_run - mx) * cs);
+                        m_run = mx;
+                        l_run *= alpha;
+                    }
+                    const float neg = m_run == -INFINITY ? 0.0f : -m_run * cs;
+                    const uint64_t neg2 = f32x2(neg, neg);
+                    uint64_t sum2 = f32x2(0.0f, 0.0f);
+                    uint32_t pk[16];
+#pragma unroll
+                    for (int e = 0; e < 32; e += 2) {
+                        float a, b;
+                        unpack_f32x2(fma_f32x2(f32x2(__uint_as_float(v[e]), __uint_as_float(v[e + 1])), cs2, neg2), a, b);
+                        a = fast_exp2(a);
+                        b = fast_exp2(b);
+                        sum2 = add_f32x2(sum2, f32x2(a, b));
+                        pk[e / 2] = pack_bf16x2(a, b);
+                    }
+                    if (u >= kPBufs) wait(&bar.p_free[pb], pph ^ 1u);
+                    const uint32_t full = p_full_addr + pb * 8;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        st_async_v4(p_addr[i] + pb * kPBytes, pk[4 * i], pk[4 * i + 1], pk[4 * i + 2], pk[4 * i + 3], full);
+                    if (kh == 0) st_async_f32(alpha_addr + pb * (kRows * 4), alpha, full);
+                    float a, b;
+                    unpack_f32x2(sum2, a, b);
+                    l_run += a + b;
+                } else if (lane == 0) {
+                    ptx::mbar_arrive(&bar.s_read[sb]);
                 }
-                // the last piece of a split row tile: the combine kernel finds it here
-                if (threadIdx.x == 0 && half == 0 && w.first && w.t0 > 0 && w.t1 == w.rt.tiles)
-                    meta[cluster] = Meta{static_cast<int64_t>(w.rt.row0) * bt.H, live, bar.first_cluster};
-                if (!more) break;
-                w = nxt;
+                if (++pb == kPBufs) {
+                    pb = 0;
+                    pph ^= 1u;
+                }
+                timed_out = __any_sync(0xffffffffu, timed_out);
+                if (timed_out) break;
             }
-        }
+            if (timed_out) break;
+            // ---- 1 / l to rank 1; the log-sum-exp (log2 units for a part)
+            if (quad_live) {
+                float l_tot = 0.0f;
+                if (w.t0 < w.t1) {
+                    bar.tmax[u & 1][kh][row] = l_run;                // the buffer of the tile before the last: read by both
+                    __syncwarp();
+                    if (lane == 0) ptx::mbar_arrive(&bar.pair[quad]);
+                    wait(&bar.pair[quad], meets & 1u);
+                    ++meets;
+                    l_tot = l_run + bar.tmax[u & 1][kh ^ 1][row];
+                    // the next row tile's first maximum goes to the same buffer: only after both have read
+                    __syncwarp();
+                    if (lane == 0) ptx::mbar_arrive(&bar.pair[quad]);
+                    wait(&bar.pair[quad], meets & 1u);
+                    ++meets;
+                    if (seg > 0) wait(&bar.fin_free, (seg - 1) & 1u);
+                    if (kh == 0)
+                        st_async_f32(map_to_rank(ptx::smem_addr(&bar.fin[row]), 1), l_tot == 0.0f ? -1.0f : 1.0f / l_tot,
+                                     map_to_rank(ptx::smem_addr(&bar.fin_full), 1));
+                }
+                if (kh == 0 && row < live) {
+                    const float lse2 = l_tot == 0.0f ? -INFINITY : m_run * cs + log2f(l_tot);
+                    if (!w.whole) part_lse[piece_slot(cluster, w) * slot_rows + row] = lse2;
+                    else if (lse_out != nullptr) lse_out[static_cast<int64_t>(w.rt.row0) * bt.H + row] = lse2 * kLn2;
+                }
+            }
+            if (w.t0 < w.t1) ++seg;
+        } while (w.next());
+        // rank 1's last signals land here before this CTA may finish
+        for (uint32_t j = u > kPBufs ? u - kPBufs : 0; j < u && !timed_out; ++j) wait(&bar.p_free[j % kPBufs], (j / kPBufs) & 1u);
+    } else if (work && warp < kTmaWarp) {
+        // ---------------------------------------------------------------- rescaling, output (rank 1)
+        const int quad = warp & 3, dh = warp >> 2;                   // rows 32 quad .. + 31, output dims 256 dh .. + 255
+        const int row = quad * 32 + lane;
+        const uint32_t o_addr = tmem + (static_cast<uint32_t>(quad * 32) << 16) + dh * 256;
+        auto wait = [&](uint64_t* b, uint32_t parity) {
+            if (!ptx::mbar_wait(b, parity, deadline)) timed_out = true;
+        };
+        uint32_t u = 0, seg = 0, pb = 0, pph = 0;
+        Walk w(bt, bar.start);
+        do {
+            const int live = w.rt.tokens * bt.H;
+            const bool quad_live = quad * 32 < live, has_tiles = w.t0 < w.t1;
+            const uint32_t quads = static_cast<uint32_t>((live + 31) / 32);
+            for (int t = w.t0; t < w.t1; ++t, ++u) {
+                if (threadIdx.x == 0) ptx::mbar_arrive_expect_tx(&bar.p_full[pb], quads * (32 * kKeys * 2 + 32 * 4));
+                wait(&bar.p_full[pb], pph);
+                if (quad_live && t > w.t0) {
+                    const float alpha = bar.alpha[pb][row];
+                    if (__any_sync(0xffffffffu, alpha != 1.0f)) {
+                        wait(&bar.pv_done[(u - 1) % kPBufs], ((u - 1) / kPBufs) & 1u);
+                        __syncwarp();
+                        ptx::tc_fence_after_sync();
+#pragma unroll 1
+                        for (int cc = 0; cc < 256; cc += 32) {
+                            uint32_t o[32];
+                            ptx::tmem_ld_32x32b_x32(o_addr + cc, o);
+                            ptx::tmem_wait_ld();
+#pragma unroll
+                            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+                            tmem_st_x32(o_addr + cc, o);
+                        }
+                        tmem_wait_st();
+                        ptx::tc_fence_before_sync();
+                    }
+                }
+                __syncwarp();
+                if (lane == 0) ptx::mbar_arrive(&bar.scaled[pb]);
+                if (++pb == kPBufs) {
+                    pb = 0;
+                    pph ^= 1u;
+                }
+                timed_out = __any_sync(0xffffffffu, timed_out);
+                if (timed_out) break;
+            }
+            if (timed_out) break;
+            float inv = -1.0f;                                       // nothing visible: O may hold 0 x NaN
+            if (has_tiles) {
+                if (threadIdx.x == 0) ptx::mbar_arrive_expect_tx(&bar.fin_full, quads * 128);
+                wait(&bar.fin_full, seg & 1u);
+                inv = bar.fin[row];
+                __syncwarp();
+                if (lane == 0) arrive_remote(map_to_rank(ptx::smem_addr(&bar.fin_free), 0));
+                wait(&bar.pv_done[(u - 1) % kPBufs], ((u - 1) / kPBufs) & 1u);
+                timed_out = __any_sync(0xffffffffu, timed_out);
+                if (timed_out) break;
+                ptx::tc_fence_after_sync();
+            }
+            if (quad_live) {
+                uint16_t* dst = out + (static_cast<int64_t>(w.rt.row0) * bt.H + row) * kValueDim + dh * 256;
+                float* pdst = part_o + (piece_slot(cluster, w) * slot_rows + row) * kValueDim + dh * 256;
+#pragma unroll 1
+                for (int cc = 0; cc < 256; cc += 32) {
+                    uint32_t o[32];
+                    if (has_tiles) {
+                        ptx::tmem_ld_32x32b_x32(o_addr + cc, o);
+                        ptx::tmem_wait_ld();
+                    }
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) o[e] = inv < 0.0f ? 0u : __float_as_uint(__uint_as_float(o[e]) * inv);
+                    if (row < live) {
+                        if (w.whole) {
+#pragma unroll
+                            for (int e = 0; e < 32; e += 8)
+                                *reinterpret_cast<uint4*>(dst + cc + e) =
+                                    make_uint4(pack_bf16x2(__uint_as_float(o[e]), __uint_as_float(o[e + 1])),
+                                               pack_bf16x2(__uint_as_float(o[e + 2]), __uint_as_float(o[e + 3])),
+                                               pack_bf16x2(__uint_as_float(o[e + 4]), __uint_as_float(o[e + 5])),
+                                               pack_bf16x2(__uint_as_float(o[e + 6]), __uint_as_float(o[e + 7])));
+                        } else {
+#pragma unroll
+                            for (int e = 0; e < 32; e += 4)
+                                *reinterpret_cast<uint4*>(pdst + cc + e) = make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+                        }
+                    }
+                }
+            }
+            if (has_tiles) {
+                ptx::tc_fence_before_sync();
+                __syncwarp();
+                if (lane == 0) ptx::mbar_arrive(&bar.o_free);
+                ++seg;
+            }
+            // the last piece of a split row tile: the combine kernel finds it here
+            if (threadIdx.x == 0 && w.first && w.t0 > 0 && w.t1 == w.rt.tiles)
+                meta[cluster] = Meta{static_cast<int64_t>(w.rt.row0) * bt.H, live, bar.first_cluster};
+        } while (w.next());
     }
     if (timed_out) raise_error(err, DSA_DEVERR_TIMEOUT);
     ptx::griddep_launch_dependents();
@@ -901,10 +856,8 @@ extern "C" dsa_status dsa_dense_mla_decode(const void* q_bf16, const void* kv_po
     if (workspace == nullptr || !aligned16(workspace) || workspace_bytes < need) return DSA_ERR_INVALID_ARG;
     auto encode = attn::tensor_map_encoder();
     if (encode == nullptr) return DSA_ERR_CUDA;
-    CUtensorMap vmap, rmap;
-    if (!attn::encode_bf16_3d(encode, &vmap, kv_pool, kLatentDim, 1, num_pages * kPage, kLatentDim, kLatentDim, 64, kKeys) ||
-        !attn::encode_bf16_3d(encode, &rmap, kv_pool, kLatentDim, 1, num_pages * kPage, kLatentDim, kLatentDim, 32, kKeys,
-                              CU_TENSOR_MAP_SWIZZLE_64B))
+    CUtensorMap kvmap;
+    if (!attn::encode_bf16_3d(encode, &kvmap, kv_pool, kLatentDim, 1, num_pages * kPage, kLatentDim, kLatentDim, 64, kKeys))
         return DSA_ERR_CUDA;
     const int clusters = decode_clusters(), slot_rows = decode_slot_rows(T, H);
     Meta* meta = static_cast<Meta*>(workspace);
@@ -915,7 +868,7 @@ extern "C" dsa_status dsa_dense_mla_decode(const void* q_bf16, const void* kv_po
                              static_cast<int>(kDecSmem)) != cudaSuccess)
         return DSA_ERR_CUDA;
     dense_mla_decode_kernel<<<2 * clusters, kDecThreads, kDecSmem, s>>>(
-        vmap, rmap, static_cast<const uint16_t*>(q_bf16), static_cast<int>(num_pages), block_table,
+        kvmap, static_cast<const uint16_t*>(q_bf16), static_cast<int>(num_pages), block_table,
         Batch{seq_lens, cu_q, B, T, H, max_pages}, scale, static_cast<uint16_t*>(out_bf16), lse, part_o, part_lse, meta,
         slot_rows, dev_err);
     if (cudaGetLastError() != cudaSuccess) return DSA_ERR_CUDA;
