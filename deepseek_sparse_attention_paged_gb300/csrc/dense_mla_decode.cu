@@ -16,7 +16,7 @@
 // the key takes, and its output accumulator (128 x 512 fp32) fills the tensor memory of an SM.  So a
 // row tile is a pipeline over the two CTAs of a cluster: rank 0 forms the scores and the softmax and
 // sends P (bf16, 16 KB a tile of 64 keys) and the rescaling factors into rank 1's shared memory
-// (st.async); rank 1 accumulates all 512 output dims and writes them.  Nothing flows back but
+// (bulk copies); rank 1 accumulates all 512 output dims and writes them.  Nothing flows back but
 // "buffer free", so latencies overlap; the products are 1152 cycles a tile in rank 0 and 1024 in rank
 // 1, where the copy of a tile's keys from HBM takes about 1560.  Both ranks read a page (rank 1 its 512
 // value dims), the second time from L2.  Splitting the dims instead, half of the scores' inner
@@ -30,7 +30,7 @@
 // Roles (384 threads), warps 10 and 11 idle:
 //   rank 0  warps 0-7  softmax: rows (tensor-memory lanes) 32 (w % 4) .. + 31, key half w / 4; queries
 //                      into tensor memory (value dims) and shared memory (rope dims);
-//           warp 8     TMA: pages as 9 chunks of 64 dims, ring of 8 stages of 3 chunks;
+//           warp 8     TMA: pages as 9 chunks of 64 dims, ring of 6 stages of 3 chunks;
 //           warp 9     MMA: S = Q K^T into a ring of 4 score tiles.
 //   rank 1  warps 0-7  O rescaled where a factor is not 1; O / l to the output, 256 dims a warp;
 //           warp 8     TMA: value chunks, ring of 5 stages of 4 chunks (half of the value dims);
@@ -50,13 +50,15 @@ using namespace attn;
 constexpr int kRows = 128;                                      // query rows of a row tile (MMA M)
 constexpr int kKeys = 64;                                       // keys of a tile: one page
 constexpr int kChunkBytes = kKeys * 128;                        // 64 keys x 64 dims, 128-byte swizzle
-constexpr int kKStageChunks = 3, kKStages = 8;                  // rank 0: a tile is 3 stages
+constexpr int kKStageChunks = 3, kKStages = 6;                  // rank 0: a tile is 3 stages
 constexpr int kVStageChunks = 4, kVStages = 5;                  // rank 1: a tile is 2 stages
+constexpr int kMaxStages = kKStages > kVStages ? kKStages : kVStages;
 constexpr int kPBufs = 3, kSBufs = 4;
-constexpr int kPBytes = kRows * kKeys * 2;                      // 16384: P, K-major, 128-byte swizzle
+constexpr int kPHalfBytes = kRows * (kKeys / 2) * 2;            // 8192: P of 32 keys, K-major, 64-byte swizzle
+constexpr int kPBytes = 2 * kPHalfBytes;
 constexpr int kQRopeBytes = kRows * 128;                        // 16384
-constexpr int kDataBytes = kKStages * kKStageChunks * kChunkBytes + kQRopeBytes;
-static_assert(kVStages * kVStageChunks * kChunkBytes + kPBufs * kPBytes <= kDataBytes, "rank 1 fits rank 0's layout");
+constexpr int kDataBytes = kKStages * kKStageChunks * kChunkBytes + kQRopeBytes + kPBufs * kPBytes;
+static_assert(kVStages * kVStageChunks * kChunkBytes + kPBufs * kPBytes == kDataBytes, "P at the same place in both ranks");
 constexpr int kTmaWarp = 8, kMmaWarp = 9;
 constexpr int kDecThreads = 384;
 constexpr uint32_t kColS = 256;                                 // rank 0: score tiles, behind the query chunks
@@ -67,7 +69,7 @@ static_assert(kDecSmem <= 232448, "shared-memory budget");
 static_assert(kMaxRequests * 4 <= kDataBytes, "schedule scratch");
 
 struct DecBars {
-    uint64_t kv_full[kKStages], kv_empty[kKStages];
+    uint64_t kv_full[kMaxStages], kv_empty[kMaxStages];
     // rank 0
     uint64_t q_full;                        // queries in place (8 softmax warps), per row tile
     uint64_t s_full[kSBufs];                // scores complete; tile_ok written
@@ -82,12 +84,12 @@ struct DecBars {
     uint64_t o_free;                        // O read out (8 row warps), per row tile
     uint64_t fin_full;                      // 1 / l arrived (armed + bytes), per row tile
     uint32_t tmem_slot;
-    int page_ok[kKStages];                  // the stage's page id was valid
+    int page_ok[kMaxStages];                // the stage's page id was valid
     int tile_ok[kSBufs];                    // ... of the score tile's page
     int start[4];                           // first request, first row tile of it, first key tile, tiles of the share
     int first_cluster;                      // cluster that holds the first piece of the first row tile
     float tmax[2][2][kRows];                // rank 0: [tile parity][key half][row]: maximum of the tile
-    float alpha[kPBufs][kRows];             // rank 1: the factors of the tile
+    alignas(16) float alpha[kPBufs][kRows]; // the factors of the tile: rank 0's, copied to rank 1
     float fin[kRows];                       // rank 1: 1 / l; -1: nothing visible
 };
 static_assert(sizeof(DecBars) <= 5120, "barrier block");
@@ -260,16 +262,18 @@ __device__ __forceinline__ uint32_t map_to_rank(uint32_t smem_addr, uint32_t ran
     asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(smem_addr), "r"(rank));
     return r;
 }
-// 16-byte store into another CTA's shared memory, counted as transaction bytes on that CTA's
-// mbarrier (the receiver's wait on it orders the data).
+// 4-byte store into another CTA's shared memory, counted as transaction bytes on that CTA's mbarrier
+// (the receiver's wait on it orders the data).
 __device__ __forceinline__ void st_async_f32(uint32_t addr, float v, uint32_t bar) {
     asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.b32 [%0], %1, [%2];" ::"r"(addr),
                  "r"(__float_as_uint(v)), "r"(bar)
                  : "memory");
 }
-__device__ __forceinline__ void st_async_v4(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d, uint32_t bar) {
-    asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.v4.b32 [%0], {%1, %2, %3, %4}, [%5];" ::"r"(addr),
-                 "r"(a), "r"(b), "r"(c), "r"(d), "r"(bar)
+// Bulk copy of this CTA's shared memory into the peer's (16-byte aligned, size a multiple of 16), counted
+// on the peer's mbarrier.
+__device__ __forceinline__ void bulk_to_peer(uint32_t dst, uint32_t src, uint32_t bytes, uint32_t bar) {
+    asm volatile("cp.async.bulk.shared::cluster.shared::cta.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+                 "r"(src), "r"(bytes), "r"(bar)
                  : "memory");
 }
 // Arrive on a barrier of the peer without ordering anything before it: used for buffers this thread has
@@ -277,6 +281,17 @@ __device__ __forceinline__ void st_async_v4(uint32_t addr, uint32_t a, uint32_t 
 __device__ __forceinline__ void arrive_remote(uint32_t bar) {
     asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
+// Descriptor of a K-major operand with the 64-byte swizzle: rows of 64 bytes, 8-row groups 512 apart.
+__device__ __forceinline__ uint64_t desc_sw64(uint32_t addr) {
+    uint64_t d = 0;
+    d |= static_cast<uint64_t>((addr >> 4) & 0x3FFFu);
+    d |= static_cast<uint64_t>(1u) << 16;
+    d |= static_cast<uint64_t>(512u >> 4) << 32;
+    d |= static_cast<uint64_t>(1u) << 46;
+    d |= static_cast<uint64_t>(4u) << 61;
+    return d;
+}
+
 // Arrive on the barrier at this offset in rank 0 once the MMAs issued so far have completed.
 __device__ __forceinline__ void umma_commit_rank0(uint64_t* bar) {
     asm volatile(
@@ -303,7 +318,7 @@ dense_mla_decode_kernel(const __grid_constant__ CUtensorMap kvmap, const uint16_
     unsigned char* base = smem_raw + (((raw_addr + 1023u) & ~1023u) - raw_addr);
     unsigned char* ring = base;                                                   // both ranks: key / value stages
     unsigned char* qrope = base + kKStages * kKStageChunks * kChunkBytes;         // rank 0: [128 rows][64 dims]
-    unsigned char* ps = base + kVStages * kVStageChunks * kChunkBytes;            // rank 1: [3][128 rows][64 keys]
+    unsigned char* ps = base + kVStages * kVStageChunks * kChunkBytes;            // [3][2 key halves][128 rows][32 keys]
     DecBars& bar = *reinterpret_cast<DecBars*>(base + kDataBytes);
 
     const int warp = uniform(static_cast<int>(threadIdx.x >> 5)), lane = threadIdx.x & 31;
@@ -311,7 +326,7 @@ dense_mla_decode_kernel(const __grid_constant__ CUtensorMap kvmap, const uint16_
     const int cluster = blockIdx.x >> 1, clusters = gridDim.x >> 1;
 
     if (threadIdx.x == 0) {
-        for (int s = 0; s < kKStages; ++s) {
+        for (int s = 0; s < kMaxStages; ++s) {
             ptx::mbar_init(&bar.kv_full[s], 1);
             ptx::mbar_init(&bar.kv_empty[s], 1);
         }
@@ -444,7 +459,7 @@ dense_mla_decode_kernel(const __grid_constant__ CUtensorMap kvmap, const uint16_
     } else if (work && warp == kMmaWarp) {
         // ---------------------------------------------------------------- MMA: O += P V
         constexpr uint32_t idesc = ptx::instr_desc(1, 1, kRows, 256) | (1u << 16);   // B MN-major
-        const uint64_t v_desc = desc_sw128(ring_addr, kChunkBytes, 1024), p_desc = desc_sw128(ptx::smem_addr(ps), 16, 1024);
+        const uint64_t v_desc = desc_sw128(ring_addr, kChunkBytes, 1024), p_desc = desc_sw64(ptx::smem_addr(ps));
         bool late = false;
         auto wait = [&](uint64_t* b, uint32_t parity) {
             if (!ptx::mbar_wait(b, parity, deadline)) late = true;
@@ -474,7 +489,6 @@ dense_mla_decode_kernel(const __grid_constant__ CUtensorMap kvmap, const uint16_
                         if (t == w.t0 && seg > 0) wait(&bar.o_free, (seg - 1) & 1u);
                         wait(&bar.p_full[pb], pph);
                         wait(&bar.scaled[pb], pph);
-                        ptx::fence_proxy_async_smem();               // P comes from st.async stores
                     }
                     __syncwarp();
                     ptx::tc_fence_after_sync();
@@ -483,7 +497,8 @@ dense_mla_decode_kernel(const __grid_constant__ CUtensorMap kvmap, const uint16_
                         const uint64_t pd = p_desc + pb * (kPBytes / 16);
 #pragma unroll
                         for (int ks = 0; ks < kKeys / 16; ++ks)
-                            ptx::umma_f16(tmem + i * 256, pd + ks * 2, vb + ks * 128, idesc, (t > w.t0 || ks != 0) ? 1u : 0u);
+                            ptx::umma_f16(tmem + i * 256, pd + (ks >> 1) * (kPHalfBytes / 16) + (ks & 1) * 2, vb + ks * 128, idesc,
+                                          (t > w.t0 || ks != 0) ? 1u : 0u);
                         ptx::umma_commit(&bar.kv_empty[s]);
                         if (i == 1) {
                             umma_commit_rank0(&bar.p_free[pb]);
@@ -513,12 +528,13 @@ dense_mla_decode_kernel(const __grid_constant__ CUtensorMap kvmap, const uint16_
         const float cs = scale * kLog2e;
         const uint64_t cs2 = f32x2(cs, cs);
         const int token = row / bt.H;
-        uint32_t p_addr[4];                                          // rank 1's places of the row's pieces of this key half
+        uint32_t p_off[4];                                           // the row's 16-byte pieces of this key half
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-            p_addr[i] = map_to_rank(ptx::smem_addr(ps), 1) + row * 128 + (((kh * 4 + i) ^ (row & 7)) << 4);
-        const uint32_t alpha_addr = map_to_rank(ptx::smem_addr(&bar.alpha[0][row]), 1);
-        const uint32_t p_full_addr = map_to_rank(ptx::smem_addr(&bar.p_full[0]), 1);
+        for (int i = 0; i < 4; ++i) p_off[i] = kh * kPHalfBytes + row * 64 + ((i ^ ((row >> 1) & 3)) << 4);
+        // this warp's 32 rows of a P buffer, and their factors, here and in rank 1
+        const uint32_t p_here = ptx::smem_addr(ps) + kh * kPHalfBytes + quad * 2048, p_there = map_to_rank(p_here, 1);
+        const uint32_t a_here = ptx::smem_addr(&bar.alpha[0][quad * 32]), a_there = map_to_rank(a_here, 1);
+        const uint32_t full_there = map_to_rank(ptx::smem_addr(&bar.p_full[0]), 1);
         auto wait = [&](uint64_t* b, uint32_t parity) {
             if (!ptx::mbar_wait(b, parity, deadline)) timed_out = true;
         };
@@ -607,11 +623,19 @@ dense_mla_decode_kernel(const __grid_constant__ CUtensorMap kvmap, const uint16_
                         pk[e / 2] = pack_bf16x2(a, b);
                     }
                     if (u >= kPBufs) wait(&bar.p_free[pb], pph ^ 1u);
-                    const uint32_t full = p_full_addr + pb * 8;
 #pragma unroll
                     for (int i = 0; i < 4; ++i)
-                        st_async_v4(p_addr[i] + pb * kPBytes, pk[4 * i], pk[4 * i + 1], pk[4 * i + 2], pk[4 * i + 3], full);
-                    if (kh == 0) st_async_f32(alpha_addr + pb * (kRows * 4), alpha, full);
+                        *reinterpret_cast<uint4*>(ps + pb * kPBytes + p_off[i]) =
+                            make_uint4(pk[4 * i], pk[4 * i + 1], pk[4 * i + 2], pk[4 * i + 3]);
+                    if (kh == 0) bar.alpha[pb][row] = alpha;
+                    // one bulk copy a warp: 16-byte st.async stores of the same bytes took about 1000 cycles a tile
+                    ptx::fence_proxy_async_smem();
+                    __syncwarp();
+                    if (elect_one()) {
+                        bulk_to_peer(p_there + pb * kPBytes, p_here + pb * kPBytes, 2048, full_there + pb * 8);
+                        if (kh == 0) bulk_to_peer(a_there + pb * (kRows * 4), a_here + pb * (kRows * 4), 128, full_there + pb * 8);
+                    }
+                    __syncwarp();
                     float a, b;
                     unpack_f32x2(sum2, a, b);
                     l_run += a + b;
