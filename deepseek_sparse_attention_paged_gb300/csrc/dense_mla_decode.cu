@@ -15,25 +15,25 @@
 // tokens of one request) needs 2176 FLOP per row and key, 70 % of the tensor time that the copy of
 // the key takes, and its output accumulator (128 x 512 fp32) fills the tensor memory of an SM.  So a
 // row tile is a pipeline over the two CTAs of a cluster: rank 0 forms the scores and the softmax and
-// sends P (bf16, 16 KB a tile of 64 keys) and the rescaling factors into rank 1's shared memory
+// sends P (bf16, 16 KB a page of 64 keys) and the rescaling factors into rank 1's shared memory
 // (bulk copies); rank 1 accumulates all 512 output dims and writes them.  Nothing flows back but
-// "buffer free", so latencies overlap; the products are 1152 cycles a tile in rank 0 and 1024 in rank
-// 1, where the copy of a tile's keys from HBM takes about 1560.  Both ranks read a page (rank 1 its 512
+// "buffer free", so latencies overlap; the products are 1152 cycles a page in rank 0 and 1024 in rank
+// 1, where the copy of a page from HBM takes about 1560.  Both ranks read a page (rank 1 its 512
 // value dims), the second time from L2.  Splitting the dims instead, half of the scores' inner
 // dimension and of the outputs each, reads every byte once but swaps partial scores every tile: two
-// trips over the cluster network in every tile's chain, measured at 3200 cycles a tile.
+// trips over the cluster network in every page's chain, measured at 3200 cycles a page.
 //
-// Work: the key tiles (64 positions = one page) of all row tiles in one sequence, cut into equal shares,
+// Work: the key tiles (128 positions = two pages) of all row tiles in one sequence, cut into equal shares,
 // one per cluster (at least kMinShare tiles).  A row tile that lies within one share is written
 // directly; the pieces of the others go to the workspace and the combine kernel joins them.
 //
 // Roles (384 threads), warps 10 and 11 idle:
-//   rank 0  warps 0-7  softmax: rows (tensor-memory lanes) 32 (w % 4) .. + 31, key half w / 4; queries
+//   rank 0  warps 0-7  softmax: rows (tensor-memory lanes) 32 (w % 4) .. + 31, page w / 4 of the tile; queries
 //                      into tensor memory (value dims) and shared memory (rope dims);
-//           warp 8     TMA: pages as 9 chunks of 64 dims, ring of 6 stages of 3 chunks;
-//           warp 9     MMA: S = Q K^T into a ring of 4 score tiles.
+//           warp 8     TMA: 9 chunks of 64 dims a tile, ring of 8;
+//           warp 9     MMA: S = Q K^T (N = 128) into two score tiles in turn.
 //   rank 1  warps 0-7  O rescaled where a factor is not 1; O / l to the output, 256 dims a warp;
-//           warp 8     TMA: value chunks, ring of 5 stages of 4 chunks (half of the value dims);
+//           warp 8     TMA: the pages' value dims, ring of 4 stages of 256 dims;
 //           warp 9     MMA: O += P V, one N = 256 half per stage.
 // Tensor memory: rank 0 query chunks (columns 0-255) and score tiles (256-511), rank 1 O (0-511).
 #include <cuda_bf16.h>
@@ -48,22 +48,23 @@ namespace {
 using namespace attn;
 
 constexpr int kRows = 128;                                      // query rows of a row tile (MMA M)
-constexpr int kKeys = 64;                                       // keys of a tile: one page
-constexpr int kChunkBytes = kKeys * 128;                        // 64 keys x 64 dims, 128-byte swizzle
-constexpr int kKStageChunks = 3, kKStages = 6;                  // rank 0: a tile is 3 stages
-constexpr int kVStageChunks = 4, kVStages = 5;                  // rank 1: a tile is 2 stages
+constexpr int kKeys = 128;                                      // keys of a tile: two pages
+constexpr int kPageChunk = kPage * 128;                         // 8192: 64 keys x 64 dims, 128-byte swizzle
+constexpr int kKStageBytes = 2 * kPageChunk, kKStages = 8;      // rank 0: 64 dims of both pages; a tile is 9 stages
+constexpr int kVStageBytes = 4 * kPageChunk, kVStages = 4;      // rank 1: 256 dims of one page; a tile is 4 stages
 constexpr int kMaxStages = kKStages > kVStages ? kKStages : kVStages;
-constexpr int kPBufs = 3, kSBufs = 4;
-constexpr int kPHalfBytes = kRows * (kKeys / 2) * 2;            // 8192: P of 32 keys, K-major, 64-byte swizzle
-constexpr int kPBytes = 2 * kPHalfBytes;
+constexpr int kSBufs = 2, kPBufs = 4;                           // score tiles; P buffers of one page
+constexpr int kPvBars = 4;
+constexpr int kPBytes = kRows * kPage * 2;                      // 16384: P of a page, K-major, 128-byte swizzle
 constexpr int kQRopeBytes = kRows * 128;                        // 16384
-constexpr int kDataBytes = kKStages * kKStageChunks * kChunkBytes + kQRopeBytes + kPBufs * kPBytes;
-static_assert(kVStages * kVStageChunks * kChunkBytes + kPBufs * kPBytes == kDataBytes, "P at the same place in both ranks");
+constexpr int kPOffset = kKStages * kKStageBytes + kQRopeBytes; // P at the same place in both ranks
+constexpr int kDataBytes = kPOffset + kPBufs * kPBytes;
+static_assert(kVStages * kVStageBytes + 8 * 2048 <= kPOffset, "rank 1's stages and output staging");
 constexpr int kTmaWarp = 8, kMmaWarp = 9;
 constexpr int kDecThreads = 384;
 constexpr uint32_t kColS = 256;                                 // rank 0: score tiles, behind the query chunks
 constexpr int kMaxRequests = 16384;                             // prefix sums of the schedule fit the ring
-constexpr int kMinShare = 4;
+constexpr int kMinShare = 2;
 constexpr size_t kDecSmem = 1024 + size_t(kDataBytes) + 5120;
 static_assert(kDecSmem <= 232448, "shared-memory budget");
 static_assert(kMaxRequests * 4 <= kDataBytes, "schedule scratch");
@@ -72,6 +73,7 @@ struct DecBars {
     uint64_t kv_full[kMaxStages], kv_empty[kMaxStages];
     // rank 0
     uint64_t q_full;                        // queries in place (8 softmax warps), per row tile
+    uint64_t q_read[kKStages];              // the query chunk in the stage has been copied out of it (4 warps)
     uint64_t s_full[kSBufs];                // scores complete; tile_ok written
     uint64_t s_read[kSBufs];                // ... and read (8 warps)
     uint64_t pair[4];                       // both key halves of a row group have written (2 warps)
@@ -79,17 +81,17 @@ struct DecBars {
     uint64_t fin_free;                      // rank 1 has read 1 / l (its 8 row warps), per row tile
     // rank 1
     uint64_t p_full[kPBufs];                // P and the factors arrived (armed + bytes)
-    uint64_t scaled[kPBufs];                // O rescaled by them (8 row warps)
-    uint64_t pv_done[kPBufs];               // P V of the tile complete (as many as tiles the row warps may be ahead)
+    uint64_t scaled[2];                     // O rescaled by them (8 row warps), per tile
+    uint64_t pv_done[kPvBars];              // P V of the tile complete (more than the tiles the row warps may be ahead)
     uint64_t o_free;                        // O read out (8 row warps), per row tile
     uint64_t fin_full;                      // 1 / l arrived (armed + bytes), per row tile
     uint32_t tmem_slot;
-    int page_ok[kMaxStages];                // the stage's page id was valid
-    int tile_ok[kSBufs];                    // ... of the score tile's page
+    int page_ok[kMaxStages];                // bit i: page i of the stage is there and its id valid
+    int tile_ok[kSBufs];                    // ... of the score tile's pages
     int start[4];                           // first request, first row tile of it, first key tile, tiles of the share
     int first_cluster;                      // cluster that holds the first piece of the first row tile
     float tmax[2][2][kRows];                // rank 0: [tile parity][key half][row]: maximum of the tile
-    alignas(16) float alpha[kPBufs][kRows]; // the factors of the tile: rank 0's, copied to rank 1
+    alignas(16) float alpha[2][kRows];      // the factors of the tile: rank 0's, copied to rank 1
     float fin[kRows];                       // rank 1: 1 / l; -1: nothing visible
 };
 static_assert(sizeof(DecBars) <= 5120, "barrier block");
@@ -281,17 +283,6 @@ __device__ __forceinline__ void bulk_to_peer(uint32_t dst, uint32_t src, uint32_
 __device__ __forceinline__ void arrive_remote(uint32_t bar) {
     asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
-// Descriptor of a K-major operand with the 64-byte swizzle: rows of 64 bytes, 8-row groups 512 apart.
-__device__ __forceinline__ uint64_t desc_sw64(uint32_t addr) {
-    uint64_t d = 0;
-    d |= static_cast<uint64_t>((addr >> 4) & 0x3FFFu);
-    d |= static_cast<uint64_t>(1u) << 16;
-    d |= static_cast<uint64_t>(512u >> 4) << 32;
-    d |= static_cast<uint64_t>(1u) << 46;
-    d |= static_cast<uint64_t>(4u) << 61;
-    return d;
-}
-
 // Arrive on the barrier at this offset in rank 0 once the MMAs issued so far have completed.
 __device__ __forceinline__ void umma_commit_rank0(uint64_t* bar) {
     asm volatile(
@@ -309,7 +300,7 @@ struct Meta {
 };
 
 __global__ void __launch_bounds__(kDecThreads, 1) __cluster_dims__(2, 1, 1)
-dense_mla_decode_kernel(const __grid_constant__ CUtensorMap kvmap, const uint16_t* __restrict__ q, int num_pages,
+dense_mla_decode_kernel(const __grid_constant__ CUtensorMap kvmap, const __grid_constant__ CUtensorMap qmap, int num_pages,
                         const int32_t* __restrict__ block_table, Batch bt, float scale, uint16_t* __restrict__ out,
                         float* __restrict__ lse_out, float* __restrict__ part_o, float* __restrict__ part_lse,
                         Meta* __restrict__ meta, int slot_rows, int32_t* err) {
@@ -317,8 +308,8 @@ dense_mla_decode_kernel(const __grid_constant__ CUtensorMap kvmap, const uint16_
     const uint32_t raw_addr = ptx::smem_addr(smem_raw);
     unsigned char* base = smem_raw + (((raw_addr + 1023u) & ~1023u) - raw_addr);
     unsigned char* ring = base;                                                   // both ranks: key / value stages
-    unsigned char* qrope = base + kKStages * kKStageChunks * kChunkBytes;         // rank 0: [128 rows][64 dims]
-    unsigned char* ps = base + kVStages * kVStageChunks * kChunkBytes;            // [3][2 key halves][128 rows][32 keys]
+    unsigned char* qrope = base + kKStages * kKStageBytes;                        // rank 0: [128 rows][64 dims]
+    unsigned char* ps = base + kPOffset;                                          // [4 pages][128 rows][64 keys]
     DecBars& bar = *reinterpret_cast<DecBars*>(base + kDataBytes);
 
     const int warp = uniform(static_cast<int>(threadIdx.x >> 5)), lane = threadIdx.x & 31;
@@ -331,6 +322,7 @@ dense_mla_decode_kernel(const __grid_constant__ CUtensorMap kvmap, const uint16_
             ptx::mbar_init(&bar.kv_empty[s], 1);
         }
         ptx::mbar_init(&bar.q_full, 8);
+        for (int s = 0; s < kKStages; ++s) ptx::mbar_init(&bar.q_read[s], 4);
         for (int i = 0; i < kSBufs; ++i) {
             ptx::mbar_init(&bar.s_full[i], 2);
             ptx::mbar_init(&bar.s_read[i], 8);
@@ -339,9 +331,9 @@ dense_mla_decode_kernel(const __grid_constant__ CUtensorMap kvmap, const uint16_
         for (int i = 0; i < kPBufs; ++i) {
             ptx::mbar_init(&bar.p_free[i], 1);
             ptx::mbar_init(&bar.p_full[i], 1);
-            ptx::mbar_init(&bar.scaled[i], 8);
-            ptx::mbar_init(&bar.pv_done[i], 1);
         }
+        for (int i = 0; i < 2; ++i) ptx::mbar_init(&bar.scaled[i], 8);
+        for (int i = 0; i < kPvBars; ++i) ptx::mbar_init(&bar.pv_done[i], 1);
         ptx::mbar_init(&bar.o_free, 8);
         ptx::mbar_init(&bar.fin_full, 1);
         ptx::mbar_init(&bar.fin_free, 8);
@@ -365,36 +357,69 @@ dense_mla_decode_kernel(const __grid_constant__ CUtensorMap kvmap, const uint16_
 
     if (work && warp == kTmaWarp) {
         // ---------------------------------------------------------------- TMA (both ranks)
-        const int chunks = rank == 0 ? kKStageChunks : kVStageChunks, per_tile = rank == 0 ? 3 : 2;
         const uint32_t stages = rank == 0 ? kKStages : kVStages;
         Walk w(bt, bar.start);
         uint32_t s = 0, ph = 0, used = 0;                            // stage, its phase, stages used so far
+        auto stage = [&]() {                                         // the next stage is free (whole warp)
+            if (!ptx::mbar_wait(&bar.kv_empty[s], ph ^ 1u, deadline)) timed_out = true;
+            timed_out = __any_sync(0xffffffffu, timed_out);
+            return !timed_out;
+        };
+        auto advance = [&]() {
+            __syncwarp();
+            ++used;
+            if (++s == stages) {
+                s = 0;
+                ph ^= 1u;
+            }
+        };
         do {
+            // the row tile's queries, 64 dims a stage (rows past its last one are other tokens', or zeros)
+            if (rank == 0 && w.t0 < w.t1)
+                for (int c = 0; c < 9 && stage(); ++c) {
+                    if (elect_one()) {
+                        ptx::mbar_arrive_expect_tx(&bar.kv_full[s], kKStageBytes);
+                        ptx::tma_load_3d(ring + s * kKStageBytes, &qmap, &bar.kv_full[s], c * 64, 0, w.rt.row0 * bt.H);
+                    }
+                    advance();
+                }
             int page = -1;
             for (int t = w.t0; t < w.t1 && !timed_out; ++t) {
-                if (((t - w.t0) & 31) == 0)                          // page ids of the next 32 tiles
-                    page = t + lane < w.t1 ? __ldg(block_table + static_cast<int64_t>(w.b) * bt.max_pages + t + lane) : 0;
-                const int pg = __shfl_sync(0xffffffffu, page, (t - w.t0) & 31);
-                const bool ok = pg >= 0 && pg < num_pages;
-                // a page outside the pool: a box past the end reads zeros, and rank 0 masks its keys
-                const int row = (ok ? pg : num_pages) * kPage;
-                if (!ok && lane == 0 && rank == 0) raise_error(err, DSA_DEVERR_PAGE_RANGE);
-                for (int i = 0; i < per_tile; ++i) {
-                    if (!ptx::mbar_wait(&bar.kv_empty[s], ph ^ 1u, deadline)) timed_out = true;
-                    timed_out = __any_sync(0xffffffffu, timed_out);
-                    if (timed_out) break;
-                    if (elect_one()) {
-                        if (rank == 0) bar.page_ok[s] = ok ? 1 : 0;
-                        ptx::mbar_arrive_expect_tx(&bar.kv_full[s], chunks * kChunkBytes);
-                        unsigned char* st = ring + s * chunks * kChunkBytes;
-                        for (int j = 0; j < chunks; ++j)
-                            ptx::tma_load_3d(st + j * kChunkBytes, &kvmap, &bar.kv_full[s], (i * chunks + j) * 64, 0, row);
+                if (((t - w.t0) & 15) == 0) {                        // page ids of the next 16 tiles
+                    const int at = 2 * t + lane;
+                    page = (at < 2 * w.t1 && at < bt.max_pages) ? __ldg(block_table + static_cast<int64_t>(w.b) * bt.max_pages + at) : -1;
+                }
+                int row[2], ok = 0;
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const int pg = __shfl_sync(0xffffffffu, page, 2 * ((t - w.t0) & 15) + i);
+                    const bool needed = (2 * t + i) * kPage < w.rt.vis0 + w.rt.tokens - 1 && 2 * t + i < bt.max_pages;
+                    const bool there = needed && pg >= 0 && pg < num_pages;
+                    // a page that is not there: a box past the end reads zeros, and rank 0 masks its keys
+                    row[i] = (there ? pg : num_pages) * kPage;
+                    ok |= there ? 1 << i : 0;
+                    if (needed && !there && lane == 0 && rank == 0) raise_error(err, DSA_DEVERR_PAGE_RANGE);
+                }
+                if (rank == 0) {
+                    for (int c = 0; c < 9 && stage(); ++c) {
+                        if (elect_one()) {
+                            bar.page_ok[s] = ok;
+                            ptx::mbar_arrive_expect_tx(&bar.kv_full[s], kKStageBytes);
+                            ptx::tma_load_3d(ring + s * kKStageBytes, &kvmap, &bar.kv_full[s], c * 64, 0, row[0]);
+                            ptx::tma_load_3d(ring + s * kKStageBytes + kPageChunk, &kvmap, &bar.kv_full[s], c * 64, 0, row[1]);
+                        }
+                        advance();
                     }
-                    __syncwarp();
-                    ++used;
-                    if (++s == stages) {
-                        s = 0;
-                        ph ^= 1u;
+                } else {
+                    for (int i = 0; i < 4 && stage(); ++i) {         // page i / 2, value dims 256 (i % 2) .. + 255
+                        if (elect_one()) {
+                            ptx::mbar_arrive_expect_tx(&bar.kv_full[s], kVStageBytes);
+#pragma unroll
+                            for (int j = 0; j < 4; ++j)
+                                ptx::tma_load_3d(ring + s * kVStageBytes + j * kPageChunk, &kvmap, &bar.kv_full[s],
+                                                 (i & 1) * 256 + j * 64, 0, row[i >> 1]);
+                        }
+                        advance();
                     }
                 }
             }
@@ -412,9 +437,20 @@ dense_mla_decode_kernel(const __grid_constant__ CUtensorMap kvmap, const uint16_
             if (!ptx::mbar_wait(b, parity, deadline)) late = true;
         };
         Walk w(bt, bar.start);
-        uint32_t u = 0, seg = 0, s = 0, ph = 0;
+        uint32_t u = 0, seg = 0, s = 0, ph = 0, q_phase = 0;          // q_phase: bit s, the phase of q_read[s]
         do {
             if (w.t0 >= w.t1) continue;
+            for (int c = 0; c < 9; ++c) {
+                wait(&bar.q_read[s], (q_phase >> s) & 1u);
+                q_phase ^= 1u << s;
+                __syncwarp();
+                if (elect_one()) ptx::mbar_arrive(&bar.kv_empty[s]);
+                __syncwarp();
+                if (++s == kKStages) {
+                    s = 0;
+                    ph ^= 1u;
+                }
+            }
             wait(&bar.q_full, seg & 1u);
             ++seg;
             for (int t = w.t0; t < w.t1; ++t, ++u) {
@@ -422,29 +458,23 @@ dense_mla_decode_kernel(const __grid_constant__ CUtensorMap kvmap, const uint16_
                 if (u >= kSBufs) wait(&bar.s_read[sb], ((u / kSBufs) & 1u) ^ 1u);
                 const uint32_t d = tmem + kColS + sb * kKeys;
 #pragma unroll
-                for (int i = 0; i < 3; ++i) {
+                for (int c = 0; c < 9; ++c) {
                     wait(&bar.kv_full[s], ph);
                     __syncwarp();
                     ptx::tc_fence_after_sync();
                     if (elect_one()) {
-                        const uint64_t so = k_desc + s * (kKStageChunks * kChunkBytes / 16);
-                        if (i == 0) {
+                        const uint64_t so = k_desc + s * (kKStageBytes / 16);
+                        if (c == 0) {
                             bar.tile_ok[sb] = bar.page_ok[s];
                             ptx::mbar_arrive(&bar.s_full[sb]);       // orders tile_ok for the softmax
                         }
 #pragma unroll
-                        for (int j = 0; j < kKStageChunks; ++j)
-#pragma unroll
-                            for (int kk = 0; kk < 4; ++kk) {
-                                const int c = i * kKStageChunks + j;
-                                if (c < 8)
-                                    umma_f16_ts(d, tmem + c * 32 + kk * 8, so + j * (kChunkBytes / 16) + kk * 2, idesc,
-                                                (c | kk) != 0 ? 1u : 0u);
-                                else
-                                    ptx::umma_f16(d, qr_desc + kk * 2, so + j * (kChunkBytes / 16) + kk * 2, idesc, 1u);
-                            }
+                        for (int kk = 0; kk < 4; ++kk) {
+                            if (c < 8) umma_f16_ts(d, tmem + c * 32 + kk * 8, so + kk * 2, idesc, (c | kk) != 0 ? 1u : 0u);
+                            else ptx::umma_f16(d, qr_desc + kk * 2, so + kk * 2, idesc, 1u);
+                        }
                         ptx::umma_commit(&bar.kv_empty[s]);
-                        if (i == 2) ptx::umma_commit(&bar.s_full[sb]);
+                        if (c == 8) ptx::umma_commit(&bar.s_full[sb]);
                     }
                     __syncwarp();
                     if (++s == kKStages) {
@@ -459,61 +489,56 @@ dense_mla_decode_kernel(const __grid_constant__ CUtensorMap kvmap, const uint16_
     } else if (work && warp == kMmaWarp) {
         // ---------------------------------------------------------------- MMA: O += P V
         constexpr uint32_t idesc = ptx::instr_desc(1, 1, kRows, 256) | (1u << 16);   // B MN-major
-        const uint64_t v_desc = desc_sw128(ring_addr, kChunkBytes, 1024), p_desc = desc_sw64(ptx::smem_addr(ps));
+        const uint64_t v_desc = desc_sw128(ring_addr, kPageChunk, 1024), p_desc = desc_sw128(ptx::smem_addr(ps), 16, 1024);
         bool late = false;
         auto wait = [&](uint64_t* b, uint32_t parity) {
             if (!ptx::mbar_wait(b, parity, deadline)) late = true;
         };
         Walk w(bt, bar.start);
-        uint32_t u = 0, seg = 0, s = 0, ph = 0, pb = 0, pph = 0;
+        uint32_t u = 0, seg = 0, s = 0, ph = 0;
         do {
             if (w.t0 >= w.t1) continue;
             for (int t = w.t0; t < w.t1; ++t, ++u) {
-                const int valid = w.rt.vis0 + w.rt.tokens - 1 - t * kKeys;
 #pragma unroll
-                for (int i = 0; i < 2; ++i) {
+                for (int i = 0; i < 4; ++i) {                        // page i / 2, value dims 256 (i % 2) .. + 255
+                    const uint32_t pb = 2 * (u & 1u) + (i >> 1);
                     wait(&bar.kv_full[s], ph);
-                    if (valid < kKeys) {
+                    const int valid = w.rt.vis0 + w.rt.tokens - 1 - t * kKeys - (i >> 1) * kPage;
+                    if (valid > 0 && valid < kPage) {
                         // rows past the last visible position may hold anything: their P is 0, but 0 times NaN
-                        // or infinity is not
+                        // or infinity is not (a page without visible rows was filled with zeros)
                         __syncwarp();
-                        unsigned char* st = ring + s * (kVStageChunks * kChunkBytes);
-                        for (int e = lane; e < (kKeys - valid) * 8; e += 32)
+                        unsigned char* st = ring + s * kVStageBytes;
+                        for (int e = lane; e < (kPage - valid) * 8; e += 32)
 #pragma unroll
-                            for (int j = 0; j < kVStageChunks; ++j)
-                                *reinterpret_cast<uint4*>(st + j * kChunkBytes + (valid + (e >> 3)) * 128 + (e & 7) * 16) =
+                            for (int j = 0; j < 4; ++j)
+                                *reinterpret_cast<uint4*>(st + j * kPageChunk + (valid + (e >> 3)) * 128 + (e & 7) * 16) =
                                     make_uint4(0u, 0u, 0u, 0u);
                         ptx::fence_proxy_async_smem();
                     }
+                    if ((i & 1) == 0) wait(&bar.p_full[pb], (u >> 1) & 1u);
                     if (i == 0) {
                         if (t == w.t0 && seg > 0) wait(&bar.o_free, (seg - 1) & 1u);
-                        wait(&bar.p_full[pb], pph);
-                        wait(&bar.scaled[pb], pph);
+                        wait(&bar.scaled[u & 1], (u >> 1) & 1u);
                     }
                     __syncwarp();
                     ptx::tc_fence_after_sync();
                     if (elect_one()) {
-                        const uint64_t vb = v_desc + s * (kVStageChunks * kChunkBytes / 16);
+                        const uint64_t vb = v_desc + s * (kVStageBytes / 16);
                         const uint64_t pd = p_desc + pb * (kPBytes / 16);
 #pragma unroll
-                        for (int ks = 0; ks < kKeys / 16; ++ks)
-                            ptx::umma_f16(tmem + i * 256, pd + (ks >> 1) * (kPHalfBytes / 16) + (ks & 1) * 2, vb + ks * 128, idesc,
-                                          (t > w.t0 || ks != 0) ? 1u : 0u);
+                        for (int ks = 0; ks < kPage / 16; ++ks)
+                            ptx::umma_f16(tmem + (i & 1) * 256, pd + ks * 2, vb + ks * 128, idesc,
+                                          (t > w.t0 || i >= 2 || ks != 0) ? 1u : 0u);
                         ptx::umma_commit(&bar.kv_empty[s]);
-                        if (i == 1) {
-                            umma_commit_rank0(&bar.p_free[pb]);
-                            ptx::umma_commit(&bar.pv_done[pb]);
-                        }
+                        if ((i & 1) == 1) umma_commit_rank0(&bar.p_free[pb]);
+                        if (i == 3) ptx::umma_commit(&bar.pv_done[u % kPvBars]);
                     }
                     __syncwarp();
                     if (++s == kVStages) {
                         s = 0;
                         ph ^= 1u;
                     }
-                }
-                if (++pb == kPBufs) {
-                    pb = 0;
-                    pph ^= 1u;
                 }
                 if (__any_sync(0xffffffffu, late)) break;
             }
@@ -528,17 +553,15 @@ dense_mla_decode_kernel(const __grid_constant__ CUtensorMap kvmap, const uint16_
         const float cs = scale * kLog2e;
         const uint64_t cs2 = f32x2(cs, cs);
         const int token = row / bt.H;
-        uint32_t p_off[4];                                           // the row's 16-byte pieces of this key half
-#pragma unroll
-        for (int i = 0; i < 4; ++i) p_off[i] = kh * kPHalfBytes + row * 64 + ((i ^ ((row >> 1) & 3)) << 4);
+        const uint32_t p_row = row * 128, p_swz = row & 7;           // the row's place in a P buffer
         // this warp's 32 rows of a P buffer, and their factors, here and in rank 1
-        const uint32_t p_here = ptx::smem_addr(ps) + kh * kPHalfBytes + quad * 2048, p_there = map_to_rank(p_here, 1);
+        const uint32_t p_here = ptx::smem_addr(ps) + quad * 4096, p_there = map_to_rank(p_here, 1);
         const uint32_t a_here = ptx::smem_addr(&bar.alpha[0][quad * 32]), a_there = map_to_rank(a_here, 1);
         const uint32_t full_there = map_to_rank(ptx::smem_addr(&bar.p_full[0]), 1);
         auto wait = [&](uint64_t* b, uint32_t parity) {
             if (!ptx::mbar_wait(b, parity, deadline)) timed_out = true;
         };
-        uint32_t u = 0, seg = 0, meets = 0, pb = 0, pph = 0;         // meets: uses of the pair barrier
+        uint32_t u = 0, seg = 0, meets = 0, used = 0;                // meets: uses of the pair barrier; used: ring stages
         Walk w(bt, bar.start);
         do {
             const int live = w.rt.tokens * bt.H;
@@ -546,56 +569,69 @@ dense_mla_decode_kernel(const __grid_constant__ CUtensorMap kvmap, const uint16_
             const int vis = min(w.rt.vis0 + token, bt.max_pages * kPage);
             float m_run = -INFINITY, l_run = 0.0f;
             if (w.t0 < w.t1) {
-                // the row tile's queries: value chunks 4 kh .. + 3 into tensor memory, half of the rope dims into
-                // shared memory (the score MMAs before are complete: their s_full has been waited for)
-                if (quad_live) {
-                    const uint4* src = reinterpret_cast<const uint4*>(
-                        q + (static_cast<int64_t>(w.rt.row0) * bt.H + row) * kLatentDim);
-                    const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
-#pragma unroll 2
-                    for (int j = 4 * kh; j < 4 * kh + 4; ++j) {
-                        uint32_t v[32];
+                // the row tile's queries out of the ring: value chunks into tensor memory, the rope chunk into its
+                // place; even chunks by the warps of page 0, odd ones by those of page 1.  (The score MMAs
+                // before are complete: their s_full has been waited for.)
+#pragma unroll 1
+                for (int c = 0; c < 9; ++c) {
+                    const uint32_t st = used % kKStages;
+                    if ((c & 1) == kh) {
+                        wait(&bar.kv_full[st], (used / kKStages) & 1u);
+                        const unsigned char* src = ring + st * kKStageBytes + p_row;
+                        if (c < 8) {
+                            uint32_t v[32];
 #pragma unroll
-                        for (int i = 0; i < 8; ++i) {
-                            const uint4 r = row < live ? __ldg(src + j * 8 + i) : zero;
-                            v[4 * i] = r.x; v[4 * i + 1] = r.y; v[4 * i + 2] = r.z; v[4 * i + 3] = r.w;
+                            for (int i = 0; i < 8; ++i) {
+                                const uint4 r = *reinterpret_cast<const uint4*>(src + ((i ^ p_swz) << 4));
+                                v[4 * i] = r.x; v[4 * i + 1] = r.y; v[4 * i + 2] = r.z; v[4 * i + 3] = r.w;
+                            }
+                            __syncwarp();
+                            tmem_st_x32(tmem + lane_base + c * 32, v);
+                        } else {
+#pragma unroll
+                            for (int i = 0; i < 8; ++i)              // the same swizzle in both places
+                                *reinterpret_cast<uint4*>(qrope + p_row + 16 * i) = *reinterpret_cast<const uint4*>(src + 16 * i);
+                            ptx::fence_proxy_async_smem();
                         }
-                        tmem_st_x32(tmem + lane_base + j * 32, v);
+                        __syncwarp();
+                        if (lane == 0) ptx::mbar_arrive(&bar.q_read[st]);
                     }
-#pragma unroll
-                    for (int i = 4 * kh; i < 4 * kh + 4; ++i)
-                        *reinterpret_cast<uint4*>(qrope + row * 128 + ((i ^ (row & 7)) << 4)) =
-                            row < live ? __ldg(src + kValueDim / 8 + i) : zero;
-                    ptx::fence_proxy_async_smem();
-                    tmem_wait_st();
+                    ++used;
                 }
+                tmem_wait_st();
                 ptx::tc_fence_before_sync();
                 __syncwarp();
                 if (lane == 0) ptx::mbar_arrive(&bar.q_full);
             }
+            used += 9u * static_cast<uint32_t>(max(0, w.t1 - w.t0));
             for (int t = w.t0; t < w.t1; ++t, ++u) {
-                const uint32_t sb = u % kSBufs;
+                const uint32_t sb = u % kSBufs, pb = 2 * (u & 1u) + kh;
                 wait(&bar.s_full[sb], (u / kSBufs) & 1u);
                 if (quad_live) {
                     __syncwarp();
                     ptx::tc_fence_after_sync();
-                    uint32_t v[32];
-                    ptx::tmem_ld_32x32b_x32(tmem + lane_base + kColS + sb * kKeys + kh * 32, v);
-                    const int lim = (bar.tile_ok[sb] ? vis - t * kKeys : 0) - kh * 32;
+                    uint32_t v[2][32];
+                    const uint32_t sa = tmem + lane_base + kColS + sb * kKeys + kh * kPage;
+                    ptx::tmem_ld_32x32b_x32(sa, v[0]);
+                    ptx::tmem_ld_32x32b_x32(sa + 32, v[1]);
+                    const int lim = ((bar.tile_ok[sb] >> kh) & 1) ? vis - t * kKeys - kh * kPage : 0;
                     ptx::tmem_wait_ld();
                     ptx::tc_fence_before_sync();
                     __syncwarp();
                     if (lane == 0) ptx::mbar_arrive(&bar.s_read[sb]);
-                    if (lim < 32) {
+                    if (lim < kPage) {
 #pragma unroll
-                        for (int e = 0; e < 32; ++e)
-                            if (e >= lim) v[e] = 0xff800000u;        // -inf
+                        for (int e = 0; e < 64; ++e)
+                            if (e >= lim) v[e >> 5][e & 31] = 0xff800000u;   // -inf
                     }
                     float mx4[4];
 #pragma unroll
-                    for (int e = 0; e < 32; ++e) mx4[e & 3] = e < 4 ? __uint_as_float(v[e]) : fmaxf(mx4[e & 3], __uint_as_float(v[e]));
+                    for (int e = 0; e < 64; ++e) {
+                        const float x = __uint_as_float(v[e >> 5][e & 31]);
+                        mx4[e & 3] = e < 4 ? x : fmaxf(mx4[e & 3], x);
+                    }
                     float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3]));
-                    // the tile's maximum over both key halves (values double-buffered by tile parity)
+                    // the tile's maximum over both pages (values double-buffered by tile parity)
                     bar.tmax[u & 1][kh][row] = mx;
                     __syncwarp();
                     if (lane == 0) ptx::mbar_arrive(&bar.pair[quad]);
@@ -612,28 +648,31 @@ dense_mla_decode_kernel(const __grid_constant__ CUtensorMap kvmap, const uint16_
                     const float neg = m_run == -INFINITY ? 0.0f : -m_run * cs;
                     const uint64_t neg2 = f32x2(neg, neg);
                     uint64_t sum2 = f32x2(0.0f, 0.0f);
-                    uint32_t pk[16];
+                    if (u >= 2) wait(&bar.p_free[pb], ((u >> 1) & 1u) ^ 1u);
+                    unsigned char* prow = ps + pb * kPBytes + p_row;
 #pragma unroll
-                    for (int e = 0; e < 32; e += 2) {
-                        float a, b;
-                        unpack_f32x2(fma_f32x2(f32x2(__uint_as_float(v[e]), __uint_as_float(v[e + 1])), cs2, neg2), a, b);
-                        a = fast_exp2(a);
-                        b = fast_exp2(b);
-                        sum2 = add_f32x2(sum2, f32x2(a, b));
-                        pk[e / 2] = pack_bf16x2(a, b);
+                    for (int i = 0; i < 8; ++i) {
+                        uint32_t pk[4];
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const int k = 8 * i + 2 * e;
+                            float a, b;
+                            unpack_f32x2(fma_f32x2(f32x2(__uint_as_float(v[k >> 5][k & 31]), __uint_as_float(v[k >> 5][(k & 31) + 1])),
+                                                   cs2, neg2), a, b);
+                            a = fast_exp2(a);
+                            b = fast_exp2(b);
+                            sum2 = add_f32x2(sum2, f32x2(a, b));
+                            pk[e] = pack_bf16x2(a, b);
+                        }
+                        *reinterpret_cast<uint4*>(prow + ((i ^ p_swz) << 4)) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
                     }
-                    if (u >= kPBufs) wait(&bar.p_free[pb], pph ^ 1u);
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        *reinterpret_cast<uint4*>(ps + pb * kPBytes + p_off[i]) =
-                            make_uint4(pk[4 * i], pk[4 * i + 1], pk[4 * i + 2], pk[4 * i + 3]);
-                    if (kh == 0) bar.alpha[pb][row] = alpha;
-                    // one bulk copy a warp: 16-byte st.async stores of the same bytes took about 1000 cycles a tile
+                    if (kh == 0) bar.alpha[u & 1][row] = alpha;
+                    // one bulk copy a warp: 16-byte st.async stores of the same bytes took about 1000 cycles a page
                     ptx::fence_proxy_async_smem();
                     __syncwarp();
                     if (elect_one()) {
-                        bulk_to_peer(p_there + pb * kPBytes, p_here + pb * kPBytes, 2048, full_there + pb * 8);
-                        if (kh == 0) bulk_to_peer(a_there + pb * (kRows * 4), a_here + pb * (kRows * 4), 128, full_there + pb * 8);
+                        bulk_to_peer(p_there + pb * kPBytes, p_here + pb * kPBytes, 4096, full_there + pb * 8);
+                        if (kh == 0) bulk_to_peer(a_there + (u & 1u) * (kRows * 4), a_here + (u & 1u) * (kRows * 4), 128, full_there + pb * 8);
                     }
                     __syncwarp();
                     float a, b;
@@ -641,10 +680,6 @@ dense_mla_decode_kernel(const __grid_constant__ CUtensorMap kvmap, const uint16_
                     l_run += a + b;
                 } else if (lane == 0) {
                     ptx::mbar_arrive(&bar.s_read[sb]);
-                }
-                if (++pb == kPBufs) {
-                    pb = 0;
-                    pph ^= 1u;
                 }
                 timed_out = __any_sync(0xffffffffu, timed_out);
                 if (timed_out) break;
@@ -679,7 +714,8 @@ dense_mla_decode_kernel(const __grid_constant__ CUtensorMap kvmap, const uint16_
             if (w.t0 < w.t1) ++seg;
         } while (w.next());
         // rank 1's last signals land here before this CTA may finish
-        for (uint32_t j = u > kPBufs ? u - kPBufs : 0; j < u && !timed_out; ++j) wait(&bar.p_free[j % kPBufs], (j / kPBufs) & 1u);
+        for (uint32_t j = 2 * u > kPBufs ? 2 * u - kPBufs : 0; j < 2 * u && !timed_out; ++j)
+            wait(&bar.p_free[j % kPBufs], (j / kPBufs) & 1u);
     } else if (work && warp < kTmaWarp) {
         // ---------------------------------------------------------------- rescaling, output (rank 1)
         const int quad = warp & 3, dh = warp >> 2;                   // rows 32 quad .. + 31, output dims 256 dh .. + 255
@@ -688,19 +724,27 @@ dense_mla_decode_kernel(const __grid_constant__ CUtensorMap kvmap, const uint16_
         auto wait = [&](uint64_t* b, uint32_t parity) {
             if (!ptx::mbar_wait(b, parity, deadline)) timed_out = true;
         };
-        uint32_t u = 0, seg = 0, pb = 0, pph = 0;
+        unsigned char* stage_out = base + kVStages * kVStageBytes + warp * 2048;   // behind rank 1's stages
+        uint32_t u = 0, seg = 0;
         Walk w(bt, bar.start);
         do {
             const int live = w.rt.tokens * bt.H;
             const bool quad_live = quad * 32 < live, has_tiles = w.t0 < w.t1;
             const uint32_t quads = static_cast<uint32_t>((live + 31) / 32);
             for (int t = w.t0; t < w.t1; ++t, ++u) {
-                if (threadIdx.x == 0) ptx::mbar_arrive_expect_tx(&bar.p_full[pb], quads * (32 * kKeys * 2 + 32 * 4));
+                const uint32_t pb = 2 * (u & 1u), pph = (u >> 1) & 1u;
+                if (threadIdx.x == 0) {
+                    // the second buffer's previous phase is over once its P V is: this warp has not waited for it
+                    if (u >= 2) wait(&bar.p_full[pb + 1], pph ^ 1u);
+                    ptx::mbar_arrive_expect_tx(&bar.p_full[pb], quads * (kPBytes / 4 + 32 * 4));
+                    ptx::mbar_arrive_expect_tx(&bar.p_full[pb + 1], quads * (kPBytes / 4));
+                }
+                __syncwarp();
                 wait(&bar.p_full[pb], pph);
                 if (quad_live && t > w.t0) {
-                    const float alpha = bar.alpha[pb][row];
+                    const float alpha = bar.alpha[u & 1][row];
                     if (__any_sync(0xffffffffu, alpha != 1.0f)) {
-                        wait(&bar.pv_done[(u - 1) % kPBufs], ((u - 1) / kPBufs) & 1u);
+                        wait(&bar.pv_done[(u - 1) % kPvBars], ((u - 1) / kPvBars) & 1u);
                         __syncwarp();
                         ptx::tc_fence_after_sync();
 #pragma unroll 1
@@ -717,11 +761,7 @@ dense_mla_decode_kernel(const __grid_constant__ CUtensorMap kvmap, const uint16_
                     }
                 }
                 __syncwarp();
-                if (lane == 0) ptx::mbar_arrive(&bar.scaled[pb]);
-                if (++pb == kPBufs) {
-                    pb = 0;
-                    pph ^= 1u;
-                }
+                if (lane == 0) ptx::mbar_arrive(&bar.scaled[u & 1]);
                 timed_out = __any_sync(0xffffffffu, timed_out);
                 if (timed_out) break;
             }
@@ -733,36 +773,59 @@ dense_mla_decode_kernel(const __grid_constant__ CUtensorMap kvmap, const uint16_
                 inv = bar.fin[row];
                 __syncwarp();
                 if (lane == 0) arrive_remote(map_to_rank(ptx::smem_addr(&bar.fin_free), 0));
-                wait(&bar.pv_done[(u - 1) % kPBufs], ((u - 1) / kPBufs) & 1u);
+                wait(&bar.pv_done[(u - 1) % kPvBars], ((u - 1) / kPvBars) & 1u);
                 timed_out = __any_sync(0xffffffffu, timed_out);
                 if (timed_out) break;
                 ptx::tc_fence_after_sync();
             }
             if (quad_live) {
-                uint16_t* dst = out + (static_cast<int64_t>(w.rt.row0) * bt.H + row) * kValueDim + dh * 256;
-                float* pdst = part_o + (piece_slot(cluster, w) * slot_rows + row) * kValueDim + dh * 256;
+                // 128 bytes of each row at a time through 2 KB of shared memory, 16 rows and then the other 16, and
+                // out as whole 128-byte lines: a thread writing its own row touches 32 lines per store
+                const int64_t row0 = w.whole ? static_cast<int64_t>(w.rt.row0) * bt.H + quad * 32
+                                             : piece_slot(cluster, w) * slot_rows + quad * 32;
+                const int width = w.whole ? 64 : 32;                 // dims of 128 bytes
+                unsigned char* dst = w.whole ? reinterpret_cast<unsigned char*>(out) : reinterpret_cast<unsigned char*>(part_o);
+                const int64_t pitch = w.whole ? kValueDim * 2 : kValueDim * 4;
+                dst += row0 * pitch + dh * (pitch / 2) + (lane & 7) * 16;
 #pragma unroll 1
-                for (int cc = 0; cc < 256; cc += 32) {
-                    uint32_t o[32];
-                    if (has_tiles) {
-                        ptx::tmem_ld_32x32b_x32(o_addr + cc, o);
-                        ptx::tmem_wait_ld();
+                for (int cc = 0; cc < 256; cc += width) {
+                    uint32_t o[32];                                  // the row's 128 bytes
+                    if (w.whole) {
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+                            uint32_t x[32];
+                            if (has_tiles) {
+                                ptx::tmem_ld_32x32b_x32(o_addr + cc + 32 * i, x);
+                                ptx::tmem_wait_ld();
+                            }
+#pragma unroll
+                            for (int e = 0; e < 32; e += 2)
+                                o[16 * i + e / 2] = inv < 0.0f ? 0u : pack_bf16x2(__uint_as_float(x[e]) * inv, __uint_as_float(x[e + 1]) * inv);
+                        }
+                    } else {
+                        if (has_tiles) {
+                            ptx::tmem_ld_32x32b_x32(o_addr + cc, o);
+                            ptx::tmem_wait_ld();
+                        }
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) o[e] = inv < 0.0f ? 0u : __float_as_uint(__uint_as_float(o[e]) * inv);
                     }
 #pragma unroll
-                    for (int e = 0; e < 32; ++e) o[e] = inv < 0.0f ? 0u : __float_as_uint(__uint_as_float(o[e]) * inv);
-                    if (row < live) {
-                        if (w.whole) {
+                    for (int h = 0; h < 2; ++h) {
+                        __syncwarp();
+                        if ((lane >> 4) == h) {
 #pragma unroll
-                            for (int e = 0; e < 32; e += 8)
-                                *reinterpret_cast<uint4*>(dst + cc + e) =
-                                    make_uint4(pack_bf16x2(__uint_as_float(o[e]), __uint_as_float(o[e + 1])),
-                                               pack_bf16x2(__uint_as_float(o[e + 2]), __uint_as_float(o[e + 3])),
-                                               pack_bf16x2(__uint_as_float(o[e + 4]), __uint_as_float(o[e + 5])),
-                                               pack_bf16x2(__uint_as_float(o[e + 6]), __uint_as_float(o[e + 7])));
-                        } else {
+                            for (int i = 0; i < 8; ++i)
+                                *reinterpret_cast<uint4*>(stage_out + (lane & 15) * 128 + ((i ^ (lane & 7)) << 4)) =
+                                    make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+                        }
+                        __syncwarp();
 #pragma unroll
-                            for (int e = 0; e < 32; e += 4)
-                                *reinterpret_cast<uint4*>(pdst + cc + e) = make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+                        for (int i = 0; i < 4; ++i) {
+                            const int r = 4 * i + (lane >> 3);       // row of the 16
+                            const uint4 v = *reinterpret_cast<const uint4*>(stage_out + r * 128 + (((lane & 7) ^ (r & 7)) << 4));
+                            if (quad * 32 + 16 * h + r < live)
+                                *reinterpret_cast<uint4*>(dst + (16 * h + r) * pitch + cc * (w.whole ? 2 : 4)) = v;
                         }
                     }
                 }
@@ -796,52 +859,77 @@ __global__ void __launch_bounds__(kCombThreads)
 dense_mla_combine_kernel(const float* __restrict__ part_o, const float* __restrict__ part_lse,
                          const Meta* __restrict__ meta, int clusters, int slot_rows, uint16_t* __restrict__ out,
                          float* __restrict__ lse_out) {
+    // the row tiles to join, read at once (one after the other they would cost a memory latency each) and
+    // listed in order, so that every block counts alike
+    __shared__ Meta list[kCombThreads];
+    __shared__ int list_c[kCombThreads], found[kCombThreads / 32];
     ptx::griddep_wait();
-    const int lane = threadIdx.x & 31;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int nwarps = gridDim.x * (kCombThreads / 32);
-    int at = blockIdx.x * (kCombThreads / 32) + (threadIdx.x >> 5);   // this warp's next task, counted over all row tiles
-    for (int c = 0; c < clusters; ++c) {
-        const Meta m = meta[c];
-        const int tasks = m.rows * 4;
-        for (; at < tasks; at += nwarps) {
-            const int row = at >> 2, d0 = (at & 3) * 128 + lane * 4;
-            const int n = c - m.first_cluster + 1;
-            auto slot_of = [&](int j) {
-                return static_cast<int64_t>(j == 0 ? 2 * m.first_cluster + 1 : 2 * (m.first_cluster + j)) * slot_rows + row;
-            };
-            float top = -INFINITY;
-            bool nan = false;
-            for (int j = lane; j < n; j += 32) {
-                const float l = part_lse[slot_of(j)];
-                top = fmaxf(top, l);
-                nan |= l != l;
-            }
-            top = warp_max(top);
-            float tot = 0.0f;
-            if (top != -INFINITY)
-                for (int j = lane; j < n; j += 32) tot += exp2f(part_lse[slot_of(j)] - top);
-            tot = warp_sum(tot);
-            if (__any_sync(0xffffffffu, nan)) tot = NAN;
-            float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-            if (top != -INFINITY) {
-                const float inv = 1.0f / tot;
-#pragma unroll 4
-                for (int j = 0; j < n; ++j) {
-                    const int64_t s = slot_of(j);
-                    const float w = exp2f(part_lse[s] - top) * inv;
-                    const float4 o = *reinterpret_cast<const float4*>(part_o + s * kValueDim + d0);
-                    acc.x = fmaf(w, o.x, acc.x);
-                    acc.y = fmaf(w, o.y, acc.y);
-                    acc.z = fmaf(w, o.z, acc.z);
-                    acc.w = fmaf(w, o.w, acc.w);
-                }
-            }
-            *reinterpret_cast<uint2*>(out + (m.out_row + row) * kValueDim + d0) =
-                make_uint2(pack_bf16x2(acc.x, acc.y), pack_bf16x2(acc.z, acc.w));
-            if (lse_out != nullptr && (at & 3) == 0 && lane == 0)
-                lse_out[m.out_row + row] = top == -INFINITY ? -INFINITY : (top + log2f(tot)) * kLn2;
+    int at = blockIdx.x * (kCombThreads / 32) + warp;                 // this warp's next task, counted over all row tiles
+    for (int c0 = 0; c0 < clusters; c0 += kCombThreads) {
+        Meta own{0, 0, 0};
+        if (c0 + static_cast<int>(threadIdx.x) < clusters) own = meta[c0 + threadIdx.x];
+        const uint32_t mask = __ballot_sync(0xffffffffu, own.rows > 0);
+        if (lane == 0) found[warp] = __popc(mask);
+        __syncthreads();
+        int total = 0, before = 0;
+        for (int i = 0; i < kCombThreads / 32; ++i) {
+            if (i == warp) before = total;
+            total += found[i];
         }
-        at -= tasks;
+        if (own.rows > 0) {
+            const int j = before + __popc(mask & ((1u << lane) - 1u));
+            list[j] = own;
+            list_c[j] = c0 + threadIdx.x;
+        }
+        __syncthreads();
+        for (int li = 0; li < total; ++li) {
+            const Meta m = list[li];
+            const int c = list_c[li];
+            const int tasks = m.rows * 4;
+            for (; at < tasks; at += nwarps) {
+                const int row = at >> 2, d0 = (at & 3) * 128 + lane * 4;
+                const int n = c - m.first_cluster + 1;
+                auto slot_of = [&](int j) {
+                    return static_cast<int64_t>(j == 0 ? 2 * m.first_cluster + 1 : 2 * (m.first_cluster + j)) * slot_rows + row;
+                };
+                float top = -INFINITY;
+                bool nan = false;
+                for (int j = lane; j < n; j += 32) {
+                    const float l = part_lse[slot_of(j)];
+                    top = fmaxf(top, l);
+                    nan |= l != l;
+                }
+                top = warp_max(top);
+                float tot = 0.0f;
+                if (top != -INFINITY)
+                    for (int j = lane; j < n; j += 32) tot += exp2f(part_lse[slot_of(j)] - top);
+                tot = warp_sum(tot);
+                nan = __any_sync(0xffffffffu, nan);
+                float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                if (top != -INFINITY) {
+                    const float inv = 1.0f / tot;
+#pragma unroll 4
+                    for (int j = 0; j < n; ++j) {
+                        const int64_t s = slot_of(j);
+                        const float w = exp2f(part_lse[s] - top) * inv;
+                        const float4 o = *reinterpret_cast<const float4*>(part_o + s * kValueDim + d0);
+                        acc.x = fmaf(w, o.x, acc.x);
+                        acc.y = fmaf(w, o.y, acc.y);
+                        acc.z = fmaf(w, o.z, acc.z);
+                        acc.w = fmaf(w, o.w, acc.w);
+                    }
+                }
+                if (nan) acc = make_float4(NAN, NAN, NAN, NAN);
+                *reinterpret_cast<uint2*>(out + (m.out_row + row) * kValueDim + d0) =
+                    make_uint2(pack_bf16x2(acc.x, acc.y), pack_bf16x2(acc.z, acc.w));
+                if (lse_out != nullptr && (at & 3) == 0 && lane == 0)
+                    lse_out[m.out_row + row] = nan ? NAN : (top == -INFINITY ? -INFINITY : (top + log2f(tot)) * kLn2);
+            }
+            at -= tasks;
+        }
+        __syncthreads();
     }
 }
 
@@ -880,8 +968,9 @@ extern "C" dsa_status dsa_dense_mla_decode(const void* q_bf16, const void* kv_po
     if (workspace == nullptr || !aligned16(workspace) || workspace_bytes < need) return DSA_ERR_INVALID_ARG;
     auto encode = attn::tensor_map_encoder();
     if (encode == nullptr) return DSA_ERR_CUDA;
-    CUtensorMap kvmap;
-    if (!attn::encode_bf16_3d(encode, &kvmap, kv_pool, kLatentDim, 1, num_pages * kPage, kLatentDim, kLatentDim, 64, kKeys))
+    CUtensorMap kvmap, qmap;
+    if (!attn::encode_bf16_3d(encode, &kvmap, kv_pool, kLatentDim, 1, num_pages * kPage, kLatentDim, kLatentDim, 64, kPage) ||
+        !attn::encode_bf16_3d(encode, &qmap, q_bf16, kLatentDim, 1, static_cast<uint64_t>(T) * H, kLatentDim, kLatentDim, 64, kRows))
         return DSA_ERR_CUDA;
     const int clusters = decode_clusters(), slot_rows = decode_slot_rows(T, H);
     Meta* meta = static_cast<Meta*>(workspace);
@@ -892,7 +981,7 @@ extern "C" dsa_status dsa_dense_mla_decode(const void* q_bf16, const void* kv_po
                              static_cast<int>(kDecSmem)) != cudaSuccess)
         return DSA_ERR_CUDA;
     dense_mla_decode_kernel<<<2 * clusters, kDecThreads, kDecSmem, s>>>(
-        kvmap, static_cast<const uint16_t*>(q_bf16), static_cast<int>(num_pages), block_table,
+        kvmap, qmap, static_cast<int>(num_pages), block_table,
         Batch{seq_lens, cu_q, B, T, H, max_pages}, scale, static_cast<uint16_t*>(out_bf16), lse, part_o, part_lse, meta,
         slot_rows, dev_err);
     if (cudaGetLastError() != cudaSuccess) return DSA_ERR_CUDA;
