@@ -583,18 +583,68 @@ def dsa_sparse_mla_decode_noalloc(q_bf16: torch.Tensor, kv_pool: torch.Tensor, b
     _count(2 if T > 0 else 0)
 
 
-def _one_device(**tensors) -> None:
-    """The tensors of a call live on one device, the current one (whose stream it is enqueued on)."""
-    for name, t in tensors.items():
-        if t is not None:
-            _need(t.is_cuda and t.device.index == torch.cuda.current_device(),
-                  f"{name} must be on the current CUDA device")
+# The calls below check and marshal their tensors with one short function each: at decode sizes the
+# binding's own time (about 25 us with a formatted message and a device query per check) is longer than
+# the kernels'.
+
+def _bad(t, dtype, dev: int, name: str):
+    """What is wrong with a tensor that failed the quick check."""
+    _need(isinstance(t, torch.Tensor) and t.is_cuda, f"{name} must be a CUDA tensor")
+    _need(t.get_device() == dev, f"{name} must be on the current CUDA device")
+    _need(t.dtype == dtype, f"{name} must be {dtype}, got {t.dtype}")
+    _need(t.is_contiguous(), f"{name} must be contiguous")
 
 
-def _err_word(dev_err: Optional[torch.Tensor]) -> None:
-    if dev_err is not None:
-        _cuda(dev_err, torch.int32, "dev_err")
-        _need(dev_err.numel() >= 1, "dev_err must hold one int32")
+def _arr(t: torch.Tensor, dtype, dev: int, name: str) -> int:
+    """Address of a contiguous tensor of `dtype` on the current device `dev`."""
+    if t.dtype is not dtype or t.get_device() != dev or not t.is_contiguous():
+        _bad(t, dtype, dev, name)
+    return t.data_ptr()
+
+
+def _opt(t: Optional[torch.Tensor], dtype, dev: int, name: str) -> Optional[int]:
+    return None if t is None else _arr(t, dtype, dev, name)
+
+
+def _dense_rows(t: torch.Tensor, dtype, width: int, dev: int, name: str):
+    """(address, rows, row stride) of a [rows, width] tensor whose rows are dense and may be strided; a
+    single row's stride is never used, so its width stands in for it."""
+    if t.dtype is not dtype or t.get_device() != dev or t.dim() != 2:
+        _need(t.dim() == 2, f"{name} must have two dimensions")
+        _bad(t, dtype, dev, name)
+    rows, cols = t.shape
+    if cols != width or (width > 1 and t.stride(1) != 1):
+        raise ValueError(f"{name} must be [rows, {width}] with dense rows")
+    return t.data_ptr(), rows, (t.stride(0) if rows > 1 else width)
+
+
+def _th(t: torch.Tensor, width: int, dev: int, name: str):
+    """(address, row stride, head stride) of a [rows, H, width] bf16 view whose last dim is dense; the
+    stride of an axis of length 1 is never used and a dense one stands in for it."""
+    if t.dtype is not torch.bfloat16 or t.get_device() != dev:
+        _bad(t, torch.bfloat16, dev, name)
+    if t.dim() != 3 or t.shape[2] != width or t.stride(2) != 1:
+        raise ValueError(f"{name} must be [rows, H, {width}], last dim dense")
+    rows, heads, _ = t.shape
+    rs, hs, _ = t.stride()
+    if heads <= 1:
+        hs = width
+    return t.data_ptr(), (rs if rows > 1 else max(width, hs * heads)), hs
+
+
+def _raw_stream(stream) -> int:
+    if stream is None:
+        return torch.cuda.current_stream().cuda_stream
+    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+
+
+def _current_device() -> int:
+    """Index of the current CUDA device; -2, which no tensor is on, where there is none."""
+    load()
+    try:
+        return torch.cuda.current_device()
+    except (RuntimeError, AssertionError):
+        return -2
 
 
 def dsa_store_latent_prologue(kv_a: torch.Tensor, norm_weight: torch.Tensor, eps: float, cos_sin_cache: torch.Tensor,
@@ -603,44 +653,31 @@ def dsa_store_latent_prologue(kv_a: torch.Tensor, norm_weight: torch.Tensor, eps
                               dev_err: Optional[torch.Tensor] = None, stream=None) -> None:
     """RMSNorm of the 512 latent dims and rotary embedding of the 64 rope dims of kv_a [n, 576] (rows may
     be strided), stored by slot into the bf16 latent cache; also written to latent_out [n, 576]."""
-    lib = load()
-    _rows(kv_a, torch.bfloat16, "kv_a")
-    _cuda(norm_weight, torch.float32, "norm_weight")
-    _cuda(cos_sin_cache, torch.float32, "cos_sin_cache")
-    _cuda(positions, torch.int64, "positions")
-    _cuda(slot_mapping, torch.int64, "slot_mapping")
-    _cuda(kv_pool, torch.bfloat16, "kv_pool")
-    _err_word(dev_err)
-    _one_device(kv_a=kv_a, norm_weight=norm_weight, cos_sin_cache=cos_sin_cache, positions=positions,
-                slot_mapping=slot_mapping, kv_pool=kv_pool, latent_out=latent_out, dev_err=dev_err)
-    n = kv_a.shape[0]
-    _need(kv_a.shape[1] == LATENT_DIM, "kv_a must be [n, 576]")
-    _need(norm_weight.numel() == VALUE_DIM, "norm_weight must have 512 entries")
-    _need(cos_sin_cache.dim() == 2 and cos_sin_cache.shape[1] == 64, "cos_sin_cache must be [max_position, 64]")
-    _need(positions.numel() == n and slot_mapping.numel() == n, "positions / slot_mapping must have n entries")
-    _need(kv_pool.dim() == 3 and tuple(kv_pool.shape[1:]) == (64, LATENT_DIM), "kv_pool must be [pages, 64, 576]")
+    dev = _current_device()
+    src, n, stride = _dense_rows(kv_a, torch.bfloat16, LATENT_DIM, dev, "kv_a")
+    w = _arr(norm_weight, torch.float32, dev, "norm_weight")
+    cs = _arr(cos_sin_cache, torch.float32, dev, "cos_sin_cache")
+    pos = _arr(positions, torch.int64, dev, "positions")
+    slots = _arr(slot_mapping, torch.int64, dev, "slot_mapping")
+    pool = _arr(kv_pool, torch.bfloat16, dev, "kv_pool")
+    err = _opt(dev_err, torch.int32, dev, "dev_err")
+    if norm_weight.numel() != VALUE_DIM:
+        raise ValueError("norm_weight must have 512 entries")
+    if cos_sin_cache.dim() != 2 or cos_sin_cache.shape[1] != 64:
+        raise ValueError("cos_sin_cache must be [max_position, 64]")
+    if positions.numel() != n or slot_mapping.numel() != n:
+        raise ValueError("positions / slot_mapping must have n entries")
+    if kv_pool.dim() != 3 or kv_pool.shape[1] != 64 or kv_pool.shape[2] != LATENT_DIM:
+        raise ValueError("kv_pool must be [pages, 64, 576]")
+    out, out_stride = None, LATENT_DIM
     if latent_out is not None:
-        _rows(latent_out, torch.bfloat16, "latent_out")
-        _need(tuple(latent_out.shape) == (n, LATENT_DIM), "latent_out must be [n, 576]")
-    _check("dsa_store_latent_prologue", lib.dsa_store_latent_prologue(
-        _ptr(kv_a), _row_stride(kv_a), _ptr(norm_weight), float(eps), _ptr(cos_sin_cache), cos_sin_cache.shape[0],
-        _ptr(positions), _ptr(slot_mapping), n, _ptr(kv_pool), kv_pool.shape[0], _ptr(latent_out),
-        LATENT_DIM if latent_out is None else _row_stride(latent_out), int(flags), _ptr(dev_err), _stream(stream)))
+        out, rows, out_stride = _dense_rows(latent_out, torch.bfloat16, LATENT_DIM, dev, "latent_out")
+        if rows != n:
+            raise ValueError("latent_out must be [n, 576]")
+    _check("dsa_store_latent_prologue", _lib.dsa_store_latent_prologue(
+        src, stride, w, eps, cs, cos_sin_cache.shape[0], pos, slots, n, pool, kv_pool.shape[0], out, out_stride, flags,
+        err, _raw_stream(stream)))
     _count(1 if n > 0 else 0)
-
-
-def _row_stride(t: torch.Tensor) -> int:
-    """Row stride in elements; a single row's stride is never used, so its width stands in for it."""
-    return t.stride(0) if t.shape[0] > 1 else t.shape[-1]
-
-
-def _th_strides(t: torch.Tensor, inner: int, name: str):
-    """(row stride, head stride) of a [rows, H, inner] bf16 CUDA view whose last dim is dense; the stride
-    of an axis of length 1 is never used and a dense one stands in for it."""
-    _need(t.is_cuda and t.dtype == torch.bfloat16, f"{name} must be a bf16 CUDA tensor")
-    _need(t.dim() == 3 and t.shape[2] == inner and t.stride(2) == 1, f"{name} must be [rows, H, {inner}], last dim dense")
-    head = t.stride(1) if t.shape[1] > 1 else inner
-    return (t.stride(0) if t.shape[0] > 1 else max(inner, head * t.shape[1])), head
 
 
 def dsa_dense_mla_prefill(q: torch.Tensor, k_nope: torch.Tensor, k_pe: torch.Tensor, v: torch.Tensor,
@@ -649,28 +686,27 @@ def dsa_dense_mla_prefill(q: torch.Tensor, k_nope: torch.Tensor, k_pe: torch.Ten
                           dev_err: Optional[torch.Tensor] = None, stream=None) -> None:
     """Expanded latent attention of ragged prompts: q [T, H, 192], k_nope / v [S, H, 128], k_pe [S, 64]
     (all may be strided views, e.g. of one [S, H, 256] up-projection), out [T, H, 128], lse [T, H]."""
-    lib = load()
-    qs = _th_strides(q, 192, "q")
-    ks = _th_strides(k_nope, 128, "k_nope")
-    vs = _th_strides(v, 128, "v")
-    os_ = _th_strides(out, 128, "out")
-    _rows(k_pe, torch.bfloat16, "k_pe")
-    _cuda(cu_q, torch.int32, "cu_q")
-    _cuda(cu_k, torch.int32, "cu_k")
-    T, H = q.shape[0], q.shape[1]
-    S, B = k_nope.shape[0], cu_q.numel() - 1
-    _need(B >= 0 and cu_k.numel() == B + 1, "cu_q and cu_k must have B + 1 entries")
-    _need(k_nope.shape[1] == H and tuple(v.shape[:2]) == (S, H), "k_nope and v must be [S, H, 128]")
-    _need(tuple(k_pe.shape) == (S, 64), "k_pe must be [S, 64]")
-    _need(tuple(out.shape[:2]) == (T, H), "out must be [T, H, 128]")
-    if lse is not None:
-        _cuda(lse, torch.float32, "lse")
-        _need(tuple(lse.shape) == (T, H), "lse must be [T, H]")
-    _err_word(dev_err)
-    _one_device(q=q, k_nope=k_nope, k_pe=k_pe, v=v, cu_q=cu_q, cu_k=cu_k, out=out, lse=lse, dev_err=dev_err)
-    _check("dsa_dense_mla_prefill", lib.dsa_dense_mla_prefill(
-        _ptr(q), *qs, _ptr(k_nope), *ks, _ptr(k_pe), _row_stride(k_pe), _ptr(v), *vs, _ptr(cu_q), _ptr(cu_k), B, T, S,
-        H, float(scale), DSA_CAUSAL if causal else 0, _ptr(out), *os_, _ptr(lse), _ptr(dev_err), _stream(stream)))
+    dev = _current_device()
+    qp, q_row, q_head = _th(q, 192, dev, "q")
+    kp, k_row, k_head = _th(k_nope, 128, dev, "k_nope")
+    vp, v_row, v_head = _th(v, 128, dev, "v")
+    op, o_row, o_head = _th(out, 128, dev, "out")
+    pep, S, pe_row = _dense_rows(k_pe, torch.bfloat16, 64, dev, "k_pe")
+    cq = _arr(cu_q, torch.int32, dev, "cu_q")
+    ck = _arr(cu_k, torch.int32, dev, "cu_k")
+    lp = _opt(lse, torch.float32, dev, "lse")
+    err = _opt(dev_err, torch.int32, dev, "dev_err")
+    T, H, _ = q.shape
+    B = cu_q.numel() - 1
+    if B < 0 or cu_k.numel() != B + 1:
+        raise ValueError("cu_q and cu_k must have B + 1 entries")
+    if k_nope.shape[:2] != (S, H) or v.shape[:2] != (S, H):
+        raise ValueError("k_nope and v must be [S, H, 128], k_pe [S, 64]")
+    if out.shape[:2] != (T, H) or (lse is not None and lse.shape != (T, H)):
+        raise ValueError("out must be [T, H, 128], lse [T, H]")
+    _check("dsa_dense_mla_prefill", _lib.dsa_dense_mla_prefill(
+        qp, q_row, q_head, kp, k_row, k_head, pep, pe_row, vp, v_row, v_head, cq, ck, B, T, S, H, scale,
+        DSA_CAUSAL if causal else 0, op, o_row, o_head, lp, err, _raw_stream(stream)))
     _count(1 if T > 0 and B > 0 and H > 0 else 0)
 
 
@@ -685,35 +721,35 @@ def dsa_dense_mla_decode(q_bf16: torch.Tensor, kv_pool: torch.Tensor, block_tabl
     """Absorbed latent attention of the query rows over every visible row of the paged cache.  `workspace`
     holds at least dsa_dense_mla_decode_workspace_size(T, H) bytes; when it is None a buffer of that size
     is taken from torch's allocator for this call."""
-    lib = load()
-    _cuda(q_bf16, torch.bfloat16, "q_bf16")
-    _cuda(kv_pool, torch.bfloat16, "kv_pool")
-    _cuda(block_table, torch.int32, "block_table")
-    _cuda(seq_lens, torch.int32, "seq_lens")
-    _cuda(cu_q, torch.int32, "cu_q")
-    _cuda(out, torch.bfloat16, "out")
-    _need(q_bf16.dim() == 3 and q_bf16.shape[2] == LATENT_DIM, "q_bf16 must be [T, H, 576]")
+    dev = _current_device()
+    qp = _arr(q_bf16, torch.bfloat16, dev, "q_bf16")
+    pool = _arr(kv_pool, torch.bfloat16, dev, "kv_pool")
+    table = _arr(block_table, torch.int32, dev, "block_table")
+    lens = _arr(seq_lens, torch.int32, dev, "seq_lens")
+    cq = _arr(cu_q, torch.int32, dev, "cu_q")
+    op = _arr(out, torch.bfloat16, dev, "out")
+    lp = _opt(lse, torch.float32, dev, "lse")
+    err = _opt(dev_err, torch.int32, dev, "dev_err")
+    if q_bf16.dim() != 3 or q_bf16.shape[2] != LATENT_DIM:
+        raise ValueError("q_bf16 must be [T, H, 576]")
     T, H, _ = q_bf16.shape
     B = seq_lens.numel()
-    _need(kv_pool.dim() == 3 and tuple(kv_pool.shape[1:]) == (64, LATENT_DIM), "kv_pool must be [pages, 64, 576]")
-    _need(cu_q.numel() == B + 1 and block_table.dim() == 2 and block_table.shape[0] == B, "metadata shapes")
-    _need(tuple(out.shape) == (T, H, VALUE_DIM), "out must be [T, H, 512]")
-    if lse is not None:
-        _cuda(lse, torch.float32, "lse")
-        _need(tuple(lse.shape) == (T, H), "lse must be [T, H]")
+    if kv_pool.dim() != 3 or kv_pool.shape[1] != 64 or kv_pool.shape[2] != LATENT_DIM:
+        raise ValueError("kv_pool must be [pages, 64, 576]")
+    if cu_q.numel() != B + 1 or block_table.dim() != 2 or block_table.shape[0] != B:
+        raise ValueError("cu_q must have B + 1 entries, block_table B rows")
+    if out.shape != (T, H, VALUE_DIM) or (lse is not None and lse.shape != (T, H)):
+        raise ValueError("out must be [T, H, 512], lse [T, H]")
     if workspace is None:
         _need(stream is None, "a call on an explicit stream brings its own workspace")
         workspace = torch.empty(max(16, dsa_dense_mla_decode_workspace_size(T, H)), dtype=torch.uint8,
                                 device=q_bf16.device)
-    _need(workspace.is_cuda and workspace.is_contiguous(), "workspace must be a contiguous CUDA tensor")
-    _err_word(dev_err)
-    _one_device(q_bf16=q_bf16, kv_pool=kv_pool, block_table=block_table, seq_lens=seq_lens, cu_q=cu_q, out=out,
-                lse=lse, workspace=workspace, dev_err=dev_err)
-    _check("dsa_dense_mla_decode", lib.dsa_dense_mla_decode(
-        _ptr(q_bf16), _ptr(kv_pool), kv_pool.shape[0], _ptr(block_table), block_table.shape[1], _ptr(seq_lens),
-        _ptr(cu_q), B, T, H, float(scale), _ptr(out), _ptr(lse), _ptr(workspace),
-        workspace.numel() * workspace.element_size(), _ptr(dev_err), _stream(stream)))
-    _count((1 + (1 if dsa_dense_mla_decode_workspace_size(T, H) > 0 else 0)) if T > 0 and B > 0 else 0)
+    elif workspace.get_device() != dev or not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous CUDA tensor on the current device")
+    _check("dsa_dense_mla_decode", _lib.dsa_dense_mla_decode(
+        qp, pool, kv_pool.shape[0], table, block_table.shape[1], lens, cq, B, T, H, scale, op, lp,
+        workspace.data_ptr(), workspace.numel() * workspace.element_size(), err, _raw_stream(stream)))
+    _count(2 if T > 0 and B > 0 else 0)   # the attention and the joining of its pieces
 
 
 def dsa_verify_drafts(target_probs: torch.Tensor, draft_tokens: torch.Tensor, cu_q: torch.Tensor,
@@ -722,29 +758,30 @@ def dsa_verify_drafts(target_probs: torch.Tensor, draft_tokens: torch.Tensor, cu
                       dev_err: Optional[torch.Tensor] = None, stream=None) -> None:
     """Accepts drafted tokens against target_probs [T, V] and draws the token after the last accepted one
     (from max(p - q, 0) after a rejection); draft_probs None: certain (greedy) drafts."""
-    lib = load()
-    _rows(target_probs, torch.float32, "target_probs")
-    _cuda(draft_tokens, torch.int32, "draft_tokens")
-    _cuda(cu_q, torch.int32, "cu_q")
-    _cuda(accept_u, torch.float32, "accept_u")
-    _cuda(sample_u, torch.float32, "sample_u")
-    _cuda(out_tokens, torch.int32, "out_tokens")
-    _cuda(accepted, torch.int32, "accepted")
-    T, V = target_probs.shape
+    dev = _current_device()
+    if target_probs.dim() != 2:
+        raise ValueError("target_probs must be [T, V]")
+    V = target_probs.shape[1]
+    tp, T, ld_t = _dense_rows(target_probs, torch.float32, V, dev, "target_probs")
+    tok = _arr(draft_tokens, torch.int32, dev, "draft_tokens")
+    cq = _arr(cu_q, torch.int32, dev, "cu_q")
+    ua = _arr(accept_u, torch.float32, dev, "accept_u")
+    us = _arr(sample_u, torch.float32, dev, "sample_u")
+    ot = _arr(out_tokens, torch.int32, dev, "out_tokens")
+    ac = _arr(accepted, torch.int32, dev, "accepted")
+    err = _opt(dev_err, torch.int32, dev, "dev_err")
     B = cu_q.numel() - 1
-    _need(B >= 0 and sample_u.numel() == B and accepted.numel() == B, "cu_q [B + 1], sample_u [B], accepted [B]")
-    _need(draft_tokens.numel() == T and accept_u.numel() == T and out_tokens.numel() == T,
-          "draft_tokens, accept_u and out_tokens must have T entries")
+    if B < 0 or sample_u.numel() != B or accepted.numel() != B:
+        raise ValueError("cu_q must have B + 1 entries, sample_u and accepted B")
+    if draft_tokens.numel() != T or accept_u.numel() != T or out_tokens.numel() != T:
+        raise ValueError("draft_tokens, accept_u and out_tokens must have T entries")
+    dp, ld_d = None, 0
     if draft_probs is not None:
-        _rows(draft_probs, torch.float32, "draft_probs")
-        _need(tuple(draft_probs.shape) == (T, V), "draft_probs must be [T, V]")
-    _err_word(dev_err)
-    _one_device(target_probs=target_probs, draft_probs=draft_probs, draft_tokens=draft_tokens, cu_q=cu_q,
-                accept_u=accept_u, sample_u=sample_u, out_tokens=out_tokens, accepted=accepted, dev_err=dev_err)
-    _check("dsa_verify_drafts", lib.dsa_verify_drafts(
-        _ptr(target_probs), _row_stride(target_probs), _ptr(draft_probs),
-        0 if draft_probs is None else _row_stride(draft_probs), V, _ptr(draft_tokens), _ptr(cu_q), B, T,
-        _ptr(accept_u), _ptr(sample_u), _ptr(out_tokens), _ptr(accepted), _ptr(dev_err), _stream(stream)))
+        dp, rows, ld_d = _dense_rows(draft_probs, torch.float32, V, dev, "draft_probs")
+        if rows != T:
+            raise ValueError("draft_probs must be [T, V]")
+    _check("dsa_verify_drafts", _lib.dsa_verify_drafts(tp, ld_t, dp, ld_d, V, tok, cq, B, T, ua, us, ot, ac, err,
+                                                       _raw_stream(stream)))
     _count(1 if B > 0 else 0)
 
 

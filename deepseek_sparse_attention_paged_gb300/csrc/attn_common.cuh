@@ -7,6 +7,8 @@
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
+#include <atomic>
+
 #include "dsa_common.cuh"
 #include "sm100_ptx.cuh"
 
@@ -120,15 +122,20 @@ using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t
                                    const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
                                    CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
 
-// cuTensorMapEncodeTiled through the runtime (no link against the driver library); NULL if it is
-// not there.
+// cuTensorMapEncodeTiled through the runtime (no link against the driver library), kept once it is found;
+// NULL if it is not there.
 inline EncodeTiledFn tensor_map_encoder() {
+    static std::atomic<EncodeTiledFn> found{nullptr};
+    EncodeTiledFn encode = found.load(std::memory_order_relaxed);
+    if (encode != nullptr) return encode;
     void* fn = nullptr;
     cudaDriverEntryPointQueryResult q;
     if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault, &q) != cudaSuccess ||
         q != cudaDriverEntryPointSuccess)
         return nullptr;
-    return reinterpret_cast<EncodeTiledFn>(fn);
+    encode = reinterpret_cast<EncodeTiledFn>(fn);
+    found.store(encode, std::memory_order_relaxed);
+    return encode;
 }
 
 // Map of a bf16 array [n2][n1][n0] (strides in elements, innermost dense), boxes [b2][1][b0] with the
