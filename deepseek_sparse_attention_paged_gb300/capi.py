@@ -632,9 +632,13 @@ def _th(t: torch.Tensor, width: int, dev: int, name: str):
     return t.data_ptr(), (rs if rows > 1 else max(width, hs * heads)), hs
 
 
-def _raw_stream(stream) -> int:
+# the current stream's handle without building a Stream object (3 us)
+_current_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _raw_stream(stream, dev: int) -> int:
     if stream is None:
-        return torch.cuda.current_stream().cuda_stream
+        return _current_raw_stream(dev) if _current_raw_stream else torch.cuda.current_stream().cuda_stream
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
@@ -676,7 +680,7 @@ def dsa_store_latent_prologue(kv_a: torch.Tensor, norm_weight: torch.Tensor, eps
             raise ValueError("latent_out must be [n, 576]")
     _check("dsa_store_latent_prologue", _lib.dsa_store_latent_prologue(
         src, stride, w, eps, cs, cos_sin_cache.shape[0], pos, slots, n, pool, kv_pool.shape[0], out, out_stride, flags,
-        err, _raw_stream(stream)))
+        err, _raw_stream(stream, dev)))
     _count(1 if n > 0 else 0)
 
 
@@ -706,7 +710,7 @@ def dsa_dense_mla_prefill(q: torch.Tensor, k_nope: torch.Tensor, k_pe: torch.Ten
         raise ValueError("out must be [T, H, 128], lse [T, H]")
     _check("dsa_dense_mla_prefill", _lib.dsa_dense_mla_prefill(
         qp, q_row, q_head, kp, k_row, k_head, pep, pe_row, vp, v_row, v_head, cq, ck, B, T, S, H, scale,
-        DSA_CAUSAL if causal else 0, op, o_row, o_head, lp, err, _raw_stream(stream)))
+        DSA_CAUSAL if causal else 0, op, o_row, o_head, lp, err, _raw_stream(stream, dev)))
     _count(1 if T > 0 and B > 0 and H > 0 else 0)
 
 
@@ -748,7 +752,7 @@ def dsa_dense_mla_decode(q_bf16: torch.Tensor, kv_pool: torch.Tensor, block_tabl
         raise ValueError("workspace must be a contiguous CUDA tensor on the current device")
     _check("dsa_dense_mla_decode", _lib.dsa_dense_mla_decode(
         qp, pool, kv_pool.shape[0], table, block_table.shape[1], lens, cq, B, T, H, scale, op, lp,
-        workspace.data_ptr(), workspace.numel() * workspace.element_size(), err, _raw_stream(stream)))
+        workspace.data_ptr(), workspace.numel() * workspace.element_size(), err, _raw_stream(stream, dev)))
     _count(2 if T > 0 and B > 0 else 0)   # the attention and the joining of its pieces
 
 
@@ -775,13 +779,15 @@ def dsa_verify_drafts(target_probs: torch.Tensor, draft_tokens: torch.Tensor, cu
         raise ValueError("cu_q must have B + 1 entries, sample_u and accepted B")
     if draft_tokens.numel() != T or accept_u.numel() != T or out_tokens.numel() != T:
         raise ValueError("draft_tokens, accept_u and out_tokens must have T entries")
+    if ot == tok and T > 0:
+        raise ValueError("out_tokens must not be draft_tokens")
     dp, ld_d = None, 0
     if draft_probs is not None:
         dp, rows, ld_d = _dense_rows(draft_probs, torch.float32, V, dev, "draft_probs")
         if rows != T:
             raise ValueError("draft_probs must be [T, V]")
     _check("dsa_verify_drafts", _lib.dsa_verify_drafts(tp, ld_t, dp, ld_d, V, tok, cq, B, T, ua, us, ot, ac, err,
-                                                       _raw_stream(stream)))
+                                                       _raw_stream(stream, dev)))
     _count(1 if B > 0 else 0)
 
 

@@ -815,25 +815,25 @@ dense_mla_decode_kernel(const __grid_constant__ CUtensorMap kvmap, const __grid_
 #pragma unroll 1
                 for (int cc = 0; cc < 256; cc += width) {
                     uint32_t o[32];                                  // the row's 128 bytes
+                    if (has_tiles) ptx::tmem_ld_32x32b_x32(o_addr + cc, o);
                     if (w.whole) {
+                        uint32_t x[32];
+                        if (has_tiles) ptx::tmem_ld_32x32b_x32(o_addr + cc + 32, x);
+                        ptx::tmem_wait_ld();
 #pragma unroll
-                        for (int i = 0; i < 2; ++i) {
-                            uint32_t x[32];
-                            if (has_tiles) {
-                                ptx::tmem_ld_32x32b_x32(o_addr + cc + 32 * i, x);
-                                ptx::tmem_wait_ld();
-                            }
+                        for (int e = 0; e < 16; ++e)
+                            o[e] = pack_bf16x2(__uint_as_float(o[2 * e]) * inv, __uint_as_float(o[2 * e + 1]) * inv);
 #pragma unroll
-                            for (int e = 0; e < 32; e += 2)
-                                o[16 * i + e / 2] = inv < 0.0f ? 0u : pack_bf16x2(__uint_as_float(x[e]) * inv, __uint_as_float(x[e + 1]) * inv);
-                        }
+                        for (int e = 0; e < 16; ++e)
+                            o[16 + e] = pack_bf16x2(__uint_as_float(x[2 * e]) * inv, __uint_as_float(x[2 * e + 1]) * inv);
                     } else {
-                        if (has_tiles) {
-                            ptx::tmem_ld_32x32b_x32(o_addr + cc, o);
-                            ptx::tmem_wait_ld();
-                        }
+                        ptx::tmem_wait_ld();
 #pragma unroll
-                        for (int e = 0; e < 32; ++e) o[e] = inv < 0.0f ? 0u : __float_as_uint(__uint_as_float(o[e]) * inv);
+                        for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * inv);
+                    }
+                    if (inv < 0.0f) {
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) o[e] = 0u;
                     }
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {

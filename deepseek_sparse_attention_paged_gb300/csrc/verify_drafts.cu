@@ -7,17 +7,17 @@
 // not, the next token is drawn from w = max(p - q, 0) (after the last draft: w = p) by inverting its
 // cumulative sum: the least v with sum_{i <= v} w_i > u_s sum_i w_i.
 //
-// Sums: the drawn token must not depend on how the sum is split, so sums are carried in about 48
-// bits: a thread adds its 16 values of a group of 512 as fp32 pairs (high word, error word) -- the
-// difference p - q included, exactly -- and group sums are added in fp64.  fp64 throughout would
-// be bound by the fp64 unit (two conversions, a subtraction and an addition per entry), the pairs
-// keep it on HBM.  Adding in fp32 would move the borders by about 2^-24 of the sum each.
+// Sums: the drawn token must not depend on how the sum is split, so every sum is an unevaluated pair of
+// fp32 numbers (about 47 bits), the difference p - q included.  fp64 would do the same, but its unit here
+// is slow enough to be felt: with it one request took 14 us.  Adding in fp32 would move the borders by
+// about 2^-24 of the sum each.
 //
 // One cluster of 8 CTAs per request, each with an eighth of the vocabulary: only the one row of p
 // and of q that the draw needs is read, once, with all group sums kept in shared memory; the CTAs
 // swap their totals through distributed shared memory, and the CTA whose range holds the border
 // re-reads one group of 512 entries.
 #include "dsa_common.cuh"
+#include "sm100_ptx.cuh"
 
 namespace dsa {
 namespace {
@@ -37,26 +37,50 @@ __device__ __forceinline__ uint32_t cluster_rank() {
 // The two halves of a cluster barrier: what comes between needs no peer.
 __device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
 __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
-__device__ __forceinline__ void cluster_sync() {
-    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+
+// A sum hi + lo, |lo| at most half a unit of hi.
+struct Sum {
+    float hi, lo;
+};
+
+__device__ __forceinline__ Sum normal(float hi, float lo) {
+    const float h = __fadd_rn(hi, lo);
+    return Sum{h, __fsub_rn(lo, __fsub_rn(h, hi))};
+}
+__device__ __forceinline__ Sum operator+(Sum a, Sum b) {
+    const float s = __fadd_rn(a.hi, b.hi);
+    return normal(s, __fadd_rn(two_sum_err(a.hi, b.hi, s), __fadd_rn(a.lo, b.lo)));
+}
+__device__ __forceinline__ bool operator>(Sum a, Sum b) { return a.hi > b.hi || (a.hi == b.hi && a.lo > b.lo); }
+__device__ __forceinline__ Sum shfl_up(Sum v, int d) {
+    return Sum{__shfl_up_sync(0xffffffffu, v.hi, d), __shfl_up_sync(0xffffffffu, v.lo, d)};
+}
+__device__ __forceinline__ Sum shfl(Sum v, int l) {
+    return Sum{__shfl_sync(0xffffffffu, v.hi, l), __shfl_sync(0xffffffffu, v.lo, l)};
+}
+// Inclusive prefix sums over the lanes.
+__device__ __forceinline__ Sum scan(Sum v, int lane) {
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+        const Sum o = shfl_up(v, d);
+        if (lane >= d) v = o + v;
+    }
+    return v;
 }
 
-// Store a double at the same shared-memory offset in CTA `rank` of the cluster.
-__device__ __forceinline__ void store_remote(double* p, uint32_t rank, double v) {
-    uint32_t a;
-    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;"
-                 : "=r"(a) : "r"(static_cast<uint32_t>(__cvta_generic_to_shared(p))), "r"(rank));
-    asm volatile("st.shared::cluster.f64 [%0], %1;" ::"r"(a), "d"(v) : "memory");
+// Store a sum at the same shared-memory offset in CTA `rank` of the cluster, counted as 8 transaction
+// bytes on the barrier at `bar`'s offset there (the receiver's wait on it orders the data).
+__device__ __forceinline__ void send_sum(Sum* p, uint64_t* bar, uint32_t rank, Sum v) {
+    uint32_t a, b;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(ptx::smem_addr(p)), "r"(rank));
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(b) : "r"(ptx::smem_addr(bar)), "r"(rank));
+    asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.v2.f32 [%0], {%1, %2}, [%3];" ::"r"(a), "f"(v.hi),
+                 "f"(v.lo), "r"(b)
+                 : "memory");
 }
 
 // How the row's weights are formed from p and q.
 enum Mode { kPlain = 0, kResidual = 1, kWithout = 2 };   // w = p; w = max(p - q, 0); w = p with entry x zeroed
-
-// An entry counts when it is positive and finite.
-__device__ __forceinline__ double weight_of(float p, float q) {
-    const double w = static_cast<double>(p) - static_cast<double>(q);
-    return (w > 0.0 && w < static_cast<double>(INFINITY)) ? w : 0.0;
-}
 
 // Four consecutive entries v .. v + 3 of the row (entries past V are 0); for kWithout q = p at x.
 template <bool VEC>
@@ -85,18 +109,12 @@ __device__ __forceinline__ void load4(const float* __restrict__ p_row, const flo
     }
 }
 
-// (hi, lo) += max(p - q, 0), the difference exact (two_sum_err), the sum to about 48 bits.
-__device__ __forceinline__ void add_pair(float& hi, float& lo, float p, float q) {
+// max(p - q, 0), exact; an entry counts when it is positive and finite.
+__device__ __forceinline__ Sum weight(float p, float q) {
     const float d = __fsub_rn(p, q);
-    const float de = two_sum_err(p, -q, d);
-    if (d > 0.0f && d < INFINITY) {              // NaN and infinite entries count as 0
-        const float s = __fadd_rn(hi, d);
-        lo = __fadd_rn(lo, __fadd_rn(two_sum_err(hi, d, s), de));
-        hi = s;
-    }
+    const float e = __fsub_rn(__fsub_rn(p, d), q);   // exact for p >= q >= 0
+    return d > 0.0f && d < INFINITY ? Sum{d, e} : Sum{0.0f, 0.0f};
 }
-
-__device__ __forceinline__ double shfl_up_f64(double v, int d) { return __shfl_up_sync(0xffffffffu, v, d); }
 
 template <bool VEC>
 __global__ void __launch_bounds__(kVerifyThreads) __cluster_dims__(kVerifyCtas, 1, 1)
@@ -104,8 +122,9 @@ verify_drafts_kernel(const float* __restrict__ target, int64_t ld_t, const float
                      int V, const int32_t* __restrict__ tokens, const int32_t* __restrict__ cu_q, int T,
                      const float* __restrict__ u_accept, const float* __restrict__ u_sample,
                      int32_t* __restrict__ out_tokens, int32_t* __restrict__ accepted, int32_t* err) {
-    extern __shared__ double group_sum[];        // [groups of this CTA]: sums, then inclusive prefix sums
-    __shared__ double totals[kVerifyCtas];
+    extern __shared__ Sum group_sum[];           // [groups of this CTA]: sums, then inclusive prefix sums
+    __shared__ Sum totals[2][kVerifyCtas];        // per pass over the row: every CTA's sum
+    __shared__ uint64_t totals_full[2];
     __shared__ int s_first, s_x;
     const int b = blockIdx.x / kVerifyCtas;
     const int rank = static_cast<int>(cluster_rank());
@@ -119,7 +138,15 @@ verify_drafts_kernel(const float* __restrict__ target, int64_t ld_t, const float
         if (rank == 0 && threadIdx.x == 0) accepted[b] = 0;
         return;
     }
-    cluster_arrive();                            // every CTA runs before any writes into its shared memory
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < 2; ++i) {
+            ptx::mbar_init(&totals_full[i], 1);
+            ptx::mbar_arrive_expect_tx(&totals_full[i], kVerifyCtas * sizeof(Sum));
+        }
+        ptx::fence_barrier_init();
+    }
+    __syncthreads();
+    cluster_arrive();                            // every CTA's barriers exist before any writes into its shared memory
     // ---- acceptance: the first row whose draft is missing or rejected (every CTA finds it for itself)
     if (warp == 0) {
         int first = n_draft, x_first = -1;
@@ -137,9 +164,9 @@ verify_drafts_kernel(const float* __restrict__ target, int64_t ld_t, const float
                 if (x >= 0) {
                     const float p = __ldg(target + static_cast<int64_t>(r0 + j) * ld_t + x);
                     const float q = draft != nullptr ? __ldg(draft + static_cast<int64_t>(r0 + j) * ld_d + x) : 1.0f;
-                    // 24 x 24 bits: the product is exact
-                    stop = !(static_cast<double>(__ldg(u_accept + r0 + j)) * static_cast<double>(q) <
-                             static_cast<double>(p));
+                    // u q < p without rounding: the product and its error
+                    const float u = __ldg(u_accept + r0 + j), uq = __fmul_rn(u, q);
+                    stop = !(uq < p || (uq == p && __fmaf_rn(u, q, -uq) < 0.0f));
                 }
             }
             const uint32_t m = __ballot_sync(0xffffffffu, stop);
@@ -169,10 +196,9 @@ verify_drafts_kernel(const float* __restrict__ target, int64_t ld_t, const float
     const int g_begin = min(groups_all, rank * per_cta), g_end = min(groups_all, g_begin + per_cta);
     const int ng = g_end - g_begin;
     int mode = x < 0 ? kPlain : (q_row != nullptr ? kResidual : kWithout);
-    double base = 0.0, all = 0.0;
-    bool peers_run = false;
-    int owner = -1;
-    const double u = static_cast<double>(__ldg(u_sample + b));
+    int pass = 0;
+    bool late = false, mass = false;
+    const uint64_t deadline = ptx::wait_deadline();
     for (;;) {
         for (int g = warp; g < ng; g += kVerifyWarps) {
             float hi = 0.0f, lo = 0.0f;
@@ -183,106 +209,110 @@ verify_drafts_kernel(const float* __restrict__ target, int64_t ld_t, const float
 #pragma unroll
             for (int s = 0; s < 4; ++s)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) add_pair(hi, lo, p[s][e], q[s][e]);
-            double sum = static_cast<double>(hi) + static_cast<double>(lo);
+                for (int e = 0; e < 4; ++e) {
+                    const Sum w = weight(p[s][e], q[s][e]);
+                    const float t = __fadd_rn(hi, w.hi);
+                    lo = __fadd_rn(lo, __fadd_rn(two_sum_err(hi, w.hi, t), w.lo));
+                    hi = t;
+                }
+            Sum sum = normal(hi, lo);
 #pragma unroll
-            for (int m = 16; m > 0; m >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, m);
+            for (int m = 16; m > 0; m >>= 1)
+                sum = sum + Sum{__shfl_xor_sync(0xffffffffu, sum.hi, m), __shfl_xor_sync(0xffffffffu, sum.lo, m)};
             if (lane == 0) group_sum[g] = sum;
         }
         __syncthreads();
-        if (!peers_run) {
-            __syncwarp();
-            cluster_wait();
-            peers_run = true;
-        }
+        if (pass == 0) cluster_wait();
         if (warp == 0) {                         // inclusive prefix sums of this CTA's groups
-            double carry = 0.0;
+            Sum carry{0.0f, 0.0f};
             for (int g0 = 0; g0 < ng; g0 += 32) {
-                double v = g0 + lane < ng ? group_sum[g0 + lane] : 0.0;
-#pragma unroll
-                for (int d = 1; d < 32; d <<= 1) {
-                    const double o = shfl_up_f64(v, d);
-                    if (lane >= d) v += o;
-                }
-                v += carry;
+                const Sum v = carry + scan(g0 + lane < ng ? group_sum[g0 + lane] : Sum{0.0f, 0.0f}, lane);
                 if (g0 + lane < ng) group_sum[g0 + lane] = v;
-                carry = __shfl_sync(0xffffffffu, v, 31);
+                carry = shfl(v, 31);
             }
-            if (lane < kVerifyCtas) store_remote(&totals[rank], lane, carry);
+            if (lane < kVerifyCtas) send_sum(&totals[pass][rank], &totals_full[pass], lane, carry);
         }
-        cluster_sync();
-        // the same sums in the same order in every CTA: base of this CTA, total, owner of the border
-        all = 0.0;
-        for (int c = 0; c < kVerifyCtas; ++c) {
-            if (c == rank) base = all;
-            all += totals[c];
+        if (!ptx::mbar_wait(&totals_full[pass], 0, deadline)) late = true;
+        if (__syncthreads_or(late)) {            // all leave together
+            if (threadIdx.x == 0) raise_error(err, DSA_DEVERR_TIMEOUT);
+            cluster_arrive();                    // not before every CTA that may still send has left or come here
+            cluster_wait();
+            return;
         }
-        const double t = u * all;
-        double run = 0.0;
-        owner = -1;
-        int last = -1;
-        for (int c = 0; c < kVerifyCtas; ++c) {
-            run += totals[c];
-            if (totals[c] > 0.0) last = c;
-            if (owner < 0 && totals[c] > 0.0 && run > t) owner = c;
-        }
-        if (owner < 0) owner = last;             // u outside [0, 1): the last entry with mass
-        cluster_sync();                          // totals read by every CTA before they may be written again
-        if (all > 0.0 || mode == kPlain) break;
-        mode = kPlain;                           // p <= q everywhere: draw from p itself
+        for (int c = 0; c < kVerifyCtas; ++c) mass |= totals[pass][c].hi > 0.0f;
+        if (mass || mode == kPlain) break;
+        mode = kPlain;                           // p <= q everywhere: draw from p itself, in a second pass
+        ++pass;
     }
+    if (warp != 0) return;
+    // the same sums in the same order in every CTA: base of this CTA, total, owner of the border
+    Sum base{0.0f, 0.0f}, all{0.0f, 0.0f};
+    for (int c = 0; c < kVerifyCtas; ++c) {
+        if (c == rank) base = all;
+        all = all + totals[pass][c];
+    }
+    const float u = __ldg(u_sample + b);
+    const float ua = __fmul_rn(u, all.hi);
+    const Sum t = normal(ua, __fmaf_rn(u, all.lo, __fmaf_rn(u, all.hi, -ua)));
+    int owner = -1, last = -1;
+    Sum run{0.0f, 0.0f};
+    for (int c = 0; c < kVerifyCtas; ++c) {
+        const Sum tc = totals[pass][c];
+        run = run + tc;
+        if (tc.hi > 0.0f) {
+            last = c;
+            if (owner < 0 && run > t) owner = c;
+        }
+    }
+    if (owner < 0) owner = last;                 // u outside [0, 1): the last entry with mass
     if (owner < 0) {                             // a row without mass
-        if (rank == 0 && threadIdx.x == 0) {
+        if (rank == 0 && lane == 0) {
             out_tokens[r0 + first] = -1;
             raise_error(err, DSA_DEVERR_PROB);
         }
         return;
     }
-    if (rank != owner || warp != 0) return;
-    const double t = u * all;
+    if (rank != owner) return;
     // the first group whose prefix passes t (the last with mass if none does)
     int g_hit = -1, g_last = -1;
     for (int g0 = 0; g0 < ng; g0 += 32) {
         const int g = g0 + lane;
-        const double inc = g < ng ? group_sum[g] : 0.0;
-        const double exc = (g < ng && g > 0) ? group_sum[g - 1] : 0.0;
-        const bool mass = g < ng && inc > exc;
-        const uint32_t hit = __ballot_sync(0xffffffffu, mass && base + inc > t);
-        const uint32_t any = __ballot_sync(0xffffffffu, mass);
+        const Sum inc = g < ng ? group_sum[g] : Sum{0.0f, 0.0f};
+        const Sum exc = (g < ng && g > 0) ? group_sum[g - 1] : Sum{0.0f, 0.0f};
+        const bool some = g < ng && inc > exc;
+        const uint32_t hit = __ballot_sync(0xffffffffu, some && base + inc > t);
+        const uint32_t any = __ballot_sync(0xffffffffu, some);
         if (any != 0u) g_last = g0 + 31 - __clz(any);
         if (hit != 0u) {
             g_hit = g0 + __ffs(hit) - 1;
             break;
         }
     }
-    if (g_hit < 0) g_hit = g_last;
-    if (g_hit < 0) g_hit = 0;                    // unreachable: the owner has mass
-    double run = base + (g_hit > 0 ? group_sum[g_hit - 1] : 0.0);
+    if (g_hit < 0) g_hit = max(g_last, 0);
+    run = g_hit > 0 ? base + group_sum[g_hit - 1] : base;
     const int v0 = (g_begin + g_hit) * kGroup + lane * 4;
     float p[4][4], q[4][4];
 #pragma unroll
     for (int s = 0; s < 4; ++s) load4<VEC>(p_row, q_row, mode, x, v0 + s * 128, V, p[s], q[s]);
     int token = -1, last_pos = -1;
+    Sum inc[4];                                  // inclusive prefix over lanes of the lanes' sums, step by step
 #pragma unroll
     for (int s = 0; s < 4; ++s) {
-        double w[4], pre = 0.0;
+        Sum own{0.0f, 0.0f};
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            w[e] = weight_of(p[s][e], q[s][e]);
-            pre += w[e];
-        }
-        double inc = pre;
+        for (int e = 0; e < 4; ++e) own = own + weight(p[s][e], q[s][e]);
+        inc[s] = scan(own, lane);
+    }
 #pragma unroll
-        for (int d = 1; d < 32; d <<= 1) {
-            const double o = shfl_up_f64(inc, d);
-            if (lane >= d) inc += o;
-        }
-        double at = run + (inc - pre);
+    for (int s = 0; s < 4; ++s) {
+        const Sum before = shfl_up(inc[s], 1);
+        Sum at = lane > 0 ? run + before : run;
         int found = -1, pos = -1;
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-            at += w[e];
-            if (w[e] > 0.0) {
+            const Sum w = weight(p[s][e], q[s][e]);
+            at = at + w;
+            if (w.hi > 0.0f) {
                 pos = v0 + s * 128 + e;
                 if (found < 0 && at > t) found = pos;
             }
@@ -291,7 +321,7 @@ verify_drafts_kernel(const float* __restrict__ target, int64_t ld_t, const float
         const uint32_t any = __ballot_sync(0xffffffffu, pos >= 0);
         if (any != 0u) last_pos = __shfl_sync(0xffffffffu, pos, 31 - __clz(any));
         if (hit != 0u && token < 0) token = __shfl_sync(0xffffffffu, found, __ffs(hit) - 1);
-        run += __shfl_sync(0xffffffffu, inc, 31);
+        run = run + shfl(inc[s], 31);
     }
     if (token < 0) token = last_pos;             // the border lies within the rounding of the group's sum
     if (lane == 0) out_tokens[r0 + first] = token;
@@ -314,7 +344,7 @@ extern "C" dsa_status dsa_verify_drafts(const float* target_probs, int64_t targe
     const bool vec = aligned16(target_probs) && target_ld % 4 == 0 &&
                      (draft_probs == nullptr || (aligned16(draft_probs) && draft_ld % 4 == 0));
     const int groups = (V + kGroup - 1) / kGroup;
-    const size_t smem = static_cast<size_t>((groups + kVerifyCtas - 1) / kVerifyCtas) * sizeof(double);   // <= 32 KB
+    const size_t smem = static_cast<size_t>((groups + kVerifyCtas - 1) / kVerifyCtas) * sizeof(Sum);   // <= 32 KB
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     const unsigned grid = static_cast<unsigned>(B) * kVerifyCtas;
     if (vec)

@@ -669,14 +669,14 @@ dsa_status dsa_dense_mla_decode(const void* q_bf16, const void* kv_pool, int64_t
  *   otherwise: the least v with w_0 + .. + w_v > sample_u[b] * sum w.
  *   out_tokens[cu_q[b] ..]: the accepted drafts, then the drawn token, then -1 up to the request's
  *   rows.  accepted[b]: the number of accepted drafts (r* - cu_q[b]).  A request without rows: 0.
- *   The differences are exact and the sums carry at least 48 bits.  Entries that are not positive
- *   and finite count as 0 in w.
+ *   The differences are exact and the sums carry about 48 bits (they must stay within fp32's range).
+ *   Entries that are not positive and finite count as 0 in w; probabilities are not negative.
  * Arguments:
  *   target_probs  fp32 rows of V entries, stride target_ld >= V.   draft_probs: nullable, likewise.
  *   V             1 .. 2^24.   draft_tokens int32 [T].   cu_q int32 [B + 1].
  *   accept_u      fp32 [T], sample_u fp32 [B]: uniform numbers in [0, 1).
- *   out_tokens    int32 [T].   accepted int32 [B].  Rows >= cu_q[B] of out_tokens are left as they
- *                 were.
+ *   out_tokens    int32 [T], not draft_tokens.   accepted int32 [B].  Rows >= cu_q[B] of out_tokens
+ *                 are left as they were.
  *   dev_err       nullable; DSA_DEVERR_INDEX_RANGE for a draft token >= V (no draft) or a cu_q range
  *                 outside [0, T] (cut to it), DSA_DEVERR_PROB for a row to draw from without mass
  *                 (the drawn token is -1).
