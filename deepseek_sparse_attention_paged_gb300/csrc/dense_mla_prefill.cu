@@ -17,13 +17,17 @@
 // one head and one request: while the softmax warps of one work, the tensor cores run the other's
 // products.
 //
-// CTA: block qb of 256 query rows of request b, head h.  Roles (384 threads):
+// Work item: block qb of 256 query rows of request b, head h.  The grid has one block per item; a CTA
+// takes over the items of blocks that have not started (cluster launch control) until none is left, so
+// that an item's first copies and products run while the one before is still writing its output.
+// Roles (384 threads):
 //   warps 0-3, 4-7  softmax of query tile 0 / 1: one thread per query (TMEM lane), 128 scores in
 //                   registers, P written back over the scores as bf16; O / l at the end;
 //   warp 8          TMA: the query tiles, then K (two 64-dim slabs of k_nope, one of k_pe) and V
 //                   (two slabs) of each 128-key tile through a ring of eight 16 KB slabs;
 //   warp 9          MMA: S = Q K^T with both operands in shared memory, O += P V with P in tensor
-//                   memory, alternating between the query tiles.
+//                   memory, alternating between the query tiles;
+//   warp 10         the work items: claims the next one, finds its request and rows (warp 11 idle).
 // Tensor memory (512 columns): S / P of tile 0, of tile 1, O of tile 0, of tile 1 (128 each).
 // Shared memory: queries 96 KB, ring 128 KB.
 #include <cuda_bf16.h>
@@ -41,27 +45,64 @@ constexpr int kTileQ = 128, kTileK = 128, kBlockQ = 2 * kTileQ;
 constexpr int kSlabBytes = 128 * 128;                     // 128 rows x 64 bf16, 128-byte swizzle
 constexpr int kRing = 8;
 constexpr int kQSlabs = 3, kKSlabs = 3, kVSlabs = 2;
-constexpr int kTmaWarp = 8, kMmaWarp = 9;
-constexpr int kPreThreads = 384;                          // three warpgroups; warps 10 and 11 only fill the third
-constexpr int kSoftmaxRegs = 192, kOtherRegs = 112;       // 2 x 128 x 192 + 128 x 112 <= 384 x 168 at launch
+constexpr int kTmaWarp = 8, kMmaWarp = 9, kWorkWarp = 10;
+constexpr int kPreThreads = 384;                          // three warpgroups; warp 11 only fills the third
+constexpr int kSoftmaxRegs = 208, kOtherRegs = 88;        // 2 x 128 x 208 + 128 x 88 <= 384 x 168 at launch
 constexpr uint32_t kColS = 0, kColO = 256;                // + 128 * tile
 constexpr size_t kPreSmem = 1024 + size_t(2 * kQSlabs + kRing) * kSlabBytes + 512;
 static_assert(kPreSmem <= 232448, "shared-memory budget");
 
+struct Work {
+    int b;                   // request; -1: no more work
+    int h, qb, q0, nq;       // head, query block, first query row and queries of the request
+    int k0, nk;              // first key row and keys of the request
+    int pad;
+};
+
 struct PreBars {
-    uint64_t q_full[2];
+    uint64_t q_full[2], q_empty[2];      // queries of the tile in place / read by the item's last S, per item
     uint64_t full[kRing], empty[kRing];
     uint64_t s_full[2];      // scores of the tile's next step complete (and with them its previous P V)
     uint64_t p_full[2];      // P written (4 softmax warps)
-    uint64_t o_full[2];      // last P V complete
+    uint64_t o_full[2];      // the item's last P V complete
+    uint64_t o_free[2];      // O read out (4 softmax warps), per item
+    uint64_t work_full[2], work_empty[2];   // a work item published / done with (TMA, MMA and 8 softmax warps)
+    uint64_t claim_full;     // answer to the claim of another block
+    alignas(16) uint32_t claim[4];
+    Work work[2];
     uint32_t tmem_slot;
-    int item[4];             // request, query block, first query row, queries of the request
 };
 static_assert(sizeof(PreBars) <= 512, "barrier block");
 
-// The CTA's work: block x in the order of requests, the last (longest) query block of each first.
-__device__ __forceinline__ void find_item(const int32_t* __restrict__ cu_q, int B, int T, int x, int lane, int* item,
-                                          int32_t* err) {
+// Asks for the item of a block that has not started; the 16-byte answer is counted on `bar`.
+__device__ __forceinline__ void claim_block(uint32_t* answer, uint64_t* bar) {
+    asm volatile("clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::"r"(
+                     ptx::smem_addr(answer)),
+                 "r"(ptx::smem_addr(bar))
+                 : "memory");
+}
+// Whether a block was claimed, and which.
+__device__ __forceinline__ bool claimed_block(const uint32_t* answer, int& x, int& y) {
+    uint32_t ok, bx, by;
+    asm volatile(
+        "{\n\t.reg .b128 r;\n\t.reg .pred p;\n\t"
+        "ld.shared.b128 r, [%3];\n\t"
+        "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, r;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t"
+        "mov.u32 %1, 0;\n\tmov.u32 %2, 0;\n\t"
+        "@p clusterlaunchcontrol.query_cancel.get_first_ctaid::x.b32.b128 %1, r;\n\t"
+        "@p clusterlaunchcontrol.query_cancel.get_first_ctaid::y.b32.b128 %2, r;\n\t}"
+        : "=r"(ok), "=r"(bx), "=r"(by)
+        : "r"(ptx::smem_addr(answer))
+        : "memory");
+    x = static_cast<int>(bx);
+    y = static_cast<int>(by);
+    return ok != 0;
+}
+
+// Block x in the order of requests, the last (longest) query block of each first; false: past the last.
+__device__ __forceinline__ bool find_item(const int32_t* __restrict__ cu_q, const int32_t* __restrict__ cu_k, int B, int T,
+                                          int S, int x, int h, int lane, Work* item, int32_t* err) {
     int carry = 0;
     bool found = false;
     for (int b0 = 0; b0 < B; b0 += 32) {
@@ -84,16 +125,33 @@ __device__ __forceinline__ void find_item(const int32_t* __restrict__ cu_q, int 
         if (!found && hit != 0u) {
             found = true;
             if (lane == __ffs(hit) - 1) {
-                item[0] = b;
-                item[1] = nb - 1 - (x - (carry + inc - nb));
-                item[2] = q0;
-                item[3] = nq;
+                const int lo = __ldg(cu_k + b), hi = __ldg(cu_k + b + 1);
+                const int k0 = max(0, min(S, lo));
+                if (lo < 0 || hi > S) raise_error(err, DSA_DEVERR_INDEX_RANGE);
+                *item = Work{b, h, nb - 1 - (x - (carry + inc - nb)), q0, nq, k0, max(0, min(S, hi) - k0), 0};
             }
-            if (x != 0) return;                                // block 0 goes on to check every range
+            if (x != 0) break;                                 // block 0 goes on to check every range
         }
         carry += __shfl_sync(0xffffffffu, inc, 31);
     }
+    __syncwarp();
+    return found;
 }
+
+// Key tiles that the rows of the item's two query tiles see.  Query i sees keys [0, nk - nq + i] (causal).
+struct Tiles {
+    int n[2], most;
+    __device__ Tiles(const Work& w, int causal) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int first = w.qb * kBlockQ + i * kTileQ;
+            const int last = min(w.nq, first + kTileQ) - 1;
+            const int seen = last < first ? 0 : (causal ? max(0, min(w.nk, w.nk - w.nq + last + 1)) : w.nk);
+            n[i] = (seen + kTileK - 1) / kTileK;
+        }
+        most = max(n[0], n[1]);
+    }
+};
 
 __global__ void __launch_bounds__(kPreThreads, 1)
 dense_mla_prefill_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kmap,
@@ -109,95 +167,144 @@ dense_mla_prefill_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_
     PreBars& bar = *reinterpret_cast<PreBars*>(ring + kRing * kSlabBytes);
 
     const int warp = uniform(static_cast<int>(threadIdx.x >> 5)), lane = threadIdx.x & 31;
-    const int h = blockIdx.y;
-    if (warp == 0) {
-        if (lane == 0) bar.item[0] = -1;
-        __syncwarp();
-        find_item(cu_q, B, T, static_cast<int>(blockIdx.x), lane, bar.item, err);
-    } else if (warp == kTmaWarp && lane == 0) {
+    if (warp == kTmaWarp && lane == 0) {
         for (int i = 0; i < 2; ++i) {
             ptx::mbar_init(&bar.q_full[i], 1);
+            ptx::mbar_init(&bar.q_empty[i], 1);
             ptx::mbar_init(&bar.s_full[i], 1);
             ptx::mbar_init(&bar.p_full[i], 4);
             ptx::mbar_init(&bar.o_full[i], 1);
+            ptx::mbar_init(&bar.o_free[i], 4);
+            ptx::mbar_init(&bar.work_full[i], 1);
+            ptx::mbar_init(&bar.work_empty[i], 10);
         }
+        ptx::mbar_init(&bar.claim_full, 1);
         for (int s = 0; s < kRing; ++s) {
             ptx::mbar_init(&bar.full[s], 1);
             ptx::mbar_init(&bar.empty[s], 1);
         }
         ptx::fence_barrier_init();
     }
-    __syncthreads();
-    const int b = uniform(bar.item[0]);
-    if (b < 0) return;                                         // past the last block (uniform)
     if (warp == kMmaWarp) {
         ptx::tmem_alloc(&bar.tmem_slot, 512);
         ptx::tmem_relinquish();
     }
-    const int qb = uniform(bar.item[1]), q0 = uniform(bar.item[2]), nq = uniform(bar.item[3]);
-    const int k_lo = uniform(__ldg(cu_k + b)), k_hi = uniform(__ldg(cu_k + b + 1));
-    const int k0 = max(0, min(S, k_lo));
-    const int nk = max(0, min(S, k_hi) - k0);
-    if (threadIdx.x == 0 && (k_lo < 0 || k_hi > S)) raise_error(err, DSA_DEVERR_INDEX_RANGE);
-    const int off = causal ? nk - nq : 0;                      // query i sees keys [0, off + i] (causal)
-    // key tiles that tile i's rows see
-    int n_tiles[2];
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        const int first = qb * kBlockQ + i * kTileQ;
-        const int last = min(nq, first + kTileQ) - 1;
-        const int seen = last < first ? 0 : (causal ? max(0, min(nk, off + last + 1)) : nk);
-        n_tiles[i] = (seen + kTileK - 1) / kTileK;
-    }
-    const int n = max(n_tiles[0], n_tiles[1]);
     ptx::tc_fence_before_sync();
     __syncthreads();
     ptx::tc_fence_after_sync();
     const uint32_t tmem = uniform(bar.tmem_slot);
     const uint64_t deadline = ptx::wait_deadline();
     bool timed_out = false;
+    // Work item k has been published, or there is no more (whole warp).  `done` gives its slot back; the
+    // softmax warps do so at the item's end, which holds the claims one item ahead.
+    uint32_t k = 0;
+    auto have_work = [&]() -> bool {
+        if (!ptx::mbar_wait(&bar.work_full[k & 1u], (k >> 1) & 1u, deadline)) timed_out = true;
+        timed_out = __any_sync(0xffffffffu, timed_out);
+        return !timed_out && uniform(bar.work[k & 1u].b) >= 0;
+    };
+    auto copy_work = [&]() -> Work {
+        const Work& x = bar.work[k & 1u];
+        return Work{0, uniform(x.h), uniform(x.qb), uniform(x.q0), uniform(x.nq), uniform(x.k0), uniform(x.nk), 0};
+    };
+    auto done = [&]() {
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(&bar.work_empty[k & 1u]);
+        ++k;
+    };
 
     if (warp >= kTmaWarp) {
         set_regs_dec<kOtherRegs>();
-        if (warp == kTmaWarp) {
-            // ---------------------------------------------------------------- TMA
-            if (lane == 0 && n > 0) {
-                uint32_t c = 0;                                    // slabs issued
-                auto next = [&]() -> unsigned char* {              // the ring's next slab, once it is free
-                    const int s = static_cast<int>(c % kRing);
-                    if (!ptx::mbar_wait(&bar.empty[s], ((c / kRing) & 1u) ^ 1u, deadline)) timed_out = true;
-                    if (timed_out) return nullptr;
-                    ptx::mbar_arrive_expect_tx(&bar.full[s], kSlabBytes);
-                    ++c;
-                    return ring + s * kSlabBytes;
-                };
-                auto bar_of_last = [&]() { return &bar.full[(c - 1) % kRing]; };
-                auto load_q = [&](int i) {
-                    if (n_tiles[i] == 0) return;
-                    ptx::mbar_arrive_expect_tx(&bar.q_full[i], kQSlabs * kSlabBytes);
-                    for (int j = 0; j < kQSlabs; ++j)
-                        ptx::tma_load_3d(qs + (i * kQSlabs + j) * kSlabBytes, &qmap, &bar.q_full[i], 64 * j, h,
-                                         q0 + qb * kBlockQ + i * kTileQ);
-                };
-                auto load_k = [&](int t) {
-                    for (int j = 0; j < kKSlabs && !timed_out; ++j)
-                        if (unsigned char* dst = next()) {
-                            if (j < 2) ptx::tma_load_3d(dst, &kmap, bar_of_last(), 64 * j, h, k0 + t * kTileK);
-                            else ptx::tma_load_3d(dst, &pmap, bar_of_last(), 0, 0, k0 + t * kTileK);
+        if (warp == kWorkWarp) {
+            // ---------------------------------------------------------------- work items
+            int x = static_cast<int>(blockIdx.x), y = static_cast<int>(blockIdx.y);
+            uint32_t claim_phase = 0;
+            for (uint32_t j = 0;;) {
+                // the slot's previous item is done with by every warp
+                if (j >= 2 && !ptx::mbar_wait(&bar.work_empty[j & 1u], ((j >> 1) & 1u) ^ 1u, deadline)) timed_out = true;
+                timed_out = __any_sync(0xffffffffu, timed_out);
+                if (timed_out) break;
+                // the first item is the CTA's own block; every other one is claimed
+                bool found = false;
+                for (bool claim = j > 0;; claim = true) {
+                    if (claim) {
+                        if (lane == 0) {
+                            ptx::fence_proxy_async_smem();           // the answer before has been read
+                            ptx::mbar_arrive_expect_tx(&bar.claim_full, 16);
+                            claim_block(bar.claim, &bar.claim_full);
                         }
-                };
-                load_q(0);
-                load_k(0);
-                load_q(1);
-                for (int t = 0; t < n && !timed_out; ++t) {
-                    for (int j = 0; j < kVSlabs && !timed_out; ++j)
-                        if (unsigned char* dst = next())
-                            ptx::tma_load_3d(dst, &vmap, bar_of_last(), 64 * j, h, k0 + t * kTileK);
-                    if (t + 1 < n) load_k(t + 1);
+                        if (!ptx::mbar_wait(&bar.claim_full, claim_phase & 1u, deadline)) timed_out = true;
+                        ++claim_phase;
+                        timed_out = __any_sync(0xffffffffu, timed_out);
+                        if (timed_out) break;
+                        const bool more = claimed_block(bar.claim, x, y);
+                        __syncwarp();
+                        if (!more) break;
+                    }
+                    found = find_item(cu_q, cu_k, B, T, S, x, y, lane, &bar.work[j & 1u], err);
+                    if (found) break;
                 }
-                // copies still in flight land before the CTA may leave (bounded)
+                if (timed_out) break;
+                if (!found && lane == 0) bar.work[j & 1u].b = -1;
+                __syncwarp();
+                if (lane == 0) ptx::mbar_arrive(&bar.work_full[j & 1u]);
+                ++j;
+                if (!found) break;
+            }
+        } else if (warp == kTmaWarp) {
+            // ---------------------------------------------------------------- TMA
+            uint32_t c = 0, qn[2] = {0, 0};                        // slabs issued; items that used the query tile
+            while (have_work()) {
+                const Work w = copy_work();
+                const Tiles n(w, causal);
+                if (lane == 0 && n.most > 0) {
+                    auto next = [&]() -> unsigned char* {          // the ring's next slab, once it is free
+                        const int s = static_cast<int>(c % kRing);
+                        if (!ptx::mbar_wait(&bar.empty[s], ((c / kRing) & 1u) ^ 1u, deadline)) timed_out = true;
+                        if (timed_out) return nullptr;
+                        ptx::mbar_arrive_expect_tx(&bar.full[s], kSlabBytes);
+                        ++c;
+                        return ring + s * kSlabBytes;
+                    };
+                    auto bar_of_last = [&]() { return &bar.full[(c - 1) % kRing]; };
+                    auto load_q = [&](int i) {
+                        if (n.n[i] == 0 || timed_out) return;
+                        if (qn[i] > 0 && !ptx::mbar_wait(&bar.q_empty[i], (qn[i] - 1) & 1u, deadline)) {
+                            timed_out = true;
+                            return;
+                        }
+                        ++qn[i];
+                        ptx::mbar_arrive_expect_tx(&bar.q_full[i], kQSlabs * kSlabBytes);
+                        for (int j = 0; j < kQSlabs; ++j)
+                            ptx::tma_load_3d(qs + (i * kQSlabs + j) * kSlabBytes, &qmap, &bar.q_full[i], 64 * j, w.h,
+                                             w.q0 + w.qb * kBlockQ + i * kTileQ);
+                    };
+                    auto load_k = [&](int t) {
+                        for (int j = 0; j < kKSlabs && !timed_out; ++j)
+                            if (unsigned char* dst = next()) {
+                                if (j < 2) ptx::tma_load_3d(dst, &kmap, bar_of_last(), 64 * j, w.h, w.k0 + t * kTileK);
+                                else ptx::tma_load_3d(dst, &pmap, bar_of_last(), 0, 0, w.k0 + t * kTileK);
+                            }
+                    };
+                    load_q(0);
+                    load_k(0);
+                    load_q(1);
+                    for (int t = 0; t < n.most && !timed_out; ++t) {
+                        for (int j = 0; j < kVSlabs && !timed_out; ++j)
+                            if (unsigned char* dst = next())
+                                ptx::tma_load_3d(dst, &vmap, bar_of_last(), 64 * j, w.h, w.k0 + t * kTileK);
+                        if (t + 1 < n.most) load_k(t + 1);
+                    }
+                }
+                timed_out = __any_sync(0xffffffffu, timed_out);
+                if (timed_out) break;
+                done();
+            }
+            // copies still in flight land before the CTA may leave (bounded)
+            if (lane == 0) {
                 for (int i = 0; i < 2; ++i)
-                    if (n_tiles[i] > 0 && !ptx::mbar_wait(&bar.q_full[i], 0, ptx::wait_deadline(20000000ull))) timed_out = true;
+                    if (qn[i] > 0 && !ptx::mbar_wait(&bar.q_full[i], (qn[i] - 1) & 1u, ptx::wait_deadline(20000000ull)))
+                        timed_out = true;
                 for (uint32_t j = c > kRing ? c - kRing : 0; j < c; ++j)
                     if (!ptx::mbar_wait(&bar.full[j % kRing], (j / kRing) & 1u, ptx::wait_deadline(20000000ull)))
                         timed_out = true;
@@ -223,8 +330,9 @@ dense_mla_prefill_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_
             const uint64_t q_desc = desc_sw128(q_addr, 16, 1024);
             const uint64_t k_desc = desc_sw128(ring_addr, 16, 1024), v_desc = desc_sw128(ring_addr, kSlabBytes, 1024);
             auto slab = [&](uint32_t cc) { return (cc % kRing) * (kSlabBytes / 16); };
-            // S_i = Q_i K^T from the slabs at c0; the first user of a key tile waits for each slab in turn
-            auto issue_s = [&](int i, uint32_t c0, bool first) {
+            // S_i = Q_i K^T from the slabs at c0; the first user of a key tile waits for each slab in turn;
+            // the item's last one gives the queries back
+            auto issue_s = [&](int i, uint32_t c0, bool first, bool last) {
                 const uint64_t a = q_desc + i * (kQSlabs * kSlabBytes / 16);
 #pragma unroll
                 for (int j = 0; j < kKSlabs; ++j) {
@@ -239,7 +347,10 @@ dense_mla_prefill_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_
                         for (int kk = 0; kk < 4; ++kk)
                             ptx::umma_f16(tmem + kColS + 128 * i, a + (j * (kSlabBytes / 16) + kk * 2), bk + kk * 2,
                                           idesc_qk, (j | kk) != 0 ? 1u : 0u);
-                        if (j == kKSlabs - 1) ptx::umma_commit(&bar.s_full[i]);
+                        if (j == kKSlabs - 1) {
+                            ptx::umma_commit(&bar.s_full[i]);
+                            if (last) ptx::umma_commit(&bar.q_empty[i]);
+                        }
                     }
                 }
             };
@@ -261,57 +372,72 @@ dense_mla_prefill_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_
                     }
                 }
             };
-            if (n > 0) {
-                bool first = true;
-                for (int i = 0; i < 2; ++i) {
-                    if (n_tiles[i] == 0) continue;
-                    wait(&bar.q_full[i], 0);
-                    issue_s(i, 0, first);
-                    first = false;
+            uint32_t c0 = 0, qn[2] = {0, 0}, sn[2] = {0, 0};   // slabs and, per tile, items and steps before this item
+            while (have_work()) {
+                const Work w = copy_work();
+                const Tiles n(w, causal);
+                done();
+                if (n.most > 0) {
+                    bool first = true;
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        if (n.n[i] == 0) continue;
+                        wait(&bar.q_full[i], qn[i] & 1u);
+                        issue_s(i, c0, first, n.n[i] == 1);
+                        first = false;
+                    }
+                    release(c0, kKSlabs);
                 }
-                release(0, kKSlabs);
-            }
-            for (int t = 0; t < n; ++t) {
-                // ring order: K(0), V(0), K(1), V(1), ...; this step uses V(t) and K(t + 1)
-                const uint32_t c_v = static_cast<uint32_t>(t) * (kKSlabs + kVSlabs) + kKSlabs, c_k = c_v + kVSlabs;
-                const int last = t < n_tiles[1] ? 1 : 0;       // the last tile that uses V(t)
-                bool first_v = true, first_k = true;
+                for (int t = 0; t < n.most; ++t) {
+                    // ring order: K(0), V(0), K(1), V(1), ...; this step uses V(t) and K(t + 1)
+                    const uint32_t c_v = c0 + static_cast<uint32_t>(t) * (kKSlabs + kVSlabs) + kKSlabs, c_k = c_v + kVSlabs;
+                    const int last = t < n.n[1] ? 1 : 0;       // the last tile that uses V(t)
+                    bool first_v = true, first_k = true;
 #pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    if (t >= n_tiles[i]) continue;
-                    if (first_v) {
-                        first_v = false;
-                        wait_slab(c_v);
-                        wait_slab(c_v + 1);
-                        const int valid = nk - t * kTileK;
-                        if (valid < kTileK) {
-                            // rows past the request's last key are another request's, or anything: their
-                            // P is 0, but 0 times NaN or infinity is not
-                            __syncwarp();
-                            for (int e = lane; e < (kTileK - valid) * 8; e += 32) {
-                                const int row = valid + (e >> 3);
+                    for (int i = 0; i < 2; ++i) {
+                        if (t >= n.n[i]) continue;
+                        if (first_v) {
+                            first_v = false;
+                            wait_slab(c_v);
+                            wait_slab(c_v + 1);
+                            const int valid = w.nk - t * kTileK;
+                            if (valid < kTileK) {
+                                // rows past the request's last key are another request's, or anything: their
+                                // P is 0, but 0 times NaN or infinity is not
+                                __syncwarp();
+                                for (int e = lane; e < (kTileK - valid) * 8; e += 32) {
+                                    const int row = valid + (e >> 3);
 #pragma unroll
-                                for (int j = 0; j < kVSlabs; ++j)
-                                    *reinterpret_cast<uint4*>(ring + ((c_v + j) % kRing) * kSlabBytes + row * 128 +
-                                                              (e & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
+                                    for (int j = 0; j < kVSlabs; ++j)
+                                        *reinterpret_cast<uint4*>(ring + ((c_v + j) % kRing) * kSlabBytes + row * 128 +
+                                                                  (e & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
+                                }
+                                ptx::fence_proxy_async_smem();
                             }
-                            ptx::fence_proxy_async_smem();
+                        }
+                        if (t == 0 && qn[i] > 0) wait(&bar.o_free[i], (qn[i] - 1) & 1u);
+                        wait(&bar.p_full[i], (sn[i] + t) & 1u);
+                        __syncwarp();
+                        ptx::tc_fence_after_sync();
+                        issue_pv(i, c_v, t != 0 ? 1u : 0u);
+                        if (i == last) release(c_v, kVSlabs);
+                        if (t + 1 < n.n[i]) {
+                            issue_s(i, c_k, first_k, t + 2 == n.n[i]);
+                            first_k = false;
+                        } else if (elect_one()) {
+                            ptx::umma_commit(&bar.o_full[i]);
                         }
                     }
-                    wait(&bar.p_full[i], t & 1);
-                    __syncwarp();
-                    ptx::tc_fence_after_sync();
-                    issue_pv(i, c_v, t != 0 ? 1u : 0u);
-                    if (i == last) release(c_v, kVSlabs);
-                    if (t + 1 < n_tiles[i]) {
-                        issue_s(i, c_k, first_k);
-                        first_k = false;
-                    } else if (elect_one()) {
-                        ptx::umma_commit(&bar.o_full[i]);
-                    }
+                    if (t + 1 < n.most) release(c_k, kKSlabs);
+                    if (__any_sync(0xffffffffu, late)) break;
                 }
-                if (t + 1 < n) release(c_k, kKSlabs);
                 if (__any_sync(0xffffffffu, late)) break;
+                c0 += static_cast<uint32_t>(n.most) * (kKSlabs + kVSlabs);
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    qn[i] += n.n[i] > 0 ? 1u : 0u;
+                    sn[i] += static_cast<uint32_t>(n.n[i]);
+                }
             }
             if (late) timed_out = true;
         }
@@ -320,121 +446,153 @@ dense_mla_prefill_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_
         // ---------------------------------------------------------------- softmax, epilogue
         const int i = warp >> 2;                               // query tile
         const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;
-        const int row = qb * kBlockQ + i * kTileQ + (warp & 3) * 32 + lane;   // query of the request
         const uint32_t s_addr = tmem + lane_base + kColS + 128 * i;
         const uint32_t o_addr = tmem + lane_base + kColO + 128 * i;
         const float cs = scale * kLog2e;
         const uint64_t cs2 = f32x2(cs, cs);
-        const int vis = row < nq ? (causal ? max(0, min(nk, off + row + 1)) : nk) : 0;
-        // keys that every row of the warp's tile sees: tiles below it need no mask
-        const int row0 = qb * kBlockQ + i * kTileQ;
-        const int all_see = causal ? min(nk, off + row0 + 1) : nk;
-        float m_run = -INFINITY, l_run = 0.0f;
-        for (int t = 0; t < n_tiles[i]; ++t) {
-            if (!ptx::mbar_wait(&bar.s_full[i], t & 1, deadline)) timed_out = true;
-            timed_out = __any_sync(0xffffffffu, timed_out);
-            if (timed_out) break;
-            ptx::tc_fence_after_sync();
-            uint32_t s[4][32];
-#pragma unroll
-            for (int q4 = 0; q4 < 4; ++q4) ptx::tmem_ld_32x32b_x32(s_addr + 32 * q4, s[q4]);
-            ptx::tmem_wait_ld();
-            if ((t + 1) * kTileK > all_see) {
-                const int lim = vis - t * kTileK;
-#pragma unroll
-                for (int q4 = 0; q4 < 4; ++q4)
-#pragma unroll
-                    for (int e = 0; e < 32; ++e)
-                        if (32 * q4 + e >= lim) s[q4][e] = 0xff800000u;   // -inf
+        uint32_t qn = 0, sn = 0;                               // the tile's items and steps so far
+        while (have_work()) {
+            // the item stays in shared memory and is read again for the output: the scores need the registers
+            int n, vis, all_see;
+            {
+                const Work w = copy_work();
+                const Tiles tiles(w, causal);
+                n = i == 0 ? tiles.n[0] : tiles.n[1];
+                const int row0 = w.qb * kBlockQ + i * kTileQ, row = row0 + (warp & 3) * 32 + lane;
+                vis = row < w.nq ? (causal ? max(0, min(w.nk, w.nk - w.nq + row + 1)) : w.nk) : 0;
+                // keys that every row of the tile sees: key tiles below need no mask
+                all_see = causal ? min(w.nk, w.nk - w.nq + row0 + 1) : w.nk;
             }
-            float mx4[4];
+            float m_run = -INFINITY, l_run = 0.0f;
+            for (int t = 0; t < n; ++t, ++sn) {
+                if (!ptx::mbar_wait(&bar.s_full[i], sn & 1u, deadline)) timed_out = true;
+                timed_out = __any_sync(0xffffffffu, timed_out);
+                if (timed_out) break;
+                ptx::tc_fence_after_sync();
+                uint32_t s[4][32];
 #pragma unroll
-            for (int q4 = 0; q4 < 4; ++q4) {
-                mx4[q4] = __uint_as_float(s[q4][0]);
+                for (int q4 = 0; q4 < 4; ++q4) ptx::tmem_ld_32x32b_x32(s_addr + 32 * q4, s[q4]);
+                ptx::tmem_wait_ld();
+                if ((t + 1) * kTileK > all_see) {
+                    const int lim = vis - t * kTileK;
 #pragma unroll
-                for (int e = 1; e < 32; ++e) mx4[q4] = fmaxf(mx4[q4], __uint_as_float(s[q4][e]));
-            }
-            const float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3]));
-            const bool grow = (mx - m_run) * cs > kRescaleThreshold || (m_run == -INFINITY && mx > -INFINITY);
-            if (__any_sync(0xffffffffu, grow)) {
-                const float alpha = grow ? (m_run == -INFINITY ? 0.0f : exp2f((m_run - mx) * cs)) : 1.0f;
-                if (grow) m_run = mx;
-                l_run *= alpha;
-                if (t > 0) {                                   // P V (t - 1) has completed: s_full covers it
+                    for (int q4 = 0; q4 < 4; ++q4)
+#pragma unroll
+                        for (int e = 0; e < 32; ++e)
+                            if (32 * q4 + e >= lim) s[q4][e] = 0xff800000u;   // -inf
+                }
+                float mx4[4];
+#pragma unroll
+                for (int q4 = 0; q4 < 4; ++q4) {
+                    mx4[q4] = __uint_as_float(s[q4][0]);
+#pragma unroll
+                    for (int e = 1; e < 32; ++e) mx4[q4] = fmaxf(mx4[q4], __uint_as_float(s[q4][e]));
+                }
+                const float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3]));
+                const bool grow = (mx - m_run) * cs > kRescaleThreshold || (m_run == -INFINITY && mx > -INFINITY);
+                if (__any_sync(0xffffffffu, grow)) {
+                    const float alpha = grow ? (m_run == -INFINITY ? 0.0f : exp2f((m_run - mx) * cs)) : 1.0f;
+                    if (grow) m_run = mx;
+                    l_run *= alpha;
+                    if (t > 0) {                               // P V (t - 1) has completed: s_full covers it
 #pragma unroll 1
-                    for (int cc = 0; cc < 128; cc += 32) {
-                        uint32_t o[32];
-                        ptx::tmem_ld_32x32b_x32(o_addr + cc, o);
-                        ptx::tmem_wait_ld();
+                        for (int cc = 0; cc < 128; cc += 32) {
+                            uint32_t o[32];
+                            ptx::tmem_ld_32x32b_x32(o_addr + cc, o);
+                            ptx::tmem_wait_ld();
 #pragma unroll
-                        for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
-                        tmem_st_x32(o_addr + cc, o);
+                            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+                            tmem_st_x32(o_addr + cc, o);
+                        }
                     }
                 }
-            }
-            const float neg = m_run == -INFINITY ? 0.0f : -m_run * cs;
-            const uint64_t neg2 = f32x2(neg, neg);
-            uint64_t sum2 = f32x2(0.0f, 0.0f);
+                const float neg = m_run == -INFINITY ? 0.0f : -m_run * cs;
+                const uint64_t neg2 = f32x2(neg, neg);
+                uint64_t sum2 = f32x2(0.0f, 0.0f);
 #pragma unroll
-            for (int q4 = 0; q4 < 4; ++q4) {
-                uint32_t pk[16];
+                for (int q4 = 0; q4 < 4; ++q4) {
+                    uint32_t pk[16];
 #pragma unroll
-                for (int e = 0; e < 32; e += 2) {
-                    float a, bb;
-                    unpack_f32x2(fma_f32x2(f32x2(__uint_as_float(s[q4][e]), __uint_as_float(s[q4][e + 1])), cs2, neg2), a, bb);
-                    a = fast_exp2(a);
-                    bb = fast_exp2(bb);
-                    sum2 = add_f32x2(sum2, f32x2(a, bb));
-                    pk[e / 2] = pack_bf16x2(a, bb);
+                    for (int e = 0; e < 32; e += 2) {
+                        float a, bb;
+                        unpack_f32x2(fma_f32x2(f32x2(__uint_as_float(s[q4][e]), __uint_as_float(s[q4][e + 1])), cs2, neg2), a, bb);
+                        a = fast_exp2(a);
+                        bb = fast_exp2(bb);
+                        sum2 = add_f32x2(sum2, f32x2(a, bb));
+                        pk[e / 2] = pack_bf16x2(a, bb);
+                    }
+                    tmem_st_x16(s_addr + 16 * q4, pk);
                 }
-                tmem_st_x16(s_addr + 16 * q4, pk);
+                tmem_wait_st();
+                ptx::tc_fence_before_sync();
+                __syncwarp();
+                if (lane == 0) ptx::mbar_arrive(&bar.p_full[i]);
+                float sa, sb;
+                unpack_f32x2(sum2, sa, sb);
+                l_run += sa + sb;
             }
-            tmem_wait_st();
-            ptx::tc_fence_before_sync();
-            __syncwarp();
-            if (lane == 0) ptx::mbar_arrive(&bar.p_full[i]);
-            float sa, sb;
-            unpack_f32x2(sum2, sa, sb);
-            l_run += sa + sb;
-        }
-        bool have_o = n_tiles[i] > 0 && !timed_out;
-        if (have_o) {
-            const bool got = ptx::mbar_wait(&bar.o_full[i], 0, deadline);
-            have_o = __all_sync(0xffffffffu, got);
-            if (!have_o) timed_out = true;
-            ptx::tc_fence_after_sync();
-        }
-        const float inv = l_run == 0.0f ? 0.0f : 1.0f / l_run;
-        uint16_t* dst = out + static_cast<int64_t>(q0 + row) * out_row + static_cast<int64_t>(h) * out_head;
+            if (timed_out) break;
+            if (n > 0) {
+                if (!ptx::mbar_wait(&bar.o_full[i], qn & 1u, deadline)) timed_out = true;
+                timed_out = __any_sync(0xffffffffu, timed_out);
+                if (timed_out) break;
+                ptx::tc_fence_after_sync();
+            }
+            const Work w = copy_work();
+            const int row0 = w.qb * kBlockQ + i * kTileQ, row = row0 + (warp & 3) * 32 + lane;   // query of the request
+            const float inv = l_run == 0.0f ? 0.0f : 1.0f / l_run;
+            const bool none = n == 0 || vis == 0;              // sees nothing: 0 (O may hold 0 x NaN)
+            uint16_t* dst = out + static_cast<int64_t>(w.h) * out_head + (lane & 7) * 8;
+            const int rows0 = row0 + (warp & 3) * 32 + (lane >> 3) * 8;   // rows this lane writes: rows0 .. + 7
 #pragma unroll 1
-        for (int cc = 0; cc < 128; cc += 32) {
-            uint32_t o[32];
-            if (have_o) {
-                ptx::tmem_ld_32x32b_x32(o_addr + cc, o);
-                ptx::tmem_wait_ld();
-            } else {
+            for (int cc = 0; cc < 128; cc += 64) {
+                uint32_t v[8][4];                              // the row's 16-byte pieces
 #pragma unroll
-                for (int e = 0; e < 32; ++e) o[e] = 0u;
-            }
-            if (vis == 0) {                                    // a query that sees nothing: 0 (O may hold 0 x NaN)
+                for (int hh = 0; hh < 2; ++hh) {
+                    uint32_t o[32];
+                    if (n > 0) {
+                        ptx::tmem_ld_32x32b_x32(o_addr + cc + 32 * hh, o);
+                        ptx::tmem_wait_ld();
+                    }
 #pragma unroll
-                for (int e = 0; e < 32; ++e) o[e] = 0u;
-            }
-            if (row < nq) {
-#pragma unroll
-                for (int e = 0; e < 32; e += 8) {
-                    uint4 w;
-                    w.x = pack_bf16x2(__uint_as_float(o[e]) * inv, __uint_as_float(o[e + 1]) * inv);
-                    w.y = pack_bf16x2(__uint_as_float(o[e + 2]) * inv, __uint_as_float(o[e + 3]) * inv);
-                    w.z = pack_bf16x2(__uint_as_float(o[e + 4]) * inv, __uint_as_float(o[e + 5]) * inv);
-                    w.w = pack_bf16x2(__uint_as_float(o[e + 6]) * inv, __uint_as_float(o[e + 7]) * inv);
-                    *reinterpret_cast<uint4*>(dst + cc + e) = w;
+                    for (int e = 0; e < 16; ++e)
+                        v[4 * hh + e / 4][e & 3] =
+                            none ? 0u : pack_bf16x2(__uint_as_float(o[2 * e]) * inv, __uint_as_float(o[2 * e + 1]) * inv);
                 }
+                // 8 x 8 transpose of the pieces within each group of 8 lanes, so that 8 lanes write a whole
+                // 128-byte line (a thread that writes its own row touches 32 lines per store)
+#pragma unroll
+                for (int m = 1; m < 8; m <<= 1) {
+                    const bool upper = (lane & m) != 0;
+#pragma unroll
+                    for (int a = 0; a < 8; ++a) {
+                        if (a & m) continue;
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const uint32_t mine = upper ? v[a][e] : v[a | m][e];
+                            const uint32_t got = __shfl_xor_sync(0xffffffffu, mine, m);
+                            if (upper) v[a][e] = got;
+                            else v[a | m][e] = got;
+                        }
+                    }
+                }
+#pragma unroll
+                for (int a = 0; a < 8; ++a)
+                    if (rows0 + a < w.nq)
+                        *reinterpret_cast<uint4*>(dst + static_cast<int64_t>(w.q0 + rows0 + a) * out_row + cc) =
+                            make_uint4(v[a][0], v[a][1], v[a][2], v[a][3]);
             }
+            if (n > 0) {
+                ptx::tc_fence_before_sync();
+                __syncwarp();
+                if (lane == 0) ptx::mbar_arrive(&bar.o_free[i]);
+                ++qn;
+            }
+            if (row < w.nq && lse_out != nullptr)
+                lse_out[static_cast<int64_t>(w.q0 + row) * H + w.h] =
+                    l_run == 0.0f ? -INFINITY : (m_run * cs + log2f(l_run)) * kLn2;
+            done();
         }
-        if (row < nq && lse_out != nullptr)
-            lse_out[static_cast<int64_t>(q0 + row) * H + h] =
-                l_run == 0.0f ? -INFINITY : (m_run * cs + log2f(l_run)) * kLn2;
     }
     if (timed_out) raise_error(err, DSA_DEVERR_TIMEOUT);
     ptx::tc_fence_before_sync();
