@@ -880,6 +880,7 @@ dense_mla_decode_kernel(const __grid_constant__ CUtensorMap kvmap, const __grid_
 // Joins the pieces of the split row tiles: one warp per (output row, 128 of its 512 dims).  The first
 // piece lies in slot 2 c0 + 1, the following ones in slots 2 (c0 + 1), .., 2 c.
 constexpr int kCombThreads = 256;
+constexpr int kCombBlocks = 4;     // per SM (32 requests of 8K: 1 block an SM 33 us of the call, 2 to 8 about 15)
 __global__ void __launch_bounds__(kCombThreads)
 dense_mla_combine_kernel(const float* __restrict__ part_o, const float* __restrict__ part_lse,
                          const Meta* __restrict__ meta, int clusters, int slot_rows, uint16_t* __restrict__ out,
@@ -919,38 +920,40 @@ dense_mla_combine_kernel(const float* __restrict__ part_o, const float* __restri
                 auto slot_of = [&](int j) {
                     return static_cast<int64_t>(j == 0 ? 2 * m.first_cluster + 1 : 2 * (m.first_cluster + j)) * slot_rows + row;
                 };
-                float top = -INFINITY;
-                bool nan = false;
-                for (int j = lane; j < n; j += 32) {
-                    const float l = part_lse[slot_of(j)];
-                    top = fmaxf(top, l);
-                    nan |= l != l;
-                }
-                top = warp_max(top);
-                float tot = 0.0f;
-                if (top != -INFINITY)
-                    for (int j = lane; j < n; j += 32) tot += exp2f(part_lse[slot_of(j)] - top);
-                tot = warp_sum(tot);
-                nan = __any_sync(0xffffffffu, nan);
+                // one pass, four pieces at a time: their sums and values are loaded together
+                float m_run = -INFINITY, tot = 0.0f;
                 float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-                if (top != -INFINITY) {
-                    const float inv = 1.0f / tot;
-#pragma unroll 4
-                    for (int j = 0; j < n; ++j) {
-                        const int64_t s = slot_of(j);
-                        const float w = exp2f(part_lse[s] - top) * inv;
-                        const float4 o = *reinterpret_cast<const float4*>(part_o + s * kValueDim + d0);
-                        acc.x = fmaf(w, o.x, acc.x);
-                        acc.y = fmaf(w, o.y, acc.y);
-                        acc.z = fmaf(w, o.z, acc.z);
-                        acc.w = fmaf(w, o.w, acc.w);
+                for (int j0 = 0; j0 < n; j0 += 4) {
+                    float l[4];
+                    float4 o[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int64_t s = slot_of(min(j0 + i, n - 1));
+                        l[i] = j0 + i < n ? part_lse[s] : -INFINITY;
+                        o[i] = *reinterpret_cast<const float4*>(part_o + s * kValueDim + d0);
+                    }
+                    const float top = fmaxf(fmaxf(fmaxf(l[0], l[1]), fmaxf(l[2], l[3])), m_run);
+                    const float ref = top == -INFINITY ? 0.0f : top;     // nothing visible so far: weights 0
+                    const float f = exp2f(m_run - ref);
+                    acc = make_float4(acc.x * f, acc.y * f, acc.z * f, acc.w * f);
+                    tot *= f;
+                    m_run = top;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const float w = exp2f(l[i] - ref);
+                        if (w == 0.0f) continue;                         // its values do not count
+                        tot += w;
+                        acc.x = fmaf(w, o[i].x, acc.x);
+                        acc.y = fmaf(w, o[i].y, acc.y);
+                        acc.z = fmaf(w, o[i].z, acc.z);
+                        acc.w = fmaf(w, o[i].w, acc.w);
                     }
                 }
-                if (nan) acc = make_float4(NAN, NAN, NAN, NAN);
+                const float inv = tot == 0.0f ? 0.0f : 1.0f / tot;
                 *reinterpret_cast<uint2*>(out + (m.out_row + row) * kValueDim + d0) =
-                    make_uint2(pack_bf16x2(acc.x, acc.y), pack_bf16x2(acc.z, acc.w));
+                    make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
                 if (lse_out != nullptr && (at & 3) == 0 && lane == 0)
-                    lse_out[m.out_row + row] = nan ? NAN : (top == -INFINITY ? -INFINITY : (top + log2f(tot)) * kLn2);
+                    lse_out[m.out_row + row] = tot == 0.0f ? -INFINITY : (m_run + log2f(tot)) * kLn2;
             }
             at -= tasks;
         }
@@ -1012,7 +1015,7 @@ extern "C" dsa_status dsa_dense_mla_decode(const void* q_bf16, const void* kv_po
     if (cudaGetLastError() != cudaSuccess) return DSA_ERR_CUDA;
     // a programmatic dependent of the attention kernel: scheduled as its CTAs end, waits for all of it
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(2 * clusters);
+    cfg.gridDim = dim3(2 * clusters * kCombBlocks);
     cfg.blockDim = dim3(kCombThreads);
     cfg.stream = s;
     cudaLaunchAttribute attr[1];
