@@ -143,6 +143,7 @@ inline EncodeTiledFn tensor_map_encoder() {
 inline bool encode_bf16_3d(EncodeTiledFn encode, CUtensorMap* map, const void* base, uint64_t n0, uint64_t n1,
                            uint64_t n2, int64_t s1, int64_t s2, uint32_t b0, uint32_t b2,
                            CUtensorMapSwizzle swizzle = CU_TENSOR_MAP_SWIZZLE_128B) {
+    if (n1 == 1) s1 = s2;   // never used, but it has to be a stride
     const cuuint64_t dims[3] = {n0, n1, n2};
     const cuuint64_t strides[2] = {static_cast<cuuint64_t>(s1) * 2, static_cast<cuuint64_t>(s2) * 2};
     const cuuint32_t box[3] = {b0, 1, b2};

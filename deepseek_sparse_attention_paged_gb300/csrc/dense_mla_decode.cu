@@ -101,6 +101,7 @@ struct Batch {
     const int32_t* seq_lens;
     const int32_t* cu_q;
     int B, T, H, max_pages;
+    int per;               // query tokens of a row tile: 128 / H
 };
 
 // Row tile g of request b: up to 128 / H consecutive query tokens.
@@ -117,11 +118,10 @@ __device__ __forceinline__ int query_range(const Batch& bt, int b, int& q0) {
 }
 
 __device__ __forceinline__ RowTile row_tile(const Batch& bt, int L, int q0, int nq, int g) {
-    const int per = kRows / bt.H;
     RowTile t;
-    t.row0 = q0 + g * per;
-    t.tokens = min(per, nq - g * per);
-    t.vis0 = L - nq + g * per + 1;
+    t.row0 = q0 + g * bt.per;
+    t.tokens = min(bt.per, nq - g * bt.per);
+    t.vis0 = L - nq + g * bt.per + 1;
     const int most = t.vis0 + t.tokens - 1;
     t.cut = most > bt.max_pages * kPage;
     t.tiles = (max(0, min(most, bt.max_pages * kPage)) + kKeys - 1) / kKeys;
@@ -163,7 +163,7 @@ struct Walk {
         if (left <= 0) return false;
         t0 = 0;
         first = false;
-        if ((g + 1) * (kRows / bt.H) < nq) {
+        if ((g + 1) * bt.per < nq) {
             ++g;
         } else {
             g = 0;
@@ -190,7 +190,7 @@ __device__ __forceinline__ int request_tiles(const Batch& bt, int b, int32_t* er
     if (nq == 0) return 0;
     const int L = __ldg(bt.seq_lens + b);
     int sum = 0;
-    for (int g = 0; g * (kRows / bt.H) < nq; ++g) {
+    for (int g = 0; g * bt.per < nq; ++g) {
         const RowTile t = row_tile(bt, L, q0, nq, g);
         if (t.cut && err != nullptr) raise_error(err, DSA_DEVERR_INDEX_RANGE);
         sum += max(1, t.tiles);
@@ -352,7 +352,8 @@ dense_mla_decode_kernel(const __grid_constant__ CUtensorMap kvmap, const __grid_
     cluster_sync_all();              // both CTAs' barriers exist before the peer signals or writes into them
     ptx::tc_fence_after_sync();
     const uint32_t tmem = uniform(bar.tmem_slot);
-    const uint64_t deadline = ptx::wait_deadline();
+    // limit of every wait, set anew every 256 tiles: a wait lasts a tile or so, the kernel may run for seconds
+    uint64_t deadline = ptx::wait_deadline();
     bool timed_out = false;
     const bool work = uniform(bar.start[3]) > 0;
     const uint32_t ring_addr = ptx::smem_addr(ring);
@@ -396,6 +397,7 @@ dense_mla_decode_kernel(const __grid_constant__ CUtensorMap kvmap, const __grid_
             for (int t = w.t0; t < w.t1 && !timed_out; ++t) {
                 const int tb = (t - w.t0) & 15;
                 if (tb == 0) {
+                    deadline = ptx::wait_deadline();
                     page = page_next;
                     page_next = load_pages(t + 16);
                 }
@@ -479,6 +481,7 @@ dense_mla_decode_kernel(const __grid_constant__ CUtensorMap kvmap, const __grid_
             wait(&bar.q_full, seg & 1u);
             ++seg;
             for (int t = w.t0; t < w.t1; ++t, ++u) {
+                if ((u & 255u) == 0u) deadline = ptx::wait_deadline();
                 const uint32_t sb = u % kSBufs;
                 if (u >= kSBufs) wait(&bar.s_read[sb], ((u / kSBufs) & 1u) ^ 1u);
                 const uint32_t d = tmem + kColS + sb * kKeys;
@@ -524,6 +527,7 @@ dense_mla_decode_kernel(const __grid_constant__ CUtensorMap kvmap, const __grid_
         do {
             if (w.t0 >= w.t1) continue;
             for (int t = w.t0; t < w.t1; ++t, ++u) {
+                if ((u & 255u) == 0u) deadline = ptx::wait_deadline();
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {                        // page i / 2, value dims 256 (i % 2) .. + 255
                     const uint32_t pb = 2 * (u & 1u) + (i >> 1);
@@ -630,6 +634,7 @@ dense_mla_decode_kernel(const __grid_constant__ CUtensorMap kvmap, const __grid_
             }
             used += 9u * static_cast<uint32_t>(max(0, w.t1 - w.t0));
             for (int t = w.t0; t < w.t1; ++t, ++u) {
+                if ((u & 255u) == 0u) deadline = ptx::wait_deadline();
                 const uint32_t sb = u % kSBufs, pb = 2 * (u & 1u) + kh;
                 wait(&bar.s_full[sb], (u / kSBufs) & 1u);
                 if (quad_live) {
@@ -757,6 +762,7 @@ dense_mla_decode_kernel(const __grid_constant__ CUtensorMap kvmap, const __grid_
             const bool quad_live = quad * 32 < live, has_tiles = w.t0 < w.t1;
             const uint32_t quads = static_cast<uint32_t>((live + 31) / 32);
             for (int t = w.t0; t < w.t1; ++t, ++u) {
+                if ((u & 255u) == 0u) deadline = ptx::wait_deadline();
                 const uint32_t pb = 2 * (u & 1u), pph = (u >> 1) & 1u;
                 if (threadIdx.x == 0) {
                     // the second buffer's previous phase is over once its P V is: this warp has not waited for it
@@ -1010,7 +1016,7 @@ extern "C" dsa_status dsa_dense_mla_decode(const void* q_bf16, const void* kv_po
         return DSA_ERR_CUDA;
     dense_mla_decode_kernel<<<2 * clusters, kDecThreads, kDecSmem, s>>>(
         kvmap, qmap, static_cast<const uint16_t*>(kv_pool), static_cast<int>(num_pages), block_table,
-        Batch{seq_lens, cu_q, B, T, H, max_pages}, scale, static_cast<uint16_t*>(out_bf16), lse, part_o, part_lse, meta,
+        Batch{seq_lens, cu_q, B, T, H, max_pages, kRows / H}, scale, static_cast<uint16_t*>(out_bf16), lse, part_o, part_lse, meta,
         slot_rows, dev_err);
     if (cudaGetLastError() != cudaSuccess) return DSA_ERR_CUDA;
     // a programmatic dependent of the attention kernel: scheduled as its CTAs end, waits for all of it

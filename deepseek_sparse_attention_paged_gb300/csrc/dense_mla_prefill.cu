@@ -41,6 +41,7 @@ namespace {
 
 using namespace attn;
 
+constexpr int kMaxKeys = 1 << 26;                         // an item stays within the limit of a wait (about 2 s)
 constexpr int kTileQ = 128, kTileK = 128, kBlockQ = 2 * kTileQ;
 constexpr int kSlabBytes = 128 * 128;                     // 128 rows x 64 bf16, 128-byte swizzle
 constexpr int kRing = 8;
@@ -100,19 +101,28 @@ __device__ __forceinline__ bool claimed_block(const uint32_t* answer, int& x, in
     return ok != 0;
 }
 
+// Where the last search ended: the chunk of 32 requests and the blocks before it.  Claimed blocks come in
+// ascending order, so a search goes on from there; from the start for each would cost a memory latency
+// per 32 requests and item.
+struct Scan {
+    int b0, before;
+};
+
 // Block x in the order of requests, the last (longest) query block of each first; false: past the last.
 __device__ __forceinline__ bool find_item(const int32_t* __restrict__ cu_q, const int32_t* __restrict__ cu_k, int B, int T,
-                                          int S, int x, int h, int lane, Work* item, int32_t* err) {
-    int carry = 0;
+                                          int S, int x, int h, int lane, Scan& scan, Work* item, int32_t* err) {
+    const bool check = x == 0 && h == 0;                       // this one looks at every request's range
+    if (x < scan.before) scan = Scan{0, 0};
+    int carry = scan.before;
     bool found = false;
-    for (int b0 = 0; b0 < B; b0 += 32) {
+    for (int b0 = scan.b0; b0 < B; b0 += 32) {
         const int b = b0 + lane;
         int q0 = 0, nq = 0;
         if (b < B) {
             const int lo = __ldg(cu_q + b), hi = __ldg(cu_q + b + 1);
             q0 = max(0, min(T, lo));
             nq = max(0, min(T, hi) - q0);
-            if (x == 0 && (lo < 0 || hi > T)) raise_error(err, DSA_DEVERR_INDEX_RANGE);
+            if (check && (lo < 0 || hi > T)) raise_error(err, DSA_DEVERR_INDEX_RANGE);
         }
         const int nb = (nq + kBlockQ - 1) / kBlockQ;
         int inc = nb;
@@ -124,13 +134,14 @@ __device__ __forceinline__ bool find_item(const int32_t* __restrict__ cu_q, cons
         const uint32_t hit = __ballot_sync(0xffffffffu, x < carry + inc);
         if (!found && hit != 0u) {
             found = true;
+            scan = Scan{b0, carry};
             if (lane == __ffs(hit) - 1) {
                 const int lo = __ldg(cu_k + b), hi = __ldg(cu_k + b + 1);
                 const int k0 = max(0, min(S, lo));
                 if (lo < 0 || hi > S) raise_error(err, DSA_DEVERR_INDEX_RANGE);
                 *item = Work{b, h, nb - 1 - (x - (carry + inc - nb)), q0, nq, k0, max(0, min(S, hi) - k0), 0};
             }
-            if (x != 0) break;                                 // block 0 goes on to check every range
+            if (!check) break;
         }
         carry += __shfl_sync(0xffffffffu, inc, 31);
     }
@@ -193,14 +204,17 @@ dense_mla_prefill_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_
     __syncthreads();
     ptx::tc_fence_after_sync();
     const uint32_t tmem = uniform(bar.tmem_slot);
-    const uint64_t deadline = ptx::wait_deadline();
+    // limit of every wait, set anew with every work item (one lasts at most about a second: kMaxKeys)
+    uint64_t deadline = ptx::wait_deadline();
     bool timed_out = false;
     // Work item k has been published, or there is no more (whole warp).  `done` gives its slot back; the
     // softmax warps do so at the item's end, which holds the claims one item ahead.
     uint32_t k = 0;
     auto have_work = [&]() -> bool {
+        deadline = ptx::wait_deadline();
         if (!ptx::mbar_wait(&bar.work_full[k & 1u], (k >> 1) & 1u, deadline)) timed_out = true;
         timed_out = __any_sync(0xffffffffu, timed_out);
+        deadline = ptx::wait_deadline();
         return !timed_out && uniform(bar.work[k & 1u].b) >= 0;
     };
     auto copy_work = [&]() -> Work {
@@ -219,7 +233,9 @@ dense_mla_prefill_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_
             // ---------------------------------------------------------------- work items
             int x = static_cast<int>(blockIdx.x), y = static_cast<int>(blockIdx.y);
             uint32_t claim_phase = 0;
+            Scan scan{0, 0};
             for (uint32_t j = 0;;) {
+                deadline = ptx::wait_deadline();
                 // the slot's previous item is done with by every warp
                 if (j >= 2 && !ptx::mbar_wait(&bar.work_empty[j & 1u], ((j >> 1) & 1u) ^ 1u, deadline)) timed_out = true;
                 timed_out = __any_sync(0xffffffffu, timed_out);
@@ -241,7 +257,7 @@ dense_mla_prefill_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_
                         __syncwarp();
                         if (!more) break;
                     }
-                    found = find_item(cu_q, cu_k, B, T, S, x, y, lane, &bar.work[j & 1u], err);
+                    found = find_item(cu_q, cu_k, B, T, S, x, y, lane, scan, &bar.work[j & 1u], err);
                     if (found) break;
                 }
                 if (timed_out) break;
@@ -637,7 +653,7 @@ extern "C" dsa_status dsa_dense_mla_prefill(const void* q_bf16, int64_t q_row_st
         return DSA_ERR_INVALID_ARG;
     if (!disjoint(out_row_stride, out_head_stride, T, H, 128)) return DSA_ERR_INVALID_ARG;
     if (!(scale > 0.0f) || !(scale < INFINITY)) return DSA_ERR_INVALID_ARG;
-    if (static_cast<int64_t>(T) * H >= 0x7fffffffLL || H > 65535) return DSA_ERR_UNSUPPORTED;
+    if (static_cast<int64_t>(T) * H >= 0x7fffffffLL || H > 65535 || S > kMaxKeys) return DSA_ERR_UNSUPPORTED;
     // tensor maps hold byte strides below 2^40
     const int64_t lim = int64_t(1) << 39;
     for (int64_t st : {q_row_stride, q_head_stride, k_row_stride, k_head_stride, pe_row_stride, v_row_stride, v_head_stride})

@@ -19,7 +19,7 @@
 namespace dsa {
 namespace {
 
-constexpr int kStoreThreads = 256;
+constexpr int kStoreThreads = 128;
 
 __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
     const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);

@@ -261,6 +261,15 @@ class DeviceBatch:
                                    self.idx if idx is None else idx, self.wl.scale, self.out, self.mla_ws,
                                    lse=self.lse, dev_err=self.dev_err, stream=stream)
 
+    def dense_mla(self, stream=None):
+        """Attention of the query rows over their whole visible context (no selection) into out / lse, with
+        a workspace of its own (allocated once)."""
+        if getattr(self, "_dense_ws", None) is None:
+            self._dense_ws = torch.empty(max(16, capi.dsa_dense_mla_decode_workspace_size(self.wl.T, self.wl.heads)),
+                                         dtype=torch.uint8, device=self.device)
+        capi.dsa_dense_mla_decode(self.mla_q, self.kv_pool, self.block_table, self.seq_lens, self.cu_q, self.wl.scale,
+                                  self.out, self._dense_ws, lse=self.lse, dev_err=self.dev_err, stream=stream)
+
     def tiles(self):
         """(row_begin, row_end) of every logits row tile, in order."""
         T, n = self.wl.T, self.tile_rows

@@ -612,8 +612,8 @@ dsa_status dsa_store_latent_prologue(const void* kv_a_bf16, int64_t row_stride, 
  *   k_pe_bf16      [S, 64] with its row stride (e.g. the last 64 columns of 576-wide latent rows).
  *   out_bf16       [T, H, 128] with its strides; must not overlap the inputs.
  *                  All bases 16-byte aligned, all strides multiples of 8 elements.
- *   cu_q, cu_k     int32 [B + 1] (device), ascending.   T, S: rows of q / out and of the keys.
- *   H              >= 1.   scale > 0, finite.   flags: 0 or DSA_CAUSAL.
+ *   cu_q, cu_k     int32 [B + 1] (device), ascending.   T, S: rows of q / out and of the keys (S at
+ *                  most 2^26).   H: 1 .. 65535.   scale > 0, finite.   flags: 0 or DSA_CAUSAL.
  *   lse            fp32 [T, H], nullable.
  *   dev_err        nullable; DSA_DEVERR_INDEX_RANGE for a cu_q / cu_k range outside [0, T] / [0, S]
  *                  (cut to it), DSA_DEVERR_TIMEOUT if a bounded wait gave up.
@@ -637,8 +637,10 @@ dsa_status dsa_dense_mla_prefill(const void* q_bf16, int64_t q_row_stride, int64
  *   v_r <= 0: out = 0, lse = -inf.  bf16 operands, fp32 accumulation, P rounded to bf16 for the
  *   product; the work is split over the cache's length and joined by log-sum-exp.  Rows >= cu_q[B]
  *   are left as they were.  Cache rows past the last visible position of a request may hold
- *   anything.
- * Arguments: as dsa_sparse_mla_decode, without idx and k.  H in {16, 32, 64, 128}.
+ *   anything.  An infinite or NaN value at a position that only later query tokens of the request see
+ *   may reach the earlier ones.
+ * Arguments: as dsa_sparse_mla_decode, without idx and k.  H in {16, 32, 64, 128}; B at most 16384;
+ *   T * max_pages < 2^31.
  *   workspace      device scratch of dsa_dense_mla_decode_workspace_size(T, H) bytes, 16-byte
  *                  aligned, nullable when that is 0.  No initialisation needed; its contents are
  *                  dead after the call, but two calls in flight at the same time must not share it.

@@ -570,3 +570,136 @@ def test_a_layer_of_prompts_then_drafted_tokens():
     u, us = torch.rand(T, generator=g), torch.rand(2, generator=g)
     got = _verify(p.cpu(), d.cpu(), tok, [q_len] * 2, u, us)
     assert got == ref.verify(p.cpu(), d.cpu(), tok.tolist(), [0, q_len, 2 * q_len], u, us)
+
+
+# ---------------------------------------------------------------- what else the calls allow
+
+def test_decode_many_requests_without_rows():
+    """3000 requests, most of them without query rows or without tokens."""
+    lens = [(7 * i) % 200 if i % 3 == 0 else 0 for i in range(3000)]
+    q_lens = [1 if i % 7 == 0 else 0 for i in range(3000)]
+    q, pool, table = _decode_inputs(lens, q_lens, 16, 80)
+    out, lse = _decode(q, pool, table, lens, q_lens)
+    ref.check(out, lse, ref.decode(q, pool, table, lens, q_lens, SCALE))
+
+
+@pytest.mark.parametrize("H", [128, 16])
+def test_decode_a_chunk_of_many_query_tokens(H):
+    """A prompt's chunk through the absorbed call: hundreds of query rows per request."""
+    lens, q_lens = [700, 300], [300, 77]
+    q, pool, table = _decode_inputs(lens, q_lens, H, 81 + H)
+    out, lse = _decode(q, pool, table, lens, q_lens)
+    ref.check(out, lse, ref.decode(q, pool, table, lens, q_lens, SCALE))
+
+
+def test_decode_negative_lengths_dirty_workspace_no_lse():
+    """A negative length sees nothing; a workspace full of NaN bytes and of an earlier call changes nothing."""
+    lens, q_lens = [-5, 3000, 9000, -1], [1, 2, 1, 2]
+    q, pool, table = _decode_inputs([max(0, n) for n in lens], q_lens, 64, 82)
+    ws = torch.full((capi.dsa_dense_mla_decode_workspace_size(6, 64),), 255, dtype=torch.uint8, device="cuda")
+    want = ref.decode(q, pool, table, [max(0, n) for n in lens], q_lens, SCALE)
+    for _ in range(2):
+        out, lse = _decode(q, pool, table, lens, q_lens, workspace=ws)
+        ref.check(out, lse, want)
+    o2 = torch.empty_like(out)
+    capi.dsa_dense_mla_decode(q, pool, table, _i32(lens), _i32(_cum(q_lens)), SCALE, o2, ws)
+    assert torch.equal(out, o2)
+
+
+def test_decode_on_two_streams_at_once():
+    """Two calls in flight, each with its own stream and workspace, give what they give alone."""
+    cases = []
+    for i, (lens, q_lens, H) in enumerate([([20000, 300], [1, 2], 128), ([5000] * 9, [1] * 9, 32)]):
+        q, pool, table = _decode_inputs(lens, q_lens, H, 83 + i)
+        out, lse = _decode(q, pool, table, lens, q_lens)
+        ws = torch.empty(capi.dsa_dense_mla_decode_workspace_size(q.shape[0], H), dtype=torch.uint8, device="cuda")
+        cases.append((q, pool, table, _i32(lens), _i32(_cum(q_lens)), out, lse, torch.zeros_like(out),
+                      torch.zeros_like(lse), ws, torch.cuda.Stream()))
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for q, pool, table, sl, cu, _, _, o, l, ws, s in cases:
+            capi.dsa_dense_mla_decode(q, pool, table, sl, cu, SCALE, o, ws, lse=l, stream=s)
+    torch.cuda.synchronize()
+    for _, _, _, _, _, out, lse, o, l, _, _ in cases:
+        assert torch.equal(out, o) and torch.equal(lse, l)
+
+
+def test_prefill_many_short_requests_and_one_head():
+    q_lens = [1 + (5 * i) % 9 for i in range(1500)]
+    k_lens = [n + (i % 4) * 40 for i, n in enumerate(q_lens)]
+    q, kv, lat = _prefill_inputs(q_lens, k_lens, 1, 84)
+    out, lse = _prefill(q, kv, lat, q_lens, k_lens)
+    ref.check(out, lse, ref.prefill(q, kv[..., :128], lat[:, 512:], kv[..., 128:], q_lens, k_lens, SCALE, True))
+
+
+def test_prefill_without_keys_and_without_lse():
+    q = torch.randn(5, 2, 192, generator=_gen(85)).to(torch.bfloat16).cuda()
+    empty = torch.empty(0, 2, 128, dtype=torch.bfloat16, device="cuda")
+    pe = torch.empty(0, 64, dtype=torch.bfloat16, device="cuda")
+    out = torch.full((5, 2, 128), 7.0, dtype=torch.bfloat16, device="cuda")
+    capi.dsa_dense_mla_prefill(q, empty, pe, empty, _i32([0, 5]), _i32([0, 0]), SCALE, out)
+    assert bool((out == 0).all())
+
+
+def test_prefill_twice_in_flight_beside_decode():
+    """Two prompts' calls and a decode call on three streams."""
+    q_lens = [900, 200]
+    q, kv, lat = _prefill_inputs(q_lens, q_lens, 16, 86)
+    want, _ = _prefill(q, kv, lat, q_lens, q_lens)
+    dq, pool, table = _decode_inputs([9000], [1], 128, 87)
+    dwant, _ = _decode(dq, pool, table, [9000], [1])
+    outs = [torch.zeros_like(want) for _ in range(2)]
+    dout = torch.zeros_like(dwant)
+    ws = torch.empty(capi.dsa_dense_mla_decode_workspace_size(1, 128), dtype=torch.uint8, device="cuda")
+    cu, sl, dcu = _i32(_cum(q_lens)), _i32([9000]), _i32([0, 1])
+    streams = [torch.cuda.Stream() for _ in range(3)]
+    torch.cuda.synchronize()
+    for _ in range(4):
+        for o, s in zip(outs, streams):
+            capi.dsa_dense_mla_prefill(q, kv[..., :128], lat[:, 512:], kv[..., 128:], cu, cu, SCALE, o, stream=s)
+        capi.dsa_dense_mla_decode(dq, pool, table, sl, dcu, SCALE, dout, ws, stream=streams[2])
+    torch.cuda.synchronize()
+    assert torch.equal(outs[0], want) and torch.equal(outs[1], want) and torch.equal(dout, dwant)
+
+
+def test_binding_refuses_what_the_calls_do_not_take():
+    f = torch.zeros(4, 16, 576, dtype=torch.bfloat16, device="cuda")
+    pool = torch.zeros(2, 64, 576, dtype=torch.bfloat16, device="cuda")
+    table, lens, cu = _i32([[0], [1]]), _i32([3, 4]), _i32([0, 2, 4])
+    out = torch.zeros(4, 16, 512, dtype=torch.bfloat16, device="cuda")
+    ws = torch.empty(capi.dsa_dense_mla_decode_workspace_size(4, 16), dtype=torch.uint8, device="cuda")
+    for bad in (dict(q_bf16=f.half()), dict(q_bf16=f[:, :, :512]), dict(kv_pool=pool[:, :, :512]), dict(cu_q=cu[:2]),
+                dict(out=out[:3]), dict(lse=torch.zeros(4, 15, device="cuda")), dict(seq_lens=lens.long()),
+                dict(block_table=table.t()), dict(workspace=torch.empty(64, dtype=torch.uint8)),
+                dict(dev_err=torch.zeros(1, device="cuda"))):
+        args = dict(q_bf16=f, kv_pool=pool, block_table=table, seq_lens=lens, cu_q=cu, scale=SCALE, out=out, workspace=ws)
+        args.update(bad)
+        with pytest.raises(ValueError):
+            capi.dsa_dense_mla_decode(**args)
+    with pytest.raises(capi.DSAError):
+        capi.dsa_dense_mla_decode(f, pool, table, lens, cu, SCALE, out, ws[:64])
+    p = torch.zeros(4, 8, device="cuda")
+    tok = torch.zeros(4, dtype=torch.int32, device="cuda")
+    u, us, acc = torch.zeros(4, device="cuda"), torch.zeros(2, device="cuda"), torch.zeros(2, dtype=torch.int32, device="cuda")
+    with pytest.raises(ValueError):
+        capi.dsa_verify_drafts(p, tok, cu, u, us, tok, acc)                    # in place
+    with pytest.raises(ValueError):
+        capi.dsa_verify_drafts(p, tok, cu, u, us, tok.clone(), acc, draft_probs=p[:, :7])
+    x = torch.zeros(4, 584, dtype=torch.bfloat16, device="cuda")
+    w, cs = torch.ones(512, device="cuda"), torch.zeros(4, 64, device="cuda")
+    i64 = torch.zeros(4, dtype=torch.int64, device="cuda")
+    with pytest.raises(capi.DSAError):
+        capi.dsa_store_latent_prologue(x[:, 4:580], w, 1e-6, cs, i64, i64, pool)     # rows not 16-byte aligned
+    with pytest.raises(ValueError):
+        capi.dsa_store_latent_prologue(x[:, :576], w, 1e-6, cs, i64[:3], i64, pool)
+
+
+def test_device_batch_dense_attention():
+    from deepseek_sparse_attention_paged_gb300 import workloads
+    from deepseek_sparse_attention_paged_gb300.pipeline import DeviceBatch
+    wl = workloads.make("tiny")
+    db = DeviceBatch(wl, build_index_cache=False)
+    db.dense_mla()
+    r = ref.decode(db.mla_q, db.kv_pool, db.block_table, wl.seq_lens.tolist(), wl.q_lens.tolist(), wl.scale)
+    ref.check(db.out, db.lse, r)
+    assert db.device_error() == (0, 0)
