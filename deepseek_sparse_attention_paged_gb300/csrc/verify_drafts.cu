@@ -245,26 +245,19 @@ verify_drafts_kernel(const float* __restrict__ target, int64_t ld_t, const float
         ++pass;
     }
     if (warp != 0) return;
-    // the same sums in the same order in every CTA: base of this CTA, total, owner of the border
-    Sum base{0.0f, 0.0f}, all{0.0f, 0.0f};
-    for (int c = 0; c < kVerifyCtas; ++c) {
-        if (c == rank) base = all;
-        all = all + totals[pass][c];
-    }
+    // the same sums in every CTA (lane c: CTA c's): base of this CTA, total, owner of the border
+    const Sum part = lane < kVerifyCtas ? totals[pass][lane] : Sum{0.0f, 0.0f};
+    const Sum upto = scan(part, lane);
+    const Sum all = shfl(upto, 31);
+    const Sum before = shfl(upto, max(rank - 1, 0));
+    const Sum base = rank > 0 ? before : Sum{0.0f, 0.0f};
     const float u = __ldg(u_sample + b);
     const float ua = __fmul_rn(u, all.hi);
     const Sum t = normal(ua, __fmaf_rn(u, all.lo, __fmaf_rn(u, all.hi, -ua)));
-    int owner = -1, last = -1;
-    Sum run{0.0f, 0.0f};
-    for (int c = 0; c < kVerifyCtas; ++c) {
-        const Sum tc = totals[pass][c];
-        run = run + tc;
-        if (tc.hi > 0.0f) {
-            last = c;
-            if (owner < 0 && run > t) owner = c;
-        }
-    }
-    if (owner < 0) owner = last;                 // u outside [0, 1): the last entry with mass
+    const uint32_t with_mass = __ballot_sync(0xffffffffu, part.hi > 0.0f);
+    const uint32_t past = __ballot_sync(0xffffffffu, part.hi > 0.0f && upto > t);
+    // u outside [0, 1): the last entry with mass
+    const int owner = past != 0u ? __ffs(past) - 1 : 31 - __clz(with_mass);   // -1: no mass
     if (owner < 0) {                             // a row without mass
         if (rank == 0 && lane == 0) {
             out_tokens[r0 + first] = -1;
@@ -289,7 +282,7 @@ verify_drafts_kernel(const float* __restrict__ target, int64_t ld_t, const float
         }
     }
     if (g_hit < 0) g_hit = max(g_last, 0);
-    run = g_hit > 0 ? base + group_sum[g_hit - 1] : base;
+    Sum run = g_hit > 0 ? base + group_sum[g_hit - 1] : base;
     const int v0 = (g_begin + g_hit) * kGroup + lane * 4;
     float p[4][4], q[4][4];
 #pragma unroll
