@@ -58,9 +58,10 @@ __device__ __forceinline__ Sum shfl_up(Sum v, int d) {
 __device__ __forceinline__ Sum shfl(Sum v, int l) {
     return Sum{__shfl_sync(0xffffffffu, v.hi, l), __shfl_sync(0xffffffffu, v.lo, l)};
 }
-// Inclusive prefix sums over the lanes.
+// Inclusive prefix sums over the lanes.  Rolled: code that runs once or twice costs its instruction fetches
+// (unrolled, the last steps of the draw took 5200 cycles).
 __device__ __forceinline__ Sum scan(Sum v, int lane) {
-#pragma unroll
+#pragma unroll 1
     for (int d = 1; d < 32; d <<= 1) {
         const Sum o = shfl_up(v, d);
         if (lane >= d) v = o + v;
@@ -216,7 +217,7 @@ verify_drafts_kernel(const float* __restrict__ target, int64_t ld_t, const float
                     hi = t;
                 }
             Sum sum = normal(hi, lo);
-#pragma unroll
+#pragma unroll 1
             for (int m = 16; m > 0; m >>= 1)
                 sum = sum + Sum{__shfl_xor_sync(0xffffffffu, sum.hi, m), __shfl_xor_sync(0xffffffffu, sum.lo, m)};
             if (lane == 0) group_sum[g] = sum;
@@ -283,40 +284,37 @@ verify_drafts_kernel(const float* __restrict__ target, int64_t ld_t, const float
     }
     if (g_hit < 0) g_hit = max(g_last, 0);
     Sum run = g_hit > 0 ? base + group_sum[g_hit - 1] : base;
-    const int v0 = (g_begin + g_hit) * kGroup + lane * 4;
-    float p[4][4], q[4][4];
-#pragma unroll
-    for (int s = 0; s < 4; ++s) load4<VEC>(p_row, q_row, mode, x, v0 + s * 128, V, p[s], q[s]);
-    int token = -1, last_pos = -1;
-    Sum inc[4];                                  // inclusive prefix over lanes of the lanes' sums, step by step
-#pragma unroll
-    for (int s = 0; s < 4; ++s) {
+    // the first of 32 runs of 16 entries whose prefix passes t, and in it the first entry; where the border
+    // lies within the rounding of a sum, the last one with mass
+    int v0 = (g_begin + g_hit) * kGroup;
+    int token = -1;
+#pragma unroll 1
+    for (int len = kGroup / 32; len > 0; len = len > 1 ? 1 : 0) {
+        const int v = v0 + lane * len;                 // len = 16: a run each; len = 1: an entry each of the run
         Sum own{0.0f, 0.0f};
+        if (len > 1) {
+#pragma unroll 1
+            for (int e = 0; e < len; e += 4) {
+                float p[4], q[4];
+                load4<VEC>(p_row, q_row, mode, x, v + e, V, p, q);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) own = own + weight(p[s][e], q[s][e]);
-        inc[s] = scan(own, lane);
-    }
-#pragma unroll
-    for (int s = 0; s < 4; ++s) {
-        const Sum before = shfl_up(inc[s], 1);
-        Sum at = lane > 0 ? run + before : run;
-        int found = -1, pos = -1;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const Sum w = weight(p[s][e], q[s][e]);
-            at = at + w;
-            if (w.hi > 0.0f) {
-                pos = v0 + s * 128 + e;
-                if (found < 0 && at > t) found = pos;
+                for (int i = 0; i < 4; ++i) own = own + weight(p[i], q[i]);
             }
+        } else if (lane < kGroup / 32) {               // one entry at any address: no vector load
+            float p[4], q[4];
+            load4<false>(p_row, q_row, mode, x, v, min(V, v + 1), p, q);
+            own = weight(p[0], q[0]);
         }
-        const uint32_t hit = __ballot_sync(0xffffffffu, found >= 0);
-        const uint32_t any = __ballot_sync(0xffffffffu, pos >= 0);
-        if (any != 0u) last_pos = __shfl_sync(0xffffffffu, pos, 31 - __clz(any));
-        if (hit != 0u && token < 0) token = __shfl_sync(0xffffffffu, found, __ffs(hit) - 1);
-        run = run + shfl(inc[s], 31);
+        const Sum upto = scan(own, lane);
+        const uint32_t some = __ballot_sync(0xffffffffu, own.hi > 0.0f);
+        const uint32_t over = __ballot_sync(0xffffffffu, own.hi > 0.0f && run + upto > t);
+        if (some == 0u) break;                         // unreachable: the group has mass
+        const int l = over != 0u ? __ffs(over) - 1 : 31 - __clz(some);
+        const Sum before_l = shfl(upto, max(l - 1, 0));
+        if (l > 0) run = run + before_l;
+        v0 += l * len;
+        if (len == 1) token = v0;
     }
-    if (token < 0) token = last_pos;             // the border lies within the rounding of the group's sum
     if (lane == 0) out_tokens[r0 + first] = token;
 }
 
