@@ -153,5 +153,17 @@ inline bool encode_bf16_3d(EncodeTiledFn encode, CUtensorMap* map, const void* b
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// Map of a dense fp32 array [rows][width], boxes [box_rows][box_width], 128-byte swizzle.
+inline bool encode_f32_rows(EncodeTiledFn encode, CUtensorMap* map, const void* base, uint64_t width, uint64_t rows,
+                            uint32_t box_width, uint32_t box_rows) {
+    const cuuint64_t dims[3] = {width, 1, rows};
+    const cuuint64_t strides[2] = {width * 4, width * 4};
+    const cuuint32_t box[3] = {box_width, 1, box_rows};
+    const cuuint32_t estr[3] = {1, 1, 1};
+    return encode(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 3, const_cast<void*>(base), dims, strides, box, estr,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 }  // namespace attn
 }  // namespace dsa

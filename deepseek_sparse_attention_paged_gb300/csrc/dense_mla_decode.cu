@@ -59,7 +59,7 @@ constexpr int kPBytes = kRows * kPage * 2;                      // 16384: P of a
 constexpr int kQRopeBytes = kRows * 128;                        // 16384
 constexpr int kPOffset = kKStages * kKStageBytes + kQRopeBytes; // P at the same place in both ranks
 constexpr int kDataBytes = kPOffset + kPBufs * kPBytes;
-static_assert(kVStages * kVStageBytes + 8 * 2048 <= kPOffset, "rank 1's stages and output staging");
+static_assert(kVStages * kVStageBytes <= kPOffset, "rank 1's stages");
 constexpr int kTmaWarp = 8, kMmaWarp = 9;
 constexpr int kDecThreads = 384;
 constexpr uint32_t kColS = 256;                                 // rank 0: score tiles, behind the query chunks
@@ -86,6 +86,8 @@ struct DecBars {
     uint64_t pv_done[kPvBars];              // P V of the tile complete (more than the tiles the row warps may be ahead)
     uint64_t o_free;                        // O read out (8 row warps), per row tile
     uint64_t fin_full;                      // 1 / l arrived (armed + bytes), per row tile
+    uint64_t stage_lent;                    // two ring stages are free for the output, per row tile
+    uint64_t stage_back;                    // ... and no longer read (8 row warps)
     uint32_t tmem_slot;
     int page_ok[kMaxStages];                // bit i: page i of the stage is there and its id valid
     int tile_ok[kSBufs];                    // ... of the score tile's pages
@@ -279,6 +281,18 @@ __device__ __forceinline__ void bulk_to_peer(uint32_t dst, uint32_t src, uint32_
                  "r"(src), "r"(bytes), "r"(bar)
                  : "memory");
 }
+// Tile of shared memory into global memory by TMA, and the waits of the thread that issued it: all but the
+// last N groups have read their source; everything is written.
+__device__ __forceinline__ void tma_store_3d(const CUtensorMap* map, const void* src, int c0, int c1, int c2) {
+    asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"(
+                     reinterpret_cast<uint64_t>(map)),
+                 "r"(ptx::smem_addr(src)), "r"(c0), "r"(c1), "r"(c2)
+                 : "memory");
+}
+__device__ __forceinline__ void bulk_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void bulk_wait_read() { asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(N) : "memory"); }
+__device__ __forceinline__ void bulk_wait_all() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
 __device__ __forceinline__ void prefetch_line(const void* p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
 // Arrive on a barrier of the peer without ordering anything before it: used for buffers this thread has
 // only read (the values are in registers).  A release at cluster scope costs about 2000 cycles here.
@@ -303,10 +317,11 @@ struct Meta {
 
 __global__ void __launch_bounds__(kDecThreads, 1) __cluster_dims__(2, 1, 1)
 dense_mla_decode_kernel(const __grid_constant__ CUtensorMap kvmap, const __grid_constant__ CUtensorMap qmap,
+                        const __grid_constant__ CUtensorMap omap, const __grid_constant__ CUtensorMap pmap,
                         const uint16_t* __restrict__ kv, int num_pages,
                         const int32_t* __restrict__ block_table, Batch bt, float scale, uint16_t* __restrict__ out,
-                        float* __restrict__ lse_out, float* __restrict__ part_o, float* __restrict__ part_lse,
-                        Meta* __restrict__ meta, int slot_rows, int32_t* err) {
+                        float* __restrict__ lse_out, float* __restrict__ part_lse, Meta* __restrict__ meta, int slot_rows,
+                        int32_t* err) {
     extern __shared__ unsigned char smem_raw[];
     const uint32_t raw_addr = ptx::smem_addr(smem_raw);
     unsigned char* base = smem_raw + (((raw_addr + 1023u) & ~1023u) - raw_addr);
@@ -339,6 +354,8 @@ dense_mla_decode_kernel(const __grid_constant__ CUtensorMap kvmap, const __grid_
         for (int i = 0; i < kPvBars; ++i) ptx::mbar_init(&bar.pv_done[i], 1);
         ptx::mbar_init(&bar.o_free, 8);
         ptx::mbar_init(&bar.fin_full, 1);
+        ptx::mbar_init(&bar.stage_lent, 1);
+        ptx::mbar_init(&bar.stage_back, 8);
         ptx::mbar_init(&bar.fin_free, 8);
         ptx::fence_barrier_init();
     }
@@ -448,6 +465,16 @@ dense_mla_decode_kernel(const __grid_constant__ CUtensorMap kvmap, const __grid_
                         }
                         advance();
                     }
+                }
+            }
+            // rank 1: two stages for the row tile's output
+            if (rank == 1 && w.t0 < w.t1 && !timed_out) {
+                for (int i = 0; i < 2 && stage(); ++i) {
+                    if (elect_one()) {
+                        ptx::mbar_arrive(&bar.kv_full[s]);           // nothing to copy: the stage's phase passes
+                        if (i == 1) ptx::mbar_arrive(&bar.stage_lent);
+                    }
+                    advance();
                 }
             }
         } while (!timed_out && w.next());
@@ -570,6 +597,15 @@ dense_mla_decode_kernel(const __grid_constant__ CUtensorMap kvmap, const __grid_
                     }
                 }
                 if (__any_sync(0xffffffffu, late)) break;
+            }
+            wait(&bar.stage_back, seg & 1u);
+            for (int i = 0; i < 2; ++i) {
+                __syncwarp();
+                if (elect_one()) ptx::mbar_arrive(&bar.kv_empty[s]);
+                if (++s == kVStages) {
+                    s = 0;
+                    ph ^= 1u;
+                }
             }
             ++seg;
         } while (!__any_sync(0xffffffffu, late) && w.next());
@@ -754,8 +790,7 @@ dense_mla_decode_kernel(const __grid_constant__ CUtensorMap kvmap, const __grid_
         auto wait = [&](uint64_t* b, uint32_t parity) {
             if (!ptx::mbar_wait(b, parity, deadline)) timed_out = true;
         };
-        unsigned char* stage_out = base + kVStages * kVStageBytes + warp * 2048;   // behind rank 1's stages
-        uint32_t u = 0, seg = 0;
+        uint32_t u = 0, seg = 0, used = 0;                           // used: ring stages before this row tile
         Walk w(bt, bar.start);
         do {
             const int live = w.rt.tokens * bt.H;
@@ -809,22 +844,26 @@ dense_mla_decode_kernel(const __grid_constant__ CUtensorMap kvmap, const __grid_
                 if (timed_out) break;
                 ptx::tc_fence_after_sync();
             }
-            if (quad_live) {
-                // 128 bytes of each row at a time through 2 KB of shared memory, 16 rows and then the other 16, and
-                // out as whole 128-byte lines: a thread writing its own row touches 32 lines per store
-                const int64_t row0 = w.whole ? static_cast<int64_t>(w.rt.row0) * bt.H + quad * 32
-                                             : piece_slot(cluster, w) * slot_rows + quad * 32;
+            if (has_tiles) {
+                // 128 bytes of each row at a time into 4 KB of a lent stage (128-byte swizzle) and out by TMA, 16 rows
+                // a copy (rows come in multiples of 16), one buffer filling while the other leaves.  Stores by
+                // threads, whole lines each, went out at 32 bytes a cycle, 4100 (parts: 8200) cycles a row tile
+                // (512 requests of 512 keys 124 -> 116 us, one of 4096 22.3 -> 21.1 us).
+                used += 4u * static_cast<uint32_t>(w.t1 - w.t0);
+                wait(&bar.stage_lent, seg & 1u);
+                timed_out = __any_sync(0xffffffffu, timed_out);
+                if (timed_out) break;
                 const int width = w.whole ? 64 : 32;                 // dims of 128 bytes
-                unsigned char* dst = w.whole ? reinterpret_cast<unsigned char*>(out) : reinterpret_cast<unsigned char*>(part_o);
-                const int64_t pitch = w.whole ? kValueDim * 2 : kValueDim * 4;
-                dst += row0 * pitch + dh * (pitch / 2) + (lane & 7) * 16;
+                const int64_t row0 = w.whole ? static_cast<int64_t>(w.rt.row0) * bt.H : piece_slot(cluster, w) * slot_rows;
+                const int swz = lane & 7;
+                int buf = 0;
 #pragma unroll 1
-                for (int cc = 0; cc < 256; cc += width) {
+                for (int cc = 0; quad_live && cc < 256; cc += width, buf ^= 1) {
                     uint32_t o[32];                                  // the row's 128 bytes
-                    if (has_tiles) ptx::tmem_ld_32x32b_x32(o_addr + cc, o);
+                    ptx::tmem_ld_32x32b_x32(o_addr + cc, o);
                     if (w.whole) {
                         uint32_t x[32];
-                        if (has_tiles) ptx::tmem_ld_32x32b_x32(o_addr + cc + 32, x);
+                        ptx::tmem_ld_32x32b_x32(o_addr + cc + 32, x);
                         ptx::tmem_wait_ld();
 #pragma unroll
                         for (int e = 0; e < 16; ++e)
@@ -837,40 +876,43 @@ dense_mla_decode_kernel(const __grid_constant__ CUtensorMap kvmap, const __grid_
 #pragma unroll
                         for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * inv);
                     }
-                    if (inv < 0.0f) {
+                    unsigned char* st = ring + ((used + buf) % kVStages) * kVStageBytes + warp * 4096;
+                    if (lane == 0) bulk_wait_read<1>();              // the buffer's previous copies have read it
+                    __syncwarp();
 #pragma unroll
-                        for (int e = 0; e < 32; ++e) o[e] = 0u;
-                    }
+                    for (int i = 0; i < 8; ++i)
+                        *reinterpret_cast<uint4*>(st + lane * 128 + ((i ^ swz) << 4)) =
+                            inv < 0.0f ? make_uint4(0u, 0u, 0u, 0u) : make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+                    ptx::fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) {
 #pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        __syncwarp();
-                        if ((lane >> 4) == h) {
-#pragma unroll
-                            for (int i = 0; i < 8; ++i)
-                                *reinterpret_cast<uint4*>(stage_out + (lane & 15) * 128 + ((i ^ (lane & 7)) << 4)) =
-                                    make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
-                        }
-                        __syncwarp();
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const int r = 4 * i + (lane >> 3);       // row of the 16
-                            const uint4 v = *reinterpret_cast<const uint4*>(stage_out + r * 128 + (((lane & 7) ^ (r & 7)) << 4));
-                            if (quad * 32 + 16 * h + r < live)
-                                *reinterpret_cast<uint4*>(dst + (16 * h + r) * pitch + cc * (w.whole ? 2 : 4)) = v;
-                        }
+                        for (int h = 0; h < 2; ++h)
+                            if (quad * 32 + 16 * h < live)
+                                tma_store_3d(w.whole ? &omap : &pmap, st + h * 2048, dh * 256 + cc, 0,
+                                             static_cast<int>(row0) + quad * 32 + 16 * h);
+                        bulk_commit();
                     }
                 }
-            }
-            if (has_tiles) {
                 ptx::tc_fence_before_sync();
                 __syncwarp();
-                if (lane == 0) ptx::mbar_arrive(&bar.o_free);
+                if (lane == 0) {
+                    ptx::mbar_arrive(&bar.o_free);
+                    bulk_wait_read<0>();
+                    ptx::mbar_arrive(&bar.stage_back);
+                }
+                used += 2;
                 ++seg;
+            } else if (quad_live) {                                  // sees nothing: zeros
+                for (int r = quad * 32; r < min(live, quad * 32 + 32); ++r)
+                    *reinterpret_cast<uint4*>(out + (static_cast<int64_t>(w.rt.row0) * bt.H + r) * kValueDim + dh * 256 + lane * 8) =
+                        make_uint4(0u, 0u, 0u, 0u);
             }
             // the last piece of a split row tile: the combine kernel finds it here
             if (threadIdx.x == 0 && w.first && w.t0 > 0 && w.t1 == w.rt.tiles)
                 meta[cluster] = Meta{static_cast<int64_t>(w.rt.row0) * bt.H, live, bar.first_cluster};
         } while (w.next());
+        if (lane == 0) bulk_wait_all();                              // written before the CTA leaves
     }
     if (timed_out) raise_error(err, DSA_DEVERR_TIMEOUT);
     ptx::griddep_launch_dependents();
@@ -1002,22 +1044,24 @@ extern "C" dsa_status dsa_dense_mla_decode(const void* q_bf16, const void* kv_po
     if (workspace == nullptr || !aligned16(workspace) || workspace_bytes < need) return DSA_ERR_INVALID_ARG;
     auto encode = attn::tensor_map_encoder();
     if (encode == nullptr) return DSA_ERR_CUDA;
-    CUtensorMap kvmap, qmap;
-    if (!attn::encode_bf16_3d(encode, &kvmap, kv_pool, kLatentDim, 1, num_pages * kPage, kLatentDim, kLatentDim, 64, kPage) ||
-        !attn::encode_bf16_3d(encode, &qmap, q_bf16, kLatentDim, 1, static_cast<uint64_t>(T) * H, kLatentDim, kLatentDim, 64, kRows))
-        return DSA_ERR_CUDA;
     const int clusters = decode_clusters(), slot_rows = decode_slot_rows(T, H);
     Meta* meta = static_cast<Meta*>(workspace);
     float* part_o = reinterpret_cast<float*>(meta + clusters);
     float* part_lse = part_o + static_cast<size_t>(2) * clusters * slot_rows * kValueDim;
+    CUtensorMap kvmap, qmap, omap, pmap;
+    if (!attn::encode_bf16_3d(encode, &kvmap, kv_pool, kLatentDim, 1, num_pages * kPage, kLatentDim, kLatentDim, 64, kPage) ||
+        !attn::encode_bf16_3d(encode, &qmap, q_bf16, kLatentDim, 1, static_cast<uint64_t>(T) * H, kLatentDim, kLatentDim, 64, kRows) ||
+        !attn::encode_bf16_3d(encode, &omap, out_bf16, kValueDim, 1, static_cast<uint64_t>(T) * H, kValueDim, kValueDim, 64, 16) ||
+        !attn::encode_f32_rows(encode, &pmap, part_o, kValueDim, static_cast<uint64_t>(2) * clusters * slot_rows, 32, 16))
+        return DSA_ERR_CUDA;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     if (cudaFuncSetAttribute(dense_mla_decode_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              static_cast<int>(kDecSmem)) != cudaSuccess)
         return DSA_ERR_CUDA;
     dense_mla_decode_kernel<<<2 * clusters, kDecThreads, kDecSmem, s>>>(
-        kvmap, qmap, static_cast<const uint16_t*>(kv_pool), static_cast<int>(num_pages), block_table,
-        Batch{seq_lens, cu_q, B, T, H, max_pages, kRows / H}, scale, static_cast<uint16_t*>(out_bf16), lse, part_o, part_lse, meta,
-        slot_rows, dev_err);
+        kvmap, qmap, omap, pmap, static_cast<const uint16_t*>(kv_pool), static_cast<int>(num_pages), block_table,
+        Batch{seq_lens, cu_q, B, T, H, max_pages, kRows / H}, scale, static_cast<uint16_t*>(out_bf16), lse, part_lse, meta, slot_rows,
+        dev_err);
     if (cudaGetLastError() != cudaSuccess) return DSA_ERR_CUDA;
     // a programmatic dependent of the attention kernel: scheduled as its CTAs end, waits for all of it
     cudaLaunchConfig_t cfg = {};
