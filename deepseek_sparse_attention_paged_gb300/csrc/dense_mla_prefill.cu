@@ -151,7 +151,8 @@ __device__ __forceinline__ bool find_item(const int32_t* __restrict__ cu_q, cons
 
 // Key tiles that the rows of the item's two query tiles see.  Query i sees keys [0, nk - nq + i] (causal).
 struct Tiles {
-    int n[2], most;
+    int n[2] = {0, 0}, most = 0;
+    Tiles() = default;
     __device__ Tiles(const Work& w, int causal) {
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
@@ -306,9 +307,10 @@ dense_mla_prefill_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_
                     load_k(0);
                     load_q(1);
                     for (int t = 0; t < n.most && !timed_out; ++t) {
+                        const int swap = c % kRing == kRing - 1 ? 1 : 0;   // see issue_pv
                         for (int j = 0; j < kVSlabs && !timed_out; ++j)
                             if (unsigned char* dst = next())
-                                ptx::tma_load_3d(dst, &vmap, bar_of_last(), 64 * j, w.h, w.k0 + t * kTileK);
+                                ptx::tma_load_3d(dst, &vmap, bar_of_last(), 64 * (j ^ swap), w.h, w.k0 + t * kTileK);
                         if (t + 1 < n.most) load_k(t + 1);
                     }
                 }
@@ -329,7 +331,6 @@ dense_mla_prefill_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_
             // ---------------------------------------------------------------- MMA
             constexpr uint32_t idesc_qk = ptx::instr_desc(1, 1, kTileQ, kTileK);
             constexpr uint32_t idesc_pv = ptx::instr_desc(1, 1, kTileQ, 128) | (1u << 16);   // B MN-major
-            constexpr uint32_t idesc_pv_half = ptx::instr_desc(1, 1, kTileQ, 64) | (1u << 16);
             const uint32_t q_addr = ptx::smem_addr(qs), ring_addr = ptx::smem_addr(ring);
             // A wait that ran out only marks the step: the warp leaves together at the step's end.  What it
             // issues until then reads shared and tensor memory of this CTA only.
@@ -342,14 +343,19 @@ dense_mla_prefill_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_
                 if (elect_one())
                     for (int j = 0; j < cnt; ++j) ptx::umma_commit(&bar.empty[(c0 + j) % kRing]);
             };
-            // descriptors differ in their start address only (low word, 16-byte units): one add each
-            const uint64_t q_desc = desc_sw128(q_addr, 16, 1024);
-            const uint64_t k_desc = desc_sw128(ring_addr, 16, 1024), v_desc = desc_sw128(ring_addr, kSlabBytes, 1024);
+            // Descriptors differ in their low word only.  What an MMA takes is made uniform right before it issues:
+            // the operands are uniform registers, and values that the compiler cannot tell to be the same in
+            // all lanes are moved there one by one for each MMA (8 prompts of 128 to 2048: 385 -> 361 us, together
+            // with V's swapped halves below, which had been products of half the width).
+            const uint64_t q_desc = desc_sw128(q_addr, 16, 1024), k_desc = desc_sw128(ring_addr, 16, 1024);
+            const uint64_t v_desc = desc_sw128(ring_addr, kSlabBytes, 1024);
+            const uint64_t v_wrap = desc_sw128(ring_addr, (kRing - 1) * kSlabBytes, 1024);
+            auto low = [](uint64_t d) { return static_cast<uint32_t>(d); };
+            auto with_low = [](uint64_t d, uint32_t lo) { return (d & 0xffffffff00000000ull) | lo; };
             auto slab = [&](uint32_t cc) { return (cc % kRing) * (kSlabBytes / 16); };
             // S_i = Q_i K^T from the slabs at c0; the first user of a key tile waits for each slab in turn;
             // the item's last one gives the queries back
             auto issue_s = [&](int i, uint32_t c0, bool first, bool last) {
-                const uint64_t a = q_desc + i * (kQSlabs * kSlabBytes / 16);
 #pragma unroll
                 for (int j = 0; j < kKSlabs; ++j) {
                     if (first) {
@@ -357,12 +363,13 @@ dense_mla_prefill_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_
                         __syncwarp();
                         ptx::tc_fence_after_sync();
                     }
+                    const uint32_t a = uniform(low(q_desc) + i * (kQSlabs * kSlabBytes / 16) + j * (kSlabBytes / 16));
+                    const uint32_t bk = uniform(low(k_desc) + slab(c0 + j)), d = uniform(tmem + kColS + 128 * i);
                     if (elect_one()) {
-                        const uint64_t bk = k_desc + slab(c0 + j);
 #pragma unroll
                         for (int kk = 0; kk < 4; ++kk)
-                            ptx::umma_f16(tmem + kColS + 128 * i, a + (j * (kSlabBytes / 16) + kk * 2), bk + kk * 2,
-                                          idesc_qk, (j | kk) != 0 ? 1u : 0u);
+                            ptx::umma_f16(d, with_low(q_desc, a + kk * 2), with_low(k_desc, bk + kk * 2), idesc_qk,
+                                          (j | kk) != 0 ? 1u : 0u);
                         if (j == kKSlabs - 1) {
                             ptx::umma_commit(&bar.s_full[i]);
                             if (last) ptx::umma_commit(&bar.q_empty[i]);
@@ -370,53 +377,53 @@ dense_mla_prefill_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_
                     }
                 }
             };
-            // O_i += P_i V from the two slabs at c0
+            // O_i += P_i V from the two slabs at c0.  Where the ring wraps between them the halves of V lie
+            // swapped: dims 0-63 in the first slab, 64-127 in the last.
             auto issue_pv = [&](int i, uint32_t c0, uint32_t accumulate) {
+                const bool wrap = c0 % kRing == kRing - 1;
+                const uint32_t bv = uniform(wrap ? low(v_wrap) : low(v_desc) + slab(c0));
+                const uint32_t o = uniform(tmem + kColO + 128 * i), p = uniform(tmem + kColS + 128 * i);
                 if (elect_one()) {
-                    const uint64_t v0 = v_desc + slab(c0), v1 = v_desc + slab(c0 + 1);
-                    const uint32_t o = tmem + kColO + 128 * i, p = tmem + kColS + 128 * i;
-                    if (v1 > v0) {
 #pragma unroll
-                        for (int ks = 0; ks < kTileK / 16; ++ks)
-                            umma_f16_ts(o, p + ks * 8, v0 + ks * 128, idesc_pv, ks != 0 ? 1u : accumulate);
-                    } else {                                   // the ring wraps between the two slabs
-#pragma unroll
-                        for (int ks = 0; ks < kTileK / 16; ++ks) {
-                            umma_f16_ts(o, p + ks * 8, v0 + ks * 128, idesc_pv_half, ks != 0 ? 1u : accumulate);
-                            umma_f16_ts(o + 64, p + ks * 8, v1 + ks * 128, idesc_pv_half, ks != 0 ? 1u : accumulate);
-                        }
-                    }
+                    for (int ks = 0; ks < kTileK / 16; ++ks)
+                        umma_f16_ts(o, p + ks * 8, with_low(v_desc, bv + ks * 128), idesc_pv, ks != 0 ? 1u : accumulate);
                 }
             };
-            uint32_t c0 = 0, qn[2] = {0, 0}, sn[2] = {0, 0};   // slabs and, per tile, items and steps before this item
-            while (have_work()) {
-                const Work w = copy_work();
-                const Tiles n(w, causal);
-                done();
-                if (n.most > 0) {
-                    bool first = true;
-#pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        if (n.n[i] == 0) continue;
-                        wait(&bar.q_full[i], qn[i] & 1u);
-                        issue_s(i, c0, first, n.n[i] == 1);
-                        first = false;
+            // A step issues P V of its key tile and the scores of the next one.  In an item's last step the next
+            // one is the first of the item after it (K of that lies behind the last V in the ring, too), so the
+            // tensor cores work while the softmax warps write the output, and a causal item's tile 0, one step
+            // shorter, goes on at once.
+            Tiles n, nn;                                       // of this item and the next
+            int nk = 0, nk_next = 0;
+            bool more = false;
+            uint32_t c_k = 0;                                  // first slab of the next K
+            uint32_t q_phase = 0, p_phase = 0, o_phase = 0, o_used = 0;   // bit i: of the tile's barriers
+            auto step = [&](int t, bool over) {
+                // ring order: K(0), V(0), K(1), V(1), ...
+                const uint32_t c_v = c_k - kVSlabs;
+                const int last = t < n.n[1] ? 1 : 0;           // the last tile that uses V(t)
+                if (over) {
+                    more = false;
+                    while (have_work()) {
+                        const Work w = copy_work();
+                        nn = Tiles(w, causal);
+                        nk_next = w.nk;
+                        done();
+                        more = nn.most > 0;
+                        if (more) break;
                     }
-                    release(c0, kKSlabs);
                 }
-                for (int t = 0; t < n.most; ++t) {
-                    // ring order: K(0), V(0), K(1), V(1), ...; this step uses V(t) and K(t + 1)
-                    const uint32_t c_v = c0 + static_cast<uint32_t>(t) * (kKSlabs + kVSlabs) + kKSlabs, c_k = c_v + kVSlabs;
-                    const int last = t < n.n[1] ? 1 : 0;       // the last tile that uses V(t)
-                    bool first_v = true, first_k = true;
+                bool first_v = true, first_k = true;
 #pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        if (t >= n.n[i]) continue;
+                for (int i = 0; i < 2; ++i) {
+                    const uint32_t bit = 1u << i;
+                    const int ni = i == 0 ? n.n[0] : n.n[1];
+                    if (t >= 0 && t < ni) {
                         if (first_v) {
                             first_v = false;
                             wait_slab(c_v);
                             wait_slab(c_v + 1);
-                            const int valid = w.nk - t * kTileK;
+                            const int valid = nk - t * kTileK;
                             if (valid < kTileK) {
                                 // rows past the request's last key are another request's, or anything: their
                                 // P is 0, but 0 times NaN or infinity is not
@@ -431,29 +438,45 @@ dense_mla_prefill_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_
                                 ptx::fence_proxy_async_smem();
                             }
                         }
-                        if (t == 0 && qn[i] > 0) wait(&bar.o_free[i], (qn[i] - 1) & 1u);
-                        wait(&bar.p_full[i], (sn[i] + t) & 1u);
+                        if (t == 0) {                                  // the item before has read its output
+                            if ((o_used & bit) != 0u) {
+                                wait(&bar.o_free[i], (o_phase >> i) & 1u);
+                                o_phase ^= bit;
+                            }
+                            o_used |= bit;
+                        }
+                        wait(&bar.p_full[i], (p_phase >> i) & 1u);
+                        p_phase ^= bit;
                         __syncwarp();
                         ptx::tc_fence_after_sync();
                         issue_pv(i, c_v, t != 0 ? 1u : 0u);
                         if (i == last) release(c_v, kVSlabs);
-                        if (t + 1 < n.n[i]) {
-                            issue_s(i, c_k, first_k, t + 2 == n.n[i]);
-                            first_k = false;
-                        } else if (elect_one()) {
-                            ptx::umma_commit(&bar.o_full[i]);
-                        }
+                        if (t + 1 == ni && elect_one()) ptx::umma_commit(&bar.o_full[i]);
+                        __syncwarp();
                     }
-                    if (t + 1 < n.most) release(c_k, kKSlabs);
+                    // score tiles of the query tile from the next step on
+                    const int left = over ? (!more ? 0 : i == 0 ? nn.n[0] : nn.n[1]) : ni - t - 1;
+                    if (left > 0) {
+                        if (over) {
+                            wait(&bar.q_full[i], (q_phase >> i) & 1u);
+                            q_phase ^= bit;
+                        }
+                        issue_s(i, c_k, first_k, left == 1);
+                        first_k = false;
+                    }
+                }
+                if (!over || more) release(c_k, kKSlabs);
+                c_k += kKSlabs + kVSlabs;
+            };
+            for (;;) {
+                // the first time there is no item yet, only the first scores of the next
+                for (int t = n.most == 0 ? -1 : 0; t < n.most; ++t) {
+                    step(t, t + 1 == n.most);
                     if (__any_sync(0xffffffffu, late)) break;
                 }
-                if (__any_sync(0xffffffffu, late)) break;
-                c0 += static_cast<uint32_t>(n.most) * (kKSlabs + kVSlabs);
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    qn[i] += n.n[i] > 0 ? 1u : 0u;
-                    sn[i] += static_cast<uint32_t>(n.n[i]);
-                }
+                if (!more || __any_sync(0xffffffffu, late)) break;
+                n = nn;
+                nk = nk_next;
             }
             if (late) timed_out = true;
         }
