@@ -15,11 +15,14 @@
 // Q K^T (K = 192) and 512 of P V at 8192 FLOP per cycle and SM, its softmax 16384 exponentials
 // (512 to 1024 cycles of the special-function unit).  So a CTA holds two tiles of 128 queries of
 // one head and one request: while the softmax warps of one work, the tensor cores run the other's
-// products.
+// products.  Measured: 8192 queries and keys, 19 heads, no mask 443 us (1.82 PFLOP/s; Q K^T reads both operands
+// from shared memory, 8 KB an MMA, which takes 79 cycles for 64); causal with 128 heads 1.65 ms; 8 prompts
+// of 128 to 2048 361 us (84 % of their tiles' area counts); 1000 queries after 15001 keys 848 us (512 equal
+// items on 152 SMs).
 //
 // Work item: block qb of 256 query rows of request b, head h.  The grid has one block per item; a CTA
 // takes over the items of blocks that have not started (cluster launch control) until none is left, so
-// that an item's first copies and products run while the one before is still writing its output.
+// that an item's first copies and scores run while the one before is still at its last step and its output.
 // Roles (384 threads):
 //   warps 0-3, 4-7  softmax of query tile 0 / 1: one thread per query (TMEM lane), 128 scores in
 //                   registers, P written back over the scores as bf16; O / l at the end;

@@ -16,6 +16,9 @@
 // and of q that the draw needs is read, once, with all group sums kept in shared memory; the CTAs
 // swap their totals through distributed shared memory, and the CTA whose range holds the border
 // re-reads one group of 512 entries.
+//
+// Bound by the chain of dependent steps (acceptance, sums, totals across the cluster, border), about 7 us.  Measured:
+// 1 request 7.7 us, 8 of 131072 entries 10.4 us, 64 of them 16.5 us (the read of 49 MB alone 7.2 us at the copy rate).
 #include "dsa_common.cuh"
 #include "sm100_ptx.cuh"
 
