@@ -406,16 +406,17 @@ dense_mla_prefill_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_
                 const uint32_t c_v = c_k - kVSlabs;
                 const int last = t < n.n[1] ? 1 : 0;           // the last tile that uses V(t)
                 if (over) {
-                    more = false;
-                    while (have_work()) {
+                    // one item ahead and no further: the one after it is published when the softmax warps are done
+                    // with this one, for which they need the products of this step
+                    more = have_work();
+                    if (more) {
                         const Work w = copy_work();
                         nn = Tiles(w, causal);
                         nk_next = w.nk;
                         done();
-                        more = nn.most > 0;
-                        if (more) break;
                     }
                 }
+                const bool next_k = over ? more && nn.most > 0 : true;   // K behind this step's V
                 bool first_v = true, first_k = true;
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
@@ -468,11 +469,14 @@ dense_mla_prefill_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_
                         first_k = false;
                     }
                 }
-                if (!over || more) release(c_k, kKSlabs);
-                c_k += kKSlabs + kVSlabs;
+                if (next_k) {
+                    release(c_k, kKSlabs);
+                    c_k += kKSlabs + kVSlabs;
+                }
             };
             for (;;) {
-                // the first time there is no item yet, only the first scores of the next
+                // the first time there is no item yet, and one that sees no key has no steps: only the first scores
+                // of the next
                 for (int t = n.most == 0 ? -1 : 0; t < n.most; ++t) {
                     step(t, t + 1 == n.most);
                     if (__any_sync(0xffffffffu, late)) break;

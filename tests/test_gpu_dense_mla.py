@@ -703,3 +703,17 @@ def test_device_batch_dense_attention():
     r = ref.decode(db.mla_q, db.kv_pool, db.block_table, wl.seq_lens.tolist(), wl.q_lens.tolist(), wl.scale)
     ref.check(db.out, db.lse, r)
     assert db.device_error() == (0, 0)
+
+
+@pytest.mark.parametrize("causal", [True, False])
+def test_prefill_items_of_every_shape_after_one_another(causal):
+    """Each CTA takes several items in turn: query tiles without rows or without visible keys, single key tiles,
+    key tails, requests without keys, in changing order."""
+    shapes = [(300, 100), (300, 40), (257, 1), (512, 130), (1, 1), (256, 256), (129, 129), (128, 500), (400, 0), (700, 690),
+              (1, 513), (130, 300), (384, 129), (2, 0), (513, 900)]
+    order = torch.randperm(3 * len(shapes), generator=_gen(73)).tolist()
+    q_lens = [shapes[i % len(shapes)][0] for i in order]
+    k_lens = [shapes[i % len(shapes)][1] for i in order]
+    q, kv, lat = _prefill_inputs(q_lens, k_lens, 24, 74)
+    out, lse = _prefill(q, kv, lat, q_lens, k_lens, causal)
+    ref.check(out, lse, ref.prefill(q, kv[..., :128], lat[:, 512:], kv[..., 128:], q_lens, k_lens, SCALE, causal))
