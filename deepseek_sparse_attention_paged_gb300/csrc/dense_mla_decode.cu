@@ -123,6 +123,9 @@ __device__ __forceinline__ int query_range(const Batch& bt, int b, int& q0) {
     return max(0, min(bt.T, __ldg(bt.cu_q + b + 1)) - q0);
 }
 
+// Lengths below 0 count as 0.
+__device__ __forceinline__ int seq_len(const Batch& bt, int b) { return max(0, __ldg(bt.seq_lens + b)); }
+
 __device__ __forceinline__ RowTile row_tile(const Batch& bt, int L, int q0, int nq, int g) {
     RowTile t;
     t.row0 = q0 + g * bt.per;
@@ -154,7 +157,7 @@ struct Walk {
     __device__ void load_request() {
         nq = uniform(query_range(bt, b, q0));
         q0 = uniform(q0);
-        L = uniform(__ldg(bt.seq_lens + b));
+        L = uniform(seq_len(bt, b));
     }
     __device__ void set_piece() {
         rt = row_tile(bt, L, q0, nq, g);
@@ -194,7 +197,7 @@ __device__ __forceinline__ int request_tiles(const Batch& bt, int b, int32_t* er
     const int nq = query_range(bt, b, q0);
     if (err != nullptr && (__ldg(bt.cu_q + b) < 0 || __ldg(bt.cu_q + b + 1) > bt.T)) raise_error(err, DSA_DEVERR_INDEX_RANGE);
     if (nq == 0) return 0;
-    const int L = __ldg(bt.seq_lens + b);
+    const int L = seq_len(bt, b);
     int sum = 0;
     for (int g = 0; g * bt.per < nq; ++g) {
         const RowTile t = row_tile(bt, L, q0, nq, g);
@@ -236,7 +239,7 @@ __device__ __forceinline__ void find_share(const Batch& bt, int c, int clusters,
                         int at = carry + inc - own;            // tiles before the request
                         int q0;
                         const int nq = query_range(bt, b, q0);
-                        const int L = __ldg(bt.seq_lens + b);
+                        const int L = seq_len(bt, b);
                         int g = 0;
                         for (;; ++g) {
                             const int n = max(1, row_tile(bt, L, q0, nq, g).tiles);

@@ -705,6 +705,41 @@ def test_device_batch_dense_attention():
     assert db.device_error() == (0, 0)
 
 
+def test_decode_extreme_lengths_and_ranges_outside_the_rows():
+    """The smallest int32 as a length sees nothing; a length past the table is cut to it; cu_q outside [0, T] is
+    cut to it; each but the first is reported."""
+    lens, q_lens = [100, 200, 300], [1, 2, 1]
+    q, pool, table = _decode_inputs(lens, q_lens, 16, 71)
+    err = _err()
+    out, lse = _decode(q, pool, table, [-2 ** 31, 200, -2 ** 31 + 1], q_lens, err)
+    assert capi.dsa_read_device_error(err) == (0, 0)
+    ref.check(out, lse, ref.decode(q, pool, table, [0, 200, 0], q_lens, SCALE))
+    table[1, :] = table[1, 0]
+    out, lse = _decode(q, pool, table, [100, 2 ** 31 - 1, 300], q_lens, err)
+    assert capi.dsa_read_device_error(err) == (capi.DSA_ERR_DEVICE_BOUNDS, capi.DSA_DEVERR_INDEX_RANGE)
+    for r in (0, 3):
+        one = ref.decode(q[r:r + 1], pool, table[[0 if r == 0 else 2]].contiguous(), [100 if r == 0 else 300], [1], SCALE)
+        ref.check(out[r:r + 1], lse[r:r + 1], one)
+    err.zero_()
+    out = torch.full((4, 16, 512), 7.0, dtype=torch.bfloat16, device="cuda")
+    two = table[:2].contiguous()
+    capi.dsa_dense_mla_decode(q, pool, two, _i32([100, 300]), _i32([-3, 1, 900]), SCALE, out, dev_err=err)
+    assert capi.dsa_read_device_error(err) == (capi.DSA_ERR_DEVICE_BOUNDS, capi.DSA_DEVERR_INDEX_RANGE)
+    want = ref.decode(q, pool, two, [100, 300], [1, 3], SCALE)
+    assert bool(((out.double() - want[0]).abs() <= want[2]).all())
+
+
+@pytest.mark.parametrize("H,lens,q_lens", [(16, [9000, 5000, 7777], [5, 1, 7]), (32, [20000, 64], [3, 4]),
+                                           (16, [130 * i for i in range(1, 60)], [1 + i % 9 for i in range(59)])])
+def test_decode_split_row_tiles_that_are_not_full(H, lens, q_lens):
+    """Pieces of row tiles with few rows, next to whole ones: nothing behind their rows is written."""
+    q, pool, table = _decode_inputs(lens, q_lens + [2], H, 72 + H)
+    out, lse = _decode(q, pool, table, lens, q_lens)
+    T = sum(q_lens)
+    assert bool((out[T:] == 7.0).all()) and bool((lse[T:] == 7.0).all())
+    ref.check(out[:T], lse[:T], ref.decode(q[:T], pool, table, lens, q_lens, SCALE))
+
+
 @pytest.mark.parametrize("causal", [True, False])
 def test_prefill_items_of_every_shape_after_one_another(causal):
     """Each CTA takes several items in turn: query tiles without rows or without visible keys, single key tiles,
