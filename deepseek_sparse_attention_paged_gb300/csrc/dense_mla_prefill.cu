@@ -16,13 +16,16 @@
 // (512 to 1024 cycles of the special-function unit).  So a CTA holds two tiles of 128 queries of
 // one head and one request: while the softmax warps of one work, the tensor cores run the other's
 // products.  Measured: 8192 queries and keys, 19 heads, no mask 443 us (1.82 PFLOP/s; Q K^T reads both operands
-// from shared memory, 8 KB an MMA, which takes 79 cycles for 64); causal with 128 heads 1.65 ms; 8 prompts
-// of 128 to 2048 361 us (84 % of their tiles' area counts); 1000 queries after 15001 keys 848 us (512 equal
-// items on 152 SMs).
+// from shared memory, 8 KB an MMA, which takes 79 cycles for 64); causal with 128 heads 1.58 ms, with 16 heads
+// 210 us; 8 prompts of 128 to 2048 358 us (84 % of their tiles' area counts); 1000 queries after 15001 keys
+// 793 us, with 16 heads 115 us.
 //
-// Work item: block qb of 256 query rows of request b, head h.  The grid has one block per item; a CTA
+// Work item: block qb of 256 query rows of request b, head h; the longest first over a group of heads whose keys
+// and values fit L2.  The grid has one block per item; a CTA
 // takes over the items of blocks that have not started (cluster launch control) until none is left, so
 // that an item's first copies and scores run while the one before is still at its last step and its output.
+// Calls with few items split each one's keys over a cluster of C = 2 or 4 CTAs instead (one item a cluster): the
+// parts' O, m and l go to the CTA that writes the rows through distributed shared memory and are joined there.
 // Roles (384 threads):
 //   warps 0-3, 4-7  softmax of query tile 0 / 1: one thread per query (TMEM lane), 128 scores in
 //                   registers, P written back over the scores as bf16; O / l at the end;
@@ -52,6 +55,11 @@ constexpr int kQSlabs = 3, kKSlabs = 3, kVSlabs = 2;
 constexpr int kTmaWarp = 8, kMmaWarp = 9, kWorkWarp = 10;
 constexpr int kPreThreads = 384;                          // three warpgroups; warp 11 only fills the third
 constexpr int kSoftmaxRegs = 208, kOtherRegs = 88;        // 2 x 128 x 208 + 128 x 88 <= 384 x 168 at launch
+// Split items: the parts of a row group of 32 queries (a softmax warp's) are joined by one CTA; a part is
+// 32 x 128 fp32 outputs, then the rows' maxima (log2 units) and sums.
+constexpr int kGroups = 8, kPartBytes = 32 * 512 + 256, kMaxSplit = 4;
+static_assert(2 * (kGroups - kGroups / kMaxSplit) * kPartBytes <= (2 * kQSlabs + kRing) * kSlabBytes, "parts sent and received");
+constexpr int64_t kGroupBytes = 96 << 20;                 // keys and values of a group of heads (L2: 129 MB)
 constexpr uint32_t kColS = 0, kColO = 256;                // + 128 * tile
 constexpr size_t kPreSmem = 1024 + size_t(2 * kQSlabs + kRing) * kSlabBytes + 512;
 static_assert(kPreSmem <= 232448, "shared-memory budget");
@@ -59,8 +67,8 @@ static_assert(kPreSmem <= 232448, "shared-memory budget");
 struct Work {
     int b;                   // request; -1: no more work
     int h, qb, q0, nq;       // head, query block, first query row and queries of the request
-    int k0, nk;              // first key row and keys of the request
-    int pad;
+    int k0, nk;              // first key row and keys (of this CTA's part of the request)
+    int diag;                // causal: query i sees the first diag + i + 1 of them
 };
 
 struct PreBars {
@@ -74,6 +82,7 @@ struct PreBars {
     uint64_t claim_full;     // answer to the claim of another block
     alignas(16) uint32_t claim[4];
     Work work[2];
+    uint64_t joined[8 / 2];  // split items: the parts of a row group arrived (armed + bytes)
     uint32_t tmem_slot;
 };
 static_assert(sizeof(PreBars) <= 512, "barrier block");
@@ -143,6 +152,7 @@ __device__ __forceinline__ bool find_item(const int32_t* __restrict__ cu_q, cons
                 const int k0 = max(0, min(S, lo));
                 if (lo < 0 || hi > S) raise_error(err, DSA_DEVERR_INDEX_RANGE);
                 *item = Work{b, h, nb - 1 - (x - (carry + inc - nb)), q0, nq, k0, max(0, min(S, hi) - k0), 0};
+                item->diag = item->nk - nq;
             }
             if (!check) break;
         }
@@ -152,7 +162,7 @@ __device__ __forceinline__ bool find_item(const int32_t* __restrict__ cu_q, cons
     return found;
 }
 
-// Key tiles that the rows of the item's two query tiles see.  Query i sees keys [0, nk - nq + i] (causal).
+// Key tiles that the rows of the item's two query tiles see.
 struct Tiles {
     int n[2] = {0, 0}, most = 0;
     Tiles() = default;
@@ -161,18 +171,19 @@ struct Tiles {
         for (int i = 0; i < 2; ++i) {
             const int first = w.qb * kBlockQ + i * kTileQ;
             const int last = min(w.nq, first + kTileQ) - 1;
-            const int seen = last < first ? 0 : (causal ? max(0, min(w.nk, w.nk - w.nq + last + 1)) : w.nk);
+            const int seen = last < first ? 0 : (causal ? max(0, min(w.nk, w.diag + last + 1)) : w.nk);
             n[i] = (seen + kTileK - 1) / kTileK;
         }
         most = max(n[0], n[1]);
     }
 };
 
+template <int C>
 __global__ void __launch_bounds__(kPreThreads, 1)
 dense_mla_prefill_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kmap,
                          const __grid_constant__ CUtensorMap pmap, const __grid_constant__ CUtensorMap vmap,
                          const int32_t* __restrict__ cu_q, const int32_t* __restrict__ cu_k, int B, int T, int S, int H,
-                         float scale, int causal, uint16_t* __restrict__ out, int64_t out_row, int64_t out_head,
+                         float scale, int causal, int group, uint16_t* __restrict__ out, int64_t out_row, int64_t out_head,
                          float* __restrict__ lse_out, int32_t* err) {
     extern __shared__ unsigned char smem_raw[];
     const uint32_t raw_addr = ptx::smem_addr(smem_raw);
@@ -194,6 +205,11 @@ dense_mla_prefill_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_
             ptx::mbar_init(&bar.work_empty[i], 10);
         }
         ptx::mbar_init(&bar.claim_full, 1);
+        if constexpr (C > 1)
+            for (int g = 0; g < kGroups / C; ++g) {
+                ptx::mbar_init(&bar.joined[g], 1);
+                ptx::mbar_arrive_expect_tx(&bar.joined[g], (C - 1) * kPartBytes);
+            }
         for (int s = 0; s < kRing; ++s) {
             ptx::mbar_init(&bar.full[s], 1);
             ptx::mbar_init(&bar.empty[s], 1);
@@ -210,7 +226,7 @@ dense_mla_prefill_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_
     const uint32_t tmem = uniform(bar.tmem_slot);
     // limit of every wait, set anew with every work item (one lasts at most about a second: kMaxKeys)
     uint64_t deadline = ptx::wait_deadline();
-    bool timed_out = false;
+    bool timed_out = false, synced = false;               // synced (C > 1): this warp has met the cluster
     // Work item k has been published, or there is no more (whole warp).  `done` gives its slot back; the
     // softmax warps do so at the item's end, which holds the claims one item ahead.
     uint32_t k = 0;
@@ -223,7 +239,7 @@ dense_mla_prefill_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_
     };
     auto copy_work = [&]() -> Work {
         const Work& x = bar.work[k & 1u];
-        return Work{0, uniform(x.h), uniform(x.qb), uniform(x.q0), uniform(x.nq), uniform(x.k0), uniform(x.nk), 0};
+        return Work{0, uniform(x.h), uniform(x.qb), uniform(x.q0), uniform(x.nq), uniform(x.k0), uniform(x.nk), uniform(x.diag)};
     };
     auto done = [&]() {
         __syncwarp();
@@ -235,7 +251,7 @@ dense_mla_prefill_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_
         set_regs_dec<kOtherRegs>();
         if (warp == kWorkWarp) {
             // ---------------------------------------------------------------- work items
-            int x = static_cast<int>(blockIdx.x), y = static_cast<int>(blockIdx.y);
+            int x = static_cast<int>(blockIdx.x) / C, y = static_cast<int>(blockIdx.y);
             uint32_t claim_phase = 0;
             Scan scan{0, 0};
             for (uint32_t j = 0;;) {
@@ -248,6 +264,7 @@ dense_mla_prefill_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_
                 bool found = false;
                 for (bool claim = j > 0;; claim = true) {
                     if (claim) {
+                        if constexpr (C > 1) break;                  // one item a cluster
                         if (lane == 0) {
                             ptx::fence_proxy_async_smem();           // the answer before has been read
                             ptx::mbar_arrive_expect_tx(&bar.claim_full, 16);
@@ -261,10 +278,27 @@ dense_mla_prefill_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_
                         __syncwarp();
                         if (!more) break;
                     }
-                    found = find_item(cu_q, cu_k, B, T, S, x, y, lane, scan, &bar.work[j & 1u], err);
+                    // the grid's order, x first, as (group of heads, block, head): long blocks of many heads come first,
+                    // and the last items of all are short ones (8K prompt x 16 heads: one head after the other
+                    // 292 us, so 210)
+                    const int blocks = static_cast<int>(gridDim.x) / C, id = y * blocks + x;
+                    const int g0 = id / (group * blocks) * group, heads = min(group, H - g0), rem = id - g0 * blocks;
+                    found = find_item(cu_q, cu_k, B, T, S, rem / heads, g0 + rem % heads, lane, scan, &bar.work[j & 1u], err);
                     if (found) break;
                 }
                 if (timed_out) break;
+                if constexpr (C > 1) {
+                    if (found) {                                     // this CTA's share of the item's key tiles
+                        Work w = bar.work[0];
+                        const Tiles all(w, causal);
+                        const int rank = static_cast<int>(blockIdx.x) % C, from = all.most * rank / C * kTileK;
+                        w.nk = max(0, min(w.nk, all.most * (rank + 1) / C * kTileK) - from);
+                        w.k0 += from;
+                        w.diag -= from;
+                        __syncwarp();
+                        if (lane == 0) bar.work[0] = w;
+                    }
+                }
                 if (!found && lane == 0) bar.work[j & 1u].b = -1;
                 __syncwarp();
                 if (lane == 0) ptx::mbar_arrive(&bar.work_full[j & 1u]);
@@ -505,9 +539,9 @@ dense_mla_prefill_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_
                 const Tiles tiles(w, causal);
                 n = i == 0 ? tiles.n[0] : tiles.n[1];
                 const int row0 = w.qb * kBlockQ + i * kTileQ, row = row0 + (warp & 3) * 32 + lane;
-                vis = row < w.nq ? (causal ? max(0, min(w.nk, w.nk - w.nq + row + 1)) : w.nk) : 0;
+                vis = row < w.nq ? (causal ? max(0, min(w.nk, w.diag + row + 1)) : w.nk) : 0;
                 // keys that every row of the tile sees: key tiles below need no mask
-                all_see = causal ? min(w.nk, w.nk - w.nq + row0 + 1) : w.nk;
+                all_see = causal ? min(w.nk, w.diag + row0 + 1) : w.nk;
             }
             float m_run = -INFINITY, l_run = 0.0f;
             for (int t = 0; t < n; ++t, ++sn) {
@@ -586,8 +620,67 @@ dense_mla_prefill_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_
             }
             const Work w = copy_work();
             const int row0 = w.qb * kBlockQ + i * kTileQ, row = row0 + (warp & 3) * 32 + lane;   // query of the request
-            const float inv = l_run == 0.0f ? 0.0f : 1.0f / l_run;
-            const bool none = n == 0 || vis == 0;              // sees nothing: 0 (O may hold 0 x NaN)
+            float m2 = m_run * cs, l_all = l_run;              // maximum (log2 units) and sum of all parts
+            float weight[C];                                   // of this CTA's part and the others'; 0: not counted
+            const unsigned char* part = nullptr;               // the others', kPartBytes each
+            if constexpr (C > 1) {
+                // The row groups are shared out over the cluster; a CTA sends its part of the others' groups through
+                // the shared memory that queries, keys and values had, and joins the parts of its own.
+                constexpr int kOwn = kGroups / C;
+                const int rank = static_cast<int>(blockIdx.x) % C, owner = warp / kOwn, group = warp % kOwn;
+                cluster_sync_all();                            // no CTA of the cluster uses it for them any more
+                synced = true;
+                unsigned char* recv = qs + (kGroups - kOwn) * kPartBytes;
+                if (owner != rank) {
+                    unsigned char* send = qs + (owner < rank ? warp : warp - kOwn) * kPartBytes;
+                    if (n > 0) {
+#pragma unroll 1
+                        for (int cc = 0; cc < 128; cc += 32) {
+                            uint32_t o[32];
+                            ptx::tmem_ld_32x32b_x32(o_addr + cc, o);
+                            ptx::tmem_wait_ld();
+#pragma unroll
+                            for (int e = 0; e < 8; ++e)
+                                *reinterpret_cast<uint4*>(send + lane * 512 + (((cc / 4 + e) ^ lane) << 4)) =
+                                    make_uint4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+                        }
+                        ptx::tc_fence_before_sync();
+                    }
+                    *reinterpret_cast<float*>(send + 16384 + lane * 4) = m2;
+                    *reinterpret_cast<float*>(send + 16512 + lane * 4) = l_run;
+                    ptx::fence_proxy_async_smem();
+                    __syncwarp();
+                    if (elect_one())
+                        bulk_to_peer(map_to_rank(ptx::smem_addr(recv) + (group * (C - 1) + (rank < owner ? rank : rank - 1)) * kPartBytes,
+                                                 owner),
+                                     ptx::smem_addr(send), kPartBytes, map_to_rank(ptx::smem_addr(&bar.joined[group]), owner));
+                    done();
+                    continue;
+                }
+                part = recv + group * (C - 1) * kPartBytes;
+                if (!ptx::mbar_wait(&bar.joined[group], 0, deadline)) timed_out = true;
+                timed_out = __any_sync(0xffffffffu, timed_out);
+                if (timed_out) break;
+                float pm[C], pl[C], top = l_run > 0.0f ? m2 : -INFINITY;
+                pm[0] = m2;
+                pl[0] = l_run;
+#pragma unroll
+                for (int p = 1; p < C; ++p) {
+                    pm[p] = *reinterpret_cast<const float*>(part + (p - 1) * kPartBytes + 16384 + lane * 4);
+                    pl[p] = *reinterpret_cast<const float*>(part + (p - 1) * kPartBytes + 16512 + lane * 4);
+                    if (pl[p] != 0.0f) top = fmaxf(top, pm[p]);
+                }
+                if (!(l_run > 0.0f) && l_run != 0.0f) top = fmaxf(top, m2);   // NaN sums count, too
+                l_all = 0.0f;
+#pragma unroll
+                for (int p = 0; p < C; ++p) {
+                    weight[p] = pl[p] == 0.0f ? 0.0f : exp2f(pm[p] - top);
+                    if (weight[p] != 0.0f) l_all = fmaf(weight[p], pl[p], l_all);
+                }
+                m2 = top;
+            }
+            const float inv = l_all == 0.0f ? 0.0f : 1.0f / l_all;
+            const bool none = C > 1 ? l_all == 0.0f : n == 0 || vis == 0;   // sees nothing: 0 (O may hold 0 x NaN)
             uint16_t* dst = out + static_cast<int64_t>(w.h) * out_head + (lane & 7) * 8;
             const int rows0 = row0 + (warp & 3) * 32 + (lane >> 3) * 8;   // rows this lane writes: rows0 .. + 7
 #pragma unroll 1
@@ -599,6 +692,24 @@ dense_mla_prefill_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_
                     if (n > 0) {
                         ptx::tmem_ld_32x32b_x32(o_addr + cc + 32 * hh, o);
                         ptx::tmem_wait_ld();
+                    }
+                    if constexpr (C > 1) {
+#pragma unroll
+                        for (int e = 0; e < 32; ++e)
+                            o[e] = weight[0] == 0.0f ? 0u : __float_as_uint(__uint_as_float(o[e]) * weight[0]);
+#pragma unroll
+                        for (int p = 1; p < C; ++p) {
+                            if (weight[p] == 0.0f) continue;
+#pragma unroll
+                            for (int e = 0; e < 8; ++e) {
+                                const float4 x = *reinterpret_cast<const float4*>(
+                                    part + (p - 1) * kPartBytes + lane * 512 + (((cc / 4 + 8 * hh + e) ^ lane) << 4));
+                                o[4 * e] = __float_as_uint(fmaf(weight[p], x.x, __uint_as_float(o[4 * e])));
+                                o[4 * e + 1] = __float_as_uint(fmaf(weight[p], x.y, __uint_as_float(o[4 * e + 1])));
+                                o[4 * e + 2] = __float_as_uint(fmaf(weight[p], x.z, __uint_as_float(o[4 * e + 2])));
+                                o[4 * e + 3] = __float_as_uint(fmaf(weight[p], x.w, __uint_as_float(o[4 * e + 3])));
+                            }
+                        }
                     }
 #pragma unroll
                     for (int e = 0; e < 16; ++e)
@@ -636,17 +747,58 @@ dense_mla_prefill_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_
             }
             if (row < w.nq && lse_out != nullptr)
                 lse_out[static_cast<int64_t>(w.q0 + row) * H + w.h] =
-                    l_run == 0.0f ? -INFINITY : (m_run * cs + log2f(l_run)) * kLn2;
+                    l_all == 0.0f ? -INFINITY : (m2 + log2f(l_all)) * kLn2;
             done();
         }
     }
     if (timed_out) raise_error(err, DSA_DEVERR_TIMEOUT);
+    if constexpr (C > 1) {
+        __syncwarp();
+        if (!synced) cluster_sync_all();
+        cluster_sync_all();                                    // the parts sent have arrived: shared memory may go
+    }
     ptx::tc_fence_before_sync();
     __syncthreads();
     if (warp == kMmaWarp) {
         ptx::tc_fence_after_sync();
         ptx::tmem_dealloc(tmem, 512);
     }
+}
+
+struct Plan {
+    int split;               // CTAs per item
+    int group;               // heads whose items are taken longest first
+};
+
+// Both from the lengths of an average request.  Splitting an item's keys pays where items are few and of like
+// length: a call takes about as many steps of a key tile (1.7 us) as its longest CTA, and an item on a cluster of
+// 2 or 4 takes a launch and a join as long as 4 or 8 of them (1000 queries after 15001 keys, CTAs per item 1, 2
+// and 4: 8 heads 211, 115 and 66 us; 16 heads 214, 115 and 130; 128 heads 850, 790 and 945).  Items of unlike
+// length (a prompt without earlier keys) balance by themselves, the long ones of a group first, unless there are
+// fewer than CTAs; a group is as large as the keys and values of its heads stay in L2 (8K prompt, 128 heads: single
+// heads 1.66 ms, 22 at a time 1.58, all at once 1.83).  Items of like length go head by head.
+Plan make_plan(int64_t T, int64_t S, int64_t B, int64_t H, int64_t blocks, bool causal) {
+    const int64_t sms = device_sm_count(), queries = (T + B - 1) / B, keys = std::max<int64_t>(1, (S + B - 1) / B);
+    const double longest = static_cast<double>(keys) / kTileK;
+    const double mean = longest - (causal ? static_cast<double>(std::min(queries, keys)) / (2 * kTileK) : 0.0);
+    const bool alike = mean > 0.75 * longest;
+    const int64_t items = (queries + kBlockQ - 1) / kBlockQ * B * H;
+    const double alone = alike ? static_cast<double>((items + sms - 1) / sms) * longest
+                               : std::max(longest, static_cast<double>(items) * mean / static_cast<double>(sms) + longest / 5);
+    int best = 1;
+    double least = 0.95 * alone;
+    for (int c = 2; c <= kMaxSplit; c *= 2) {
+        // clusters at a time; of four, 36 fit the 152 SMs (they do not span groups of SMs)
+        const int64_t fit = std::max<int64_t>(1, c == 2 ? sms / 2 : sms / 4 - 2), waves = (blocks * H + fit - 1) / fit;
+        if (!alike && waves > 1) continue;
+        const double steps = static_cast<double>(waves) * (longest / c + 2 * c);
+        if (steps < least) {
+            best = c;
+            least = steps;
+        }
+    }
+    const int64_t most = std::max<int64_t>(1, kGroupBytes / (keys * 512)), groups = (H + most - 1) / most;
+    return Plan{best, alike ? 1 : static_cast<int>((H + groups - 1) / groups)};   // groups of equal size
 }
 
 bool strides_ok(int64_t row, int64_t head, int64_t heads, int64_t width) {
@@ -700,13 +852,27 @@ extern "C" dsa_status dsa_dense_mla_prefill(const void* q_bf16, int64_t q_row_st
         !attn::encode_bf16_3d(encode, &vmap, keys ? v_bf16 : q_bf16, 128, H, keys ? S : T,
                               keys ? v_head_stride : q_head_stride, keys ? v_row_stride : q_row_stride, 64, kTileK))
         return DSA_ERR_CUDA;
-    if (cudaFuncSetAttribute(dense_mla_prefill_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             static_cast<int>(kPreSmem)) != cudaSuccess)
+    // at least the sum of the requests' blocks (ceil(n / 256) <= (n + 255) / 256 each)
+    const int64_t blocks = (T + (kBlockQ - 1) * static_cast<int64_t>(std::min(B, T))) / kBlockQ;
+    const bool causal = (flags & DSA_CAUSAL) != 0;
+    const Plan plan = make_plan(T, S, B, H, blocks, causal);
+    const int split = plan.split;
+    auto kernel = split == 1 ? dense_mla_prefill_kernel<1> : split == 2 ? dense_mla_prefill_kernel<2> : dense_mla_prefill_kernel<4>;
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kPreSmem)) != cudaSuccess)
         return DSA_ERR_CUDA;
-    const int64_t blocks = T / kBlockQ + std::min<int64_t>(B, T);   // >= the sum of the requests' blocks
-    dense_mla_prefill_kernel<<<dim3(static_cast<unsigned>(blocks), static_cast<unsigned>(H)), kPreThreads, kPreSmem,
-                               static_cast<cudaStream_t>(stream)>>>(
-        qmap, kmap, pmap, vmap, cu_q, cu_k, B, T, S, H, scale, (flags & DSA_CAUSAL) ? 1 : 0,
-        static_cast<uint16_t*>(out_bf16), out_row_stride, out_head_stride, lse, dev_err);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(blocks * split), static_cast<unsigned>(H));
+    cfg.blockDim = dim3(kPreThreads);
+    cfg.dynamicSmemBytes = kPreSmem;
+    cfg.stream = static_cast<cudaStream_t>(stream);
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = static_cast<unsigned>(split);
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = split > 1 ? 1 : 0;
+    if (cudaLaunchKernelEx(&cfg, kernel, qmap, kmap, pmap, vmap, cu_q, cu_k, B, T, S, H, scale, causal ? 1 : 0, plan.group,
+                           static_cast<uint16_t*>(out_bf16), out_row_stride, out_head_stride, lse, dev_err) != cudaSuccess)
+        return DSA_ERR_CUDA;
     return launch_status();
 }

@@ -752,3 +752,60 @@ def test_prefill_items_of_every_shape_after_one_another(causal):
     q, kv, lat = _prefill_inputs(q_lens, k_lens, 24, 74)
     out, lse = _prefill(q, kv, lat, q_lens, k_lens, causal)
     ref.check(out, lse, ref.prefill(q, kv[..., :128], lat[:, 512:], kv[..., 128:], q_lens, k_lens, SCALE, causal))
+
+
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("H,q_lens,k_lens", [
+    (2, [40], [3000]), (40, [10], [2500]), (1, [1], [5000]), (1, [4000], [4000]), (2, [1500], [1500]),
+    (3, [300, 1, 7], [2000, 6000, 1]),              # parts without a key tile beside long ones
+    (2, [500, 3, 0, 2], [400, 9000, 30, 0]),        # rows that see nothing, no rows, no keys
+    (16, [1000], [4100]), (9, [257], [2561]),
+])
+def test_prefill_keys_split_over_a_cluster(H, q_lens, k_lens, causal):
+    """Few items with many keys: several CTAs share an item's keys and join their parts."""
+    q, kv, lat = _prefill_inputs(q_lens, k_lens, H, 800 + sum(k_lens), extra=5)
+    T, S = sum(q_lens), sum(k_lens)
+    kv[S:], lat[S:] = math.nan, math.nan
+    err = _err()
+    out, lse = _prefill(q, kv, lat, q_lens, k_lens, causal, err)
+    assert capi.dsa_read_device_error(err) == (0, 0)
+    assert bool((out[T:] == 7.0).all()) and bool((lse[T:] == 7.0).all())
+    ref.check(out[:T], lse[:T], ref.prefill(q[:T], kv[:S, :, :128], lat[:S, 512:], kv[:S, :, 128:], q_lens, k_lens, SCALE,
+                                            causal))
+
+
+def test_prefill_split_keys_extreme_scores_graph_and_streams():
+    """Parts whose maxima are far apart; the same bits again, on two streams at once and from a graph."""
+    q_lens, k_lens = [70], [4000]
+    q, kv, lat = _prefill_inputs(q_lens, k_lens, 3, 91)
+    kv[1000:2000, :, :128] *= 30
+    kv[3500:, :, :128] = 0
+    lat[3500:, 512:] = 0
+    out, lse = _prefill(q, kv, lat, q_lens, k_lens)
+    ref.check(out, lse, ref.prefill(q, kv[..., :128], lat[:, 512:], kv[..., 128:], q_lens, k_lens, SCALE, True))
+    cu, ck = _i32(_cum(q_lens)), _i32(_cum(k_lens))
+
+    def call(o, l):
+        capi.dsa_dense_mla_prefill(q, kv[..., :128], lat[:, 512:], kv[..., 128:], cu, ck, SCALE, o, lse=l)
+
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    outs = [(torch.zeros_like(out), torch.zeros_like(lse)) for _ in streams]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for s, (o, l) in zip(streams, outs):
+            with torch.cuda.stream(s):
+                call(o, l)
+    torch.cuda.synchronize()
+    for o, l in outs:
+        assert torch.equal(o, out) and torch.equal(l, lse)
+    o, l = torch.zeros_like(out), torch.zeros_like(lse)
+    with torch.cuda.stream(streams[0]):
+        call(o, l)
+        streams[0].synchronize()
+        gr = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(gr, stream=streams[0]):
+            call(o, l)
+    o.zero_()
+    gr.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(o, out) and torch.equal(l, lse)
