@@ -28,8 +28,8 @@
 // directly; the pieces of the others go to the workspace and the combine kernel joins them.
 //
 // Measured (128 heads, one new token): 64 requests of 4K to 64K 351 us (5.4 TB/s, 80 % of the copy rate; 326 us with
-// every load in L2, where the issue of the scores bounds it); 32 of 8192 84.5 us (12 of them the combine); 1 of
-// 4096 21 us, 1 of 64 15 us (the chain of one row tile); 8 of about 128K with two rows of 16 heads 172 us (88 %).
+// every load in L2, where the issue of the scores bounds it); 32 of 8192 83 us (11 of them the combine); 1 of
+// 4096 20.6 us, 1 of 64 15 us (the chain of one row tile); 8 of about 128K with two rows of 16 heads 172 us (88 %).
 //
 // Roles (384 threads), warps 10 and 11 idle:
 //   rank 0  warps 0-7  softmax: rows (tensor-memory lanes) 32 (w % 4) .. + 31, page w / 4 of the tile; queries
@@ -916,10 +916,68 @@ dense_mla_decode_kernel(const __grid_constant__ CUtensorMap kvmap, const __grid_
     cluster_sync_all();   // neither CTA leaves while its peer may still signal or write into it
 }
 
-// Joins the pieces of the split row tiles: one warp per (output row, 128 of its 512 dims).  The first
-// piece lies in slot 2 c0 + 1, the following ones in slots 2 (c0 + 1), .., 2 c.
+// Joins the pieces of the split row tiles.  The first piece lies in slot 2 c0 + 1, the following ones in slots
+// 2 (c0 + 1), .., 2 c.  Bound by the latency of its loads: a task is 128 dims of an output row, four pieces at a
+// time, when there are few rows, and a whole row, two pieces at a time, when there are many (512 requests of 512
+// keys 116 -> 112 us, 32 of 8192 84.1 -> 83.0; without this kernel 98 and 73).
 constexpr int kCombThreads = 256;
 constexpr int kCombBlocks = 4;     // per SM (32 requests of 8K: 1 block an SM 33 us of the call, 2 to 8 about 15)
+
+// V x 128 dims from d0 on of one row, P pieces at a time: their sums and values are loaded together.
+template <int V, int P>
+__device__ __forceinline__ void join_row(const float* __restrict__ part_o, const float* __restrict__ part_lse,
+                                         const Meta& m, int c, int slot_rows, int row, int d0, int lane,
+                                         uint16_t* __restrict__ out, float* __restrict__ lse_out) {
+    const int n = c - m.first_cluster + 1;
+    auto slot_of = [&](int j) {
+        return static_cast<int64_t>(j == 0 ? 2 * m.first_cluster + 1 : 2 * (m.first_cluster + j)) * slot_rows + row;
+    };
+    float m_run = -INFINITY, tot = 0.0f;
+    float4 acc[V];
+#pragma unroll
+    for (int v = 0; v < V; ++v) acc[v] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    for (int j0 = 0; j0 < n; j0 += P) {
+        float l[P];
+        float4 o[P][V];
+#pragma unroll
+        for (int i = 0; i < P; ++i) {
+            const int64_t s = slot_of(min(j0 + i, n - 1));
+            l[i] = j0 + i < n ? part_lse[s] : -INFINITY;
+#pragma unroll
+            for (int v = 0; v < V; ++v) o[i][v] = *reinterpret_cast<const float4*>(part_o + s * kValueDim + d0 + v * 128 + lane * 4);
+        }
+        float top = m_run;
+#pragma unroll
+        for (int i = 0; i < P; ++i) top = fmaxf(top, l[i]);
+        const float ref = top == -INFINITY ? 0.0f : top;                 // nothing visible so far: weights 0
+        const float f = exp2f(m_run - ref);
+#pragma unroll
+        for (int v = 0; v < V; ++v) acc[v] = make_float4(acc[v].x * f, acc[v].y * f, acc[v].z * f, acc[v].w * f);
+        tot *= f;
+        m_run = top;
+#pragma unroll
+        for (int i = 0; i < P; ++i) {
+            const float w = exp2f(l[i] - ref);
+            if (w == 0.0f) continue;                                     // its values do not count
+            tot += w;
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                acc[v].x = fmaf(w, o[i][v].x, acc[v].x);
+                acc[v].y = fmaf(w, o[i][v].y, acc[v].y);
+                acc[v].z = fmaf(w, o[i][v].z, acc[v].z);
+                acc[v].w = fmaf(w, o[i][v].w, acc[v].w);
+            }
+        }
+    }
+    const float inv = tot == 0.0f ? 0.0f : 1.0f / tot;
+#pragma unroll
+    for (int v = 0; v < V; ++v)
+        *reinterpret_cast<uint2*>(out + (m.out_row + row) * kValueDim + d0 + v * 128 + lane * 4) =
+            make_uint2(pack_bf16x2(acc[v].x * inv, acc[v].y * inv), pack_bf16x2(acc[v].z * inv, acc[v].w * inv));
+    if (lse_out != nullptr && d0 == 0 && lane == 0)
+        lse_out[m.out_row + row] = tot == 0.0f ? -INFINITY : (m_run + log2f(tot)) * kLn2;
+}
+
 __global__ void __launch_bounds__(kCombThreads)
 dense_mla_combine_kernel(const float* __restrict__ part_o, const float* __restrict__ part_lse,
                          const Meta* __restrict__ meta, int clusters, int slot_rows, uint16_t* __restrict__ out,
@@ -931,7 +989,7 @@ dense_mla_combine_kernel(const float* __restrict__ part_o, const float* __restri
     ptx::griddep_wait();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int nwarps = gridDim.x * (kCombThreads / 32);
-    int at = blockIdx.x * (kCombThreads / 32) + warp;                 // this warp's next task, counted over all row tiles
+    const int first = blockIdx.x * (kCombThreads / 32) + warp;
     for (int c0 = 0; c0 < clusters; c0 += kCombThreads) {
         Meta own{0, 0, 0};
         if (c0 + static_cast<int>(threadIdx.x) < clusters) own = meta[c0 + threadIdx.x];
@@ -949,50 +1007,15 @@ dense_mla_combine_kernel(const float* __restrict__ part_o, const float* __restri
             list_c[j] = c0 + threadIdx.x;
         }
         __syncthreads();
+        const bool many = total * slot_rows >= nwarps;
+        int at = first;                                                   // this warp's next task, counted over the list
         for (int li = 0; li < total; ++li) {
             const Meta m = list[li];
             const int c = list_c[li];
-            const int tasks = m.rows * 4;
+            const int tasks = many ? m.rows : m.rows * 4;
             for (; at < tasks; at += nwarps) {
-                const int row = at >> 2, d0 = (at & 3) * 128 + lane * 4;
-                const int n = c - m.first_cluster + 1;
-                auto slot_of = [&](int j) {
-                    return static_cast<int64_t>(j == 0 ? 2 * m.first_cluster + 1 : 2 * (m.first_cluster + j)) * slot_rows + row;
-                };
-                // one pass, four pieces at a time: their sums and values are loaded together
-                float m_run = -INFINITY, tot = 0.0f;
-                float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-                for (int j0 = 0; j0 < n; j0 += 4) {
-                    float l[4];
-                    float4 o[4];
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const int64_t s = slot_of(min(j0 + i, n - 1));
-                        l[i] = j0 + i < n ? part_lse[s] : -INFINITY;
-                        o[i] = *reinterpret_cast<const float4*>(part_o + s * kValueDim + d0);
-                    }
-                    const float top = fmaxf(fmaxf(fmaxf(l[0], l[1]), fmaxf(l[2], l[3])), m_run);
-                    const float ref = top == -INFINITY ? 0.0f : top;     // nothing visible so far: weights 0
-                    const float f = exp2f(m_run - ref);
-                    acc = make_float4(acc.x * f, acc.y * f, acc.z * f, acc.w * f);
-                    tot *= f;
-                    m_run = top;
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const float w = exp2f(l[i] - ref);
-                        if (w == 0.0f) continue;                         // its values do not count
-                        tot += w;
-                        acc.x = fmaf(w, o[i].x, acc.x);
-                        acc.y = fmaf(w, o[i].y, acc.y);
-                        acc.z = fmaf(w, o[i].z, acc.z);
-                        acc.w = fmaf(w, o[i].w, acc.w);
-                    }
-                }
-                const float inv = tot == 0.0f ? 0.0f : 1.0f / tot;
-                *reinterpret_cast<uint2*>(out + (m.out_row + row) * kValueDim + d0) =
-                    make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
-                if (lse_out != nullptr && (at & 3) == 0 && lane == 0)
-                    lse_out[m.out_row + row] = tot == 0.0f ? -INFINITY : (m_run + log2f(tot)) * kLn2;
+                if (many) join_row<4, 2>(part_o, part_lse, m, c, slot_rows, at, 0, lane, out, lse_out);
+                else join_row<1, 4>(part_o, part_lse, m, c, slot_rows, at >> 2, (at & 3) * 128, lane, out, lse_out);
             }
             at -= tasks;
         }
