@@ -609,27 +609,30 @@ def _opt(t: Optional[torch.Tensor], dtype, dev: int, name: str) -> Optional[int]
 def _dense_rows(t: torch.Tensor, dtype, width: int, dev: int, name: str):
     """(address, rows, row stride) of a [rows, width] tensor whose rows are dense and may be strided; a
     single row's stride is never used, so its width stands in for it."""
-    if t.dtype is not dtype or t.get_device() != dev or t.dim() != 2:
-        _need(t.dim() == 2, f"{name} must have two dimensions")
+    shape = t.shape
+    if t.dtype is not dtype or t.get_device() != dev or len(shape) != 2:
+        _need(len(shape) == 2, f"{name} must have two dimensions")
         _bad(t, dtype, dev, name)
-    rows, cols = t.shape
-    if cols != width or (width > 1 and t.stride(1) != 1):
+    rows, cols = shape
+    stride, inner = t.stride()
+    if cols != width or (width > 1 and inner != 1):
         raise ValueError(f"{name} must be [rows, {width}] with dense rows")
-    return t.data_ptr(), rows, (t.stride(0) if rows > 1 else width)
+    return t.data_ptr(), rows, (stride if rows > 1 else width)
 
 
 def _th(t: torch.Tensor, width: int, dev: int, name: str):
-    """(address, row stride, head stride) of a [rows, H, width] bf16 view whose last dim is dense; the
-    stride of an axis of length 1 is never used and a dense one stands in for it."""
+    """(address, row stride, head stride, rows, H) of a [rows, H, width] bf16 view whose last dim is dense;
+    the stride of an axis of length 1 is never used and a dense one stands in for it."""
     if t.dtype is not torch.bfloat16 or t.get_device() != dev:
         _bad(t, torch.bfloat16, dev, name)
-    if t.dim() != 3 or t.shape[2] != width or t.stride(2) != 1:
+    shape, strides = t.shape, t.stride()
+    if len(shape) != 3 or shape[2] != width or strides[2] != 1:
         raise ValueError(f"{name} must be [rows, H, {width}], last dim dense")
-    rows, heads, _ = t.shape
-    rs, hs, _ = t.stride()
+    rows, heads, _ = shape
+    rs, hs, _ = strides
     if heads <= 1:
         hs = width
-    return t.data_ptr(), (rs if rows > 1 else max(width, hs * heads)), hs
+    return t.data_ptr(), (rs if rows > 1 else max(width, hs * heads)), hs, rows, heads
 
 
 # the current stream's handle without building a Stream object (3 us)
@@ -667,11 +670,13 @@ def dsa_store_latent_prologue(kv_a: torch.Tensor, norm_weight: torch.Tensor, eps
     err = _opt(dev_err, torch.int32, dev, "dev_err")
     if norm_weight.numel() != VALUE_DIM:
         raise ValueError("norm_weight must have 512 entries")
-    if cos_sin_cache.dim() != 2 or cos_sin_cache.shape[1] != 64:
+    table = cos_sin_cache.shape
+    if len(table) != 2 or table[1] != 64:
         raise ValueError("cos_sin_cache must be [max_position, 64]")
     if positions.numel() != n or slot_mapping.numel() != n:
         raise ValueError("positions / slot_mapping must have n entries")
-    if kv_pool.dim() != 3 or kv_pool.shape[1] != 64 or kv_pool.shape[2] != LATENT_DIM:
+    pages = kv_pool.shape
+    if len(pages) != 3 or pages[1] != 64 or pages[2] != LATENT_DIM:
         raise ValueError("kv_pool must be [pages, 64, 576]")
     out, out_stride = None, LATENT_DIM
     if latent_out is not None:
@@ -679,7 +684,7 @@ def dsa_store_latent_prologue(kv_a: torch.Tensor, norm_weight: torch.Tensor, eps
         if rows != n:
             raise ValueError("latent_out must be [n, 576]")
     _check("dsa_store_latent_prologue", _lib.dsa_store_latent_prologue(
-        src, stride, w, eps, cs, cos_sin_cache.shape[0], pos, slots, n, pool, kv_pool.shape[0], out, out_stride, flags,
+        src, stride, w, eps, cs, table[0], pos, slots, n, pool, pages[0], out, out_stride, flags,
         err, _raw_stream(stream, dev)))
     _count(1 if n > 0 else 0)
 
@@ -691,22 +696,21 @@ def dsa_dense_mla_prefill(q: torch.Tensor, k_nope: torch.Tensor, k_pe: torch.Ten
     """Expanded latent attention of ragged prompts: q [T, H, 192], k_nope / v [S, H, 128], k_pe [S, 64]
     (all may be strided views, e.g. of one [S, H, 256] up-projection), out [T, H, 128], lse [T, H]."""
     dev = _current_device()
-    qp, q_row, q_head = _th(q, 192, dev, "q")
-    kp, k_row, k_head = _th(k_nope, 128, dev, "k_nope")
-    vp, v_row, v_head = _th(v, 128, dev, "v")
-    op, o_row, o_head = _th(out, 128, dev, "out")
+    qp, q_row, q_head, T, H = _th(q, 192, dev, "q")
+    kp, k_row, k_head, k_rows, k_heads = _th(k_nope, 128, dev, "k_nope")
+    vp, v_row, v_head, v_rows, v_heads = _th(v, 128, dev, "v")
+    op, o_row, o_head, o_rows, o_heads = _th(out, 128, dev, "out")
     pep, S, pe_row = _dense_rows(k_pe, torch.bfloat16, 64, dev, "k_pe")
     cq = _arr(cu_q, torch.int32, dev, "cu_q")
     ck = _arr(cu_k, torch.int32, dev, "cu_k")
     lp = _opt(lse, torch.float32, dev, "lse")
     err = _opt(dev_err, torch.int32, dev, "dev_err")
-    T, H, _ = q.shape
     B = cu_q.numel() - 1
     if B < 0 or cu_k.numel() != B + 1:
         raise ValueError("cu_q and cu_k must have B + 1 entries")
-    if k_nope.shape[:2] != (S, H) or v.shape[:2] != (S, H):
+    if k_rows != S or v_rows != S or k_heads != H or v_heads != H:
         raise ValueError("k_nope and v must be [S, H, 128], k_pe [S, 64]")
-    if out.shape[:2] != (T, H) or (lse is not None and lse.shape != (T, H)):
+    if o_rows != T or o_heads != H or (lse is not None and lse.shape != (T, H)):
         raise ValueError("out must be [T, H, 128], lse [T, H]")
     _check("dsa_dense_mla_prefill", _lib.dsa_dense_mla_prefill(
         qp, q_row, q_head, kp, k_row, k_head, pep, pe_row, vp, v_row, v_head, cq, ck, B, T, S, H, scale,
@@ -734,13 +738,14 @@ def dsa_dense_mla_decode(q_bf16: torch.Tensor, kv_pool: torch.Tensor, block_tabl
     op = _arr(out, torch.bfloat16, dev, "out")
     lp = _opt(lse, torch.float32, dev, "lse")
     err = _opt(dev_err, torch.int32, dev, "dev_err")
-    if q_bf16.dim() != 3 or q_bf16.shape[2] != LATENT_DIM:
+    shape, pages, rows = q_bf16.shape, kv_pool.shape, block_table.shape
+    if len(shape) != 3 or shape[2] != LATENT_DIM:
         raise ValueError("q_bf16 must be [T, H, 576]")
-    T, H, _ = q_bf16.shape
+    T, H, _ = shape
     B = seq_lens.numel()
-    if kv_pool.dim() != 3 or kv_pool.shape[1] != 64 or kv_pool.shape[2] != LATENT_DIM:
+    if len(pages) != 3 or pages[1] != 64 or pages[2] != LATENT_DIM:
         raise ValueError("kv_pool must be [pages, 64, 576]")
-    if cu_q.numel() != B + 1 or block_table.dim() != 2 or block_table.shape[0] != B:
+    if cu_q.numel() != B + 1 or len(rows) != 2 or rows[0] != B:
         raise ValueError("cu_q must have B + 1 entries, block_table B rows")
     if out.shape != (T, H, VALUE_DIM) or (lse is not None and lse.shape != (T, H)):
         raise ValueError("out must be [T, H, 512], lse [T, H]")
@@ -751,7 +756,7 @@ def dsa_dense_mla_decode(q_bf16: torch.Tensor, kv_pool: torch.Tensor, block_tabl
     elif workspace.get_device() != dev or not workspace.is_contiguous():
         raise ValueError("workspace must be a contiguous CUDA tensor on the current device")
     _check("dsa_dense_mla_decode", _lib.dsa_dense_mla_decode(
-        qp, pool, kv_pool.shape[0], table, block_table.shape[1], lens, cq, B, T, H, scale, op, lp,
+        qp, pool, pages[0], table, rows[1], lens, cq, B, T, H, scale, op, lp,
         workspace.data_ptr(), workspace.numel() * workspace.element_size(), err, _raw_stream(stream, dev)))
     _count(2 if T > 0 and B > 0 else 0)   # the attention and the joining of its pieces
 
