@@ -622,7 +622,11 @@ dense_mla_decode_kernel(const __grid_constant__ CUtensorMap kvmap, const __grid_
         do {
             const int live = w.rt.tokens * bt.H;
             const bool quad_live = quad * 32 < live;
-            const int vis = min(w.rt.vis0 + token, bt.max_pages * kPage);
+            // Rows behind the last one are other requests' queries, stale P and its products: nothing reads what comes
+            // of them, but zeros there let the tensor cores idle, and a long call runs at the power limit (8 requests of
+            // about 128K with two rows of 16 heads, one call after the other: 200 -> 178 us at 1.47 -> 1.78 GHz)
+            const bool row_live = row < live;
+            const int vis = row_live ? min(w.rt.vis0 + token, bt.max_pages * kPage) : 0;
             float m_run = -INFINITY, l_run = 0.0f;
             if (w.t0 < w.t1) {
                 // the row tile's queries out of the ring: value chunks into tensor memory, the rope chunk into its
@@ -639,14 +643,18 @@ dense_mla_decode_kernel(const __grid_constant__ CUtensorMap kvmap, const __grid_
 #pragma unroll
                             for (int i = 0; i < 8; ++i) {
                                 const uint4 r = *reinterpret_cast<const uint4*>(src + ((i ^ p_swz) << 4));
-                                v[4 * i] = r.x; v[4 * i + 1] = r.y; v[4 * i + 2] = r.z; v[4 * i + 3] = r.w;
+                                v[4 * i] = row_live ? r.x : 0u;
+                                v[4 * i + 1] = row_live ? r.y : 0u;
+                                v[4 * i + 2] = row_live ? r.z : 0u;
+                                v[4 * i + 3] = row_live ? r.w : 0u;
                             }
                             __syncwarp();
                             tmem_st_x32(tmem + lane_base + c * 32, v);
                         } else {
 #pragma unroll
                             for (int i = 0; i < 8; ++i)              // the same swizzle in both places
-                                *reinterpret_cast<uint4*>(qrope + p_row + 16 * i) = *reinterpret_cast<const uint4*>(src + 16 * i);
+                                *reinterpret_cast<uint4*>(qrope + p_row + 16 * i) =
+                                    row_live ? *reinterpret_cast<const uint4*>(src + 16 * i) : make_uint4(0u, 0u, 0u, 0u);
                             ptx::fence_proxy_async_smem();
                         }
                         __syncwarp();
@@ -782,11 +790,20 @@ dense_mla_decode_kernel(const __grid_constant__ CUtensorMap kvmap, const __grid_
             if (!ptx::mbar_wait(b, parity, deadline)) timed_out = true;
         };
         uint32_t u = 0, seg = 0, used = 0;                           // used: ring stages before this row tile
+        bool clean = false;                                          // this row group's P buffers are zero
         Walk w(bt, bar.start);
         do {
             const int live = w.rt.tokens * bt.H;
             const bool quad_live = quad * 32 < live, has_tiles = w.t0 < w.t1;
             const uint32_t quads = static_cast<uint32_t>((live + 31) / 32);
+            if (quad_live) {
+                clean = false;
+            } else if (has_tiles && !clean) {                        // no P comes for these rows (their products before are done)
+                clean = true;
+                for (int e = lane; e < 2 * 256; e += 32)
+                    *reinterpret_cast<uint4*>(ps + (2 * dh + (e >> 8)) * kPBytes + quad * 4096 + (e & 255) * 16) = make_uint4(0u, 0u, 0u, 0u);
+                ptx::fence_proxy_async_smem();
+            }
             for (int t = w.t0; t < w.t1; ++t, ++u) {
                 if ((u & 255u) == 0u) deadline = ptx::wait_deadline();
                 const uint32_t pb = 2 * (u & 1u), pph = (u >> 1) & 1u;
