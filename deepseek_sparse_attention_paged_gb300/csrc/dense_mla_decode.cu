@@ -354,6 +354,7 @@ dense_mla_decode_kernel(const __grid_constant__ CUtensorMap kvmap, const __grid_
         ptx::tmem_alloc(&bar.tmem_slot, 512);
         ptx::tmem_relinquish();
     }
+    ptx::griddep_wait();             // a programmatic dependent: what came before is complete
     find_share(bt, cluster, clusters, reinterpret_cast<int*>(ring), bar, rank == 0 ? err : nullptr);
     ptx::fence_proxy_async_smem();   // the schedule's scratch lies where copies will land
     ptx::tc_fence_before_sync();
@@ -1004,6 +1005,7 @@ dense_mla_combine_kernel(const float* __restrict__ part_o, const float* __restri
     __shared__ Meta list[kCombThreads];
     __shared__ int list_c[kCombThreads], found[kCombThreads / 32];
     ptx::griddep_wait();
+    ptx::griddep_launch_dependents();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int nwarps = gridDim.x * (kCombThreads / 32);
     const int first = blockIdx.x * (kCombThreads / 32) + warp;
@@ -1089,21 +1091,24 @@ extern "C" dsa_status dsa_dense_mla_decode(const void* q_bf16, const void* kv_po
     if (cudaFuncSetAttribute(dense_mla_decode_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              static_cast<int>(kDecSmem)) != cudaSuccess)
         return DSA_ERR_CUDA;
-    dense_mla_decode_kernel<<<2 * clusters, kDecThreads, kDecSmem, s>>>(
-        kvmap, qmap, omap, pmap, static_cast<const uint16_t*>(kv_pool), static_cast<int>(num_pages), block_table,
-        Batch{seq_lens, cu_q, B, T, H, max_pages, kRows / H}, scale, static_cast<uint16_t*>(out_bf16), lse, part_lse, meta, slot_rows,
-        dev_err);
-    if (cudaGetLastError() != cudaSuccess) return DSA_ERR_CUDA;
-    // a programmatic dependent of the attention kernel: scheduled as its CTAs end, waits for all of it
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(2 * clusters * kCombBlocks);
-    cfg.blockDim = dim3(kCombThreads);
-    cfg.stream = s;
+    // both kernels are programmatic dependents: scheduled as the CTAs of the one before end, they wait for all of it
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(2 * clusters);
+    cfg.blockDim = dim3(kDecThreads);
+    cfg.dynamicSmemBytes = kDecSmem;
+    cfg.stream = s;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
+    if (cudaLaunchKernelEx(&cfg, dense_mla_decode_kernel, kvmap, qmap, omap, pmap, static_cast<const uint16_t*>(kv_pool),
+                           static_cast<int>(num_pages), block_table, Batch{seq_lens, cu_q, B, T, H, max_pages, kRows / H},
+                           scale, static_cast<uint16_t*>(out_bf16), lse, part_lse, meta, slot_rows, dev_err) != cudaSuccess)
+        return DSA_ERR_CUDA;
+    cfg.gridDim = dim3(2 * clusters * kCombBlocks);
+    cfg.blockDim = dim3(kCombThreads);
+    cfg.dynamicSmemBytes = 0;
     if (cudaLaunchKernelEx(&cfg, dense_mla_combine_kernel, static_cast<const float*>(part_o),
                            static_cast<const float*>(part_lse), static_cast<const Meta*>(meta), clusters, slot_rows,
                            static_cast<uint16_t*>(out_bf16), lse) != cudaSuccess)

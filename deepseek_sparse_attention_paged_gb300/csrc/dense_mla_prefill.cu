@@ -220,6 +220,7 @@ dense_mla_prefill_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_
         ptx::tmem_alloc(&bar.tmem_slot, 512);
         ptx::tmem_relinquish();
     }
+    ptx::griddep_wait();   // a programmatic dependent: what came before is complete
     ptx::tc_fence_before_sync();
     __syncthreads();
     ptx::tc_fence_after_sync();
@@ -865,12 +866,14 @@ extern "C" dsa_status dsa_dense_mla_prefill(const void* q_bf16, int64_t q_row_st
     cfg.blockDim = dim3(kPreThreads);
     cfg.dynamicSmemBytes = kPreSmem;
     cfg.stream = static_cast<cudaStream_t>(stream);
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = static_cast<unsigned>(split);
-    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = static_cast<unsigned>(split);
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = split > 1 ? 1 : 0;
+    cfg.numAttrs = split > 1 ? 2 : 1;
     if (cudaLaunchKernelEx(&cfg, kernel, qmap, kmap, pmap, vmap, cu_q, cu_k, B, T, S, H, scale, causal ? 1 : 0, plan.group,
                            static_cast<uint16_t*>(out_bf16), out_row_stride, out_head_stride, lse, dev_err) != cudaSuccess)
         return DSA_ERR_CUDA;

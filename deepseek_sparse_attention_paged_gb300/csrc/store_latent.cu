@@ -17,6 +17,7 @@
 #include <cuda_bf16.h>
 
 #include "dsa_common.cuh"
+#include "sm100_ptx.cuh"
 
 namespace dsa {
 namespace {
@@ -44,6 +45,8 @@ store_latent_prologue_kernel(const uint16_t* raw, int64_t raw_stride, const floa
                              const int64_t* __restrict__ positions, const int64_t* __restrict__ slots, int64_t n,
                              uint16_t* __restrict__ pool, int64_t num_pages, uint16_t* latent_out,
                              int64_t out_stride, int interleaved, int32_t* err) {
+    ptx::griddep_wait();                         // a programmatic dependent: what came before is complete
+    ptx::griddep_launch_dependents();            // (the next kernel waits for this one in the same way)
     const int64_t token = (static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x) >> 5;
     const int lane = threadIdx.x & 31;
     if (token >= n) return;                      // warp-uniform
@@ -142,10 +145,19 @@ extern "C" dsa_status dsa_store_latent_prologue(const void* kv_a_bf16, int64_t r
     if (num_pages > 0x7fffffffffffLL / (kPage * kLatentDim)) return DSA_ERR_UNSUPPORTED;
     const int64_t blocks = (n + kStoreThreads / 32 - 1) / (kStoreThreads / 32);
     if (blocks > 0x7fffffffLL) return DSA_ERR_INVALID_ARG;
-    store_latent_prologue_kernel<<<static_cast<unsigned>(blocks), kStoreThreads, 0,
-                                   static_cast<cudaStream_t>(stream)>>>(
-        static_cast<const uint16_t*>(kv_a_bf16), row_stride, norm_weight, eps, cos_sin_cache, max_position, positions,
-        slot_mapping, n, static_cast<uint16_t*>(kv_pool), num_pages, static_cast<uint16_t*>(latent_out),
-        out_row_stride, (flags & DSA_ROPE_INTERLEAVED) ? 1 : 0, dev_err);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(blocks));
+    cfg.blockDim = dim3(kStoreThreads);
+    cfg.stream = static_cast<cudaStream_t>(stream);
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (cudaLaunchKernelEx(&cfg, store_latent_prologue_kernel, static_cast<const uint16_t*>(kv_a_bf16), row_stride,
+                           norm_weight, eps, cos_sin_cache, max_position, positions, slot_mapping, n,
+                           static_cast<uint16_t*>(kv_pool), num_pages, static_cast<uint16_t*>(latent_out), out_row_stride,
+                           (flags & DSA_ROPE_INTERLEAVED) ? 1 : 0, dev_err) != cudaSuccess)
+        return DSA_ERR_CUDA;
     return launch_status();
 }

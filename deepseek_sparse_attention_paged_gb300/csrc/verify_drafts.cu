@@ -130,6 +130,7 @@ verify_drafts_kernel(const float* __restrict__ target, int64_t ld_t, const float
     __shared__ Sum totals[2][kVerifyCtas];        // per pass over the row: every CTA's sum
     __shared__ uint64_t totals_full[2];
     __shared__ int s_first, s_x;
+    ptx::griddep_wait();                         // a programmatic dependent: what came before is complete
     const int b = blockIdx.x / kVerifyCtas;
     const int rank = static_cast<int>(cluster_rank());
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -339,15 +340,19 @@ extern "C" dsa_status dsa_verify_drafts(const float* target_probs, int64_t targe
                      (draft_probs == nullptr || (aligned16(draft_probs) && draft_ld % 4 == 0));
     const int groups = (V + kGroup - 1) / kGroup;
     const size_t smem = static_cast<size_t>((groups + kVerifyCtas - 1) / kVerifyCtas) * sizeof(Sum);   // <= 32 KB
-    cudaStream_t s = static_cast<cudaStream_t>(stream);
-    const unsigned grid = static_cast<unsigned>(B) * kVerifyCtas;
-    if (vec)
-        verify_drafts_kernel<true><<<grid, kVerifyThreads, smem, s>>>(target_probs, target_ld, draft_probs, draft_ld, V,
-                                                                      draft_tokens, cu_q, T, accept_u, sample_u,
-                                                                      out_tokens, accepted, dev_err);
-    else
-        verify_drafts_kernel<false><<<grid, kVerifyThreads, smem, s>>>(target_probs, target_ld, draft_probs, draft_ld,
-                                                                       V, draft_tokens, cu_q, T, accept_u, sample_u,
-                                                                       out_tokens, accepted, dev_err);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(B) * kVerifyCtas);
+    cfg.blockDim = dim3(kVerifyThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = static_cast<cudaStream_t>(stream);
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (cudaLaunchKernelEx(&cfg, vec ? verify_drafts_kernel<true> : verify_drafts_kernel<false>, target_probs, target_ld,
+                           draft_probs, draft_ld, V, draft_tokens, cu_q, T, accept_u, sample_u, out_tokens, accepted,
+                           dev_err) != cudaSuccess)
+        return DSA_ERR_CUDA;
     return launch_status();
 }
