@@ -1005,7 +1005,6 @@ dense_mla_combine_kernel(const float* __restrict__ part_o, const float* __restri
     __shared__ Meta list[kCombThreads];
     __shared__ int list_c[kCombThreads], found[kCombThreads / 32];
     ptx::griddep_wait();
-    ptx::griddep_launch_dependents();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int nwarps = gridDim.x * (kCombThreads / 32);
     const int first = blockIdx.x * (kCombThreads / 32) + warp;
