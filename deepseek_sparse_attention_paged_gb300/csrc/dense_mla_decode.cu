@@ -27,9 +27,10 @@
 // one per cluster (at least kMinShare tiles).  A row tile that lies within one share is written
 // directly; the pieces of the others go to the workspace and the combine kernel joins them.
 //
-// Measured (128 heads, one new token): 64 requests of 4K to 64K 351 us (5.4 TB/s, 80 % of the copy rate; 326 us with
-// every load in L2, where the issue of the scores bounds it); 32 of 8192 83 us (11 of them the combine); 1 of
-// 4096 20.6 us, 1 of 64 15 us (the chain of one row tile); 8 of about 128K with two rows of 16 heads 172 us (88 %).
+// Measured (128 heads, one new token): 64 requests of 4K to 64K 352 us (5.4 TB/s, 80 % of the copy rate; 326 us with
+// every load in L2, where the issue of the scores bounds it; 380 to 400 one call after the other, at the power
+// limit); 32 of 8192 83 us (10 of them the combine); 1 of 4096 20.1 us, 1 of 64 15 us (the chain of one row
+// tile); 8 of about 128K with two rows of 16 heads 173 us (6.0 TB/s, 88 %).
 //
 // Roles (384 threads), warps 10 and 11 idle:
 //   rank 0  warps 0-7  softmax: rows (tensor-memory lanes) 32 (w % 4) .. + 31, page w / 4 of the tile; queries

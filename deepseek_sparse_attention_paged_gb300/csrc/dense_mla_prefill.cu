@@ -16,9 +16,9 @@
 // (512 to 1024 cycles of the special-function unit).  So a CTA holds two tiles of 128 queries of
 // one head and one request: while the softmax warps of one work, the tensor cores run the other's
 // products.  Measured: 8192 queries and keys, 19 heads, no mask 443 us (1.82 PFLOP/s; Q K^T reads both operands
-// from shared memory, 8 KB an MMA, which takes 79 cycles for 64); causal with 128 heads 1.58 ms, with 16 heads
-// 210 us; 8 prompts of 128 to 2048 358 us (84 % of their tiles' area counts); 1000 queries after 15001 keys
-// 793 us, with 16 heads 115 us.
+// from shared memory, 8 KB an MMA, which takes 79 cycles for 64); causal with 128 heads 1.60 ms (1.77 one call
+// after the other, at the power limit), with 16 heads 210 us; 8 prompts of 128 to 2048 361 us (84 % of their tiles'
+// area counts); 1000 queries after 15001 keys 785 us, with 16 heads 114 us.
 //
 // Work item: block qb of 256 query rows of request b, head h; the longest first over a group of heads whose keys
 // and values fit L2.  The grid has one block per item; a CTA
