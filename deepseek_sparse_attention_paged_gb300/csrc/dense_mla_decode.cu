@@ -792,20 +792,12 @@ dense_mla_decode_kernel(const __grid_constant__ CUtensorMap kvmap, const __grid_
             if (!ptx::mbar_wait(b, parity, deadline)) timed_out = true;
         };
         uint32_t u = 0, seg = 0, used = 0;                           // used: ring stages before this row tile
-        bool clean = false;                                          // this row group's P buffers are zero
+        uint32_t clean = 0;                                          // bit i: this row group's P is zero in buffers 2 i and 2 i + 1
         Walk w(bt, bar.start);
         do {
             const int live = w.rt.tokens * bt.H;
             const bool quad_live = quad * 32 < live, has_tiles = w.t0 < w.t1;
             const uint32_t quads = static_cast<uint32_t>((live + 31) / 32);
-            if (quad_live) {
-                clean = false;
-            } else if (has_tiles && !clean) {                        // no P comes for these rows (their products before are done)
-                clean = true;
-                for (int e = lane; e < 2 * 256; e += 32)
-                    *reinterpret_cast<uint4*>(ps + (2 * dh + (e >> 8)) * kPBytes + quad * 4096 + (e & 255) * 16) = make_uint4(0u, 0u, 0u, 0u);
-                ptx::fence_proxy_async_smem();
-            }
             for (int t = w.t0; t < w.t1; ++t, ++u) {
                 if ((u & 255u) == 0u) deadline = ptx::wait_deadline();
                 const uint32_t pb = 2 * (u & 1u), pph = (u >> 1) & 1u;
@@ -817,6 +809,16 @@ dense_mla_decode_kernel(const __grid_constant__ CUtensorMap kvmap, const __grid_
                 }
                 __syncwarp();
                 wait(&bar.p_full[pb], pph);
+                if (quad_live) {
+                    clean &= ~(1u << (u & 1u));
+                } else if (((clean >> (u & 1u)) & 1u) == 0u) {
+                    // no P comes for these rows.  Only this tile's buffers: rank 0 writes into them again when its
+                    // products are complete, into the others it may have sent the next row tile's already
+                    clean |= 1u << (u & 1u);
+                    for (int e = lane; e < 256; e += 32)
+                        *reinterpret_cast<uint4*>(ps + (pb + dh) * kPBytes + quad * 4096 + e * 16) = make_uint4(0u, 0u, 0u, 0u);
+                    ptx::fence_proxy_async_smem();
+                }
                 if (quad_live && t > w.t0) {
                     const float alpha = bar.alpha[u & 1][row];
                     if (__any_sync(0xffffffffu, alpha != 1.0f)) {

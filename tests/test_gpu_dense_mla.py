@@ -809,3 +809,28 @@ def test_prefill_split_keys_extreme_scores_graph_and_streams():
     gr.replay()
     torch.cuda.synchronize()
     assert torch.equal(o, out) and torch.equal(l, lse)
+
+
+@pytest.mark.parametrize("H,per", [(16, 8), (32, 4), (64, 2)])
+def test_decode_row_tiles_of_changing_height_after_one_another(H, per):
+    """Many short row tiles in turn in each cluster, full ones and ones with few rows in changing order, with one to
+    three key tiles: what the scores' CTA sends ahead for the next one stays."""
+    g = _gen(95 + H)
+    B = 500
+    lens = (torch.randint(1, 130, (B,), generator=g) + 128 * (torch.rand(B, generator=g) < 0.2)).tolist()
+    q_lens = torch.randint(1, 2 * per, (B,), generator=g).tolist()
+    q, pool, table = _decode_inputs(lens, q_lens, H, 96 + H)
+    want = ref.decode(q, pool, table, lens, q_lens, SCALE)
+    for _ in range(5):
+        out, lse = _decode(q, pool, table, lens, q_lens)
+        ref.check(out, lse, want)
+
+
+def test_decode_short_row_tiles_behind_ones_that_see_nothing():
+    """Row tiles of one key tile behind low ones and ones without a visible key, whose zeros take the output's CTA
+    long: P of the row tile after next is there before it has begun the next."""
+    lens = [18, 4116, 6914, 0, 1, 1805, 3, 2657, 13815, 2, 32, 66, 3977]
+    q_lens = [2, 37, 2, 38, 31, 30, 28, 21, 26, 39, 4, 24, 8]
+    q, pool, table = _decode_inputs(lens, q_lens, 32, 99)
+    out, lse = _decode(q, pool, table, lens, q_lens)
+    ref.check(out, lse, ref.decode(q, pool, table, lens, q_lens, SCALE))
