@@ -169,9 +169,9 @@ verify_drafts_kernel(const float* __restrict__ target, int64_t ld_t, const float
                 if (x >= 0) {
                     const float p = __ldg(target + static_cast<int64_t>(r0 + j) * ld_t + x);
                     const float q = draft != nullptr ? __ldg(draft + static_cast<int64_t>(r0 + j) * ld_d + x) : 1.0f;
-                    // u q < p without rounding: the product and its error
-                    const float u = __ldg(u_accept + r0 + j), uq = __fmul_rn(u, q);
-                    stop = !(uq < p || (uq == p && __fmaf_rn(u, q, -uq) < 0.0f));
+                    // u q < p without rounding: the product of two fp32 numbers is exact in fp64, subnormal ones
+                    // included (in fp32 the error of a product below 2^-102 is itself cut off)
+                    stop = !(static_cast<double>(__ldg(u_accept + r0 + j)) * static_cast<double>(q) < static_cast<double>(p));
                 }
             }
             const uint32_t m = __ballot_sync(0xffffffffu, stop);

@@ -834,3 +834,30 @@ def test_decode_short_row_tiles_behind_ones_that_see_nothing():
     q, pool, table = _decode_inputs(lens, q_lens, 32, 99)
     out, lse = _decode(q, pool, table, lens, q_lens)
     ref.check(out, lse, ref.decode(q, pool, table, lens, q_lens, SCALE))
+
+
+def test_verify_accepts_at_the_border_down_to_the_smallest_numbers():
+    """u q < p without a rounding, also where the product or its error lies below fp32's smallest numbers: p is u q
+    rounded, for random u and q of every magnitude, and the neighbours of such a p."""
+    g = _gen(63)
+    n = 4000
+    q = torch.ldexp(1 + torch.rand(n, generator=g), -torch.randint(1, 150, (n,), generator=g).float()).float()
+    u = torch.ldexp(torch.randint(1, 2 ** 24, (n,), generator=g).float(), -torch.randint(24, 40, (n,), generator=g).float())
+    q[:4] = torch.tensor([2.0 ** -126, 2.0 ** -126, 2.0 ** -126, 3 * 2.0 ** -149])
+    u[:4] = torch.tensor([0.5 - 2.0 ** -25, 0.5, 0.5 + 2.0 ** -24, 11184810 * 2.0 ** -25])
+    exact = u.double() * q.double()
+    p = exact.float()
+    step = torch.randint(-1, 2, (n,), generator=g)
+    step[:4] = 0
+    p = torch.where(step > 0, torch.nextafter(p, torch.tensor(2.0)), torch.where(step < 0, torch.nextafter(p, torch.tensor(0.0)), p))
+    V = 4
+    target, draft = torch.zeros(2 * n, V), torch.zeros(2 * n, V)
+    target[:, 2] = 1.0
+    target[0::2, 1], draft[0::2, 1] = p, q
+    tok = torch.tensor([1, -1] * n, dtype=torch.int32)
+    ua = torch.zeros(2 * n)
+    ua[0::2] = u
+    got = _verify(target, draft, tok, [2] * n, ua, torch.full((n,), 0.5))
+    wrong = torch.nonzero(torch.tensor(got[1]) != (exact < p.double()).int())[:, 0].tolist()
+    assert not wrong, f"{len(wrong)} of {n}, the first {wrong[:5]}"
+    assert got[1][:4] == [1, 0, 0, 1]
