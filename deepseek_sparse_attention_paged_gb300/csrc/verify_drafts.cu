@@ -239,7 +239,10 @@ verify_drafts_kernel(const float* __restrict__ target, int64_t ld_t, const float
         }
         if (!ptx::mbar_wait(&totals_full[pass], 0, deadline)) late = true;
         if (__syncthreads_or(late)) {            // all leave together
-            if (threadIdx.x == 0) raise_error(err, DSA_DEVERR_TIMEOUT);
+            if (threadIdx.x == 0) {              // no token, whichever CTA would have drawn it
+                out_tokens[r0 + first] = -1;
+                raise_error(err, DSA_DEVERR_TIMEOUT);
+            }
             cluster_arrive();                    // not before every CTA that may still send has left or come here
             cluster_wait();
             return;

@@ -681,7 +681,8 @@ dsa_status dsa_dense_mla_decode(const void* q_bf16, const void* kv_pool, int64_t
  *                 are left as they were.
  *   dev_err       nullable; DSA_DEVERR_INDEX_RANGE for a draft token >= V (no draft) or a cu_q range
  *                 outside [0, T] (cut to it), DSA_DEVERR_PROB for a row to draw from without mass
- *                 (the drawn token is -1).
+ *                 (the drawn token is -1), DSA_DEVERR_TIMEOUT if a bounded wait gave up (a request
+ *                 whose draw it reached has -1 as its drawn token, or the right one).
  */
 dsa_status dsa_verify_drafts(const float* target_probs, int64_t target_ld, const float* draft_probs,
                              int64_t draft_ld, int32_t V, const int32_t* draft_tokens, const int32_t* cu_q, int32_t B,

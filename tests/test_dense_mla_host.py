@@ -2,6 +2,8 @@
 call) and of the Python binding, and the plain definitions the GPU tests compare with."""
 import ctypes
 import math
+import os
+import re
 
 import pytest
 import torch
@@ -136,3 +138,15 @@ def test_verify_definition_keeps_the_target_distribution():
                 mass[out[0]] += float(q[0, x]) / (n * n)
                 assert acc[0] == (1 if out[1] >= 0 else 0)
     assert torch.allclose(mass, p[0].double(), atol=2.0 / n)
+
+
+@pytest.mark.parametrize("call,source", [("dsa_store_latent_prologue", "store_latent.cu"), ("dsa_dense_mla_prefill", "dense_mla_prefill.cu"),
+                                         ("dsa_dense_mla_decode", "dense_mla_decode.cu"), ("dsa_verify_drafts", "verify_drafts.cu")])
+def test_header_names_the_device_errors_that_a_call_raises(call, source):
+    """The comment in front of a call's declaration names exactly the error bits that its kernels set."""
+    with open(os.path.join(build.CSRC, source)) as f:
+        raised = set(re.findall(r"raise_error\([^;]*?(DSA_DEVERR_\w+)\)", f.read()))
+    with open(os.path.join(build.INCLUDE, "dsa.h")) as f:
+        header = f.read()
+    doc = header[header.index(f" * {call} -- "):header.index(f"dsa_status {call}(")]
+    assert raised and set(re.findall(r"DSA_DEVERR_\w+", doc)) == raised
