@@ -129,6 +129,10 @@ class DeviceBatch:
             self.lse = torch.empty((wl.T, wl.heads), dtype=torch.float32, device=dev)
             self.mla_ws = torch.empty(max(16, capi.dsa_sparse_mla_workspace_size(wl.T, wl.heads, wl.topk)),
                                       dtype=torch.uint8, device=dev)
+            # from the start, not at the first dense call: that one may come on another stream than the current
+            # one, whose memory torch would hand out, or inside a graph's capture, whose memory goes with the graph
+            self.dense_ws = torch.empty(max(16, capi.dsa_dense_mla_decode_workspace_size(wl.T, wl.heads)),
+                                        dtype=torch.uint8, device=dev)
             self._pack_io()
 
     # ---- packed step I/O: one contiguous device buffer for the inputs, one for the outputs
@@ -262,13 +266,10 @@ class DeviceBatch:
                                    lse=self.lse, dev_err=self.dev_err, stream=stream)
 
     def dense_mla(self, stream=None):
-        """Attention of the query rows over their whole visible context (no selection) into out / lse, with
-        a workspace of its own (allocated once)."""
-        if getattr(self, "_dense_ws", None) is None:
-            self._dense_ws = torch.empty(max(16, capi.dsa_dense_mla_decode_workspace_size(self.wl.T, self.wl.heads)),
-                                         dtype=torch.uint8, device=self.device)
+        """Attention of the query rows over their whole visible context (no selection) into out / lse.  The batch
+        has one workspace for it: one call at a time, on one stream or ordered by the caller."""
         capi.dsa_dense_mla_decode(self.mla_q, self.kv_pool, self.block_table, self.seq_lens, self.cu_q, self.wl.scale,
-                                  self.out, self._dense_ws, lse=self.lse, dev_err=self.dev_err, stream=stream)
+                                  self.out, self.dense_ws, lse=self.lse, dev_err=self.dev_err, stream=stream)
 
     def tiles(self):
         """(row_begin, row_end) of every logits row tile, in order."""

@@ -861,3 +861,53 @@ def test_verify_accepts_at_the_border_down_to_the_smallest_numbers():
     wrong = torch.nonzero(torch.tensor(got[1]) != (exact < p.double()).int())[:, 0].tolist()
     assert not wrong, f"{len(wrong)} of {n}, the first {wrong[:5]}"
     assert got[1][:4] == [1, 0, 0, 1]
+
+
+def test_device_batch_dense_attention_on_another_stream():
+    """The workspace is the batch's own from the start: a first call on a stream of its own neither waits for the
+    current stream nor takes memory that work there still uses."""
+    from deepseek_sparse_attention_paged_gb300 import workloads
+    from deepseek_sparse_attention_paged_gb300.pipeline import DeviceBatch
+    wl = workloads.make_custom("dense_on_a_stream", 262, [700, 90], 1, topk=64, heads=128)
+    db = DeviceBatch(wl, build_index_cache=False)
+    size = max(16, capi.dsa_dense_mla_decode_workspace_size(wl.T, wl.heads))
+    capi.dsa_dense_mla_decode(db.mla_q, db.kv_pool, db.block_table, db.seq_lens, db.cu_q, wl.scale, db.out)   # loaded
+    torch.cuda.synchronize()
+    torch.cuda.empty_cache()
+    a = torch.full((size,), 255, dtype=torch.uint8, device="cuda")
+    b = torch.zeros_like(a)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    torch.cuda._sleep(1_000_000_000)
+    b.copy_(a)
+    del a
+    db.dense_mla(stream=side)
+    side.synchronize()
+    torch.cuda.synchronize()
+    assert bool((b == 255).all())
+    r = ref.decode(db.mla_q, db.kv_pool, db.block_table, wl.seq_lens.tolist(), wl.q_lens.tolist(), wl.scale)
+    ref.check(db.out, db.lse, r)
+
+
+def test_device_batch_dense_attention_first_called_in_a_capture():
+    """The first dense call is a captured one: the workspace is not the graph's, and outlives it."""
+    from deepseek_sparse_attention_paged_gb300 import workloads
+    from deepseek_sparse_attention_paged_gb300.pipeline import DeviceBatch
+    wl = workloads.make("tiny")
+    db = DeviceBatch(wl, build_index_cache=False)
+    ws = db.dense_ws.data_ptr()
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        gr = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(gr, stream=s):
+            db.dense_mla()
+    gr.replay()
+    torch.cuda.synchronize()
+    r = ref.decode(db.mla_q, db.kv_pool, db.block_table, wl.seq_lens.tolist(), wl.q_lens.tolist(), wl.scale)
+    ref.check(db.out, db.lse, r)
+    del gr
+    db.out.zero_()
+    db.dense_mla()
+    ref.check(db.out, db.lse, r)
+    assert db.dense_ws.data_ptr() == ws
