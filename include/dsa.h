@@ -604,7 +604,9 @@ dsa_status dsa_store_latent_prologue(const void* kv_a_bf16, int64_t row_stride, 
  *   bf16 operands, fp32 accumulation, P rounded to bf16 for the product with v.
  *   Query rows >= cu_q[B] are left as they were; key rows >= cu_k[B] are not used (they may hold
  *   anything).  Within a request, an infinite or NaN value in v at a position that a query does not
- *   see may reach that query when it lies in the same 128-key tile as one that it does see.
+ *   see may reach that query when another query of its group of 128 (queries 128 i .. 128 i + 127 of
+ *   the request) sees a key of the same group of 128 (keys 128 j .. 128 j + 127 of the request): P is
+ *   0 there, and 0 times it is NaN.  In k_nope and k_pe it reaches only queries that see it.
  * Arguments:
  *   q_bf16         element (t, h, d), d < 192, at q_bf16[t * q_row_stride + h * q_head_stride + d].
  *   k_nope_bf16    [S, H, 128] with its strides; v_bf16 [S, H, 128] with its strides (both may be

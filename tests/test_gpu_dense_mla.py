@@ -911,3 +911,26 @@ def test_device_batch_dense_attention_first_called_in_a_capture():
     db.dense_mla()
     ref.check(db.out, db.lse, r)
     assert db.dense_ws.data_ptr() == ws
+
+
+@pytest.mark.parametrize("bad", [math.nan, math.inf])
+@pytest.mark.parametrize("H,nq,nk,at", [(2, 128, 228, 200), (2, 300, 401, 128), (2, 300, 401, 290), (1, 70, 4000, 3950),
+                                        (3, 513, 1000, 600), (40, 400, 1500, 1111)])
+def test_prefill_bad_values_within_a_request_reach_what_is_documented(H, nq, nk, at, bad):
+    """A value that is not finite reaches a query that does not see its position only where another query of its
+    group of 128 sees a key of the same 128; queries that see it get what the formula gives; a key there reaches
+    no query that does not see it."""
+    q, kv, lat = _prefill_inputs([nq], [nk], H, 900 + nk + at)
+    want = ref.prefill(q, kv[..., :128], lat[:, 512:], kv[..., 128:], [nq], [nk], SCALE, True)
+    kv[at, :, 128:] = bad
+    out, lse = _prefill(q, kv, lat, [nq], [nk])
+    seen = nk - nq + 1 + torch.arange(nq)
+    last = torch.minimum((torch.arange(nq) // 128 + 1) * 128, torch.tensor(nq)) - 1
+    clean = torch.nonzero((seen[last] + 127) // 128 <= at // 128)[:, 0].cuda()
+    ref.check(out[clean], lse, tuple(t[clean] if i % 2 == 0 else t for i, t in enumerate(want)))
+    sees = torch.nonzero(seen > at)[:, 0].cuda()
+    assert not bool(out[sees].isfinite().any())
+    kv[at, :, 128:], kv[at, :, :128] = 0.0, bad
+    blind = torch.nonzero(seen <= at)[:, 0].cuda()
+    out, lse = _prefill(q, kv, lat, [nq], [nk])
+    ref.check(out[blind], lse[blind], tuple(t[blind] for t in want))
