@@ -845,10 +845,14 @@ dense_mla_decode_kernel(const __grid_constant__ CUtensorMap kvmap, const __grid_
             }
             if (timed_out) break;
             float inv = -1.0f;                                       // nothing visible: O may hold 0 x NaN
+            uint32_t hidden = 0xffffffffu;                           // bit l: row of lane l, nothing visible
             if (has_tiles) {
                 if (threadIdx.x == 0) ptx::mbar_arrive_expect_tx(&bar.fin_full, quads * 128);
                 wait(&bar.fin_full, seg & 1u);
                 inv = bar.fin[row];
+                // the arrive orders nothing: the ballot, which takes every lane's value, comes before it, so all are read
+                // when rank 0 learns that it may write the next ones
+                hidden = __ballot_sync(0xffffffffu, inv < 0.0f);
                 __syncwarp();
                 if (lane == 0) arrive_remote(map_to_rank(ptx::smem_addr(&bar.fin_free), 0));
                 wait(&bar.pv_done[(u - 1) % kPvBars], ((u - 1) / kPvBars) & 1u);
@@ -894,7 +898,7 @@ dense_mla_decode_kernel(const __grid_constant__ CUtensorMap kvmap, const __grid_
 #pragma unroll
                     for (int i = 0; i < 8; ++i)
                         *reinterpret_cast<uint4*>(st + lane * 128 + ((i ^ swz) << 4)) =
-                            inv < 0.0f ? make_uint4(0u, 0u, 0u, 0u) : make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+                            (hidden >> lane) & 1u ? make_uint4(0u, 0u, 0u, 0u) : make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
                     ptx::fence_proxy_async_smem();
                     __syncwarp();
                     if (lane == 0) {
