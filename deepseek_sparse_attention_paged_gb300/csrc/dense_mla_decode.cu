@@ -633,7 +633,9 @@ dense_mla_decode_kernel(const __grid_constant__ CUtensorMap kvmap, const __grid_
             if (w.t0 < w.t1) {
                 // the row tile's queries out of the ring: value chunks into tensor memory, the rope chunk into its
                 // place; even chunks by the warps of page 0, odd ones by those of page 1.  (The score MMAs
-                // before are complete: their s_full has been waited for.)
+                // before are complete: their s_full has been waited for.  Warps without live rows have not passed a
+                // fence since, and the stores to come may not move ahead of that wait.)
+                ptx::tc_fence_after_sync();
 #pragma unroll 1
                 for (int c = 0; c < 9; ++c) {
                     const uint32_t st = used % kKStages;
