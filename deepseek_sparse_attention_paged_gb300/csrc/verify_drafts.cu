@@ -339,6 +339,10 @@ extern "C" dsa_status dsa_verify_drafts(const float* target_probs, int64_t targe
     if (!cu_q || !accepted) return DSA_ERR_INVALID_ARG;
     if (T > 0 && (!target_probs || !draft_tokens || !accept_u || !sample_u || !out_tokens)) return DSA_ERR_INVALID_ARG;
     if (T > 0 && (target_ld < V || (draft_probs != nullptr && draft_ld < V))) return DSA_ERR_INVALID_ARG;
+    // every CTA of a cluster reads the drafts, and of other requests at any time: the output may not lie over them
+    const uintptr_t in_at = reinterpret_cast<uintptr_t>(draft_tokens), out_at = reinterpret_cast<uintptr_t>(out_tokens);
+    const uintptr_t in_bytes = static_cast<uintptr_t>(T) * sizeof(int32_t);
+    if (T > 0 && in_at < out_at + in_bytes && out_at < in_at + in_bytes) return DSA_ERR_INVALID_ARG;
     const bool vec = aligned16(target_probs) && target_ld % 4 == 0 &&
                      (draft_probs == nullptr || (aligned16(draft_probs) && draft_ld % 4 == 0));
     const int groups = (V + kGroup - 1) / kGroup;

@@ -679,7 +679,7 @@ dsa_status dsa_dense_mla_decode(const void* q_bf16, const void* kv_pool, int64_t
  *   target_probs  fp32 rows of V entries, stride target_ld >= V.   draft_probs: nullable, likewise.
  *   V             1 .. 2^24.   draft_tokens int32 [T].   cu_q int32 [B + 1].
  *   accept_u      fp32 [T], sample_u fp32 [B]: uniform numbers in [0, 1).
- *   out_tokens    int32 [T], not draft_tokens.   accepted int32 [B].  Rows >= cu_q[B] of out_tokens
+ *   out_tokens    int32 [T], apart from draft_tokens.   accepted int32 [B].  Rows >= cu_q[B] of out_tokens
  *                 are left as they were.
  *   dev_err       nullable; DSA_DEVERR_INDEX_RANGE for a draft token >= V (no draft) or a cu_q range
  *                 outside [0, T] (cut to it), DSA_DEVERR_PROB for a row to draw from without mass

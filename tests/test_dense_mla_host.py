@@ -90,6 +90,12 @@ def test_verify_refusals(lib):
     assert _verify(lib, v=(1 << 24) + 1, ldp=1 << 25, ldq=1 << 25) == UNSUPPORTED
 
 
+@pytest.mark.parametrize("at", [-7, -1, 0, 3, 7])
+def test_verify_refuses_outputs_over_the_drafts(lib, at):
+    """out_tokens apart from draft_tokens in all 8 entries."""
+    assert _verify(lib, t=8, out=ctypes.c_void_p(C_.value + 4 * at)) == INVALID
+
+
 def test_binding_refuses_cpu_tensors():
     bf = torch.zeros(2, 16, 576, dtype=torch.bfloat16)
     with pytest.raises(ValueError):

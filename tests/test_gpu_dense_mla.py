@@ -934,3 +934,20 @@ def test_prefill_bad_values_within_a_request_reach_what_is_documented(H, nq, nk,
     blind = torch.nonzero(seen <= at)[:, 0].cuda()
     out, lse = _prefill(q, kv, lat, [nq], [nk])
     ref.check(out[blind], lse[blind], tuple(t[blind] for t in want))
+
+
+def test_verify_beside_its_drafts_and_not_over_them():
+    """One buffer for drafts and outputs: apart works, half over each other is refused before anything runs."""
+    p, d, tok, u, us = _verify_inputs([4, 4], 700, 64)
+    buf = torch.full((24,), -7, dtype=torch.int32, device="cuda")
+    buf[8:16] = tok.cuda()
+    acc = torch.zeros(2, dtype=torch.int32, device="cuda")
+    args = (p.cuda(), buf[8:16], _i32([0, 4, 8]), u.cuda(), us.cuda())
+    for at in (1, 4, 7, 9, 12, 15):
+        with pytest.raises(ValueError):
+            capi.dsa_verify_drafts(*args, buf[at:at + 8], acc, draft_probs=d.cuda())
+    assert bool((buf[:8] == -7).all()) and bool((buf[16:] == -7).all()) and torch.equal(buf[8:16].cpu(), tok)
+    want = ref.verify(p, d, tok.tolist(), [0, 4, 8], u, us)
+    for at in (0, 16):
+        capi.dsa_verify_drafts(*args, buf[at:at + 8], acc, draft_probs=d.cuda())
+        assert (buf[at:at + 8].tolist(), acc.tolist()) == want
