@@ -951,3 +951,33 @@ def test_verify_beside_its_drafts_and_not_over_them():
     for at in (0, 16):
         capi.dsa_verify_drafts(*args, buf[at:at + 8], acc, draft_probs=d.cuda())
         assert (buf[at:at + 8].tolist(), acc.tolist()) == want
+
+
+def test_binding_refuses_what_the_prefill_does_not_take():
+    q = torch.zeros(6, 2, 192, dtype=torch.bfloat16, device="cuda")
+    kv = torch.zeros(9, 2, 256, dtype=torch.bfloat16, device="cuda")
+    lat = torch.zeros(9, 576, dtype=torch.bfloat16, device="cuda")
+    out = torch.full((6, 2, 128), 7.0, dtype=torch.bfloat16, device="cuda")
+    good = dict(q=q, k_nope=kv[..., :128], k_pe=lat[:, 512:], v=kv[..., 128:], cu_q=_i32([0, 4, 6]), cu_k=_i32([0, 4, 9]),
+                scale=SCALE, out=out)
+    for bad in (dict(q=q.half()), dict(q=q[..., :128]), dict(q=q[0]), dict(q=q.cpu()), dict(k_nope=kv[:8, :, :128]),
+                dict(k_nope=kv[:, :1, :128]), dict(k_nope=kv), dict(v=kv[:8, :, 128:]), dict(v=kv[..., 128:].float()),
+                dict(v=kv[:, :1, 128:]), dict(k_pe=lat[:, 504:]), dict(k_pe=lat[:8, 512:]), dict(k_pe=lat),
+                dict(k_pe=torch.zeros(64, 9, dtype=torch.bfloat16, device="cuda").t()), dict(cu_q=_i32([0, 6])),
+                dict(cu_k=_i32([0, 9])), dict(cu_q=_i32([])), dict(cu_q=torch.tensor([0, 4, 6]).cuda()),
+                dict(cu_k=torch.tensor([0, 4, 9], dtype=torch.int32)), dict(out=out[:5]), dict(out=out[:, :1]),
+                dict(out=out.float()), dict(out=out.transpose(1, 2)), dict(lse=torch.zeros(6, 3, device="cuda")),
+                dict(lse=torch.zeros(6, 2, dtype=torch.float64, device="cuda")), dict(dev_err=torch.zeros(1, device="cuda"))):
+        with pytest.raises(ValueError):
+            capi.dsa_dense_mla_prefill(**{**good, **bad})
+    wide = torch.zeros(6, 2, 200, dtype=torch.bfloat16, device="cuda")
+    odd = torch.zeros(9, 2, 260, dtype=torch.bfloat16, device="cuda")
+    for bad in (dict(q=wide[..., 4:196]), dict(k_nope=odd[..., :128]), dict(v=odd[..., 132:]), dict(scale=0.0),
+                dict(scale=-1.0), dict(scale=math.nan), dict(scale=math.inf), dict(out=out[:1].expand(6, 2, 128)),
+                dict(k_pe=lat[:1, 512:].expand(9, 64))):
+        with pytest.raises(capi.DSAError):
+            capi.dsa_dense_mla_prefill(**{**good, **bad})
+    torch.cuda.synchronize()
+    assert bool((out == 7.0).all())                              # nothing ran
+    capi.dsa_dense_mla_prefill(**good)
+    assert bool((out == 0).all())
