@@ -27,10 +27,10 @@
 // one per cluster (at least kMinShare tiles).  A row tile that lies within one share is written
 // directly; the pieces of the others go to the workspace and the combine kernel joins them.
 //
-// Measured (128 heads, one new token): 64 requests of 4K to 64K 352 us (5.4 TB/s, 80 % of the copy rate; 326 us with
-// every load in L2, where the issue of the scores bounds it; 380 to 400 one call after the other, at the power
-// limit); 32 of 8192 83 us (10 of them the combine); 1 of 4096 20.1 us, 1 of 64 15 us (the chain of one row
-// tile); 8 of about 128K with two rows of 16 heads 173 us (6.0 TB/s, 88 %).
+// Measured (128 heads, one new token; calls in a captured graph): 64 requests of 4K to 64K 354 us (5.4 TB/s, 80 % of
+// the copy rate; 326 us with every load in L2, where the issue of the scores bounds it; 400 one call after the other
+// for a second, at the power limit and 1.56 GHz); 32 of 8192 83.6 us (10 of them the combine); 1 of 4096 20.5 us, 1 of
+// 64 15.5 us (the chain of one row tile); 8 of about 128K with two rows of 16 heads 173 us (6.0 TB/s, 88 %).
 //
 // Roles (384 threads), warps 10 and 11 idle:
 //   rank 0  warps 0-7  softmax: rows (tensor-memory lanes) 32 (w % 4) .. + 31, page w / 4 of the tile; queries
@@ -413,7 +413,7 @@ dense_mla_decode_kernel(const __grid_constant__ CUtensorMap kvmap, const __grid_
                 }
                 if (rank == 1 && t + kAhead < w.t1) {
                     // the pages kAhead tiles further into L2: rank 0's ring holds less than the latency of HBM times
-                    // its rate (418 -> 388 us on 64 requests of 4K to 64K; from rank 0, or further ahead, slower)
+                    // its rate (418 -> 393 us on 64 requests of 4K to 64K; from rank 0, or further ahead, slower)
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
                         const int src = 2 * (tb + kAhead) + i;
@@ -626,7 +626,7 @@ dense_mla_decode_kernel(const __grid_constant__ CUtensorMap kvmap, const __grid_
             const bool quad_live = quad * 32 < live;
             // Rows behind the last one are other requests' queries, stale P and its products: nothing reads what comes
             // of them, but zeros there let the tensor cores idle, and a long call runs at the power limit (8 requests of
-            // about 128K with two rows of 16 heads, one call after the other: 200 -> 178 us at 1.47 -> 1.78 GHz)
+            // about 128K with two rows of 16 heads, one call after the other: 200 -> 178 us at 1.47 -> 1.74 GHz)
             const bool row_live = row < live;
             const int vis = row_live ? min(w.rt.vis0 + token, bt.max_pages * kPage) : 0;
             float m_run = -INFINITY, l_run = 0.0f;

@@ -15,13 +15,13 @@
 // Q K^T (K = 192) and 512 of P V at 8192 FLOP per cycle and SM, its softmax 16384 exponentials
 // (512 to 1024 cycles of the special-function unit).  So a CTA holds two tiles of 128 queries of
 // one head and one request: while the softmax warps of one work, the tensor cores run the other's
-// products.  Measured: 8192 queries and keys, 19 heads, no mask 443 us (1.82 PFLOP/s; Q K^T reads both operands
-// from shared memory, 8 KB an MMA, which takes 79 cycles for 64); causal with 128 heads 1.60 ms (1.77 one call
-// after the other, at the power limit), with 16 heads 210 us; 8 prompts of 128 to 2048 361 us (84 % of their tiles'
-// area counts); 1000 queries after 15001 keys 785 us, with 16 heads 114 us.
+// products.  Measured: 8192 queries and keys, 19 heads, no mask 448 us (1.82 PFLOP/s; Q K^T reads both operands
+// from shared memory, 8 KB an MMA, which takes 79 cycles for 64); causal with 128 heads 1.58 ms (1.78 one call
+// after the other, at the power limit), with 16 heads 213 us; 8 prompts of 128 to 2048 362 us (84 % of their tiles'
+// area counts); 1000 queries after 15001 keys 789 us, with 16 heads 115 us.
 //
-// Work item: block qb of 256 query rows of request b, head h; the longest first over a group of heads whose keys
-// and values fit L2.  The grid has one block per item; a CTA
+// Work item: block qb of 256 query rows of request b, head h; requests in the caller's order, of each the longest
+// block first, over a group of heads whose keys and values fit L2.  The grid has one block per item; a CTA
 // takes over the items of blocks that have not started (cluster launch control) until none is left, so
 // that an item's first copies and scores run while the one before is still at its last step and its output.
 // Calls with few items split each one's keys over a cluster of C = 2 or 4 CTAs instead (one item a cluster): the
@@ -279,8 +279,8 @@ dense_mla_prefill_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_
                         __syncwarp();
                         if (!more) break;
                     }
-                    // the grid's order, x first, as (group of heads, block, head): long blocks of many heads come first,
-                    // and the last items of all are short ones (8K prompt x 16 heads: one head after the other
+                    // the grid's order, x first, as (group of heads, block, head): a prompt's long blocks of many heads
+                    // come first, and its last items are short ones (8K prompt x 16 heads: one head after the other
                     // 292 us, so 210)
                     const int blocks = static_cast<int>(gridDim.x) / C, id = y * blocks + x;
                     const int g0 = id / (group * blocks) * group, heads = min(group, H - g0), rem = id - g0 * blocks;
@@ -771,7 +771,9 @@ struct Plan {
     int group;               // heads whose items are taken longest first
 };
 
-// Both from the lengths of an average request.  Splitting an item's keys pays where items are few and of like
+// Both from the lengths of an average request, T / B and S / B of the arrays: the lengths themselves are on the
+// device.  One long prompt among many short ones is therefore planned like the short ones, and a padded batch like
+// its padding.  Splitting an item's keys pays where items are few and of like
 // length: a call takes about as many steps of a key tile (1.7 us) as its longest CTA, and an item on a cluster of
 // 2 or 4 takes a launch and a join as long as 4 or 8 of them (1000 queries after 15001 keys, CTAs per item 1, 2
 // and 4: 8 heads 211, 115 and 66 us; 16 heads 214, 115 and 130; 128 heads 850, 790 and 945).  Items of unlike

@@ -12,8 +12,8 @@
 // One warp per token: lane l holds dims 8 l .. 8 l + 7 and 256 + 8 l .. 256 + 8 l + 7 (two 16-byte
 // loads) and rope dims 2 l, 2 l + 1, so the norm is one warp reduction and nothing passes through
 // shared memory.  HBM-bound: 1152 bytes read, 256 of the cos/sin table, 1152 or 2304 written.  Measured:
-// 32768 tokens 20.3 us, 131072 tokens with both outputs 76 us (6.0 TB/s, 88 % of the copy rate), 64 tokens
-// 2.5 us (launch).
+// 32768 tokens 21.5 us (20.3 when L2 holds part of them), 131072 tokens with both outputs 76 us (6.0 TB/s, 88 % of
+// the copy rate), 64 tokens 2.7 us (launch).
 #include <cuda_bf16.h>
 
 #include "dsa_common.cuh"

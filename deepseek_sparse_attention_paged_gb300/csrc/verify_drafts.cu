@@ -18,7 +18,8 @@
 // re-reads one group of 512 entries.
 //
 // Bound by the chain of dependent steps (acceptance, sums, totals across the cluster, border), about 7 us.  Measured:
-// 1 request 7.7 us, 8 of 131072 entries 10.4 us, 64 of them 16.5 us (the read of 49 MB alone 7.2 us at the copy rate).
+// 1 request 7.9 us, 8 of 131072 entries 11.2 us, 64 of them 18.6 us with the inputs in HBM (the read of 49 MB alone
+// 7.2 us at the copy rate; 16.6 us when L2 holds it).
 #include "dsa_common.cuh"
 #include "sm100_ptx.cuh"
 

@@ -673,7 +673,7 @@ dsa_status dsa_dense_mla_decode(const void* q_bf16, const void* kv_pool, int64_t
  *   otherwise: the least v with w_0 + .. + w_v > sample_u[b] * sum w.
  *   out_tokens[cu_q[b] ..]: the accepted drafts, then the drawn token, then -1 up to the request's
  *   rows.  accepted[b]: the number of accepted drafts (r* - cu_q[b]).  A request without rows: 0.
- *   The differences are exact and the sums carry about 48 bits (they must stay within fp32's range).
+ *   The differences are exact and the sums carry about 47 bits (they must stay within fp32's range).
  *   Entries that are not positive and finite count as 0 in w; probabilities are not negative.
  * Arguments:
  *   target_probs  fp32 rows of V entries, stride target_ld >= V.   draft_probs: nullable, likewise.
