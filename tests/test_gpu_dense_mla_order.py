@@ -113,3 +113,67 @@ def test_verify_behind_the_calls_that_make_its_inputs():
     for _ in range(5):
         for got, t in zip(calls(lambda: None), want):
             assert torch.equal(got, t)
+
+
+@pytest.mark.parametrize("fork", [False, True])
+def test_a_captured_step_replayed_on_other_inputs(fork):
+    """Store, decode, prompt and verification in one graph, on one stream or with the prompt on a second one that
+    starts behind the store and is waited for by the verification; each replay gives what the calls give one by one."""
+    H, n, lens = 16, 40000, [20000, 64, 15000, 4000]
+    q, pool, table = _decode_inputs(lens, [1] * 4, H, 150)
+    raws = [torch.randn(n, 576, generator=_gen(151 + i)).to(torch.bfloat16).cuda() for i in range(2)]
+    slots = torch.cat([table[b].cpu().long()[torch.arange(m) // 64] * 64 + torch.arange(m) % 64 for b, m in enumerate(lens)] +
+                      [torch.full((n - sum(lens),), -1)]).cuda()
+    pos, w = torch.arange(n).cuda() % 300, torch.ones(512, device="cuda")
+    ang = torch.rand(300, 32, generator=_gen(153), dtype=torch.float64) * 6.3
+    cs = torch.cat([ang.cos(), ang.sin()], 1).float().cuda()
+    raw, lat = torch.empty_like(raws[0]), torch.empty_like(raws[0])
+    pq = torch.randn(300, 2, 192, generator=_gen(154)).to(torch.bfloat16).cuda()
+    kv = torch.randn(9000, 2, 256, generator=_gen(155)).to(torch.bfloat16).cuda()
+    ws = torch.empty(capi.dsa_dense_mla_decode_workspace_size(4, H), dtype=torch.uint8, device="cuda")
+    out = torch.empty(4, H, 512, dtype=torch.bfloat16, device="cuda")
+    pout = torch.empty(300, 2, 128, dtype=torch.bfloat16, device="cuda")
+    lse, probs = torch.empty(4, H, device="cuda"), torch.empty(4, 300 * 2 * 32, device="cuda")
+    tok, acc = torch.empty(4, dtype=torch.int32, device="cuda"), torch.empty(2, dtype=torch.int32, device="cuda")
+    seq, cu, pcu, pck, vcu = _i32(lens), _i32([0, 1, 2, 3, 4]), _i32([0, 300]), _i32([0, 9000]), _i32([0, 3, 4])
+    draft = _i32([5, 9, -1, -1])
+    u, us = torch.full((4,), 1e-4, device="cuda"), torch.tensor([0.3, 0.8], device="cuda")
+    main, side = torch.cuda.Stream(), torch.cuda.Stream()
+
+    def step(sync, forked):
+        capi.dsa_store_latent_prologue(raw, w, 1e-6, cs, pos, slots, pool, latent_out=lat)
+        sync()
+        if forked:
+            side.wait_stream(main)
+        with torch.cuda.stream(side if forked else torch.cuda.current_stream()):
+            capi.dsa_dense_mla_prefill(pq, kv[..., :128], lat[:9000, 512:], kv[..., 128:], pcu, pck, SCALE, pout)
+        sync()
+        capi.dsa_dense_mla_decode(q, pool, table, seq, cu, SCALE, out, ws, lse=lse)
+        sync()
+        if forked:
+            main.wait_stream(side)
+        torch.softmax(pout.view(4, -1).float() * out.float().mean(), 1, out=probs)
+        sync()
+        capi.dsa_verify_drafts(probs, draft, vcu, u, us, tok, acc)
+        sync()
+
+    results = (pool, lat, out, lse, pout, probs, tok, acc)
+    want = []
+    for r in raws:
+        raw.copy_(r)
+        step(torch.cuda.synchronize, False)
+        want.append([t.clone() for t in results])
+    assert not torch.equal(want[0][2], want[1][2])
+    main.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(main):
+        gr = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(gr, stream=main):
+            step(lambda: None, fork)
+        for i in (0, 1, 1, 0, 1):
+            for t in (out, pout, lat):
+                t.fill_(7.0)
+            raw.copy_(raws[i])
+            gr.replay()
+            main.synchronize()
+            for got, t in zip(results, want[i]):
+                assert torch.equal(got, t)
