@@ -30,12 +30,14 @@ DSA_DEVERR_INDEX_RANGE = 0x4
 DSA_DEVERR_TIMEOUT = 0x8
 DSA_DEVERR_POSITION = 0x10
 DSA_DEVERR_PROB = 0x20
+DSA_DEVERR_NO_PAGE = 0x40
 DSA_Q_ROTATE = 0x1
 DSA_NORM_RMS = 0x2
 DSA_ROPE_INTERLEAVED = 0x4
 DSA_K_NO_ROTATE = 0x8
 DSA_SCALE_UE8M0 = 0x10
 DSA_CAUSAL = 0x40
+DSA_LOGITS_BF16 = 0x80
 DSA_KEYS_CMP4 = 0x20          # the index cache holds compressed keys, one per 4 tokens
 PAGE_SIZE = 64
 INDEX_PAGE_BYTES = 64 * 132
@@ -117,7 +119,12 @@ def load(path: str = LIB_PATH):
         "dsa_dense_mla_decode_workspace_size": (sz, [i32, i32]),
         "dsa_dense_mla_decode": (ctypes.c_int, [P, P, i64, P, i32, P, P, i32, i32, i32, ctypes.c_float, P, P, P, sz,
                                                 P, P]),
+        "dsa_dense_mla_decode_shared_workspace_size": (sz, [i32, i32]),
+        "dsa_dense_mla_decode_shared": (ctypes.c_int, [P, P, i64, P, i32, P, P, i32, i32, i32, P, P, i32, ctypes.c_float,
+                                                       P, P, P, sz, P, P]),
         "dsa_verify_drafts": (ctypes.c_int, [P, i64, P, i64, i32, P, P, i32, i32, P, P, P, P, P, P]),
+        "dsa_sample_tokens": (ctypes.c_int, [P, i64, i32, i32, u32, P, P, P, P, P, P, P, i64, P, P]),
+        "dsa_step_tables": (ctypes.c_int, [P, P, P, P, i32, P, i32, i64, P, P, P, P, P, P, P, P, i32, P, P]),
     }
     for name, (res, args) in sigs.items():
         fn = getattr(lib, name)
@@ -722,14 +729,8 @@ def dsa_dense_mla_decode_workspace_size(T: int, H: int) -> int:
     return int(load().dsa_dense_mla_decode_workspace_size(int(T), int(H)))
 
 
-def dsa_dense_mla_decode(q_bf16: torch.Tensor, kv_pool: torch.Tensor, block_table: torch.Tensor,
-                         seq_lens: torch.Tensor, cu_q: torch.Tensor, scale: float, out: torch.Tensor,
-                         workspace: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None,
-                         dev_err: Optional[torch.Tensor] = None, stream=None) -> None:
-    """Absorbed latent attention of the query rows over every visible row of the paged cache.  `workspace`
-    holds at least dsa_dense_mla_decode_workspace_size(T, H) bytes; when it is None a buffer of that size
-    is taken from torch's allocator for this call."""
-    dev = _current_device()
+def _decode_args(q_bf16, kv_pool, block_table, seq_lens, cu_q, out, lse, dev: int):
+    """Checked arguments that the dense decode calls have in common: (addresses, sizes)."""
     qp = _arr(q_bf16, torch.bfloat16, dev, "q_bf16")
     pool = _arr(kv_pool, torch.bfloat16, dev, "kv_pool")
     table = _arr(block_table, torch.int32, dev, "block_table")
@@ -737,7 +738,6 @@ def dsa_dense_mla_decode(q_bf16: torch.Tensor, kv_pool: torch.Tensor, block_tabl
     cq = _arr(cu_q, torch.int32, dev, "cu_q")
     op = _arr(out, torch.bfloat16, dev, "out")
     lp = _opt(lse, torch.float32, dev, "lse")
-    err = _opt(dev_err, torch.int32, dev, "dev_err")
     shape, pages, rows = q_bf16.shape, kv_pool.shape, block_table.shape
     if len(shape) != 3 or shape[2] != LATENT_DIM:
         raise ValueError("q_bf16 must be [T, H, 576]")
@@ -749,16 +749,61 @@ def dsa_dense_mla_decode(q_bf16: torch.Tensor, kv_pool: torch.Tensor, block_tabl
         raise ValueError("cu_q must have B + 1 entries, block_table B rows")
     if out.shape != (T, H, VALUE_DIM) or (lse is not None and lse.shape != (T, H)):
         raise ValueError("out must be [T, H, 512], lse [T, H]")
+    return (qp, pool, pages[0], table, rows[1], lens, cq, B, T, H), op, lp
+
+
+def _scratch(workspace: Optional[torch.Tensor], size, T: int, H: int, stream, q: torch.Tensor, dev: int) -> torch.Tensor:
+    """The caller's workspace, checked, or one from torch's allocator for this call."""
     if workspace is None:
         _need(stream is None, "a call on an explicit stream brings its own workspace")
-        workspace = torch.empty(max(16, dsa_dense_mla_decode_workspace_size(T, H)), dtype=torch.uint8,
-                                device=q_bf16.device)
-    elif workspace.get_device() != dev or not workspace.is_contiguous():
+        return torch.empty(max(16, size(T, H)), dtype=torch.uint8, device=q.device)
+    if workspace.get_device() != dev or not workspace.is_contiguous():
         raise ValueError("workspace must be a contiguous CUDA tensor on the current device")
+    return workspace
+
+
+def dsa_dense_mla_decode(q_bf16: torch.Tensor, kv_pool: torch.Tensor, block_table: torch.Tensor,
+                         seq_lens: torch.Tensor, cu_q: torch.Tensor, scale: float, out: torch.Tensor,
+                         workspace: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None,
+                         dev_err: Optional[torch.Tensor] = None, stream=None) -> None:
+    """Absorbed latent attention of the query rows over every visible row of the paged cache.  `workspace`
+    holds at least dsa_dense_mla_decode_workspace_size(T, H) bytes; when it is None a buffer of that size
+    is taken from torch's allocator for this call."""
+    dev = _current_device()
+    args, op, lp = _decode_args(q_bf16, kv_pool, block_table, seq_lens, cu_q, out, lse, dev)
+    err = _opt(dev_err, torch.int32, dev, "dev_err")
+    B, T, H = args[7:]
+    ws = _scratch(workspace, dsa_dense_mla_decode_workspace_size, T, H, stream, q_bf16, dev)
     _check("dsa_dense_mla_decode", _lib.dsa_dense_mla_decode(
-        qp, pool, pages[0], table, rows[1], lens, cq, B, T, H, scale, op, lp,
-        workspace.data_ptr(), workspace.numel() * workspace.element_size(), err, _raw_stream(stream, dev)))
+        *args, scale, op, lp, ws.data_ptr(), ws.numel() * ws.element_size(), err, _raw_stream(stream, dev)))
     _count(2 if T > 0 and B > 0 else 0)   # the attention and the joining of its pieces
+
+
+def dsa_dense_mla_decode_shared_workspace_size(T: int, H: int) -> int:
+    return int(load().dsa_dense_mla_decode_shared_workspace_size(int(T), int(H)))
+
+
+def dsa_dense_mla_decode_shared(q_bf16: torch.Tensor, kv_pool: torch.Tensor, block_table: torch.Tensor,
+                                seq_lens: torch.Tensor, cu_q: torch.Tensor, cu_group: torch.Tensor,
+                                shared_lens: torch.Tensor, scale: float, out: torch.Tensor,
+                                workspace: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None,
+                                dev_err: Optional[torch.Tensor] = None, stream=None) -> None:
+    """dsa_dense_mla_decode where the requests [cu_group[g], cu_group[g + 1]) have their first shared_lens[g]
+    positions (whole pages) in common: those are read once a group.  `workspace` as there, of
+    dsa_dense_mla_decode_shared_workspace_size(T, H) bytes."""
+    dev = _current_device()
+    args, op, lp = _decode_args(q_bf16, kv_pool, block_table, seq_lens, cu_q, out, lse, dev)
+    cg = _arr(cu_group, torch.int32, dev, "cu_group")
+    sh = _arr(shared_lens, torch.int32, dev, "shared_lens")
+    err = _opt(dev_err, torch.int32, dev, "dev_err")
+    B, T, H = args[7:]
+    G = shared_lens.numel()
+    if cu_group.numel() != G + 1:
+        raise ValueError("cu_group must have G + 1 entries")
+    ws = _scratch(workspace, dsa_dense_mla_decode_shared_workspace_size, T, H, stream, q_bf16, dev)
+    _check("dsa_dense_mla_decode_shared", _lib.dsa_dense_mla_decode_shared(
+        *args, cg, sh, G, scale, op, lp, ws.data_ptr(), ws.numel() * ws.element_size(), err, _raw_stream(stream, dev)))
+    _count(2 if T > 0 and B > 0 else 0)   # the attention and the joining of its parts
 
 
 def dsa_verify_drafts(target_probs: torch.Tensor, draft_tokens: torch.Tensor, cu_q: torch.Tensor,
@@ -793,6 +838,80 @@ def dsa_verify_drafts(target_probs: torch.Tensor, draft_tokens: torch.Tensor, cu
             raise ValueError("draft_probs must be [T, V]")
     _check("dsa_verify_drafts", _lib.dsa_verify_drafts(tp, ld_t, dp, ld_d, V, tok, cq, B, T, ua, us, ot, ac, err,
                                                        _raw_stream(stream, dev)))
+    _count(1 if B > 0 else 0)
+
+
+def dsa_sample_tokens(logits: torch.Tensor, u: torch.Tensor, tokens: torch.Tensor,
+                      temperature: Optional[torch.Tensor] = None, top_k: Optional[torch.Tensor] = None,
+                      top_p: Optional[torch.Tensor] = None, min_p: Optional[torch.Tensor] = None,
+                      probs: Optional[torch.Tensor] = None, dev_err: Optional[torch.Tensor] = None, stream=None) -> None:
+    """Draws tokens[r] from row r of logits [R, V] (fp32 or bf16, rows may be strided) with the uniform number
+    u[r], after temperature, top-k, top-p and min-p (fp32 / int32 [R] each, None: not applied); probs [R, V]
+    (fp32, rows may be strided) gets the filtered distribution."""
+    dev = _current_device()
+    if logits.dim() != 2:
+        raise ValueError("logits must be [R, V]")
+    bf16 = logits.dtype is torch.bfloat16
+    V = logits.shape[1]
+    lg, R, ld = _dense_rows(logits, torch.bfloat16 if bf16 else torch.float32, V, dev, "logits")
+    up = _arr(u, torch.float32, dev, "u")
+    tk = _arr(tokens, torch.int32, dev, "tokens")
+    tp = _opt(temperature, torch.float32, dev, "temperature")
+    kp = _opt(top_k, torch.int32, dev, "top_k")
+    pp = _opt(top_p, torch.float32, dev, "top_p")
+    mp = _opt(min_p, torch.float32, dev, "min_p")
+    err = _opt(dev_err, torch.int32, dev, "dev_err")
+    if u.numel() != R or tokens.numel() != R:
+        raise ValueError("u and tokens must have R entries")
+    for t, name in ((temperature, "temperature"), (top_k, "top_k"), (top_p, "top_p"), (min_p, "min_p")):
+        if t is not None and t.numel() != R:
+            raise ValueError(f"{name} must have R entries")
+    pr, ld_p = None, V
+    if probs is not None:
+        pr, rows, ld_p = _dense_rows(probs, torch.float32, V, dev, "probs")
+        if rows != R:
+            raise ValueError("probs must be [R, V]")
+    _check("dsa_sample_tokens", _lib.dsa_sample_tokens(lg, ld, V, R, DSA_LOGITS_BF16 if bf16 else 0, tp, kp, pp, mp, up, tk,
+                                                       pr, ld_p, err, _raw_stream(stream, dev)))
+    _count(1 if R > 0 else 0)
+
+
+def dsa_step_tables(cached_lens: torch.Tensor, q_lens: torch.Tensor, page_counts: torch.Tensor,
+                    block_table: torch.Tensor, num_pages: int, free_pages: torch.Tensor, free_count: torch.Tensor,
+                    seq_lens: torch.Tensor, page_counts_out: torch.Tensor, free_count_out: torch.Tensor,
+                    cu_q: torch.Tensor, positions: torch.Tensor, slot_mapping: torch.Tensor,
+                    keep_pages: Optional[torch.Tensor] = None, dev_err: Optional[torch.Tensor] = None,
+                    stream=None) -> None:
+    """Lengths, row offsets, positions and slots of a step from cached_lens / q_lens [B] (q_lens < 0: the request
+    ends); block_table [B, max_pages] and the stack free_pages [num_pages] are updated in place."""
+    dev = _current_device()
+    i32 = torch.int32
+    ca = _arr(cached_lens, i32, dev, "cached_lens")
+    ql = _arr(q_lens, i32, dev, "q_lens")
+    pc = _arr(page_counts, i32, dev, "page_counts")
+    kp = _opt(keep_pages, i32, dev, "keep_pages")
+    bt = _arr(block_table, i32, dev, "block_table")
+    fp = _arr(free_pages, i32, dev, "free_pages")
+    fc = _arr(free_count, i32, dev, "free_count")
+    sl = _arr(seq_lens, i32, dev, "seq_lens")
+    po = _arr(page_counts_out, i32, dev, "page_counts_out")
+    fo = _arr(free_count_out, i32, dev, "free_count_out")
+    cq = _arr(cu_q, i32, dev, "cu_q")
+    ps = _arr(positions, torch.int64, dev, "positions")
+    sm = _arr(slot_mapping, torch.int64, dev, "slot_mapping")
+    err = _opt(dev_err, i32, dev, "dev_err")
+    B, T = cached_lens.numel(), positions.numel()
+    if (q_lens.numel() != B or page_counts.numel() != B or seq_lens.numel() != B or page_counts_out.numel() != B or
+            (keep_pages is not None and keep_pages.numel() != B) or cu_q.numel() != B + 1):
+        raise ValueError("lengths and counts must have B entries, cu_q B + 1")
+    if block_table.dim() != 2 or block_table.shape[0] != B:
+        raise ValueError("block_table must be [B, max_pages]")
+    if slot_mapping.numel() != T:
+        raise ValueError("positions and slot_mapping must have T entries each")
+    if free_pages.numel() != num_pages or free_count.numel() != 1 or free_count_out.numel() != 1:
+        raise ValueError("free_pages must have num_pages entries, free_count and free_count_out one")
+    _check("dsa_step_tables", _lib.dsa_step_tables(ca, ql, pc, kp, B, bt, block_table.shape[1], num_pages, fp, fc, sl, po, fo,
+                                                   cq, ps, sm, T, err, _raw_stream(stream, dev)))
     _count(1 if B > 0 else 0)
 
 

@@ -73,7 +73,7 @@ constexpr int kMinShare = 2;
 constexpr int kAhead = 2;                                       // tiles between a page's prefetch and its copy
 constexpr size_t kDecSmem = 1024 + size_t(kDataBytes) + 5120;
 static_assert(kDecSmem <= 232448, "shared-memory budget");
-static_assert(kMaxRequests * 4 <= kDataBytes, "schedule scratch");
+static_assert(2 * kMaxRequests * 4 <= kDataBytes, "schedule scratch");
 
 struct DecBars {
     uint64_t kv_full[kMaxStages], kv_empty[kMaxStages];
@@ -96,7 +96,7 @@ struct DecBars {
     uint32_t tmem_slot;
     int page_ok[kMaxStages];                // bit i: page i of the stage is there and its id valid
     int tile_ok[kSBufs];                    // ... of the score tile's pages
-    int start[4];                           // first request, first row tile of it, first key tile, tiles of the share
+    int start[4];                           // first unit, first row tile of it, first key tile, tiles of the share
     int first_cluster;                      // cluster that holds the first piece of the first row tile
     float tmax[2][2][kRows];                // rank 0: [tile parity][key half][row]: maximum of the tile
     alignas(16) float alpha[2][kRows];      // the factors of the tile: rank 0's, copied to rank 1
@@ -109,13 +109,30 @@ struct Batch {
     const int32_t* cu_q;
     int B, T, H, max_pages;
     int per;               // query tokens of a row tile: 128 / H
+    // requests [cu_group[g], cu_group[g + 1]) have their first shared_lens[g] positions in common
+    const int32_t* cu_group;
+    const int32_t* shared_lens;
+    int G;
 };
 
-// Row tile g of request b: up to 128 / H consecutive query tokens.
+// What the row tiles of a unit have in common: a request's query tokens and keys, or, with shared prefixes,
+// a group's query tokens over the group's prefix (units 0 .. G - 1), then a request's over what it has behind its
+// group's prefix (unit G + b).  Positions count from the unit's first key.
+struct Unit {
+    int q0, nq;            // query tokens
+    int vis;               // visible keys of the last one (each earlier one sees one less); a prefix: its length
+    int table, page0;      // row of the block table, first page in it
+    int pages;             // pages of that row from there on
+    bool prefix;           // every token sees the same keys, but for those of requests that are shorter
+    bool part;             // its tokens have another unit: the results are parts
+};
+
+// Row tile g of a unit: up to 128 / H consecutive query tokens.
 struct RowTile {
     int row0, tokens;      // first query token (global row), number of tokens
     int vis0;              // visible keys of the first one (each next one sees one more; may be <= 0)
-    int tiles;             // key tiles of the one that sees most
+    int most;              // ... of the one that sees most
+    int tiles;             // key tiles of that one
     bool cut;              // visible keys past the block table
 };
 
@@ -127,41 +144,89 @@ __device__ __forceinline__ int query_range(const Batch& bt, int b, int& q0) {
 // Lengths below 0 count as 0.
 __device__ __forceinline__ int seq_len(const Batch& bt, int b) { return max(0, __ldg(bt.seq_lens + b)); }
 
-__device__ __forceinline__ RowTile row_tile(const Batch& bt, int L, int q0, int nq, int g) {
+// Positions of group g's shared prefix: whole pages, inside the table.
+__device__ __forceinline__ int prefix_len(const Batch& bt, int g) {
+    return max(0, min(bt.max_pages, __ldg(bt.shared_lens + g) / kPage)) * kPage;
+}
+// ... of request b's group (the last one that begins at or before it; 0 outside all groups).
+__device__ __forceinline__ int request_prefix(const Batch& bt, int b) {
+    if (bt.G < 1) return 0;
+    const int g = row_request(bt.cu_group, bt.G, b);
+    return __ldg(bt.cu_group + g) <= b && b < __ldg(bt.cu_group + g + 1) ? prefix_len(bt, g) : 0;
+}
+
+template <bool kShared>
+__device__ __forceinline__ int unit_count(const Batch& bt) { return kShared ? bt.G + bt.B : bt.B; }
+
+template <bool kShared>
+__device__ __forceinline__ Unit unit(const Batch& bt, int i) {
+    Unit u;
+    if (kShared && i < bt.G) {
+        const int b0 = max(0, min(bt.B, __ldg(bt.cu_group + i))), b1 = max(b0, min(bt.B, __ldg(bt.cu_group + i + 1)));
+        u.vis = prefix_len(bt, i);
+        u.q0 = max(0, min(bt.T, __ldg(bt.cu_q + b0)));
+        u.nq = b1 > b0 && u.vis > 0 ? max(0, min(bt.T, __ldg(bt.cu_q + b1)) - u.q0) : 0;
+        u.table = min(b0, bt.B - 1);
+        u.page0 = 0;
+        u.pages = u.vis / kPage;
+        u.prefix = u.part = true;
+        return u;
+    }
+    const int b = kShared ? i - bt.G : i;
+    const int prefix = kShared ? request_prefix(bt, b) : 0;
+    u.nq = query_range(bt, b, u.q0);
+    u.vis = seq_len(bt, b) - prefix;
+    u.table = b;
+    u.page0 = prefix / kPage;
+    u.pages = bt.max_pages - u.page0;
+    u.prefix = false;
+    u.part = prefix > 0;
+    return u;
+}
+
+__device__ __forceinline__ RowTile row_tile(const Batch& bt, const Unit& u, int g) {
     RowTile t;
-    t.row0 = q0 + g * bt.per;
-    t.tokens = min(bt.per, nq - g * bt.per);
-    t.vis0 = L - nq + g * bt.per + 1;
-    const int most = t.vis0 + t.tokens - 1;
-    t.cut = most > bt.max_pages * kPage;
-    t.tiles = (max(0, min(most, bt.max_pages * kPage)) + kKeys - 1) / kKeys;
+    t.row0 = u.q0 + g * bt.per;
+    t.tokens = min(bt.per, u.nq - g * bt.per);
+    t.vis0 = u.prefix ? u.vis : u.vis - u.nq + g * bt.per + 1;
+    t.most = u.prefix ? u.vis : t.vis0 + t.tokens - 1;
+    t.cut = t.most > u.pages * kPage;
+    t.tiles = (max(0, min(t.most, u.pages * kPage)) + kKeys - 1) / kKeys;
     return t;
 }
 
 // A share's pieces, one row tile after the other; every role walks them by itself.
+template <bool kShared>
 struct Walk {
     Batch bt;
-    int b, g, q0, nq, L, left;
+    int i, g, left;        // unit, row tile of it, tiles left in the share
+    Unit u;
     RowTile rt;
     int t0, t1;            // key tiles [t0, t1) of the piece (t0 == t1: a row tile that sees nothing)
     bool whole, first;     // the piece is its whole row tile; the share's first piece
 
     __device__ Walk(const Batch& batch, const int* start) : bt(batch) {
-        b = uniform(start[0]);
+        i = uniform(start[0]);
         g = uniform(start[1]);
         t0 = uniform(start[2]);
         left = uniform(start[3]);
         first = true;
-        load_request();
+        load_unit();
         set_piece();
     }
-    __device__ void load_request() {
-        nq = uniform(query_range(bt, b, q0));
-        q0 = uniform(q0);
-        L = uniform(seq_len(bt, b));
+    __device__ void load_unit() {
+        u = unit<kShared>(bt, i);
+        u.nq = uniform(u.nq);
+        u.q0 = uniform(u.q0);
+        u.vis = uniform(u.vis);
+        if (kShared) {
+            u.table = uniform(u.table);
+            u.page0 = uniform(u.page0);
+            u.pages = uniform(u.pages);
+        }
     }
     __device__ void set_piece() {
-        rt = row_tile(bt, L, q0, nq, g);
+        rt = row_tile(bt, u, g);
         const int n = max(1, rt.tiles);
         const int take = min(n - t0, left);
         whole = take == n;
@@ -173,14 +238,14 @@ struct Walk {
         if (left <= 0) return false;
         t0 = 0;
         first = false;
-        if ((g + 1) * bt.per < nq) {
+        if ((g + 1) * bt.per < u.nq) {
             ++g;
         } else {
             g = 0;
             do {
-                if (++b >= bt.B) return false;
-                load_request();
-            } while (nq == 0);
+                if (++i >= unit_count<kShared>(bt)) return false;
+                load_unit();
+            } while (u.nq == 0);
         }
         set_piece();
         return true;
@@ -188,34 +253,43 @@ struct Walk {
 };
 
 // Workspace slot of a part: 2 c for the one that starts share c but not its row tile, else 2 c + 1.
-__device__ __forceinline__ int64_t piece_slot(int cluster, const Walk& w) {
+template <bool kShared>
+__device__ __forceinline__ int64_t piece_slot(int cluster, const Walk<kShared>& w) {
     return 2 * static_cast<int64_t>(cluster) + ((w.first && w.t0 > 0) ? 0 : 1);
 }
 
-// Key tiles of request b over all its row tiles (a row tile that sees nothing counts as one).
-__device__ __forceinline__ int request_tiles(const Batch& bt, int b, int32_t* err) {
-    int q0;
-    const int nq = query_range(bt, b, q0);
+// Key tiles of a unit over all its row tiles (a row tile that sees nothing counts as one).
+template <bool kShared>
+__device__ __forceinline__ int unit_tiles(const Batch& bt, int i, int32_t* err) {
+    const Unit u = unit<kShared>(bt, i);
+    if (kShared && u.prefix) {
+        if (err != nullptr && (__ldg(bt.cu_group + i) < 0 || __ldg(bt.cu_group + i + 1) < __ldg(bt.cu_group + i) ||
+                               __ldg(bt.cu_group + i + 1) > bt.B || __ldg(bt.shared_lens + i) / kPage > bt.max_pages))
+            raise_error(err, DSA_DEVERR_INDEX_RANGE);
+        return (u.nq + bt.per - 1) / bt.per * ((u.vis + kKeys - 1) / kKeys);
+    }
+    const int b = kShared ? i - bt.G : i;
     if (err != nullptr && (__ldg(bt.cu_q + b) < 0 || __ldg(bt.cu_q + b + 1) > bt.T)) raise_error(err, DSA_DEVERR_INDEX_RANGE);
-    if (nq == 0) return 0;
-    const int L = seq_len(bt, b);
+    if (u.nq == 0) return 0;
     int sum = 0;
-    for (int g = 0; g * bt.per < nq; ++g) {
-        const RowTile t = row_tile(bt, L, q0, nq, g);
+    for (int g = 0; g * bt.per < u.nq; ++g) {
+        const RowTile t = row_tile(bt, u, g);
         if (t.cut && err != nullptr) raise_error(err, DSA_DEVERR_INDEX_RANGE);
         sum += max(1, t.tiles);
     }
     return sum;
 }
 
-// The share of cluster c: sums of all requests in `sums` (shared), then one warp finds the start.
+// The share of cluster c: sums of all units in `sums` (shared), then one warp finds the start.
+template <bool kShared>
 __device__ __forceinline__ void find_share(const Batch& bt, int c, int clusters, int* sums, DecBars& bar, int32_t* err) {
-    for (int b = threadIdx.x; b < bt.B; b += kDecThreads) sums[b] = request_tiles(bt, b, c == 0 ? err : nullptr);
+    const int units = unit_count<kShared>(bt);
+    for (int b = threadIdx.x; b < units; b += kDecThreads) sums[b] = unit_tiles<kShared>(bt, b, c == 0 ? err : nullptr);
     __syncthreads();
     if (threadIdx.x < 32) {
         const int lane = threadIdx.x;
         int total = 0;
-        for (int b = lane; b < bt.B; b += 32) total += sums[b];
+        for (int b = lane; b < units; b += 32) total += sums[b];
 #pragma unroll
         for (int m = 16; m > 0; m >>= 1) total += __shfl_xor_sync(0xffffffffu, total, m);
         const int share = max((total + clusters - 1) / clusters, kMinShare);
@@ -225,9 +299,9 @@ __device__ __forceinline__ void find_share(const Batch& bt, int c, int clusters,
         }
         if (w0 < total) {
             int carry = 0;
-            for (int b0 = 0; b0 < bt.B; b0 += 32) {
+            for (int b0 = 0; b0 < units; b0 += 32) {
                 const int b = b0 + lane;
-                int inc = b < bt.B ? sums[b] : 0;
+                int inc = b < units ? sums[b] : 0;
                 const int own = inc;
 #pragma unroll
                 for (int d = 1; d < 32; d <<= 1) {
@@ -237,13 +311,11 @@ __device__ __forceinline__ void find_share(const Batch& bt, int c, int clusters,
                 const uint32_t hit = __ballot_sync(0xffffffffu, w0 < carry + inc);
                 if (hit != 0u) {
                     if (lane == __ffs(hit) - 1) {
-                        int at = carry + inc - own;            // tiles before the request
-                        int q0;
-                        const int nq = query_range(bt, b, q0);
-                        const int L = seq_len(bt, b);
+                        int at = carry + inc - own;            // tiles before the unit
+                        const Unit u = unit<kShared>(bt, b);
                         int g = 0;
                         for (;; ++g) {
-                            const int n = max(1, row_tile(bt, L, q0, nq, g).tiles);
+                            const int n = max(1, row_tile(bt, u, g).tiles);
                             if (w0 < at + n) break;
                             at += n;
                         }
@@ -307,13 +379,22 @@ struct Meta {
     int first_cluster;
 };
 
+// With shared prefixes, where the parts of a query token's rows lie, over its group's prefix ([0]) and over the rest ([1]).
+struct Parts {
+    int first;             // kWritten: there are none, kWholePart: one, in the rows' own place; else the first cluster's
+    int last;              // the last cluster
+    int row0;              // first token of the row tile
+};
+constexpr int kWritten = -2, kWholePart = -1;
+
+template <bool kShared>
 __global__ void __launch_bounds__(kDecThreads, 1) __cluster_dims__(2, 1, 1)
 dense_mla_decode_kernel(const __grid_constant__ CUtensorMap kvmap, const __grid_constant__ CUtensorMap qmap,
                         const __grid_constant__ CUtensorMap omap, const __grid_constant__ CUtensorMap pmap,
                         const uint16_t* __restrict__ kv, int num_pages,
                         const int32_t* __restrict__ block_table, Batch bt, float scale, uint16_t* __restrict__ out,
-                        float* __restrict__ lse_out, float* __restrict__ part_lse, Meta* __restrict__ meta, int slot_rows,
-                        int32_t* err) {
+                        float* __restrict__ lse_out, float* __restrict__ part_lse, Meta* __restrict__ meta,
+                        Parts* __restrict__ parts, int slot_rows, int32_t* err) {
     extern __shared__ unsigned char smem_raw[];
     const uint32_t raw_addr = ptx::smem_addr(smem_raw);
     unsigned char* base = smem_raw + (((raw_addr + 1023u) & ~1023u) - raw_addr);
@@ -356,7 +437,7 @@ dense_mla_decode_kernel(const __grid_constant__ CUtensorMap kvmap, const __grid_
         ptx::tmem_relinquish();
     }
     ptx::griddep_wait();             // a programmatic dependent: what came before is complete
-    find_share(bt, cluster, clusters, reinterpret_cast<int*>(ring), bar, rank == 0 ? err : nullptr);
+    find_share<kShared>(bt, cluster, clusters, reinterpret_cast<int*>(ring), bar, rank == 0 ? err : nullptr);
     ptx::fence_proxy_async_smem();   // the schedule's scratch lies where copies will land
     ptx::tc_fence_before_sync();
     cluster_sync_all();              // both CTAs' barriers exist before the peer signals or writes into them
@@ -367,12 +448,16 @@ dense_mla_decode_kernel(const __grid_constant__ CUtensorMap kvmap, const __grid_
     bool timed_out = false;
     const bool work = uniform(bar.start[3]) > 0;
     const uint32_t ring_addr = ptx::smem_addr(ring);
-    if (threadIdx.x == 0 && rank == 1) meta[cluster].rows = 0;
+    if (!kShared && threadIdx.x == 0 && rank == 1) meta[cluster].rows = 0;
+    // first row of a whole row tile's parts: behind the slots, those over a prefix first
+    auto part_row = [&](const Walk<kShared>& w) {
+        return 2 * static_cast<int64_t>(clusters) * slot_rows + (static_cast<int64_t>(w.u.prefix ? 0 : bt.T) + w.rt.row0) * bt.H;
+    };
 
     if (work && warp == kTmaWarp) {
         // ---------------------------------------------------------------- TMA (both ranks)
         const uint32_t stages = rank == 0 ? kKStages : kVStages;
-        Walk w(bt, bar.start);
+        Walk<kShared> w(bt, bar.start);
         uint32_t s = 0, ph = 0, used = 0;                            // stage, its phase, stages used so far
         auto stage = [&]() {                                         // the next stage is free (whole warp)
             if (!ptx::mbar_wait(&bar.kv_empty[s], ph ^ 1u, deadline)) timed_out = true;
@@ -397,11 +482,12 @@ dense_mla_decode_kernel(const __grid_constant__ CUtensorMap kvmap, const __grid_
                     }
                     advance();
                 }
-            const int most = w.rt.vis0 + w.rt.tokens - 1;            // visible keys of the token that sees most
+            const int most = w.rt.most;
+            const int32_t* table = block_table + static_cast<int64_t>(w.u.table) * bt.max_pages + w.u.page0;
             auto load_pages = [&](int t) {                           // page ids of 16 tiles from t on
                 const int at = 2 * t + lane;
-                const bool needed = at < 2 * w.t1 && at * kPage < most && at < bt.max_pages;
-                return needed ? __ldg(block_table + static_cast<int64_t>(w.b) * bt.max_pages + at) : -1;
+                const bool needed = at < 2 * w.t1 && at * kPage < most && at < w.u.pages;
+                return needed ? __ldg(table + at) : -1;
             };
             int page = -1, page_next = load_pages(w.t0);
             for (int t = w.t0; t < w.t1 && !timed_out; ++t) {
@@ -430,7 +516,7 @@ dense_mla_decode_kernel(const __grid_constant__ CUtensorMap kvmap, const __grid_
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
                     const int pg = __shfl_sync(0xffffffffu, page, 2 * tb + i);
-                    const bool needed = (2 * t + i) * kPage < most && 2 * t + i < bt.max_pages;
+                    const bool needed = (2 * t + i) * kPage < most && 2 * t + i < w.u.pages;
                     const bool there = needed && pg >= 0 && pg < num_pages;
                     // a page that is not there: a box past the end reads zeros, and rank 0 masks its keys
                     row[i] = (there ? pg : num_pages) * kPage;
@@ -483,7 +569,7 @@ dense_mla_decode_kernel(const __grid_constant__ CUtensorMap kvmap, const __grid_
         auto wait = [&](uint64_t* b, uint32_t parity) {
             if (!ptx::mbar_wait(b, parity, deadline)) late = true;
         };
-        Walk w(bt, bar.start);
+        Walk<kShared> w(bt, bar.start);
         uint32_t u = 0, seg = 0, s = 0, ph = 0, q_phase = 0;          // q_phase: bit s, the phase of q_read[s]
         do {
             if (w.t0 >= w.t1) continue;
@@ -542,7 +628,7 @@ dense_mla_decode_kernel(const __grid_constant__ CUtensorMap kvmap, const __grid_
         auto wait = [&](uint64_t* b, uint32_t parity) {
             if (!ptx::mbar_wait(b, parity, deadline)) late = true;
         };
-        Walk w(bt, bar.start);
+        Walk<kShared> w(bt, bar.start);
         uint32_t u = 0, seg = 0, s = 0, ph = 0;
         do {
             if (w.t0 >= w.t1) continue;
@@ -552,7 +638,7 @@ dense_mla_decode_kernel(const __grid_constant__ CUtensorMap kvmap, const __grid_
                 for (int i = 0; i < 4; ++i) {                        // page i / 2, value dims 256 (i % 2) .. + 255
                     const uint32_t pb = 2 * (u & 1u) + (i >> 1);
                     wait(&bar.kv_full[s], ph);
-                    const int valid = w.rt.vis0 + w.rt.tokens - 1 - t * kKeys - (i >> 1) * kPage;
+                    const int valid = w.rt.most - t * kKeys - (i >> 1) * kPage;
                     if (valid > 0 && valid < kPage) {
                         // rows past the last visible position may hold anything: their P is 0, but 0 times NaN
                         // or infinity is not (a page without visible rows was filled with zeros)
@@ -620,7 +706,7 @@ dense_mla_decode_kernel(const __grid_constant__ CUtensorMap kvmap, const __grid_
             if (!ptx::mbar_wait(b, parity, deadline)) timed_out = true;
         };
         uint32_t u = 0, seg = 0, meets = 0, used = 0;                // meets: uses of the pair barrier; used: ring stages
-        Walk w(bt, bar.start);
+        Walk<kShared> w(bt, bar.start);
         do {
             const int live = w.rt.tokens * bt.H;
             const bool quad_live = quad * 32 < live;
@@ -628,7 +714,14 @@ dense_mla_decode_kernel(const __grid_constant__ CUtensorMap kvmap, const __grid_
             // of them, but zeros there let the tensor cores idle, and a long call runs at the power limit (8 requests of
             // about 128K with two rows of 16 heads, one call after the other: 200 -> 178 us at 1.47 -> 1.74 GHz)
             const bool row_live = row < live;
-            const int vis = row_live ? min(w.rt.vis0 + token, bt.max_pages * kPage) : 0;
+            int vis = row_live ? min(w.rt.vis0 + token, w.u.pages * kPage) : 0;
+            if (kShared && w.u.prefix && row_live) {
+                // a request shorter than its group's prefix sees its own length of it
+                const int r = w.rt.row0 + token, b = row_request(bt.cu_q, bt.B, r);
+                int q0;
+                const int nq = query_range(bt, b, q0);
+                vis = min(w.u.vis, seq_len(bt, b) - nq + (r - q0) + 1);
+            }
             float m_run = -INFINITY, l_run = 0.0f;
             if (w.t0 < w.t1) {
                 // the row tile's queries out of the ring: value chunks into tensor memory, the rope chunk into its
@@ -777,6 +870,7 @@ dense_mla_decode_kernel(const __grid_constant__ CUtensorMap kvmap, const __grid_
                 if (kh == 0 && row < live) {
                     const float lse2 = l_tot == 0.0f ? -INFINITY : m_run * cs + log2f(l_tot);
                     if (!w.whole) part_lse[piece_slot(cluster, w) * slot_rows + row] = lse2;
+                    else if (kShared && w.u.part) part_lse[part_row(w) + row] = lse2;
                     else if (lse_out != nullptr) lse_out[static_cast<int64_t>(w.rt.row0) * bt.H + row] = lse2 * kLn2;
                 }
             }
@@ -795,7 +889,7 @@ dense_mla_decode_kernel(const __grid_constant__ CUtensorMap kvmap, const __grid_
         };
         uint32_t u = 0, seg = 0, used = 0;                           // used: ring stages before this row tile
         uint32_t clean = 0;                                          // bit i: this row group's P is zero in buffers 2 i and 2 i + 1
-        Walk w(bt, bar.start);
+        Walk<kShared> w(bt, bar.start);
         do {
             const int live = w.rt.tokens * bt.H;
             const bool quad_live = quad * 32 < live, has_tiles = w.t0 < w.t1;
@@ -871,15 +965,17 @@ dense_mla_decode_kernel(const __grid_constant__ CUtensorMap kvmap, const __grid_
                 wait(&bar.stage_lent, seg & 1u);
                 timed_out = __any_sync(0xffffffffu, timed_out);
                 if (timed_out) break;
-                const int width = w.whole ? 64 : 32;                 // dims of 128 bytes
-                const int64_t row0 = w.whole ? static_cast<int64_t>(w.rt.row0) * bt.H : piece_slot(cluster, w) * slot_rows;
+                const bool final = w.whole && !(kShared && w.u.part);
+                const int width = final ? 64 : 32;                   // dims of 128 bytes
+                const int64_t row0 = final ? static_cast<int64_t>(w.rt.row0) * bt.H
+                                           : (w.whole ? part_row(w) : piece_slot(cluster, w) * slot_rows);
                 const int swz = lane & 7;
                 int buf = 0;
 #pragma unroll 1
                 for (int cc = 0; quad_live && cc < 256; cc += width, buf ^= 1) {
                     uint32_t o[32];                                  // the row's 128 bytes
                     ptx::tmem_ld_32x32b_x32(o_addr + cc, o);
-                    if (w.whole) {
+                    if (final) {
                         uint32_t x[32];
                         ptx::tmem_ld_32x32b_x32(o_addr + cc + 32, x);
                         ptx::tmem_wait_ld();
@@ -907,7 +1003,7 @@ dense_mla_decode_kernel(const __grid_constant__ CUtensorMap kvmap, const __grid_
 #pragma unroll
                         for (int h = 0; h < 2; ++h)
                             if (quad * 32 + 16 * h < live)
-                                tma_store_3d(w.whole ? &omap : &pmap, st + h * 2048, dh * 256 + cc, 0,
+                                tma_store_3d(final ? &omap : &pmap, st + h * 2048, dh * 256 + cc, 0,
                                              static_cast<int>(row0) + quad * 32 + 16 * h);
                         bulk_commit();
                     }
@@ -921,13 +1017,19 @@ dense_mla_decode_kernel(const __grid_constant__ CUtensorMap kvmap, const __grid_
                 }
                 used += 2;
                 ++seg;
-            } else if (quad_live) {                                  // sees nothing: zeros
+            } else if (quad_live && !(kShared && w.u.part)) {        // sees nothing: zeros
                 for (int r = quad * 32; r < min(live, quad * 32 + 32); ++r)
                     *reinterpret_cast<uint4*>(out + (static_cast<int64_t>(w.rt.row0) * bt.H + r) * kValueDim + dh * 256 + lane * 8) =
                         make_uint4(0u, 0u, 0u, 0u);
             }
             // the last piece of a split row tile: the combine kernel finds it here
-            if (threadIdx.x == 0 && w.first && w.t0 > 0 && w.t1 == w.rt.tiles)
+            if (kShared && w.t1 == w.rt.tiles && static_cast<int>(threadIdx.x) < w.rt.tokens) {
+                const int at = w.rt.row0 + threadIdx.x;
+                const int where = !w.whole ? bar.first_cluster : (w.u.part ? kWholePart : kWritten);
+                parts[w.u.prefix ? at : bt.T + at] = Parts{where, cluster, w.rt.row0};
+                if (!w.u.part) parts[at] = Parts{kWritten, 0, 0};
+            }
+            if (!kShared && threadIdx.x == 0 && w.first && w.t0 > 0 && w.t1 == w.rt.tiles)
                 meta[cluster] = Meta{static_cast<int64_t>(w.rt.row0) * bt.H, live, bar.first_cluster};
         } while (w.next());
         if (lane == 0) bulk_wait_all();                              // written before the CTA leaves
@@ -950,15 +1052,12 @@ dense_mla_decode_kernel(const __grid_constant__ CUtensorMap kvmap, const __grid_
 constexpr int kCombThreads = 256;
 constexpr int kCombBlocks = 4;     // per SM (32 requests of 8K: 1 block an SM 33 us of the call, 2 to 8 about 15)
 
-// V x 128 dims from d0 on of one row, P pieces at a time: their sums and values are loaded together.
-template <int V, int P>
-__device__ __forceinline__ void join_row(const float* __restrict__ part_o, const float* __restrict__ part_lse,
-                                         const Meta& m, int c, int slot_rows, int row, int d0, int lane,
-                                         uint16_t* __restrict__ out, float* __restrict__ lse_out) {
-    const int n = c - m.first_cluster + 1;
-    auto slot_of = [&](int j) {
-        return static_cast<int64_t>(j == 0 ? 2 * m.first_cluster + 1 : 2 * (m.first_cluster + j)) * slot_rows + row;
-    };
+// V x 128 dims from d0 on of one output row, joined from n parts, P at a time: their sums and values are loaded
+// together.  slot_of(j): the row of part j.
+template <int V, int P, typename F>
+__device__ __forceinline__ void join_row(const float* __restrict__ part_o, const float* __restrict__ part_lse, int n,
+                                         F slot_of, int64_t out_row, int d0, int lane, uint16_t* __restrict__ out,
+                                         float* __restrict__ lse_out) {
     float m_run = -INFINITY, tot = 0.0f;
     float4 acc[V];
 #pragma unroll
@@ -999,10 +1098,10 @@ __device__ __forceinline__ void join_row(const float* __restrict__ part_o, const
     const float inv = tot == 0.0f ? 0.0f : 1.0f / tot;
 #pragma unroll
     for (int v = 0; v < V; ++v)
-        *reinterpret_cast<uint2*>(out + (m.out_row + row) * kValueDim + d0 + v * 128 + lane * 4) =
+        *reinterpret_cast<uint2*>(out + out_row * kValueDim + d0 + v * 128 + lane * 4) =
             make_uint2(pack_bf16x2(acc[v].x * inv, acc[v].y * inv), pack_bf16x2(acc[v].z * inv, acc[v].w * inv));
     if (lse_out != nullptr && d0 == 0 && lane == 0)
-        lse_out[m.out_row + row] = tot == 0.0f ? -INFINITY : (m_run + log2f(tot)) * kLn2;
+        lse_out[out_row] = tot == 0.0f ? -INFINITY : (m_run + log2f(tot)) * kLn2;
 }
 
 __global__ void __launch_bounds__(kCombThreads)
@@ -1041,8 +1140,12 @@ dense_mla_combine_kernel(const float* __restrict__ part_o, const float* __restri
             const int c = list_c[li];
             const int tasks = many ? m.rows : m.rows * 4;
             for (; at < tasks; at += nwarps) {
-                if (many) join_row<4, 2>(part_o, part_lse, m, c, slot_rows, at, 0, lane, out, lse_out);
-                else join_row<1, 4>(part_o, part_lse, m, c, slot_rows, at >> 2, (at & 3) * 128, lane, out, lse_out);
+                const int row = many ? at : at >> 2, n = c - m.first_cluster + 1;
+                auto slot_of = [&](int j) {
+                    return static_cast<int64_t>(j == 0 ? 2 * m.first_cluster + 1 : 2 * (m.first_cluster + j)) * slot_rows + row;
+                };
+                if (many) join_row<4, 2>(part_o, part_lse, n, slot_of, m.out_row + row, 0, lane, out, lse_out);
+                else join_row<1, 4>(part_o, part_lse, n, slot_of, m.out_row + row, (at & 3) * 128, lane, out, lse_out);
             }
             at -= tasks;
         }
@@ -1050,53 +1153,81 @@ dense_mla_combine_kernel(const float* __restrict__ part_o, const float* __restri
     }
 }
 
+// The same with shared prefixes: each query token says where its parts are.
+__global__ void __launch_bounds__(kCombThreads)
+dense_mla_combine_shared_kernel(const float* __restrict__ part_o, const float* __restrict__ part_lse,
+                                const Parts* __restrict__ parts, const int32_t* __restrict__ cu_q, int B, int T, int H,
+                                int clusters, int slot_rows, uint16_t* __restrict__ out, float* __restrict__ lse_out) {
+    ptx::griddep_wait();
+    const int lane = threadIdx.x & 31;
+    const int64_t nwarps = static_cast<int64_t>(gridDim.x) * (kCombThreads / 32);
+    const int r0 = max(0, min(T, __ldg(cu_q))), r1 = max(0, min(T, __ldg(cu_q + B)));
+    const int64_t rows = static_cast<int64_t>(max(0, r1 - r0)) * H;
+    const bool many = rows >= nwarps;
+    for (int64_t at = static_cast<int64_t>(blockIdx.x) * (kCombThreads / 32) + (threadIdx.x >> 5); at < (many ? rows : rows * 4);
+         at += nwarps) {
+        const int64_t row = static_cast<int64_t>(r0) * H + (many ? at : at >> 2);
+        const int token = static_cast<int>(row / H), h = static_cast<int>(row - static_cast<int64_t>(token) * H);
+        const Parts a = parts[token], b = parts[T + token];
+        if (b.first == kWritten) continue;
+        // (numbers of clusters are cut to those there are: a token of no request has none that mean anything)
+        auto count = [&](const Parts& p) {
+            return p.first == kWritten ? 0 : (p.first < 0 ? 1 : max(1, min(p.last, clusters - 1) - min(p.first, clusters - 1) + 1));
+        };
+        auto place = [&](const Parts& p, int j, int64_t whole) {
+            if (p.first < 0) return whole + row;
+            const int first = min(p.first, clusters - 1);
+            const int in_tile = max(0, min(slot_rows - 1, (token - p.row0) * H + h));
+            return static_cast<int64_t>(j == 0 ? 2 * first + 1 : 2 * (first + j)) * slot_rows + in_tile;
+        };
+        const int na = count(a), n = na + count(b);
+        const int64_t whole = 2 * static_cast<int64_t>(clusters) * slot_rows;
+        auto slot_of = [&](int j) {
+            return j < na ? place(a, j, whole) : place(b, j - na, whole + static_cast<int64_t>(T) * H);
+        };
+        if (many) join_row<4, 2>(part_o, part_lse, n, slot_of, row, 0, lane, out, lse_out);
+        else join_row<1, 4>(part_o, part_lse, n, slot_of, row, static_cast<int>(at & 3) * 128, lane, out, lse_out);
+    }
+}
+
 int decode_clusters() { return std::max(1, device_sm_count() / 2); }
 int decode_slot_rows(int64_t T, int64_t H) { return static_cast<int>(std::min<int64_t>(kRows, T * H)); }
 
-}  // namespace
-}  // namespace dsa
-
-extern "C" size_t dsa_dense_mla_decode_workspace_size(int32_t T, int32_t H) {
-    using namespace dsa;
+// Rows of 512 partial results: two slots a cluster, and with shared prefixes two for each output row.
+size_t partial_rows(int32_t T, int32_t H, bool shared) {
+    return static_cast<size_t>(2) * decode_clusters() * decode_slot_rows(T, H) + (shared ? static_cast<size_t>(2) * T * H : 0);
+}
+// ... and in front of them what the combine kernel finds them by.
+size_t directory_bytes(int32_t T, bool shared) {
+    return shared ? (static_cast<size_t>(2) * T * sizeof(Parts) + 15) / 16 * 16 : static_cast<size_t>(decode_clusters()) * sizeof(Meta);
+}
+size_t workspace_bytes_of(int32_t T, int32_t H, bool shared) {
     if (T <= 0 || H <= 0) return 0;
-    const size_t c = static_cast<size_t>(decode_clusters()), rows = static_cast<size_t>(decode_slot_rows(T, H));
-    return c * sizeof(Meta) + 2 * c * rows * (kValueDim + 1) * sizeof(float);
+    return directory_bytes(T, shared) + partial_rows(T, H, shared) * (kValueDim + 1) * sizeof(float);
 }
 
-extern "C" dsa_status dsa_dense_mla_decode(const void* q_bf16, const void* kv_pool, int64_t num_pages,
-                                           const int32_t* block_table, int32_t max_pages, const int32_t* seq_lens,
-                                           const int32_t* cu_q, int32_t B, int32_t T, int32_t H, float scale,
-                                           void* out_bf16, float* lse, void* workspace, size_t workspace_bytes,
-                                           int32_t* dev_err, void* stream) {
-    using namespace dsa;
-    if (H != 16 && H != 32 && H != 64 && H != 128) return DSA_ERR_UNSUPPORTED;
-    if (T < 0 || B < 0 || max_pages < 0 || num_pages < 0) return DSA_ERR_INVALID_ARG;
-    if (T == 0 || B == 0) return DSA_OK;
-    if (num_pages < 1 || max_pages < 1) return DSA_ERR_INVALID_ARG;
-    if (!q_bf16 || !kv_pool || !block_table || !seq_lens || !cu_q || !out_bf16) return DSA_ERR_INVALID_ARG;
-    if (!aligned16(q_bf16) || !aligned16(kv_pool) || !aligned16(out_bf16)) return DSA_ERR_INVALID_ARG;
-    if (!(scale > 0.0f) || !(scale < INFINITY)) return DSA_ERR_INVALID_ARG;
-    if ((num_pages + 1) * kPage >= 0x7fffffffLL || static_cast<int64_t>(max_pages) * kPage >= 0x7fffffffLL ||
-        static_cast<int64_t>(T) * H >= 0x7fffffffLL || B > kMaxRequests)
-        return DSA_ERR_UNSUPPORTED;
-    // the schedule counts key tiles in 32 bits
-    if (static_cast<int64_t>(T) * max_pages >= 0x7fffffffLL) return DSA_ERR_UNSUPPORTED;
-    const size_t need = dsa_dense_mla_decode_workspace_size(T, H);
-    if (workspace == nullptr || !aligned16(workspace) || workspace_bytes < need) return DSA_ERR_INVALID_ARG;
+template <bool kShared>
+dsa_status launch_decode(const void* q_bf16, const void* kv_pool, int64_t num_pages, const int32_t* block_table,
+                         const Batch& bt, float scale, void* out_bf16, float* lse, void* workspace,
+                         size_t workspace_bytes, int32_t* dev_err, void* stream) {
+    const int T = bt.T, H = bt.H;
+    if (workspace == nullptr || !aligned16(workspace) || workspace_bytes < workspace_bytes_of(T, H, kShared)) return DSA_ERR_INVALID_ARG;
     auto encode = attn::tensor_map_encoder();
     if (encode == nullptr) return DSA_ERR_CUDA;
     const int clusters = decode_clusters(), slot_rows = decode_slot_rows(T, H);
-    Meta* meta = static_cast<Meta*>(workspace);
-    float* part_o = reinterpret_cast<float*>(meta + clusters);
-    float* part_lse = part_o + static_cast<size_t>(2) * clusters * slot_rows * kValueDim;
+    const size_t rows = partial_rows(T, H, kShared);
+    float* part_o = reinterpret_cast<float*>(static_cast<unsigned char*>(workspace) + directory_bytes(T, kShared));
+    float* part_lse = part_o + rows * kValueDim;
+    Meta* meta = kShared ? nullptr : static_cast<Meta*>(workspace);
+    Parts* parts = kShared ? static_cast<Parts*>(workspace) : nullptr;
     CUtensorMap kvmap, qmap, omap, pmap;
     if (!attn::encode_bf16_3d(encode, &kvmap, kv_pool, kLatentDim, 1, num_pages * kPage, kLatentDim, kLatentDim, 64, kPage) ||
         !attn::encode_bf16_3d(encode, &qmap, q_bf16, kLatentDim, 1, static_cast<uint64_t>(T) * H, kLatentDim, kLatentDim, 64, kRows) ||
         !attn::encode_bf16_3d(encode, &omap, out_bf16, kValueDim, 1, static_cast<uint64_t>(T) * H, kValueDim, kValueDim, 64, 16) ||
-        !attn::encode_f32_rows(encode, &pmap, part_o, kValueDim, static_cast<uint64_t>(2) * clusters * slot_rows, 32, 16))
+        !attn::encode_f32_rows(encode, &pmap, part_o, kValueDim, rows, 32, 16))
         return DSA_ERR_CUDA;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    if (cudaFuncSetAttribute(dense_mla_decode_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    if (cudaFuncSetAttribute(dense_mla_decode_kernel<kShared>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              static_cast<int>(kDecSmem)) != cudaSuccess)
         return DSA_ERR_CUDA;
     // both kernels are programmatic dependents: scheduled as the CTAs of the one before end, they wait for all of it
@@ -1110,16 +1241,85 @@ extern "C" dsa_status dsa_dense_mla_decode(const void* q_bf16, const void* kv_po
     cfg.stream = s;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    if (cudaLaunchKernelEx(&cfg, dense_mla_decode_kernel, kvmap, qmap, omap, pmap, static_cast<const uint16_t*>(kv_pool),
-                           static_cast<int>(num_pages), block_table, Batch{seq_lens, cu_q, B, T, H, max_pages, kRows / H},
-                           scale, static_cast<uint16_t*>(out_bf16), lse, part_lse, meta, slot_rows, dev_err) != cudaSuccess)
+    if (cudaLaunchKernelEx(&cfg, dense_mla_decode_kernel<kShared>, kvmap, qmap, omap, pmap, static_cast<const uint16_t*>(kv_pool),
+                           static_cast<int>(num_pages), block_table, bt, scale, static_cast<uint16_t*>(out_bf16), lse,
+                           part_lse, meta, parts, slot_rows, dev_err) != cudaSuccess)
         return DSA_ERR_CUDA;
     cfg.gridDim = dim3(2 * clusters * kCombBlocks);
     cfg.blockDim = dim3(kCombThreads);
     cfg.dynamicSmemBytes = 0;
-    if (cudaLaunchKernelEx(&cfg, dense_mla_combine_kernel, static_cast<const float*>(part_o),
-                           static_cast<const float*>(part_lse), static_cast<const Meta*>(meta), clusters, slot_rows,
-                           static_cast<uint16_t*>(out_bf16), lse) != cudaSuccess)
-        return DSA_ERR_CUDA;
+    cudaError_t e;
+    if constexpr (kShared)
+        e = cudaLaunchKernelEx(&cfg, dense_mla_combine_shared_kernel, static_cast<const float*>(part_o),
+                               static_cast<const float*>(part_lse), static_cast<const Parts*>(parts), bt.cu_q, bt.B, T, H,
+                               clusters, slot_rows, static_cast<uint16_t*>(out_bf16), lse);
+    else
+        e = cudaLaunchKernelEx(&cfg, dense_mla_combine_kernel, static_cast<const float*>(part_o),
+                               static_cast<const float*>(part_lse), static_cast<const Meta*>(meta), clusters, slot_rows,
+                               static_cast<uint16_t*>(out_bf16), lse);
+    if (e != cudaSuccess) return DSA_ERR_CUDA;
     return launch_status();
+}
+
+// What both calls refuse before the workspace; DSA_OK with *nothing set where there is nothing to do.
+dsa_status check_decode(const void* q_bf16, const void* kv_pool, int64_t num_pages, const int32_t* block_table,
+                        const Batch& bt, float scale, const void* out_bf16, bool* nothing) {
+    const int T = bt.T, B = bt.B, H = bt.H, max_pages = bt.max_pages;
+    *nothing = false;
+    if (H != 16 && H != 32 && H != 64 && H != 128) return DSA_ERR_UNSUPPORTED;
+    if (T < 0 || B < 0 || max_pages < 0 || num_pages < 0) return DSA_ERR_INVALID_ARG;
+    *nothing = T == 0 || B == 0;
+    if (*nothing) return DSA_OK;
+    if (num_pages < 1 || max_pages < 1) return DSA_ERR_INVALID_ARG;
+    if (!q_bf16 || !kv_pool || !block_table || !bt.seq_lens || !bt.cu_q || !out_bf16) return DSA_ERR_INVALID_ARG;
+    if (!aligned16(q_bf16) || !aligned16(kv_pool) || !aligned16(out_bf16)) return DSA_ERR_INVALID_ARG;
+    if (!(scale > 0.0f) || !(scale < INFINITY)) return DSA_ERR_INVALID_ARG;
+    if ((num_pages + 1) * kPage >= 0x7fffffffLL || static_cast<int64_t>(max_pages) * kPage >= 0x7fffffffLL ||
+        static_cast<int64_t>(T) * H >= 0x7fffffffLL || B > kMaxRequests)
+        return DSA_ERR_UNSUPPORTED;
+    // the schedule counts key tiles in 32 bits
+    if (static_cast<int64_t>(T) * max_pages >= 0x7fffffffLL) return DSA_ERR_UNSUPPORTED;
+    return DSA_OK;
+}
+
+}  // namespace
+}  // namespace dsa
+
+extern "C" size_t dsa_dense_mla_decode_workspace_size(int32_t T, int32_t H) { return dsa::workspace_bytes_of(T, H, false); }
+
+extern "C" dsa_status dsa_dense_mla_decode(const void* q_bf16, const void* kv_pool, int64_t num_pages,
+                                           const int32_t* block_table, int32_t max_pages, const int32_t* seq_lens,
+                                           const int32_t* cu_q, int32_t B, int32_t T, int32_t H, float scale,
+                                           void* out_bf16, float* lse, void* workspace, size_t workspace_bytes,
+                                           int32_t* dev_err, void* stream) {
+    using namespace dsa;
+    const Batch bt{seq_lens, cu_q, B, T, H, max_pages, H > 0 ? kRows / H : 0, nullptr, nullptr, 0};
+    bool nothing;
+    const dsa_status st = check_decode(q_bf16, kv_pool, num_pages, block_table, bt, scale, out_bf16, &nothing);
+    if (st != DSA_OK || nothing) return st;
+    return launch_decode<false>(q_bf16, kv_pool, num_pages, block_table, bt, scale, out_bf16, lse, workspace,
+                                workspace_bytes, dev_err, stream);
+}
+
+extern "C" size_t dsa_dense_mla_decode_shared_workspace_size(int32_t T, int32_t H) { return dsa::workspace_bytes_of(T, H, true); }
+
+extern "C" dsa_status dsa_dense_mla_decode_shared(const void* q_bf16, const void* kv_pool, int64_t num_pages,
+                                                  const int32_t* block_table, int32_t max_pages,
+                                                  const int32_t* seq_lens, const int32_t* cu_q, int32_t B, int32_t T,
+                                                  int32_t H, const int32_t* cu_group, const int32_t* shared_lens,
+                                                  int32_t G, float scale, void* out_bf16, float* lse, void* workspace,
+                                                  size_t workspace_bytes, int32_t* dev_err, void* stream) {
+    using namespace dsa;
+    const Batch bt{seq_lens, cu_q, B, T, H, max_pages, H > 0 ? kRows / H : 0, cu_group, shared_lens, G};
+    bool nothing;
+    const dsa_status st = check_decode(q_bf16, kv_pool, num_pages, block_table, bt, scale, out_bf16, &nothing);
+    if (st != DSA_OK) return st;
+    if (G < 0) return DSA_ERR_INVALID_ARG;
+    if (nothing) return DSA_OK;
+    if (G > 0 && (!cu_group || !shared_lens)) return DSA_ERR_INVALID_ARG;
+    // groups' tiles come on top of the requests'; the parts' rows are counted in 32 bits
+    if (G > kMaxRequests || static_cast<int64_t>(T) * max_pages >= 0x3fffffffLL || static_cast<int64_t>(T) * H >= 0x3ff00000LL)
+        return DSA_ERR_UNSUPPORTED;
+    return launch_decode<true>(q_bf16, kv_pool, num_pages, block_table, bt, scale, out_bf16, lse, workspace,
+                               workspace_bytes, dev_err, stream);
 }

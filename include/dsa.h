@@ -16,7 +16,9 @@
  * workspace.
  * Dense latent attention (contexts and layers without a selection): the latent row's norm, rotary
  * embedding and paged store, the prompt's attention in expanded form, the attention of new tokens
- * over the whole paged cache in absorbed form, and the verification of drafted tokens.
+ * over the whole paged cache in absorbed form (also behind prefixes that requests share), and the
+ * verification of drafted tokens.  Around a step: its tables from the requests' lengths, and the
+ * sampling of tokens from logits.
  *
  * Conventions shared by every call
  * --------------------------------
@@ -77,7 +79,8 @@ typedef enum {
 #define DSA_DEVERR_INDEX_RANGE 0x4 /* a top-k index outside [0, v_r) (entry skipped) */
 #define DSA_DEVERR_TIMEOUT 0x8     /* a bounded spin-wait gave up */
 #define DSA_DEVERR_POSITION 0x10   /* a rotary position outside [0, max_position) */
-#define DSA_DEVERR_PROB 0x20       /* verify: a distribution without a positive finite entry */
+#define DSA_DEVERR_PROB 0x20       /* verify, sample: a distribution without a positive finite entry */
+#define DSA_DEVERR_NO_PAGE 0x40    /* step tables: more pages needed than the free stack holds */
 
 /* Flags of dsa_indexer_logits. */
 #define DSA_Q_ROTATE 0x1u          /* Hadamard-rotate each query head before quantising it */
@@ -100,6 +103,9 @@ typedef enum {
 
 /* Flag of dsa_dense_mla_prefill: a query sees the keys up to its own position only. */
 #define DSA_CAUSAL 0x40u
+
+/* Flag of dsa_sample_tokens: the logits are bf16 (default: fp32). */
+#define DSA_LOGITS_BF16 0x80u
 
 /* Fixed shape constants of the path. */
 #define DSA_PAGE_SIZE 64
@@ -657,6 +663,32 @@ dsa_status dsa_dense_mla_decode(const void* q_bf16, const void* kv_pool, int64_t
                                 float* lse, void* workspace, size_t workspace_bytes, int32_t* dev_err, void* stream);
 
 /*
+ * dsa_dense_mla_decode_shared -- dsa_dense_mla_decode for a batch in which groups of requests have their first
+ * pages in common (a system prompt, a document, samples of one prompt): a group's keys are read once for the query
+ * rows of all its requests, each request's other keys for itself.
+ * Source: as dsa_dense_mla_decode; merge_attn_states (vllm mla/common.py) joins the two by log-sum-exp.
+ *   The same results as dsa_dense_mla_decode on the same tables, up to the order of sums.  Group g has the requests
+ *   [cu_group[g], cu_group[g + 1]); positions < shared_lens[g], whole pages of them, are read through the first
+ *   request's row of the block table.  A request of a group sees no more than its own length of the prefix.
+ *   Requests outside all groups have nothing in common with others.
+ *   An infinite or NaN value in a shared prefix may reach every row of the group.
+ * Arguments: as dsa_dense_mla_decode, and
+ *   cu_group       int32 [G + 1], not falling, within [0, B].   shared_lens int32 [G].   Nullable when G = 0.
+ *                  G at most 16384; T * max_pages < 2^30.
+ *   workspace      dsa_dense_mla_decode_shared_workspace_size(T, H) bytes, as there (two fp32 partial results for
+ *                  each row on top: 4 KB).
+ *   dev_err        nullable; DSA_DEVERR_PAGE_RANGE and DSA_DEVERR_TIMEOUT as dsa_dense_mla_decode,
+ *                  DSA_DEVERR_INDEX_RANGE also for a range of requests that falls or leaves [0, B] (cut to it), or a
+ *                  prefix past max_pages * 64 (cut to it).
+ */
+size_t dsa_dense_mla_decode_shared_workspace_size(int32_t T, int32_t H);
+dsa_status dsa_dense_mla_decode_shared(const void* q_bf16, const void* kv_pool, int64_t num_pages,
+                                       const int32_t* block_table, int32_t max_pages, const int32_t* seq_lens,
+                                       const int32_t* cu_q, int32_t B, int32_t T, int32_t H, const int32_t* cu_group,
+                                       const int32_t* shared_lens, int32_t G, float scale, void* out_bf16, float* lse,
+                                       void* workspace, size_t workspace_bytes, int32_t* dev_err, void* stream);
+
+/*
  * dsa_verify_drafts -- verification of drafted tokens (target-verify of the q_len >= 2 rows) from
  * given random numbers.
  *   The source pages score the drafted tokens' rows (sglang dsa_indexer.py, next_n >= 2 target
@@ -690,6 +722,72 @@ dsa_status dsa_verify_drafts(const float* target_probs, int64_t target_ld, const
                              int64_t draft_ld, int32_t V, const int32_t* draft_tokens, const int32_t* cu_q, int32_t B,
                              int32_t T, const float* accept_u, const float* sample_u, int32_t* out_tokens,
                              int32_t* accepted, int32_t* dev_err, void* stream);
+
+/*
+ * dsa_sample_tokens -- the next token of each row of logits, from given random numbers, or the filtered
+ * distribution itself (as dsa_verify_drafts takes it).
+ *   The source pages leave the sampling to the engine; these are the usual rules.
+ *   w_i = exp((z_i - max z) / temperature).  Order: larger z first, equal ones by index.  Kept are, in that order,
+ *   the first top_k; of those the ones before which less than top_p of their mass lies (the first one always); of
+ *   those the ones with w >= min_p (min_p above 1 counts as 1).
+ *   tokens[r]: the least v with sum_{i <= v} w_i > u[r] * sum w over what is kept (u >= 1: the last one).
+ *   probs[r, v] = w_v / sum w, 0 for what is not kept.
+ *   temperature <= 0 (or NaN): the largest entry, the lowest index among equals; probs 1 there.
+ *   Weights are whole multiples of 2^-45 of the largest (relative error about 2^-35 before) and their sums are exact,
+ *   so a token does not depend on how the work is split; an entry below 2^-46 of the largest is never drawn.  probs are
+ *   rounded to fp32 once, from the same weights before they are cut.
+ *   A logit that is NaN counts as -infinity (never kept), +infinity as the type's largest number.
+ * Arguments:
+ *   logits         fp32 (DSA_LOGITS_BF16: bf16) rows of V entries, stride ld >= V; element alignment.
+ *   V              1 .. 2^18.   R rows.   flags 0 or DSA_LOGITS_BF16.
+ *   temperature    fp32 [R] (NULL: 1).   top_k int32 [R] (NULL, <= 0 or >= V: all).   top_p fp32 [R] (NULL, >= 1 or
+ *                  NaN: all; <= 0: the first).   min_p fp32 [R] (NULL, <= 0 or NaN: all).
+ *   u              fp32 [R]: uniform numbers in [0, 1).
+ *   tokens         int32 [R].   probs nullable, fp32 rows of stride ld_probs >= V, apart from logits.
+ *   dev_err        nullable; DSA_DEVERR_PROB for a row without a finite logit (token -1, probs 0).
+ */
+dsa_status dsa_sample_tokens(const void* logits, int64_t ld, int32_t V, int32_t R, uint32_t flags,
+                             const float* temperature, const int32_t* top_k, const float* top_p, const float* min_p,
+                             const float* u, int32_t* tokens, float* probs, int64_t ld_probs, int32_t* dev_err,
+                             void* stream);
+
+/*
+ * dsa_step_tables -- the tables of a step from the requests' lengths: block table, slot mapping, positions, row
+ * offsets and lengths, with the pages that the step takes from and gives back to a free stack.
+ * Source: vllm mla/common.py, MLACommonMetadataBuilder.build (query_start_loc, seq_lens, block_table and
+ * slot_mapping, made on the host there); the source pages leave the pages to the engine.
+ *   Request b holds cached_lens[b] tokens in its first page_counts[b] pages and gets q_lens[b] new ones;
+ *   q_lens[b] < 0: it ends.  A request's first keep_pages[b] pages are not its own (a shared prefix).
+ *   Rows: cu_q[b + 1] - cu_q[b] = n_b = max(q_lens[b], 0), cut where T rows are used up (DSA_DEVERR_INDEX_RANGE).
+ *   Given back: requests that end push their pages keep_pages[b] .. page_counts[b] - 1 onto the free stack,
+ *   requests and pages in order; their seq_lens and page_counts_out are 0.  Their table rows stay as they are.
+ *   Taken: the others need ceil((cached_lens[b] + n_b) / 64) pages; the i-th page that is missing (requests in
+ *   order, pages in order) is the i-th from the top of the stack, pages given back in this call included.
+ *   seq_lens[b] = cached_lens[b] + n_b; page_counts_out[b] counts the pages mapped then (never fewer than before).
+ *   New token j of request b: position cached_lens[b] + j, slot block_table[b][position / 64] * 64 +
+ *   position % 64.  Rows >= cu_q[B]: position 0, slot -1.
+ * Arguments:
+ *   cached_lens, q_lens, page_counts  int32 [B].   keep_pages int32 [B], nullable (0).
+ *   block_table      int32 [B, max_pages], updated in place (only entries that get a page are written).
+ *   free_pages       int32 [num_pages], updated in place: the stack, *free_count entries, the last one on top.
+ *                    Entries above the new top are left over and mean nothing.
+ *   free_count       int32 [1].   free_count_out int32 [1].
+ *   seq_lens, page_counts_out int32 [B], cu_q int32 [B + 1], positions and slot_mapping int64 [T].
+ *   Every output lies apart from every input and from the other outputs (a loop swaps cached_lens with seq_lens,
+ *   page_counts with page_counts_out and free_count with free_count_out from step to step).
+ *   B at most 16384, B * max_pages < 2^31, num_pages < 2^25.
+ *   Lengths below 0 count as 0; counts are cut to [0, max_pages], keep_pages to [0, page_counts], *free_count
+ *   to [0, num_pages].
+ *   dev_err          nullable; DSA_DEVERR_NO_PAGE when the stack runs out (table entries -1 that are not counted,
+ *                    slots -1), DSA_DEVERR_PAGE_RANGE for a page id outside [0, num_pages) in the table or on the
+ *                    stack (the entry -1, slots -1), DSA_DEVERR_INDEX_RANGE for rows that were cut, tokens past
+ *                    max_pages * 64 (slot -1) or a stack that would pass num_pages entries (cut).
+ */
+dsa_status dsa_step_tables(const int32_t* cached_lens, const int32_t* q_lens, const int32_t* page_counts,
+                           const int32_t* keep_pages, int32_t B, int32_t* block_table, int32_t max_pages,
+                           int64_t num_pages, int32_t* free_pages, const int32_t* free_count, int32_t* seq_lens,
+                           int32_t* page_counts_out, int32_t* free_count_out, int32_t* cu_q, int64_t* positions,
+                           int64_t* slot_mapping, int32_t T, int32_t* dev_err, void* stream);
 
 /*
  * dsa_read_device_error -- synchronise `stream`, copy the device error word to the host
