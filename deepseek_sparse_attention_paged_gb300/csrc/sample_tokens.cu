@@ -5,19 +5,19 @@
 // first k; top-p those of them before which less than p of their mass lies; min-p those with w >= min_p.  The
 // token is the least v with sum_{i <= v} w_i > u sum w over what is kept.
 //
-// Sums: a token must not depend on how a sum is split, and a border between two of 10^5 tokens is missed where
-// sums are off by 10^-5 of a weight.  So a weight is formed to about 2^-35 of itself (z - max z and its product
-// with log2 e / t as unevaluated pairs of fp32, 2^(j / 1024) from a table of 46-bit integers, the rest a cubic)
-// and held as an integer, 2^45 the largest: integer sums do not round, in any order, and u S and p M are compared
-// exactly (24 x 64 bits).  The fp64 unit would take ten times as long as the read of the row.
+// Sums: a token must not depend on how a sum is split, and a border between two of 10^5 tokens is missed where sums
+// are off by 10^-5 of a weight.  So a weight is formed to 2^-30 of itself (2^-35 for the largest, which count in every
+// sum) and held as an integer, 2^46 about the largest: integer sums do not round, in any order, and u S and p M are
+// compared exactly (24 x 64 bits).  1024 log2 w = n + f: one fused product leaves f with all the bits it needs
+// (|f| <= 1/2), 2^(n / 1024) is a shift and a table of 1024 integers, 2^(f / 1024) a quadratic.  The fp64 unit would take ten
+// times as long as the read of the row.
 //
 // A row is split over the CTAs of a cluster, each with a slice of it in shared memory: logits are read from global
 // memory once.
 //   * top-k up to 1024: the k-th largest of all threads' maxima is a bound from below that few more than k
-//     entries pass (with G threads about -G ln(1 - k / G)); those go to the first CTA, which sorts them and does the
-//     rest alone.
+//     entries pass (with G threads about -G ln(1 - k / G)); those go to the first CTA, which does the rest alone.
 //   * top-p without top-k: masses of 1024 bins of z (32 an octave of w) find the bin of the border; its entries
-//     go to the first CTA, which sorts them and finds the last one kept.  A second pass sums what is kept.
+//     go to the first CTA, which finds the last one kept.  A second pass sums what is kept.
 //   * where more entries than fit (2048) come together (ties, a temperature far above 1), or for a larger top-k:
 //     bisection over the 32 bits of z, a pass over the slices each.
 #include <float.h>
@@ -30,19 +30,21 @@
 namespace dsa {
 namespace {
 
-constexpr int kThreads = 512;
-constexpr int kWarps = kThreads / 32;
 constexpr int kMaxCtas = 8;
-constexpr int kList = 2048;                    // entries that the first CTA sorts
+constexpr int kList = 2048;                    // entries that the first CTA takes in
+constexpr int kRegion = kList / kMaxCtas;      // of one CTA without a count beforehand
+constexpr int kFew = 128;                      // entries that are compared with one another
 constexpr int kMaxTopK = 1024;
 constexpr int kBins = 1024, kBinsPerOctave = 32;
-constexpr int kOne = 45;                       // fraction bits of a weight
-constexpr int kMaxSampleVocab = 1 << 18;       // sums of weights stay below 2^63
+constexpr int kSelectBins = 256;
+constexpr int kOne = 46;                       // fraction bits of a weight
+constexpr int kMaxSampleVocab = 1 << 18;       // sums of weights stay below 2^64
 constexpr int kPowBits = 10;
 
-// 2^(j / 1024) with kOne fraction bits, by the exponential series in 62-bit fixed point.
+// 2^(j / 1024) with kOne - 1 fraction bits, by the exponential series in 62-bit fixed point, and with 31.
 struct PowTable {
-    uint64_t v[1 << kPowBits];
+    uint64_t fine[1 << kPowBits];
+    uint32_t coarse[1 << kPowBits];
 };
 constexpr PowTable make_pow_table() {
     using u128 = unsigned __int128;
@@ -57,7 +59,8 @@ constexpr PowTable make_pow_table() {
             sum += term;
             term = ((term * x) >> 62) / n;
         }
-        t.v[j] = static_cast<uint64_t>((sum + (u128(1) << (61 - kOne))) >> (62 - kOne));
+        t.fine[j] = static_cast<uint64_t>((sum + (u128(1) << (62 - kOne))) >> (63 - kOne));
+        t.coarse[j] = static_cast<uint32_t>((sum + (u128(1) << 30)) >> 31);
     }
     return t;
 }
@@ -79,30 +82,42 @@ struct SampleArgs {
     int32_t* err;
 };
 
+template <int NT>
 struct alignas(16) SampleShared {
+    static constexpr int kStage = kMaxCtas * NT / 2;
+    static_assert(kStage >= kBins && kStage >= 2 * kFew && kStage <= kList, "scratch");
     union {
-        float maxima[kMaxCtas * kThreads];     // every thread's largest entry, of all CTAs
+        float maxima[kMaxCtas * NT];           // every thread's largest entry, of all CTAs
         uint2 hist[kBins];                     // masses (low and high word)
-        uint64_t stage[kList];                 // entries of this CTA on their way to the first one
+        uint64_t stage[kStage];                // entries of this CTA on their way to the first one
+        struct {
+            uint64_t entry[kFew], mass[kFew];
+        } few;
     };
     uint64_t list[kList];                      // first CTA: (order key of z, ~index)
-    uint64_t pow[1 << kPowBits];
+    uint32_t pow[1 << kPowBits];
+    uint2 sel_mass[kSelectBins];
+    uint32_t sel_count[kSelectBins];
+    uint64_t sel_value;
+    uint64_t sum, limit;
     // written by all CTAs of the cluster
     float cta_max[kMaxCtas];
     int cta_index[kMaxCtas];
     uint32_t cta_count[kMaxCtas];
     uint64_t cta_sum[2][kMaxCtas];
-    uint32_t list_count;
     uint32_t cut_key;
     int cut_index;
     int bin;
     uint64_t bin_before;
     // this CTA's
-    uint64_t warp_sum[2][kWarps];
-    float warp_max[kWarps];
-    uint32_t stage_count, stage_base;
+    uint64_t warp_sum[2][NT / 32];
+    uint32_t warp_lo[NT / 32], warp_hi[NT / 32];
+    float warp_max[NT / 32];
+    uint32_t stage_count;
     int found;
+    double t_ln_min;                           // temperature ln min_p
     float rh, rl, zmin;
+    float2 inv;
 };
 
 // ---------------------------------------------------------------- cluster
@@ -134,12 +149,6 @@ __device__ __forceinline__ uint2 get2(const void* p, uint32_t rank) {
     asm volatile("ld.shared::cluster.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(remote(p, rank)) : "memory");
     return v;
 }
-__device__ __forceinline__ uint32_t add_remote(void* p, uint32_t rank, uint32_t v) {
-    uint32_t old;
-    asm volatile("atom.shared::cluster.add.u32 %0, [%1], %2;" : "=r"(old) : "r"(remote(p, rank)), "r"(v) : "memory");
-    return old;
-}
-
 // ---------------------------------------------------------------- numbers
 
 // Unsigned order of finite fp32 numbers and -infinity; -0 and 0 are one number.
@@ -151,75 +160,118 @@ __device__ __forceinline__ float key_value(uint32_t k) {
     return __uint_as_float((k & 0x80000000u) != 0u ? k & 0x7fffffffu : ~k);
 }
 
-// max z, log2 e / t = rh + rl
+// The largest logit and 1024 log2 e / t = rh + rl.
 struct Scale {
     float top, rh, rl;
+    int e0;                    // weights are held relative to 2^e0: e0 - 1 <= log2 e / t max z < e0
+    bool wide;                 // log2 e / t max z past the range of `split`: relative to twice the largest weight
 };
+constexpr float kMagic = 12582912.0f;                        // 1.5 2^23: adding it rounds to whole numbers
+constexpr int kMagicBits = 0x4b400000;
+constexpr float kWide = 3900.0f;                             // |1024 y| stays below 2^22 down to weights of 2^-160
+constexpr int kFine = 8;                                     // octaves below 2^e0 with the fine table
 
-// log2 w, as a pair
-__device__ __forceinline__ float log2_weight(float z, const Scale& c, float& lo) {
-    const float s = __fsub_rn(z, c.top);
-    const float e = two_sum_err(z, -c.top, s);
-    const float y = __fmul_rn(s, c.rh);
-    lo = __fadd_rn(__fmaf_rn(s, c.rh, -y), __fmaf_rn(s, c.rl, __fmul_rn(e, c.rh)));
-    return y;
+__device__ __forceinline__ Scale make_scale(float top, float rh, float rl) {
+    const float y = top * rh * (1.0f / 1024.0f);             // infinite where rh overflowed: wide
+    Scale c{top, rh, rl, 1, !(fabsf(y) < kWide)};
+    // 1 more where rounding may have lost it (a scale of all weights)
+    if (!c.wide) c.e0 = static_cast<int>(floorf(y + 0x1p-10f)) + 1;
+    return c;
 }
-// w 2^kOne = x 2^-shift, x of 46 bits, for y = log2 w in [-200, 0]
-__device__ __forceinline__ uint64_t power(float y, float lo, const uint64_t* pow, int& shift) {
-    constexpr float kMagic = 12582912.0f;                    // 1.5 2^23: adding it rounds to whole numbers
-    const float t = __fmaf_rn(y, 1024.0f, kMagic);
-    const int n = __float_as_int(t) - __float_as_int(kMagic);
-    const float f = __fadd_rn(__fmaf_rn(__fsub_rn(t, kMagic), -1.0f / 1024.0f, y), lo);   // |f| <= 2^-11
-    // 2^f - 1 with 41 fraction bits: ln 2, ln^2 2 / 2, ln^3 2 / 6 times 2^41
-    constexpr float c1 = 0.69314718055994531f * 0x1p41f, c2 = 0.24022650695910072f * 0x1p41f, c3 = 0.05550410866482158f * 0x1p41f;
+
+// shr and shl of more than 31 places give 0
+__device__ __forceinline__ uint32_t shr(uint32_t v, int n) {
+    uint32_t r;
+    asm("shr.u32 %0, %1, %2;" : "=r"(r) : "r"(v), "r"(n));
+    return r;
+}
+
+// w 2^kOne = x 2^-shift, x of 46 bits, for log2 w = (n + f) / 1024, |f| <= 1 / 2
+__device__ __forceinline__ uint64_t power_fine(int n, float f, int e0, int& shift) {
+    // 2^(f / 1024) - 1 with 41 fraction bits: ln 2 / 1024 and ln^2 2 / 2 / 1024^2 times 2^41
+    constexpr float c1 = 0.69314718055994531f * 0x1p31f, c2 = 0.24022650695910072f * 0x1p21f, c3 = 0.05550410866482158f * 0x1p11f;
     const int g = __float2int_rn(f * __fmaf_rn(f, __fmaf_rn(f, c3, c2), c1));
-    const uint64_t p = pow[n & ((1 << kPowBits) - 1)];
-    shift = -(n >> kPowBits);
+    const uint64_t p = kPow.fine[n & ((1 << kPowBits) - 1)];
+    shift = e0 - 1 - (n >> kPowBits);
     return p + static_cast<uint64_t>((static_cast<int64_t>(static_cast<int>(p >> 15)) * g) >> 26);
 }
-// w 2^kOne as a whole number; 0 below 2^-46
-__device__ __forceinline__ uint64_t weight(float z, const Scale& c, const uint64_t* pow) {
-    float lo;
-    const float y = log2_weight(z, c, lo);
-    if (!(y > -46.0f)) return 0;
-    int shift;
-    const uint64_t x = power(y, lo, pow, shift);
-    return (x + ((1ull << shift) >> 1)) >> shift;
+
+// 1024 log2 of the weight relative to 2^e0 as n + f, n as it stands in the bits of a float past kMagic.  The product's
+// rounding errors are those of f alone (2^-25 of 1/1024 octave), as n is taken from it before it is rounded.
+__device__ __forceinline__ int split(float z, const Scale& c, float& f) {
+    const float t = __fmaf_rn(z, c.rh, kMagic);
+    f = __fmaf_rn(z, c.rl, __fmaf_rn(z, c.rh, -__fsub_rn(t, kMagic)));
+    return __float_as_int(t);
+}
+// The same for rows whose scale passes the table's range: z - max z and its product as pairs first.
+__device__ __noinline__ int split_wide(float z, float top, float rh, float rl, float& f) {
+    const float s = __fsub_rn(z, top);
+    const float e = two_sum_err(z, -top, s);
+    const float y = __fmul_rn(s, rh);
+    const float lo = __fadd_rn(__fmaf_rn(s, rh, -y), __fmaf_rn(s, rl, __fmul_rn(e, rh)));
+    if (!(y > -200.0f * 1024.0f)) {
+        f = 0.0f;
+        return kMagicBits - 400 * 1024;
+    }
+    const float t = __fadd_rn(y, kMagic);
+    f = __fadd_rn(__fsub_rn(y, __fsub_rn(t, kMagic)), lo);
+    return __float_as_int(t);
 }
 
-// 1 / sum as a pair; probabilities from it
-struct Inverse {
-    float hi, lo;
-};
-__device__ __forceinline__ Inverse inverse(uint64_t sum) {
-    const double d = 1.0 / static_cast<double>(sum);
-    const float hi = static_cast<float>(d);
-    return Inverse{hi, static_cast<float>(d - static_cast<double>(hi))};
+// Mantissa (31 fraction bits, in [1, 2)) and exponent of the weight relative to 2^e0.
+__device__ __forceinline__ uint32_t power(int bits, float f, const uint32_t* pow) {
+    // 2^(f / 1024) - 1 with 32 fraction bits, rounded by the addition of kMagic
+    constexpr float c1 = 0.69314718055994531f * 0x1p22f, c2 = 0.24022650695910072f * 0x1p12f;
+    const int g = __float_as_int(__fmaf_rn(f, __fmaf_rn(f, c2, c1), kMagic)) - kMagicBits;
+    const uint32_t p = pow[bits & ((1 << kPowBits) - 1)];
+    // p g / 2^32 for unsigned p: the signed product counts p - 2^32
+    return p + static_cast<uint32_t>(__mulhi(static_cast<int>(p), g) + g);
 }
-__device__ __forceinline__ float probability(float z, const Scale& c, const uint64_t* pow, Inverse inv) {
-    float lo;
-    const float y = log2_weight(z, c, lo);
-    if (!(y > -160.0f)) return 0.0f;
-    int shift;
-    const uint64_t x = power(y, lo, pow, shift);
-    const float xh = static_cast<float>(static_cast<uint32_t>(x >> 22)), xl = static_cast<float>(static_cast<uint32_t>(x) & 0x3fffffu) * 0x1p-22f;
-    const float p = __fmaf_rn(xh, inv.hi, __fmaf_rn(xh, inv.lo, xl * inv.hi));
-    const int first = min(shift, 100);                       // a subnormal number rounds once
-    return p * __int_as_float((127 + 22 - first) << 23) * __int_as_float((127 - (shift - first)) << 23);
+__device__ __forceinline__ int octave(int bits, const Scale& c) { return (bits >> kPowBits) - (kMagicBits >> kPowBits) - c.e0; }
+
+// w 2^kOne / 2^e0 as a whole number, 0 below 2^-(kOne + 1)
+__device__ __forceinline__ uint64_t weight(float z, const Scale& c, const uint32_t* pow) {
+    float f;
+    const int bits = c.wide ? split_wide(z, c.top, c.rh, c.rl, f) : split(z, c, f);
+    const int i = octave(bits, c);                           // 2^i <= w < 2^(i + 1), i < 0
+    if (i >= -kFine) {
+        int shift;
+        const uint64_t x = power_fine(bits - kMagicBits, f, c.e0, shift);
+        return x >> shift;
+    }
+    const uint32_t m = power(bits, f, pow);
+    const int left = i + kOne - 31;                          // of m
+    // cut bits leave a 1 in the last place: as often too much as too little
+    uint32_t w = shr(m, max(-left, 0));
+    w |= min(w, 1u);
+    return static_cast<uint64_t>(w) << max(left, 0);
 }
 
-// floor(a s), rounded up where `up` is set and it is not whole: a >= 0 finite, s < 2^63; saturates
+// w / sum, from 1 / sum as a pair: rounded once
+__device__ __forceinline__ float probability(float z, const Scale& c, const uint32_t* pow, float2 inv) {
+    float f;
+    const int bits = c.wide ? split_wide(z, c.top, c.rh, c.rl, f) : split(z, c, f);
+    const int i = octave(bits, c);
+    if (i < -160) return 0.0f;
+    const uint32_t m = power(bits, f, pow);
+    const float xh = static_cast<float>(m >> 8), xl = static_cast<float>(m & 0xffu) * 0x1p-8f;
+    const float p = __fmaf_rn(xh, inv.x, __fmaf_rn(xh, inv.y, xl * inv.x));     // m / 2^8 / sum, at least 2^-41
+    const int e = i + kOne - 31 + 8, first = max(e, -80);    // a subnormal number rounds once
+    return p * __int_as_float((127 + first) << 23) * __int_as_float((127 + e - first) << 23);
+}
+
+// floor(a s), rounded up where `up` is set and it is not whole: a >= 0; saturates
 __device__ __forceinline__ uint64_t scaled(float a, uint64_t s, bool up) {
     if (!(a > 0.0f)) return 0;
     const uint32_t b = __float_as_uint(a);
     const int ex = static_cast<int>(b >> 23);
     const uint64_t m = ex != 0 ? (b & 0x7fffffu) | 0x800000u : b & 0x7fffffu;
     const int right = 150 - max(ex, 1);                      // a = m 2^-right
-    uint64_t lo = m * s, hi = __umul64hi(m, s);
-    if (right <= 0) return ~0ull >> 1;                       // a >= 2^23
+    const uint64_t lo = m * s, hi = __umul64hi(m, s);
+    if (right <= 0) return ~0ull;                            // a >= 2^23
     uint64_t out, rest;
     if (right < 64) {
-        if ((hi >> right) != 0u) return ~0ull >> 1;
+        if ((hi >> right) != 0u) return ~0ull;
         out = (hi << (64 - right)) | (lo >> right);
         rest = lo & ((1ull << right) - 1);
     } else if (right < 128) {
@@ -345,88 +397,117 @@ __device__ __forceinline__ uint4 load_group(const E* row, int v, int begin, int 
 
 // ---------------------------------------------------------------- the first CTA's list
 
-// Largest first.  Few entries: each counts those before it.
-__device__ void sort_list(uint64_t* a, int n) {
-    const int tid = threadIdx.x;
-    if (n <= 256) {
-        const uint64_t x = tid < n ? a[tid] : 0;
-        int r = 0;
-        if (tid < n)
-            for (int j = 0; j < n; ++j) r += a[j] > x ? 1 : 0;
-        __syncthreads();
-        if (tid < n) a[r] = x;
-        __syncthreads();
-        return;
-    }
-    int p = 512;
-    while (p < n) p <<= 1;
-    for (int i = n + tid; i < p; i += kThreads) a[i] = 0;    // below every entry
-    __syncthreads();
-    for (int k = 2; k <= p; k <<= 1)
-        for (int j = k >> 1; j > 0; j >>= 1) {
-            for (int i = tid; i < p; i += kThreads) {
-                const int o = i ^ j;
-                if (o > i) {
-                    const uint64_t x = a[i], y = a[o];
-                    if ((x < y) == ((i & k) == 0)) {
-                        a[i] = y;
-                        a[o] = x;
-                    }
-                }
-            }
-            __syncthreads();
-        }
-}
-
+__device__ __forceinline__ uint64_t list_entry(float z, int v) { return (static_cast<uint64_t>(order_key(z)) << 32) | ~static_cast<uint32_t>(v); }
 __device__ __forceinline__ float list_value(uint64_t e) { return key_value(static_cast<uint32_t>(e >> 32)); }
 __device__ __forceinline__ int list_index(uint64_t e) { return static_cast<int>(~static_cast<uint32_t>(e)); }
 
 // Sum over the block; all threads get it.  `slot` alternates between two calls in a row.
-__device__ __forceinline__ uint64_t block_sum64(SampleShared& s, uint64_t v, int slot) {
+template <int NT>
+__device__ __forceinline__ uint64_t block_sum64(SampleShared<NT>& s, uint64_t v, int slot) {
     v = warp_sum64(v);
     if ((threadIdx.x & 31) == 0) s.warp_sum[slot][threadIdx.x >> 5] = v;
     __syncthreads();
     uint64_t t = 0;
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) t += s.warp_sum[slot][w];
+    for (int w = 0; w < NT / 32; ++w) t += s.warp_sum[slot][w];
     return t;
 }
 
-constexpr int kPerThread = kList / kThreads;
+// Adds a 64-bit number to one in shared memory kept as two words (the exact sum, in any order).
+__device__ __forceinline__ void add_wide(uint2* h, uint64_t w) {
+    const uint32_t wl = static_cast<uint32_t>(w), old = atomicAdd(&h->x, wl);
+    const uint32_t wh = static_cast<uint32_t>(w >> 32) + (old + wl < old ? 1u : 0u);
+    if (wh != 0u) atomicAdd(&h->y, wh);
+}
 
-// Weights of the sorted entries list[0, n): thread t has entries t kPerThread ..; `before` the mass in front of each.
-__device__ __forceinline__ uint64_t list_masses(SampleShared& s, int n, const Scale& c, uint64_t (&w)[kPerThread],
-                                                uint64_t (&before)[kPerThread]) {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    uint64_t own = 0;
+// Of entries with distinct values v and masses w (in registers, N a thread, w = 0: not there), taken from the largest
+// value down: the value of the one whose mass takes the sum from below `limit` to it or past it (the total reaches
+// it).  By 256 bins of the range of values in turn.
+template <int NT, int N>
+__device__ __noinline__ uint64_t select(SampleShared<NT>& s, const uint64_t (&v)[N], const uint64_t (&w)[N], uint64_t limit) {
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    uint32_t least = 0xffffffffu, most = 0;
 #pragma unroll
-    for (int i = 0; i < kPerThread; ++i) {
-        const int at = threadIdx.x * kPerThread + i;
-        w[i] = at < n ? weight(list_value(s.list[at]), c, s.pow) : 0;
-        before[i] = own;
-        own += w[i];
-    }
-    const uint64_t inc = warp_scan64(own, lane);
-    __syncthreads();                                         // warp_sum is free
-    if (lane == 31) s.warp_sum[0][warp] = inc;
+    for (int e = 0; e < N; ++e)
+        if (w[e] != 0) {
+            least = min(least, static_cast<uint32_t>(v[e] >> 32));
+            most = max(most, static_cast<uint32_t>(v[e] >> 32));
+        }
+    least = __reduce_min_sync(0xffffffffu, least);
+    most = __reduce_max_sync(0xffffffffu, most);
     __syncthreads();
-    uint64_t base = inc - own, total = 0;
-    for (int i = 0; i < kWarps; ++i) {
-        if (i < warp) base += s.warp_sum[0][i];
-        total += s.warp_sum[0][i];
+    if (lane == 0) {
+        s.warp_lo[warp] = least;
+        s.warp_hi[warp] = most;
+    }
+    if (tid < kSelectBins) {
+        s.sel_mass[tid] = make_uint2(0u, 0u);
+        s.sel_count[tid] = 0;
+    }
+    __syncthreads();
+    for (int i = 0; i < NT / 32; ++i) {
+        least = min(least, s.warp_lo[i]);
+        most = max(most, s.warp_hi[i]);
+    }
+    uint64_t lo = static_cast<uint64_t>(least) << 32, range = (static_cast<uint64_t>(most - least) << 32) | 0xffffffffull;
+    int shift = max(0, 64 - __clzll(static_cast<long long>(range)) - 8);
+    for (;;) {
+#pragma unroll
+        for (int e = 0; e < N; ++e)
+            if (w[e] != 0 && v[e] - lo <= range) {           // (below lo: wraps to more)
+                const int b = static_cast<int>((v[e] - lo) >> shift);
+                add_wide(&s.sel_mass[b], w[e]);
+                atomicAdd(&s.sel_count[b], 1u);
+            }
+        __syncthreads();
+        uint64_t m[8], own = 0;                              // every warp: 8 bins a lane, the largest values first
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const uint2 h = s.sel_mass[kSelectBins - 1 - lane * 8 - i];
+            m[i] = (static_cast<uint64_t>(h.y) << 32) | h.x;
+            own += m[i];
+        }
+        uint64_t before = warp_scan64(own, lane) - own;
+        const uint32_t hit = __ballot_sync(0xffffffffu, before < limit && before + own >= limit);
+        const int owner = hit != 0u ? __ffs(static_cast<int>(hit)) - 1 : 31;
+        int bin = 0;
+        bool open = true;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            if (open && before + m[i] >= limit) {
+                bin = kSelectBins - 1 - lane * 8 - i;
+                open = false;
+            }
+            if (open) before += m[i];
+        }
+        bin = __shfl_sync(0xffffffffu, bin, owner);
+        limit -= __shfl_sync(0xffffffffu, before, owner);
+        lo += static_cast<uint64_t>(bin) << shift;
+        range = (1ull << shift) - 1;
+        const bool one = s.sel_count[bin] == 1 || shift == 0;
+        __syncthreads();
+        if (one) break;
+        if (tid < kSelectBins) {
+            s.sel_mass[tid] = make_uint2(0u, 0u);
+            s.sel_count[tid] = 0;
+        }
+        __syncthreads();
+        shift = max(0, shift - 8);
     }
 #pragma unroll
-    for (int i = 0; i < kPerThread; ++i) before[i] += base;
-    return total;
+    for (int e = 0; e < N; ++e)
+        if (w[e] != 0 && v[e] - lo <= range) s.sel_value = v[e];
+    __syncthreads();
+    return s.sel_value;
 }
 
 // ---------------------------------------------------------------- kernel
 
-template <typename E>
-__global__ void __launch_bounds__(kThreads) sample_tokens_kernel(const SampleArgs a) {
+template <typename E, int NT>
+__global__ void __launch_bounds__(NT, 1024 / NT) sample_tokens_kernel(const SampleArgs a) {
     extern __shared__ __align__(16) unsigned char smem[];
-    SampleShared& s = *reinterpret_cast<SampleShared*>(smem);
-    constexpr int kGroup = 16 / sizeof(E);
+    SampleShared<NT>& s = *reinterpret_cast<SampleShared<NT>*>(smem);
+    constexpr int kGroup = 16 / sizeof(E), kWarps = NT / 32, kEntries = kList / NT;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int C = a.ctas;
     const int row = blockIdx.x / C;
@@ -442,7 +523,7 @@ __global__ void __launch_bounds__(kThreads) sample_tokens_kernel(const SampleArg
     const float u = __ldg(a.u + row);
     const bool greedy = !(temperature > 0.0f);
     const bool use_k = k_in > 0 && k_in < a.V, use_p = p_in < 1.0f, use_m = m_in > 0.0f;
-    const bool by_list = use_k && k_in <= min(kMaxTopK, C * kThreads / 2);
+    const bool by_list = use_k && k_in <= min(kMaxTopK, C * NT / 2);
 
     // ---- the slice
     const E* logits = static_cast<const E*>(a.logits) + static_cast<int64_t>(row) * a.ld;
@@ -451,7 +532,7 @@ __global__ void __launch_bounds__(kThreads) sample_tokens_kernel(const SampleArg
     sl.end = min(a.V, sl.begin + a.slice);
     const int shift_in = static_cast<int>((reinterpret_cast<uintptr_t>(logits + sl.begin) & 15u) / sizeof(E));
     sl.first = sl.begin - shift_in;
-    sl.data = reinterpret_cast<uint4*>(smem + sizeof(SampleShared));
+    sl.data = reinterpret_cast<uint4*>(smem + sizeof(SampleShared<NT>));
     sl.lane = lane;
     const int groups = sl.end > sl.begin ? (sl.end - sl.first + kGroup - 1) / kGroup : 0;
     const int per = (groups + kWarps - 1) / kWarps;
@@ -473,20 +554,22 @@ __global__ void __launch_bounds__(kThreads) sample_tokens_kernel(const SampleArg
                 for (int e = 0; e < kGroup; ++e) top_own = fmaxf(top_own, x[e]);
             }
     }
-    for (int i = tid; i < (1 << kPowBits); i += kThreads) s.pow[i] = kPow.v[i];
+    for (int i = tid; i < (1 << kPowBits) / 4; i += NT)
+        reinterpret_cast<uint4*>(s.pow)[i] = __ldg(reinterpret_cast<const uint4*>(kPow.coarse) + i);
     if (tid == 0) {
-        s.list_count = 0;
         s.stage_count = 0;
         s.found = 0x7fffffff;
-        const double r = 1.4426950408889634074 / static_cast<double>(temperature);
+        const double r = 1024.0 * 1.4426950408889634074 / static_cast<double>(temperature);
         s.rh = r < FLT_MAX ? static_cast<float>(r) : FLT_MAX;
         s.rl = r < FLT_MAX ? static_cast<float>(r - static_cast<double>(s.rh)) : 0.0f;
     }
+    // by one thread: the fp64 unit is slow (by all of them 5 us)
+    if (use_m && tid == 32) s.t_ln_min = static_cast<double>(temperature) * log(static_cast<double>(fminf(m_in, 1.0f)));
 
     // ---- the largest entry
     cluster_wait();
     if (by_list && !greedy)
-        for (int c = 0; c < C; ++c) put(&s.maxima[rank * kThreads + tid], c, __float_as_uint(top_own));
+        for (int c = 0; c < C; ++c) put(&s.maxima[rank * NT + tid], c, __float_as_uint(top_own));
     {
         const float m = warp_max(top_own);
         if (lane == 0) s.warp_max[warp] = m;
@@ -498,11 +581,9 @@ __global__ void __launch_bounds__(kThreads) sample_tokens_kernel(const SampleArg
         }
     }
     cluster_sync();
-    Scale sc;
-    sc.top = -INFINITY;
-    for (int c = 0; c < C; ++c) sc.top = fmaxf(sc.top, s.cta_max[c]);
-    sc.rh = s.rh;
-    sc.rl = s.rl;
+    float top = -INFINITY;
+    for (int c = 0; c < C; ++c) top = fmaxf(top, s.cta_max[c]);
+    const Scale sc = make_scale(top, s.rh, s.rl);
 
     float* probs = a.probs != nullptr ? a.probs + static_cast<int64_t>(row) * a.ld_probs : nullptr;
     auto clear_probs = [&]() {
@@ -510,11 +591,11 @@ __global__ void __launch_bounds__(kThreads) sample_tokens_kernel(const SampleArg
         const bool vec = (reinterpret_cast<uintptr_t>(probs + sl.begin) & 15u) == 0;
         const int n = sl.end - sl.begin;
         if (vec) {
-            for (int i = tid; i < n / 4; i += kThreads)
+            for (int i = tid; i < n / 4; i += NT)
                 *reinterpret_cast<float4*>(probs + sl.begin + 4 * i) = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-            for (int i = n / 4 * 4 + tid; i < n; i += kThreads) probs[sl.begin + i] = 0.0f;
+            for (int i = n / 4 * 4 + tid; i < n; i += NT) probs[sl.begin + i] = 0.0f;
         } else {
-            for (int i = tid; i < n; i += kThreads) probs[sl.begin + i] = 0.0f;
+            for (int i = tid; i < n; i += NT) probs[sl.begin + i] = 0.0f;
         }
     };
 
@@ -546,148 +627,235 @@ __global__ void __launch_bounds__(kThreads) sample_tokens_kernel(const SampleArg
         return;
     }
 
-    // Entries that `pick` takes, to the first CTA's list; true if they fit (the same in every CTA).  The area of
-    // maxima, bins and stage is free when it is called.
+    // Entries that `pick` takes, to the first CTA's list: their number (the same in every CTA), the list is whole if
+    // that is at most kList and no CTA has more than its stage holds (else kList + 1 is returned).  Each CTA has a region
+    // of the list; where one does not suffice they are sent again, packed.  The area of maxima, bins and stage is free.
+    bool packed = false;
     auto collect = [&](auto pick) {
         __syncthreads();
-        for (int st = 0; st < sl.steps(); ++st) {
-            float x[kGroup];
-            const int v = sl.read(st, x);
-            bool any = false;
-#pragma unroll
-            for (int i = 0; i < kGroup; ++i) any |= pick(x[i], v + i);
-            if (!__any_sync(0xffffffffu, any)) continue;
-            if (any) {
-#pragma unroll 1
-                for (int i = 0; i < kGroup; ++i) {
-                    float z = x[0];
-#pragma unroll
-                    for (int j = 1; j < kGroup; ++j) z = i == j ? x[j] : z;
-                    if (!pick(z, v + i)) continue;
-                    const uint32_t at = atomicAdd(&s.stage_count, 1u);
-                    if (at < kList) s.stage[at] = (static_cast<uint64_t>(order_key(z)) << 32) | ~static_cast<uint32_t>(v + i);
-                }
-            }
-        }
+        sl.each([&](float z, int v) {
+            if (!pick(z, v)) return;
+            const uint32_t at = atomicAdd(&s.stage_count, 1u);
+            const uint64_t e = list_entry(z, v);
+            if (at < SampleShared<NT>::kStage) s.stage[at] = e;
+            if (at < kRegion) put(&s.list[rank * kRegion + at], 0u, e);
+        });
         __syncthreads();
         const uint32_t n = s.stage_count;
         if (tid < C) put(&s.cta_count[rank], tid, n);
-        if (tid == 0) s.stage_base = n > 0 ? add_remote(&s.list_count, 0, n) : 0;
-        __syncthreads();
-        const uint32_t base = s.stage_base;
-        for (uint32_t i = tid; i < n; i += kThreads)
-            if (i < kList && base + i < kList) put(&s.list[base + i], 0u, s.stage[i]);
         cluster_sync();
-        uint32_t all = 0;
-        for (int c = 0; c < C; ++c) all += s.cta_count[c];
-        return all;
+        uint32_t all = 0, most = 0, before = 0;
+        for (int c = 0; c < C; ++c) {
+            const uint32_t m = s.cta_count[c];
+            if (c < static_cast<int>(rank)) before += m;
+            all += m;
+            most = max(most, m);
+        }
+        packed = most > kRegion;
+        if (packed && all <= kList && most <= SampleShared<NT>::kStage) {
+            for (uint32_t i = tid; i < n; i += NT) put(&s.list[before + i], 0u, s.stage[i]);
+            cluster_sync();
+        }
+        return most <= SampleShared<NT>::kStage ? all : kList + 1u;
+    };
+    // Entry i of the list
+    auto entry = [&](int i) {
+        if (packed) return s.list[i];
+        int c = 0;
+        while (i >= static_cast<int>(s.cta_count[c])) i -= static_cast<int>(s.cta_count[c++]);
+        return s.list[c * kRegion + i];
     };
 
     // smallest entry that min-p keeps
     float zmin = -INFINITY;
-    if (use_m) {
-        const double t = static_cast<double>(sc.top) + static_cast<double>(temperature) * log(static_cast<double>(fminf(m_in, 1.0f)));
+    if (use_m && tid == 0) {
+        const double t = static_cast<double>(sc.top) + s.t_ln_min;
         zmin = static_cast<float>(t);
         if (static_cast<double>(zmin) < t) zmin = nextafterf(zmin, INFINITY);
-        zmin = fminf(zmin, sc.top);
+        s.zmin = fminf(zmin, sc.top);
     }
+    if (use_m) {
+        __syncthreads();
+        zmin = s.zmin;
+    }
+    // 1 / sum, by one thread as well
+    auto inverse_of = [&](uint64_t sum) {
+        if (tid == 0) {
+            const double d = 1.0 / static_cast<double>(sum);
+            const float hi = static_cast<float>(d);
+            s.inv = make_float2(hi, static_cast<float>(d - static_cast<double>(hi)));
+        }
+        __syncthreads();
+        return s.inv;
+    };
 
-    bool listed = false;
     if (by_list) {
-        // ---- a bound that at least k entries reach: the k-th largest of the threads' maxima, or a little less
+        // ---- a bound that at least k entries reach: the k-th largest of the threads' maxima, or a little less, by 256
+        // bins of their range in turn
         uint32_t key[kMaxCtas];
-        uint32_t hi = order_key(sc.top) + 1, lo = 0;         // entries >= lo: at least k; >= hi: fewer
+        const uint32_t none = order_key(-INFINITY);
+        uint32_t least = 0xffffffffu, finite = 0;
 #pragma unroll
-        for (int c = 0; c < kMaxCtas; ++c) key[c] = c < C ? order_key(s.maxima[c * kThreads + tid]) : 0;
-        const uint32_t enough = static_cast<uint32_t>(k_in) + k_in / 8 + 8;
-        int slot = 0;
-        while (hi - lo > 1) {
-            const uint32_t mid = lo + (hi - lo) / 2;
-            uint32_t n = 0;
-#pragma unroll
-            for (int c = 0; c < kMaxCtas; ++c) n += key[c] >= mid ? 1u : 0u;
-            n = __reduce_add_sync(0xffffffffu, n);
-            if (lane == 0) s.warp_sum[slot][warp] = n;
-            __syncthreads();
-            uint32_t total = 0;
-#pragma unroll
-            for (int w = 0; w < kWarps; ++w) total += static_cast<uint32_t>(s.warp_sum[slot][w]);
-            slot ^= 1;
-            if (total >= static_cast<uint32_t>(k_in)) {
-                lo = mid;
-                if (total <= enough) break;
-            } else {
-                hi = mid;
+        for (int c = 0; c < kMaxCtas; ++c) {
+            key[c] = c < C ? order_key(s.maxima[c * NT + tid]) : none;
+            if (key[c] != none) {
+                least = min(least, key[c]);
+                ++finite;
             }
         }
-        const float bound = lo <= 0x007fffffu ? -INFINITY : key_value(lo);   // below every number: all of them
+        least = __reduce_min_sync(0xffffffffu, least);
+        finite = __reduce_add_sync(0xffffffffu, finite);
+        if (lane == 0) {
+            s.warp_lo[warp] = least;
+            s.warp_hi[warp] = finite;
+        }
+        if (tid < kSelectBins) s.sel_count[tid] = 0;
+        __syncthreads();
+        finite = 0;
+        for (int i = 0; i < kWarps; ++i) {
+            least = min(least, s.warp_lo[i]);
+            finite += s.warp_hi[i];
+        }
+        const uint32_t wanted = static_cast<uint32_t>(k_in), enough = wanted + wanted / 8 + 8;
+        float bound = -INFINITY;                             // fewer maxima than k: all entries
+        if (finite >= wanted) {
+            uint32_t lo = least, range = order_key(sc.top) - least, above = 0;
+            int shift = max(0, 32 - __clz(static_cast<int>(range)) - 8);
+            for (;;) {
+#pragma unroll
+                for (int c = 0; c < kMaxCtas; ++c)
+                    if (key[c] != none && key[c] - lo <= range) atomicAdd(&s.sel_count[(key[c] - lo) >> shift], 1u);
+                __syncthreads();
+                uint32_t m[8], own = 0;                      // every warp: 8 bins a lane, the largest first
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    m[i] = s.sel_count[kSelectBins - 1 - lane * 8 - i];
+                    own += m[i];
+                }
+                uint32_t upto = own;
+#pragma unroll
+                for (int d = 1; d < 32; d <<= 1) {
+                    const uint32_t o = __shfl_up_sync(0xffffffffu, upto, d);
+                    if (lane >= d) upto += o;
+                }
+                uint32_t at = above + upto - own;
+                const int owner = __ffs(static_cast<int>(__ballot_sync(0xffffffffu, at < wanted && at + own >= wanted))) - 1;
+                int bin = 0;
+                bool open = true;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    if (open && at + m[i] >= wanted) {
+                        bin = kSelectBins - 1 - lane * 8 - i;
+                        own = m[i];
+                        open = false;
+                    }
+                    if (open) at += m[i];
+                }
+                bin = __shfl_sync(0xffffffffu, bin, owner);
+                above = __shfl_sync(0xffffffffu, at, owner);
+                own = __shfl_sync(0xffffffffu, own, owner);
+                lo += static_cast<uint32_t>(bin) << shift;
+                range = (1u << shift) - 1;
+                if (above + own <= enough || shift == 0) break;
+                __syncthreads();
+                if (tid < kSelectBins) s.sel_count[tid] = 0;
+                __syncthreads();
+                shift = max(0, shift - 8);
+            }
+            bound = key_value(lo);
+        }
         clear_probs();
         const uint32_t n_all = collect([&](float z, int) { return z >= bound && z > -INFINITY; });
-        listed = n_all <= kList;
-        if (listed) {
+        if (n_all <= kList) {
             if (rank != 0) return;
             const int n = static_cast<int>(n_all), k = min(k_in, n);
-            sort_list(s.list, n);
-            uint64_t w[kPerThread], before[kPerThread];
-            const uint64_t mass = list_masses(s, k, sc, w, before);
-            const uint64_t limit = use_p ? max(scaled(p_in, mass, true), uint64_t(1)) : ~0ull;
-            // how many of the sorted entries are kept, and their mass
-            int kept = 0;
-            uint64_t own = 0;
+            if (n <= kFew) {
+                // ---- a few entries: each compares itself with all of them, twice
+                uint64_t x = 0, w = 0;
+                if (tid < n) {
+                    x = entry(tid);
+                    w = weight(list_value(x), sc, s.pow);
+                    s.few.entry[tid] = x;
+                    s.few.mass[tid] = w;
+                }
+                __syncthreads();
+                int r = 0;
+                uint64_t before = 0;
+                if (tid < n) {
+#pragma unroll 8
+                    for (int j = 0; j < n; ++j)
+                        if (s.few.entry[j] > x) {
+                            ++r;
+                            before += s.few.mass[j];
+                        }
+                    if (r == k - 1) s.limit = use_p ? max(scaled(p_in, before + w, true), uint64_t(1)) : ~0ull;
+                }
+                __syncthreads();
+                const bool kept = tid < n && r < k && before < s.limit && list_value(x) >= zmin;
+                const int nk = __syncthreads_count(kept);
+                if (tid < n && !kept) s.few.mass[tid] = 0;
+                if (kept && r == nk - 1) {                   // the last one kept: all before it are
+                    s.sum = before + w;
+                    s.limit = min(scaled(u, before + w, false), before + w - 1);
+                }
+                __syncthreads();
+                const uint64_t target = s.limit;
+                float2 inv{0.0f, 0.0f};
+                if (probs != nullptr) inv = inverse_of(s.sum);
+                if (kept) {
+                    if (probs != nullptr) probs[list_index(x)] = probability(list_value(x), sc, s.pow, inv);
+                    uint64_t upto = 0;                       // mass of the indices up to this one's
+#pragma unroll 8
+                    for (int j = 0; j < n; ++j) upto += static_cast<uint32_t>(s.few.entry[j]) >= static_cast<uint32_t>(x) ? s.few.mass[j] : 0;
+                    if (upto > target && upto - w <= target) a.tokens[row] = list_index(x);
+                }
+                return;
+            }
+            // ---- more of them: three selections, by z for k, by z for p, by index for u
+            uint64_t v[kEntries], w[kEntries], ones[kEntries];
+            uint32_t kept = 0;
 #pragma unroll
-            for (int i = 0; i < kPerThread; ++i) {
-                const int at = tid * kPerThread + i;
-                if (at < k && before[i] < limit && list_value(s.list[at]) >= zmin) {
-                    ++kept;
-                    own += w[i];
+            for (int e = 0; e < kEntries; ++e) {
+                const int i = tid + e * NT;
+                v[e] = w[e] = ones[e] = 0;
+                if (i < n) {
+                    v[e] = entry(i);
+                    w[e] = weight(list_value(v[e]), sc, s.pow);
+                    ones[e] = 1;
+                    kept |= 1u << e;
                 }
             }
-            __syncthreads();
-            const uint64_t sum = block_sum64(s, own, 0);
-            const int nk = static_cast<int>(block_sum64(s, static_cast<uint64_t>(kept), 1));
-            const uint64_t target = scaled(u, sum, false);
-            // the masses where `stage` was: every CTA has sent its own
+            auto keep_from = [&](uint64_t least_entry) {
 #pragma unroll
-            for (int i = 0; i < kPerThread; ++i)
-                if (tid * kPerThread + i < nk) s.stage[tid * kPerThread + i] = w[i];
-            __syncthreads();
-            const Inverse inv = inverse(sum);
-            int v = 0x7fffffff, last = -1;
-            for (int i = tid; i < nk; i += kThreads) {
-                const int idx = list_index(s.list[i]);
-                if (probs != nullptr) probs[idx] = probability(list_value(s.list[i]), sc, s.pow, inv);
-                if (s.stage[i] == 0) continue;
-                last = max(last, idx);
-                if (nk <= 512) {
-                    uint64_t upto = 0;
-                    for (int j = 0; j < nk; ++j) upto += list_index(s.list[j]) <= idx ? s.stage[j] : 0;
-                    if (upto > target) v = min(v, idx);
-                }
+                for (int e = 0; e < kEntries; ++e)
+                    if (v[e] < least_entry) {
+                        w[e] = 0;
+                        kept &= ~(1u << e);
+                    }
+            };
+            auto total = [&](int slot) {
+                uint64_t m = 0;
+#pragma unroll
+                for (int e = 0; e < kEntries; ++e) m += w[e];
+                return block_sum64(s, m, slot);
+            };
+            if (n > k) keep_from(select<NT, kEntries>(s, v, ones, static_cast<uint64_t>(k)));
+            if (use_p) {
+                const uint64_t mass = total(0);
+                keep_from(select<NT, kEntries>(s, v, w, max(scaled(p_in, mass, true), uint64_t(1))));
             }
-            if (nk > 512) {
-                // the least index up to which more than the target lies
-                int below = -1, at = a.V - 1;
-                while (at - below > 1) {
-                    const int mid = below + (at - below) / 2;
-                    uint64_t upto = 0;
-                    for (int i = tid; i < nk; i += kThreads) upto += list_index(s.list[i]) <= mid ? s.stage[i] : 0;
-                    if (block_sum64(s, upto, slot) > target) at = mid; else below = mid;
-                    slot ^= 1;
-                }
-                v = sum > target ? at : 0x7fffffff;
+            keep_from(static_cast<uint64_t>(order_key(zmin)) << 32);
+            const uint64_t sum = total(1);
+            if (probs != nullptr) {
+                const float2 inv = inverse_of(sum);
+#pragma unroll
+                for (int e = 0; e < kEntries; ++e)
+                    if ((kept >> e) & 1u) probs[list_index(v[e])] = probability(list_value(v[e]), sc, s.pow, inv);
             }
-            v = __reduce_min_sync(0xffffffffu, v);
-            last = __reduce_max_sync(0xffffffffu, last);
-            __syncthreads();
-            if (lane == 0) s.warp_sum[0][warp] = (static_cast<uint64_t>(static_cast<uint32_t>(v)) << 32) | static_cast<uint32_t>(last + 1);
-            __syncthreads();
-            if (tid == 0) {
-                for (int i = 0; i < kWarps; ++i) {
-                    v = min(v, static_cast<int>(s.warp_sum[0][i] >> 32));
-                    last = max(last, static_cast<int>(static_cast<uint32_t>(s.warp_sum[0][i])) - 1);
-                }
-                a.tokens[row] = v != 0x7fffffff ? v : last;  // u of 1 or more: the last one kept
-            }
+#pragma unroll
+            for (int e = 0; e < kEntries; ++e) v[e] <<= 32;  // ~index: the lowest first
+            const uint64_t hit = select<NT, kEntries>(s, v, w, min(scaled(u, sum, false), sum - 1) + 1);
+            if (tid == 0) a.tokens[row] = static_cast<int>(~static_cast<uint32_t>(hit >> 32));
             return;
         }
     }
@@ -763,28 +931,23 @@ __global__ void __launch_bounds__(kThreads) sample_tokens_kernel(const SampleArg
     if (use_p) {
         // ---- masses of bins of z, largest first
         __syncthreads();
-        for (int i = tid; i < kBins; i += kThreads) s.hist[i] = make_uint2(0u, 0u);
+        for (int i = tid; i < kBins; i += NT) s.hist[i] = make_uint2(0u, 0u);
         if (tid == 0) s.stage_count = 0;
-        if (rank == 0 && tid == 0) s.list_count = 0;
         __syncthreads();
-        auto bin_of = [&](float z) { return min(kBins - 1, static_cast<int>(fminf((sc.top - z) * sc.rh * kBinsPerOctave, 1.0e6f))); };
+        const float per_bin = sc.rh * (kBinsPerOctave / 1024.0f);
+        auto place_of = [&](float z) { return fminf((sc.top - z) * per_bin, static_cast<float>(kBins - 1)); };
         sl.each([&](float z, int v) {
-            if (!cut.keeps(z, v)) return;
             const uint64_t w = weight(z, sc, s.pow);
-            if (w == 0) return;
-            uint2* h = &s.hist[bin_of(z)];
-            const uint32_t wl = static_cast<uint32_t>(w), old = atomicAdd(&h->x, wl);
-            const uint32_t wh = static_cast<uint32_t>(w >> 32) + (old + wl < old ? 1u : 0u);
-            if (wh != 0u) atomicAdd(&h->y, wh);
+            if (w != 0 && cut.keeps(z, v)) add_wide(&s.hist[static_cast<int>(place_of(z))], w);
         });
         cluster_sync();
         // this CTA's share of the bins: sums over the cluster, then the mass of the share to every CTA
         const int share = kBins / C, b0 = static_cast<int>(rank) * share;      // C is a power of two
-        uint64_t own[kBins / kThreads];
+        uint64_t own[kBins / NT];
         uint64_t mine = 0;
-        const int each = (share + kThreads - 1) / kThreads;
+        const int each = (share + NT - 1) / NT;
 #pragma unroll
-        for (int i = 0; i < kBins / kThreads; ++i) {
+        for (int i = 0; i < kBins / NT; ++i) {
             own[i] = 0;
             const int b = tid * each + i;
             if (i < each && b < share)
@@ -803,7 +966,7 @@ __global__ void __launch_bounds__(kThreads) sample_tokens_kernel(const SampleArg
         const uint64_t limit = max(scaled(p_in, mass, true), uint64_t(1));
         // the bin of the last entry before which less than the limit lies: mass up to it reaches the limit
 #pragma unroll
-        for (int i = 0; i < kBins / kThreads; ++i) {
+        for (int i = 0; i < kBins / NT; ++i) {
             if (own[i] != 0 && before < limit && before + own[i] >= limit)
                 for (int c = 0; c < C; ++c) {
                     put(&s.bin, c, static_cast<uint32_t>(b0 + tid * each + i));
@@ -812,23 +975,25 @@ __global__ void __launch_bounds__(kThreads) sample_tokens_kernel(const SampleArg
             before += own[i];
         }
         cluster_sync();
-        const int bin = s.bin;
+        const float bin = static_cast<float>(s.bin);
         const uint64_t bin_before = s.bin_before;
-        const uint32_t n = collect([&](float z, int v) { return z > -INFINITY && bin_of(z) == bin && cut.keeps(z, v); });
+        const uint32_t n = collect([&](float z, int v) {
+            const float b = place_of(z);
+            return b >= bin && b < bin + 1.0f && z > -INFINITY && cut.keeps(z, v);
+        });
         if (n <= kList) {
             if (rank == 0) {
-                sort_list(s.list, static_cast<int>(n));
-                uint64_t w[kPerThread], b[kPerThread];
-                list_masses(s, static_cast<int>(n), sc, w, b);
+                uint64_t v[kEntries], w[kEntries];
 #pragma unroll
-                for (int i = 0; i < kPerThread; ++i) {
-                    const int at = tid * kPerThread + i;
-                    // weights fall: the entry whose mass reaches the limit
-                    if (w[i] != 0 && bin_before + b[i] < limit && bin_before + b[i] + w[i] >= limit)
-                        for (int c = 0; c < C; ++c) {
-                            put(&s.cut_key, c, static_cast<uint32_t>(s.list[at] >> 32));
-                            put(&s.cut_index, c, static_cast<uint32_t>(list_index(s.list[at])));
-                        }
+                for (int e = 0; e < kEntries; ++e) {
+                    const int i = tid + e * NT;
+                    v[e] = i < static_cast<int>(n) ? entry(i) : 0;
+                    w[e] = i < static_cast<int>(n) ? weight(list_value(v[e]), sc, s.pow) : 0;
+                }
+                const uint64_t last = select<NT, kEntries>(s, v, w, limit - bin_before);
+                if (tid < C) {
+                    put(&s.cut_key, tid, static_cast<uint32_t>(last >> 32));
+                    put(&s.cut_index, tid, static_cast<uint32_t>(list_index(last)));
                 }
             }
             cluster_sync();
@@ -880,7 +1045,7 @@ __global__ void __launch_bounds__(kThreads) sample_tokens_kernel(const SampleArg
         }
     }
     if (probs != nullptr) {
-        const Inverse inv = inverse(sum);
+        const float2 inv = inverse_of(sum);
         for (int g = sl.g0 + lane; g < sl.g1; g += 32) {
             float x[kGroup];
             Slice<E>::unpack(sl.data[g], x);
@@ -920,15 +1085,19 @@ extern "C" dsa_status dsa_sample_tokens(const void* logits, int64_t ld, int32_t 
     int ctas = 1;
     while (ctas < kMaxCtas && V > ctas * 2048) ctas *= 2;
     const int slice = ((V + ctas - 1) / ctas + 7) / 8 * 8;
-    const size_t smem = sizeof(SampleShared) + (static_cast<size_t>(slice) * align + 15) / 16 * 16 + 16;
+    const size_t bytes = (static_cast<size_t>(slice) * align + 15) / 16 * 16 + 16;
+    const bool large = bytes > 40 * 1024;
+    const size_t smem = bytes + (large ? sizeof(SampleShared<512>) : sizeof(SampleShared<256>));
     SampleArgs a{logits, ld, V, temperature, top_k, top_p, min_p, u, tokens, probs, ld_probs, ctas, slice, dev_err};
-    const void* kernel = bf16 ? reinterpret_cast<const void*>(&sample_tokens_kernel<uint16_t>)
-                              : reinterpret_cast<const void*>(&sample_tokens_kernel<float>);
+    const void* kernel = bf16 ? (large ? reinterpret_cast<const void*>(&sample_tokens_kernel<uint16_t, 512>)
+                                       : reinterpret_cast<const void*>(&sample_tokens_kernel<uint16_t, 256>))
+                              : (large ? reinterpret_cast<const void*>(&sample_tokens_kernel<float, 512>)
+                                       : reinterpret_cast<const void*>(&sample_tokens_kernel<float, 256>));
     if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)) != cudaSuccess)
         return DSA_ERR_CUDA;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(R) * ctas);
-    cfg.blockDim = dim3(kThreads);
+    cfg.blockDim = dim3(large ? 512 : 256);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = static_cast<cudaStream_t>(stream);
     cudaLaunchAttribute attr[2];

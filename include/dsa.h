@@ -733,9 +733,9 @@ dsa_status dsa_verify_drafts(const float* target_probs, int64_t target_ld, const
  *   tokens[r]: the least v with sum_{i <= v} w_i > u[r] * sum w over what is kept (u >= 1: the last one).
  *   probs[r, v] = w_v / sum w, 0 for what is not kept.
  *   temperature <= 0 (or NaN): the largest entry, the lowest index among equals; probs 1 there.
- *   Weights are whole multiples of 2^-45 of the largest (relative error about 2^-35 before) and their sums are exact,
- *   so a token does not depend on how the work is split; an entry below 2^-46 of the largest is never drawn.  probs are
- *   rounded to fp32 once, from the same weights before they are cut.
+ *   Weights are good to 2^-30 of themselves and held as whole multiples of about 2^-45 of the largest (less than
+ *   that: never drawn); their sums are exact, so a token does not depend on how the work is split.  probs come
+ *   from the weights before that cut and are rounded to fp32 once.
  *   A logit that is NaN counts as -infinity (never kept), +infinity as the type's largest number.
  * Arguments:
  *   logits         fp32 (DSA_LOGITS_BF16: bf16) rows of V entries, stride ld >= V; element alignment.

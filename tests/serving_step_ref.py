@@ -1,18 +1,22 @@
 """Plain definitions of the calls around a serving step, for their tests (CPU): the step's tables with lists, the
 sampling in float64.
 
-Sampling: the kernel holds a weight w_i (largest 1) as a multiple of 2^-45, rounded once, of a value with these errors:
-z - max z and its product with log2 e / t exact as pairs of fp32 (2^-44); the argument of the power after the table,
-|f| <= 2^-11, rounded twice to fp32 (2 x 2^-36, times ln 2); 2^f - 1, at most 2^-11.5, with 6 fp32 roundings (6 x 2^-24 x
-2^-11.5 < 2^-32.9) and rounded to 2^-41; the table 2^-46.  Together less than 2^-32 of the weight.  So sums over
-kept weights are good to 2^-32 S + n 2^-46.  BORDER = 2^-31 covers that and the float64 reference; `sample` raises
-where a border of its input lies nearer, so inputs have to keep away from it (ties are exact on both sides).
-probs: weight before the last rounding, relative error 2^-32, one rounding to fp32 (2^-24): 2^-24 + 2^-30 of the value, and 2^-150 for subnormal ones (half a step of 2^-149)."""
+Sampling: errors of a weight w_i before it is cut to a whole number of units (2^-46 of a power of two between the largest
+weight and twice that): 1024 log2 of it is n + f with |f| <= 1/2, f from two fused products (2^-26 each) and the pair for
+1024 log2 e / t (2^-49 of at most 2^22): less than 2^-24.6, which is 2^-35 of the weight; the power of f is off by 2^-33 (its
+rounding) and 2^-35 + 2^-36 + 2^-37 (its sum and coefficients, the cubic term); the table by 2^-32; the product with it is cut
+at 2^-31.  Together less than d = 2^-30.  Cut off: less than one unit, 2^-45 of the largest.  A border is a share x = c / S
+of the kept mass: weights that are off by d each move it by at most 2 d x (1 - x) <= 2^-31, the cuts of n weights by n 2^-45
+in c and in S.  border(n) = 2^-31 + n 2^-44 covers both.  `sample` raises where a border of its input lies nearer, so inputs
+have to keep away from it (ties are exact on both sides).
+probs: the ratio of a weight before the cut and the sum (2^-30 each, and the n 2^-45), rounded to fp32 once (2^-24; 2^-150 for
+subnormal ones, half a step of 2^-149)."""
 import math
 
 import numpy as np
 
-BORDER = 2.0 ** -31
+def border(n):
+    return 2.0 ** -31 + n * 2.0 ** -44
 
 
 class NearBorder(Exception):
@@ -46,13 +50,13 @@ def sample(z, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0, u=0.0):
         gap = np.abs(before[1:] - limit)
         # a border between equal weights that are exact on both sides is no matter of rounding
         exact = np.all(d == 0)
-        if not exact and gap.size and gap.min() < BORDER * w.sum():
+        if not exact and gap.size and gap.min() < border(V) * w.sum():
             raise NearBorder
         order, w = order[keep], w[keep]
     if min_p > 0:
         keep = w >= min(min_p, 1.0)
         near = np.abs(w / min(min_p, 1.0) - 1)
-        if np.any((near < BORDER) & (w != 1.0)):
+        if np.any((near < 2.0 ** -40) & (w != 1.0)):
             raise NearBorder
         order, w = order[keep], w[keep]
     by = np.argsort(order)
@@ -60,7 +64,7 @@ def sample(z, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0, u=0.0):
     c = np.cumsum(w)
     some = w > 2.0 ** -46
     hit = np.flatnonzero((c > u * c[-1]) & some)
-    if 0 < u < 1 and np.abs(c[:-1] - u * c[-1]).min(initial=np.inf) < BORDER * c[-1] and not np.all(w == 1.0):
+    if 0 < u < 1 and np.abs(c[:-1] - u * c[-1]).min(initial=np.inf) < border(V) * c[-1] and not np.all(w == 1.0):
         raise NearBorder
     token = int(order[hit[0]]) if hit.size else int(order[np.flatnonzero(some)[-1]])
     probs[order] = w / c[-1]
@@ -137,4 +141,4 @@ def tables(cached, q, counts, keep, table, num_pages, stack, have, T):
 
 
 def round_probs_bound(p):
-    return (2.0 ** -24 + 2.0 ** -30) * np.abs(p) + 2.0 ** -150
+    return (2.0 ** -24 + 2.0 ** -29 + p.size * 2.0 ** -45) * np.abs(p) + 2.0 ** -150
