@@ -199,22 +199,15 @@ __device__ __forceinline__ uint64_t power_fine(int n, float f, int e0, int& shif
 // 1024 log2 of the weight relative to 2^e0 as n + f, n as it stands in the bits of a float past kMagic.  The product's
 // rounding errors are those of f alone (2^-25 of 1/1024 octave), as n is taken from it before it is rounded.
 __device__ __forceinline__ int split(float z, const Scale& c, float& f) {
+    float e = 0.0f;
+    if (c.wide) {                                            // z - max z, as a pair, in the place of z
+        const float d = __fsub_rn(z, c.top);
+        e = two_sum_err(z, -c.top, d);
+        z = d;
+    }
     const float t = __fmaf_rn(z, c.rh, kMagic);
     f = __fmaf_rn(z, c.rl, __fmaf_rn(z, c.rh, -__fsub_rn(t, kMagic)));
-    return __float_as_int(t);
-}
-// The same for rows whose scale passes the table's range: z - max z and its product as pairs first.
-__device__ __noinline__ int split_wide(float z, float top, float rh, float rl, float& f) {
-    const float s = __fsub_rn(z, top);
-    const float e = two_sum_err(z, -top, s);
-    const float y = __fmul_rn(s, rh);
-    const float lo = __fadd_rn(__fmaf_rn(s, rh, -y), __fmaf_rn(s, rl, __fmul_rn(e, rh)));
-    if (!(y > -200.0f * 1024.0f)) {
-        f = 0.0f;
-        return kMagicBits - 400 * 1024;
-    }
-    const float t = __fadd_rn(y, kMagic);
-    f = __fadd_rn(__fsub_rn(y, __fsub_rn(t, kMagic)), lo);
+    if (c.wide) f = __fmaf_rn(e, c.rh, f);
     return __float_as_int(t);
 }
 
@@ -232,7 +225,7 @@ __device__ __forceinline__ int octave(int bits, const Scale& c) { return (bits >
 // w 2^kOne / 2^e0 as a whole number, 0 below 2^-(kOne + 1)
 __device__ __forceinline__ uint64_t weight(float z, const Scale& c, const uint32_t* pow) {
     float f;
-    const int bits = c.wide ? split_wide(z, c.top, c.rh, c.rl, f) : split(z, c, f);
+    const int bits = split(z, c, f);
     const int i = octave(bits, c);                           // 2^i <= w < 2^(i + 1), i < 0
     if (i >= -kFine) {
         int shift;
@@ -250,7 +243,7 @@ __device__ __forceinline__ uint64_t weight(float z, const Scale& c, const uint32
 // w / sum, from 1 / sum as a pair: rounded once
 __device__ __forceinline__ float probability(float z, const Scale& c, const uint32_t* pow, float2 inv) {
     float f;
-    const int bits = c.wide ? split_wide(z, c.top, c.rh, c.rl, f) : split(z, c, f);
+    const int bits = split(z, c, f);
     const int i = octave(bits, c);
     if (i < -160) return 0.0f;
     const uint32_t m = power(bits, f, pow);
@@ -420,25 +413,29 @@ __device__ __forceinline__ void add_wide(uint2* h, uint64_t w) {
     if (wh != 0u) atomicAdd(&h->y, wh);
 }
 
-// Of entries with distinct values v and masses w (in registers, N a thread, w = 0: not there), taken from the largest
-// value down: the value of the one whose mass takes the sum from below `limit` to it or past it (the total reaches
-// it).  By 256 bins of the range of values in turn.
-template <int NT, int N>
-__device__ __noinline__ uint64_t select(SampleShared<NT>& s, const uint64_t (&v)[N], const uint64_t (&w)[N], uint64_t limit) {
+// What a selection over the list goes by: from the largest z down by number or by mass, or from the lowest index up by mass.
+enum Order { kByCount, kByMass, kByIndex };
+
+// Entries list[0, n) that are `least` or more, in the given order: the one whose mass takes the sum from below `limit`
+// to it or past it (the total reaches it).  By 256 bins of the range of values in turn.
+template <int NT>
+__device__ __noinline__ uint64_t select(SampleShared<NT>& s, int n, uint64_t least, Order order, uint64_t limit, const Scale c) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    uint32_t least = 0xffffffffu, most = 0;
-#pragma unroll
-    for (int e = 0; e < N; ++e)
-        if (w[e] != 0) {
-            least = min(least, static_cast<uint32_t>(v[e] >> 32));
-            most = max(most, static_cast<uint32_t>(v[e] >> 32));
-        }
-    least = __reduce_min_sync(0xffffffffu, least);
-    most = __reduce_max_sync(0xffffffffu, most);
+    auto value = [&](uint64_t e) { return order == kByIndex ? e << 32 : e; };
+    uint32_t low = 0xffffffffu, high = 0;
+    for (int i = tid; i < n; i += NT) {
+        const uint64_t e = s.list[i];
+        if (e < least) continue;
+        const uint32_t v = static_cast<uint32_t>(value(e) >> 32);
+        low = min(low, v);
+        high = max(high, v);
+    }
+    low = __reduce_min_sync(0xffffffffu, low);
+    high = __reduce_max_sync(0xffffffffu, high);
     __syncthreads();
     if (lane == 0) {
-        s.warp_lo[warp] = least;
-        s.warp_hi[warp] = most;
+        s.warp_lo[warp] = low;
+        s.warp_hi[warp] = high;
     }
     if (tid < kSelectBins) {
         s.sel_mass[tid] = make_uint2(0u, 0u);
@@ -446,19 +443,20 @@ __device__ __noinline__ uint64_t select(SampleShared<NT>& s, const uint64_t (&v)
     }
     __syncthreads();
     for (int i = 0; i < NT / 32; ++i) {
-        least = min(least, s.warp_lo[i]);
-        most = max(most, s.warp_hi[i]);
+        low = min(low, s.warp_lo[i]);
+        high = max(high, s.warp_hi[i]);
     }
-    uint64_t lo = static_cast<uint64_t>(least) << 32, range = (static_cast<uint64_t>(most - least) << 32) | 0xffffffffull;
+    uint64_t lo = static_cast<uint64_t>(low) << 32, range = (static_cast<uint64_t>(high - low) << 32) | 0xffffffffull;
     int shift = max(0, 64 - __clzll(static_cast<long long>(range)) - 8);
     for (;;) {
-#pragma unroll
-        for (int e = 0; e < N; ++e)
-            if (w[e] != 0 && v[e] - lo <= range) {           // (below lo: wraps to more)
-                const int b = static_cast<int>((v[e] - lo) >> shift);
-                add_wide(&s.sel_mass[b], w[e]);
-                atomicAdd(&s.sel_count[b], 1u);
-            }
+        for (int i = tid; i < n; i += NT) {
+            const uint64_t e = s.list[i], v = value(e);
+            if (e < least || v - lo > range) continue;       // (below lo: wraps to more)
+            const int b = static_cast<int>((v - lo) >> shift);
+            const uint64_t w = order == kByCount ? 1 : weight(list_value(e), c, s.pow);
+            if (w != 0) add_wide(&s.sel_mass[b], w);
+            atomicAdd(&s.sel_count[b], 1u);
+        }
         __syncthreads();
         uint64_t m[8], own = 0;                              // every warp: 8 bins a lane, the largest values first
 #pragma unroll
@@ -494,9 +492,10 @@ __device__ __noinline__ uint64_t select(SampleShared<NT>& s, const uint64_t (&v)
         __syncthreads();
         shift = max(0, shift - 8);
     }
-#pragma unroll
-    for (int e = 0; e < N; ++e)
-        if (w[e] != 0 && v[e] - lo <= range) s.sel_value = v[e];
+    for (int i = tid; i < n; i += NT) {
+        const uint64_t e = s.list[i];
+        if (e >= least && value(e) - lo <= range) s.sel_value = e;
+    }
     __syncthreads();
     return s.sel_value;
 }
@@ -658,12 +657,24 @@ __global__ void __launch_bounds__(NT, 1024 / NT) sample_tokens_kernel(const Samp
         }
         return most <= SampleShared<NT>::kStage ? all : kList + 1u;
     };
-    // Entry i of the list
+    // Entry i of the list as it came in
     auto entry = [&](int i) {
         if (packed) return s.list[i];
         int c = 0;
         while (i >= static_cast<int>(s.cta_count[c])) i -= static_cast<int>(s.cta_count[c++]);
         return s.list[c * kRegion + i];
+    };
+    // ... and the whole list without gaps
+    auto pack = [&](int n) {
+        if (packed) return;
+        uint64_t v[kEntries];
+#pragma unroll
+        for (int e = 0; e < kEntries; ++e) v[e] = tid + e * NT < n ? entry(tid + e * NT) : 0;
+        __syncthreads();
+#pragma unroll
+        for (int e = 0; e < kEntries; ++e)
+            if (tid + e * NT < n) s.list[tid + e * NT] = v[e];
+        __syncthreads();
     };
 
     // smallest entry that min-p keeps
@@ -812,50 +823,27 @@ __global__ void __launch_bounds__(NT, 1024 / NT) sample_tokens_kernel(const Samp
                 return;
             }
             // ---- more of them: three selections, by z for k, by z for p, by index for u
-            uint64_t v[kEntries], w[kEntries], ones[kEntries];
-            uint32_t kept = 0;
-#pragma unroll
-            for (int e = 0; e < kEntries; ++e) {
-                const int i = tid + e * NT;
-                v[e] = w[e] = ones[e] = 0;
-                if (i < n) {
-                    v[e] = entry(i);
-                    w[e] = weight(list_value(v[e]), sc, s.pow);
-                    ones[e] = 1;
-                    kept |= 1u << e;
-                }
-            }
-            auto keep_from = [&](uint64_t least_entry) {
-#pragma unroll
-                for (int e = 0; e < kEntries; ++e)
-                    if (v[e] < least_entry) {
-                        w[e] = 0;
-                        kept &= ~(1u << e);
-                    }
-            };
-            auto total = [&](int slot) {
+            pack(n);
+            auto total = [&](uint64_t least, int slot) {
                 uint64_t m = 0;
-#pragma unroll
-                for (int e = 0; e < kEntries; ++e) m += w[e];
+                for (int i = tid; i < n; i += NT)
+                    if (s.list[i] >= least) m += weight(list_value(s.list[i]), sc, s.pow);
                 return block_sum64(s, m, slot);
             };
-            if (n > k) keep_from(select<NT, kEntries>(s, v, ones, static_cast<uint64_t>(k)));
+            uint64_t least = n > k ? select(s, n, 0, kByCount, static_cast<uint64_t>(k), sc) : 0;
             if (use_p) {
-                const uint64_t mass = total(0);
-                keep_from(select<NT, kEntries>(s, v, w, max(scaled(p_in, mass, true), uint64_t(1))));
+                const uint64_t mass = total(least, 0);
+                least = select(s, n, least, kByMass, max(scaled(p_in, mass, true), uint64_t(1)), sc);
             }
-            keep_from(static_cast<uint64_t>(order_key(zmin)) << 32);
-            const uint64_t sum = total(1);
+            least = max(least, static_cast<uint64_t>(order_key(zmin)) << 32);
+            const uint64_t sum = total(least, 1);
             if (probs != nullptr) {
                 const float2 inv = inverse_of(sum);
-#pragma unroll
-                for (int e = 0; e < kEntries; ++e)
-                    if ((kept >> e) & 1u) probs[list_index(v[e])] = probability(list_value(v[e]), sc, s.pow, inv);
+                for (int i = tid; i < n; i += NT)
+                    if (s.list[i] >= least) probs[list_index(s.list[i])] = probability(list_value(s.list[i]), sc, s.pow, inv);
             }
-#pragma unroll
-            for (int e = 0; e < kEntries; ++e) v[e] <<= 32;  // ~index: the lowest first
-            const uint64_t hit = select<NT, kEntries>(s, v, w, min(scaled(u, sum, false), sum - 1) + 1);
-            if (tid == 0) a.tokens[row] = static_cast<int>(~static_cast<uint32_t>(hit >> 32));
+            const uint64_t hit = select(s, n, least, kByIndex, min(scaled(u, sum, false), sum - 1) + 1, sc);
+            if (tid == 0) a.tokens[row] = list_index(hit);
             return;
         }
     }
@@ -983,14 +971,8 @@ __global__ void __launch_bounds__(NT, 1024 / NT) sample_tokens_kernel(const Samp
         });
         if (n <= kList) {
             if (rank == 0) {
-                uint64_t v[kEntries], w[kEntries];
-#pragma unroll
-                for (int e = 0; e < kEntries; ++e) {
-                    const int i = tid + e * NT;
-                    v[e] = i < static_cast<int>(n) ? entry(i) : 0;
-                    w[e] = i < static_cast<int>(n) ? weight(list_value(v[e]), sc, s.pow) : 0;
-                }
-                const uint64_t last = select<NT, kEntries>(s, v, w, limit - bin_before);
+                pack(static_cast<int>(n));
+                const uint64_t last = select(s, static_cast<int>(n), 0, kByMass, limit - bin_before, sc);
                 if (tid < C) {
                     put(&s.cut_key, tid, static_cast<uint32_t>(last >> 32));
                     put(&s.cut_index, tid, static_cast<uint32_t>(list_index(last)));
