@@ -73,7 +73,14 @@ constexpr int kMinShare = 2;
 constexpr int kAhead = 2;                                       // tiles between a page's prefetch and its copy
 constexpr size_t kDecSmem = 1024 + size_t(kDataBytes) + 5120;
 static_assert(kDecSmem <= 232448, "shared-memory budget");
-static_assert(2 * kMaxRequests * 4 <= kDataBytes, "schedule scratch");
+static_assert(3 * kMaxRequests * 4 <= kDataBytes, "schedule scratch");
+
+// Where a share begins.
+struct Share {
+    int unit, g, tile;     // first unit, first row tile (or pair of them) of it, first key tile
+    int left;              // key tiles of the share
+    int first;             // the one that holds the first piece of the first row tile
+};
 
 struct DecBars {
     uint64_t kv_full[kMaxStages], kv_empty[kMaxStages];
@@ -96,8 +103,8 @@ struct DecBars {
     uint32_t tmem_slot;
     int page_ok[kMaxStages];                // bit i: page i of the stage is there and its id valid
     int tile_ok[kSBufs];                    // ... of the score tile's pages
-    int start[4];                           // first unit, first row tile of it, first key tile, tiles of the share
-    int first_cluster;                      // cluster that holds the first piece of the first row tile
+    // this pair's share of the work, and with shared prefixes (second) the cluster's share of what its pairs do together
+    Share share[2];
     float tmax[2][2][kRows];                // rank 0: [tile parity][key half][row]: maximum of the tile
     alignas(16) float alpha[2][kRows];      // the factors of the tile: rank 0's, copied to rank 1
     float fin[kRows];                       // rank 1: 1 / l; -1: nothing visible
@@ -115,9 +122,10 @@ struct Batch {
     int G;
 };
 
-// What the row tiles of a unit have in common: a request's query tokens and keys, or, with shared prefixes,
-// a group's query tokens over the group's prefix (units 0 .. G - 1), then a request's over what it has behind its
-// group's prefix (unit G + b).  Positions count from the unit's first key.
+// What the row tiles of a unit have in common: a request's query tokens and keys.  With shared prefixes the units of
+// a pair's share are a group's last row tile over the group's prefix, where their number is odd (units 0 .. G - 1),
+// then a request's tokens over what it has behind that prefix (unit G + b); the units of a cluster's are a group's
+// other row tiles, two at a time.  Positions count from the unit's first key.
 struct Unit {
     int q0, nq;            // query tokens
     int vis;               // visible keys of the last one (each earlier one sees one less); a prefix: its length
@@ -156,16 +164,23 @@ __device__ __forceinline__ int request_prefix(const Batch& bt, int b) {
 }
 
 template <bool kShared>
-__device__ __forceinline__ int unit_count(const Batch& bt) { return kShared ? bt.G + bt.B : bt.B; }
+__device__ __forceinline__ int unit_count(const Batch& bt, bool multi) { return multi ? bt.G : (kShared ? bt.G + bt.B : bt.B); }
 
 template <bool kShared>
-__device__ __forceinline__ Unit unit(const Batch& bt, int i) {
+__device__ __forceinline__ Unit unit(const Batch& bt, int i, bool multi) {
     Unit u;
     if (kShared && i < bt.G) {
         const int b0 = max(0, min(bt.B, __ldg(bt.cu_group + i))), b1 = max(b0, min(bt.B, __ldg(bt.cu_group + i + 1)));
         u.vis = prefix_len(bt, i);
         u.q0 = max(0, min(bt.T, __ldg(bt.cu_q + b0)));
         u.nq = b1 > b0 && u.vis > 0 ? max(0, min(bt.T, __ldg(bt.cu_q + b1)) - u.q0) : 0;
+        const int paired = (u.nq + bt.per - 1) / bt.per / 2 * 2 * bt.per;       // tokens of the paired row tiles
+        if (multi) {
+            u.nq = min(u.nq, paired);
+        } else {
+            u.q0 += paired;
+            u.nq = max(0, u.nq - paired);
+        }
         u.table = min(b0, bt.B - 1);
         u.page0 = 0;
         u.pages = u.vis / kPage;
@@ -195,27 +210,35 @@ __device__ __forceinline__ RowTile row_tile(const Batch& bt, const Unit& u, int 
     return t;
 }
 
-// A share's pieces, one row tile after the other; every role walks them by itself.
+// The pieces of a pair's shares, one row tile after the other; every role walks them by itself.  What a cluster does
+// together comes first, with both pairs on the same keys, each with its own row tile of two.
 template <bool kShared>
 struct Walk {
     Batch bt;
-    int i, g, left;        // unit, row tile of it, tiles left in the share
+    const Share* share;
+    int pair;
+    int i, g, left;        // unit, row tile (or pair of them) of it, tiles left in the share
     Unit u;
     RowTile rt;
     int t0, t1;            // key tiles [t0, t1) of the piece (t0 == t1: a row tile that sees nothing)
     bool whole, first;     // the piece is its whole row tile; the share's first piece
+    bool multi;            // the cluster's share
 
-    __device__ Walk(const Batch& batch, const int* start) : bt(batch) {
-        i = uniform(start[0]);
-        g = uniform(start[1]);
-        t0 = uniform(start[2]);
-        left = uniform(start[3]);
+    __device__ Walk(const Batch& batch, const Share* shares, int pair_) : bt(batch), share(shares), pair(pair_) {
+        multi = kShared && uniform(shares[1].left) > 0;
+        begin(shares[kShared && multi ? 1 : 0]);
+    }
+    __device__ void begin(const Share& s) {
+        i = uniform(s.unit);
+        g = uniform(s.g);
+        t0 = uniform(s.tile);
+        left = uniform(s.left);
         first = true;
         load_unit();
         set_piece();
     }
     __device__ void load_unit() {
-        u = unit<kShared>(bt, i);
+        u = unit<kShared>(bt, i, multi);
         u.nq = uniform(u.nq);
         u.q0 = uniform(u.q0);
         u.vis = uniform(u.vis);
@@ -226,24 +249,29 @@ struct Walk {
         }
     }
     __device__ void set_piece() {
-        rt = row_tile(bt, u, g);
+        rt = row_tile(bt, u, kShared && multi ? 2 * g + pair : g);
         const int n = max(1, rt.tiles);
         const int take = min(n - t0, left);
         whole = take == n;
         left -= take;
         t1 = min(t0 + take, rt.tiles);
     }
-    // false: the share is done
+    // false: the shares are done
     __device__ bool next() {
-        if (left <= 0) return false;
+        if (left <= 0) {
+            if (!kShared || !multi || uniform(share[0].left) <= 0) return false;
+            multi = false;
+            begin(share[0]);
+            return true;
+        }
         t0 = 0;
         first = false;
-        if ((g + 1) * bt.per < u.nq) {
+        if ((g + 1) * (kShared && multi ? 2 * bt.per : bt.per) < u.nq) {
             ++g;
         } else {
             g = 0;
             do {
-                if (++i >= unit_count<kShared>(bt)) return false;
+                if (++i >= unit_count<kShared>(bt, multi)) return false;
                 load_unit();
             } while (u.nq == 0);
         }
@@ -252,21 +280,24 @@ struct Walk {
     }
 };
 
-// Workspace slot of a part: 2 c for the one that starts share c but not its row tile, else 2 c + 1.
+// Workspace slots of a share's parts: 2 c for the one that starts share c but not its row tile, else 2 c + 1.  With
+// shared prefixes a pair has four: two for its cluster's share, then two for its own.
 template <bool kShared>
-__device__ __forceinline__ int64_t piece_slot(int cluster, const Walk<kShared>& w) {
-    return 2 * static_cast<int64_t>(cluster) + ((w.first && w.t0 > 0) ? 0 : 1);
+__device__ __forceinline__ int64_t piece_slot(int pair_id, const Walk<kShared>& w) {
+    return (kShared ? 4 * static_cast<int64_t>(pair_id) + (w.multi ? 0 : 2) : 2 * static_cast<int64_t>(pair_id)) +
+           ((w.first && w.t0 > 0) ? 0 : 1);
 }
 
-// Key tiles of a unit over all its row tiles (a row tile that sees nothing counts as one).
+// Key tiles of a unit over all its row tiles, or pairs of them (a row tile that sees nothing counts as one).
 template <bool kShared>
-__device__ __forceinline__ int unit_tiles(const Batch& bt, int i, int32_t* err) {
-    const Unit u = unit<kShared>(bt, i);
+__device__ __forceinline__ int unit_tiles(const Batch& bt, int i, bool multi, int32_t* err) {
+    const Unit u = unit<kShared>(bt, i, multi);
     if (kShared && u.prefix) {
         if (err != nullptr && (__ldg(bt.cu_group + i) < 0 || __ldg(bt.cu_group + i + 1) < __ldg(bt.cu_group + i) ||
                                __ldg(bt.cu_group + i + 1) > bt.B || __ldg(bt.shared_lens + i) / kPage > bt.max_pages))
             raise_error(err, DSA_DEVERR_INDEX_RANGE);
-        return (u.nq + bt.per - 1) / bt.per * ((u.vis + kKeys - 1) / kKeys);
+        const int per = multi ? 2 * bt.per : bt.per;
+        return (u.nq + per - 1) / per * ((u.vis + kKeys - 1) / kKeys);
     }
     const int b = kShared ? i - bt.G : i;
     if (err != nullptr && (__ldg(bt.cu_q + b) < 0 || __ldg(bt.cu_q + b + 1) > bt.T)) raise_error(err, DSA_DEVERR_INDEX_RANGE);
@@ -280,56 +311,59 @@ __device__ __forceinline__ int unit_tiles(const Batch& bt, int i, int32_t* err) 
     return sum;
 }
 
-// The share of cluster c: sums of all units in `sums` (shared), then one warp finds the start.
+// One warp: share c of `workers` equal ones, from the sums of all units.
 template <bool kShared>
-__device__ __forceinline__ void find_share(const Batch& bt, int c, int clusters, int* sums, DecBars& bar, int32_t* err) {
-    const int units = unit_count<kShared>(bt);
-    for (int b = threadIdx.x; b < units; b += kDecThreads) sums[b] = unit_tiles<kShared>(bt, b, c == 0 ? err : nullptr);
-    __syncthreads();
-    if (threadIdx.x < 32) {
-        const int lane = threadIdx.x;
-        int total = 0;
-        for (int b = lane; b < units; b += 32) total += sums[b];
+__device__ __forceinline__ void cut_share(const Batch& bt, int c, int workers, const int* sums, bool multi, Share& out) {
+    const int lane = threadIdx.x & 31, units = unit_count<kShared>(bt, multi);
+    int total = 0;
+    for (int b = lane; b < units; b += 32) total += sums[b];
 #pragma unroll
-        for (int m = 16; m > 0; m >>= 1) total += __shfl_xor_sync(0xffffffffu, total, m);
-        const int share = max((total + clusters - 1) / clusters, kMinShare);
-        const int64_t w0 = static_cast<int64_t>(c) * share;
-        if (lane == 0) {
-            bar.start[3] = w0 < total ? static_cast<int>(min(static_cast<int64_t>(share), total - w0)) : 0;
+    for (int m = 16; m > 0; m >>= 1) total += __shfl_xor_sync(0xffffffffu, total, m);
+    const int share = max((total + workers - 1) / workers, kMinShare);
+    const int64_t w0 = static_cast<int64_t>(c) * share;
+    if (lane == 0) out.left = w0 < total ? static_cast<int>(min(static_cast<int64_t>(share), total - w0)) : 0;
+    if (w0 >= total) return;
+    int carry = 0;
+    for (int b0 = 0; b0 < units; b0 += 32) {
+        const int b = b0 + lane;
+        int inc = b < units ? sums[b] : 0;
+        const int own = inc;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const int o = __shfl_up_sync(0xffffffffu, inc, d);
+            if (lane >= d) inc += o;
         }
-        if (w0 < total) {
-            int carry = 0;
-            for (int b0 = 0; b0 < units; b0 += 32) {
-                const int b = b0 + lane;
-                int inc = b < units ? sums[b] : 0;
-                const int own = inc;
-#pragma unroll
-                for (int d = 1; d < 32; d <<= 1) {
-                    const int o = __shfl_up_sync(0xffffffffu, inc, d);
-                    if (lane >= d) inc += o;
+        const uint32_t hit = __ballot_sync(0xffffffffu, w0 < carry + inc);
+        if (hit != 0u) {
+            if (lane == __ffs(hit) - 1) {
+                int at = carry + inc - own;                    // tiles before the unit
+                const Unit u = unit<kShared>(bt, b, multi);
+                int g = 0;
+                for (;; ++g) {
+                    const int n = max(1, row_tile(bt, u, multi ? 2 * g : g).tiles);
+                    if (w0 < at + n) break;
+                    at += n;
                 }
-                const uint32_t hit = __ballot_sync(0xffffffffu, w0 < carry + inc);
-                if (hit != 0u) {
-                    if (lane == __ffs(hit) - 1) {
-                        int at = carry + inc - own;            // tiles before the unit
-                        const Unit u = unit<kShared>(bt, b);
-                        int g = 0;
-                        for (;; ++g) {
-                            const int n = max(1, row_tile(bt, u, g).tiles);
-                            if (w0 < at + n) break;
-                            at += n;
-                        }
-                        bar.start[0] = b;
-                        bar.start[1] = g;
-                        bar.start[2] = static_cast<int>(w0 - at);
-                        bar.first_cluster = at / share;
-                    }
-                    break;
-                }
-                carry += __shfl_sync(0xffffffffu, inc, 31);
+                out.unit = b;
+                out.g = g;
+                out.tile = static_cast<int>(w0 - at);
+                out.first = at / share;
             }
+            break;
         }
+        carry += __shfl_sync(0xffffffffu, inc, 31);
     }
+}
+
+// The shares of this pair: sums of all units in `sums` (shared), then a warp for each finds the start.
+template <bool kShared>
+__device__ __forceinline__ void find_share(const Batch& bt, int pair_id, int pairs, int* sums, DecBars& bar, int32_t* err) {
+    const int multi_units = kShared ? bt.G : 0, units = unit_count<kShared>(bt, false);
+    for (int b = threadIdx.x; b < multi_units + units; b += kDecThreads)
+        sums[b] = unit_tiles<kShared>(bt, b < multi_units ? b : b - multi_units, b < multi_units, pair_id == 0 ? err : nullptr);
+    __syncthreads();
+    if (threadIdx.x < 32) cut_share<kShared>(bt, pair_id, pairs, sums + multi_units, false, bar.share[0]);
+    if (kShared && threadIdx.x >= 32 && threadIdx.x < 64) cut_share<kShared>(bt, pair_id >> 1, pairs >> 1, sums, true, bar.share[1]);
     __syncthreads();
 }
 
@@ -363,13 +397,25 @@ __device__ __forceinline__ void prefetch_line(const void* p) { asm volatile("pre
 __device__ __forceinline__ void arrive_remote(uint32_t bar) {
     asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
-// Arrive on the barrier at this offset in rank 0 once the MMAs issued so far have completed.
-__device__ __forceinline__ void umma_commit_rank0(uint64_t* bar) {
+// Arrive on the barrier at this offset in the CTAs of `mask` once the MMAs issued so far have completed.
+__device__ __forceinline__ void umma_commit_to(uint64_t* bar, uint32_t mask) {
     asm volatile(
         "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
             ptx::smem_addr(bar)),
-        "h"(static_cast<uint16_t>(1))
+        "h"(static_cast<uint16_t>(mask))
         : "memory");
+}
+// TMA load into the same place of all CTAs of `mask`, counted on the barrier at this offset in each.
+__device__ __forceinline__ void tma_load_3d_to(void* dst, const CUtensorMap* map, uint64_t* bar, int c0, int c1, int c2, uint32_t mask) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.multicast::cluster"
+        " [%0], [%1, {%3, %4, %5}], [%2], %6;" ::"r"(ptx::smem_addr(dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(ptx::smem_addr(bar)), "r"(c0), "r"(c1), "r"(c2),
+        "h"(static_cast<uint16_t>(mask))
+        : "memory");
+}
+__device__ __forceinline__ void mbar_arrive_n(uint64_t* bar, uint32_t n) {
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0], %1;" ::"r"(ptx::smem_addr(bar)), "r"(n) : "memory");
 }
 
 // What a cluster leaves for the combine kernel: the split row tile whose last piece it computed.
@@ -382,13 +428,14 @@ struct Meta {
 // With shared prefixes, where the parts of a query token's rows lie, over its group's prefix ([0]) and over the rest ([1]).
 struct Parts {
     int first;             // kWritten: there are none, kWholePart: one, in the rows' own place; else the first cluster's
-    int last;              // the last cluster
+    int last;              // the last cluster (or pair: a pair's own share)
     int row0;              // first token of the row tile
+    int pair;              // which pair of the clusters; -1: first and last are pairs
 };
 constexpr int kWritten = -2, kWholePart = -1;
 
 template <bool kShared>
-__global__ void __launch_bounds__(kDecThreads, 1) __cluster_dims__(2, 1, 1)
+__global__ void __launch_bounds__(kDecThreads, 1) __cluster_dims__(kShared ? 4 : 2, 1, 1)
 dense_mla_decode_kernel(const __grid_constant__ CUtensorMap kvmap, const __grid_constant__ CUtensorMap qmap,
                         const __grid_constant__ CUtensorMap omap, const __grid_constant__ CUtensorMap pmap,
                         const uint16_t* __restrict__ kv, int num_pages,
@@ -404,13 +451,17 @@ dense_mla_decode_kernel(const __grid_constant__ CUtensorMap kvmap, const __grid_
     DecBars& bar = *reinterpret_cast<DecBars*>(base + kDataBytes);
 
     const int warp = uniform(static_cast<int>(threadIdx.x >> 5)), lane = threadIdx.x & 31;
-    const uint32_t rank = cluster_ctarank();
+    // pairs of CTAs: a cluster is one, with shared prefixes two that share the copies of what both read
+    const uint32_t cta = cluster_ctarank(), rank = kShared ? cta & 1u : cta;
+    const uint32_t score_cta = kShared ? cta & 2u : 0u, value_cta = score_cta + 1u;
+    const int pair = kShared ? static_cast<int>(uniform(cta >> 1)) : 0;
+    const uint32_t both = rank == 0 ? 0x5u : 0xau;                // this role's CTAs of both pairs
     const int cluster = blockIdx.x >> 1, clusters = gridDim.x >> 1;
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < kMaxStages; ++s) {
             ptx::mbar_init(&bar.kv_full[s], 1);
-            ptx::mbar_init(&bar.kv_empty[s], 1);
+            ptx::mbar_init(&bar.kv_empty[s], kShared ? 2 : 1);    // the stage has been read: here and in the other pair
         }
         ptx::mbar_init(&bar.q_full, 8);
         for (int s = 0; s < kKStages; ++s) ptx::mbar_init(&bar.q_read[s], 4);
@@ -446,18 +497,33 @@ dense_mla_decode_kernel(const __grid_constant__ CUtensorMap kvmap, const __grid_
     // limit of every wait, set anew every 256 tiles: a wait lasts a tile or so, the kernel may run for seconds
     uint64_t deadline = ptx::wait_deadline();
     bool timed_out = false;
-    const bool work = uniform(bar.start[3]) > 0;
+    const bool work = uniform(bar.share[0].left) > 0 || (kShared && uniform(bar.share[1].left) > 0);
     const uint32_t ring_addr = ptx::smem_addr(ring);
     if (!kShared && threadIdx.x == 0 && rank == 1) meta[cluster].rows = 0;
     // first row of a whole row tile's parts: behind the slots, those over a prefix first
     auto part_row = [&](const Walk<kShared>& w) {
-        return 2 * static_cast<int64_t>(clusters) * slot_rows + (static_cast<int64_t>(w.u.prefix ? 0 : bt.T) + w.rt.row0) * bt.H;
+        return 4 * static_cast<int64_t>(clusters) * slot_rows + (static_cast<int64_t>(w.u.prefix ? 0 : bt.T) + w.rt.row0) * bt.H;
+    };
+    // One thread gives a stage back: once the MMAs issued so far have completed, and now.  In a cluster's share the copies
+    // land in both pairs, so both give back to both; in a pair's own it stands for the other as well.
+    auto commit_stage = [&](uint64_t* b, bool multi) {
+        if (kShared && multi) {
+            umma_commit_to(b, both);
+        } else {
+            ptx::umma_commit(b);
+            if (kShared) ptx::umma_commit(b);
+        }
+    };
+    auto give_stage = [&](uint64_t* b, bool multi) {
+        if (kShared && multi) umma_commit_to(b, both);
+        else if (kShared) mbar_arrive_n(b, 2);
+        else ptx::mbar_arrive(b);
     };
 
     if (work && warp == kTmaWarp) {
         // ---------------------------------------------------------------- TMA (both ranks)
         const uint32_t stages = rank == 0 ? kKStages : kVStages;
-        Walk<kShared> w(bt, bar.start);
+        Walk<kShared> w(bt, bar.share, pair);
         uint32_t s = 0, ph = 0, used = 0;                            // stage, its phase, stages used so far
         auto stage = [&]() {                                         // the next stage is free (whole warp)
             if (!ptx::mbar_wait(&bar.kv_empty[s], ph ^ 1u, deadline)) timed_out = true;
@@ -502,6 +568,7 @@ dense_mla_decode_kernel(const __grid_constant__ CUtensorMap kvmap, const __grid_
                     // its rate (418 -> 393 us on 64 requests of 4K to 64K; from rank 0, or further ahead, slower)
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
+                        if (kShared && w.multi && i != pair) continue;
                         const int src = 2 * (tb + kAhead) + i;
                         const int near = __shfl_sync(0xffffffffu, page, src & 31), far = __shfl_sync(0xffffffffu, page_next, src & 31);
                         const int pg = src < 32 ? near : far;
@@ -528,8 +595,13 @@ dense_mla_decode_kernel(const __grid_constant__ CUtensorMap kvmap, const __grid_
                         if (elect_one()) {
                             bar.page_ok[s] = ok;
                             ptx::mbar_arrive_expect_tx(&bar.kv_full[s], kKStageBytes);
-                            ptx::tma_load_3d(ring + s * kKStageBytes, &kvmap, &bar.kv_full[s], c * 64, 0, row[0]);
-                            ptx::tma_load_3d(ring + s * kKStageBytes + kPageChunk, &kvmap, &bar.kv_full[s], c * 64, 0, row[1]);
+                            if (kShared && w.multi) {                // a page each, to both
+                                tma_load_3d_to(ring + s * kKStageBytes + pair * kPageChunk, &kvmap, &bar.kv_full[s], c * 64, 0,
+                                               pair == 0 ? row[0] : row[1], both);
+                            } else {
+                                ptx::tma_load_3d(ring + s * kKStageBytes, &kvmap, &bar.kv_full[s], c * 64, 0, row[0]);
+                                ptx::tma_load_3d(ring + s * kKStageBytes + kPageChunk, &kvmap, &bar.kv_full[s], c * 64, 0, row[1]);
+                            }
                         }
                         advance();
                     }
@@ -537,10 +609,17 @@ dense_mla_decode_kernel(const __grid_constant__ CUtensorMap kvmap, const __grid_
                     for (int i = 0; i < 4 && stage(); ++i) {         // page i / 2, value dims 256 (i % 2) .. + 255
                         if (elect_one()) {
                             ptx::mbar_arrive_expect_tx(&bar.kv_full[s], kVStageBytes);
+                            if (kShared && w.multi) {                // 128 of the dims each, to both
 #pragma unroll
-                            for (int j = 0; j < 4; ++j)
-                                ptx::tma_load_3d(ring + s * kVStageBytes + j * kPageChunk, &kvmap, &bar.kv_full[s],
-                                                 (i & 1) * 256 + j * 64, 0, row[i >> 1]);
+                                for (int j = 0; j < 2; ++j)
+                                    tma_load_3d_to(ring + s * kVStageBytes + (2 * pair + j) * kPageChunk, &kvmap, &bar.kv_full[s],
+                                                   (i & 1) * 256 + (2 * pair + j) * 64, 0, row[i >> 1], both);
+                            } else {
+#pragma unroll
+                                for (int j = 0; j < 4; ++j)
+                                    ptx::tma_load_3d(ring + s * kVStageBytes + j * kPageChunk, &kvmap, &bar.kv_full[s],
+                                                     (i & 1) * 256 + j * 64, 0, row[i >> 1]);
+                            }
                         }
                         advance();
                     }
@@ -569,7 +648,7 @@ dense_mla_decode_kernel(const __grid_constant__ CUtensorMap kvmap, const __grid_
         auto wait = [&](uint64_t* b, uint32_t parity) {
             if (!ptx::mbar_wait(b, parity, deadline)) late = true;
         };
-        Walk<kShared> w(bt, bar.start);
+        Walk<kShared> w(bt, bar.share, pair);
         uint32_t u = 0, seg = 0, s = 0, ph = 0, q_phase = 0;          // q_phase: bit s, the phase of q_read[s]
         do {
             if (w.t0 >= w.t1) continue;
@@ -577,7 +656,7 @@ dense_mla_decode_kernel(const __grid_constant__ CUtensorMap kvmap, const __grid_
                 wait(&bar.q_read[s], (q_phase >> s) & 1u);
                 q_phase ^= 1u << s;
                 __syncwarp();
-                if (elect_one()) ptx::mbar_arrive(&bar.kv_empty[s]);
+                if (elect_one()) give_stage(&bar.kv_empty[s], w.multi);
                 __syncwarp();
                 if (++s == kKStages) {
                     s = 0;
@@ -607,7 +686,7 @@ dense_mla_decode_kernel(const __grid_constant__ CUtensorMap kvmap, const __grid_
                             if (c < 8) umma_f16_ts(d, tmem + c * 32 + kk * 8, so + kk * 2, idesc, (c | kk) != 0 ? 1u : 0u);
                             else ptx::umma_f16(d, qr_desc + kk * 2, so + kk * 2, idesc, 1u);
                         }
-                        ptx::umma_commit(&bar.kv_empty[s]);
+                        commit_stage(&bar.kv_empty[s], w.multi);
                         if (c == 8) ptx::umma_commit(&bar.s_full[sb]);
                     }
                     __syncwarp();
@@ -628,7 +707,7 @@ dense_mla_decode_kernel(const __grid_constant__ CUtensorMap kvmap, const __grid_
         auto wait = [&](uint64_t* b, uint32_t parity) {
             if (!ptx::mbar_wait(b, parity, deadline)) late = true;
         };
-        Walk<kShared> w(bt, bar.start);
+        Walk<kShared> w(bt, bar.share, pair);
         uint32_t u = 0, seg = 0, s = 0, ph = 0;
         do {
             if (w.t0 >= w.t1) continue;
@@ -665,8 +744,8 @@ dense_mla_decode_kernel(const __grid_constant__ CUtensorMap kvmap, const __grid_
                         for (int ks = 0; ks < kPage / 16; ++ks)
                             ptx::umma_f16(tmem + (i & 1) * 256, pd + ks * 2, vb + ks * 128, idesc,
                                           (t > w.t0 || i >= 2 || ks != 0) ? 1u : 0u);
-                        ptx::umma_commit(&bar.kv_empty[s]);
-                        if ((i & 1) == 1) umma_commit_rank0(&bar.p_free[pb]);
+                        commit_stage(&bar.kv_empty[s], w.multi);
+                        if ((i & 1) == 1) umma_commit_to(&bar.p_free[pb], 1u << score_cta);
                         if (i == 3) ptx::umma_commit(&bar.pv_done[u % kPvBars]);
                     }
                     __syncwarp();
@@ -680,7 +759,7 @@ dense_mla_decode_kernel(const __grid_constant__ CUtensorMap kvmap, const __grid_
             wait(&bar.stage_back, seg & 1u);
             for (int i = 0; i < 2; ++i) {
                 __syncwarp();
-                if (elect_one()) ptx::mbar_arrive(&bar.kv_empty[s]);
+                if (elect_one()) give_stage(&bar.kv_empty[s], w.multi);
                 if (++s == kVStages) {
                     s = 0;
                     ph ^= 1u;
@@ -699,14 +778,14 @@ dense_mla_decode_kernel(const __grid_constant__ CUtensorMap kvmap, const __grid_
         const int token = row / bt.H;
         const uint32_t p_row = row * 128, p_swz = row & 7;           // the row's place in a P buffer
         // this warp's 32 rows of a P buffer, and their factors, here and in rank 1
-        const uint32_t p_here = ptx::smem_addr(ps) + quad * 4096, p_there = map_to_rank(p_here, 1);
-        const uint32_t a_here = ptx::smem_addr(&bar.alpha[0][quad * 32]), a_there = map_to_rank(a_here, 1);
-        const uint32_t full_there = map_to_rank(ptx::smem_addr(&bar.p_full[0]), 1);
+        const uint32_t p_here = ptx::smem_addr(ps) + quad * 4096, p_there = map_to_rank(p_here, value_cta);
+        const uint32_t a_here = ptx::smem_addr(&bar.alpha[0][quad * 32]), a_there = map_to_rank(a_here, value_cta);
+        const uint32_t full_there = map_to_rank(ptx::smem_addr(&bar.p_full[0]), value_cta);
         auto wait = [&](uint64_t* b, uint32_t parity) {
             if (!ptx::mbar_wait(b, parity, deadline)) timed_out = true;
         };
         uint32_t u = 0, seg = 0, meets = 0, used = 0;                // meets: uses of the pair barrier; used: ring stages
-        Walk<kShared> w(bt, bar.start);
+        Walk<kShared> w(bt, bar.share, pair);
         do {
             const int live = w.rt.tokens * bt.H;
             const bool quad_live = quad * 32 < live;
@@ -864,8 +943,8 @@ dense_mla_decode_kernel(const __grid_constant__ CUtensorMap kvmap, const __grid_
                     ++meets;
                     if (seg > 0) wait(&bar.fin_free, (seg - 1) & 1u);
                     if (kh == 0)
-                        st_async_f32(map_to_rank(ptx::smem_addr(&bar.fin[row]), 1), l_tot == 0.0f ? -1.0f : 1.0f / l_tot,
-                                     map_to_rank(ptx::smem_addr(&bar.fin_full), 1));
+                        st_async_f32(map_to_rank(ptx::smem_addr(&bar.fin[row]), value_cta), l_tot == 0.0f ? -1.0f : 1.0f / l_tot,
+                                     map_to_rank(ptx::smem_addr(&bar.fin_full), value_cta));
                 }
                 if (kh == 0 && row < live) {
                     const float lse2 = l_tot == 0.0f ? -INFINITY : m_run * cs + log2f(l_tot);
@@ -889,7 +968,7 @@ dense_mla_decode_kernel(const __grid_constant__ CUtensorMap kvmap, const __grid_
         };
         uint32_t u = 0, seg = 0, used = 0;                           // used: ring stages before this row tile
         uint32_t clean = 0;                                          // bit i: this row group's P is zero in buffers 2 i and 2 i + 1
-        Walk<kShared> w(bt, bar.start);
+        Walk<kShared> w(bt, bar.share, pair);
         do {
             const int live = w.rt.tokens * bt.H;
             const bool quad_live = quad * 32 < live, has_tiles = w.t0 < w.t1;
@@ -950,7 +1029,7 @@ dense_mla_decode_kernel(const __grid_constant__ CUtensorMap kvmap, const __grid_
                 // when rank 0 learns that it may write the next ones
                 hidden = __ballot_sync(0xffffffffu, inv < 0.0f);
                 __syncwarp();
-                if (lane == 0) arrive_remote(map_to_rank(ptx::smem_addr(&bar.fin_free), 0));
+                if (lane == 0) arrive_remote(map_to_rank(ptx::smem_addr(&bar.fin_free), score_cta));
                 wait(&bar.pv_done[(u - 1) % kPvBars], ((u - 1) / kPvBars) & 1u);
                 timed_out = __any_sync(0xffffffffu, timed_out);
                 if (timed_out) break;
@@ -1025,12 +1104,13 @@ dense_mla_decode_kernel(const __grid_constant__ CUtensorMap kvmap, const __grid_
             // the last piece of a split row tile: the combine kernel finds it here
             if (kShared && w.t1 == w.rt.tiles && static_cast<int>(threadIdx.x) < w.rt.tokens) {
                 const int at = w.rt.row0 + threadIdx.x;
-                const int where = !w.whole ? bar.first_cluster : (w.u.part ? kWholePart : kWritten);
-                parts[w.u.prefix ? at : bt.T + at] = Parts{where, cluster, w.rt.row0};
-                if (!w.u.part) parts[at] = Parts{kWritten, 0, 0};
+                const int where = !w.whole ? bar.share[w.multi ? 1 : 0].first : (w.u.part ? kWholePart : kWritten);
+                parts[w.u.prefix ? at : bt.T + at] =
+                    Parts{where, w.multi ? cluster >> 1 : cluster, w.rt.row0, w.multi ? pair : -1};
+                if (!w.u.part) parts[at] = Parts{kWritten, 0, 0, -1};
             }
             if (!kShared && threadIdx.x == 0 && w.first && w.t0 > 0 && w.t1 == w.rt.tiles)
-                meta[cluster] = Meta{static_cast<int64_t>(w.rt.row0) * bt.H, live, bar.first_cluster};
+                meta[cluster] = Meta{static_cast<int64_t>(w.rt.row0) * bt.H, live, bar.share[0].first};
         } while (w.next());
         if (lane == 0) bulk_wait_all();                              // written before the CTA leaves
     }
@@ -1171,17 +1251,18 @@ dense_mla_combine_shared_kernel(const float* __restrict__ part_o, const float* _
         const Parts a = parts[token], b = parts[T + token];
         if (b.first == kWritten) continue;
         // (numbers of clusters are cut to those there are: a token of no request has none that mean anything)
+        auto top_of = [&](const Parts& p) { return (p.pair < 0 ? clusters : clusters >> 1) - 1; };
         auto count = [&](const Parts& p) {
-            return p.first == kWritten ? 0 : (p.first < 0 ? 1 : max(1, min(p.last, clusters - 1) - min(p.first, clusters - 1) + 1));
+            return p.first == kWritten ? 0 : (p.first < 0 ? 1 : max(1, min(p.last, top_of(p)) - min(p.first, top_of(p)) + 1));
         };
         auto place = [&](const Parts& p, int j, int64_t whole) {
             if (p.first < 0) return whole + row;
-            const int first = min(p.first, clusters - 1);
-            const int in_tile = max(0, min(slot_rows - 1, (token - p.row0) * H + h));
-            return static_cast<int64_t>(j == 0 ? 2 * first + 1 : 2 * (first + j)) * slot_rows + in_tile;
+            const int at = min(p.first, top_of(p)) + j;
+            const int64_t slot = p.pair < 0 ? 4 * static_cast<int64_t>(at) + 2 : 4 * (2 * static_cast<int64_t>(at) + (p.pair & 1));
+            return (slot + (j == 0 ? 1 : 0)) * slot_rows + max(0, min(slot_rows - 1, (token - p.row0) * H + h));
         };
         const int na = count(a), n = na + count(b);
-        const int64_t whole = 2 * static_cast<int64_t>(clusters) * slot_rows;
+        const int64_t whole = 4 * static_cast<int64_t>(clusters) * slot_rows;
         auto slot_of = [&](int j) {
             return j < na ? place(a, j, whole) : place(b, j - na, whole + static_cast<int64_t>(T) * H);
         };
@@ -1193,9 +1274,9 @@ dense_mla_combine_shared_kernel(const float* __restrict__ part_o, const float* _
 int decode_clusters() { return std::max(1, device_sm_count() / 2); }
 int decode_slot_rows(int64_t T, int64_t H) { return static_cast<int>(std::min<int64_t>(kRows, T * H)); }
 
-// Rows of 512 partial results: two slots a cluster, and with shared prefixes two for each output row.
+// Rows of 512 partial results: two slots a cluster; with shared prefixes four a pair and two for each output row.
 size_t partial_rows(int32_t T, int32_t H, bool shared) {
-    return static_cast<size_t>(2) * decode_clusters() * decode_slot_rows(T, H) + (shared ? static_cast<size_t>(2) * T * H : 0);
+    return static_cast<size_t>(shared ? 4 : 2) * decode_clusters() * decode_slot_rows(T, H) + (shared ? static_cast<size_t>(2) * T * H : 0);
 }
 // ... and in front of them what the combine kernel finds them by.
 size_t directory_bytes(int32_t T, bool shared) {
@@ -1206,6 +1287,31 @@ size_t workspace_bytes_of(int32_t T, int32_t H, bool shared) {
     return directory_bytes(T, shared) + partial_rows(T, H, shared) * (kValueDim + 1) * sizeof(float);
 }
 
+// Clusters of four CTAs that the device holds at once (a GPC whose number of SMs is not a multiple of four leaves some
+// over: 36 on a GPU of 152 SMs); asked once a device.
+int shared_clusters() {
+    static std::atomic<int> known[64];
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return 0;
+    if (dev < 64 && known[dev].load(std::memory_order_relaxed) > 0) return known[dev].load(std::memory_order_relaxed);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(4 * decode_clusters());
+    cfg.blockDim = dim3(kDecThreads);
+    cfg.dynamicSmemBytes = kDecSmem;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 4;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    int n = 0;
+    if (cudaOccupancyMaxActiveClusters(&n, dense_mla_decode_kernel<true>, &cfg) != cudaSuccess) return 0;
+    n = std::min(n, decode_clusters() / 2);
+    if (dev < 64 && n > 0) known[dev].store(n, std::memory_order_relaxed);
+    return n;
+}
+
 template <bool kShared>
 dsa_status launch_decode(const void* q_bf16, const void* kv_pool, int64_t num_pages, const int32_t* block_table,
                          const Batch& bt, float scale, void* out_bf16, float* lse, void* workspace,
@@ -1214,7 +1320,7 @@ dsa_status launch_decode(const void* q_bf16, const void* kv_pool, int64_t num_pa
     if (workspace == nullptr || !aligned16(workspace) || workspace_bytes < workspace_bytes_of(T, H, kShared)) return DSA_ERR_INVALID_ARG;
     auto encode = attn::tensor_map_encoder();
     if (encode == nullptr) return DSA_ERR_CUDA;
-    const int clusters = decode_clusters(), slot_rows = decode_slot_rows(T, H);
+    const int slot_rows = decode_slot_rows(T, H);
     const size_t rows = partial_rows(T, H, kShared);
     float* part_o = reinterpret_cast<float*>(static_cast<unsigned char*>(workspace) + directory_bytes(T, kShared));
     float* part_lse = part_o + rows * kValueDim;
@@ -1230,6 +1336,8 @@ dsa_status launch_decode(const void* q_bf16, const void* kv_pool, int64_t num_pa
     if (cudaFuncSetAttribute(dense_mla_decode_kernel<kShared>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              static_cast<int>(kDecSmem)) != cudaSuccess)
         return DSA_ERR_CUDA;
+    const int clusters = kShared ? 2 * shared_clusters() : decode_clusters();     // pairs of CTAs
+    if (clusters < 1) return DSA_ERR_CUDA;
     // both kernels are programmatic dependents: scheduled as the CTAs of the one before end, they wait for all of it
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
