@@ -73,14 +73,7 @@ constexpr int kMinShare = 2;
 constexpr int kAhead = 2;                                       // tiles between a page's prefetch and its copy
 constexpr size_t kDecSmem = 1024 + size_t(kDataBytes) + 5120;
 static_assert(kDecSmem <= 232448, "shared-memory budget");
-static_assert(3 * kMaxRequests * 4 <= kDataBytes, "schedule scratch");
-
-// Where a share begins.
-struct Share {
-    int unit, g, tile;     // first unit, first row tile (or pair of them) of it, first key tile
-    int left;              // key tiles of the share
-    int first;             // the one that holds the first piece of the first row tile
-};
+static_assert(kMaxRequests * 4 <= kDataBytes, "schedule scratch");
 
 struct DecBars {
     uint64_t kv_full[kMaxStages], kv_empty[kMaxStages];
@@ -103,8 +96,8 @@ struct DecBars {
     uint32_t tmem_slot;
     int page_ok[kMaxStages];                // bit i: page i of the stage is there and its id valid
     int tile_ok[kSBufs];                    // ... of the score tile's pages
-    // this pair's share of the work, and with shared prefixes (second) the cluster's share of what its pairs do together
-    Share share[2];
+    int start[4];                           // first request, first row tile of it, first key tile, tiles of the share
+    int first_cluster;                      // cluster that holds the first piece of the first row tile
     float tmax[2][2][kRows];                // rank 0: [tile parity][key half][row]: maximum of the tile
     alignas(16) float alpha[2][kRows];      // the factors of the tile: rank 0's, copied to rank 1
     float fin[kRows];                       // rank 1: 1 / l; -1: nothing visible
@@ -116,31 +109,13 @@ struct Batch {
     const int32_t* cu_q;
     int B, T, H, max_pages;
     int per;               // query tokens of a row tile: 128 / H
-    // requests [cu_group[g], cu_group[g + 1]) have their first shared_lens[g] positions in common
-    const int32_t* cu_group;
-    const int32_t* shared_lens;
-    int G;
 };
 
-// What the row tiles of a unit have in common: a request's query tokens and keys.  With shared prefixes the units of
-// a pair's share are a group's last row tile over the group's prefix, where their number is odd (units 0 .. G - 1),
-// then a request's tokens over what it has behind that prefix (unit G + b); the units of a cluster's are a group's
-// other row tiles, two at a time.  Positions count from the unit's first key.
-struct Unit {
-    int q0, nq;            // query tokens
-    int vis;               // visible keys of the last one (each earlier one sees one less); a prefix: its length
-    int table, page0;      // row of the block table, first page in it
-    int pages;             // pages of that row from there on
-    bool prefix;           // every token sees the same keys, but for those of requests that are shorter
-    bool part;             // its tokens have another unit: the results are parts
-};
-
-// Row tile g of a unit: up to 128 / H consecutive query tokens.
+// Row tile g of request b: up to 128 / H consecutive query tokens.
 struct RowTile {
     int row0, tokens;      // first query token (global row), number of tokens
     int vis0;              // visible keys of the first one (each next one sees one more; may be <= 0)
-    int most;              // ... of the one that sees most
-    int tiles;             // key tiles of that one
+    int tiles;             // key tiles of the one that sees most
     bool cut;              // visible keys past the block table
 };
 
@@ -152,218 +127,137 @@ __device__ __forceinline__ int query_range(const Batch& bt, int b, int& q0) {
 // Lengths below 0 count as 0.
 __device__ __forceinline__ int seq_len(const Batch& bt, int b) { return max(0, __ldg(bt.seq_lens + b)); }
 
-// Positions of group g's shared prefix: whole pages, inside the table.
-__device__ __forceinline__ int prefix_len(const Batch& bt, int g) {
-    return max(0, min(bt.max_pages, __ldg(bt.shared_lens + g) / kPage)) * kPage;
-}
-// ... of request b's group (the last one that begins at or before it; 0 outside all groups).
-__device__ __forceinline__ int request_prefix(const Batch& bt, int b) {
-    if (bt.G < 1) return 0;
-    const int g = row_request(bt.cu_group, bt.G, b);
-    return __ldg(bt.cu_group + g) <= b && b < __ldg(bt.cu_group + g + 1) ? prefix_len(bt, g) : 0;
-}
-
-template <bool kShared>
-__device__ __forceinline__ int unit_count(const Batch& bt, bool multi) { return multi ? bt.G : (kShared ? bt.G + bt.B : bt.B); }
-
-template <bool kShared>
-__device__ __forceinline__ Unit unit(const Batch& bt, int i, bool multi) {
-    Unit u;
-    if (kShared && i < bt.G) {
-        const int b0 = max(0, min(bt.B, __ldg(bt.cu_group + i))), b1 = max(b0, min(bt.B, __ldg(bt.cu_group + i + 1)));
-        u.vis = prefix_len(bt, i);
-        u.q0 = max(0, min(bt.T, __ldg(bt.cu_q + b0)));
-        u.nq = b1 > b0 && u.vis > 0 ? max(0, min(bt.T, __ldg(bt.cu_q + b1)) - u.q0) : 0;
-        const int paired = (u.nq + bt.per - 1) / bt.per / 2 * 2 * bt.per;       // tokens of the paired row tiles
-        if (multi) {
-            u.nq = min(u.nq, paired);
-        } else {
-            u.q0 += paired;
-            u.nq = max(0, u.nq - paired);
-        }
-        u.table = min(b0, bt.B - 1);
-        u.page0 = 0;
-        u.pages = u.vis / kPage;
-        u.prefix = u.part = true;
-        return u;
-    }
-    const int b = kShared ? i - bt.G : i;
-    const int prefix = kShared ? request_prefix(bt, b) : 0;
-    u.nq = query_range(bt, b, u.q0);
-    u.vis = seq_len(bt, b) - prefix;
-    u.table = b;
-    u.page0 = prefix / kPage;
-    u.pages = bt.max_pages - u.page0;
-    u.prefix = false;
-    u.part = prefix > 0;
-    return u;
-}
-
-__device__ __forceinline__ RowTile row_tile(const Batch& bt, const Unit& u, int g) {
+__device__ __forceinline__ RowTile row_tile(const Batch& bt, int L, int q0, int nq, int g) {
     RowTile t;
-    t.row0 = u.q0 + g * bt.per;
-    t.tokens = min(bt.per, u.nq - g * bt.per);
-    t.vis0 = u.prefix ? u.vis : u.vis - u.nq + g * bt.per + 1;
-    t.most = u.prefix ? u.vis : t.vis0 + t.tokens - 1;
-    t.cut = t.most > u.pages * kPage;
-    t.tiles = (max(0, min(t.most, u.pages * kPage)) + kKeys - 1) / kKeys;
+    t.row0 = q0 + g * bt.per;
+    t.tokens = min(bt.per, nq - g * bt.per);
+    t.vis0 = L - nq + g * bt.per + 1;
+    const int most = t.vis0 + t.tokens - 1;
+    t.cut = most > bt.max_pages * kPage;
+    t.tiles = (max(0, min(most, bt.max_pages * kPage)) + kKeys - 1) / kKeys;
     return t;
 }
 
-// The pieces of a pair's shares, one row tile after the other; every role walks them by itself.  What a cluster does
-// together comes first, with both pairs on the same keys, each with its own row tile of two.
-template <bool kShared>
+// A share's pieces, one row tile after the other; every role walks them by itself.
 struct Walk {
     Batch bt;
-    const Share* share;
-    int pair;
-    int i, g, left;        // unit, row tile (or pair of them) of it, tiles left in the share
-    Unit u;
+    int b, g, q0, nq, L, left;
     RowTile rt;
     int t0, t1;            // key tiles [t0, t1) of the piece (t0 == t1: a row tile that sees nothing)
     bool whole, first;     // the piece is its whole row tile; the share's first piece
-    bool multi;            // the cluster's share
 
-    __device__ Walk(const Batch& batch, const Share* shares, int pair_) : bt(batch), share(shares), pair(pair_) {
-        multi = kShared && uniform(shares[1].left) > 0;
-        begin(shares[kShared && multi ? 1 : 0]);
-    }
-    __device__ void begin(const Share& s) {
-        i = uniform(s.unit);
-        g = uniform(s.g);
-        t0 = uniform(s.tile);
-        left = uniform(s.left);
+    __device__ Walk(const Batch& batch, const int* start) : bt(batch) {
+        b = uniform(start[0]);
+        g = uniform(start[1]);
+        t0 = uniform(start[2]);
+        left = uniform(start[3]);
         first = true;
-        load_unit();
+        load_request();
         set_piece();
     }
-    __device__ void load_unit() {
-        u = unit<kShared>(bt, i, multi);
-        u.nq = uniform(u.nq);
-        u.q0 = uniform(u.q0);
-        u.vis = uniform(u.vis);
-        if (kShared) {
-            u.table = uniform(u.table);
-            u.page0 = uniform(u.page0);
-            u.pages = uniform(u.pages);
-        }
+    __device__ void load_request() {
+        nq = uniform(query_range(bt, b, q0));
+        q0 = uniform(q0);
+        L = uniform(seq_len(bt, b));
     }
     __device__ void set_piece() {
-        rt = row_tile(bt, u, kShared && multi ? 2 * g + pair : g);
+        rt = row_tile(bt, L, q0, nq, g);
         const int n = max(1, rt.tiles);
         const int take = min(n - t0, left);
         whole = take == n;
         left -= take;
         t1 = min(t0 + take, rt.tiles);
     }
-    // false: the shares are done
+    // false: the share is done
     __device__ bool next() {
-        if (left <= 0) {
-            if (!kShared || !multi || uniform(share[0].left) <= 0) return false;
-            multi = false;
-            begin(share[0]);
-            return true;
-        }
+        if (left <= 0) return false;
         t0 = 0;
         first = false;
-        if ((g + 1) * (kShared && multi ? 2 * bt.per : bt.per) < u.nq) {
+        if ((g + 1) * bt.per < nq) {
             ++g;
         } else {
             g = 0;
             do {
-                if (++i >= unit_count<kShared>(bt, multi)) return false;
-                load_unit();
-            } while (u.nq == 0);
+                if (++b >= bt.B) return false;
+                load_request();
+            } while (nq == 0);
         }
         set_piece();
         return true;
     }
 };
 
-// Workspace slots of a share's parts: 2 c for the one that starts share c but not its row tile, else 2 c + 1.  With
-// shared prefixes a pair has four: two for its cluster's share, then two for its own.
-template <bool kShared>
-__device__ __forceinline__ int64_t piece_slot(int pair_id, const Walk<kShared>& w) {
-    return (kShared ? 4 * static_cast<int64_t>(pair_id) + (w.multi ? 0 : 2) : 2 * static_cast<int64_t>(pair_id)) +
-           ((w.first && w.t0 > 0) ? 0 : 1);
+// Workspace slot of a part: 2 c for the one that starts share c but not its row tile, else 2 c + 1.
+__device__ __forceinline__ int64_t piece_slot(int cluster, const Walk& w) {
+    return 2 * static_cast<int64_t>(cluster) + ((w.first && w.t0 > 0) ? 0 : 1);
 }
 
-// Key tiles of a unit over all its row tiles, or pairs of them (a row tile that sees nothing counts as one).
-template <bool kShared>
-__device__ __forceinline__ int unit_tiles(const Batch& bt, int i, bool multi, int32_t* err) {
-    const Unit u = unit<kShared>(bt, i, multi);
-    if (kShared && u.prefix) {
-        if (err != nullptr && (__ldg(bt.cu_group + i) < 0 || __ldg(bt.cu_group + i + 1) < __ldg(bt.cu_group + i) ||
-                               __ldg(bt.cu_group + i + 1) > bt.B || __ldg(bt.shared_lens + i) / kPage > bt.max_pages))
-            raise_error(err, DSA_DEVERR_INDEX_RANGE);
-        const int per = multi ? 2 * bt.per : bt.per;
-        return (u.nq + per - 1) / per * ((u.vis + kKeys - 1) / kKeys);
-    }
-    const int b = kShared ? i - bt.G : i;
+// Key tiles of request b over all its row tiles (a row tile that sees nothing counts as one).
+__device__ __forceinline__ int request_tiles(const Batch& bt, int b, int32_t* err) {
+    int q0;
+    const int nq = query_range(bt, b, q0);
     if (err != nullptr && (__ldg(bt.cu_q + b) < 0 || __ldg(bt.cu_q + b + 1) > bt.T)) raise_error(err, DSA_DEVERR_INDEX_RANGE);
-    if (u.nq == 0) return 0;
+    if (nq == 0) return 0;
+    const int L = seq_len(bt, b);
     int sum = 0;
-    for (int g = 0; g * bt.per < u.nq; ++g) {
-        const RowTile t = row_tile(bt, u, g);
+    for (int g = 0; g * bt.per < nq; ++g) {
+        const RowTile t = row_tile(bt, L, q0, nq, g);
         if (t.cut && err != nullptr) raise_error(err, DSA_DEVERR_INDEX_RANGE);
         sum += max(1, t.tiles);
     }
     return sum;
 }
 
-// One warp: share c of `workers` equal ones, from the sums of all units.
-template <bool kShared>
-__device__ __forceinline__ void cut_share(const Batch& bt, int c, int workers, const int* sums, bool multi, Share& out) {
-    const int lane = threadIdx.x & 31, units = unit_count<kShared>(bt, multi);
-    int total = 0;
-    for (int b = lane; b < units; b += 32) total += sums[b];
-#pragma unroll
-    for (int m = 16; m > 0; m >>= 1) total += __shfl_xor_sync(0xffffffffu, total, m);
-    const int share = max((total + workers - 1) / workers, kMinShare);
-    const int64_t w0 = static_cast<int64_t>(c) * share;
-    if (lane == 0) out.left = w0 < total ? static_cast<int>(min(static_cast<int64_t>(share), total - w0)) : 0;
-    if (w0 >= total) return;
-    int carry = 0;
-    for (int b0 = 0; b0 < units; b0 += 32) {
-        const int b = b0 + lane;
-        int inc = b < units ? sums[b] : 0;
-        const int own = inc;
-#pragma unroll
-        for (int d = 1; d < 32; d <<= 1) {
-            const int o = __shfl_up_sync(0xffffffffu, inc, d);
-            if (lane >= d) inc += o;
-        }
-        const uint32_t hit = __ballot_sync(0xffffffffu, w0 < carry + inc);
-        if (hit != 0u) {
-            if (lane == __ffs(hit) - 1) {
-                int at = carry + inc - own;                    // tiles before the unit
-                const Unit u = unit<kShared>(bt, b, multi);
-                int g = 0;
-                for (;; ++g) {
-                    const int n = max(1, row_tile(bt, u, multi ? 2 * g : g).tiles);
-                    if (w0 < at + n) break;
-                    at += n;
-                }
-                out.unit = b;
-                out.g = g;
-                out.tile = static_cast<int>(w0 - at);
-                out.first = at / share;
-            }
-            break;
-        }
-        carry += __shfl_sync(0xffffffffu, inc, 31);
-    }
-}
-
-// The shares of this pair: sums of all units in `sums` (shared), then a warp for each finds the start.
-template <bool kShared>
-__device__ __forceinline__ void find_share(const Batch& bt, int pair_id, int pairs, int* sums, DecBars& bar, int32_t* err) {
-    const int multi_units = kShared ? bt.G : 0, units = unit_count<kShared>(bt, false);
-    for (int b = threadIdx.x; b < multi_units + units; b += kDecThreads)
-        sums[b] = unit_tiles<kShared>(bt, b < multi_units ? b : b - multi_units, b < multi_units, pair_id == 0 ? err : nullptr);
+// The share of cluster c: sums of all requests in `sums` (shared), then one warp finds the start.
+__device__ __forceinline__ void find_share(const Batch& bt, int c, int clusters, int* sums, DecBars& bar, int32_t* err) {
+    for (int b = threadIdx.x; b < bt.B; b += kDecThreads) sums[b] = request_tiles(bt, b, c == 0 ? err : nullptr);
     __syncthreads();
-    if (threadIdx.x < 32) cut_share<kShared>(bt, pair_id, pairs, sums + multi_units, false, bar.share[0]);
-    if (kShared && threadIdx.x >= 32 && threadIdx.x < 64) cut_share<kShared>(bt, pair_id >> 1, pairs >> 1, sums, true, bar.share[1]);
+    if (threadIdx.x < 32) {
+        const int lane = threadIdx.x;
+        int total = 0;
+        for (int b = lane; b < bt.B; b += 32) total += sums[b];
+#pragma unroll
+        for (int m = 16; m > 0; m >>= 1) total += __shfl_xor_sync(0xffffffffu, total, m);
+        const int share = max((total + clusters - 1) / clusters, kMinShare);
+        const int64_t w0 = static_cast<int64_t>(c) * share;
+        if (lane == 0) {
+            bar.start[3] = w0 < total ? static_cast<int>(min(static_cast<int64_t>(share), total - w0)) : 0;
+        }
+        if (w0 < total) {
+            int carry = 0;
+            for (int b0 = 0; b0 < bt.B; b0 += 32) {
+                const int b = b0 + lane;
+                int inc = b < bt.B ? sums[b] : 0;
+                const int own = inc;
+#pragma unroll
+                for (int d = 1; d < 32; d <<= 1) {
+                    const int o = __shfl_up_sync(0xffffffffu, inc, d);
+                    if (lane >= d) inc += o;
+                }
+                const uint32_t hit = __ballot_sync(0xffffffffu, w0 < carry + inc);
+                if (hit != 0u) {
+                    if (lane == __ffs(hit) - 1) {
+                        int at = carry + inc - own;            // tiles before the request
+                        int q0;
+                        const int nq = query_range(bt, b, q0);
+                        const int L = seq_len(bt, b);
+                        int g = 0;
+                        for (;; ++g) {
+                            const int n = max(1, row_tile(bt, L, q0, nq, g).tiles);
+                            if (w0 < at + n) break;
+                            at += n;
+                        }
+                        bar.start[0] = b;
+                        bar.start[1] = g;
+                        bar.start[2] = static_cast<int>(w0 - at);
+                        bar.first_cluster = at / share;
+                    }
+                    break;
+                }
+                carry += __shfl_sync(0xffffffffu, inc, 31);
+            }
+        }
+    }
     __syncthreads();
 }
 
@@ -397,25 +291,13 @@ __device__ __forceinline__ void prefetch_line(const void* p) { asm volatile("pre
 __device__ __forceinline__ void arrive_remote(uint32_t bar) {
     asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
-// Arrive on the barrier at this offset in the CTAs of `mask` once the MMAs issued so far have completed.
-__device__ __forceinline__ void umma_commit_to(uint64_t* bar, uint32_t mask) {
+// Arrive on the barrier at this offset in rank 0 once the MMAs issued so far have completed.
+__device__ __forceinline__ void umma_commit_rank0(uint64_t* bar) {
     asm volatile(
         "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
             ptx::smem_addr(bar)),
-        "h"(static_cast<uint16_t>(mask))
+        "h"(static_cast<uint16_t>(1))
         : "memory");
-}
-// TMA load into the same place of all CTAs of `mask`, counted on the barrier at this offset in each.
-__device__ __forceinline__ void tma_load_3d_to(void* dst, const CUtensorMap* map, uint64_t* bar, int c0, int c1, int c2, uint32_t mask) {
-    asm volatile(
-        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.multicast::cluster"
-        " [%0], [%1, {%3, %4, %5}], [%2], %6;" ::"r"(ptx::smem_addr(dst)),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(ptx::smem_addr(bar)), "r"(c0), "r"(c1), "r"(c2),
-        "h"(static_cast<uint16_t>(mask))
-        : "memory");
-}
-__device__ __forceinline__ void mbar_arrive_n(uint64_t* bar, uint32_t n) {
-    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0], %1;" ::"r"(ptx::smem_addr(bar)), "r"(n) : "memory");
 }
 
 // What a cluster leaves for the combine kernel: the split row tile whose last piece it computed.
@@ -425,23 +307,13 @@ struct Meta {
     int first_cluster;
 };
 
-// With shared prefixes, where the parts of a query token's rows lie, over its group's prefix ([0]) and over the rest ([1]).
-struct Parts {
-    int first;             // kWritten: there are none, kWholePart: one, in the rows' own place; else the first cluster's
-    int last;              // the last cluster (or pair: a pair's own share)
-    int row0;              // first token of the row tile
-    int pair;              // which pair of the clusters; -1: first and last are pairs
-};
-constexpr int kWritten = -2, kWholePart = -1;
-
-template <bool kShared>
-__global__ void __launch_bounds__(kDecThreads, 1) __cluster_dims__(kShared ? 4 : 2, 1, 1)
+__global__ void __launch_bounds__(kDecThreads, 1) __cluster_dims__(2, 1, 1)
 dense_mla_decode_kernel(const __grid_constant__ CUtensorMap kvmap, const __grid_constant__ CUtensorMap qmap,
                         const __grid_constant__ CUtensorMap omap, const __grid_constant__ CUtensorMap pmap,
                         const uint16_t* __restrict__ kv, int num_pages,
                         const int32_t* __restrict__ block_table, Batch bt, float scale, uint16_t* __restrict__ out,
-                        float* __restrict__ lse_out, float* __restrict__ part_lse, Meta* __restrict__ meta,
-                        Parts* __restrict__ parts, int slot_rows, int32_t* err) {
+                        float* __restrict__ lse_out, float* __restrict__ part_lse, Meta* __restrict__ meta, int slot_rows,
+                        int32_t* err) {
     extern __shared__ unsigned char smem_raw[];
     const uint32_t raw_addr = ptx::smem_addr(smem_raw);
     unsigned char* base = smem_raw + (((raw_addr + 1023u) & ~1023u) - raw_addr);
@@ -451,17 +323,13 @@ dense_mla_decode_kernel(const __grid_constant__ CUtensorMap kvmap, const __grid_
     DecBars& bar = *reinterpret_cast<DecBars*>(base + kDataBytes);
 
     const int warp = uniform(static_cast<int>(threadIdx.x >> 5)), lane = threadIdx.x & 31;
-    // pairs of CTAs: a cluster is one, with shared prefixes two that share the copies of what both read
-    const uint32_t cta = cluster_ctarank(), rank = kShared ? cta & 1u : cta;
-    const uint32_t score_cta = kShared ? cta & 2u : 0u, value_cta = score_cta + 1u;
-    const int pair = kShared ? static_cast<int>(uniform(cta >> 1)) : 0;
-    const uint32_t both = rank == 0 ? 0x5u : 0xau;                // this role's CTAs of both pairs
+    const uint32_t rank = cluster_ctarank();
     const int cluster = blockIdx.x >> 1, clusters = gridDim.x >> 1;
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < kMaxStages; ++s) {
             ptx::mbar_init(&bar.kv_full[s], 1);
-            ptx::mbar_init(&bar.kv_empty[s], kShared ? 2 : 1);    // the stage has been read: here and in the other pair
+            ptx::mbar_init(&bar.kv_empty[s], 1);
         }
         ptx::mbar_init(&bar.q_full, 8);
         for (int s = 0; s < kKStages; ++s) ptx::mbar_init(&bar.q_read[s], 4);
@@ -488,7 +356,7 @@ dense_mla_decode_kernel(const __grid_constant__ CUtensorMap kvmap, const __grid_
         ptx::tmem_relinquish();
     }
     ptx::griddep_wait();             // a programmatic dependent: what came before is complete
-    find_share<kShared>(bt, cluster, clusters, reinterpret_cast<int*>(ring), bar, rank == 0 ? err : nullptr);
+    find_share(bt, cluster, clusters, reinterpret_cast<int*>(ring), bar, rank == 0 ? err : nullptr);
     ptx::fence_proxy_async_smem();   // the schedule's scratch lies where copies will land
     ptx::tc_fence_before_sync();
     cluster_sync_all();              // both CTAs' barriers exist before the peer signals or writes into them
@@ -497,33 +365,14 @@ dense_mla_decode_kernel(const __grid_constant__ CUtensorMap kvmap, const __grid_
     // limit of every wait, set anew every 256 tiles: a wait lasts a tile or so, the kernel may run for seconds
     uint64_t deadline = ptx::wait_deadline();
     bool timed_out = false;
-    const bool work = uniform(bar.share[0].left) > 0 || (kShared && uniform(bar.share[1].left) > 0);
+    const bool work = uniform(bar.start[3]) > 0;
     const uint32_t ring_addr = ptx::smem_addr(ring);
-    if (!kShared && threadIdx.x == 0 && rank == 1) meta[cluster].rows = 0;
-    // first row of a whole row tile's parts: behind the slots, those over a prefix first
-    auto part_row = [&](const Walk<kShared>& w) {
-        return 4 * static_cast<int64_t>(clusters) * slot_rows + (static_cast<int64_t>(w.u.prefix ? 0 : bt.T) + w.rt.row0) * bt.H;
-    };
-    // One thread gives a stage back: once the MMAs issued so far have completed, and now.  In a cluster's share the copies
-    // land in both pairs, so both give back to both; in a pair's own it stands for the other as well.
-    auto commit_stage = [&](uint64_t* b, bool multi) {
-        if (kShared && multi) {
-            umma_commit_to(b, both);
-        } else {
-            ptx::umma_commit(b);
-            if (kShared) ptx::umma_commit(b);
-        }
-    };
-    auto give_stage = [&](uint64_t* b, bool multi) {
-        if (kShared && multi) umma_commit_to(b, both);
-        else if (kShared) mbar_arrive_n(b, 2);
-        else ptx::mbar_arrive(b);
-    };
+    if (threadIdx.x == 0 && rank == 1) meta[cluster].rows = 0;
 
     if (work && warp == kTmaWarp) {
         // ---------------------------------------------------------------- TMA (both ranks)
         const uint32_t stages = rank == 0 ? kKStages : kVStages;
-        Walk<kShared> w(bt, bar.share, pair);
+        Walk w(bt, bar.start);
         uint32_t s = 0, ph = 0, used = 0;                            // stage, its phase, stages used so far
         auto stage = [&]() {                                         // the next stage is free (whole warp)
             if (!ptx::mbar_wait(&bar.kv_empty[s], ph ^ 1u, deadline)) timed_out = true;
@@ -548,12 +397,11 @@ dense_mla_decode_kernel(const __grid_constant__ CUtensorMap kvmap, const __grid_
                     }
                     advance();
                 }
-            const int most = w.rt.most;
-            const int32_t* table = block_table + static_cast<int64_t>(w.u.table) * bt.max_pages + w.u.page0;
+            const int most = w.rt.vis0 + w.rt.tokens - 1;            // visible keys of the token that sees most
             auto load_pages = [&](int t) {                           // page ids of 16 tiles from t on
                 const int at = 2 * t + lane;
-                const bool needed = at < 2 * w.t1 && at * kPage < most && at < w.u.pages;
-                return needed ? __ldg(table + at) : -1;
+                const bool needed = at < 2 * w.t1 && at * kPage < most && at < bt.max_pages;
+                return needed ? __ldg(block_table + static_cast<int64_t>(w.b) * bt.max_pages + at) : -1;
             };
             int page = -1, page_next = load_pages(w.t0);
             for (int t = w.t0; t < w.t1 && !timed_out; ++t) {
@@ -568,7 +416,6 @@ dense_mla_decode_kernel(const __grid_constant__ CUtensorMap kvmap, const __grid_
                     // its rate (418 -> 393 us on 64 requests of 4K to 64K; from rank 0, or further ahead, slower)
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
-                        if (kShared && w.multi && i != pair) continue;
                         const int src = 2 * (tb + kAhead) + i;
                         const int near = __shfl_sync(0xffffffffu, page, src & 31), far = __shfl_sync(0xffffffffu, page_next, src & 31);
                         const int pg = src < 32 ? near : far;
@@ -583,7 +430,7 @@ dense_mla_decode_kernel(const __grid_constant__ CUtensorMap kvmap, const __grid_
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
                     const int pg = __shfl_sync(0xffffffffu, page, 2 * tb + i);
-                    const bool needed = (2 * t + i) * kPage < most && 2 * t + i < w.u.pages;
+                    const bool needed = (2 * t + i) * kPage < most && 2 * t + i < bt.max_pages;
                     const bool there = needed && pg >= 0 && pg < num_pages;
                     // a page that is not there: a box past the end reads zeros, and rank 0 masks its keys
                     row[i] = (there ? pg : num_pages) * kPage;
@@ -595,13 +442,8 @@ dense_mla_decode_kernel(const __grid_constant__ CUtensorMap kvmap, const __grid_
                         if (elect_one()) {
                             bar.page_ok[s] = ok;
                             ptx::mbar_arrive_expect_tx(&bar.kv_full[s], kKStageBytes);
-                            if (kShared && w.multi) {                // a page each, to both
-                                tma_load_3d_to(ring + s * kKStageBytes + pair * kPageChunk, &kvmap, &bar.kv_full[s], c * 64, 0,
-                                               pair == 0 ? row[0] : row[1], both);
-                            } else {
-                                ptx::tma_load_3d(ring + s * kKStageBytes, &kvmap, &bar.kv_full[s], c * 64, 0, row[0]);
-                                ptx::tma_load_3d(ring + s * kKStageBytes + kPageChunk, &kvmap, &bar.kv_full[s], c * 64, 0, row[1]);
-                            }
+                            ptx::tma_load_3d(ring + s * kKStageBytes, &kvmap, &bar.kv_full[s], c * 64, 0, row[0]);
+                            ptx::tma_load_3d(ring + s * kKStageBytes + kPageChunk, &kvmap, &bar.kv_full[s], c * 64, 0, row[1]);
                         }
                         advance();
                     }
@@ -609,17 +451,10 @@ dense_mla_decode_kernel(const __grid_constant__ CUtensorMap kvmap, const __grid_
                     for (int i = 0; i < 4 && stage(); ++i) {         // page i / 2, value dims 256 (i % 2) .. + 255
                         if (elect_one()) {
                             ptx::mbar_arrive_expect_tx(&bar.kv_full[s], kVStageBytes);
-                            if (kShared && w.multi) {                // 128 of the dims each, to both
 #pragma unroll
-                                for (int j = 0; j < 2; ++j)
-                                    tma_load_3d_to(ring + s * kVStageBytes + (2 * pair + j) * kPageChunk, &kvmap, &bar.kv_full[s],
-                                                   (i & 1) * 256 + (2 * pair + j) * 64, 0, row[i >> 1], both);
-                            } else {
-#pragma unroll
-                                for (int j = 0; j < 4; ++j)
-                                    ptx::tma_load_3d(ring + s * kVStageBytes + j * kPageChunk, &kvmap, &bar.kv_full[s],
-                                                     (i & 1) * 256 + j * 64, 0, row[i >> 1]);
-                            }
+                            for (int j = 0; j < 4; ++j)
+                                ptx::tma_load_3d(ring + s * kVStageBytes + j * kPageChunk, &kvmap, &bar.kv_full[s],
+                                                 (i & 1) * 256 + j * 64, 0, row[i >> 1]);
                         }
                         advance();
                     }
@@ -648,7 +483,7 @@ dense_mla_decode_kernel(const __grid_constant__ CUtensorMap kvmap, const __grid_
         auto wait = [&](uint64_t* b, uint32_t parity) {
             if (!ptx::mbar_wait(b, parity, deadline)) late = true;
         };
-        Walk<kShared> w(bt, bar.share, pair);
+        Walk w(bt, bar.start);
         uint32_t u = 0, seg = 0, s = 0, ph = 0, q_phase = 0;          // q_phase: bit s, the phase of q_read[s]
         do {
             if (w.t0 >= w.t1) continue;
@@ -656,7 +491,7 @@ dense_mla_decode_kernel(const __grid_constant__ CUtensorMap kvmap, const __grid_
                 wait(&bar.q_read[s], (q_phase >> s) & 1u);
                 q_phase ^= 1u << s;
                 __syncwarp();
-                if (elect_one()) give_stage(&bar.kv_empty[s], w.multi);
+                if (elect_one()) ptx::mbar_arrive(&bar.kv_empty[s]);
                 __syncwarp();
                 if (++s == kKStages) {
                     s = 0;
@@ -686,7 +521,7 @@ dense_mla_decode_kernel(const __grid_constant__ CUtensorMap kvmap, const __grid_
                             if (c < 8) umma_f16_ts(d, tmem + c * 32 + kk * 8, so + kk * 2, idesc, (c | kk) != 0 ? 1u : 0u);
                             else ptx::umma_f16(d, qr_desc + kk * 2, so + kk * 2, idesc, 1u);
                         }
-                        commit_stage(&bar.kv_empty[s], w.multi);
+                        ptx::umma_commit(&bar.kv_empty[s]);
                         if (c == 8) ptx::umma_commit(&bar.s_full[sb]);
                     }
                     __syncwarp();
@@ -707,7 +542,7 @@ dense_mla_decode_kernel(const __grid_constant__ CUtensorMap kvmap, const __grid_
         auto wait = [&](uint64_t* b, uint32_t parity) {
             if (!ptx::mbar_wait(b, parity, deadline)) late = true;
         };
-        Walk<kShared> w(bt, bar.share, pair);
+        Walk w(bt, bar.start);
         uint32_t u = 0, seg = 0, s = 0, ph = 0;
         do {
             if (w.t0 >= w.t1) continue;
@@ -717,7 +552,7 @@ dense_mla_decode_kernel(const __grid_constant__ CUtensorMap kvmap, const __grid_
                 for (int i = 0; i < 4; ++i) {                        // page i / 2, value dims 256 (i % 2) .. + 255
                     const uint32_t pb = 2 * (u & 1u) + (i >> 1);
                     wait(&bar.kv_full[s], ph);
-                    const int valid = w.rt.most - t * kKeys - (i >> 1) * kPage;
+                    const int valid = w.rt.vis0 + w.rt.tokens - 1 - t * kKeys - (i >> 1) * kPage;
                     if (valid > 0 && valid < kPage) {
                         // rows past the last visible position may hold anything: their P is 0, but 0 times NaN
                         // or infinity is not (a page without visible rows was filled with zeros)
@@ -744,8 +579,8 @@ dense_mla_decode_kernel(const __grid_constant__ CUtensorMap kvmap, const __grid_
                         for (int ks = 0; ks < kPage / 16; ++ks)
                             ptx::umma_f16(tmem + (i & 1) * 256, pd + ks * 2, vb + ks * 128, idesc,
                                           (t > w.t0 || i >= 2 || ks != 0) ? 1u : 0u);
-                        commit_stage(&bar.kv_empty[s], w.multi);
-                        if ((i & 1) == 1) umma_commit_to(&bar.p_free[pb], 1u << score_cta);
+                        ptx::umma_commit(&bar.kv_empty[s]);
+                        if ((i & 1) == 1) umma_commit_rank0(&bar.p_free[pb]);
                         if (i == 3) ptx::umma_commit(&bar.pv_done[u % kPvBars]);
                     }
                     __syncwarp();
@@ -759,7 +594,7 @@ dense_mla_decode_kernel(const __grid_constant__ CUtensorMap kvmap, const __grid_
             wait(&bar.stage_back, seg & 1u);
             for (int i = 0; i < 2; ++i) {
                 __syncwarp();
-                if (elect_one()) give_stage(&bar.kv_empty[s], w.multi);
+                if (elect_one()) ptx::mbar_arrive(&bar.kv_empty[s]);
                 if (++s == kVStages) {
                     s = 0;
                     ph ^= 1u;
@@ -778,14 +613,14 @@ dense_mla_decode_kernel(const __grid_constant__ CUtensorMap kvmap, const __grid_
         const int token = row / bt.H;
         const uint32_t p_row = row * 128, p_swz = row & 7;           // the row's place in a P buffer
         // this warp's 32 rows of a P buffer, and their factors, here and in rank 1
-        const uint32_t p_here = ptx::smem_addr(ps) + quad * 4096, p_there = map_to_rank(p_here, value_cta);
-        const uint32_t a_here = ptx::smem_addr(&bar.alpha[0][quad * 32]), a_there = map_to_rank(a_here, value_cta);
-        const uint32_t full_there = map_to_rank(ptx::smem_addr(&bar.p_full[0]), value_cta);
+        const uint32_t p_here = ptx::smem_addr(ps) + quad * 4096, p_there = map_to_rank(p_here, 1);
+        const uint32_t a_here = ptx::smem_addr(&bar.alpha[0][quad * 32]), a_there = map_to_rank(a_here, 1);
+        const uint32_t full_there = map_to_rank(ptx::smem_addr(&bar.p_full[0]), 1);
         auto wait = [&](uint64_t* b, uint32_t parity) {
             if (!ptx::mbar_wait(b, parity, deadline)) timed_out = true;
         };
         uint32_t u = 0, seg = 0, meets = 0, used = 0;                // meets: uses of the pair barrier; used: ring stages
-        Walk<kShared> w(bt, bar.share, pair);
+        Walk w(bt, bar.start);
         do {
             const int live = w.rt.tokens * bt.H;
             const bool quad_live = quad * 32 < live;
@@ -793,14 +628,7 @@ dense_mla_decode_kernel(const __grid_constant__ CUtensorMap kvmap, const __grid_
             // of them, but zeros there let the tensor cores idle, and a long call runs at the power limit (8 requests of
             // about 128K with two rows of 16 heads, one call after the other: 200 -> 178 us at 1.47 -> 1.74 GHz)
             const bool row_live = row < live;
-            int vis = row_live ? min(w.rt.vis0 + token, w.u.pages * kPage) : 0;
-            if (kShared && w.u.prefix && row_live) {
-                // a request shorter than its group's prefix sees its own length of it
-                const int r = w.rt.row0 + token, b = row_request(bt.cu_q, bt.B, r);
-                int q0;
-                const int nq = query_range(bt, b, q0);
-                vis = min(w.u.vis, seq_len(bt, b) - nq + (r - q0) + 1);
-            }
+            const int vis = row_live ? min(w.rt.vis0 + token, bt.max_pages * kPage) : 0;
             float m_run = -INFINITY, l_run = 0.0f;
             if (w.t0 < w.t1) {
                 // the row tile's queries out of the ring: value chunks into tensor memory, the rope chunk into its
@@ -943,13 +771,12 @@ dense_mla_decode_kernel(const __grid_constant__ CUtensorMap kvmap, const __grid_
                     ++meets;
                     if (seg > 0) wait(&bar.fin_free, (seg - 1) & 1u);
                     if (kh == 0)
-                        st_async_f32(map_to_rank(ptx::smem_addr(&bar.fin[row]), value_cta), l_tot == 0.0f ? -1.0f : 1.0f / l_tot,
-                                     map_to_rank(ptx::smem_addr(&bar.fin_full), value_cta));
+                        st_async_f32(map_to_rank(ptx::smem_addr(&bar.fin[row]), 1), l_tot == 0.0f ? -1.0f : 1.0f / l_tot,
+                                     map_to_rank(ptx::smem_addr(&bar.fin_full), 1));
                 }
                 if (kh == 0 && row < live) {
                     const float lse2 = l_tot == 0.0f ? -INFINITY : m_run * cs + log2f(l_tot);
                     if (!w.whole) part_lse[piece_slot(cluster, w) * slot_rows + row] = lse2;
-                    else if (kShared && w.u.part) part_lse[part_row(w) + row] = lse2;
                     else if (lse_out != nullptr) lse_out[static_cast<int64_t>(w.rt.row0) * bt.H + row] = lse2 * kLn2;
                 }
             }
@@ -968,7 +795,7 @@ dense_mla_decode_kernel(const __grid_constant__ CUtensorMap kvmap, const __grid_
         };
         uint32_t u = 0, seg = 0, used = 0;                           // used: ring stages before this row tile
         uint32_t clean = 0;                                          // bit i: this row group's P is zero in buffers 2 i and 2 i + 1
-        Walk<kShared> w(bt, bar.share, pair);
+        Walk w(bt, bar.start);
         do {
             const int live = w.rt.tokens * bt.H;
             const bool quad_live = quad * 32 < live, has_tiles = w.t0 < w.t1;
@@ -1029,7 +856,7 @@ dense_mla_decode_kernel(const __grid_constant__ CUtensorMap kvmap, const __grid_
                 // when rank 0 learns that it may write the next ones
                 hidden = __ballot_sync(0xffffffffu, inv < 0.0f);
                 __syncwarp();
-                if (lane == 0) arrive_remote(map_to_rank(ptx::smem_addr(&bar.fin_free), score_cta));
+                if (lane == 0) arrive_remote(map_to_rank(ptx::smem_addr(&bar.fin_free), 0));
                 wait(&bar.pv_done[(u - 1) % kPvBars], ((u - 1) / kPvBars) & 1u);
                 timed_out = __any_sync(0xffffffffu, timed_out);
                 if (timed_out) break;
@@ -1044,17 +871,15 @@ dense_mla_decode_kernel(const __grid_constant__ CUtensorMap kvmap, const __grid_
                 wait(&bar.stage_lent, seg & 1u);
                 timed_out = __any_sync(0xffffffffu, timed_out);
                 if (timed_out) break;
-                const bool final = w.whole && !(kShared && w.u.part);
-                const int width = final ? 64 : 32;                   // dims of 128 bytes
-                const int64_t row0 = final ? static_cast<int64_t>(w.rt.row0) * bt.H
-                                           : (w.whole ? part_row(w) : piece_slot(cluster, w) * slot_rows);
+                const int width = w.whole ? 64 : 32;                 // dims of 128 bytes
+                const int64_t row0 = w.whole ? static_cast<int64_t>(w.rt.row0) * bt.H : piece_slot(cluster, w) * slot_rows;
                 const int swz = lane & 7;
                 int buf = 0;
 #pragma unroll 1
                 for (int cc = 0; quad_live && cc < 256; cc += width, buf ^= 1) {
                     uint32_t o[32];                                  // the row's 128 bytes
                     ptx::tmem_ld_32x32b_x32(o_addr + cc, o);
-                    if (final) {
+                    if (w.whole) {
                         uint32_t x[32];
                         ptx::tmem_ld_32x32b_x32(o_addr + cc + 32, x);
                         ptx::tmem_wait_ld();
@@ -1082,7 +907,7 @@ dense_mla_decode_kernel(const __grid_constant__ CUtensorMap kvmap, const __grid_
 #pragma unroll
                         for (int h = 0; h < 2; ++h)
                             if (quad * 32 + 16 * h < live)
-                                tma_store_3d(final ? &omap : &pmap, st + h * 2048, dh * 256 + cc, 0,
+                                tma_store_3d(w.whole ? &omap : &pmap, st + h * 2048, dh * 256 + cc, 0,
                                              static_cast<int>(row0) + quad * 32 + 16 * h);
                         bulk_commit();
                     }
@@ -1096,21 +921,14 @@ dense_mla_decode_kernel(const __grid_constant__ CUtensorMap kvmap, const __grid_
                 }
                 used += 2;
                 ++seg;
-            } else if (quad_live && !(kShared && w.u.part)) {        // sees nothing: zeros
+            } else if (quad_live) {                                  // sees nothing: zeros
                 for (int r = quad * 32; r < min(live, quad * 32 + 32); ++r)
                     *reinterpret_cast<uint4*>(out + (static_cast<int64_t>(w.rt.row0) * bt.H + r) * kValueDim + dh * 256 + lane * 8) =
                         make_uint4(0u, 0u, 0u, 0u);
             }
             // the last piece of a split row tile: the combine kernel finds it here
-            if (kShared && w.t1 == w.rt.tiles && static_cast<int>(threadIdx.x) < w.rt.tokens) {
-                const int at = w.rt.row0 + threadIdx.x;
-                const int where = !w.whole ? bar.share[w.multi ? 1 : 0].first : (w.u.part ? kWholePart : kWritten);
-                parts[w.u.prefix ? at : bt.T + at] =
-                    Parts{where, w.multi ? cluster >> 1 : cluster, w.rt.row0, w.multi ? pair : -1};
-                if (!w.u.part) parts[at] = Parts{kWritten, 0, 0, -1};
-            }
-            if (!kShared && threadIdx.x == 0 && w.first && w.t0 > 0 && w.t1 == w.rt.tiles)
-                meta[cluster] = Meta{static_cast<int64_t>(w.rt.row0) * bt.H, live, bar.share[0].first};
+            if (threadIdx.x == 0 && w.first && w.t0 > 0 && w.t1 == w.rt.tiles)
+                meta[cluster] = Meta{static_cast<int64_t>(w.rt.row0) * bt.H, live, bar.first_cluster};
         } while (w.next());
         if (lane == 0) bulk_wait_all();                              // written before the CTA leaves
     }
@@ -1132,12 +950,15 @@ dense_mla_decode_kernel(const __grid_constant__ CUtensorMap kvmap, const __grid_
 constexpr int kCombThreads = 256;
 constexpr int kCombBlocks = 4;     // per SM (32 requests of 8K: 1 block an SM 33 us of the call, 2 to 8 about 15)
 
-// V x 128 dims from d0 on of one output row, joined from n parts, P at a time: their sums and values are loaded
-// together.  slot_of(j): the row of part j.
-template <int V, int P, typename F>
-__device__ __forceinline__ void join_row(const float* __restrict__ part_o, const float* __restrict__ part_lse, int n,
-                                         F slot_of, int64_t out_row, int d0, int lane, uint16_t* __restrict__ out,
-                                         float* __restrict__ lse_out) {
+// V x 128 dims from d0 on of one row, P pieces at a time: their sums and values are loaded together.
+template <int V, int P>
+__device__ __forceinline__ void join_row(const float* __restrict__ part_o, const float* __restrict__ part_lse,
+                                         const Meta& m, int c, int slot_rows, int row, int d0, int lane,
+                                         uint16_t* __restrict__ out, float* __restrict__ lse_out) {
+    const int n = c - m.first_cluster + 1;
+    auto slot_of = [&](int j) {
+        return static_cast<int64_t>(j == 0 ? 2 * m.first_cluster + 1 : 2 * (m.first_cluster + j)) * slot_rows + row;
+    };
     float m_run = -INFINITY, tot = 0.0f;
     float4 acc[V];
 #pragma unroll
@@ -1178,10 +999,10 @@ __device__ __forceinline__ void join_row(const float* __restrict__ part_o, const
     const float inv = tot == 0.0f ? 0.0f : 1.0f / tot;
 #pragma unroll
     for (int v = 0; v < V; ++v)
-        *reinterpret_cast<uint2*>(out + out_row * kValueDim + d0 + v * 128 + lane * 4) =
+        *reinterpret_cast<uint2*>(out + (m.out_row + row) * kValueDim + d0 + v * 128 + lane * 4) =
             make_uint2(pack_bf16x2(acc[v].x * inv, acc[v].y * inv), pack_bf16x2(acc[v].z * inv, acc[v].w * inv));
     if (lse_out != nullptr && d0 == 0 && lane == 0)
-        lse_out[out_row] = tot == 0.0f ? -INFINITY : (m_run + log2f(tot)) * kLn2;
+        lse_out[m.out_row + row] = tot == 0.0f ? -INFINITY : (m_run + log2f(tot)) * kLn2;
 }
 
 __global__ void __launch_bounds__(kCombThreads)
@@ -1220,12 +1041,8 @@ dense_mla_combine_kernel(const float* __restrict__ part_o, const float* __restri
             const int c = list_c[li];
             const int tasks = many ? m.rows : m.rows * 4;
             for (; at < tasks; at += nwarps) {
-                const int row = many ? at : at >> 2, n = c - m.first_cluster + 1;
-                auto slot_of = [&](int j) {
-                    return static_cast<int64_t>(j == 0 ? 2 * m.first_cluster + 1 : 2 * (m.first_cluster + j)) * slot_rows + row;
-                };
-                if (many) join_row<4, 2>(part_o, part_lse, n, slot_of, m.out_row + row, 0, lane, out, lse_out);
-                else join_row<1, 4>(part_o, part_lse, n, slot_of, m.out_row + row, (at & 3) * 128, lane, out, lse_out);
+                if (many) join_row<4, 2>(part_o, part_lse, m, c, slot_rows, at, 0, lane, out, lse_out);
+                else join_row<1, 4>(part_o, part_lse, m, c, slot_rows, at >> 2, (at & 3) * 128, lane, out, lse_out);
             }
             at -= tasks;
         }
@@ -1233,111 +1050,55 @@ dense_mla_combine_kernel(const float* __restrict__ part_o, const float* __restri
     }
 }
 
-// The same with shared prefixes: each query token says where its parts are.
-__global__ void __launch_bounds__(kCombThreads)
-dense_mla_combine_shared_kernel(const float* __restrict__ part_o, const float* __restrict__ part_lse,
-                                const Parts* __restrict__ parts, const int32_t* __restrict__ cu_q, int B, int T, int H,
-                                int clusters, int slot_rows, uint16_t* __restrict__ out, float* __restrict__ lse_out) {
-    ptx::griddep_wait();
-    const int lane = threadIdx.x & 31;
-    const int64_t nwarps = static_cast<int64_t>(gridDim.x) * (kCombThreads / 32);
-    const int r0 = max(0, min(T, __ldg(cu_q))), r1 = max(0, min(T, __ldg(cu_q + B)));
-    const int64_t rows = static_cast<int64_t>(max(0, r1 - r0)) * H;
-    const bool many = rows >= nwarps;
-    for (int64_t at = static_cast<int64_t>(blockIdx.x) * (kCombThreads / 32) + (threadIdx.x >> 5); at < (many ? rows : rows * 4);
-         at += nwarps) {
-        const int64_t row = static_cast<int64_t>(r0) * H + (many ? at : at >> 2);
-        const int token = static_cast<int>(row / H), h = static_cast<int>(row - static_cast<int64_t>(token) * H);
-        const Parts a = parts[token], b = parts[T + token];
-        if (b.first == kWritten) continue;
-        // (numbers of clusters are cut to those there are: a token of no request has none that mean anything)
-        auto top_of = [&](const Parts& p) { return (p.pair < 0 ? clusters : clusters >> 1) - 1; };
-        auto count = [&](const Parts& p) {
-            return p.first == kWritten ? 0 : (p.first < 0 ? 1 : max(1, min(p.last, top_of(p)) - min(p.first, top_of(p)) + 1));
-        };
-        auto place = [&](const Parts& p, int j, int64_t whole) {
-            if (p.first < 0) return whole + row;
-            const int at = min(p.first, top_of(p)) + j;
-            const int64_t slot = p.pair < 0 ? 4 * static_cast<int64_t>(at) + 2 : 4 * (2 * static_cast<int64_t>(at) + (p.pair & 1));
-            return (slot + (j == 0 ? 1 : 0)) * slot_rows + max(0, min(slot_rows - 1, (token - p.row0) * H + h));
-        };
-        const int na = count(a), n = na + count(b);
-        const int64_t whole = 4 * static_cast<int64_t>(clusters) * slot_rows;
-        auto slot_of = [&](int j) {
-            return j < na ? place(a, j, whole) : place(b, j - na, whole + static_cast<int64_t>(T) * H);
-        };
-        if (many) join_row<4, 2>(part_o, part_lse, n, slot_of, row, 0, lane, out, lse_out);
-        else join_row<1, 4>(part_o, part_lse, n, slot_of, row, static_cast<int>(at & 3) * 128, lane, out, lse_out);
-    }
-}
-
 int decode_clusters() { return std::max(1, device_sm_count() / 2); }
 int decode_slot_rows(int64_t T, int64_t H) { return static_cast<int>(std::min<int64_t>(kRows, T * H)); }
 
-// Rows of 512 partial results: two slots a cluster; with shared prefixes four a pair and two for each output row.
-size_t partial_rows(int32_t T, int32_t H, bool shared) {
-    return static_cast<size_t>(shared ? 4 : 2) * decode_clusters() * decode_slot_rows(T, H) + (shared ? static_cast<size_t>(2) * T * H : 0);
-}
-// ... and in front of them what the combine kernel finds them by.
-size_t directory_bytes(int32_t T, bool shared) {
-    return shared ? (static_cast<size_t>(2) * T * sizeof(Parts) + 15) / 16 * 16 : static_cast<size_t>(decode_clusters()) * sizeof(Meta);
-}
-size_t workspace_bytes_of(int32_t T, int32_t H, bool shared) {
+}  // namespace
+}  // namespace dsa
+
+extern "C" size_t dsa_dense_mla_decode_workspace_size(int32_t T, int32_t H) {
+    using namespace dsa;
     if (T <= 0 || H <= 0) return 0;
-    return directory_bytes(T, shared) + partial_rows(T, H, shared) * (kValueDim + 1) * sizeof(float);
+    const size_t c = static_cast<size_t>(decode_clusters()), rows = static_cast<size_t>(decode_slot_rows(T, H));
+    return c * sizeof(Meta) + 2 * c * rows * (kValueDim + 1) * sizeof(float);
 }
 
-// Clusters of four CTAs that the device holds at once (a GPC whose number of SMs is not a multiple of four leaves some
-// over: 36 on a GPU of 152 SMs); asked once a device.
-int shared_clusters() {
-    static std::atomic<int> known[64];
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess) return 0;
-    if (dev < 64 && known[dev].load(std::memory_order_relaxed) > 0) return known[dev].load(std::memory_order_relaxed);
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(4 * decode_clusters());
-    cfg.blockDim = dim3(kDecThreads);
-    cfg.dynamicSmemBytes = kDecSmem;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = 4;
-    attr[0].val.clusterDim.y = 1;
-    attr[0].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    int n = 0;
-    if (cudaOccupancyMaxActiveClusters(&n, dense_mla_decode_kernel<true>, &cfg) != cudaSuccess) return 0;
-    n = std::min(n, decode_clusters() / 2);
-    if (dev < 64 && n > 0) known[dev].store(n, std::memory_order_relaxed);
-    return n;
-}
-
-template <bool kShared>
-dsa_status launch_decode(const void* q_bf16, const void* kv_pool, int64_t num_pages, const int32_t* block_table,
-                         const Batch& bt, float scale, void* out_bf16, float* lse, void* workspace,
-                         size_t workspace_bytes, int32_t* dev_err, void* stream) {
-    const int T = bt.T, H = bt.H;
-    if (workspace == nullptr || !aligned16(workspace) || workspace_bytes < workspace_bytes_of(T, H, kShared)) return DSA_ERR_INVALID_ARG;
+extern "C" dsa_status dsa_dense_mla_decode(const void* q_bf16, const void* kv_pool, int64_t num_pages,
+                                           const int32_t* block_table, int32_t max_pages, const int32_t* seq_lens,
+                                           const int32_t* cu_q, int32_t B, int32_t T, int32_t H, float scale,
+                                           void* out_bf16, float* lse, void* workspace, size_t workspace_bytes,
+                                           int32_t* dev_err, void* stream) {
+    using namespace dsa;
+    if (H != 16 && H != 32 && H != 64 && H != 128) return DSA_ERR_UNSUPPORTED;
+    if (T < 0 || B < 0 || max_pages < 0 || num_pages < 0) return DSA_ERR_INVALID_ARG;
+    if (T == 0 || B == 0) return DSA_OK;
+    if (num_pages < 1 || max_pages < 1) return DSA_ERR_INVALID_ARG;
+    if (!q_bf16 || !kv_pool || !block_table || !seq_lens || !cu_q || !out_bf16) return DSA_ERR_INVALID_ARG;
+    if (!aligned16(q_bf16) || !aligned16(kv_pool) || !aligned16(out_bf16)) return DSA_ERR_INVALID_ARG;
+    if (!(scale > 0.0f) || !(scale < INFINITY)) return DSA_ERR_INVALID_ARG;
+    if ((num_pages + 1) * kPage >= 0x7fffffffLL || static_cast<int64_t>(max_pages) * kPage >= 0x7fffffffLL ||
+        static_cast<int64_t>(T) * H >= 0x7fffffffLL || B > kMaxRequests)
+        return DSA_ERR_UNSUPPORTED;
+    // the schedule counts key tiles in 32 bits
+    if (static_cast<int64_t>(T) * max_pages >= 0x7fffffffLL) return DSA_ERR_UNSUPPORTED;
+    const size_t need = dsa_dense_mla_decode_workspace_size(T, H);
+    if (workspace == nullptr || !aligned16(workspace) || workspace_bytes < need) return DSA_ERR_INVALID_ARG;
     auto encode = attn::tensor_map_encoder();
     if (encode == nullptr) return DSA_ERR_CUDA;
-    const int slot_rows = decode_slot_rows(T, H);
-    const size_t rows = partial_rows(T, H, kShared);
-    float* part_o = reinterpret_cast<float*>(static_cast<unsigned char*>(workspace) + directory_bytes(T, kShared));
-    float* part_lse = part_o + rows * kValueDim;
-    Meta* meta = kShared ? nullptr : static_cast<Meta*>(workspace);
-    Parts* parts = kShared ? static_cast<Parts*>(workspace) : nullptr;
+    const int clusters = decode_clusters(), slot_rows = decode_slot_rows(T, H);
+    Meta* meta = static_cast<Meta*>(workspace);
+    float* part_o = reinterpret_cast<float*>(meta + clusters);
+    float* part_lse = part_o + static_cast<size_t>(2) * clusters * slot_rows * kValueDim;
     CUtensorMap kvmap, qmap, omap, pmap;
     if (!attn::encode_bf16_3d(encode, &kvmap, kv_pool, kLatentDim, 1, num_pages * kPage, kLatentDim, kLatentDim, 64, kPage) ||
         !attn::encode_bf16_3d(encode, &qmap, q_bf16, kLatentDim, 1, static_cast<uint64_t>(T) * H, kLatentDim, kLatentDim, 64, kRows) ||
         !attn::encode_bf16_3d(encode, &omap, out_bf16, kValueDim, 1, static_cast<uint64_t>(T) * H, kValueDim, kValueDim, 64, 16) ||
-        !attn::encode_f32_rows(encode, &pmap, part_o, kValueDim, rows, 32, 16))
+        !attn::encode_f32_rows(encode, &pmap, part_o, kValueDim, static_cast<uint64_t>(2) * clusters * slot_rows, 32, 16))
         return DSA_ERR_CUDA;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    if (cudaFuncSetAttribute(dense_mla_decode_kernel<kShared>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    if (cudaFuncSetAttribute(dense_mla_decode_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              static_cast<int>(kDecSmem)) != cudaSuccess)
         return DSA_ERR_CUDA;
-    const int clusters = kShared ? 2 * shared_clusters() : decode_clusters();     // pairs of CTAs
-    if (clusters < 1) return DSA_ERR_CUDA;
     // both kernels are programmatic dependents: scheduled as the CTAs of the one before end, they wait for all of it
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -1349,85 +1110,16 @@ dsa_status launch_decode(const void* q_bf16, const void* kv_pool, int64_t num_pa
     cfg.stream = s;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    if (cudaLaunchKernelEx(&cfg, dense_mla_decode_kernel<kShared>, kvmap, qmap, omap, pmap, static_cast<const uint16_t*>(kv_pool),
-                           static_cast<int>(num_pages), block_table, bt, scale, static_cast<uint16_t*>(out_bf16), lse,
-                           part_lse, meta, parts, slot_rows, dev_err) != cudaSuccess)
+    if (cudaLaunchKernelEx(&cfg, dense_mla_decode_kernel, kvmap, qmap, omap, pmap, static_cast<const uint16_t*>(kv_pool),
+                           static_cast<int>(num_pages), block_table, Batch{seq_lens, cu_q, B, T, H, max_pages, kRows / H},
+                           scale, static_cast<uint16_t*>(out_bf16), lse, part_lse, meta, slot_rows, dev_err) != cudaSuccess)
         return DSA_ERR_CUDA;
     cfg.gridDim = dim3(2 * clusters * kCombBlocks);
     cfg.blockDim = dim3(kCombThreads);
     cfg.dynamicSmemBytes = 0;
-    cudaError_t e;
-    if constexpr (kShared)
-        e = cudaLaunchKernelEx(&cfg, dense_mla_combine_shared_kernel, static_cast<const float*>(part_o),
-                               static_cast<const float*>(part_lse), static_cast<const Parts*>(parts), bt.cu_q, bt.B, T, H,
-                               clusters, slot_rows, static_cast<uint16_t*>(out_bf16), lse);
-    else
-        e = cudaLaunchKernelEx(&cfg, dense_mla_combine_kernel, static_cast<const float*>(part_o),
-                               static_cast<const float*>(part_lse), static_cast<const Meta*>(meta), clusters, slot_rows,
-                               static_cast<uint16_t*>(out_bf16), lse);
-    if (e != cudaSuccess) return DSA_ERR_CUDA;
+    if (cudaLaunchKernelEx(&cfg, dense_mla_combine_kernel, static_cast<const float*>(part_o),
+                           static_cast<const float*>(part_lse), static_cast<const Meta*>(meta), clusters, slot_rows,
+                           static_cast<uint16_t*>(out_bf16), lse) != cudaSuccess)
+        return DSA_ERR_CUDA;
     return launch_status();
-}
-
-// What both calls refuse before the workspace; DSA_OK with *nothing set where there is nothing to do.
-dsa_status check_decode(const void* q_bf16, const void* kv_pool, int64_t num_pages, const int32_t* block_table,
-                        const Batch& bt, float scale, const void* out_bf16, bool* nothing) {
-    const int T = bt.T, B = bt.B, H = bt.H, max_pages = bt.max_pages;
-    *nothing = false;
-    if (H != 16 && H != 32 && H != 64 && H != 128) return DSA_ERR_UNSUPPORTED;
-    if (T < 0 || B < 0 || max_pages < 0 || num_pages < 0) return DSA_ERR_INVALID_ARG;
-    *nothing = T == 0 || B == 0;
-    if (*nothing) return DSA_OK;
-    if (num_pages < 1 || max_pages < 1) return DSA_ERR_INVALID_ARG;
-    if (!q_bf16 || !kv_pool || !block_table || !bt.seq_lens || !bt.cu_q || !out_bf16) return DSA_ERR_INVALID_ARG;
-    if (!aligned16(q_bf16) || !aligned16(kv_pool) || !aligned16(out_bf16)) return DSA_ERR_INVALID_ARG;
-    if (!(scale > 0.0f) || !(scale < INFINITY)) return DSA_ERR_INVALID_ARG;
-    if ((num_pages + 1) * kPage >= 0x7fffffffLL || static_cast<int64_t>(max_pages) * kPage >= 0x7fffffffLL ||
-        static_cast<int64_t>(T) * H >= 0x7fffffffLL || B > kMaxRequests)
-        return DSA_ERR_UNSUPPORTED;
-    // the schedule counts key tiles in 32 bits
-    if (static_cast<int64_t>(T) * max_pages >= 0x7fffffffLL) return DSA_ERR_UNSUPPORTED;
-    return DSA_OK;
-}
-
-}  // namespace
-}  // namespace dsa
-
-extern "C" size_t dsa_dense_mla_decode_workspace_size(int32_t T, int32_t H) { return dsa::workspace_bytes_of(T, H, false); }
-
-extern "C" dsa_status dsa_dense_mla_decode(const void* q_bf16, const void* kv_pool, int64_t num_pages,
-                                           const int32_t* block_table, int32_t max_pages, const int32_t* seq_lens,
-                                           const int32_t* cu_q, int32_t B, int32_t T, int32_t H, float scale,
-                                           void* out_bf16, float* lse, void* workspace, size_t workspace_bytes,
-                                           int32_t* dev_err, void* stream) {
-    using namespace dsa;
-    const Batch bt{seq_lens, cu_q, B, T, H, max_pages, H > 0 ? kRows / H : 0, nullptr, nullptr, 0};
-    bool nothing;
-    const dsa_status st = check_decode(q_bf16, kv_pool, num_pages, block_table, bt, scale, out_bf16, &nothing);
-    if (st != DSA_OK || nothing) return st;
-    return launch_decode<false>(q_bf16, kv_pool, num_pages, block_table, bt, scale, out_bf16, lse, workspace,
-                                workspace_bytes, dev_err, stream);
-}
-
-extern "C" size_t dsa_dense_mla_decode_shared_workspace_size(int32_t T, int32_t H) { return dsa::workspace_bytes_of(T, H, true); }
-
-extern "C" dsa_status dsa_dense_mla_decode_shared(const void* q_bf16, const void* kv_pool, int64_t num_pages,
-                                                  const int32_t* block_table, int32_t max_pages,
-                                                  const int32_t* seq_lens, const int32_t* cu_q, int32_t B, int32_t T,
-                                                  int32_t H, const int32_t* cu_group, const int32_t* shared_lens,
-                                                  int32_t G, float scale, void* out_bf16, float* lse, void* workspace,
-                                                  size_t workspace_bytes, int32_t* dev_err, void* stream) {
-    using namespace dsa;
-    const Batch bt{seq_lens, cu_q, B, T, H, max_pages, H > 0 ? kRows / H : 0, cu_group, shared_lens, G};
-    bool nothing;
-    const dsa_status st = check_decode(q_bf16, kv_pool, num_pages, block_table, bt, scale, out_bf16, &nothing);
-    if (st != DSA_OK) return st;
-    if (G < 0) return DSA_ERR_INVALID_ARG;
-    if (nothing) return DSA_OK;
-    if (G > 0 && (!cu_group || !shared_lens)) return DSA_ERR_INVALID_ARG;
-    // groups' tiles come on top of the requests'; the parts' rows are counted in 32 bits
-    if (G > kMaxRequests || static_cast<int64_t>(T) * max_pages >= 0x3fffffffLL || static_cast<int64_t>(T) * H >= 0x3ff00000LL)
-        return DSA_ERR_UNSUPPORTED;
-    return launch_decode<true>(q_bf16, kv_pool, num_pages, block_table, bt, scale, out_bf16, lse, workspace,
-                               workspace_bytes, dev_err, stream);
 }
