@@ -60,6 +60,8 @@ constexpr int kTmaWarp = 8, kMmaWarp = 9;
 constexpr int kThreads = 384;
 constexpr uint32_t kColS = 256;                                 // scores: score tiles, behind the query chunks
 constexpr int kMinShare = 2;
+constexpr int kUnitCost = 4;                                    // tiles that the change to another unit takes as long as,
+constexpr int kLongShare = 8;                                   // counted in shares of this many tiles or more
 constexpr int kAhead = 2;                                       // tiles between a page's prefetch and its copy
 constexpr int kMaxRequests = 16384, kMaxGroups = 8192, kMaxUnits = 16384;   // units of 256 rows
 constexpr size_t kBarBytes = 6144;
@@ -69,8 +71,9 @@ static_assert((kMaxUnits + kMaxGroups + 3) * 4 <= kDataBytes, "schedule scratch"
 
 // Where a cluster's share begins.
 struct Share {
-    int unit, tile, left;   // first unit, first key tile of it, key tiles of the share
+    int unit, at, left;     // first unit, where in it, length of the share
     int first;              // the cluster that holds the first piece of the first unit
+    int cost;               // length of a unit in front of its tiles
 };
 
 struct Bars {
@@ -117,6 +120,7 @@ struct Batch {
     const int32_t* shared_lens;
     int G;
     int units;             // numbers that the units lie within: T / (2 per) + G + 3
+    int shift;             // 2 per = 1 << shift
 };
 
 __device__ __forceinline__ int token_at(const Batch& bt, int b) { return max(0, min(bt.T, __ldg(bt.cu_q + b))); }
@@ -134,12 +138,13 @@ __device__ __forceinline__ int span_prefix(const Batch& bt, int k) {
     return k < 1 || k > bt.G ? 0 : max(0, min(bt.max_pages, __ldg(bt.shared_lens + k - 1) / kPage)) * kPage;
 }
 // Number of its first unit: the last one's is below the next span's.
-__device__ __forceinline__ int span_unit(const Batch& bt, int k) { return token_at(bt, span_begin(bt, k)) / (2 * bt.per) + k; }
+__device__ __forceinline__ int span_unit(const Batch& bt, int k) { return (token_at(bt, span_begin(bt, k)) >> bt.shift) + k; }
 
 struct Unit {
     int q0, nq;            // query tokens
     int prefix;            // positions of the shared prefix
     int b0;                // the request through whose row of the table it is read
+    int requests, span_q0, span_nq;    // of the whole group
 };
 
 __device__ __forceinline__ Unit unit_of(const Batch& bt, int i) {
@@ -150,13 +155,20 @@ __device__ __forceinline__ Unit unit_of(const Batch& bt, int i) {
     }
     const int b0 = span_begin(bt, k), b1 = max(b0, span_begin(bt, k + 1));
     const int q0 = token_at(bt, b0), nq = b1 > b0 ? max(0, token_at(bt, b1) - q0) : 0;
-    const int64_t at = static_cast<int64_t>(i - span_unit(bt, k)) * 2 * bt.per;
-    Unit u{0, 0, span_prefix(bt, k), min(b0, bt.B - 1)};
+    const int64_t at = static_cast<int64_t>(i - span_unit(bt, k)) << bt.shift;
+    Unit u{0, 0, span_prefix(bt, k), min(b0, bt.B - 1), b1 - b0, q0, nq};
     if (at >= 0 && at < nq) {
         u.q0 = q0 + static_cast<int>(at);
         u.nq = min(2 * bt.per, nq - static_cast<int>(at));
     }
     return u;
+}
+
+// The request of query token r, which is one of [b0, b1)'s: where all have as many tokens, the first guess.
+__device__ __forceinline__ int request_of(const Batch& bt, const Unit& u, int r) {
+    const int guess = u.b0 + min(u.requests - 1, static_cast<int>(__fdividef(static_cast<float>(r - u.span_q0) * u.requests, static_cast<float>(u.span_nq))));
+    if (guess >= 0 && guess < bt.B && __ldg(bt.cu_q + guess) <= r && r < __ldg(bt.cu_q + guess + 1)) return guess;
+    return row_request(bt.cu_q, bt.B, r);
 }
 
 // A query token of a unit: its request, the keys it sees of the prefix and behind it.
@@ -179,7 +191,7 @@ __device__ __forceinline__ Token token_of(const Batch& bt, const Unit& u, int r,
 }
 // Pages behind the prefix (of each request as many as its last token in the unit sees).
 __device__ __forceinline__ int own_pages(const Batch& bt, const Unit& u, bool& cut) {
-    Token t = token_of(bt, u, u.q0, row_request(bt.cu_q, bt.B, u.q0));
+    Token t = token_of(bt, u, u.q0, request_of(bt, u, u.q0));
     int pages = 0;
     cut = t.cut;
     for (int j = 1; j < u.nq; ++j) {
@@ -190,15 +202,25 @@ __device__ __forceinline__ int own_pages(const Batch& bt, const Unit& u, bool& c
     }
     return pages + (t.own + kPage - 1) / kPage;
 }
-// Key tiles of a unit (one that sees nothing counts as one).
-__device__ __forceinline__ int unit_tiles(const Batch& bt, int i, int32_t* err) {
-    const Unit u = unit_of(bt, i);
-    if (u.nq == 0) return 0;
-    bool cut;
-    const int pages = u.prefix / kPage + own_pages(bt, u, cut);
-    if (cut && err != nullptr) raise_error(err, DSA_DEVERR_INDEX_RANGE);
-    return max(1, (pages + 1) / 2);
+// The same by a warp, a token a lane: lane j's token, the first of its request's pages among the unit's, how many (at the
+// request's last token, else 0).  Returns all of the unit's pages.
+__device__ __forceinline__ int unit_segments(const Batch& bt, const Unit& u, Token& tok, int& seg_at, int& seg_pages) {
+    const int lane = threadIdx.x & 31;
+    tok = Token{-1, 0, 0, false};
+    if (lane < u.nq) tok = token_of(bt, u, u.q0 + lane, request_of(bt, u, u.q0));
+    const int next_b = __shfl_down_sync(0xffffffffu, tok.b, 1);
+    seg_pages = lane < u.nq && (lane == u.nq - 1 || next_b != tok.b) ? (tok.own + kPage - 1) / kPage : 0;
+    int upto = seg_pages;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+        const int o = __shfl_up_sync(0xffffffffu, upto, d);
+        if (lane >= d) upto += o;
+    }
+    seg_at = u.prefix / kPage + upto - seg_pages;
+    return u.prefix / kPage + __shfl_sync(0xffffffffu, upto, 31);
 }
+// Key tiles of a unit in the schedule: one that sees nothing counts as one.
+__device__ __forceinline__ int schedule_tiles(int pages) { return max(1, (pages + 1) / 2); }
 
 // A share's pieces, one unit after the other; every role walks them by itself (whole warps).
 struct Walk {
@@ -208,6 +230,8 @@ struct Walk {
     int pages, tiles;      // of the unit
     int t0, t1;            // key tiles [t0, t1) of the piece (t0 == t1: a unit that sees nothing)
     bool whole, first;     // the piece is its whole unit; the share's first piece
+    bool nothing;          // no piece at all
+    int at, cost;          // where in the unit's length the share is; what of that comes in front of its tiles
     // lane j: token j's request, the first of that request's pages among the unit's, how many (at the request's last
     // token, else 0), and the keys it sees
     Token tok;
@@ -215,36 +239,27 @@ struct Walk {
 
     __device__ Walk(const Batch& batch, const Share& s) : bt(batch) {
         i = uniform(s.unit);
-        t0 = uniform(s.tile);
+        at = uniform(s.at);
+        cost = uniform(s.cost);
         left = uniform(s.left);
         first = true;
         u = unit_of(bt, i);
         set_piece();
     }
     __device__ void set_piece() {
-        const int lane = threadIdx.x & 31;
         u.q0 = uniform(u.q0);
         u.nq = uniform(u.nq);
         u.prefix = uniform(u.prefix);
-        const int b = row_request(bt.cu_q, bt.B, u.q0);
-        tok = Token{-1, 0, 0, false};
-        if (lane < u.nq) tok = token_of(bt, u, u.q0 + lane, b);
-        const int next_b = __shfl_down_sync(0xffffffffu, tok.b, 1);
-        seg_pages = lane < u.nq && (lane == u.nq - 1 || next_b != tok.b) ? (tok.own + kPage - 1) / kPage : 0;
-        int upto = seg_pages;
-#pragma unroll
-        for (int d = 1; d < 32; d <<= 1) {
-            const int o = __shfl_up_sync(0xffffffffu, upto, d);
-            if (lane >= d) upto += o;
-        }
-        seg_at = u.prefix / kPage + upto - seg_pages;
-        pages = uniform(u.prefix / kPage + __shfl_sync(0xffffffffu, upto, 31));
+        pages = uniform(unit_segments(bt, u, tok, seg_at, seg_pages));
         tiles = (pages + 1) / 2;
-        const int n = max(1, tiles);
-        const int take = min(n - t0, left);
-        whole = take == n;
+        // of the unit's length (what a change of units costs, then the tiles) from `at` on
+        const int n = cost + schedule_tiles(pages);
+        const int take = min(n - at, left);
+        t0 = max(0, at - cost);
+        whole = t0 == 0 && at + take == n;
         left -= take;
-        t1 = min(t0 + take, tiles);
+        t1 = min(max(0, at + take - cost), tiles);
+        nothing = at + take <= cost;                             // the share ends before the first tile
     }
     // Tokens of one rank's row tile
     __device__ int tokens(int side) const { return max(0, min(bt.per, u.nq - side * bt.per)); }
@@ -265,20 +280,39 @@ struct Walk {
     // false: the share is done
     __device__ bool next() {
         if (left <= 0) return false;
-        t0 = 0;
+        at = 0;
         first = false;
         do {
             if (++i >= bt.units) return false;
             u = unit_of(bt, i);
         } while (u.nq == 0);
         set_piece();
-        return true;
+        return !nothing;
     }
 };
 
-// The share of cluster c: tiles of all units in `sums` (shared), then one warp finds the start.
+// The share of cluster c: lengths of all units in `sums` (shared), then one warp finds the start.
 __device__ __forceinline__ void find_share(const Batch& bt, int c, int clusters, int* sums, Share& out, int32_t* err) {
-    for (int i = threadIdx.x; i < bt.units; i += kThreads) sums[i] = unit_tiles(bt, i, err);
+    // few units: a warp each, a token a lane; many: a thread each, one token after the other
+    bool cut = false;
+    if (bt.units <= 64) {
+        for (int i = threadIdx.x >> 5; i < bt.units; i += kThreads / 32) {
+            const Unit u = unit_of(bt, i);
+            Token tok;
+            int seg_at, seg_pages;
+            const int pages = unit_segments(bt, u, tok, seg_at, seg_pages);
+            cut |= tok.cut;
+            if ((threadIdx.x & 31) == 0) sums[i] = u.nq > 0 ? schedule_tiles(pages) : 0;
+        }
+    } else {
+        for (int i = threadIdx.x; i < bt.units; i += kThreads) {
+            const Unit u = unit_of(bt, i);
+            bool c = false;
+            sums[i] = u.nq > 0 ? schedule_tiles(u.prefix / kPage + own_pages(bt, u, c)) : 0;
+            cut |= c;
+        }
+    }
+    if (cut && err != nullptr) raise_error(err, DSA_DEVERR_INDEX_RANGE);
     if (err != nullptr) {
         for (int b = threadIdx.x; b < bt.B; b += kThreads)
             if (__ldg(bt.cu_q + b) < 0 || __ldg(bt.cu_q + b + 1) > bt.T) raise_error(err, DSA_DEVERR_INDEX_RANGE);
@@ -290,17 +324,24 @@ __device__ __forceinline__ void find_share(const Batch& bt, int c, int clusters,
     __syncthreads();
     if (threadIdx.x < 32) {
         const int lane = threadIdx.x;
-        int total = 0;
-        for (int i = lane; i < bt.units; i += 32) total += sums[i];
-#pragma unroll
-        for (int m = 16; m > 0; m >>= 1) total += __shfl_xor_sync(0xffffffffu, total, m);
-        const int share = max((total + clusters - 1) / clusters, kMinShare);
+        int tiles = 0, some = 0;
+        for (int i = lane; i < bt.units; i += 32) {
+            tiles += sums[i];
+            some += sums[i] > 0 ? 1 : 0;
+        }
+        tiles = __reduce_add_sync(0xffffffffu, tiles);
+        some = __reduce_add_sync(0xffffffffu, some);
+        // a cluster that changes units gets fewer tiles (64 requests behind 32K: 119 -> 108 us); few tiles are cut as they are
+        const int cost = tiles >= kLongShare * clusters ? kUnitCost : 0;
+        const int total = tiles + some * cost;
+        const int share = max((total + clusters - 1) / clusters, cost + kMinShare);
         const int64_t w0 = static_cast<int64_t>(c) * share;
+        if (lane == 0) out.cost = cost;
         if (lane == 0) out.left = w0 < total ? static_cast<int>(min(static_cast<int64_t>(share), total - w0)) : 0;
         int carry = 0;
         for (int i0 = 0; i0 < bt.units && w0 < total; i0 += 32) {
             const int i = i0 + lane;
-            const int own = i < bt.units ? sums[i] : 0;
+            const int own = i < bt.units && sums[i] > 0 ? sums[i] + cost : 0;
             int inc = own;
 #pragma unroll
             for (int d = 1; d < 32; d <<= 1) {
@@ -310,10 +351,10 @@ __device__ __forceinline__ void find_share(const Batch& bt, int c, int clusters,
             const uint32_t hit = __ballot_sync(0xffffffffu, w0 < carry + inc);
             if (hit != 0u) {
                 if (lane == __ffs(hit) - 1) {
-                    const int at = carry + inc - own;            // tiles before the unit
+                    const int at = carry + inc - own;            // length before the unit
                     out.unit = i;
-                    out.tile = static_cast<int>(w0 - at);
-                    out.first = at / share;
+                    out.at = static_cast<int>(w0 - at);
+                    out.first = (at + cost) / share;
                 }
                 break;
             }
@@ -474,7 +515,7 @@ dense_mla_shared_kernel(const __grid_constant__ Maps maps, const uint16_t* __res
     // limit of every wait, set anew every 256 tiles: a wait lasts a tile or so, the kernel may run for seconds
     uint64_t deadline = ptx::wait_deadline();
     bool timed_out = false;
-    const bool work = uniform(bar.share.left) > 0;
+    const bool work = uniform(bar.share.left) > 0;   // (its first unit may begin after the share's end)
     const uint32_t ring_addr = ptx::smem_addr(ring);
     const int pair_id = 2 * cluster + side;
     // workspace slot of a piece that is not a whole unit: 2 c for the one that starts share c but not its unit, else 2 c + 1
@@ -1217,7 +1258,7 @@ extern "C" dsa_status dsa_dense_mla_decode_shared(const void* q_bf16, const void
     auto encode = attn::tensor_map_encoder();
     if (encode == nullptr) return DSA_ERR_CUDA;
     const int per = kRows / H, pairs = slot_pairs(), slot_rows = shared_slot_rows(T, H);
-    const Batch bt{seq_lens, cu_q, B, T, H, max_pages, per, cu_group, shared_lens, G, T / (2 * per) + G + 3};
+    const Batch bt{seq_lens, cu_q, B, T, H, max_pages, per, cu_group, shared_lens, G, T / (2 * per) + G + 3, H == 16 ? 4 : (H == 32 ? 3 : (H == 64 ? 2 : 1))};
     Meta* meta = static_cast<Meta*>(workspace);
     float* part_o = reinterpret_cast<float*>(meta + pairs);
     float* part_lse = part_o + static_cast<size_t>(2) * pairs * slot_rows * kValueDim;
