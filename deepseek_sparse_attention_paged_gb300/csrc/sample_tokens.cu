@@ -300,13 +300,45 @@ struct Cut {
     __device__ __forceinline__ bool keeps(float x, int v) const { return x > z || (x == z && v <= index); }
 };
 
-// A CTA's slice in shared memory: groups of 16 bytes that lie as they do in global memory (on 16-byte
-// boundaries), entries outside the slice -infinity.  Warp w has the groups [w per, (w + 1) per), its lanes
-// one after the other: a thread reads only what it wrote itself, and warps, steps and lanes follow the indices.
+// NaN counts as -infinity, +infinity as the largest number of the type.
 template <typename E>
+__device__ __forceinline__ float largest() { return sizeof(E) == 4 ? FLT_MAX : __uint_as_float(0x7f7f0000u); }
+__device__ __forceinline__ float clean(float z, float most) { return fminf(fmaxf(z, -INFINITY), most); }
+
+// 16 bytes of a row, entries outside [begin, end) -infinity.
+template <typename E>
+__device__ __forceinline__ uint4 load_group(const E* row, int v, int begin, int end) {
+    constexpr int n = 16 / sizeof(E);
+    if (v >= begin && v + n <= end) return __ldg(reinterpret_cast<const uint4*>(row + v));
+    uint32_t w[4];
+    if constexpr (sizeof(E) == 4) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) w[i] = v + i >= begin && v + i < end ? __ldg(reinterpret_cast<const uint32_t*>(row) + v + i) : 0xff800000u;
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            uint32_t h[2];
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const int k = v + 2 * i + j;
+                h[j] = k >= begin && k < end ? static_cast<uint32_t>(__ldg(reinterpret_cast<const uint16_t*>(row) + k)) : 0xff80u;
+            }
+            w[i] = h[0] | (h[1] << 16);
+        }
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// A CTA's slice of a row: groups of 16 bytes on 16-byte boundaries, entries outside the slice -infinity.  Warp w has the
+// groups [w per, (w + 1) per), its lanes one after the other: warps, steps and lanes follow the indices, and a thread
+// reads only what it wrote itself.  kStaged: the slice lies in shared memory, read from global memory once.  Else every
+// pass reads it from there, the first into L2.
+template <typename E, bool kStaged>
 struct Slice {
     static constexpr int kGroup = 16 / sizeof(E);
     uint4* data;
+    const E* row;
+    float most;                                // values are cut to it: the type's largest, once it is known the row's
     int first;                                 // index of the first entry of group 0 (may lie before the slice)
     int begin, end;                            // indices of the slice
     int g0, g1;                                // groups of this warp
@@ -327,11 +359,52 @@ struct Slice {
     }
     __device__ __forceinline__ int steps() const { return (g1 - g0 + 31) / 32; }
     __device__ __forceinline__ int group_index(int g) const { return first + g * kGroup; }
+    __device__ __forceinline__ uint4 raw(int g) const {
+        if constexpr (kStaged) return data[g];
+        else return load_group<E>(row, group_index(g), begin, end);
+    }
+    __device__ __forceinline__ void values(const uint4& r, float (&x)[kGroup]) const {
+        unpack(r, x);
+        if constexpr (!kStaged) {
+#pragma unroll
+            for (int i = 0; i < kGroup; ++i) x[i] = clean(x[i], most);
+        }
+    }
+    // The first pass: the largest entry of this thread's.
+    __device__ __forceinline__ float take_in() const {
+        constexpr int kLoads = kStaged ? 8 : 4;              // (of 64 and of 32 registers)
+        float top = -INFINITY;
+        for (int g = g0 + lane; g < g1; g += 32 * kLoads) {
+            uint4 r[kLoads];
+#pragma unroll
+            for (int i = 0; i < kLoads; ++i)
+                if (g + 32 * i < g1) r[i] = load_group<E>(row, group_index(g + 32 * i), begin, end);
+#pragma unroll
+            for (int i = 0; i < kLoads; ++i)
+                if (g + 32 * i < g1) {
+                    float x[kGroup];
+                    unpack(r[i], x);
+                    if constexpr (kStaged) {
+                        uint32_t w[4];
+#pragma unroll
+                        for (int e = 0; e < kGroup; ++e) x[e] = clean(x[e], most);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            w[e] = sizeof(E) == 4 ? __float_as_uint(x[e % kGroup])
+                                                  : (__float_as_uint(x[(2 * e) % kGroup]) >> 16) | __float_as_uint(x[(2 * e + 1) % kGroup]);
+                        data[g + 32 * i] = make_uint4(w[0], w[1], w[2], w[3]);
+                    }
+#pragma unroll
+                    for (int e = 0; e < kGroup; ++e) top = fmaxf(top, x[e]);
+                }
+        }
+        return fminf(top, most);
+    }
     // entries of this lane's group of a step; -infinity past the warp's groups
     __device__ __forceinline__ int read(int step, float (&x)[kGroup]) const {
         const int g = g0 + step * 32 + lane;
         if (g < g1) {
-            unpack(data[g], x);
+            values(raw(g), x);
         } else {
 #pragma unroll
             for (int i = 0; i < kGroup; ++i) x[i] = -INFINITY;
@@ -341,52 +414,24 @@ struct Slice {
     // f(z, index) for every entry of this thread
     template <typename F>
     __device__ __forceinline__ void each(F f) const {
-        for (int g = g0 + lane; g < g1; g += 32) {
-            float x[kGroup];
-            unpack(data[g], x);
-            const int v = group_index(g);
+        constexpr int kLoads = kStaged ? 1 : 4;
+        for (int g = g0 + lane; g < g1; g += 32 * kLoads) {
+            uint4 r[kLoads];
 #pragma unroll
-            for (int i = 0; i < kGroup; ++i) f(x[i], v + i);
+            for (int j = 0; j < kLoads; ++j)
+                if (g + 32 * j < g1) r[j] = raw(g + 32 * j);
+#pragma unroll
+            for (int j = 0; j < kLoads; ++j)
+                if (g + 32 * j < g1) {
+                    float x[kGroup];
+                    values(r[j], x);
+                    const int v = group_index(g + 32 * j);
+#pragma unroll
+                    for (int i = 0; i < kGroup; ++i) f(x[i], v + i);
+                }
         }
     }
 };
-
-// From global memory: NaN counts as -infinity, +infinity as the largest number of the type.
-template <typename E>
-__device__ __forceinline__ uint32_t clean(uint32_t w) {
-    if constexpr (sizeof(E) == 4) {
-        return __float_as_uint(fminf(fmaxf(__uint_as_float(w), -INFINITY), FLT_MAX));
-    } else {
-        const float lo = fminf(fmaxf(bf16_lo(w), -INFINITY), __uint_as_float(0x7f7f0000u));
-        const float hi = fminf(fmaxf(bf16_hi(w), -INFINITY), __uint_as_float(0x7f7f0000u));
-        return (__float_as_uint(lo) >> 16) | __float_as_uint(hi);
-    }
-}
-
-template <typename E>
-__device__ __forceinline__ uint4 load_group(const E* row, int v, int begin, int end) {
-    constexpr int n = 16 / sizeof(E);
-    uint32_t w[4];
-    if (v >= begin && v + n <= end) {
-        const uint4 r = __ldg(reinterpret_cast<const uint4*>(row + v));
-        w[0] = r.x; w[1] = r.y; w[2] = r.z; w[3] = r.w;
-    } else if constexpr (sizeof(E) == 4) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) w[i] = v + i >= begin && v + i < end ? __ldg(reinterpret_cast<const uint32_t*>(row) + v + i) : 0xff800000u;
-    } else {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            uint32_t h[2];
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                const int k = v + 2 * i + j;
-                h[j] = k >= begin && k < end ? static_cast<uint32_t>(__ldg(reinterpret_cast<const uint16_t*>(row) + k)) : 0xff80u;
-            }
-            w[i] = h[0] | (h[1] << 16);
-        }
-    }
-    return make_uint4(clean<E>(w[0]), clean<E>(w[1]), clean<E>(w[2]), clean<E>(w[3]));
-}
 
 // ---------------------------------------------------------------- the first CTA's list
 
@@ -502,8 +547,8 @@ __device__ __noinline__ uint64_t select(SampleShared<NT>& s, int n, uint64_t lea
 
 // ---------------------------------------------------------------- kernel
 
-template <typename E, int NT>
-__global__ void __launch_bounds__(NT, 1024 / NT) sample_tokens_kernel(const SampleArgs a) {
+template <typename E, int NT, bool kStaged>
+__global__ void __launch_bounds__(NT, (kStaged ? 1024 : 2048) / NT) sample_tokens_kernel(const SampleArgs a) {
     extern __shared__ __align__(16) unsigned char smem[];
     SampleShared<NT>& s = *reinterpret_cast<SampleShared<NT>*>(smem);
     constexpr int kGroup = 16 / sizeof(E), kWarps = NT / 32, kEntries = kList / NT;
@@ -526,33 +571,20 @@ __global__ void __launch_bounds__(NT, 1024 / NT) sample_tokens_kernel(const Samp
 
     // ---- the slice
     const E* logits = static_cast<const E*>(a.logits) + static_cast<int64_t>(row) * a.ld;
-    Slice<E> sl;
+    Slice<E, kStaged> sl;
     sl.begin = min(a.V, static_cast<int>(rank) * a.slice);
     sl.end = min(a.V, sl.begin + a.slice);
     const int shift_in = static_cast<int>((reinterpret_cast<uintptr_t>(logits + sl.begin) & 15u) / sizeof(E));
     sl.first = sl.begin - shift_in;
     sl.data = reinterpret_cast<uint4*>(smem + sizeof(SampleShared<NT>));
+    sl.row = logits;
+    sl.most = largest<E>();
     sl.lane = lane;
     const int groups = sl.end > sl.begin ? (sl.end - sl.first + kGroup - 1) / kGroup : 0;
     const int per = (groups + kWarps - 1) / kWarps;
     sl.g0 = min(groups, warp * per);
     sl.g1 = min(groups, sl.g0 + per);
-    float top_own = -INFINITY;
-    for (int g = sl.g0 + lane; g < sl.g1; g += 32 * 8) {
-        uint4 r[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-            if (g + 32 * i < sl.g1) r[i] = load_group<E>(logits, sl.group_index(g + 32 * i), sl.begin, sl.end);
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-            if (g + 32 * i < sl.g1) {
-                sl.data[g + 32 * i] = r[i];
-                float x[kGroup];
-                Slice<E>::unpack(r[i], x);
-#pragma unroll
-                for (int e = 0; e < kGroup; ++e) top_own = fmaxf(top_own, x[e]);
-            }
-    }
+    const float top_own = sl.take_in();
     for (int i = tid; i < (1 << kPowBits) / 4; i += NT)
         reinterpret_cast<uint4*>(s.pow)[i] = __ldg(reinterpret_cast<const uint4*>(kPow.coarse) + i);
     if (tid == 0) {
@@ -583,6 +615,7 @@ __global__ void __launch_bounds__(NT, 1024 / NT) sample_tokens_kernel(const Samp
     float top = -INFINITY;
     for (int c = 0; c < C; ++c) top = fmaxf(top, s.cta_max[c]);
     const Scale sc = make_scale(top, s.rh, s.rl);
+    sl.most = top;
 
     float* probs = a.probs != nullptr ? a.probs + static_cast<int64_t>(row) * a.ld_probs : nullptr;
     auto clear_probs = [&]() {
@@ -1030,7 +1063,7 @@ __global__ void __launch_bounds__(NT, 1024 / NT) sample_tokens_kernel(const Samp
         const float2 inv = inverse_of(sum);
         for (int g = sl.g0 + lane; g < sl.g1; g += 32) {
             float x[kGroup];
-            Slice<E>::unpack(sl.data[g], x);
+            sl.values(sl.raw(g), x);
             const int v = sl.group_index(g);
 #pragma unroll
             for (int i = 0; i < kGroup; ++i)
@@ -1069,12 +1102,19 @@ extern "C" dsa_status dsa_sample_tokens(const void* logits, int64_t ld, int32_t 
     const int slice = ((V + ctas - 1) / ctas + 7) / 8 * 8;
     const size_t bytes = (static_cast<size_t>(slice) * align + 15) / 16 * 16 + 16;
     const bool large = bytes > 40 * 1024;
-    const size_t smem = bytes + (large ? sizeof(SampleShared<512>) : sizeof(SampleShared<256>));
+    // Staged unless most of the work is rows with a top-k, read twice, and there are enough of them to fill the GPU several
+    // times: then more CTAs an SM count for more (256 rows of 131072 with k = 50 and probabilities 134 -> 100 us; 64 rows of
+    // mixed settings 53 -> 63, 300 with top-p alone 268 -> 361)
+    const bool staged = top_k == nullptr || static_cast<int64_t>(R) * ctas <= 4 * static_cast<int64_t>(device_sm_count());
+    const size_t smem = (staged ? bytes : 0) + (large ? sizeof(SampleShared<512>) : sizeof(SampleShared<256>));
     SampleArgs a{logits, ld, V, temperature, top_k, top_p, min_p, u, tokens, probs, ld_probs, ctas, slice, dev_err};
-    const void* kernel = bf16 ? (large ? reinterpret_cast<const void*>(&sample_tokens_kernel<uint16_t, 512>)
-                                       : reinterpret_cast<const void*>(&sample_tokens_kernel<uint16_t, 256>))
-                              : (large ? reinterpret_cast<const void*>(&sample_tokens_kernel<float, 512>)
-                                       : reinterpret_cast<const void*>(&sample_tokens_kernel<float, 256>));
+    using Kernel = void (*)(SampleArgs);
+    static const Kernel kernels[2][2][2] = {
+        {{sample_tokens_kernel<float, 256, false>, sample_tokens_kernel<float, 256, true>},
+         {sample_tokens_kernel<float, 512, false>, sample_tokens_kernel<float, 512, true>}},
+        {{sample_tokens_kernel<uint16_t, 256, false>, sample_tokens_kernel<uint16_t, 256, true>},
+         {sample_tokens_kernel<uint16_t, 512, false>, sample_tokens_kernel<uint16_t, 512, true>}}};
+    const void* kernel = reinterpret_cast<const void*>(kernels[bf16][large][staged]);
     if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)) != cudaSuccess)
         return DSA_ERR_CUDA;
     cudaLaunchConfig_t cfg = {};
