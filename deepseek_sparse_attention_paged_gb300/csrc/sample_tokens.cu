@@ -18,11 +18,13 @@
 //     entries pass (with G threads about -G ln(1 - k / G)); those go to the first CTA, which does the rest alone.
 //   * top-p without top-k: masses of 1024 bins of z (32 an octave of w) find the bin of the border; its entries
 //     go to the first CTA, which finds the last one kept.  A second pass sums what is kept.
+//     For bf16 the values themselves are the bins, and counts take the place of masses.
 //   * where more entries than fit (2048) come together (ties, a temperature far above 1), or for a larger top-k:
 //     bisection over the 32 bits of z, a pass over the slices each.
 #include <float.h>
 
 #include <algorithm>
+#include <cstddef>
 
 #include "dsa_common.cuh"
 #include "sm100_ptx.cuh"
@@ -37,6 +39,8 @@ constexpr int kFew = 128;                      // entries that are compared with
 constexpr int kMaxTopK = 1024;
 constexpr int kBins = 1024, kBinsPerOctave = 32;
 constexpr int kSelectBins = 256;
+// bf16 numbers from 2^-9 up to 2^7, of both signs, each a bin: 16 octaves of 128; in the middle one for all smaller ones
+constexpr int kSide = 16 * 128, kValueBins = 2 * kSide + 1, kFirstBits = (127 - 9) << 7;
 constexpr int kOne = 46;                       // fraction bits of a weight
 constexpr int kMaxSampleVocab = 1 << 18;       // sums of weights stay below 2^64
 constexpr int kPowBits = 10;
@@ -113,7 +117,7 @@ struct alignas(16) SampleShared {
     uint64_t warp_sum[2][NT / 32];
     uint32_t warp_lo[NT / 32], warp_hi[NT / 32];
     float warp_max[NT / 32];
-    uint32_t stage_count;
+    uint32_t stage_count, quota;
     int found;
     double t_ln_min;                           // temperature ln min_p
     float rh, rl, zmin;
@@ -144,6 +148,12 @@ __device__ __forceinline__ void put(void* p, uint32_t rank, uint32_t v) {
 __device__ __forceinline__ void put(void* p, uint32_t rank, uint64_t v) {
     asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(remote(p, rank)), "l"(v) : "memory");
 }
+__device__ __forceinline__ uint32_t get(const void* p, uint32_t rank) {
+    uint32_t v;
+    asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(remote(p, rank)) : "memory");
+    return v;
+}
+__device__ __forceinline__ uint64_t wide(uint2 h) { return (static_cast<uint64_t>(h.y) << 32) | h.x; }
 __device__ __forceinline__ uint2 get2(const void* p, uint32_t rank) {
     uint2 v;
     asm volatile("ld.shared::cluster.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(remote(p, rank)) : "memory");
@@ -304,6 +314,11 @@ struct Cut {
 template <typename E>
 __device__ __forceinline__ float largest() { return sizeof(E) == 4 ? FLT_MAX : __uint_as_float(0x7f7f0000u); }
 __device__ __forceinline__ float clean(float z, float most) { return fminf(fmaxf(z, -INFINITY), most); }
+
+__device__ __forceinline__ float bin_value(int bin) {
+    const uint32_t bits = bin > kSide ? kFirstBits + (bin - kSide - 1) : 0x8000u | (kFirstBits + (kSide - 1 - bin));
+    return __uint_as_float(bits << 16);
+}
 
 // 16 bytes of a row, entries outside [begin, end) -infinity.
 template <typename E>
@@ -948,8 +963,145 @@ __global__ void __launch_bounds__(NT, (kStaged ? 1024 : 2048) / NT) sample_token
     };
 
     Cut cut{-INFINITY, -1};
+    bool counted = false;                        // the border is found and `mine` the mass kept, by counts of values
+    uint64_t mine = 0;
+    if constexpr (sizeof(E) == 2 && kStaged) {
+        // ---- top-p alone, bf16: few distinct values, so their numbers say all.  A count is one addition in shared memory where a
+        // mass is 30 operations and two of them; each weight is formed once a value, and once the border is known
+        // the counts give the mass that a CTA keeps.  (300 rows of 100003: 258 -> MEASURED us)
+        if (use_p && !use_k && C == kMaxCtas && !sc.wide && sc.top < 128.0f) {
+            static_assert(sizeof(s.maxima) + sizeof(s.list) >= kValueBins * sizeof(uint32_t) && offsetof(SampleShared<NT>, list) == sizeof(s.maxima), "counts");
+            uint32_t* counts = reinterpret_cast<uint32_t*>(&s);              // over maxima and list
+            uint2* odd = s.sel_mass;                                         // masses of the numbers below 2^-9, and of those down from -2^7
+            __syncthreads();
+            for (int i = tid; i < kValueBins; i += NT) counts[i] = 0;
+            if (tid < 2) odd[tid] = make_uint2(0u, 0u);
+            __syncthreads();
+            for (int g = sl.g0 + lane; g < sl.g1; g += 32) {
+                const uint4 r = sl.data[g];
+                const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const uint32_t h = (i & 1) != 0 ? w[i >> 1] >> 16 : w[i >> 1] & 0xffffu;
+                    const uint32_t at = (h & 0x7fffu) - kFirstBits;
+                    if (at < static_cast<uint32_t>(kSide)) {
+                        const int d = static_cast<int>(at) + 1;
+                        atomicAdd(&counts[(h & 0x8000u) != 0u ? kSide - d : kSide + d], 1u);
+                    } else if (h != 0xff80u) {
+                        const uint64_t m = weight(__uint_as_float(h << 16), sc, s.pow);
+                        if (m != 0) add_wide(&odd[(h & 0x7fffu) < static_cast<uint32_t>(kFirstBits) ? 0 : 1], m);
+                    }
+                }
+            }
+            cluster_sync();
+            // this CTA's share of the bins, the largest values first, three a thread: masses over the cluster
+            constexpr int kShare = (kValueBins + kMaxCtas - 1) / kMaxCtas;
+            static_assert(3 * NT >= kShare, "bins a thread");
+            auto bin_at = [&](int i) {                                       // -1: none
+                const int d = static_cast<int>(rank) * kShare + tid * 3 + i;
+                return tid * 3 + i < kShare && d < kValueBins ? kValueBins - 1 - d : -1;
+            };
+            uint64_t own[3];
+#pragma unroll
+            for (int i = 0; i < 3; ++i) {
+                const int bin = bin_at(i);
+                own[i] = 0;
+                if (bin >= 0) {
+                    if (bin != kSide) {
+                        uint32_t n = 0;
+                        for (int c = 0; c < kMaxCtas; ++c) n += get(&counts[bin], c);
+                        own[i] = n == 0 ? 0 : n * weight(bin_value(bin), sc, s.pow);
+                    } else {
+                        for (int c = 0; c < kMaxCtas; ++c) own[i] += wide(get2(&odd[0], c));
+                    }
+                }
+                mine += own[i];
+            }
+            uint64_t rest = 0;                                               // behind all bins: what lies below -2^7
+            if (rank == kMaxCtas - 1 && tid == NT - 1)
+                for (int c = 0; c < kMaxCtas; ++c) rest += wide(get2(&odd[1], c));
+            const int now = flip;
+            const uint64_t mass = cluster_sum(mine + rest);
+            uint64_t before = 0;
+            for (int c = 0; c < static_cast<int>(rank); ++c) before += s.cta_sum[now][c];
+            for (int w = 0; w < warp; ++w) before += s.warp_sum[now][w];
+            before += warp_scan64(mine + rest, lane) - (mine + rest);
+            const uint64_t limit = max(scaled(p_in, mass, true), uint64_t(1));
+            // the value of the border, and how many of the entries that are equal to it each CTA keeps (in all bins but the
+            // two that hold several values)
+            if (rest != 0 && before + mine < limit)
+                for (int c = 0; c < kMaxCtas; ++c) put(&s.bin, c, 0xffffffffu);
+#pragma unroll
+            for (int i = 0; i < 3; ++i) {
+                if (own[i] != 0 && before < limit && before + own[i] >= limit) {
+                    const int bin = bin_at(i);
+                    uint64_t left = 0;
+                    if (bin != kSide) {
+                        const uint64_t w = weight(bin_value(bin), sc, s.pow);
+                        left = (limit - before + w - 1) / w;
+                    }
+                    for (int c = 0; c < kMaxCtas; ++c) {
+                        const uint32_t n = bin != kSide ? get(&counts[bin], c) : 0;
+                        const uint32_t q = static_cast<uint32_t>(min(static_cast<uint64_t>(n), left));
+                        left -= q;
+                        put(&s.quota, c, q);
+                        put(&s.bin, c, bin != kSide ? static_cast<uint32_t>(bin) : 0xffffffffu);
+                    }
+                }
+                before += own[i];
+            }
+            cluster_sync();
+            const int border = s.bin;
+            const float z_cut = border >= 0 ? fmaxf(bin_value(border), zmin) : 0.0f;
+            counted = fabsf(z_cut) >= 0x1p-9f;                               // else among the small numbers: by masses, below
+            if (counted) {
+                cut = Cut{z_cut, 0x7fffffff};
+                const uint32_t ties = counts[border], quota = s.quota;
+                if (z_cut > bin_value(border)) {
+                    // min-p keeps less: all that are not below it
+                } else if (quota < ties) {
+                    cut.index = -1;
+                    if (quota > 0) {                                         // the last one kept, in the order of the indices
+                        uint64_t n = 0;
+                        sl.each([&](float z, int) { n += z == z_cut ? 1 : 0; });
+                        const uint64_t in_warp = warp_sum64(n);
+                        block_sum64(s, n, flip);
+                        uint64_t seen = 0;
+                        for (int w = 0; w < warp; ++w) seen += s.warp_sum[flip][w];
+                        if (seen < quota && seen + in_warp >= quota) {
+                            for (int st = 0; st < sl.steps(); ++st) {
+                                float x[kGroup];
+                                const int v = sl.read(st, x);
+                                uint32_t here = 0;
+#pragma unroll
+                                for (int i = 0; i < kGroup; ++i) here += x[i] == z_cut ? 1u : 0u;
+                                uint64_t at = seen + warp_scan64(here, lane) - here;
+#pragma unroll
+                                for (int i = 0; i < kGroup; ++i)
+                                    if (x[i] == z_cut && ++at == quota) s.cut_index = v + i;
+                                seen += __reduce_add_sync(0xffffffffu, here);
+                            }
+                        }
+                        __syncthreads();
+                        cut.index = s.cut_index;
+                    }
+                }
+                mine = 0;
+                for (int b = tid; b < kValueBins; b += NT) {
+                    if (b == kSide) {
+                        if (z_cut < 0.0f) mine += wide(odd[0]);
+                        continue;
+                    }
+                    const float z = bin_value(b);
+                    const uint32_t n = z > z_cut || (z == z_cut && cut.index == 0x7fffffff) ? counts[b] : (z == z_cut ? quota : 0);
+                    if (n != 0) mine += n * weight(z, sc, s.pow);
+                }
+                // no CTA reads the counts of another any more, and this one's lie where lists do
+            }
+        }
+    }
     if (use_k) cut = narrow(cut, false, static_cast<uint64_t>(k_in));
-    if (use_p) {
+    if (use_p && !counted) {
         // ---- masses of bins of z, largest first
         __syncthreads();
         for (int i = tid; i < kBins; i += NT) s.hist[i] = make_uint2(0u, 0u);
@@ -965,7 +1117,7 @@ __global__ void __launch_bounds__(NT, (kStaged ? 1024 : 2048) / NT) sample_token
         // this CTA's share of the bins: sums over the cluster, then the mass of the share to every CTA
         const int share = kBins / C, b0 = static_cast<int>(rank) * share;      // C is a power of two
         uint64_t own[kBins / NT];
-        uint64_t mine = 0;
+        mine = 0;
         const int each = (share + NT - 1) / NT;
 #pragma unroll
         for (int i = 0; i < kBins / NT; ++i) {
@@ -1020,17 +1172,29 @@ __global__ void __launch_bounds__(NT, (kStaged ? 1024 : 2048) / NT) sample_token
     if (zmin > cut.z) cut = Cut{zmin, 0x7fffffff};
 
     // ---- the sum of what is kept, by warps; the warp with the border looks again
-    uint64_t mine = 0;
-    sl.each([&](float z, int v) {
-        if (cut.keeps(z, v)) mine += weight(z, sc, s.pow);
-    });
-    const uint64_t in_warp = warp_sum64(mine);
-    const int now = flip;
+    auto sum_up = [&]() {
+        mine = 0;
+        sl.each([&](float z, int v) {
+            if (cut.keeps(z, v)) mine += weight(z, sc, s.pow);
+        });
+    };
+    if (!counted) sum_up();
+    int now = flip;
     __syncthreads();
     const uint64_t sum = cluster_sum(mine);
     const uint64_t target = min(scaled(u, sum, false), sum - 1);       // u of 1 or more: the last one kept
     uint64_t before = 0;
     for (int c = 0; c < static_cast<int>(rank); ++c) before += s.cta_sum[now][c];
+    if (counted) {                                                     // only the CTA with the border needs its warps' sums
+        if (before <= target && target < before + s.cta_sum[now][rank]) {
+            sum_up();
+            now = flip;
+            block_sum64(s, mine, now);
+        } else {
+            mine = 0;
+        }
+    }
+    const uint64_t in_warp = warp_sum64(mine);
     for (int w = 0; w < warp; ++w) before += s.warp_sum[now][w];
     if (before <= target && target < before + in_warp) {
         bool done = false;

@@ -478,6 +478,42 @@ def test_sample_masked_rows():
     assert got == [2000, 3, 2500] and err == 0 and p[0, 100] == 0.5 and p[1, 3] == 1.0 and np.all(p[2] == np.float32(1 / V))
 
 
+@pytest.mark.parametrize("kind", ["whole", "halves", "tiny", "low", "high", "mixed", "one", "two"])
+def test_sample_bf16_values(kind):
+    """bf16 rows with top-p: many equal values (borders within them, in any part of the row), numbers next to 0, far below
+    it and past 128, few values."""
+    R, V = 8, 20003
+    g = torch.Generator().manual_seed(len(kind))
+    x = 2.0 * torch.randn(R, V, generator=g)
+    if kind == "whole":
+        x = x.round()
+    elif kind == "halves":
+        x = (2 * x).round() / 2 - 6.0
+    elif kind == "tiny":
+        x = x * 1e-4
+        x[:, 5000:5003] = 1.0
+    elif kind == "low":
+        x = 8 * x - 130.0
+    elif kind == "high":
+        x = x + 128.0
+    elif kind == "mixed":
+        x[:, ::2] = x[:, ::2] * 1e-3
+        x[:, 1::7] = -500.0
+    elif kind == "one":
+        x[:] = 3.0
+    elif kind == "two":
+        x[:] = -1.0
+        x[:, 11::3] = 2.0
+    x = x.to(torch.bfloat16)
+    u = torch.rand(R, generator=g).tolist()
+    p = [0.5, 0.9, 0.99, 0.3, 0.75, 0.999, 0.21, 0.95]
+    t = [1.0, 0.7, 1.5, 1.0, 3.0, 20.0, 0.1, 1.0]
+    _check_sample(x, V, u, top_p=p)
+    _check_sample(x, V, u, top_p=p, temperature=t)
+    _check_sample(x, V, u, top_p=p, min_p=[0.0, 0.1, 0.5, 0.9, 1.0, 0.3, 0.01, 0.6])
+    _check_sample(x[:, 1:], V - 1, u, top_p=p, probs=False)
+
+
 def test_sample_random_numbers_at_the_ends():
     """u = 0: the first kept entry with weight; u of 1 or more, infinite: the last; negative, NaN: as 0."""
     x = torch.tensor([[-200.0, 1.0, 1.0, 1.0, 3.0, 1.0, -200.0]] * 7)
