@@ -426,9 +426,9 @@ struct Slice {
         }
         return group_index(g);
     }
-    // f(z, index) for every entry of this thread
+    // f(group, its index) for every group of this thread, as it lies in memory
     template <typename F>
-    __device__ __forceinline__ void each(F f) const {
+    __device__ __forceinline__ void each_group(F f) const {
         constexpr int kLoads = kStaged ? 1 : 4;
         for (int g = g0 + lane; g < g1; g += 32 * kLoads) {
             uint4 r[kLoads];
@@ -437,14 +437,18 @@ struct Slice {
                 if (g + 32 * j < g1) r[j] = raw(g + 32 * j);
 #pragma unroll
             for (int j = 0; j < kLoads; ++j)
-                if (g + 32 * j < g1) {
-                    float x[kGroup];
-                    values(r[j], x);
-                    const int v = group_index(g + 32 * j);
-#pragma unroll
-                    for (int i = 0; i < kGroup; ++i) f(x[i], v + i);
-                }
+                if (g + 32 * j < g1) f(r[j], group_index(g + 32 * j));
         }
+    }
+    // f(z, index) for every entry of this thread
+    template <typename F>
+    __device__ __forceinline__ void each(F f) const {
+        each_group([&](const uint4& r, int v) {
+            float x[kGroup];
+            values(r, x);
+#pragma unroll
+            for (int i = 0; i < kGroup; ++i) f(x[i], v + i);
+        });
     }
 };
 
@@ -965,11 +969,12 @@ __global__ void __launch_bounds__(NT, (kStaged ? 1024 : 2048) / NT) sample_token
     Cut cut{-INFINITY, -1};
     bool counted = false;                        // the border is found and `mine` the mass kept, by counts of values
     uint64_t mine = 0;
-    if constexpr (sizeof(E) == 2 && kStaged) {
+    if constexpr (sizeof(E) == 2) {
         // ---- top-p alone, bf16: few distinct values, so their numbers say all.  A count is one addition in shared memory where a
         // mass is 30 operations and two of them; each weight is formed once a value, and once the border is known
-        // the counts give the mass that a CTA keeps.  (300 rows of 100003: 258 -> MEASURED us)
-        if (use_p && !use_k && C == kMaxCtas && !sc.wide && sc.top < 128.0f) {
+        // the counts give the mass that a CTA keeps.  (300 rows of 100003: 258 -> 165 us)
+        const int share = (kValueBins + C - 1) / C;                          // of the bins
+        if (use_p && !use_k && share <= 3 * NT && !sc.wide && sc.top < 128.0f) {
             static_assert(sizeof(s.maxima) + sizeof(s.list) >= kValueBins * sizeof(uint32_t) && offsetof(SampleShared<NT>, list) == sizeof(s.maxima), "counts");
             uint32_t* counts = reinterpret_cast<uint32_t*>(&s);              // over maxima and list
             uint2* odd = s.sel_mass;                                         // masses of the numbers below 2^-9, and of those down from -2^7
@@ -977,29 +982,26 @@ __global__ void __launch_bounds__(NT, (kStaged ? 1024 : 2048) / NT) sample_token
             for (int i = tid; i < kValueBins; i += NT) counts[i] = 0;
             if (tid < 2) odd[tid] = make_uint2(0u, 0u);
             __syncthreads();
-            for (int g = sl.g0 + lane; g < sl.g1; g += 32) {
-                const uint4 r = sl.data[g];
+            sl.each_group([&](const uint4& r, int) {
                 const uint32_t w[4] = {r.x, r.y, r.z, r.w};
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
                     const uint32_t h = (i & 1) != 0 ? w[i >> 1] >> 16 : w[i >> 1] & 0xffffu;
-                    const uint32_t at = (h & 0x7fffu) - kFirstBits;
+                    const uint32_t size = h & 0x7fffu, at = size - kFirstBits;
                     if (at < static_cast<uint32_t>(kSide)) {
                         const int d = static_cast<int>(at) + 1;
                         atomicAdd(&counts[(h & 0x8000u) != 0u ? kSide - d : kSide + d], 1u);
-                    } else if (h != 0xff80u) {
+                    } else if (size < 0x7f80u) {                             // (the row has no +infinity here)
                         const uint64_t m = weight(__uint_as_float(h << 16), sc, s.pow);
-                        if (m != 0) add_wide(&odd[(h & 0x7fffu) < static_cast<uint32_t>(kFirstBits) ? 0 : 1], m);
+                        if (m != 0) add_wide(&odd[size < static_cast<uint32_t>(kFirstBits) ? 0 : 1], m);
                     }
                 }
-            }
+            });
             cluster_sync();
             // this CTA's share of the bins, the largest values first, three a thread: masses over the cluster
-            constexpr int kShare = (kValueBins + kMaxCtas - 1) / kMaxCtas;
-            static_assert(3 * NT >= kShare, "bins a thread");
             auto bin_at = [&](int i) {                                       // -1: none
-                const int d = static_cast<int>(rank) * kShare + tid * 3 + i;
-                return tid * 3 + i < kShare && d < kValueBins ? kValueBins - 1 - d : -1;
+                const int d = static_cast<int>(rank) * share + tid * 3 + i;
+                return tid * 3 + i < share && d < kValueBins ? kValueBins - 1 - d : -1;
             };
             uint64_t own[3];
 #pragma unroll
@@ -1009,17 +1011,17 @@ __global__ void __launch_bounds__(NT, (kStaged ? 1024 : 2048) / NT) sample_token
                 if (bin >= 0) {
                     if (bin != kSide) {
                         uint32_t n = 0;
-                        for (int c = 0; c < kMaxCtas; ++c) n += get(&counts[bin], c);
+                        for (int c = 0; c < C; ++c) n += get(&counts[bin], c);
                         own[i] = n == 0 ? 0 : n * weight(bin_value(bin), sc, s.pow);
                     } else {
-                        for (int c = 0; c < kMaxCtas; ++c) own[i] += wide(get2(&odd[0], c));
+                        for (int c = 0; c < C; ++c) own[i] += wide(get2(&odd[0], c));
                     }
                 }
                 mine += own[i];
             }
             uint64_t rest = 0;                                               // behind all bins: what lies below -2^7
-            if (rank == kMaxCtas - 1 && tid == NT - 1)
-                for (int c = 0; c < kMaxCtas; ++c) rest += wide(get2(&odd[1], c));
+            if (static_cast<int>(rank) == C - 1 && tid == NT - 1)
+                for (int c = 0; c < C; ++c) rest += wide(get2(&odd[1], c));
             const int now = flip;
             const uint64_t mass = cluster_sum(mine + rest);
             uint64_t before = 0;
@@ -1030,7 +1032,7 @@ __global__ void __launch_bounds__(NT, (kStaged ? 1024 : 2048) / NT) sample_token
             // the value of the border, and how many of the entries that are equal to it each CTA keeps (in all bins but the
             // two that hold several values)
             if (rest != 0 && before + mine < limit)
-                for (int c = 0; c < kMaxCtas; ++c) put(&s.bin, c, 0xffffffffu);
+                for (int c = 0; c < C; ++c) put(&s.bin, c, 0xffffffffu);
 #pragma unroll
             for (int i = 0; i < 3; ++i) {
                 if (own[i] != 0 && before < limit && before + own[i] >= limit) {
@@ -1040,7 +1042,7 @@ __global__ void __launch_bounds__(NT, (kStaged ? 1024 : 2048) / NT) sample_token
                         const uint64_t w = weight(bin_value(bin), sc, s.pow);
                         left = (limit - before + w - 1) / w;
                     }
-                    for (int c = 0; c < kMaxCtas; ++c) {
+                    for (int c = 0; c < C; ++c) {
                         const uint32_t n = bin != kSide ? get(&counts[bin], c) : 0;
                         const uint32_t q = static_cast<uint32_t>(min(static_cast<uint64_t>(n), left));
                         left -= q;

@@ -123,6 +123,15 @@ __global__ void __launch_bounds__(kTabThreads) step_tables_kernel(const StepTabl
     const int have = static_cast<int>(min(static_cast<int64_t>(have0) + n_give, static_cast<int64_t>(s.num_pages)));
     if (static_cast<int64_t>(have0) + n_give > s.num_pages) bad |= DSA_DEVERR_INDEX_RANGE;
 
+    // The last request whose sum is at most x: it has x's row or page, as those behind with the same sum have none.
+    auto owner = [&](const uint32_t* before, uint32_t x) {
+        int lo = 0, hi = s.B - 1;
+        while (lo < hi) {
+            const int mid = (lo + hi + 1) >> 1;
+            if (before[mid] <= x) lo = mid; else hi = mid - 1;
+        }
+        return lo;
+    };
     // The page of this rank from the top; -1: the stack is empty, or the entry is no page.
     auto page_of = [&](uint32_t rank) {
         if (rank >= static_cast<uint32_t>(have)) {
@@ -135,12 +144,7 @@ __global__ void __launch_bounds__(kTabThreads) step_tables_kernel(const StepTabl
             page = s.free_pages[i];
         } else {                                 // given back in this call
             const uint32_t j = static_cast<uint32_t>(i - have0);
-            int lo = 0, hi = s.B - 1;
-            while (lo < hi) {
-                const int mid = (lo + hi + 1) >> 1;
-                if (given[mid] <= j) lo = mid; else hi = mid - 1;
-            }
-            const int c = mapped(s, lo);
+            const int lo = owner(given, j), c = mapped(s, lo);
             page = s.table[static_cast<int64_t>(lo) * s.max_pages + kept(s, lo, c) + (j - given[lo])];
         }
         if (page < 0 || page >= s.num_pages) {
@@ -155,11 +159,7 @@ __global__ void __launch_bounds__(kTabThreads) step_tables_kernel(const StepTabl
     for (int64_t r = static_cast<int64_t>(blockIdx.x) * kTabThreads + tid; r < s.T; r += static_cast<int64_t>(gridDim.x) * kTabThreads) {
         int64_t pos = 0, slot = -1;
         if (r < used) {
-            int lo = 0, hi = s.B - 1;            // the last request that begins at or before the row: it has rows
-            while (lo < hi) {
-                const int mid = (lo + hi + 1) >> 1;
-                if (cu[mid] <= static_cast<uint32_t>(r)) lo = mid; else hi = mid - 1;
-            }
+            const int lo = owner(cu, static_cast<uint32_t>(r));
             pos = static_cast<int64_t>(max(0, __ldg(s.cached + lo))) + (r - cu[lo]);
             const int64_t p = pos / kPage;
             const int c = mapped(s, lo);
@@ -180,20 +180,17 @@ __global__ void __launch_bounds__(kTabThreads) step_tables_kernel(const StepTabl
         s.positions[r] = pos;
         s.slots[r] = slot;
     }
-    // ---- pages, a request a warp
-    const int lane = tid & 31;
-    for (int b = blockIdx.x * kTabWarps + (tid >> 5); b < s.B; b += gridDim.x * kTabWarps) {
-        const int t = static_cast<int>(taken[b + 1] - taken[b]), g = static_cast<int>(given[b + 1] - given[b]);
-        if (t == 0 && g == 0) continue;
-        const int c = mapped(s, b);
-        int32_t* row = s.table + static_cast<int64_t>(b) * s.max_pages;
-#pragma unroll 4
-        for (int i = lane; i < t; i += 32) row[c + i] = page_of(taken[b] + i);
-        const int k = kept(s, b, c);
-        const int64_t top = static_cast<int64_t>(have0) + given[b];
-#pragma unroll 4
-        for (int i = lane; i < g; i += 32)
-            if (top + i < s.num_pages) s.free_pages[top + i] = row[k + i];
+    // ---- pages taken and given back, a page a thread (a warp a request would go over a long one's pages in turn: 40 of
+    // 500 requests that end with up to 1000 pages 8.5 -> 7.0 us)
+    const uint32_t first = blockIdx.x * kTabThreads + tid, stride = gridDim.x * kTabThreads;
+    for (uint32_t i = first; i < n_take; i += stride) {
+        const int b = owner(taken, i);
+        s.table[static_cast<int64_t>(b) * s.max_pages + mapped(s, b) + (i - taken[b])] = page_of(i);
+    }
+    for (uint32_t i = first; i < n_give; i += stride) {
+        const int b = owner(given, i), c = mapped(s, b);
+        const int64_t top = static_cast<int64_t>(have0) + i;
+        if (top < s.num_pages) s.free_pages[top] = s.table[static_cast<int64_t>(b) * s.max_pages + kept(s, b, c) + (i - given[b])];
     }
     // ---- lengths and counts, a request a thread
     for (int b = blockIdx.x * kTabThreads + tid; b < s.B; b += gridDim.x * kTabThreads) {
