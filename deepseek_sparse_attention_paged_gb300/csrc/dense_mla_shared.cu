@@ -19,7 +19,15 @@
 // whole in each SM (the plain call) the copies in flight (128 KB an SM) cover 2300 cycles of products, less than
 // they take, and a tile took 3300 cycles whether both pairs read the same tile (multicast) or not; halves cover twice that.
 //
-// MEASURED
+// A tile of a long prefix takes about 2800 cycles, 82 % of the nominal rate of its products, which is what the library's bf16
+// product reaches on this GPU (81 %); more stages, more buffers for P or two groups of softmax warps in turn change nothing.
+// Behind the prefix a tile costs the same for the few rows that see it.
+//
+// Measured (calls in a captured graph, one new token): 200 requests of 16 heads behind 131008 common keys 630 us (1.46
+// PFLOP/s of what is needed, 76 % of the measured rate; the plain call, by its rate at 8 x 128K x 2 rows, about 4.3 ms), 64 of 16
+// heads behind 32768 with 64 to 4096 of their own 107 us, 32 of 128 heads behind 16384 121 us, 60 of 32 heads with two
+// rows behind 5 prefixes of 2K to 32K 99 us, 4 of 16 heads behind 1024 24 us (a chain of about 20 steps).  144 of 152 SMs: clusters of
+// four do not fill a GPC whose SMs are no multiple of four.
 //
 // Roles (384 threads), warps 10 and 11 idle; "leader": the pair's even rank, whose MMA warp issues for both:
 //   score pair  warps 0-7  softmax: rows (tensor-memory lanes) 32 (w % 4) .. + 31, page w / 4 of the tile; queries
@@ -60,7 +68,8 @@ constexpr int kTmaWarp = 8, kMmaWarp = 9;
 constexpr int kThreads = 384;
 constexpr uint32_t kColS = 256;                                 // scores: score tiles, behind the query chunks
 constexpr int kMinShare = 2;
-constexpr int kUnitCost = 4;                                    // tiles that the change to another unit takes as long as,
+constexpr int kUnitCost = 8;                                    // tiles that the change to another unit takes as long as (0: b64 119 us,
+                                                                // 4: 107; b32 x 128 heads 4: 124, 8: 121, 12: 123),
 constexpr int kLongShare = 8;                                   // counted in shares of this many tiles or more
 constexpr int kAhead = 2;                                       // tiles between a page's prefetch and its copy
 constexpr int kMaxRequests = 16384, kMaxGroups = 8192, kMaxUnits = 16384;   // units of 256 rows
