@@ -14,8 +14,8 @@
 //
 // A row is split over the CTAs of a cluster, each with a slice of it in shared memory: logits are read from global
 // memory once.
-//   * top-k up to 1024: the k-th largest of all threads' maxima is a bound from below that few more than k
-//     entries pass (with G threads about -G ln(1 - k / G)); those go to the first CTA, which does the rest alone.
+//   * top-k up to 1024: the k-th largest of the maxima of all pairs of threads is a bound from below that few more than
+//     k entries pass (with G pairs about -G ln(1 - k / G)); those go to the first CTA, which does the rest alone.
 //   * top-p without top-k: masses of 1024 bins of z (32 an octave of w) find the bin of the border; its entries
 //     go to the first CTA, which finds the last one kept.  A second pass sums what is kept.
 //     For bf16 the values themselves are the bins, and counts take the place of masses.
@@ -88,10 +88,10 @@ struct SampleArgs {
 
 template <int NT>
 struct alignas(16) SampleShared {
-    static constexpr int kStage = kMaxCtas * NT / 2;
-    static_assert(kStage >= kBins && kStage >= 2 * kFew && kStage <= kList, "scratch");
+    static constexpr int kStage = kBins;
+    static_assert(kStage >= 2 * kFew && kStage <= kList, "scratch");
     union {
-        float maxima[kMaxCtas * NT];           // every thread's largest entry, of all CTAs
+        float maxima[kMaxCtas * NT / 2];       // every two threads' largest entry, of all CTAs
         uint2 hist[kBins];                     // masses (low and high word)
         uint64_t stage[kStage];                // entries of this CTA on their way to the first one
         struct {
@@ -586,7 +586,7 @@ __global__ void __launch_bounds__(NT, (kStaged ? 1024 : 2048) / NT) sample_token
     const float u = __ldg(a.u + row);
     const bool greedy = !(temperature > 0.0f);
     const bool use_k = k_in > 0 && k_in < a.V, use_p = p_in < 1.0f, use_m = m_in > 0.0f;
-    const bool by_list = use_k && k_in <= min(kMaxTopK, C * NT / 2);
+    const bool by_list = use_k && k_in <= min(kMaxTopK, C * NT / 4);
 
     // ---- the slice
     const E* logits = static_cast<const E*>(a.logits) + static_cast<int64_t>(row) * a.ld;
@@ -618,8 +618,11 @@ __global__ void __launch_bounds__(NT, (kStaged ? 1024 : 2048) / NT) sample_token
 
     // ---- the largest entry
     cluster_wait();
-    if (by_list && !greedy)
-        for (int c = 0; c < C; ++c) put(&s.maxima[rank * NT + tid], c, __float_as_uint(top_own));
+    if (by_list && !greedy) {
+        const float two = fmaxf(top_own, __shfl_xor_sync(0xffffffffu, top_own, 1));
+        if ((tid & 1) == 0)
+            for (int c = 0; c < C; ++c) put(&s.maxima[(rank * NT + tid) / 2], c, __float_as_uint(two));
+    }
     {
         const float m = warp_max(top_own);
         if (lane == 0) s.warp_max[warp] = m;
@@ -682,14 +685,25 @@ __global__ void __launch_bounds__(NT, (kStaged ? 1024 : 2048) / NT) sample_token
     // that is at most kList and no CTA has more than its stage holds (else kList + 1 is returned).  Each CTA has a region
     // of the list; where one does not suffice they are sent again, packed.  The area of maxima, bins and stage is free.
     bool packed = false;
-    auto collect = [&](auto pick) {
+    // The entries are `floor` or more, and `pick` takes them; whole groups below it are passed over.
+    auto collect = [&](float floor, auto pick) {
         __syncthreads();
-        sl.each([&](float z, int v) {
-            if (!pick(z, v)) return;
-            const uint32_t at = atomicAdd(&s.stage_count, 1u);
-            const uint64_t e = list_entry(z, v);
-            if (at < SampleShared<NT>::kStage) s.stage[at] = e;
-            if (at < kRegion) put(&s.list[rank * kRegion + at], 0u, e);
+        sl.each_group([&](const uint4& r, int v) {
+            float x[kGroup];
+            Slice<E, kStaged>::unpack(r, x);
+            float most = x[0];
+#pragma unroll
+            for (int i = 1; i < kGroup; ++i) most = fmaxf(most, x[i]);
+            if (!(most >= floor) || most == -INFINITY) return;
+#pragma unroll
+            for (int i = 0; i < kGroup; ++i) {
+                const float z = kStaged ? x[i] : clean(x[i], sl.most);
+                if (!(z >= floor) || z == -INFINITY || !pick(z, v + i)) continue;
+                const uint32_t at = atomicAdd(&s.stage_count, 1u);
+                const uint64_t e = list_entry(z, v + i);
+                if (at < SampleShared<NT>::kStage) s.stage[at] = e;
+                if (at < kRegion) put(&s.list[rank * kRegion + at], 0u, e);
+            }
         });
         __syncthreads();
         const uint32_t n = s.stage_count;
@@ -753,14 +767,15 @@ __global__ void __launch_bounds__(NT, (kStaged ? 1024 : 2048) / NT) sample_token
     };
 
     if (by_list) {
-        // ---- a bound that at least k entries reach: the k-th largest of the threads' maxima, or a little less, by 256
+        // ---- a bound that at least k entries reach: the k-th largest of the maxima, or a little less, by 256
         // bins of their range in turn
-        uint32_t key[kMaxCtas];
+        constexpr int kKeys = kMaxCtas / 2;
+        uint32_t key[kKeys];
         const uint32_t none = order_key(-INFINITY);
         uint32_t least = 0xffffffffu, finite = 0;
 #pragma unroll
-        for (int c = 0; c < kMaxCtas; ++c) {
-            key[c] = c < C ? order_key(s.maxima[c * NT + tid]) : none;
+        for (int c = 0; c < kKeys; ++c) {
+            key[c] = c * NT + tid < C * NT / 2 ? order_key(s.maxima[c * NT + tid]) : none;
             if (key[c] != none) {
                 least = min(least, key[c]);
                 ++finite;
@@ -786,7 +801,7 @@ __global__ void __launch_bounds__(NT, (kStaged ? 1024 : 2048) / NT) sample_token
             int shift = max(0, 32 - __clz(static_cast<int>(range)) - 8);
             for (;;) {
 #pragma unroll
-                for (int c = 0; c < kMaxCtas; ++c)
+                for (int c = 0; c < kKeys; ++c)
                     if (key[c] != none && key[c] - lo <= range) atomicAdd(&s.sel_count[(key[c] - lo) >> shift], 1u);
                 __syncthreads();
                 uint32_t m[8], own = 0;                      // every warp: 8 bins a lane, the largest first
@@ -828,7 +843,7 @@ __global__ void __launch_bounds__(NT, (kStaged ? 1024 : 2048) / NT) sample_token
             bound = key_value(lo);
         }
         clear_probs();
-        const uint32_t n_all = collect([&](float z, int) { return z >= bound && z > -INFINITY; });
+        const uint32_t n_all = collect(bound, [](float, int) { return true; });
         if (n_all <= kList) {
             if (rank != 0) return;
             const int n = static_cast<int>(n_all), k = min(k_in, n);
@@ -968,6 +983,7 @@ __global__ void __launch_bounds__(NT, (kStaged ? 1024 : 2048) / NT) sample_token
 
     Cut cut{-INFINITY, -1};
     bool counted = false;                        // the border is found and `mine` the mass kept, by counts of values
+    uint32_t kept_ties = 0;                      // of this CTA's entries at the border, where it lies among them
     uint64_t mine = 0;
     if constexpr (sizeof(E) == 2) {
         // ---- top-p alone, bf16: few distinct values, so their numbers say all.  A count is one addition in shared memory where a
@@ -975,8 +991,8 @@ __global__ void __launch_bounds__(NT, (kStaged ? 1024 : 2048) / NT) sample_token
         // the counts give the mass that a CTA keeps.  (300 rows of 100003: 258 -> 165 us)
         const int share = (kValueBins + C - 1) / C;                          // of the bins
         if (use_p && !use_k && share <= 3 * NT && !sc.wide && sc.top < 128.0f) {
-            static_assert(sizeof(s.maxima) + sizeof(s.list) >= kValueBins * sizeof(uint32_t) && offsetof(SampleShared<NT>, list) == sizeof(s.maxima), "counts");
-            uint32_t* counts = reinterpret_cast<uint32_t*>(&s);              // over maxima and list
+            static_assert(sizeof(s.stage) + sizeof(s.list) >= kValueBins * sizeof(uint32_t) && offsetof(SampleShared<NT>, list) == sizeof(s.stage), "counts");
+            uint32_t* counts = reinterpret_cast<uint32_t*>(&s);              // over stage and list
             uint2* odd = s.sel_mass;                                         // masses of the numbers below 2^-9, and of those down from -2^7
             __syncthreads();
             for (int i = tid; i < kValueBins; i += NT) counts[i] = 0;
@@ -1010,8 +1026,11 @@ __global__ void __launch_bounds__(NT, (kStaged ? 1024 : 2048) / NT) sample_token
                 own[i] = 0;
                 if (bin >= 0) {
                     if (bin != kSide) {
-                        uint32_t n = 0;
-                        for (int c = 0; c < C; ++c) n += get(&counts[bin], c);
+                        uint32_t each[kMaxCtas], n = 0;
+#pragma unroll
+                        for (int c = 0; c < kMaxCtas; ++c) each[c] = c < C ? get(&counts[bin], c) : 0;
+#pragma unroll
+                        for (int c = 0; c < kMaxCtas; ++c) n += each[c];
                         own[i] = n == 0 ? 0 : n * weight(bin_value(bin), sc, s.pow);
                     } else {
                         for (int c = 0; c < C; ++c) own[i] += wide(get2(&odd[0], c));
@@ -1063,31 +1082,8 @@ __global__ void __launch_bounds__(NT, (kStaged ? 1024 : 2048) / NT) sample_token
                     // min-p keeps less: all that are not below it
                 } else if (quota < ties) {
                     cut.index = -1;
-                    if (quota > 0) {                                         // the last one kept, in the order of the indices
-                        uint64_t n = 0;
-                        sl.each([&](float z, int) { n += z == z_cut ? 1 : 0; });
-                        const uint64_t in_warp = warp_sum64(n);
-                        block_sum64(s, n, flip);
-                        uint64_t seen = 0;
-                        for (int w = 0; w < warp; ++w) seen += s.warp_sum[flip][w];
-                        if (seen < quota && seen + in_warp >= quota) {
-                            for (int st = 0; st < sl.steps(); ++st) {
-                                float x[kGroup];
-                                const int v = sl.read(st, x);
-                                uint32_t here = 0;
-#pragma unroll
-                                for (int i = 0; i < kGroup; ++i) here += x[i] == z_cut ? 1u : 0u;
-                                uint64_t at = seen + warp_scan64(here, lane) - here;
-#pragma unroll
-                                for (int i = 0; i < kGroup; ++i)
-                                    if (x[i] == z_cut && ++at == quota) s.cut_index = v + i;
-                                seen += __reduce_add_sync(0xffffffffu, here);
-                            }
-                        }
-                        __syncthreads();
-                        cut.index = s.cut_index;
-                    }
                 }
+                kept_ties = z_cut > bin_value(border) || quota == ties ? 0 : quota;   // 0: all or none
                 mine = 0;
                 for (int b = tid; b < kValueBins; b += NT) {
                     if (b == kSide) {
@@ -1152,9 +1148,9 @@ __global__ void __launch_bounds__(NT, (kStaged ? 1024 : 2048) / NT) sample_token
         cluster_sync();
         const float bin = static_cast<float>(s.bin);
         const uint64_t bin_before = s.bin_before;
-        const uint32_t n = collect([&](float z, int v) {
+        const uint32_t n = collect(-INFINITY, [&](float z, int v) {
             const float b = place_of(z);
-            return b >= bin && b < bin + 1.0f && z > -INFINITY && cut.keeps(z, v);
+            return b >= bin && b < bin + 1.0f && cut.keeps(z, v);
         });
         if (n <= kList) {
             if (rank == 0) {
@@ -1188,9 +1184,35 @@ __global__ void __launch_bounds__(NT, (kStaged ? 1024 : 2048) / NT) sample_token
     uint64_t before = 0;
     for (int c = 0; c < static_cast<int>(rank); ++c) before += s.cta_sum[now][c];
     if (counted) {                                                     // only the CTA with the border needs its warps' sums
-        if (before <= target && target < before + s.cta_sum[now][rank]) {
+        const bool here = before <= target && target < before + s.cta_sum[now][rank];
+        if (kept_ties > 0 && (here || probs != nullptr)) {             // the last one kept, in the order of the indices
+            uint64_t n = 0;
+            sl.each([&](float z, int) { n += z == cut.z ? 1 : 0; });
+            const uint64_t in_warp = warp_sum64(n);
+            block_sum64(s, n, flip);
+            uint64_t seen = 0;
+            for (int w = 0; w < warp; ++w) seen += s.warp_sum[flip][w];
+            if (seen < kept_ties && seen + in_warp >= kept_ties) {
+                for (int st = 0; st < sl.steps(); ++st) {
+                    float x[kGroup];
+                    const int v = sl.read(st, x);
+                    uint32_t own = 0;
+#pragma unroll
+                    for (int i = 0; i < kGroup; ++i) own += x[i] == cut.z ? 1u : 0u;
+                    uint64_t at = seen + warp_scan64(own, lane) - own;
+#pragma unroll
+                    for (int i = 0; i < kGroup; ++i)
+                        if (x[i] == cut.z && ++at == kept_ties) s.cut_index = v + i;
+                    seen += __reduce_add_sync(0xffffffffu, own);
+                }
+            }
+            __syncthreads();
+            cut.index = s.cut_index;
+        }
+        if (here) {
             sum_up();
             now = flip;
+            __syncthreads();
             block_sum64(s, mine, now);
         } else {
             mine = 0;
@@ -1237,8 +1259,7 @@ __global__ void __launch_bounds__(NT, (kStaged ? 1024 : 2048) / NT) sample_token
                     probs[v + i] = cut.keeps(x[i], v + i) ? probability(x[i], sc, s.pow, inv) : 0.0f;
         }
     }
-    // no CTA leaves while another may still write into or read from its shared memory
-    cluster_sync();
+    // (nothing reaches into another CTA's shared memory after the barrier of the sum)
 }
 
 }  // namespace
