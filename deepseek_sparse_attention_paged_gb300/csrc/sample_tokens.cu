@@ -1288,20 +1288,18 @@ extern "C" dsa_status dsa_sample_tokens(const void* logits, int64_t ld, int32_t 
     while (ctas < kMaxCtas && V > ctas * 2048) ctas *= 2;
     const int slice = ((V + ctas - 1) / ctas + 7) / 8 * 8;
     const size_t bytes = (static_cast<size_t>(slice) * align + 15) / 16 * 16 + 16;
-    const bool large = bytes > 40 * 1024;
     // Staged unless most of the work is rows with a top-k, read twice, and there are enough of them to fill the GPU several
     // times: then more CTAs an SM count for more (256 rows of 131072 with k = 50 and probabilities 134 -> 100 us; 64 rows of
     // mixed settings 53 -> 63, 300 with top-p alone 268 -> 361)
     const bool staged = top_k == nullptr || static_cast<int64_t>(R) * ctas <= 4 * static_cast<int64_t>(device_sm_count());
+    const bool large = bytes > 40 * 1024 || !staged;
     const size_t smem = (staged ? bytes : 0) + (large ? sizeof(SampleShared<512>) : sizeof(SampleShared<256>));
     SampleArgs a{logits, ld, V, temperature, top_k, top_p, min_p, u, tokens, probs, ld_probs, ctas, slice, dev_err};
     using Kernel = void (*)(SampleArgs);
-    static const Kernel kernels[2][2][2] = {
-        {{sample_tokens_kernel<float, 256, false>, sample_tokens_kernel<float, 256, true>},
-         {sample_tokens_kernel<float, 512, false>, sample_tokens_kernel<float, 512, true>}},
-        {{sample_tokens_kernel<uint16_t, 256, false>, sample_tokens_kernel<uint16_t, 256, true>},
-         {sample_tokens_kernel<uint16_t, 512, false>, sample_tokens_kernel<uint16_t, 512, true>}}};
-    const void* kernel = reinterpret_cast<const void*>(kernels[bf16][large][staged]);
+    static const Kernel kernels[2][3] = {
+        {sample_tokens_kernel<float, 512, false>, sample_tokens_kernel<float, 256, true>, sample_tokens_kernel<float, 512, true>},
+        {sample_tokens_kernel<uint16_t, 512, false>, sample_tokens_kernel<uint16_t, 256, true>, sample_tokens_kernel<uint16_t, 512, true>}};
+    const void* kernel = reinterpret_cast<const void*>(kernels[bf16 ? 1 : 0][!staged ? 0 : (large ? 2 : 1)]);
     if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)) != cudaSuccess)
         return DSA_ERR_CUDA;
     cudaLaunchConfig_t cfg = {};
