@@ -1061,12 +1061,17 @@ __global__ void __launch_bounds__(NT, (kStaged ? 1024 : 2048) / NT) sample_token
                         const uint64_t w = weight(bin_value(bin), sc, s.pow);
                         left = (limit - before + w - 1) / w;
                     }
-                    for (int c = 0; c < C; ++c) {
-                        const uint32_t n = bin != kSide ? get(&counts[bin], c) : 0;
-                        const uint32_t q = static_cast<uint32_t>(min(static_cast<uint64_t>(n), left));
+                    uint32_t each[kMaxCtas];
+#pragma unroll
+                    for (int c = 0; c < kMaxCtas; ++c) each[c] = c < C ? get(&counts[bin], c) : 0;
+#pragma unroll
+                    for (int c = 0; c < kMaxCtas; ++c) {
+                        const uint32_t q = static_cast<uint32_t>(min(static_cast<uint64_t>(each[c]), left));
                         left -= q;
-                        put(&s.quota, c, q);
-                        put(&s.bin, c, bin != kSide ? static_cast<uint32_t>(bin) : 0xffffffffu);
+                        if (c < C) {
+                            put(&s.quota, c, q);
+                            put(&s.bin, c, bin != kSide ? static_cast<uint32_t>(bin) : 0xffffffffu);
+                        }
                     }
                 }
                 before += own[i];
@@ -1121,11 +1126,13 @@ __global__ void __launch_bounds__(NT, (kStaged ? 1024 : 2048) / NT) sample_token
         for (int i = 0; i < kBins / NT; ++i) {
             own[i] = 0;
             const int b = tid * each + i;
-            if (i < each && b < share)
-                for (int c = 0; c < C; ++c) {
-                    const uint2 h = get2(&s.hist[b0 + b], c);
-                    own[i] += (static_cast<uint64_t>(h.y) << 32) | h.x;
-                }
+            if (i < each && b < share) {
+                uint2 h[kMaxCtas];
+#pragma unroll
+                for (int c = 0; c < kMaxCtas; ++c) h[c] = c < C ? get2(&s.hist[b0 + b], c) : make_uint2(0u, 0u);
+#pragma unroll
+                for (int c = 0; c < kMaxCtas; ++c) own[i] += wide(h[c]);
+            }
             mine += own[i];
         }
         const int now = flip;
