@@ -88,7 +88,7 @@ struct SampleArgs {
 
 template <int NT>
 struct alignas(16) SampleShared {
-    static constexpr int kStage = kBins;
+    static constexpr int kStage = kBins;                       // (8 KB)
     static_assert(kStage >= 2 * kFew && kStage <= kList, "scratch");
     union {
         float maxima[kMaxCtas * NT / 2];       // every two threads' largest entry, of all CTAs
@@ -571,6 +571,7 @@ __global__ void __launch_bounds__(NT, (kStaged ? 1024 : 2048) / NT) sample_token
     extern __shared__ __align__(16) unsigned char smem[];
     SampleShared<NT>& s = *reinterpret_cast<SampleShared<NT>*>(smem);
     constexpr int kGroup = 16 / sizeof(E), kWarps = NT / 32, kEntries = kList / NT;
+    constexpr bool kTable = NT == 1024;          // a CTA a row: weights of bf16 values looked up
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int C = a.ctas;
     const int row = blockIdx.x / C;
@@ -984,14 +985,17 @@ __global__ void __launch_bounds__(NT, (kStaged ? 1024 : 2048) / NT) sample_token
     Cut cut{-INFINITY, -1};
     bool counted = false;                        // the border is found and `mine` the mass kept, by counts of values
     uint32_t kept_ties = 0;                      // of this CTA's entries at the border, where it lies among them
+    uint64_t tie_weight = 0;
+    uint64_t* table = reinterpret_cast<uint64_t*>(smem + sizeof(SampleShared<NT>));   // kTable: weights of the values that are kept
     uint64_t mine = 0;
     if constexpr (sizeof(E) == 2) {
         // ---- top-p alone, bf16: few distinct values, so their numbers say all.  A count is one addition in shared memory where a
         // mass is 30 operations and two of them; each weight is formed once a value, and once the border is known
         // the counts give the mass that a CTA keeps.  (300 rows of 100003: 258 -> 165 us)
         const int share = (kValueBins + C - 1) / C;                          // of the bins
-        if (use_p && !use_k && share <= 3 * NT && !sc.wide && sc.top < 128.0f) {
-            static_assert(sizeof(s.stage) + sizeof(s.list) >= kValueBins * sizeof(uint32_t) && offsetof(SampleShared<NT>, list) == sizeof(s.stage), "counts");
+        constexpr int kEach = kTable ? 5 : 3;                                // bins a thread
+        if (use_p && !use_k && share <= kEach * NT && !sc.wide && sc.top < 128.0f) {
+            static_assert(offsetof(SampleShared<NT>, list) + sizeof(s.list) >= kValueBins * sizeof(uint32_t), "counts");
             uint32_t* counts = reinterpret_cast<uint32_t*>(&s);              // over stage and list
             uint2* odd = s.sel_mass;                                         // masses of the numbers below 2^-9, and of those down from -2^7
             __syncthreads();
@@ -1014,14 +1018,14 @@ __global__ void __launch_bounds__(NT, (kStaged ? 1024 : 2048) / NT) sample_token
                 }
             });
             cluster_sync();
-            // this CTA's share of the bins, the largest values first, three a thread: masses over the cluster
+            // this CTA's share of the bins, the largest values first, kEach a thread: masses over the cluster
             auto bin_at = [&](int i) {                                       // -1: none
-                const int d = static_cast<int>(rank) * share + tid * 3 + i;
-                return tid * 3 + i < share && d < kValueBins ? kValueBins - 1 - d : -1;
+                const int d = static_cast<int>(rank) * share + tid * kEach + i;
+                return tid * kEach + i < share && d < kValueBins ? kValueBins - 1 - d : -1;
             };
-            uint64_t own[3];
+            uint64_t own[kEach];
 #pragma unroll
-            for (int i = 0; i < 3; ++i) {
+            for (int i = 0; i < kEach; ++i) {
                 const int bin = bin_at(i);
                 own[i] = 0;
                 if (bin >= 0) {
@@ -1053,7 +1057,7 @@ __global__ void __launch_bounds__(NT, (kStaged ? 1024 : 2048) / NT) sample_token
             if (rest != 0 && before + mine < limit)
                 for (int c = 0; c < C; ++c) put(&s.bin, c, 0xffffffffu);
 #pragma unroll
-            for (int i = 0; i < 3; ++i) {
+            for (int i = 0; i < kEach; ++i) {
                 if (own[i] != 0 && before < limit && before + own[i] >= limit) {
                     const int bin = bin_at(i);
                     uint64_t left = 0;
@@ -1090,6 +1094,7 @@ __global__ void __launch_bounds__(NT, (kStaged ? 1024 : 2048) / NT) sample_token
                 }
                 kept_ties = z_cut > bin_value(border) || quota == ties ? 0 : quota;   // 0: all or none
                 mine = 0;
+                tie_weight = kept_ties > 0 ? weight(z_cut, sc, s.pow) : 0;
                 for (int b = tid; b < kValueBins; b += NT) {
                     if (b == kSide) {
                         if (z_cut < 0.0f) mine += wide(odd[0]);
@@ -1097,7 +1102,11 @@ __global__ void __launch_bounds__(NT, (kStaged ? 1024 : 2048) / NT) sample_token
                     }
                     const float z = bin_value(b);
                     const uint32_t n = z > z_cut || (z == z_cut && cut.index == 0x7fffffff) ? counts[b] : (z == z_cut ? quota : 0);
-                    if (n != 0) mine += n * weight(z, sc, s.pow);
+                    if (kTable || n != 0) {
+                        const uint64_t w = kTable && (z < z_cut || (z == z_cut && cut.index != 0x7fffffff)) ? 0 : weight(z, sc, s.pow);
+                        if (kTable) table[b] = w;
+                        mine += kTable && kept_ties > 0 && z == z_cut ? n * tie_weight : n * w;
+                    }
                 }
                 // no CTA reads the counts of another any more, and this one's lie where lists do
             }
@@ -1190,8 +1199,95 @@ __global__ void __launch_bounds__(NT, (kStaged ? 1024 : 2048) / NT) sample_token
     const uint64_t target = min(scaled(u, sum, false), sum - 1);       // u of 1 or more: the last one kept
     uint64_t before = 0;
     for (int c = 0; c < static_cast<int>(rank); ++c) before += s.cta_sum[now][c];
+    if constexpr (kTable) {
+        if (counted) {
+            // ---- the draw, every entry's weight from the table; entries equal to the border's value are counted, the first
+            // kept_ties of them, in the order of the indices, are kept
+            const uint32_t border_bits = kept_ties > 0 ? __float_as_uint(cut.z) >> 16 : 0xffffu;      // (no number)
+            auto kept_weight = [&](uint32_t h) -> uint64_t {
+                const uint32_t size = h & 0x7fffu, at = size - kFirstBits;
+                if (at < static_cast<uint32_t>(kSide)) {
+                    const int d = static_cast<int>(at) + 1;
+                    return table[(h & 0x8000u) != 0u ? kSide - d : kSide + d];
+                }
+                return size < static_cast<uint32_t>(kFirstBits) && cut.z < 0.0f ? weight(__uint_as_float(h << 16), sc, s.pow) : 0;
+            };
+            auto half = [](const uint4& r, int i) {
+                const uint32_t w = (i >> 1) == 0 ? r.x : ((i >> 1) == 1 ? r.y : ((i >> 1) == 2 ? r.z : r.w));
+                return (i & 1) != 0 ? w >> 16 : w & 0xffffu;
+            };
+            uint64_t own = 0;
+            uint32_t ties = 0;
+            __syncthreads();                                           // the table is written
+            sl.each_group([&](const uint4& r, int) {
+#pragma unroll
+                for (int i = 0; i < kGroup; ++i) {
+                    own += kept_weight(half(r, i));
+                    ties += half(r, i) == border_bits ? 1u : 0u;
+                }
+            });
+            own = warp_sum64(own);
+            ties = __reduce_add_sync(0xffffffffu, ties);
+            if (lane == 0) {
+                s.warp_sum[flip][warp] = own;
+                s.warp_lo[warp] = ties;
+            }
+            __syncthreads();
+            // lane l: warp l's
+            auto scan32 = [&](uint32_t v) {
+#pragma unroll
+                for (int d = 1; d < 32; d <<= 1) {
+                    const uint32_t o = __shfl_up_sync(0xffffffffu, v, d);
+                    if (lane >= d) v += o;
+                }
+                return v;
+            };
+            const uint32_t t_own = s.warp_lo[lane], t_before = scan32(t_own) - t_own;
+            const uint32_t t_kept = min(t_own, kept_ties - min(kept_ties, t_before));
+            const uint64_t m_own = s.warp_sum[flip][lane] + t_kept * tie_weight, m_upto = warp_scan64(m_own, lane);
+            uint64_t upto = __shfl_sync(0xffffffffu, m_upto, warp);
+            uint64_t from = upto - __shfl_sync(0xffffffffu, m_own, warp);
+            uint32_t seen = __shfl_sync(0xffffffffu, t_before, warp);
+            if (from <= target && target < upto) {
+                bool done = false;
+                for (int st = 0; st < sl.steps() && !done; ++st) {
+                    const int g = sl.g0 + st * 32 + lane;
+                    const uint4 r = g < sl.g1 ? sl.raw(g) : make_uint4(0xff80ff80u, 0xff80ff80u, 0xff80ff80u, 0xff80ff80u);
+                    uint32_t n = 0;
+#pragma unroll
+                    for (int i = 0; i < kGroup; ++i) n += half(r, i) == border_bits ? 1u : 0u;
+                    uint32_t tie = seen + scan32(n) - n;               // ties in front of this lane's
+                    seen = __shfl_sync(0xffffffffu, tie + n, 31);
+                    uint64_t w[kGroup], sum_own = 0;
+#pragma unroll
+                    for (int i = 0; i < kGroup; ++i) {
+                        const bool is_tie = half(r, i) == border_bits;
+                        w[i] = is_tie ? (tie < kept_ties ? tie_weight : 0) : kept_weight(half(r, i));
+                        tie += is_tie ? 1u : 0u;
+                        sum_own += w[i];
+                    }
+                    const uint64_t inc = from + warp_scan64(sum_own, lane);
+                    uint64_t at = inc - sum_own;
+                    if (at <= target && target < inc) {
+                        int token = -1;
+#pragma unroll
+                        for (int i = 0; i < kGroup; ++i) {
+                            at += w[i];
+                            if (token < 0 && at > target) token = sl.group_index(g) + i;
+                        }
+                        a.tokens[row] = token;
+                        done = true;
+                    }
+                    done = __any_sync(0xffffffffu, done);
+                    from = __shfl_sync(0xffffffffu, inc, 31);
+                }
+            }
+            if (probs == nullptr) return;
+            __syncthreads();
+        }
+    }
     if (counted) {                                                     // only the CTA with the border needs its warps' sums
-        const bool here = before <= target && target < before + s.cta_sum[now][rank];
+        const bool here = !kTable && before <= target && target < before + s.cta_sum[now][rank];
         if (kept_ties > 0 && (here || probs != nullptr)) {             // the last one kept, in the order of the indices
             uint64_t n = 0;
             sl.each([&](float z, int) { n += z == cut.z ? 1 : 0; });
@@ -1300,18 +1396,29 @@ extern "C" dsa_status dsa_sample_tokens(const void* logits, int64_t ld, int32_t 
     // mixed settings 53 -> 63, 300 with top-p alone 268 -> 361)
     const bool staged = top_k == nullptr || static_cast<int64_t>(R) * ctas <= 4 * static_cast<int64_t>(device_sm_count());
     const bool large = bytes > 40 * 1024 || !staged;
-    const size_t smem = (staged ? bytes : 0) + (large ? sizeof(SampleShared<512>) : sizeof(SampleShared<256>));
+    size_t smem = (staged ? bytes : 0) + (large ? sizeof(SampleShared<512>) : sizeof(SampleShared<256>));
     SampleArgs a{logits, ld, V, temperature, top_k, top_p, min_p, u, tokens, probs, ld_probs, ctas, slice, dev_err};
     using Kernel = void (*)(SampleArgs);
+    // A CTA a row where top-p alone goes by counts of values and there are rows enough: no exchanges between CTAs, and what
+    // each CTA does for all values is done once a row (300 rows of 100003: 135 -> MEASURED us)
+    const bool single = bf16 && top_k == nullptr && top_p != nullptr && R >= device_sm_count();
     static const Kernel kernels[2][3] = {
         {sample_tokens_kernel<float, 512, false>, sample_tokens_kernel<float, 256, true>, sample_tokens_kernel<float, 512, true>},
         {sample_tokens_kernel<uint16_t, 512, false>, sample_tokens_kernel<uint16_t, 256, true>, sample_tokens_kernel<uint16_t, 512, true>}};
     const void* kernel = reinterpret_cast<const void*>(kernels[bf16 ? 1 : 0][!staged ? 0 : (large ? 2 : 1)]);
+    int threads = large ? 512 : 256;
+    if (single) {
+        kernel = reinterpret_cast<const void*>(&sample_tokens_kernel<uint16_t, 1024, false>);
+        threads = 1024;
+        ctas = a.ctas = 1;
+        a.slice = (V + 7) / 8 * 8;
+        smem = sizeof(SampleShared<1024>) + kValueBins * sizeof(uint64_t);
+    }
     if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)) != cudaSuccess)
         return DSA_ERR_CUDA;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(R) * ctas);
-    cfg.blockDim = dim3(large ? 512 : 256);
+    cfg.blockDim = dim3(static_cast<unsigned>(threads));
     cfg.dynamicSmemBytes = smem;
     cfg.stream = static_cast<cudaStream_t>(stream);
     cudaLaunchAttribute attr[2];

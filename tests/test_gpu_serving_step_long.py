@@ -165,3 +165,35 @@ def test_sample_rows_in_large_batches_as_alone(bf16):
         many = _run_sample(x.repeat(n, 1), V, u * n, **{k: v * n for k, v in kw.items()})
         assert many[0] == few[0] * n and few[2] == many[2]
         assert bool((torch.from_numpy(many[1]).view(n, 8, V) == torch.from_numpy(few[1])[None]).all())
+
+
+@pytest.mark.parametrize("kind", ["usual", "whole", "tiny", "high", "two", "masked"])
+def test_sample_top_p_rows_in_large_batches(kind):
+    """bf16 rows with top-p alone, as many as make a CTA take each: as in a small batch, bit for bit, odd strides and rows of
+    every alignment among them."""
+    V, n = 30011, 30
+    g = torch.Generator().manual_seed(80 + len(kind))
+    x = _logits(8, V, 81, True)
+    if kind == "whole":
+        x = x.float().round().to(torch.bfloat16)
+    elif kind == "tiny":
+        x = (x.float() * 1e-4).to(torch.bfloat16)
+    elif kind == "high":
+        x = (x.float() + 150.0).to(torch.bfloat16)
+    elif kind == "two":
+        x[:] = -1.0
+        x[:, 5::4] = 0.5
+    elif kind == "masked":
+        x[:, 100:] = torch.where(torch.rand(8, V - 100, generator=g) < 0.9, torch.tensor(-math.inf), x[:, 100:].float()).to(torch.bfloat16)
+        x[3] = -math.inf
+        x[4, 7:] = math.nan
+    u = torch.rand(8, generator=g).tolist()
+    for kw in (dict(top_p=[0.9, 0.5, 0.99, 0.1, 0.75, 0.95, 1.0, 0.0]),
+               dict(top_p=[0.9, 0.5, 0.99, 0.3, 0.6, 0.95, 0.8, 0.7], temperature=[1.0, 0.0, 0.3, 1.0, 2.0, 8.0, 1.0, 0.9],
+                    min_p=[0.0, 0.0, 0.1, 0.5, 0.0, 0.9, 1.0, 0.2])):
+        few = _run_sample(x, V, u, **kw)
+        for probs in (True, False):
+            many = _run_sample(x.repeat(n, 1), V, u * n, probs=probs, **{k: v * n for k, v in kw.items()})
+            assert many[0] == few[0] * n and few[2] == many[2]
+            if probs:
+                assert bool((torch.from_numpy(many[1]).view(n, 8, V) == torch.from_numpy(few[1])[None]).all())
