@@ -40,6 +40,7 @@ constexpr int kMaxTopK = 1024;
 constexpr int kBins = 1024, kBinsPerOctave = 32;
 constexpr int kSelectBins = 256;
 // bf16 numbers from 2^-9 up to 2^7, of both signs, each a bin: 16 octaves of 128; in the middle one for all smaller ones
+constexpr int kOddList = 4096;                 // others that are listed
 constexpr int kSide = 16 * 128, kValueBins = 2 * kSide + 1, kFirstBits = (127 - 9) << 7;
 constexpr int kOne = 46;                       // fraction bits of a weight
 constexpr int kMaxSampleVocab = 1 << 18;       // sums of weights stay below 2^64
@@ -385,8 +386,9 @@ struct Slice {
             for (int i = 0; i < kGroup; ++i) x[i] = clean(x[i], most);
         }
     }
-    // The first pass: the largest entry of this thread's.
-    __device__ __forceinline__ float take_in() const {
+    // The first pass: the largest entry of this thread's; f(group) for each group as it lies in memory.
+    template <typename F>
+    __device__ __forceinline__ float take_in(F f) const {
         constexpr int kLoads = kStaged ? 8 : 4;              // (of 64 and of 32 registers)
         float top = -INFINITY;
         for (int g = g0 + lane; g < g1; g += 32 * kLoads) {
@@ -397,6 +399,7 @@ struct Slice {
 #pragma unroll
             for (int i = 0; i < kLoads; ++i)
                 if (g + 32 * i < g1) {
+                    f(r[i]);
                     float x[kGroup];
                     unpack(r[i], x);
                     if constexpr (kStaged) {
@@ -604,11 +607,44 @@ __global__ void __launch_bounds__(NT, (kStaged ? 1024 : 2048) / NT) sample_token
     const int per = (groups + kWarps - 1) / kWarps;
     sl.g0 = min(groups, warp * per);
     sl.g1 = min(groups, sl.g0 + per);
-    const float top_own = sl.take_in();
+    // Numbers of the values of bf16 rows (below).  A CTA that has a row for itself counts as it reads; what has no bin of its
+    // own it lists.
+    uint32_t* counts = reinterpret_cast<uint32_t*>(&s);                      // over stage and list
+    static_assert(offsetof(SampleShared<NT>, list) + sizeof(s.list) >= kValueBins * sizeof(uint32_t) + (kTable ? kOddList * sizeof(uint16_t) : 0), "counts");
+    uint16_t* odd_list = reinterpret_cast<uint16_t*>(counts + kValueBins);
+    auto count_values = [&](const uint4& r, auto odd_one) {
+        const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const uint32_t h = (i & 1) != 0 ? w[i >> 1] >> 16 : w[i >> 1] & 0xffffu;
+            const uint32_t size = h & 0x7fffu, at = size - kFirstBits;
+            if (at < static_cast<uint32_t>(kSide)) {
+                const int d = static_cast<int>(at) + 1;
+                atomicAdd(&counts[(h & 0x8000u) != 0u ? kSide - d : kSide + d], 1u);
+            } else if (size < 0x7f80u) {                                     // (a row with +infinity does not go by counts)
+                odd_one(h);
+            }
+        }
+    };
+    bool counting = false;
+    if constexpr (kTable) counting = use_p && !use_k && !greedy;
+    if (counting) {
+        for (int i = tid; i < kValueBins; i += NT) counts[i] = 0;
+        if (tid == 0) s.stage_count = 0;
+        __syncthreads();
+    }
+    const float top_own = sl.take_in([&](const uint4& r) {
+        if constexpr (kTable)
+            if (counting)
+                count_values(r, [&](uint32_t h) {
+                    const uint32_t at = atomicAdd(&s.stage_count, 1u);
+                    if (at < kOddList) odd_list[at] = static_cast<uint16_t>(h);
+                });
+    });
     for (int i = tid; i < (1 << kPowBits) / 4; i += NT)
         reinterpret_cast<uint4*>(s.pow)[i] = __ldg(reinterpret_cast<const uint4*>(kPow.coarse) + i);
     if (tid == 0) {
-        s.stage_count = 0;
+        if (!counting) s.stage_count = 0;
         s.found = 0x7fffffff;
         const double r = 1024.0 * 1.4426950408889634074 / static_cast<double>(temperature);
         s.rh = r < FLT_MAX ? static_cast<float>(r) : FLT_MAX;
@@ -994,29 +1030,23 @@ __global__ void __launch_bounds__(NT, (kStaged ? 1024 : 2048) / NT) sample_token
         // the counts give the mass that a CTA keeps.  (300 rows of 100003: 258 -> 165 us)
         const int share = (kValueBins + C - 1) / C;                          // of the bins
         constexpr int kEach = kTable ? 5 : 3;                                // bins a thread
-        if (use_p && !use_k && share <= kEach * NT && !sc.wide && sc.top < 128.0f) {
+        if (use_p && !use_k && share <= kEach * NT && !sc.wide && sc.top < 128.0f && (!kTable || s.stage_count <= kOddList)) {
             static_assert(offsetof(SampleShared<NT>, list) + sizeof(s.list) >= kValueBins * sizeof(uint32_t), "counts");
-            uint32_t* counts = reinterpret_cast<uint32_t*>(&s);              // over stage and list
             uint2* odd = s.sel_mass;                                         // masses of the numbers below 2^-9, and of those down from -2^7
+            auto odd_one = [&](uint32_t h) {
+                const uint64_t m = weight(__uint_as_float(h << 16), sc, s.pow);
+                if (m != 0) add_wide(&odd[(h & 0x7fffu) < static_cast<uint32_t>(kFirstBits) ? 0 : 1], m);
+            };
             __syncthreads();
-            for (int i = tid; i < kValueBins; i += NT) counts[i] = 0;
+            if (!kTable)
+                for (int i = tid; i < kValueBins; i += NT) counts[i] = 0;
             if (tid < 2) odd[tid] = make_uint2(0u, 0u);
             __syncthreads();
-            sl.each_group([&](const uint4& r, int) {
-                const uint32_t w[4] = {r.x, r.y, r.z, r.w};
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const uint32_t h = (i & 1) != 0 ? w[i >> 1] >> 16 : w[i >> 1] & 0xffffu;
-                    const uint32_t size = h & 0x7fffu, at = size - kFirstBits;
-                    if (at < static_cast<uint32_t>(kSide)) {
-                        const int d = static_cast<int>(at) + 1;
-                        atomicAdd(&counts[(h & 0x8000u) != 0u ? kSide - d : kSide + d], 1u);
-                    } else if (size < 0x7f80u) {                             // (the row has no +infinity here)
-                        const uint64_t m = weight(__uint_as_float(h << 16), sc, s.pow);
-                        if (m != 0) add_wide(&odd[size < static_cast<uint32_t>(kFirstBits) ? 0 : 1], m);
-                    }
-                }
-            });
+            if constexpr (kTable) {
+                for (int i = tid; i < static_cast<int>(s.stage_count); i += NT) odd_one(odd_list[i]);
+            } else {
+                sl.each_group([&](const uint4& r, int) { count_values(r, odd_one); });
+            }
             cluster_sync();
             // this CTA's share of the bins, the largest values first, kEach a thread: masses over the cluster
             auto bin_at = [&](int i) {                                       // -1: none
@@ -1035,7 +1065,9 @@ __global__ void __launch_bounds__(NT, (kStaged ? 1024 : 2048) / NT) sample_token
                         for (int c = 0; c < kMaxCtas; ++c) each[c] = c < C ? get(&counts[bin], c) : 0;
 #pragma unroll
                         for (int c = 0; c < kMaxCtas; ++c) n += each[c];
-                        own[i] = n == 0 ? 0 : n * weight(bin_value(bin), sc, s.pow);
+                        const uint64_t w = n == 0 ? 0 : weight(bin_value(bin), sc, s.pow);
+                        if (kTable) table[bin] = w;
+                        own[i] = n * w;
                     } else {
                         for (int c = 0; c < C; ++c) own[i] += wide(get2(&odd[0], c));
                     }
@@ -1102,11 +1134,7 @@ __global__ void __launch_bounds__(NT, (kStaged ? 1024 : 2048) / NT) sample_token
                     }
                     const float z = bin_value(b);
                     const uint32_t n = z > z_cut || (z == z_cut && cut.index == 0x7fffffff) ? counts[b] : (z == z_cut ? quota : 0);
-                    if (kTable || n != 0) {
-                        const uint64_t w = kTable && (z < z_cut || (z == z_cut && cut.index != 0x7fffffff)) ? 0 : weight(z, sc, s.pow);
-                        if (kTable) table[b] = w;
-                        mine += kTable && kept_ties > 0 && z == z_cut ? n * tie_weight : n * w;
-                    }
+                    if (n != 0) mine += n * (kTable ? table[b] : weight(z, sc, s.pow));
                 }
                 // no CTA reads the counts of another any more, and this one's lie where lists do
             }
@@ -1204,13 +1232,16 @@ __global__ void __launch_bounds__(NT, (kStaged ? 1024 : 2048) / NT) sample_token
             // ---- the draw, every entry's weight from the table; entries equal to the border's value are counted, the first
             // kept_ties of them, in the order of the indices, are kept
             const uint32_t border_bits = kept_ties > 0 ? __float_as_uint(cut.z) >> 16 : 0xffffu;      // (no number)
+            const bool whole = kept_ties == 0;                         // those at the border are kept
             auto kept_weight = [&](uint32_t h) -> uint64_t {
+                const float z = __uint_as_float(h << 16);
+                if (!(z > cut.z || (whole && z == cut.z))) return 0;
                 const uint32_t size = h & 0x7fffu, at = size - kFirstBits;
                 if (at < static_cast<uint32_t>(kSide)) {
                     const int d = static_cast<int>(at) + 1;
                     return table[(h & 0x8000u) != 0u ? kSide - d : kSide + d];
                 }
-                return size < static_cast<uint32_t>(kFirstBits) && cut.z < 0.0f ? weight(__uint_as_float(h << 16), sc, s.pow) : 0;
+                return weight(z, sc, s.pow);
             };
             auto half = [](const uint4& r, int i) {
                 const uint32_t w = (i >> 1) == 0 ? r.x : ((i >> 1) == 1 ? r.y : ((i >> 1) == 2 ? r.z : r.w));
