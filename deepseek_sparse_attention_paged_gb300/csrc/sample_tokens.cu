@@ -40,7 +40,7 @@ constexpr int kMaxTopK = 1024;
 constexpr int kBins = 1024, kBinsPerOctave = 32;
 constexpr int kSelectBins = 256;
 // bf16 numbers from 2^-9 up to 2^7, of both signs, each a bin: 16 octaves of 128; in the middle one for all smaller ones
-constexpr int kOddList = 4096;                 // others that are listed
+constexpr int kOddList = 3072;                 // entries of other values that are listed
 constexpr int kSide = 16 * 128, kValueBins = 2 * kSide + 1, kFirstBits = (127 - 9) << 7;
 constexpr int kOne = 46;                       // fraction bits of a weight
 constexpr int kMaxSampleVocab = 1 << 18;       // sums of weights stay below 2^64
@@ -386,7 +386,7 @@ struct Slice {
             for (int i = 0; i < kGroup; ++i) x[i] = clean(x[i], most);
         }
     }
-    // The first pass: the largest entry of this thread's; f(group) for each group as it lies in memory.
+    // The first pass: the largest entry of this thread's; f(group, its index) for each group as it lies in memory.
     template <typename F>
     __device__ __forceinline__ float take_in(F f) const {
         constexpr int kLoads = kStaged ? 8 : 4;              // (of 64 and of 32 registers)
@@ -399,7 +399,7 @@ struct Slice {
 #pragma unroll
             for (int i = 0; i < kLoads; ++i)
                 if (g + 32 * i < g1) {
-                    f(r[i]);
+                    f(r[i], group_index(g + 32 * i));
                     float x[kGroup];
                     unpack(r[i], x);
                     if constexpr (kStaged) {
@@ -610,9 +610,9 @@ __global__ void __launch_bounds__(NT, (kStaged ? 1024 : 2048) / NT) sample_token
     // Numbers of the values of bf16 rows (below).  A CTA that has a row for itself counts as it reads; what has no bin of its
     // own it lists.
     uint32_t* counts = reinterpret_cast<uint32_t*>(&s);                      // over stage and list
-    static_assert(offsetof(SampleShared<NT>, list) + sizeof(s.list) >= kValueBins * sizeof(uint32_t) + (kTable ? kOddList * sizeof(uint16_t) : 0), "counts");
-    uint16_t* odd_list = reinterpret_cast<uint16_t*>(counts + kValueBins);
-    auto count_values = [&](const uint4& r, auto odd_one) {
+    static_assert(offsetof(SampleShared<NT>, list) + sizeof(s.list) >= kValueBins * sizeof(uint32_t) + (kTable ? kOddList * sizeof(uint32_t) : 0), "counts");
+    uint32_t* odd_list = counts + kValueBins;                                // indices
+    auto count_values = [&](const uint4& r, int v, auto odd_one) {
         const uint32_t w[4] = {r.x, r.y, r.z, r.w};
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
@@ -622,7 +622,7 @@ __global__ void __launch_bounds__(NT, (kStaged ? 1024 : 2048) / NT) sample_token
                 const int d = static_cast<int>(at) + 1;
                 atomicAdd(&counts[(h & 0x8000u) != 0u ? kSide - d : kSide + d], 1u);
             } else if (size < 0x7f80u) {                                     // (a row with +infinity does not go by counts)
-                odd_one(h);
+                odd_one(h, v + i);
             }
         }
     };
@@ -633,12 +633,12 @@ __global__ void __launch_bounds__(NT, (kStaged ? 1024 : 2048) / NT) sample_token
         if (tid == 0) s.stage_count = 0;
         __syncthreads();
     }
-    const float top_own = sl.take_in([&](const uint4& r) {
+    const float top_own = sl.take_in([&](const uint4& r, int v) {
         if constexpr (kTable)
             if (counting)
-                count_values(r, [&](uint32_t h) {
+                count_values(r, v, [&](uint32_t, int index) {
                     const uint32_t at = atomicAdd(&s.stage_count, 1u);
-                    if (at < kOddList) odd_list[at] = static_cast<uint16_t>(h);
+                    if (at < kOddList) odd_list[at] = static_cast<uint32_t>(index);
                 });
     });
     for (int i = tid; i < (1 << kPowBits) / 4; i += NT)
@@ -1033,7 +1033,7 @@ __global__ void __launch_bounds__(NT, (kStaged ? 1024 : 2048) / NT) sample_token
         if (use_p && !use_k && share <= kEach * NT && !sc.wide && sc.top < 128.0f && (!kTable || s.stage_count <= kOddList)) {
             static_assert(offsetof(SampleShared<NT>, list) + sizeof(s.list) >= kValueBins * sizeof(uint32_t), "counts");
             uint2* odd = s.sel_mass;                                         // masses of the numbers below 2^-9, and of those down from -2^7
-            auto odd_one = [&](uint32_t h) {
+            auto odd_one = [&](uint32_t h, int) {
                 const uint64_t m = weight(__uint_as_float(h << 16), sc, s.pow);
                 if (m != 0) add_wide(&odd[(h & 0x7fffu) < static_cast<uint32_t>(kFirstBits) ? 0 : 1], m);
             };
@@ -1043,9 +1043,10 @@ __global__ void __launch_bounds__(NT, (kStaged ? 1024 : 2048) / NT) sample_token
             if (tid < 2) odd[tid] = make_uint2(0u, 0u);
             __syncthreads();
             if constexpr (kTable) {
-                for (int i = tid; i < static_cast<int>(s.stage_count); i += NT) odd_one(odd_list[i]);
+                for (int i = tid; i < static_cast<int>(s.stage_count); i += NT)
+                    odd_one(static_cast<uint32_t>(reinterpret_cast<const uint16_t*>(logits)[odd_list[i]]), 0);
             } else {
-                sl.each_group([&](const uint4& r, int) { count_values(r, odd_one); });
+                sl.each_group([&](const uint4& r, int v) { count_values(r, v, odd_one); });
             }
             cluster_sync();
             // this CTA's share of the bins, the largest values first, kEach a thread: masses over the cluster
@@ -1062,7 +1063,7 @@ __global__ void __launch_bounds__(NT, (kStaged ? 1024 : 2048) / NT) sample_token
                     if (bin != kSide) {
                         uint32_t each[kMaxCtas], n = 0;
 #pragma unroll
-                        for (int c = 0; c < kMaxCtas; ++c) each[c] = c < C ? get(&counts[bin], c) : 0;
+                        for (int c = 0; c < kMaxCtas; ++c) each[c] = kTable ? (c == 0 ? counts[bin] : 0) : (c < C ? get(&counts[bin], c) : 0);
 #pragma unroll
                         for (int c = 0; c < kMaxCtas; ++c) n += each[c];
                         const uint64_t w = n == 0 ? 0 : weight(bin_value(bin), sc, s.pow);
@@ -1232,16 +1233,16 @@ __global__ void __launch_bounds__(NT, (kStaged ? 1024 : 2048) / NT) sample_token
             // ---- the draw, every entry's weight from the table; entries equal to the border's value are counted, the first
             // kept_ties of them, in the order of the indices, are kept
             const uint32_t border_bits = kept_ties > 0 ? __float_as_uint(cut.z) >> 16 : 0xffffu;      // (no number)
-            const bool whole = kept_ties == 0;                         // those at the border are kept
-            auto kept_weight = [&](uint32_t h) -> uint64_t {
+            const float below = kept_ties == 0 ? nextafterf(cut.z, -INFINITY) : cut.z;               // kept: z > below
+            auto bin_weight = [&](uint32_t h) -> uint64_t {
+                const uint32_t at = (h & 0x7fffu) - kFirstBits;
+                const int neg = static_cast<int>(h << 16) >> 31, d = (static_cast<int>(at + 1) ^ neg) - neg;
+                return __uint_as_float(h << 16) > below && at < static_cast<uint32_t>(kSide) ? table[kSide + d] : 0;
+            };
+            // an entry without a bin of its own
+            auto odd_weight = [&](uint32_t h) -> uint64_t {
                 const float z = __uint_as_float(h << 16);
-                if (!(z > cut.z || (whole && z == cut.z))) return 0;
-                const uint32_t size = h & 0x7fffu, at = size - kFirstBits;
-                if (at < static_cast<uint32_t>(kSide)) {
-                    const int d = static_cast<int>(at) + 1;
-                    return table[(h & 0x8000u) != 0u ? kSide - d : kSide + d];
-                }
-                return weight(z, sc, s.pow);
+                return z > below && (h & 0x7fffu) < static_cast<uint32_t>(kFirstBits) ? weight(z, sc, s.pow) : 0;
             };
             auto half = [](const uint4& r, int i) {
                 const uint32_t w = (i >> 1) == 0 ? r.x : ((i >> 1) == 1 ? r.y : ((i >> 1) == 2 ? r.z : r.w));
@@ -1253,16 +1254,25 @@ __global__ void __launch_bounds__(NT, (kStaged ? 1024 : 2048) / NT) sample_token
             sl.each_group([&](const uint4& r, int) {
 #pragma unroll
                 for (int i = 0; i < kGroup; ++i) {
-                    own += kept_weight(half(r, i));
+                    own += bin_weight(half(r, i));
                     ties += half(r, i) == border_bits ? 1u : 0u;
                 }
             });
             own = warp_sum64(own);
             ties = __reduce_add_sync(0xffffffffu, ties);
+            uint2* odd_sums = s.sel_mass;                              // of each warp's entries without a bin
             if (lane == 0) {
                 s.warp_sum[flip][warp] = own;
                 s.warp_lo[warp] = ties;
             }
+            if (tid < kWarps) odd_sums[tid] = make_uint2(0u, 0u);
+            __syncthreads();
+            if (below < 0.0f)
+                for (int i = tid; i < static_cast<int>(s.stage_count); i += NT) {
+                    const int v = static_cast<int>(odd_list[i]);
+                    const uint64_t w = odd_weight(reinterpret_cast<const uint16_t*>(logits)[v]);
+                    if (w != 0) add_wide(&odd_sums[(v - sl.first) / kGroup / per], w);
+                }
             __syncthreads();
             // lane l: warp l's
             auto scan32 = [&](uint32_t v) {
@@ -1275,15 +1285,26 @@ __global__ void __launch_bounds__(NT, (kStaged ? 1024 : 2048) / NT) sample_token
             };
             const uint32_t t_own = s.warp_lo[lane], t_before = scan32(t_own) - t_own;
             const uint32_t t_kept = min(t_own, kept_ties - min(kept_ties, t_before));
-            const uint64_t m_own = s.warp_sum[flip][lane] + t_kept * tie_weight, m_upto = warp_scan64(m_own, lane);
+            const uint64_t m_own = s.warp_sum[flip][lane] + wide(odd_sums[lane]) + t_kept * tie_weight, m_upto = warp_scan64(m_own, lane);
             uint64_t upto = __shfl_sync(0xffffffffu, m_upto, warp);
             uint64_t from = upto - __shfl_sync(0xffffffffu, m_own, warp);
             uint32_t seen = __shfl_sync(0xffffffffu, t_before, warp);
             if (from <= target && target < upto) {
                 bool done = false;
+                constexpr int kLoads = 4;                              // steps' groups loaded together
+                uint4 next[kLoads];
                 for (int st = 0; st < sl.steps() && !done; ++st) {
+                    if (st % kLoads == 0) {
+#pragma unroll
+                        for (int j = 0; j < kLoads; ++j) {
+                            const int g = sl.g0 + (st + j) * 32 + lane;
+                            next[j] = g < sl.g1 ? sl.raw(g) : make_uint4(0xff80ff80u, 0xff80ff80u, 0xff80ff80u, 0xff80ff80u);
+                        }
+                    }
                     const int g = sl.g0 + st * 32 + lane;
-                    const uint4 r = g < sl.g1 ? sl.raw(g) : make_uint4(0xff80ff80u, 0xff80ff80u, 0xff80ff80u, 0xff80ff80u);
+                    const uint4 r = next[0];
+#pragma unroll
+                    for (int j = 1; j < kLoads; ++j) next[j - 1] = next[j];
                     uint32_t n = 0;
 #pragma unroll
                     for (int i = 0; i < kGroup; ++i) n += half(r, i) == border_bits ? 1u : 0u;
@@ -1293,7 +1314,7 @@ __global__ void __launch_bounds__(NT, (kStaged ? 1024 : 2048) / NT) sample_token
 #pragma unroll
                     for (int i = 0; i < kGroup; ++i) {
                         const bool is_tie = half(r, i) == border_bits;
-                        w[i] = is_tie ? (tie < kept_ties ? tie_weight : 0) : kept_weight(half(r, i));
+                        w[i] = is_tie ? (tie < kept_ties ? tie_weight : 0) : bin_weight(half(r, i)) + odd_weight(half(r, i));
                         tie += is_tie ? 1u : 0u;
                         sum_own += w[i];
                     }
