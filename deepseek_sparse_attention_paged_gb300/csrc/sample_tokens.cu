@@ -14,8 +14,8 @@
 //
 // A row is split over the CTAs of a cluster, each with a slice of it in shared memory: logits are read from global
 // memory once.
-//   * top-k up to 1024: the k-th largest of the maxima of all pairs of threads is a bound from below that few more than
-//     k entries pass (with G pairs about -G ln(1 - k / G)); those go to the first CTA, which does the rest alone.
+//   * top-k up to 1024: the k-th largest of the maxima of all threads (or pairs of them) is a bound from below that few more
+//     than k entries pass (with G maxima about -G ln(1 - k / G)); those go to the first CTA, which does the rest alone.
 //   * top-p without top-k: masses of 1024 bins of z (32 an octave of w) find the bin of the border; its entries
 //     go to the first CTA, which finds the last one kept.  A second pass sums what is kept.
 //     For bf16 the values themselves are the bins, and counts take the place of masses.
@@ -43,6 +43,7 @@ constexpr int kSelectBins = 256;
 constexpr int kOddList = 3072;                 // entries of other values that are listed
 constexpr int kSide = 16 * 128, kValueBins = 2 * kSide + 1, kFirstBits = (127 - 9) << 7;
 constexpr int kOne = 46;                       // fraction bits of a weight
+constexpr int kSingleRows = 64, kSingleVocab = 2048;   // where a CTA takes a row for itself
 constexpr int kMaxSampleVocab = 1 << 18;       // sums of weights stay below 2^64
 constexpr int kPowBits = 10;
 
@@ -92,7 +93,7 @@ struct alignas(16) SampleShared {
     static constexpr int kStage = kBins;                       // (8 KB)
     static_assert(kStage >= 2 * kFew && kStage <= kList, "scratch");
     union {
-        float maxima[kMaxCtas * NT / 2];       // every two threads' largest entry, of all CTAs
+        float maxima[kMaxCtas * NT / 2];       // every thread's largest entry, of all CTAs (of eight: every two threads')
         uint2 hist[kBins];                     // masses (low and high word)
         uint64_t stage[kStage];                // entries of this CTA on their way to the first one
         struct {
@@ -590,7 +591,7 @@ __global__ void __launch_bounds__(NT, (kStaged ? 1024 : 2048) / NT) sample_token
     const float u = __ldg(a.u + row);
     const bool greedy = !(temperature > 0.0f);
     const bool use_k = k_in > 0 && k_in < a.V, use_p = p_in < 1.0f, use_m = m_in > 0.0f;
-    const bool by_list = use_k && k_in <= min(kMaxTopK, C * NT / 4);
+    const bool by_list = use_k && k_in <= min(kMaxTopK, (C > 4 ? C * NT / 2 : C * NT) / 2);
 
     // ---- the slice
     const E* logits = static_cast<const E*>(a.logits) + static_cast<int64_t>(row) * a.ld;
@@ -657,7 +658,9 @@ __global__ void __launch_bounds__(NT, (kStaged ? 1024 : 2048) / NT) sample_token
     cluster_wait();
     if (by_list && !greedy) {
         const float two = fmaxf(top_own, __shfl_xor_sync(0xffffffffu, top_own, 1));
-        if ((tid & 1) == 0)
+        if (C <= 4)
+            for (int c = 0; c < C; ++c) put(&s.maxima[rank * NT + tid], c, __float_as_uint(top_own));
+        else if ((tid & 1) == 0)
             for (int c = 0; c < C; ++c) put(&s.maxima[(rank * NT + tid) / 2], c, __float_as_uint(two));
     }
     {
@@ -812,7 +815,7 @@ __global__ void __launch_bounds__(NT, (kStaged ? 1024 : 2048) / NT) sample_token
         uint32_t least = 0xffffffffu, finite = 0;
 #pragma unroll
         for (int c = 0; c < kKeys; ++c) {
-            key[c] = c * NT + tid < C * NT / 2 ? order_key(s.maxima[c * NT + tid]) : none;
+            key[c] = c * NT + tid < (C > 4 ? C * NT / 2 : C * NT) ? order_key(s.maxima[c * NT + tid]) : none;
             if (key[c] != none) {
                 least = min(least, key[c]);
                 ++finite;
@@ -1441,6 +1444,10 @@ extern "C" dsa_status dsa_sample_tokens(const void* logits, int64_t ld, int32_t 
     }
     int ctas = 1;
     while (ctas < kMaxCtas && V > ctas * 2048) ctas *= 2;
+    // many rows: not more CTAs than need be (a top-k of up to 1024 wants four), with 8192 entries or so each (k = 50: 512 rows of
+    // 16000 93 -> 51 us, 160 of 32000 31 -> 19; top-p alone: 512 of 16000 174 -> 121, but 120 of 32000 64 -> 77)
+    const int64_t enough = (top_k != nullptr ? 4 : 8) * static_cast<int64_t>(device_sm_count());
+    if (ctas == 8 && R * static_cast<int64_t>(ctas) > enough && V <= 8 * 8192) ctas = 4;
     const int slice = ((V + ctas - 1) / ctas + 7) / 8 * 8;
     const size_t bytes = (static_cast<size_t>(slice) * align + 15) / 16 * 16 + 16;
     // Staged unless most of the work is rows with a top-k, read twice, and there are enough of them to fill the GPU several
@@ -1452,8 +1459,9 @@ extern "C" dsa_status dsa_sample_tokens(const void* logits, int64_t ld, int32_t 
     SampleArgs a{logits, ld, V, temperature, top_k, top_p, min_p, u, tokens, probs, ld_probs, ctas, slice, dev_err};
     using Kernel = void (*)(SampleArgs);
     // A CTA a row where top-p alone goes by counts of values and there are rows enough: no exchanges between CTAs, and what
-    // each CTA does for all values is done once a row (300 rows of 100003: 135 -> MEASURED us)
-    const bool single = bf16 && top_k == nullptr && top_p != nullptr && R >= device_sm_count();
+    // each CTA does for all values is done once a row (rows x entries: 300 x 100003 135 -> 88 us, 512 x 16000 162 -> 65,
+    // 80 x 100000 72 -> 59; 40 x 100000 46 -> 59, 512 x 1000 34 -> 54)
+    const bool single = bf16 && top_k == nullptr && top_p != nullptr && R >= kSingleRows && V > kSingleVocab;
     static const Kernel kernels[2][3] = {
         {sample_tokens_kernel<float, 512, false>, sample_tokens_kernel<float, 256, true>, sample_tokens_kernel<float, 512, true>},
         {sample_tokens_kernel<uint16_t, 512, false>, sample_tokens_kernel<uint16_t, 256, true>, sample_tokens_kernel<uint16_t, 512, true>}};
