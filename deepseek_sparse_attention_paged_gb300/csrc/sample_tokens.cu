@@ -17,7 +17,8 @@
 //   * top-k up to 1024: the k-th largest of the maxima of all threads (or pairs of them) is a bound from below that few more
 //     than k entries pass (with G maxima about -G ln(1 - k / G)); those go to the first CTA, which does the rest alone.
 //   * top-p without top-k: masses of 1024 bins of z (32 an octave of w) find the bin of the border; its entries
-//     go to the first CTA, which finds the last one kept.  A second pass sums what is kept.
+//     go to the first CTA, which finds the last one kept.  With that the masses say what each CTA keeps, and the one
+//     that the random number falls to looks for the token in a second pass.
 //     For bf16 the values themselves are the bins, and counts take the place of masses.
 //   * where more entries than fit (2048) come together (ties, a temperature far above 1), or for a larger top-k:
 //     bisection over the 32 bits of z, a pass over the slices each.
@@ -114,7 +115,7 @@ struct alignas(16) SampleShared {
     uint32_t cut_key;
     int cut_index;
     int bin;
-    uint64_t bin_before;
+    uint64_t bin_before, border_mass;
     // this CTA's
     uint64_t warp_sum[2][NT / 32];
     uint32_t warp_lo[NT / 32], warp_hi[NT / 32];
@@ -350,7 +351,8 @@ __device__ __forceinline__ uint4 load_group(const E* row, int v, int begin, int 
 // groups [w per, (w + 1) per), its lanes one after the other: warps, steps and lanes follow the indices, and a thread
 // reads only what it wrote itself.  kStaged: the slice lies in shared memory, read from global memory once.  Else every
 // pass reads it from there, the first into L2.
-template <typename E, bool kStaged>
+// kDepth: groups that a thread loads together where it reads global memory (by the registers that the kernel has).
+template <typename E, bool kStaged, int kDepth>
 struct Slice {
     static constexpr int kGroup = 16 / sizeof(E);
     uint4* data;
@@ -390,7 +392,7 @@ struct Slice {
     // The first pass: the largest entry of this thread's; f(group, its index) for each group as it lies in memory.
     template <typename F>
     __device__ __forceinline__ float take_in(F f) const {
-        constexpr int kLoads = kStaged ? 8 : 4;              // (of 64 and of 32 registers)
+        constexpr int kLoads = kDepth;
         float top = -INFINITY;
         for (int g = g0 + lane; g < g1; g += 32 * kLoads) {
             uint4 r[kLoads];
@@ -433,7 +435,7 @@ struct Slice {
     // f(group, its index) for every group of this thread, as it lies in memory
     template <typename F>
     __device__ __forceinline__ void each_group(F f) const {
-        constexpr int kLoads = kStaged ? 1 : 4;
+        constexpr int kLoads = kStaged ? 1 : kDepth;
         for (int g = g0 + lane; g < g1; g += 32 * kLoads) {
             uint4 r[kLoads];
 #pragma unroll
@@ -575,7 +577,7 @@ __global__ void __launch_bounds__(NT, (kStaged ? 1024 : 2048) / NT) sample_token
     extern __shared__ __align__(16) unsigned char smem[];
     SampleShared<NT>& s = *reinterpret_cast<SampleShared<NT>*>(smem);
     constexpr int kGroup = 16 / sizeof(E), kWarps = NT / 32, kEntries = kList / NT;
-    constexpr bool kTable = NT == 1024;          // a CTA a row: weights of bf16 values looked up
+    constexpr bool kTable = NT == 1024;          // a CTA a row, no top-k: weights of bf16 values looked up
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int C = a.ctas;
     const int row = blockIdx.x / C;
@@ -590,12 +592,13 @@ __global__ void __launch_bounds__(NT, (kStaged ? 1024 : 2048) / NT) sample_token
     const float m_in = a.min_p != nullptr ? __ldg(a.min_p + row) : 0.0f;
     const float u = __ldg(a.u + row);
     const bool greedy = !(temperature > 0.0f);
-    const bool use_k = k_in > 0 && k_in < a.V, use_p = p_in < 1.0f, use_m = m_in > 0.0f;
+    const bool use_k = !kTable && k_in > 0 && k_in < a.V, use_p = p_in < 1.0f, use_m = m_in > 0.0f;
     const bool by_list = use_k && k_in <= min(kMaxTopK, (C > 4 ? C * NT / 2 : C * NT) / 2);
 
     // ---- the slice
     const E* logits = static_cast<const E*>(a.logits) + static_cast<int64_t>(row) * a.ld;
-    Slice<E, kStaged> sl;
+    constexpr int kDepth = kStaged ? 8 : (kTable ? 2 : 4);
+    Slice<E, kStaged, kDepth> sl;
     sl.begin = min(a.V, static_cast<int>(rank) * a.slice);
     sl.end = min(a.V, sl.begin + a.slice);
     const int shift_in = static_cast<int>((reinterpret_cast<uintptr_t>(logits + sl.begin) & 15u) / sizeof(E));
@@ -730,7 +733,7 @@ __global__ void __launch_bounds__(NT, (kStaged ? 1024 : 2048) / NT) sample_token
         __syncthreads();
         sl.each_group([&](const uint4& r, int v) {
             float x[kGroup];
-            Slice<E, kStaged>::unpack(r, x);
+            Slice<E, kStaged, kDepth>::unpack(r, x);
             float most = x[0];
 #pragma unroll
             for (int i = 1; i < kGroup; ++i) most = fmaxf(most, x[i]);
@@ -806,7 +809,7 @@ __global__ void __launch_bounds__(NT, (kStaged ? 1024 : 2048) / NT) sample_token
         return s.inv;
     };
 
-    if (by_list) {
+    if constexpr (!kTable) if (by_list) {
         // ---- a bound that at least k entries reach: the k-th largest of the maxima, or a little less, by 256
         // bins of their range in turn
         constexpr int kKeys = kMaxCtas / 2;
@@ -1022,7 +1025,8 @@ __global__ void __launch_bounds__(NT, (kStaged ? 1024 : 2048) / NT) sample_token
     };
 
     Cut cut{-INFINITY, -1};
-    bool counted = false;                        // the border is found and `mine` the mass kept, by counts of values
+    bool counted = false;                        // the border is found, and the mass kept (sum of `mine`), without another pass
+    bool by_counts = false;                      // ... from the numbers of values
     uint32_t kept_ties = 0;                      // of this CTA's entries at the border, where it lies among them
     uint64_t tie_weight = 0;
     uint64_t* table = reinterpret_cast<uint64_t*>(smem + sizeof(SampleShared<NT>));   // kTable: weights of the values that are kept
@@ -1119,7 +1123,7 @@ __global__ void __launch_bounds__(NT, (kStaged ? 1024 : 2048) / NT) sample_token
             cluster_sync();
             const int border = s.bin;
             const float z_cut = border >= 0 ? fmaxf(bin_value(border), zmin) : 0.0f;
-            counted = fabsf(z_cut) >= 0x1p-9f;                               // else among the small numbers: by masses, below
+            counted = by_counts = fabsf(z_cut) >= 0x1p-9f;                   // else among the small numbers: by masses, below
             if (counted) {
                 cut = Cut{z_cut, 0x7fffffff};
                 const uint32_t ties = counts[border], quota = s.quota;
@@ -1144,7 +1148,8 @@ __global__ void __launch_bounds__(NT, (kStaged ? 1024 : 2048) / NT) sample_token
             }
         }
     }
-    if (use_k) cut = narrow(cut, false, static_cast<uint64_t>(k_in));
+    if constexpr (!kTable)
+        if (use_k) cut = narrow(cut, false, static_cast<uint64_t>(k_in));
     if (use_p && !counted) {
         // ---- masses of bins of z, largest first
         __syncthreads();
@@ -1196,6 +1201,9 @@ __global__ void __launch_bounds__(NT, (kStaged ? 1024 : 2048) / NT) sample_token
         cluster_sync();
         const float bin = static_cast<float>(s.bin);
         const uint64_t bin_before = s.bin_before;
+        mine = 0;                                                      // this CTA's mass above the border's bin
+        if constexpr (!kTable)
+            for (int b = tid; b < s.bin; b += NT) mine += wide(s.hist[b]);
         const uint32_t n = collect(-INFINITY, [&](float z, int v) {
             const float b = place_of(z);
             return b >= bin && b < bin + 1.0f && cut.keeps(z, v);
@@ -1204,13 +1212,22 @@ __global__ void __launch_bounds__(NT, (kStaged ? 1024 : 2048) / NT) sample_token
             if (rank == 0) {
                 pack(static_cast<int>(n));
                 const uint64_t last = select(s, static_cast<int>(n), 0, kByMass, limit - bin_before, sc);
+                // and each CTA's mass in the bin
+                if (tid < kMaxCtas) s.sel_mass[tid] = make_uint2(0u, 0u);
+                __syncthreads();
+                for (int i = tid; !kTable && i < static_cast<int>(n); i += NT)
+                    if (s.list[i] >= last) add_wide(&s.sel_mass[list_index(s.list[i]) / a.slice], weight(list_value(s.list[i]), sc, s.pow));
+                __syncthreads();
                 if (tid < C) {
+                    put(&s.border_mass, tid, wide(s.sel_mass[tid]));
                     put(&s.cut_key, tid, static_cast<uint32_t>(last >> 32));
                     put(&s.cut_index, tid, static_cast<uint32_t>(list_index(last)));
                 }
             }
             cluster_sync();
             cut = Cut{key_value(s.cut_key), s.cut_index};
+            counted = !kTable && !(zmin > cut.z);
+            if (tid == 0) mine += s.border_mass;
         } else {
             cut = narrow(cut, true, limit);
         }
@@ -1231,8 +1248,9 @@ __global__ void __launch_bounds__(NT, (kStaged ? 1024 : 2048) / NT) sample_token
     const uint64_t target = min(scaled(u, sum, false), sum - 1);       // u of 1 or more: the last one kept
     uint64_t before = 0;
     for (int c = 0; c < static_cast<int>(rank); ++c) before += s.cta_sum[now][c];
+    bool drawn = false;
     if constexpr (kTable) {
-        if (counted) {
+        if (by_counts) {
             // ---- the draw, every entry's weight from the table; entries equal to the border's value are counted, the first
             // kept_ties of them, in the order of the indices, are kept
             const uint32_t border_bits = kept_ties > 0 ? __float_as_uint(cut.z) >> 16 : 0xffffu;      // (no number)
@@ -1338,11 +1356,12 @@ __global__ void __launch_bounds__(NT, (kStaged ? 1024 : 2048) / NT) sample_token
                 }
             }
             if (probs == nullptr) return;
+            drawn = true;
             __syncthreads();
         }
     }
     if (counted) {                                                     // only the CTA with the border needs its warps' sums
-        const bool here = !kTable && before <= target && target < before + s.cta_sum[now][rank];
+        const bool here = !drawn && before <= target && target < before + s.cta_sum[now][rank];
         if (kept_ties > 0 && (here || probs != nullptr)) {             // the last one kept, in the order of the indices
             uint64_t n = 0;
             sl.each([&](float z, int) { n += z == cut.z ? 1 : 0; });
