@@ -1,8 +1,7 @@
 // dense_mla_shared.cu -- absorbed latent attention of new tokens over the paged latent cache for batches in which groups
 // of requests have their first pages in common (sm_103a).
 //
-// Follows vllm mla/common.py, MLACommonImpl.forward decode branch (_forward_decode) and merge_attn_states, as
-// dense_mla_decode.cu does; the mathematics is the same.
+// Mathematics of dense_mla_decode.cu: per row o = sum_k 2^(s_k - m) v_k / sum_k 2^(s_k - m), in one pass with a running m.
 //
 // Work: the query tokens of a group in units of 256 rows (heads x tokens, tokens of several requests one after the
 // other).  A unit's keys are the pages of the prefix, which all of its rows see, then the pages that each of its
@@ -23,13 +22,18 @@
 // product reaches on this GPU (81 %); more stages, more buffers for P or two groups of softmax warps in turn change nothing.
 // Behind the prefix a tile costs the same for the few rows that see it.
 //
-// Measured (calls in a captured graph, one new token): 200 requests of 16 heads behind 131008 common keys 630 us (1.46
-// PFLOP/s of what is needed, 76 % of the measured rate; the plain call, by its rate at 8 x 128K x 2 rows, about 4.3 ms), 64 of 16
-// heads behind 32768 with 64 to 4096 of their own 107 us, 32 of 128 heads behind 16384 121 us, 60 of 32 heads with two
-// rows behind 5 prefixes of 2K to 32K 99 us, 4 of 16 heads behind 1024 24 us (a chain of about 20 steps).  144 of 152 SMs: clusters of
-// four do not fill a GPC whose SMs are no multiple of four.
+// Measured (calls in a captured graph; in brackets the plain call on the same batch):
+//   200 requests of 16 heads behind 131008 common keys            640 us (3780)   1.44 PFLOP/s of what is needed, 75 % of
+//                                                                                 the measured rate
+//   64 of 16 heads behind 32768, with 64 to 4096 of their own     107 us (327)
+//   60 of 32 heads, two rows each, behind 5 of 2K to 32K           97 us (99)
+//   32 of 128 heads behind 16384                                  118 us (116)    a request fills a tile by itself
+//   4 of 16 heads behind 1024                                      24 us (21)     a chain of about 20 steps
+// So it is for many requests of few heads behind one long prefix; prefixes that the L2 holds cost the plain call little where
+// its own row tiles are full.  144 of 152 SMs: clusters of four do not fill a GPC whose SMs are no multiple of four.
 //
-// Roles (384 threads), warps 10 and 11 idle; "leader": the pair's even rank, whose MMA warp issues for both:
+// Roles (384 threads; warp 10 of each rank finds the units for the others, warp 11 is idle); "leader": the pair's even
+// rank, whose MMA warp issues for both:
 //   score pair  warps 0-7  softmax: rows (tensor-memory lanes) 32 (w % 4) .. + 31, page w / 4 of the tile; queries
 //                          into tensor memory (value dims) and shared memory (rope dims);
 //               warp 8     TMA: the rank's page, 9 chunks of 64 dims a tile;
@@ -64,16 +68,18 @@ constexpr int kQRopeBytes = kRows * 128;                        // 16384
 constexpr int kPOffset = kKStages * kKStageBytes + kQRopeBytes; // P at the same place in all ranks
 constexpr int kDataBytes = kPOffset + kPBufs * kPBytes;
 static_assert(kVStages * kVStageBytes <= kPOffset, "value stages");
-constexpr int kTmaWarp = 8, kMmaWarp = 9;
+constexpr int kTmaWarp = 8, kMmaWarp = 9, kWalkWarp = 10;
+constexpr int kReaders = 10;                                    // warps that walk the pieces: 0 - 9
+constexpr int kPieces = 3, kUnitTokens = 16;                    // pieces known ahead; tokens of a unit
 constexpr int kThreads = 384;
 constexpr uint32_t kColS = 256;                                 // scores: score tiles, behind the query chunks
 constexpr int kMinShare = 2;
-constexpr int kUnitCost = 8;                                    // tiles that the change to another unit takes as long as (0: b64 119 us,
-                                                                // 4: 107; b32 x 128 heads 4: 124, 8: 121, 12: 123),
+constexpr int kUnitCost = 8;                                    // tiles that the change to another unit takes as long as (64 requests 0: 119 us,
+                                                                // 4: 107; 32 requests of 128 heads 4: 124, 8: 121, 12: 123),
 constexpr int kLongShare = 8;                                   // counted in shares of this many tiles or more
 constexpr int kAhead = 2;                                       // tiles between a page's prefetch and its copy
 constexpr int kMaxRequests = 16384, kMaxGroups = 8192, kMaxUnits = 16384;   // units of 256 rows
-constexpr size_t kBarBytes = 6144;
+constexpr size_t kBarBytes = 7168;
 constexpr size_t kSmem = 1024 + size_t(kDataBytes) + kBarBytes;
 static_assert(kSmem <= 232448, "shared-memory budget");
 static_assert((kMaxUnits + kMaxGroups + 3) * 4 <= kDataBytes, "schedule scratch");
@@ -83,6 +89,16 @@ struct Share {
     int unit, at, left;     // first unit, where in it, length of the share
     int first;              // the cluster that holds the first piece of the first unit
     int cost;               // length of a unit in front of its tiles
+};
+
+// A piece of a share: the key tiles [t0, t1) of a unit (t0 == t1: a unit that sees nothing), and per token of the unit its
+// request, the first of that request's pages among the unit's, how many (at the request's last token, else 0), and the keys
+// it sees of the prefix and behind it.
+struct Piece {
+    int q0, nq, prefix, b0, pages, t0, t1;
+    int whole, first;      // the piece is its whole unit; the share's first piece
+    int end;               // no piece: the share is done
+    int b[kUnitTokens], at[kUnitTokens], n[kUnitTokens], seen[kUnitTokens], own[kUnitTokens];
 };
 
 struct Bars {
@@ -110,7 +126,10 @@ struct Bars {
     uint64_t fin_full;                      // 1 / l arrived (armed + bytes), per unit
     uint64_t stage_lent;                    // kLent ring stages are free for the output, per unit
     uint64_t stage_back;                    // ... and no longer read (8 row warps)
+    uint64_t piece_full[kPieces], piece_free[kPieces];
+    int stop;                               // a wait ran out somewhere in the CTA
     uint32_t tmem_slot;
+    Piece piece[kPieces];
     int tile_ok[kInfo];                     // bit i: page i of the tile is there and its id valid
     Share share;
     float tmax[2][2][kRows];                // [tile parity][key half][row]: maximum of the tile
@@ -231,19 +250,17 @@ __device__ __forceinline__ int unit_segments(const Batch& bt, const Unit& u, Tok
 // Key tiles of a unit in the schedule: one that sees nothing counts as one.
 __device__ __forceinline__ int schedule_tiles(int pages) { return max(1, (pages + 1) / 2); }
 
-// A share's pieces, one unit after the other; every role walks them by itself (whole warps).
+// A share's pieces, one unit after the other (a whole warp).
 struct Walk {
     Batch bt;
     int i, left;           // unit, tiles left in the share
     Unit u;
     int pages, tiles;      // of the unit
-    int t0, t1;            // key tiles [t0, t1) of the piece (t0 == t1: a unit that sees nothing)
-    bool whole, first;     // the piece is its whole unit; the share's first piece
+    int t0, t1;
+    bool whole, first;
     bool nothing;          // no piece at all
     int at, cost;          // where in the unit's length the share is; what of that comes in front of its tiles
-    // lane j: token j's request, the first of that request's pages among the unit's, how many (at the request's last
-    // token, else 0), and the keys it sees
-    Token tok;
+    Token tok;             // lane j: token j's (see Piece)
     int seg_at, seg_pages;
 
     __device__ Walk(const Batch& batch, const Share& s) : bt(batch) {
@@ -270,22 +287,6 @@ struct Walk {
         t1 = min(max(0, at + take - cost), tiles);
         nothing = at + take <= cost;                             // the share ends before the first tile
     }
-    // Tokens of one rank's row tile
-    __device__ int tokens(int side) const { return max(0, min(bt.per, u.nq - side * bt.per)); }
-    // Page `at` of the unit's keys (whole warp, `at` may differ): its entry in the block table, and how many of its rows count.
-    __device__ int64_t page_entry(int at, int& valid) const {
-        int64_t entry = static_cast<int64_t>(u.b0) * bt.max_pages + at;
-        valid = kPage;
-        for (int j = 0; j < u.nq; ++j) {
-            const int b = __shfl_sync(0xffffffffu, tok.b, j), n = __shfl_sync(0xffffffffu, seg_pages, j),
-                      from = __shfl_sync(0xffffffffu, seg_at, j), own = __shfl_sync(0xffffffffu, tok.own, j);
-            if (at >= from && at < from + n) {
-                entry = static_cast<int64_t>(b) * bt.max_pages + u.prefix / kPage + (at - from);
-                valid = min(kPage, own - (at - from) * kPage);
-            }
-        }
-        return entry;
-    }
     // false: the share is done
     __device__ bool next() {
         if (left <= 0) return false;
@@ -297,6 +298,60 @@ struct Walk {
         } while (u.nq == 0);
         set_piece();
         return !nothing;
+    }
+};
+
+// The pieces as the other warps read them.  One warp finds them for all: with that code inlined in every role, each role
+// fetched its own copy at the first piece (5 prefixes, 32 heads: 98 -> 96.5 us; 32 requests of 16K keys, 128 heads: 120 -> 118.5).
+struct Reader {
+    Bars& bar;
+    int per;
+    uint32_t n = 0;        // pieces read
+    bool late = false;     // a wait ran out
+    int q0 = 0, nq = 0, prefix = 0, pages = 0, t0 = 0, t1 = 0;      // (no rows, if the first wait runs out)
+    bool whole = false, first = false;
+
+    __device__ Reader(Bars& b, int per_) : bar(b), per(per_) { load(); }
+    __device__ const Piece& piece() const { return bar.piece[n % kPieces]; }
+    __device__ bool load() {
+        if (!ptx::mbar_wait(&bar.piece_full[n % kPieces], (n / kPieces) & 1u, ptx::wait_deadline())) late = true;
+        late = __any_sync(0xffffffffu, late);
+        if (late) return false;
+        const Piece& p = piece();
+        if (uniform(p.end) != 0) return false;
+        q0 = uniform(p.q0);
+        nq = uniform(p.nq);
+        prefix = uniform(p.prefix);
+        pages = uniform(p.pages);
+        t0 = uniform(p.t0);
+        t1 = uniform(p.t1);
+        whole = uniform(p.whole) != 0;
+        first = uniform(p.first) != 0;
+        return true;
+    }
+    // false: the share is done
+    __device__ bool next() {
+        __syncwarp();
+        if ((threadIdx.x & 31) == 0) ptx::mbar_arrive(&bar.piece_free[n % kPieces]);
+        ++n;
+        return load();
+    }
+    // Tokens of one rank's row tile
+    __device__ int tokens(int side) const { return max(0, min(per, nq - side * per)); }
+    // Page `at` of the unit's keys: its entry in the block table, and how many of its rows count.
+    __device__ int64_t page_entry(int max_pages, int at, int& valid) const {
+        const Piece& p = piece();
+        int64_t entry = static_cast<int64_t>(p.b0) * max_pages + at;
+        valid = kPage;
+#pragma unroll 1
+        for (int j = 0; j < nq; ++j) {
+            const int from = p.at[j], n_of = p.n[j];
+            if (at >= from && at < from + n_of) {
+                entry = static_cast<int64_t>(p.b[j]) * max_pages + prefix / kPage + (at - from);
+                valid = min(kPage, p.own[j] - (at - from) * kPage);
+            }
+        }
+        return entry;
     }
 };
 
@@ -491,6 +546,11 @@ dense_mla_shared_kernel(const __grid_constant__ Maps maps, const uint16_t* __res
             ptx::mbar_init(&bar.q_read[s], 2);
         }
         ptx::mbar_init(&bar.lead_pass, 1);
+        for (int i = 0; i < kPieces; ++i) {
+            ptx::mbar_init(&bar.piece_full[i], 1);
+            ptx::mbar_init(&bar.piece_free[i], kReaders);
+        }
+        bar.stop = 0;
         ptx::mbar_init(&bar.q_full, 16);
         for (int i = 0; i < kSBufs; ++i) {
             ptx::mbar_init(&bar.s_full[i], 1);
@@ -528,13 +588,13 @@ dense_mla_shared_kernel(const __grid_constant__ Maps maps, const uint16_t* __res
     const uint32_t ring_addr = ptx::smem_addr(ring);
     const int pair_id = 2 * cluster + side;
     // workspace slot of a piece that is not a whole unit: 2 c for the one that starts share c but not its unit, else 2 c + 1
-    auto piece_slot = [&](const Walk& w) { return 2 * static_cast<int64_t>(pair_id) + ((w.first && w.t0 > 0) ? 0 : 1); };
+    auto piece_slot = [&](const Reader& w) { return 2 * static_cast<int64_t>(pair_id) + ((w.first && w.t0 > 0) ? 0 : 1); };
     if (threadIdx.x == 0 && !scores) meta[pair_id].rows = 0;
 
     if (work && warp == kTmaWarp) {
         // ---------------------------------------------------------------- TMA (all ranks)
         const uint32_t stages = scores ? kKStages : kVStages;
-        Walk w(bt, bar.share);
+        Reader w(bar, bt.per);
         uint32_t s = 0, ph = 0, used = 0, u = 0;                     // stage, its phase, stages used so far, tiles
         auto stage = [&]() {                                         // the next stage is free (whole warp)
             if (!ptx::mbar_wait(&bar.kv_empty[s], ph ^ 1u, deadline)) timed_out = true;
@@ -558,13 +618,13 @@ dense_mla_shared_kernel(const __grid_constant__ Maps maps, const uint16_t* __res
                         if (leader) ptx::mbar_arrive(&bar.kv_full[s]);   // no keys in it: the stage's phase passes first
                         ptx::mbar_arrive_expect_tx(&bar.q_land[c], kKStageBytes);
                         ptx::tma_load_3d(ring + s * kKStageBytes, &maps.q, &bar.q_land[c], (c >> 1) * 64, 0,
-                                         (w.u.q0 + side * bt.per) * bt.H + (c & 1) * 64);
+                                         (w.q0 + side * bt.per) * bt.H + (c & 1) * 64);
                     }
                     advance();
                 }
             auto load_pages = [&](int t, int& valid) {               // page ids of 16 tiles from t on
                 const int at = 2 * t + lane;
-                const int64_t entry = w.page_entry(at, valid);
+                const int64_t entry = w.page_entry(bt.max_pages, at, valid);
                 return at < 2 * w.t1 && at < w.pages ? __ldg(block_table + entry) : -1;
             };
             int valid = 0, valid_next = 0;
@@ -655,6 +715,7 @@ dense_mla_shared_kernel(const __grid_constant__ Maps maps, const uint16_t* __res
                 }
             }
         } while (!timed_out && w.next());
+        timed_out |= w.late;
         // copies still in flight land before the cluster may leave (bounded): the leader sees both ranks'
         if (leader)
             for (uint32_t j = used > stages ? used - stages : 0; j < used; ++j)
@@ -669,7 +730,7 @@ dense_mla_shared_kernel(const __grid_constant__ Maps maps, const uint16_t* __res
         auto wait = [&](uint64_t* b, uint32_t parity) {
             if (!ptx::mbar_wait(b, parity, deadline)) late = true;
         };
-        Walk w(bt, bar.share);
+        Reader w(bar, bt.per);
         uint32_t u = 0, seg = 0, s = 0, ph = 0;
         do {
             if (w.t0 >= w.t1) continue;
@@ -716,10 +777,10 @@ dense_mla_shared_kernel(const __grid_constant__ Maps maps, const uint16_t* __res
                 if (__any_sync(0xffffffffu, late)) break;
             }
         } while (!__any_sync(0xffffffffu, late) && w.next());
-        if (late) timed_out = true;
+        if (late || w.late) timed_out = true;
     } else if (work && warp == kMmaWarp && scores) {
         // ---------------------------------------------------------------- the other score rank: its query stages given back
-        Walk w(bt, bar.share);
+        Reader w(bar, bt.per);
         uint32_t seg = 0, s = 0;
         do {
             if (w.t0 >= w.t1) continue;
@@ -735,6 +796,7 @@ dense_mla_shared_kernel(const __grid_constant__ Maps maps, const uint16_t* __res
             ++seg;
             s = (s + 9u * static_cast<uint32_t>(w.t1 - w.t0)) % kKStages;
         } while (!timed_out && w.next());
+        timed_out |= w.late;
     } else if (work && warp == kMmaWarp && leader) {
         // ---------------------------------------------------------------- MMA: O += P V, for both ranks
         constexpr uint32_t idesc = ptx::instr_desc(1, 1, 2 * kRows, 256) | (1u << 16);   // B MN-major
@@ -744,7 +806,7 @@ dense_mla_shared_kernel(const __grid_constant__ Maps maps, const uint16_t* __res
         auto wait = [&](uint64_t* b, uint32_t parity) {
             if (!ptx::mbar_wait(b, parity, deadline)) late = true;
         };
-        Walk w(bt, bar.share);
+        Reader w(bar, bt.per);
         uint32_t u = 0, seg = 0, s = 0, ph = 0;
         do {
             if (w.t0 >= w.t1) continue;
@@ -795,14 +857,14 @@ dense_mla_shared_kernel(const __grid_constant__ Maps maps, const uint16_t* __res
             }
             ++seg;
         } while (!__any_sync(0xffffffffu, late) && w.next());
-        if (late) timed_out = true;
+        if (late || w.late) timed_out = true;
     } else if (work && warp == kMmaWarp) {
         // ---------------------------------------------------------------- the other value rank: its P for the leader
         auto wait = [&](uint64_t* b, uint32_t parity) {
             if (!ptx::mbar_wait(b, parity, deadline)) timed_out = true;
         };
         const uint32_t there = map_to_rank(ptx::smem_addr(&bar.p_peer[0]), leader_cta);
-        Walk w(bt, bar.share);
+        Reader w(bar, bt.per);
         uint32_t u = 0, seg = 0, s = 0;
         do {
             if (w.t0 >= w.t1) continue;
@@ -831,6 +893,7 @@ dense_mla_shared_kernel(const __grid_constant__ Maps maps, const uint16_t* __res
             }
             ++seg;
         } while (!timed_out && w.next());
+        timed_out |= w.late;
     } else if (work && warp < kTmaWarp && scores) {
         // ---------------------------------------------------------------- softmax (score pair)
         const int quad = warp & 3, kh = warp >> 2;
@@ -851,7 +914,7 @@ dense_mla_shared_kernel(const __grid_constant__ Maps maps, const uint16_t* __res
             if (!ptx::mbar_wait(b, parity, deadline)) timed_out = true;
         };
         uint32_t u = 0, seg = 0, meets = 0, used = 0;                // meets: uses of the pair barrier; used: ring stages
-        Walk w(bt, bar.share);
+        Reader w(bar, bt.per);
         do {
             const int live = w.tokens(side) * bt.H;
             const bool quad_live = quad * 32 < live;
@@ -859,10 +922,9 @@ dense_mla_shared_kernel(const __grid_constant__ Maps maps, const uint16_t* __res
             // of them, but zeros there let the tensor cores idle, and a long call runs at the power limit
             const bool row_live = row < live;
             // the row's keys: [0, seen) of the prefix's pages, [lo, hi) of those behind
-            const int from_token = min(token, 31);
-            int seen = __shfl_sync(0xffffffffu, w.tok.seen, from_token);
-            const int lo = __shfl_sync(0xffffffffu, w.seg_at, from_token) * kPage;
-            const int own = __shfl_sync(0xffffffffu, w.tok.own, from_token);
+            const Piece& piece = w.piece();
+            int seen = piece.seen[token];
+            const int lo = piece.at[token] * kPage, own = piece.own[token];
             const int hi = row_live ? lo + own : lo;
             if (!row_live) seen = 0;
             float m_run = -INFINITY, l_run = 0.0f;
@@ -923,7 +985,7 @@ dense_mla_shared_kernel(const __grid_constant__ Maps maps, const uint16_t* __res
                     ptx::tmem_ld_32x32b_x32(sa, v[0]);
                     ptx::tmem_ld_32x32b_x32(sa + 32, v[1]);
                     const int at = t * kKeys + kh * kPage;           // the page's first position in the unit's keys
-                    const bool behind = at >= w.u.prefix;
+                    const bool behind = at >= w.prefix;
                     const int from = behind ? lo - at : 0;           // the row's: [from, lim)
                     const int lim = ((bar.tile_ok[u % kInfo] >> kh) & 1) ? (behind ? hi : seen) - at : 0;
                     ptx::tmem_wait_ld();
@@ -1019,11 +1081,12 @@ dense_mla_shared_kernel(const __grid_constant__ Maps maps, const uint16_t* __res
                 if (kh == 0 && row < live) {
                     const float lse2 = l_tot == 0.0f ? -INFINITY : m_run * cs + log2f(l_tot);
                     if (!w.whole) part_lse[piece_slot(w) * slot_rows + row] = lse2;
-                    else if (lse_out != nullptr) lse_out[static_cast<int64_t>(w.u.q0 + side * bt.per) * bt.H + row] = lse2 * kLn2;
+                    else if (lse_out != nullptr) lse_out[static_cast<int64_t>(w.q0 + side * bt.per) * bt.H + row] = lse2 * kLn2;
                 }
             }
             if (w.t0 < w.t1) ++seg;
         } while (w.next());
+        timed_out |= w.late;
         // the value pair's last signals land here before this CTA may finish
         for (uint32_t j = 2 * u > kPBufs ? 2 * u - kPBufs : 0; j < 2 * u && !timed_out; ++j)
             wait(&bar.p_free[j % kPBufs], (j / kPBufs) & 1u);
@@ -1039,10 +1102,10 @@ dense_mla_shared_kernel(const __grid_constant__ Maps maps, const uint16_t* __res
         uint32_t clean = 0;                                          // bit i: this row group's P is zero in buffers 2 i and 2 i + 1
         const uint32_t free_there = map_to_rank(ptx::smem_addr(&bar.o_free), leader_cta);
         const uint32_t fin_free_there = map_to_rank(ptx::smem_addr(&bar.fin_free), static_cast<uint32_t>(side));
-        Walk w(bt, bar.share);
+        Reader w(bar, bt.per);
         do {
             const int live = w.tokens(side) * bt.H;
-            const int64_t out_row = static_cast<int64_t>(w.u.q0 + side * bt.per) * bt.H;
+            const int64_t out_row = static_cast<int64_t>(w.q0 + side * bt.per) * bt.H;
             const bool quad_live = quad * 32 < live, has_tiles = w.t0 < w.t1;
             const uint32_t quads = static_cast<uint32_t>((live + 31) / 32);
             for (int t = w.t0; t < w.t1; ++t, ++u) {
@@ -1174,12 +1237,56 @@ dense_mla_shared_kernel(const __grid_constant__ Maps maps, const uint16_t* __res
                         make_uint4(0u, 0u, 0u, 0u);
             }
             // the last piece of a split unit: the combine kernel finds it here
-            if (threadIdx.x == 0 && w.first && w.t0 > 0 && w.t1 == w.tiles && live > 0)
+            if (threadIdx.x == 0 && w.first && w.t0 > 0 && w.t1 == (w.pages + 1) / 2 && live > 0)
                 meta[pair_id] = Meta{out_row, live, bar.share.first};
         } while (w.next());
+        timed_out |= w.late;
         if (lane == 0) bulk_wait_all();                              // written before the CTA leaves
     }
-    if (timed_out) raise_error(err, DSA_DEVERR_TIMEOUT);
+    if (work && warp == kWalkWarp) {
+        // ---------------------------------------------------------------- the pieces, for all other warps
+        Walk w(bt, bar.share);
+        bool more = true;
+        for (uint32_t n = 0;; ++n) {
+            const uint32_t i = n % kPieces;
+            // (a piece may take long: the others' waits are limited, and tell when one has run out)
+            bool free = n < kPieces;
+            for (int tries = 0; tries < 64 && !free && *static_cast<volatile int*>(&bar.stop) == 0; ++tries)
+                free = ptx::mbar_wait(&bar.piece_free[i], ((n / kPieces) & 1u) ^ 1u, ptx::wait_deadline());
+            if (!__all_sync(0xffffffffu, free)) {
+                timed_out = true;
+                break;
+            }
+            Piece& p = bar.piece[i];
+            if (lane < kUnitTokens) {
+                p.b[lane] = w.tok.b;
+                p.at[lane] = w.seg_at;
+                p.n[lane] = w.seg_pages;
+                p.seen[lane] = w.tok.seen;
+                p.own[lane] = w.tok.own;
+            }
+            if (lane == 0) {
+                p.q0 = w.u.q0;
+                p.nq = w.u.nq;
+                p.prefix = w.u.prefix;
+                p.b0 = w.u.b0;
+                p.pages = w.pages;
+                p.t0 = w.t0;
+                p.t1 = w.t1;
+                p.whole = w.whole;
+                p.first = w.first;
+                p.end = !more;
+            }
+            __syncwarp();
+            if (lane == 0) ptx::mbar_arrive(&bar.piece_full[i]);
+            if (!more) break;
+            more = w.next();
+        }
+    }
+    if (timed_out) {
+        raise_error(err, DSA_DEVERR_TIMEOUT);
+        *static_cast<volatile int*>(&bar.stop) = 1;
+    }
     ptx::griddep_launch_dependents();
     ptx::tc_fence_before_sync();
     cluster_sync_all();   // the pair's products are done with both tensor memories

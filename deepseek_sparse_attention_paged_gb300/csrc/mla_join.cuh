@@ -98,7 +98,7 @@ __device__ __forceinline__ void join_listed(const float* __restrict__ part_o, co
             list[j] = own;
         }
         __syncthreads();
-        const bool many = total * slot_rows >= nwarps;
+        const bool many = 2 * total * slot_rows >= nwarps;
         int at = first;                                                   // this warp's next task, counted over the list
         for (int li = 0; li < total; ++li) {
             const JoinTask m = list[li];
