@@ -22,6 +22,12 @@
 //     For bf16 the values themselves are the bins, and counts take the place of masses.
 //   * where more entries than fit (2048) come together (ties, a temperature far above 1), or for a larger top-k:
 //     bisection over the 32 bits of z, a pass over the slices each.
+//
+// Measured (calls in a captured graph, bf16): one row of 32000 with top-k 50 and top-p 8.2 us, 64 of 131072 with top-k, top-p
+// and min-p 50 us, 300 of 100003 with top-p alone 84 us (112 where the logits come from DRAM), 256 of 131072 with the
+// probabilities written 75 us: 168 MB in and out at 2.7 TB/s.  Bound: a few rows by the cluster's exchanges (launch, maxima, list,
+// sums: about 1.2 us each) and by the slowest of eight CTAs, many by forming a weight of 30 bits per entry (about 20
+// integer instructions) and by shared-memory atomics for the bins; in no case by the memory.
 #include <float.h>
 
 #include <algorithm>
@@ -41,7 +47,7 @@ constexpr int kMaxTopK = 1024;
 constexpr int kBins = 1024, kBinsPerOctave = 32;
 constexpr int kSelectBins = 256;
 // bf16 numbers from 2^-9 up to 2^7, of both signs, each a bin: 16 octaves of 128; in the middle one for all smaller ones
-constexpr int kOddList = 3072;                 // entries of other values that are listed
+constexpr int kOddList = 3000;                 // entries of other values that are listed
 constexpr int kSide = 16 * 128, kValueBins = 2 * kSide + 1, kFirstBits = (127 - 9) << 7;
 constexpr int kOne = 46;                       // fraction bits of a weight
 constexpr int kSingleRows = 64, kSingleVocab = 2048;   // where a CTA takes a row for itself

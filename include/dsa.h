@@ -666,7 +666,7 @@ dsa_status dsa_dense_mla_decode(const void* q_bf16, const void* kv_pool, int64_t
  * dsa_dense_mla_decode_shared -- dsa_dense_mla_decode for a batch in which groups of requests have their first
  * pages in common (a system prompt, a document, samples of one prompt): a group's keys are read once for the query
  * rows of all its requests, each request's other keys for itself.
- * Source: as dsa_dense_mla_decode; merge_attn_states (vllm mla/common.py) joins the two by log-sum-exp.
+ * Source: as dsa_dense_mla_decode.
  *   The same results as dsa_dense_mla_decode on the same tables, up to the order of sums.  Group g has the requests
  *   [cu_group[g], cu_group[g + 1]); positions < shared_lens[g], whole pages of them, are read through the first
  *   request's row of the block table.  A request of a group sees no more than its own length of the prefix.
@@ -753,8 +753,7 @@ dsa_status dsa_sample_tokens(const void* logits, int64_t ld, int32_t V, int32_t 
 /*
  * dsa_step_tables -- the tables of a step from the requests' lengths: block table, slot mapping, positions, row
  * offsets and lengths, with the pages that the step takes from and gives back to a free stack.
- * Source: vllm mla/common.py, MLACommonMetadataBuilder.build (query_start_loc, seq_lens, block_table and
- * slot_mapping, made on the host there); the source pages leave the pages to the engine.
+ * Source: none on the pages, which leave the pages of a request to the engine.
  *   Request b holds cached_lens[b] tokens in its first page_counts[b] pages and gets q_lens[b] new ones;
  *   q_lens[b] < 0: it ends.  A request's first keep_pages[b] pages are not its own (a shared prefix).
  *   Rows: cu_q[b + 1] - cu_q[b] = n_b = max(q_lens[b], 0), cut where T rows are used up (DSA_DEVERR_INDEX_RANGE).
