@@ -199,6 +199,11 @@ __device__ __forceinline__ int request_of(const Batch& bt, const Unit& u, int r)
     return row_request(bt.cu_q, bt.B, r);
 }
 
+// Keys that query token r, of request b, sees.
+__device__ __forceinline__ int64_t sees_of(const Batch& bt, int b, int r) {
+    const int q0 = token_at(bt, b), nq = max(0, token_at(bt, b + 1) - q0);
+    return static_cast<int64_t>(seq_len(bt, b)) - nq + (r - q0) + 1;
+}
 // A query token of a unit: its request, the keys it sees of the prefix and behind it.
 struct Token {
     int b, seen, own;
@@ -207,8 +212,7 @@ struct Token {
 // b: a request at or before the token's (the one of an earlier token of the unit).
 __device__ __forceinline__ Token token_of(const Batch& bt, const Unit& u, int r, int b) {
     while (b + 1 < bt.B && __ldg(bt.cu_q + b + 1) <= r) ++b;
-    const int q0 = token_at(bt, b), nq = max(0, token_at(bt, b + 1) - q0);
-    const int64_t sees = static_cast<int64_t>(seq_len(bt, b)) - nq + (r - q0) + 1;
+    const int64_t sees = sees_of(bt, b, r);
     const int64_t room = static_cast<int64_t>(bt.max_pages) * kPage - u.prefix;
     Token t;
     t.b = b;
@@ -217,9 +221,20 @@ __device__ __forceinline__ Token token_of(const Batch& bt, const Unit& u, int r,
     t.cut = sees - u.prefix > room;
     return t;
 }
+// A unit's prefix ends with the last page that one of its tokens sees the whole of: what lies behind that may not be there.
+__device__ __forceinline__ int seen_prefix(const Unit& u, int64_t most) {
+    return static_cast<int>(min(static_cast<int64_t>(u.prefix), max(static_cast<int64_t>(0), most) / kPage * kPage));
+}
 // Pages behind the prefix (of each request as many as its last token in the unit sees).
-__device__ __forceinline__ int own_pages(const Batch& bt, const Unit& u, bool& cut) {
-    Token t = token_of(bt, u, u.q0, request_of(bt, u, u.q0));
+__device__ __forceinline__ int own_pages(const Batch& bt, Unit& u, bool& cut) {
+    const int b0 = request_of(bt, u, u.q0);
+    int64_t most = 0;
+    for (int j = 0, b = b0; j < u.nq && most < u.prefix; ++j) {
+        while (b + 1 < bt.B && __ldg(bt.cu_q + b + 1) <= u.q0 + j) ++b;
+        most = max(most, sees_of(bt, b, u.q0 + j));
+    }
+    u.prefix = seen_prefix(u, most);
+    Token t = token_of(bt, u, u.q0, b0);
     int pages = 0;
     cut = t.cut;
     for (int j = 1; j < u.nq; ++j) {
@@ -232,10 +247,16 @@ __device__ __forceinline__ int own_pages(const Batch& bt, const Unit& u, bool& c
 }
 // The same by a warp, a token a lane: lane j's token, the first of its request's pages among the unit's, how many (at the
 // request's last token, else 0).  Returns all of the unit's pages.
-__device__ __forceinline__ int unit_segments(const Batch& bt, const Unit& u, Token& tok, int& seg_at, int& seg_pages) {
+__device__ __forceinline__ int unit_segments(const Batch& bt, Unit& u, Token& tok, int& seg_at, int& seg_pages) {
     const int lane = threadIdx.x & 31;
     tok = Token{-1, 0, 0, false};
-    if (lane < u.nq) tok = token_of(bt, u, u.q0 + lane, request_of(bt, u, u.q0));
+    int b = 0, most = 0;
+    if (lane < u.nq) {
+        b = request_of(bt, u, u.q0 + lane);
+        most = static_cast<int>(max(static_cast<int64_t>(0), min(sees_of(bt, b, u.q0 + lane), static_cast<int64_t>(u.prefix))));
+    }
+    u.prefix = seen_prefix(u, __reduce_max_sync(0xffffffffu, most));
+    if (lane < u.nq) tok = token_of(bt, u, u.q0 + lane, b);
     const int next_b = __shfl_down_sync(0xffffffffu, tok.b, 1);
     seg_pages = lane < u.nq && (lane == u.nq - 1 || next_b != tok.b) ? (tok.own + kPage - 1) / kPage : 0;
     int upto = seg_pages;
@@ -361,7 +382,7 @@ __device__ __forceinline__ void find_share(const Batch& bt, int c, int clusters,
     bool cut = false;
     if (bt.units <= 64) {
         for (int i = threadIdx.x >> 5; i < bt.units; i += kThreads / 32) {
-            const Unit u = unit_of(bt, i);
+            Unit u = unit_of(bt, i);
             Token tok;
             int seg_at, seg_pages;
             const int pages = unit_segments(bt, u, tok, seg_at, seg_pages);
@@ -370,9 +391,10 @@ __device__ __forceinline__ void find_share(const Batch& bt, int c, int clusters,
         }
     } else {
         for (int i = threadIdx.x; i < bt.units; i += kThreads) {
-            const Unit u = unit_of(bt, i);
+            Unit u = unit_of(bt, i);
             bool c = false;
-            sums[i] = u.nq > 0 ? schedule_tiles(u.prefix / kPage + own_pages(bt, u, c)) : 0;
+            const int own = u.nq > 0 ? own_pages(bt, u, c) : 0;
+            sums[i] = u.nq > 0 ? schedule_tiles(u.prefix / kPage + own) : 0;
             cut |= c;
         }
     }

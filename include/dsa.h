@@ -669,9 +669,10 @@ dsa_status dsa_dense_mla_decode(const void* q_bf16, const void* kv_pool, int64_t
  * Source: as dsa_dense_mla_decode.
  *   The same results as dsa_dense_mla_decode on the same tables, up to the order of sums.  Group g has the requests
  *   [cu_group[g], cu_group[g + 1]); positions < shared_lens[g], whole pages of them, are read through the first
- *   request's row of the block table.  A request of a group sees no more than its own length of the prefix.
+ *   request's row of the block table.  A request of a group sees no more than its own length of the prefix, and what
+ *   none of them sees is not read.
  *   Requests outside all groups have nothing in common with others.
- *   An infinite or NaN value in a shared prefix may reach every row of the group.
+ *   An infinite or NaN value in a shared prefix, at a position that a row of the group sees, may reach the others.
  * Arguments: as dsa_dense_mla_decode, and
  *   cu_group       int32 [G + 1], not falling, within [0, B].   shared_lens int32 [G].   Nullable when G = 0.
  *                  G at most 8192; T * H at most 2^22, T * max_pages < 2^30.

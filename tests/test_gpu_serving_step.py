@@ -292,6 +292,18 @@ def test_shared_stale_rows():
     _check_shared(_shared_inputs([(320, [(1, 1), (63, 1), (64, 1), (65, 2), (100, 3)]), (0, [(10, 1)])], 16, 16, stale=math.nan))
 
 
+@pytest.mark.parametrize("n_groups", [1, 70])
+def test_shared_prefix_that_no_request_sees_whole(n_groups):
+    """What lies behind the longest request of a group is not read: pages that are not there, rows that hold NaN."""
+    lens = [540, 100, 448, 541, 1]
+    q, pool, table, seq, q_lens, cu_group, shared = _shared_inputs([(1024, [(n - 1024, 1) for n in lens])] * n_groups, 16, 19)
+    for g in range(n_groups):
+        first = table[5 * g]
+        pool[first[8], 541 - 512:] = math.nan
+        table[5 * g:5 * g + 5, 9:] = -1
+    _check_shared((q, pool, table, seq, q_lens, cu_group, shared))
+
+
 def test_shared_equals_the_plain_call_on_copied_pages():
     """Pages are taken from the first request's row: other rows' entries below the prefix are not read."""
     inp = list(_shared_inputs([(256, [(9, 1)] * 6)], 64, 17))
