@@ -53,6 +53,7 @@ constexpr int kOne = 46;                       // fraction bits of a weight
 constexpr int kSingleRows = 64, kSingleVocab = 2048;   // where a CTA takes a row for itself
 constexpr int kMaxSampleVocab = 1 << 18;       // sums of weights stay below 2^64
 constexpr int kPowBits = 10;
+constexpr int kMaxSmem = 227 * 1024;
 
 // 2^(j / 1024) with kOne - 1 fraction bits, by the exponential series in 62-bit fixed point, and with 31.
 struct PowTable {
@@ -1499,7 +1500,8 @@ extern "C" dsa_status dsa_sample_tokens(const void* logits, int64_t ld, int32_t 
         a.slice = (V + 7) / 8 * 8;
         smem = sizeof(SampleShared<1024>) + kValueBins * sizeof(uint64_t);
     }
-    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)) != cudaSuccess)
+    // (the same limit in every call: another thread's may come between this and the launch)
+    if (smem > kMaxSmem || cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem) != cudaSuccess)
         return DSA_ERR_CUDA;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(R) * ctas);

@@ -1,6 +1,7 @@
 """GPU tests of the calls around a serving step at large sizes and directly behind one another: every page of a long shared
 prefix counts once (dense_mla_marked), batches of many units, order on the stream, large batches of rows to sample."""
 import math
+import threading
 
 import pytest
 import torch
@@ -197,3 +198,33 @@ def test_sample_top_p_rows_in_large_batches(kind):
             assert many[0] == few[0] * n and few[2] == many[2]
             if probs:
                 assert bool((torch.from_numpy(many[1]).view(n, 8, V) == torch.from_numpy(few[1])[None]).all())
+
+
+def test_calls_from_two_threads():
+    """Two threads with sizes that take different amounts of shared memory, a stream each: no call is refused."""
+    sizes = [(3, 200000), (5, 20000)]
+    inputs = [(_logits(R, V, 90 + V % 7, False).cuda(), _f32([0.3, 0.6, 0.9, 0.1, 0.5][:R]), _f32([0.9] * R)) for R, V in sizes]
+    want = []
+    for x, u, p in inputs:
+        tokens = _i32([-5] * x.shape[0])
+        capi.dsa_sample_tokens(x, u, tokens, top_p=p)
+        want.append(tokens.tolist())
+    got = [None, None]
+
+    def work(i):
+        x, u, p = inputs[i]
+        stream = torch.cuda.Stream()
+        outs = [_i32([-5] * x.shape[0]) for _ in range(300)]
+        torch.cuda.synchronize()
+        for out in outs:
+            capi.dsa_sample_tokens(x, u, out, top_p=p, stream=stream)
+        stream.synchronize()
+        got[i] = [o.tolist() for o in outs]
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    for g, w in zip(got, want):
+        assert g == [w] * 300
