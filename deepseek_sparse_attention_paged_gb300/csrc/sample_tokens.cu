@@ -41,7 +41,6 @@ namespace {
 
 constexpr int kMaxCtas = 8;
 constexpr int kList = 2048;                    // entries that the first CTA takes in
-constexpr int kRegion = kList / kMaxCtas;      // of one CTA without a count beforehand
 constexpr int kFew = 128;                      // entries that are compared with one another
 constexpr int kMaxTopK = 1024;
 constexpr int kBins = 1024, kBinsPerOctave = 32;
@@ -93,6 +92,7 @@ struct SampleArgs {
     float* probs;
     int64_t ld_probs;
     int ctas, slice;                           // CTAs of a row, entries of a CTA
+    uint32_t region;                           // part of the list that a CTA has without a count beforehand
     int32_t* err;
 };
 
@@ -396,11 +396,14 @@ struct Slice {
             for (int i = 0; i < kGroup; ++i) x[i] = clean(x[i], most);
         }
     }
-    // The first pass: the largest entry of this thread's; f(group, its index) for each group as it lies in memory.
-    template <typename F>
-    __device__ __forceinline__ float take_in(F f) const {
+    // The first pass: the largest entry of this thread's, in kParts parts; f(group, its index) for each group as it lies in
+    // memory.
+    template <int kParts, typename F>
+    __device__ __forceinline__ void take_in(float (&top)[kParts], F f) const {
         constexpr int kLoads = kDepth;
-        float top = -INFINITY;
+        static_assert(kLoads % kParts == 0, "parts");
+#pragma unroll
+        for (int i = 0; i < kParts; ++i) top[i] = -INFINITY;
         for (int g = g0 + lane; g < g1; g += 32 * kLoads) {
             uint4 r[kLoads];
 #pragma unroll
@@ -423,10 +426,11 @@ struct Slice {
                         data[g + 32 * i] = make_uint4(w[0], w[1], w[2], w[3]);
                     }
 #pragma unroll
-                    for (int e = 0; e < kGroup; ++e) top = fmaxf(top, x[e]);
+                    for (int e = 0; e < kGroup; ++e) top[i % kParts] = fmaxf(top[i % kParts], x[e]);
                 }
         }
-        return fminf(top, most);
+#pragma unroll
+        for (int i = 0; i < kParts; ++i) top[i] = fminf(top[i], most);
     }
     // entries of this lane's group of a step; -infinity past the warp's groups
     __device__ __forceinline__ int read(int step, float (&x)[kGroup]) const {
@@ -600,7 +604,11 @@ __global__ void __launch_bounds__(NT, (kStaged ? 1024 : 2048) / NT) sample_token
     const float u = __ldg(a.u + row);
     const bool greedy = !(temperature > 0.0f);
     const bool use_k = !kTable && k_in > 0 && k_in < a.V, use_p = p_in < 1.0f, use_m = m_in > 0.0f;
-    const bool by_list = use_k && k_in <= min(kMaxTopK, (C > 4 ? C * NT / 2 : C * NT) / 2);
+    // maxima that bound the k-th largest entry: of every thread, of two where there are many, of parts of a thread's entries where
+    // a row has few CTAs
+    constexpr int kParts = kStaged || kTable ? 1 : (sizeof(E) == 4 ? 2 : 4);
+    const int num_maxima = C > 4 ? C * NT / 2 : C * NT * max(1, min(kParts, 4 / C));
+    const bool by_list = use_k && k_in <= min(kMaxTopK, num_maxima / 2);
 
     // ---- the slice
     const E* logits = static_cast<const E*>(a.logits) + static_cast<int64_t>(row) * a.ld;
@@ -644,7 +652,8 @@ __global__ void __launch_bounds__(NT, (kStaged ? 1024 : 2048) / NT) sample_token
         if (tid == 0) s.stage_count = 0;
         __syncthreads();
     }
-    const float top_own = sl.take_in([&](const uint4& r, int v) {
+    float top_part[kParts];
+    sl.take_in(top_part, [&](const uint4& r, int v) {
         if constexpr (kTable)
             if (counting)
                 count_values(r, v, [&](uint32_t, int index) {
@@ -652,6 +661,9 @@ __global__ void __launch_bounds__(NT, (kStaged ? 1024 : 2048) / NT) sample_token
                     if (at < kOddList) odd_list[at] = static_cast<uint32_t>(index);
                 });
     });
+    float top_own = top_part[0];
+#pragma unroll
+    for (int i = 1; i < kParts; ++i) top_own = fmaxf(top_own, top_part[i]);
     for (int i = tid; i < (1 << kPowBits) / 4; i += NT)
         reinterpret_cast<uint4*>(s.pow)[i] = __ldg(reinterpret_cast<const uint4*>(kPow.coarse) + i);
     if (tid == 0) {
@@ -668,7 +680,14 @@ __global__ void __launch_bounds__(NT, (kStaged ? 1024 : 2048) / NT) sample_token
     cluster_wait();
     if (by_list && !greedy) {
         const float two = fmaxf(top_own, __shfl_xor_sync(0xffffffffu, top_own, 1));
-        if (C <= 4)
+        if (kParts > 1 && C < 4) {
+            const int used = min(kParts, 4 / C);
+#pragma unroll
+            for (int i = 0; i < kParts; ++i) {
+                const float part = used == kParts ? top_part[i] : fmaxf(top_part[i], top_part[(i + 2) % kParts]);
+                for (int c = 0; c < C && i < used; ++c) put(&s.maxima[(rank * used + i) * NT + tid], c, __float_as_uint(part));
+            }
+        } else if (C <= 4)
             for (int c = 0; c < C; ++c) put(&s.maxima[rank * NT + tid], c, __float_as_uint(top_own));
         else if ((tid & 1) == 0)
             for (int c = 0; c < C; ++c) put(&s.maxima[(rank * NT + tid) / 2], c, __float_as_uint(two));
@@ -752,7 +771,7 @@ __global__ void __launch_bounds__(NT, (kStaged ? 1024 : 2048) / NT) sample_token
                 const uint32_t at = atomicAdd(&s.stage_count, 1u);
                 const uint64_t e = list_entry(z, v + i);
                 if (at < SampleShared<NT>::kStage) s.stage[at] = e;
-                if (at < kRegion) put(&s.list[rank * kRegion + at], 0u, e);
+                if (at < a.region) put(&s.list[rank * a.region + at], 0u, e);
             }
         });
         __syncthreads();
@@ -766,19 +785,19 @@ __global__ void __launch_bounds__(NT, (kStaged ? 1024 : 2048) / NT) sample_token
             all += m;
             most = max(most, m);
         }
-        packed = most > kRegion;
+        packed = most > a.region;
         if (packed && all <= kList && most <= SampleShared<NT>::kStage) {
             for (uint32_t i = tid; i < n; i += NT) put(&s.list[before + i], 0u, s.stage[i]);
             cluster_sync();
         }
-        return most <= SampleShared<NT>::kStage ? all : kList + 1u;
+        return most <= max(a.region, static_cast<uint32_t>(SampleShared<NT>::kStage)) ? all : kList + 1u;
     };
     // Entry i of the list as it came in
     auto entry = [&](int i) {
         if (packed) return s.list[i];
         int c = 0;
         while (i >= static_cast<int>(s.cta_count[c])) i -= static_cast<int>(s.cta_count[c++]);
-        return s.list[c * kRegion + i];
+        return s.list[c * a.region + i];
     };
     // ... and the whole list without gaps
     auto pack = [&](int n) {
@@ -825,7 +844,7 @@ __global__ void __launch_bounds__(NT, (kStaged ? 1024 : 2048) / NT) sample_token
         uint32_t least = 0xffffffffu, finite = 0;
 #pragma unroll
         for (int c = 0; c < kKeys; ++c) {
-            key[c] = c * NT + tid < (C > 4 ? C * NT / 2 : C * NT) ? order_key(s.maxima[c * NT + tid]) : none;
+            key[c] = c * NT + tid < num_maxima ? order_key(s.maxima[c * NT + tid]) : none;
             if (key[c] != none) {
                 least = min(least, key[c]);
                 ++finite;
@@ -1474,15 +1493,33 @@ extern "C" dsa_status dsa_sample_tokens(const void* logits, int64_t ld, int32_t 
     // 16000 93 -> 51 us, 160 of 32000 31 -> 19; top-p alone: 512 of 16000 174 -> 121, but 120 of 32000 64 -> 77)
     const int64_t enough = (top_k != nullptr ? 4 : 8) * static_cast<int64_t>(device_sm_count());
     if (ctas == 8 && R * static_cast<int64_t>(ctas) > enough && V <= 8 * 8192) ctas = 4;
-    const int slice = ((V + ctas - 1) / ctas + 7) / 8 * 8;
-    const size_t bytes = (static_cast<size_t>(slice) * align + 15) / 16 * 16 + 16;
     // Staged unless most of the work is rows with a top-k, read twice, and there are enough of them to fill the GPU several
     // times: then more CTAs an SM count for more (256 rows of 131072 with k = 50 and probabilities 134 -> 100 us; 64 rows of
     // mixed settings 53 -> 63, 300 with top-p alone 268 -> 361)
-    const bool staged = top_k == nullptr || static_cast<int64_t>(R) * ctas <= 4 * static_cast<int64_t>(device_sm_count());
+    const int64_t slots = 4 * static_cast<int64_t>(device_sm_count());
+    const bool staged = top_k == nullptr || R * static_cast<int64_t>(ctas) <= slots;
+    if (!staged) {
+        // A CTA takes about as long as 16384 entries for what it does besides reading: as many CTAs a row as make the least of
+        // that times the waves.  Not slices whose sum the L2 does not hold, which would be read twice from DRAM (400 rows of
+        // 131072 fp32 with probabilities on four CTAs 104 us, two 119), nor one CTA for fp32, where a thread keeps two
+        // maxima, not four (registers: 256 x 131072 with probabilities 72 -> 74).  With this rule instead of eight CTAs a row:
+        // 300 rows of 131072 bf16 65 -> 34 us, 300 of 32000 33 -> 21, 512 of 16000 54 -> 23, 100 of 131072 fp32 29 -> 22
+        int64_t best = INT64_MAX;
+        const int most = ctas;
+        for (int c = most; c >= std::min(most, bf16 ? 1 : 2); c /= 2) {
+            const int64_t part = (V + c - 1) / c, time = (R * static_cast<int64_t>(c) + slots - 1) / slots * (16384 + part);
+            if (c < most && part * static_cast<int64_t>(align) > 160 * 1024) break;
+            if (time < best) {
+                best = time;
+                ctas = c;
+            }
+        }
+    }
+    const int slice = ((V + ctas - 1) / ctas + 7) / 8 * 8;
+    const size_t bytes = (static_cast<size_t>(slice) * align + 15) / 16 * 16 + 16;
     const bool large = bytes > 40 * 1024 || !staged;
     size_t smem = (staged ? bytes : 0) + (large ? sizeof(SampleShared<512>) : sizeof(SampleShared<256>));
-    SampleArgs a{logits, ld, V, temperature, top_k, top_p, min_p, u, tokens, probs, ld_probs, ctas, slice, dev_err};
+    SampleArgs a{logits, ld, V, temperature, top_k, top_p, min_p, u, tokens, probs, ld_probs, ctas, slice, static_cast<uint32_t>(kList / ctas), dev_err};
     using Kernel = void (*)(SampleArgs);
     // A CTA a row where top-p alone goes by counts of values and there are rows enough: no exchanges between CTAs, and what
     // each CTA does for all values is done once a row (rows x entries: 300 x 100003 135 -> 88 us, 512 x 16000 162 -> 65,

@@ -228,3 +228,28 @@ def test_calls_from_two_threads():
         t.join()
     for g, w in zip(got, want):
         assert g == [w] * 300
+
+
+@pytest.mark.parametrize("V,n,bf16", [(5003, 80, True), (20001, 60, False), (20001, 70, True), (60007, 35, True), (60007, 30, False),
+                                      (131072, 25, False), (100003, 40, True)])
+def test_sample_top_k_rows_in_large_batches(V, n, bf16):
+    """Rows with a top-k in batches that a CTA, or two or four, take a row of: as in a small batch, bit for bit; the largest
+    entries all in one place, evenly spread, equal."""
+    x = _logits(8, V, 95, False)
+    x[0] = x[0].sort(descending=True).values
+    x[1] = x[1].sort().values
+    x[2, 1000:3100] += 20.0
+    x[3] = x[3].round()
+    x[4, ::2] = -math.inf
+    x[5] = 2.5
+    x[6, 600:] = -math.inf
+    if bf16:
+        x = x.to(torch.bfloat16)
+    u = [0.1, 0.9, 0.3, 0.5, 0.7, 0.2, 0.999, 0.4]
+    for kw in (dict(top_k=[1024, 1000, 1023, 20, 513, 7, 700, 1]), dict(top_k=[50, 600, 40, 1024, 1, 1024, 50, 1000], top_p=[0.9] * 4 + [1.0] * 4),
+               dict(top_k=[0, 1025, 50, 0, 5000, 3, 0, 256], top_p=[0.8, 0.9, 0.99, 0.5, 0.95, 1.0, 0.7, 0.6], min_p=[0.0, 0.1] * 4,
+                    temperature=[0.7, 1.0, 0.0, 2.0, 1.0, 1.0, 0.8, 5.0])):
+        few = _run_sample(x, V, u, **kw)
+        many = _run_sample(x.repeat(n, 1), V, u * n, **{k: v * n for k, v in kw.items()})
+        assert many[0] == few[0] * n and few[2] == many[2]
+        assert bool((torch.from_numpy(many[1]).view(n, 8, V) == torch.from_numpy(few[1])[None]).all())
