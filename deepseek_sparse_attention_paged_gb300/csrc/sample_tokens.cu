@@ -1053,6 +1053,8 @@ __global__ void __launch_bounds__(NT, (kStaged ? 1024 : 2048) / NT) sample_token
     Cut cut{-INFINITY, -1};
     bool counted = false;                        // the border is found, and the mass kept (sum of `mine`), without another pass
     bool by_counts = false;                      // ... from the numbers of values
+    bool small = false;                          // the border lies among the numbers below 2^-9: `mine` is the mass above them
+    uint64_t limit = 0;                          // of the mass that top-p keeps
     uint32_t kept_ties = 0;                      // of this CTA's entries at the border, where it lies among them
     uint64_t tie_weight = 0;
     uint64_t* table = reinterpret_cast<uint64_t*>(smem + sizeof(SampleShared<NT>));   // kTable: weights of the values that are kept
@@ -1117,7 +1119,7 @@ __global__ void __launch_bounds__(NT, (kStaged ? 1024 : 2048) / NT) sample_token
             for (int c = 0; c < static_cast<int>(rank); ++c) before += s.cta_sum[now][c];
             for (int w = 0; w < warp; ++w) before += s.warp_sum[now][w];
             before += warp_scan64(mine + rest, lane) - (mine + rest);
-            const uint64_t limit = max(scaled(p_in, mass, true), uint64_t(1));
+            limit = max(scaled(p_in, mass, true), uint64_t(1));
             // the value of the border, and how many of the entries that are equal to it each CTA keeps (in all bins but the
             // two that hold several values)
             if (rest != 0 && before + mine < limit)
@@ -1140,7 +1142,8 @@ __global__ void __launch_bounds__(NT, (kStaged ? 1024 : 2048) / NT) sample_token
                         left -= q;
                         if (c < C) {
                             put(&s.quota, c, q);
-                            put(&s.bin, c, bin != kSide ? static_cast<uint32_t>(bin) : 0xffffffffu);
+                            put(&s.bin, c, bin != kSide ? static_cast<uint32_t>(bin) : 0xfffffffeu);
+                            put(&s.bin_before, c, before);
                         }
                     }
                 }
@@ -1149,7 +1152,14 @@ __global__ void __launch_bounds__(NT, (kStaged ? 1024 : 2048) / NT) sample_token
             cluster_sync();
             const int border = s.bin;
             const float z_cut = border >= 0 ? fmaxf(bin_value(border), zmin) : 0.0f;
-            counted = by_counts = fabsf(z_cut) >= 0x1p-9f;                   // else among the small numbers: by masses, below
+            counted = by_counts = fabsf(z_cut) >= 0x1p-9f;                   // else below
+            small = border == -2;
+            if (small) {
+                mine = 0;
+                for (int b = kSide + 1 + tid; b < kValueBins; b += NT)
+                    if (counts[b] != 0) mine += counts[b] * weight(bin_value(b), sc, s.pow);
+                cluster_sync();                                              // the counts lie where the list does
+            }
             if (counted) {
                 cut = Cut{z_cut, 0x7fffffff};
                 const uint32_t ties = counts[border], quota = s.quota;
@@ -1177,60 +1187,63 @@ __global__ void __launch_bounds__(NT, (kStaged ? 1024 : 2048) / NT) sample_token
     if constexpr (!kTable)
         if (use_k) cut = narrow(cut, false, static_cast<uint64_t>(k_in));
     if (use_p && !counted) {
-        // ---- masses of bins of z, largest first
-        __syncthreads();
-        for (int i = tid; i < kBins; i += NT) s.hist[i] = make_uint2(0u, 0u);
-        if (tid == 0) s.stage_count = 0;
-        __syncthreads();
         const float per_bin = sc.rh * (kBinsPerOctave / 1024.0f);
         auto place_of = [&](float z) { return fminf((sc.top - z) * per_bin, static_cast<float>(kBins - 1)); };
-        sl.each([&](float z, int v) {
-            const uint64_t w = weight(z, sc, s.pow);
-            if (w != 0 && cut.keeps(z, v)) add_wide(&s.hist[static_cast<int>(place_of(z))], w);
-        });
-        cluster_sync();
-        // this CTA's share of the bins: sums over the cluster, then the mass of the share to every CTA
-        const int share = kBins / C, b0 = static_cast<int>(rank) * share;      // C is a power of two
-        uint64_t own[kBins / NT];
-        mine = 0;
-        const int each = (share + NT - 1) / NT;
+        __syncthreads();
+        if (tid == 0) s.stage_count = 0;
+        if (!small) {
+            // ---- masses of bins of z, largest first
+            for (int i = tid; i < kBins; i += NT) s.hist[i] = make_uint2(0u, 0u);
+            __syncthreads();
+            sl.each([&](float z, int v) {
+                const uint64_t w = weight(z, sc, s.pow);
+                if (w != 0 && cut.keeps(z, v)) add_wide(&s.hist[static_cast<int>(place_of(z))], w);
+            });
+            cluster_sync();
+            // this CTA's share of the bins: sums over the cluster, then the mass of the share to every CTA
+            const int share = kBins / C, b0 = static_cast<int>(rank) * share;      // C is a power of two
+            uint64_t own[kBins / NT];
+            mine = 0;
+            const int each = (share + NT - 1) / NT;
 #pragma unroll
-        for (int i = 0; i < kBins / NT; ++i) {
-            own[i] = 0;
-            const int b = tid * each + i;
-            if (i < each && b < share) {
-                uint2 h[kMaxCtas];
+            for (int i = 0; i < kBins / NT; ++i) {
+                own[i] = 0;
+                const int b = tid * each + i;
+                if (i < each && b < share) {
+                    uint2 h[kMaxCtas];
 #pragma unroll
-                for (int c = 0; c < kMaxCtas; ++c) h[c] = c < C ? get2(&s.hist[b0 + b], c) : make_uint2(0u, 0u);
+                    for (int c = 0; c < kMaxCtas; ++c) h[c] = c < C ? get2(&s.hist[b0 + b], c) : make_uint2(0u, 0u);
 #pragma unroll
-                for (int c = 0; c < kMaxCtas; ++c) own[i] += wide(h[c]);
-            }
-            mine += own[i];
-        }
-        const int now = flip;
-        const uint64_t mass = cluster_sum(mine);
-        uint64_t before = 0;
-        for (int c = 0; c < static_cast<int>(rank); ++c) before += s.cta_sum[now][c];
-        for (int w = 0; w < warp; ++w) before += s.warp_sum[now][w];
-        before += warp_scan64(mine, lane) - mine;
-        const uint64_t limit = max(scaled(p_in, mass, true), uint64_t(1));
-        // the bin of the last entry before which less than the limit lies: mass up to it reaches the limit
-#pragma unroll
-        for (int i = 0; i < kBins / NT; ++i) {
-            if (own[i] != 0 && before < limit && before + own[i] >= limit)
-                for (int c = 0; c < C; ++c) {
-                    put(&s.bin, c, static_cast<uint32_t>(b0 + tid * each + i));
-                    put(&s.bin_before, c, before);
+                    for (int c = 0; c < kMaxCtas; ++c) own[i] += wide(h[c]);
                 }
-            before += own[i];
+                mine += own[i];
+            }
+            const int now = flip;
+            const uint64_t mass = cluster_sum(mine);
+            uint64_t before = 0;
+            for (int c = 0; c < static_cast<int>(rank); ++c) before += s.cta_sum[now][c];
+            for (int w = 0; w < warp; ++w) before += s.warp_sum[now][w];
+            before += warp_scan64(mine, lane) - mine;
+            limit = max(scaled(p_in, mass, true), uint64_t(1));
+            // the bin of the last entry before which less than the limit lies: mass up to it reaches the limit
+#pragma unroll
+            for (int i = 0; i < kBins / NT; ++i) {
+                if (own[i] != 0 && before < limit && before + own[i] >= limit)
+                    for (int c = 0; c < C; ++c) {
+                        put(&s.bin, c, static_cast<uint32_t>(b0 + tid * each + i));
+                        put(&s.bin_before, c, before);
+                    }
+                before += own[i];
+            }
+            cluster_sync();
+            mine = 0;                                                      // this CTA's mass above the border's bin
+            if constexpr (!kTable)
+                for (int b = tid; b < s.bin; b += NT) mine += wide(s.hist[b]);
         }
-        cluster_sync();
         const float bin = static_cast<float>(s.bin);
         const uint64_t bin_before = s.bin_before;
-        mine = 0;                                                      // this CTA's mass above the border's bin
-        if constexpr (!kTable)
-            for (int b = tid; b < s.bin; b += NT) mine += wide(s.hist[b]);
-        const uint32_t n = collect(-INFINITY, [&](float z, int v) {
+        const uint32_t n = collect(small ? -0x1p-9f : -INFINITY, [&](float z, int v) {
+            if (small) return fabsf(z) < 0x1p-9f;
             const float b = place_of(z);
             return b >= bin && b < bin + 1.0f && cut.keeps(z, v);
         });
@@ -1241,7 +1254,7 @@ __global__ void __launch_bounds__(NT, (kStaged ? 1024 : 2048) / NT) sample_token
                 // and each CTA's mass in the bin
                 if (tid < kMaxCtas) s.sel_mass[tid] = make_uint2(0u, 0u);
                 __syncthreads();
-                for (int i = tid; !kTable && i < static_cast<int>(n); i += NT)
+                for (int i = tid; (!kTable || small) && i < static_cast<int>(n); i += NT)
                     if (s.list[i] >= last) add_wide(&s.sel_mass[list_index(s.list[i]) / a.slice], weight(list_value(s.list[i]), sc, s.pow));
                 __syncthreads();
                 if (tid < C) {
@@ -1252,7 +1265,7 @@ __global__ void __launch_bounds__(NT, (kStaged ? 1024 : 2048) / NT) sample_token
             }
             cluster_sync();
             cut = Cut{key_value(s.cut_key), s.cut_index};
-            counted = !kTable && !(zmin > cut.z);
+            counted = (!kTable || small) && !(zmin > cut.z);
             if (tid == 0) mine += s.border_mass;
         } else {
             cut = narrow(cut, true, limit);

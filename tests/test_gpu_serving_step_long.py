@@ -3,13 +3,14 @@ prefix counts once (dense_mla_marked), batches of many units, order on the strea
 import math
 import threading
 
+import numpy as np
 import pytest
 import torch
 
 import dense_mla_marked as marked
 import dense_mla_ref
 from deepseek_sparse_attention_paged_gb300 import capi
-from test_gpu_serving_step import SCALE, _check_shared, _cum, _err, _f32, _i32, _logits, _run_sample, _shared_inputs
+from test_gpu_serving_step import SCALE, _check_sample, _check_shared, _cum, _err, _f32, _i32, _logits, _run_sample, _shared_inputs
 
 pytestmark = pytest.mark.gpu
 
@@ -253,3 +254,38 @@ def test_sample_top_k_rows_in_large_batches(V, n, bf16):
         many = _run_sample(x.repeat(n, 1), V, u * n, **{k: v * n for k, v in kw.items()})
         assert many[0] == few[0] * n and few[2] == many[2]
         assert bool((torch.from_numpy(many[1]).view(n, 8, V) == torch.from_numpy(few[1])[None]).all())
+
+
+@pytest.mark.parametrize("kind", ["distinct", "zeros", "equal"])
+def test_sample_top_p_border_among_small_numbers(kind):
+    """bf16 rows whose top-p ends within a few hundred numbers next to 0: in the middle of an entry's weight, so that the
+    rounding of top_p decides nothing."""
+    R, V, n = 8, 20003, 10
+    g = torch.Generator().manual_seed(100 + len(kind))
+    x = 2.0 * torch.randn(R, V, generator=g)
+    x[:, 5::37] = {"distinct": 5e-4, "zeros": 1e-3, "equal": 1e-9}[kind] * torch.randn(R, len(range(5, V, 37)), generator=g)
+    if kind == "zeros":
+        x[:, 5::74] = 0.0
+        x[:, 42::148] = -0.0
+    elif kind == "equal":
+        x[:, 5::37] = 2.0 ** -12
+    x = x.to(torch.bfloat16)
+    t = [1.0, 0.7, 1.5, 1.0, 3.0, 20.0, 1.2, 1.0]
+    p = []
+    for r in range(R):
+        z = x[r].double().numpy()
+        z = np.sort(z)[::-1]
+        w = np.exp((z - z[0]) / np.float32(t[r]).astype(np.float64))
+        small = np.flatnonzero(np.abs(z) < 2.0 ** -9)
+        at = small[(7 * r + 3) * len(small) // 64]
+        p.append(float((w[:at].sum() + 0.5 * w[at]) / w.sum()))
+    u = torch.rand(R, generator=g).tolist()
+    u[7] = 0.9999999
+    for kw in (dict(top_p=p, temperature=t), dict(top_p=p, temperature=t, min_p=[0.0, 1e-9, 0.5, 0.0, 1e-6, 0.0, 0.9, 1e-30])):
+        _check_sample(x, V, u, **kw)
+        few = _run_sample(x, V, u, **kw)
+        for probs in (True, False):
+            many = _run_sample(x.repeat(n, 1), V, u * n, probs=probs, **{k: v * n for k, v in kw.items()})
+            assert many[0] == few[0] * n and few[2] == many[2]
+            if probs:
+                assert bool((torch.from_numpy(many[1]).view(n, R, V) == torch.from_numpy(few[1])[None]).all())
