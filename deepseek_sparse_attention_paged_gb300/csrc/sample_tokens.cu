@@ -15,7 +15,8 @@
 // A row is split over the CTAs of a cluster, each with a slice of it in shared memory: logits are read from global
 // memory once.
 //   * top-k up to 1024: the k-th largest of the maxima of all threads (or pairs of them) is a bound from below that few more
-//     than k entries pass (with G maxima about -G ln(1 - k / G)); those go to the first CTA, which does the rest alone.
+//     than k entries pass (with G maxima about -G ln(1 - k / G)).  Only the threads whose own maximum reaches it look at their
+//     entries again; those that pass go to the first CTA, which does the rest alone.
 //   * top-p without top-k: masses of 1024 bins of z (32 an octave of w) find the bin of the border; its entries
 //     go to the first CTA, which finds the last one kept.  With that the masses say what each CTA keeps, and the one
 //     that the random number falls to looks for the token in a second pass.
@@ -23,11 +24,12 @@
 //   * where more entries than fit (2048) come together (ties, a temperature far above 1), or for a larger top-k:
 //     bisection over the 32 bits of z, a pass over the slices each.
 //
-// Measured (calls in a captured graph, bf16): one row of 32000 with top-k 50 and top-p 8.2 us, 64 of 131072 with top-k, top-p
-// and min-p 50 us, 300 of 100003 with top-p alone 84 us (112 where the logits come from DRAM), 256 of 131072 with the
-// probabilities written 75 us: 168 MB in and out at 2.7 TB/s.  Bound: a few rows by the cluster's exchanges (launch, maxima, list,
-// sums: about 1.2 us each) and by the slowest of eight CTAs, many by forming a weight of 30 bits per entry (about 20
-// integer instructions) and by shared-memory atomics for the bins; in no case by the memory.
+// Measured (calls in a captured graph): one row of 32000 (bf16) with top-k 50 and top-p 8.2 us, 64 of 131072 (fp32) with
+// top-k, top-p and min-p, a setting each, 49 us, 300 of 100003 (bf16) with top-p alone 84 us, 256 of 131072 (fp32) with top-k 50
+// and the probabilities written 66 us: 268 MB at 4.1 TB/s.  Bound: a few rows by the cluster's exchanges (launch, maxima, list,
+// sums: about 1.2 us each) and by the slowest of eight CTAs; many rows with a top-k by the memory while all CTAs read and
+// by latency while all select; top-p alone by forming a weight of 30 bits per entry (about 20 integer instructions) and by
+// shared-memory atomics for the bins.
 #include <float.h>
 
 #include <algorithm>
@@ -715,7 +717,7 @@ __global__ void __launch_bounds__(NT, (kStaged ? 1024 : 2048) / NT) sample_token
         const int n = sl.end - sl.begin;
         if (vec) {
             for (int i = tid; i < n / 4; i += NT)
-                *reinterpret_cast<float4*>(probs + sl.begin + 4 * i) = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                __stcs(reinterpret_cast<float4*>(probs + sl.begin + 4 * i), make_float4(0.0f, 0.0f, 0.0f, 0.0f));
             for (int i = n / 4 * 4 + tid; i < n; i += NT) probs[sl.begin + i] = 0.0f;
         } else {
             for (int i = tid; i < n; i += NT) probs[sl.begin + i] = 0.0f;
@@ -754,10 +756,12 @@ __global__ void __launch_bounds__(NT, (kStaged ? 1024 : 2048) / NT) sample_token
     // that is at most kList and no CTA has more than its stage holds (else kList + 1 is returned).  Each CTA has a region
     // of the list; where one does not suffice they are sent again, packed.  The area of maxima, bins and stage is free.
     bool packed = false;
-    // The entries are `floor` or more, and `pick` takes them; whole groups below it are passed over.
+    // The entries are `floor` or more, and `pick` takes them; threads whose largest entry is below it have none (256 rows of
+    // 131072 fp32 with probabilities, whose rows the L2 does not hold for a second read: 71 -> 64 us), other threads' groups
+    // below it are passed over.
     auto collect = [&](float floor, auto pick) {
         __syncthreads();
-        sl.each_group([&](const uint4& r, int v) {
+        if (top_own >= floor) sl.each_group([&](const uint4& r, int v) {
             float x[kGroup];
             Slice<E, kStaged, kDepth>::unpack(r, x);
             float most = x[0];
@@ -1513,15 +1517,13 @@ extern "C" dsa_status dsa_sample_tokens(const void* logits, int64_t ld, int32_t 
     const bool staged = top_k == nullptr || R * static_cast<int64_t>(ctas) <= slots;
     if (!staged) {
         // A CTA takes about as long as 16384 entries for what it does besides reading: as many CTAs a row as make the least of
-        // that times the waves.  Not slices whose sum the L2 does not hold, which would be read twice from DRAM (400 rows of
-        // 131072 fp32 with probabilities on four CTAs 104 us, two 119), nor one CTA for fp32, where a thread keeps two
-        // maxima, not four (registers: 256 x 131072 with probabilities 72 -> 74).  With this rule instead of eight CTAs a row:
-        // 300 rows of 131072 bf16 65 -> 34 us, 300 of 32000 33 -> 21, 512 of 16000 54 -> 23, 100 of 131072 fp32 29 -> 22
+        // that times the waves, but not one for fp32, where a thread keeps two maxima, not four (registers: 256 x 131072 with
+        // probabilities 2 us more).  With this rule instead of eight CTAs a row: 300 rows of 131072 bf16 65 -> 34 us, 300 of
+        // 32000 33 -> 21, 512 of 16000 54 -> 23, 200 of 131072 fp32 with probabilities 61 -> 52, 100 without 29 -> 21
         int64_t best = INT64_MAX;
         const int most = ctas;
         for (int c = most; c >= std::min(most, bf16 ? 1 : 2); c /= 2) {
             const int64_t part = (V + c - 1) / c, time = (R * static_cast<int64_t>(c) + slots - 1) / slots * (16384 + part);
-            if (c < most && part * static_cast<int64_t>(align) > 160 * 1024) break;
             if (time < best) {
                 best = time;
                 ctas = c;
