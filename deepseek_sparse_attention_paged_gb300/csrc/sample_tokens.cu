@@ -24,9 +24,9 @@
 //   * where more entries than fit (2048) come together (ties, a temperature far above 1), or for a larger top-k:
 //     bisection over the 32 bits of z, a pass over the slices each.
 //
-// Measured (calls in a captured graph): one row of 32000 (bf16) with top-k 50 and top-p 8.2 us, 64 of 131072 (fp32) with
+// Measured (calls in a captured graph): one row of 32000 (bf16) with top-k 50 and top-p 8.5 us, 64 of 131072 (fp32) with
 // top-k, top-p and min-p, a setting each, 49 us, 300 of 100003 (bf16) with top-p alone 84 us, 256 of 131072 (fp32) with top-k 50
-// and the probabilities written 66 us: 268 MB at 4.1 TB/s.  Bound: a few rows by the cluster's exchanges (launch, maxima, list,
+// and the probabilities written 64 us: 268 MB at 4.2 TB/s.  Bound: a few rows by the cluster's exchanges (launch, maxima, list,
 // sums: about 1.2 us each) and by the slowest of eight CTAs; many rows with a top-k by the memory while all CTAs read and
 // by latency while all select; top-p alone by forming a weight of 30 bits per entry (about 20 integer instructions) and by
 // shared-memory atomics for the bins.
@@ -43,6 +43,7 @@ namespace {
 
 constexpr int kMaxCtas = 8;
 constexpr int kList = 2048;                    // entries that the first CTA takes in
+constexpr int kMaxima = 2048;                  // that bound the k-th largest entry from below
 constexpr int kFew = 128;                      // entries that are compared with one another
 constexpr int kMaxTopK = 1024;
 constexpr int kBins = 1024, kBinsPerOctave = 32;
@@ -103,7 +104,7 @@ struct alignas(16) SampleShared {
     static constexpr int kStage = kBins;                       // (8 KB)
     static_assert(kStage >= 2 * kFew && kStage <= kList, "scratch");
     union {
-        float maxima[kMaxCtas * NT / 2];       // every thread's largest entry, of all CTAs (of eight: every two threads')
+        float maxima[NT == 1024 ? kMaxCtas * NT / 2 : kMaxima];   // of all CTAs (one of 1024 threads has its counts here)
         uint2 hist[kBins];                     // masses (low and high word)
         uint64_t stage[kStage];                // entries of this CTA on their way to the first one
         struct {
@@ -403,7 +404,7 @@ struct Slice {
     template <int kParts, typename F>
     __device__ __forceinline__ void take_in(float (&top)[kParts], F f) const {
         constexpr int kLoads = kDepth;
-        static_assert(kLoads % kParts == 0, "parts");
+        static_assert(kGroup % kParts == 0, "parts");
 #pragma unroll
         for (int i = 0; i < kParts; ++i) top[i] = -INFINITY;
         for (int g = g0 + lane; g < g1; g += 32 * kLoads) {
@@ -428,7 +429,7 @@ struct Slice {
                         data[g + 32 * i] = make_uint4(w[0], w[1], w[2], w[3]);
                     }
 #pragma unroll
-                    for (int e = 0; e < kGroup; ++e) top[i % kParts] = fmaxf(top[i % kParts], x[e]);
+                    for (int e = 0; e < kGroup; ++e) top[e % kParts] = fmaxf(top[e % kParts], x[e]);
                 }
         }
 #pragma unroll
@@ -606,11 +607,13 @@ __global__ void __launch_bounds__(NT, (kStaged ? 1024 : 2048) / NT) sample_token
     const float u = __ldg(a.u + row);
     const bool greedy = !(temperature > 0.0f);
     const bool use_k = !kTable && k_in > 0 && k_in < a.V, use_p = p_in < 1.0f, use_m = m_in > 0.0f;
-    // maxima that bound the k-th largest entry: of every thread, of two where there are many, of parts of a thread's entries where
-    // a row has few CTAs
-    constexpr int kParts = kStaged || kTable ? 1 : (sizeof(E) == 4 ? 2 : 4);
-    const int num_maxima = C > 4 ? C * NT / 2 : C * NT * max(1, min(kParts, 4 / C));
-    const bool by_list = use_k && k_in <= min(kMaxTopK, num_maxima / 2);
+    // Maxima that bound the k-th largest entry, 2048, or 1024 where they do for few threads (one row of 32000 9.0 -> 8.5 us): of
+    // every thread, of two where the row has more threads, of parts of a thread's entries where it has fewer
+    constexpr int kParts = kTable ? 1 : (kStaged ? (NT == 256 ? 4 : 1) : (sizeof(E) == 4 ? 2 : 4));
+    const int up_to = NT == 256 && k_in <= kMaxima / 4 ? kMaxima / 2 : kMaxima;
+    const int threads = C * NT, parts = threads >= up_to ? 1 : min(kParts, up_to / threads);
+    const int num_maxima = min(up_to, threads * parts);
+    const bool by_list = use_k && k_in <= kMaxTopK && (k_in <= num_maxima / 2 || a.V <= kList);
 
     // ---- the slice
     const E* logits = static_cast<const E*>(a.logits) + static_cast<int64_t>(row) * a.ld;
@@ -654,7 +657,8 @@ __global__ void __launch_bounds__(NT, (kStaged ? 1024 : 2048) / NT) sample_token
         if (tid == 0) s.stage_count = 0;
         __syncthreads();
     }
-    float top_part[kParts];
+    constexpr int kTracked = kStaged ? 1 : kParts;           // (a slice in shared memory is looked at again where parts are wanted)
+    float top_part[kTracked];
     sl.take_in(top_part, [&](const uint4& r, int v) {
         if constexpr (kTable)
             if (counting)
@@ -665,7 +669,7 @@ __global__ void __launch_bounds__(NT, (kStaged ? 1024 : 2048) / NT) sample_token
     });
     float top_own = top_part[0];
 #pragma unroll
-    for (int i = 1; i < kParts; ++i) top_own = fmaxf(top_own, top_part[i]);
+    for (int i = 1; i < kTracked; ++i) top_own = fmaxf(top_own, top_part[i]);
     for (int i = tid; i < (1 << kPowBits) / 4; i += NT)
         reinterpret_cast<uint4*>(s.pow)[i] = __ldg(reinterpret_cast<const uint4*>(kPow.coarse) + i);
     if (tid == 0) {
@@ -681,18 +685,29 @@ __global__ void __launch_bounds__(NT, (kStaged ? 1024 : 2048) / NT) sample_token
     // ---- the largest entry
     cluster_wait();
     if (by_list && !greedy) {
-        const float two = fmaxf(top_own, __shfl_xor_sync(0xffffffffu, top_own, 1));
-        if (kParts > 1 && C < 4) {
-            const int used = min(kParts, 4 / C);
+        if (threads > up_to) {
+            const float two = fmaxf(top_own, __shfl_xor_sync(0xffffffffu, top_own, 1));
+            if ((tid & 1) == 0)
+                for (int c = 0; c < C; ++c) put(&s.maxima[(rank * NT + tid) / 2], c, __float_as_uint(two));
+        } else if (parts == 1) {
+            for (int c = 0; c < C; ++c) put(&s.maxima[rank * NT + tid], c, __float_as_uint(top_own));
+        } else {
+            float top_of[kParts];
+#pragma unroll
+            for (int i = 0; i < kParts; ++i) top_of[i] = kStaged ? -INFINITY : top_part[i % kTracked];
+            if constexpr (kStaged)
+                sl.each_group([&](const uint4& r, int) {
+                    float x[kGroup];
+                    Slice<E, kStaged, kDepth>::unpack(r, x);
+#pragma unroll
+                    for (int e = 0; e < kGroup; ++e) top_of[e % kParts] = fmaxf(top_of[e % kParts], x[e]);
+                });
 #pragma unroll
             for (int i = 0; i < kParts; ++i) {
-                const float part = used == kParts ? top_part[i] : fmaxf(top_part[i], top_part[(i + 2) % kParts]);
-                for (int c = 0; c < C && i < used; ++c) put(&s.maxima[(rank * used + i) * NT + tid], c, __float_as_uint(part));
+                const float part = parts == kParts ? top_of[i] : fmaxf(top_of[i], top_of[(i + 2) % kParts]);
+                for (int c = 0; c < C && i < parts; ++c) put(&s.maxima[(rank * parts + i) * NT + tid], c, __float_as_uint(part));
             }
-        } else if (C <= 4)
-            for (int c = 0; c < C; ++c) put(&s.maxima[rank * NT + tid], c, __float_as_uint(top_own));
-        else if ((tid & 1) == 0)
-            for (int c = 0; c < C; ++c) put(&s.maxima[(rank * NT + tid) / 2], c, __float_as_uint(two));
+        }
     }
     {
         const float m = warp_max(top_own);
@@ -842,14 +857,14 @@ __global__ void __launch_bounds__(NT, (kStaged ? 1024 : 2048) / NT) sample_token
     if constexpr (!kTable) if (by_list) {
         // ---- a bound that at least k entries reach: the k-th largest of the maxima, or a little less, by 256
         // bins of their range in turn
-        constexpr int kKeys = kMaxCtas / 2;
+        constexpr int kKeys = kMaxima / NT;
         uint32_t key[kKeys];
         const uint32_t none = order_key(-INFINITY);
         uint32_t least = 0xffffffffu, finite = 0;
 #pragma unroll
         for (int c = 0; c < kKeys; ++c) {
             key[c] = c * NT + tid < num_maxima ? order_key(s.maxima[c * NT + tid]) : none;
-            if (key[c] != none) {
+            if (c * NT < num_maxima && key[c] != none) {
                 least = min(least, key[c]);
                 ++finite;
             }
@@ -875,7 +890,7 @@ __global__ void __launch_bounds__(NT, (kStaged ? 1024 : 2048) / NT) sample_token
             for (;;) {
 #pragma unroll
                 for (int c = 0; c < kKeys; ++c)
-                    if (key[c] != none && key[c] - lo <= range) atomicAdd(&s.sel_count[(key[c] - lo) >> shift], 1u);
+                    if (c * NT < num_maxima && key[c] != none && key[c] - lo <= range) atomicAdd(&s.sel_count[(key[c] - lo) >> shift], 1u);
                 __syncthreads();
                 uint32_t m[8], own = 0;                      // every warp: 8 bins a lane, the largest first
 #pragma unroll
@@ -1510,20 +1525,22 @@ extern "C" dsa_status dsa_sample_tokens(const void* logits, int64_t ld, int32_t 
     // 16000 93 -> 51 us, 160 of 32000 31 -> 19; top-p alone: 512 of 16000 174 -> 121, but 120 of 32000 64 -> 77)
     const int64_t enough = (top_k != nullptr ? 4 : 8) * static_cast<int64_t>(device_sm_count());
     if (ctas == 8 && R * static_cast<int64_t>(ctas) > enough && V <= 8 * 8192) ctas = 4;
-    // Staged unless most of the work is rows with a top-k, read twice, and there are enough of them to fill the GPU several
+    // Staged unless most of the work is rows with a top-k, and there are enough of them to fill the GPU several
     // times: then more CTAs an SM count for more (256 rows of 131072 with k = 50 and probabilities 134 -> 100 us; 64 rows of
     // mixed settings 53 -> 63, 300 with top-p alone 268 -> 361)
     const int64_t slots = 4 * static_cast<int64_t>(device_sm_count());
     const bool staged = top_k == nullptr || R * static_cast<int64_t>(ctas) <= slots;
     if (!staged) {
         // A CTA takes about as long as 16384 entries for what it does besides reading: as many CTAs a row as make the least of
-        // that times the waves, but not one for fp32, where a thread keeps two maxima, not four (registers: 256 x 131072 with
-        // probabilities 2 us more).  With this rule instead of eight CTAs a row: 300 rows of 131072 bf16 65 -> 34 us, 300 of
-        // 32000 33 -> 21, 512 of 16000 54 -> 23, 200 of 131072 fp32 with probabilities 61 -> 52, 100 without 29 -> 21
+        // that times the waves.  Not more than 32768 entries for one: rows without a top-k go over them several times (300 rows
+        // of 131072 bf16, k = 50: four CTAs a row 43 us, two 34, but with a setting each 111 and 203).  Not one for fp32, where
+        // a thread keeps two maxima (registers).  With this rule instead of eight CTAs a row: 300 rows of 131072 bf16 65 -> 43
+        // us, with a setting each 131 -> 111, 300 of 32000 33 -> 21, 512 of 16000 54 -> 23, with a setting each 112 -> 84
         int64_t best = INT64_MAX;
         const int most = ctas;
         for (int c = most; c >= std::min(most, bf16 ? 1 : 2); c /= 2) {
             const int64_t part = (V + c - 1) / c, time = (R * static_cast<int64_t>(c) + slots - 1) / slots * (16384 + part);
+            if (c < most && part > 32768) break;
             if (time < best) {
                 best = time;
                 ctas = c;
