@@ -672,7 +672,8 @@ dsa_status dsa_dense_mla_decode(const void* q_bf16, const void* kv_pool, int64_t
  *   request's row of the block table.  A request of a group sees no more than its own length of the prefix, and what
  *   none of them sees is not read.
  *   Requests outside all groups have nothing in common with others.
- *   An infinite or NaN value in a shared prefix, at a position that a row of the group sees, may reach the others.
+ *   An infinite or NaN value in a shared prefix, at a position that a row of the group sees, may reach the others of
+ *   the group; one behind the prefix reaches rows of its own request only.
  * Arguments: as dsa_dense_mla_decode, and
  *   cu_group       int32 [G + 1], not falling, within [0, B].   shared_lens int32 [G].   Nullable when G = 0.
  *                  G at most 8192; T * H at most 2^22, T * max_pages < 2^30.

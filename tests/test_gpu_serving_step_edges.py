@@ -1,0 +1,64 @@
+"""GPU tests of the calls around a serving step where requests could reach one another or a setting leaves the usual range.
+Bounds as in test_gpu_serving_step."""
+import math
+
+import pytest
+import torch
+
+import dense_mla_ref
+from deepseek_sparse_attention_paged_gb300 import capi
+from test_gpu_serving_step import SCALE, _cum, _run_shared, _shared_inputs
+
+pytestmark = pytest.mark.gpu
+
+
+# ---------------------------------------------------------------- shared prefixes
+
+def _poison(inp, bad, value, dims):
+    """`value` in one visible row of the last page that each request of `bad` has for itself."""
+    q, pool, table, lens, q_lens, cu_group, shared = inp
+    pool = pool.clone()
+    for b in bad:
+        at = lens[b] - 1 - q_lens[b]                     # seen by every query token of the request
+        page = int(table[b, at // 64])
+        assert at >= 0 and int((table == page).sum()) == 1
+        pool[page, at % 64, dims] = value
+    return q, pool, table, lens, q_lens, cu_group, shared
+
+
+def _check_others(inp, bad, **kw):
+    out, lse, err = _run_shared(inp, **kw)
+    q, pool, table, lens, q_lens, _, _ = inp
+    want = dense_mla_ref.decode(q.cuda(), pool.cuda(), table.cuda(), lens, q_lens, SCALE)
+    cu = _cum(q_lens)
+    rows = [r for b in range(len(lens)) if b not in bad for r in range(cu[b], cu[b + 1])]
+    dense_mla_ref.check(out[rows], lse[rows], tuple(x[rows] for x in want))
+    assert err == 0
+    for b in bad:
+        assert not bool(torch.isfinite(out[cu[b]:cu[b + 1]].float()).all(-1).any()), b
+
+
+@pytest.mark.parametrize("value,dims", [(math.nan, slice(0, 576)), (math.inf, slice(100, 101)), (-math.inf, slice(500, 512))])
+@pytest.mark.parametrize("groups,H", [
+    ([(192, [(20 + 37 * i, 1 + i % 2) for i in range(20)])], 16),                    # units of 16 tokens
+    ([(64 * 41, [(10 + 3 * i, 1) for i in range(32)]), (64, [(5 + i, 2) for i in range(3)])], 16),   # odd pages: split tiles
+    ([(0, [(700 + 64 * i, 1) for i in range(16)])], 16),                             # no prefix: pieces that begin in own pages
+    ([(128, [(100, 2), (200, 1), (65, 3), (30, 1)])], 32),
+    ([(6400, [(2000 + i, 1) for i in range(8)])], 64),
+    ([(1024, [(70, 1), (400, 1), (90, 2), (3, 1)])], 128),
+])
+def test_shared_values_of_one_request_reach_no_other(groups, H, value, dims):
+    """Infinite and NaN values that a request sees in pages of its own: the other requests of its unit, whose weights for
+    that page are 0, do not."""
+    inp = _shared_inputs(groups, H, 51)
+    bad = list(range(1, len(inp[3]), 3))
+    inp = _poison(inp, bad, value, dims)
+    _check_others(inp, bad, T=inp[0].shape[0] + 2)
+    # the same batch with nothing in common, and with the groups' borders elsewhere
+    _check_others(inp, bad, cu_group=[0], shared=[])
+
+
+def test_shared_values_reach_no_request_outside_the_groups():
+    inp = _shared_inputs([(320, [(9, 1)] * 5)], 16, 52, alone=13)
+    bad = [1, 7, 11]
+    _check_others(_poison(inp, bad, math.nan, slice(0, 576)), bad)
