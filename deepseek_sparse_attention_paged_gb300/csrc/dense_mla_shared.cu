@@ -94,9 +94,10 @@ struct Share {
     int cost;               // length of a unit in front of its tiles
 };
 
-// A piece of a share: the key tiles [t0, t1) of a unit (t0 == t1: a unit that sees nothing), and per token of the unit its
-// request, the first of that request's pages among the unit's, how many (at the request's last token, else 0), and the keys
-// it sees of the prefix and behind it.
+// A piece of a share: the key tiles [t0, t1) of a unit (t0 == t1: a unit that sees nothing), and per token of the unit the
+// request through whose row of the table the pages behind `prefix` are read (its own, but the prefix's first request where
+// the prefix goes on), the first of its own request's pages among the unit's, how many (at the request's last token, else 0),
+// and the keys it sees of the prefix and behind it.
 struct Piece {
     int q0, nq, prefix, b0, pages, t0, t1;
     int whole, first;      // the piece is its whole unit; the share's first piece
@@ -283,6 +284,7 @@ struct Walk {
     int t0, t1;
     bool whole, first;
     bool nothing;          // no piece at all
+    bool inside;           // no token sees more than a part of the prefix's next page: what lies behind is all in that page
     int at, cost;          // where in the unit's length the share is; what of that comes in front of its tiles
     Token tok;             // lane j: token j's (see Piece)
     int seg_at, seg_pages;
@@ -300,7 +302,9 @@ struct Walk {
         u.q0 = uniform(u.q0);
         u.nq = uniform(u.nq);
         u.prefix = uniform(u.prefix);
+        const int common = u.prefix;
         pages = uniform(unit_segments(bt, u, tok, seg_at, seg_pages));
+        inside = u.prefix < common;
         tiles = (pages + 1) / 2;
         // of the unit's length (what a change of units costs, then the tiles) from `at` on
         const int n = cost + schedule_tiles(pages);
@@ -1332,7 +1336,7 @@ dense_mla_shared_kernel(const __grid_constant__ Maps maps, const uint16_t* __res
             }
             Piece& p = bar.piece[i];
             if (lane < kUnitTokens) {
-                p.b[lane] = w.tok.b;
+                p.b[lane] = w.inside ? w.u.b0 : w.tok.b;
                 p.at[lane] = w.seg_at;
                 p.n[lane] = w.seg_pages;
                 p.seen[lane] = w.tok.seen;

@@ -62,3 +62,21 @@ def test_shared_values_reach_no_request_outside_the_groups():
     inp = _shared_inputs([(320, [(9, 1)] * 5)], 16, 52, alone=13)
     bad = [1, 7, 11]
     _check_others(_poison(inp, bad, math.nan, slice(0, 576)), bad)
+
+
+@pytest.mark.parametrize("H", [16, 128])
+def test_shared_prefix_is_read_through_the_first_row_where_it_is_seen_in_part(H):
+    """Requests that end inside their group's prefix, alone in their unit or with longer ones: their own entries below the
+    prefix are not read."""
+    groups = [(256, [(-1, 1), (-56, 2), (-255, 1), (-64, 1)]),                       # nobody sees the whole of the last page
+              (640, [(20 + i, 1) for i in range(16)] + [(-30, 1), (-130, 3), (-577, 1)]),     # the short ones in a unit of their own
+              (128, [(-70, 1), (5, 1), (-1, 1)])]
+    inp = list(_shared_inputs(groups, H, 53))
+    want = dense_mla_ref.decode(inp[0].cuda(), inp[1].cuda(), inp[2].cuda(), inp[3], inp[4], SCALE)
+    inp[2], b = inp[2].clone(), 0
+    for prefix, reqs in groups:
+        inp[2][b + 1:b + len(reqs), :prefix // 64] = -7
+        b += len(reqs)
+    out, lse, err = _run_shared(tuple(inp))
+    dense_mla_ref.check(out, lse, want)
+    assert err == 0
