@@ -1446,6 +1446,9 @@ extern "C" dsa_status dsa_dense_mla_decode_shared(const void* q_bf16, const void
     // one list of all units lies in shared memory; key tiles are counted in 32 bits, and a unit has up to 16 requests'
     if (static_cast<int64_t>(T) * H > static_cast<int64_t>(kMaxUnits) * 2 * kRows || static_cast<int64_t>(T) * max_pages >= 0x3fffffffLL)
         return DSA_ERR_UNSUPPORTED;
+    // and so are the positions of a unit: the prefix and the own pages of all its requests, rounded up to a tile
+    const int64_t unit_requests = std::min<int64_t>(std::min(T, B), 2 * kRows / H);
+    if (unit_requests * max_pages * kPage >= 0x7fffffffLL - kKeys) return DSA_ERR_UNSUPPORTED;
     if (workspace == nullptr || !aligned16(workspace) || workspace_bytes < dsa_dense_mla_decode_shared_workspace_size(T, H))
         return DSA_ERR_INVALID_ARG;
     auto encode = attn::tensor_map_encoder();

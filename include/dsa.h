@@ -676,7 +676,8 @@ dsa_status dsa_dense_mla_decode(const void* q_bf16, const void* kv_pool, int64_t
  *   the group; one behind the prefix reaches rows of its own request only.
  * Arguments: as dsa_dense_mla_decode, and
  *   cu_group       int32 [G + 1], not falling, within [0, B].   shared_lens int32 [G].   Nullable when G = 0.
- *                  G at most 8192; T * H at most 2^22, T * max_pages < 2^30.
+ *                  G at most 8192; T * H at most 2^22, T * max_pages < 2^30, min(B, T, 256 / H) * max_pages <
+ *                  2^25 - 2.
  *   workspace      dsa_dense_mla_decode_shared_workspace_size(T, H) bytes, as there.
  *   dev_err        nullable; DSA_DEVERR_PAGE_RANGE and DSA_DEVERR_TIMEOUT as dsa_dense_mla_decode,
  *                  DSA_DEVERR_INDEX_RANGE also for a range of requests that falls or leaves [0, B] (cut to it), or a
