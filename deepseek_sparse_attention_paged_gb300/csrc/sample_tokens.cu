@@ -679,8 +679,10 @@ __global__ void __launch_bounds__(NT, (kStaged ? 1024 : 2048) / NT) sample_token
         s.rh = r < FLT_MAX ? static_cast<float>(r) : FLT_MAX;
         s.rl = r < FLT_MAX ? static_cast<float>(r - static_cast<double>(s.rh)) : 0.0f;
     }
-    // by one thread: the fp64 unit is slow (by all of them 5 us)
-    if (use_m && tid == 32) s.t_ln_min = static_cast<double>(temperature) * log(static_cast<double>(fminf(m_in, 1.0f)));
+    // by one thread: the fp64 unit is slow (by all of them 5 us).  At an infinite temperature all weights are 1, which no
+    // min-p is above (infinity times the logarithm of 1 would be NaN)
+    if (use_m && tid == 32)
+        s.t_ln_min = temperature < INFINITY ? static_cast<double>(temperature) * log(static_cast<double>(fminf(m_in, 1.0f))) : -INFINITY;
 
     // ---- the largest entry
     cluster_wait();

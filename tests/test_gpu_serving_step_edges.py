@@ -2,12 +2,15 @@
 Bounds as in test_gpu_serving_step."""
 import math
 
+import numpy as np
 import pytest
 import torch
 
 import dense_mla_ref
+import serving_step_ref as ref
 from deepseek_sparse_attention_paged_gb300 import capi
-from test_gpu_serving_step import SCALE, _cum, _run_shared, _shared_inputs
+from test_gpu_serving_step import (SCALE, _check_sample, _cum, _logits, _run_sample, _run_shared,
+                                   _shared_inputs)
 
 pytestmark = pytest.mark.gpu
 
@@ -79,4 +82,27 @@ def test_shared_prefix_is_read_through_the_first_row_where_it_is_seen_in_part(H)
         b += len(reqs)
     out, lse, err = _run_shared(tuple(inp))
     dense_mla_ref.check(out, lse, want)
+    assert err == 0
+
+
+# ---------------------------------------------------------------- sampling
+
+@pytest.mark.parametrize("V,R,bf16", [(700, 6, False), (3000, 6, False), (3001, 6, True), (40001, 5, False), (2500, 80, True)])
+def test_sample_min_p_at_an_infinite_temperature(V, R, bf16):
+    """All weights are 1: every min-p keeps everything that is finite."""
+    x = _logits(R, V, 60 + V, bf16)
+    u = torch.rand(R, generator=torch.Generator().manual_seed(V)).tolist()
+    hot = [math.inf] * R
+    for m in (1.0, 5.0, math.inf, 0.5):
+        _check_sample(x, V, u, temperature=hot, min_p=[m] * R)
+        _check_sample(x, V, u, temperature=hot, min_p=[m] * R, top_k=[7] * R)
+    # top-p of equal weights, exact on both sides: the first half in the order of z, rounded up
+    got, p, err = _run_sample(x, V, u, hot, None, [0.5] * R, [1.0] * R)
+    n = (V + 1) // 2
+    for r in range(R):
+        kept = np.sort(np.argsort(-x[r, :V].double().numpy(), kind="stable")[:n])
+        want = np.zeros(V)
+        want[kept] = 1.0 / n
+        assert got[r] == kept[math.floor(float(np.float32(u[r])) * n)]
+        assert np.all(np.abs(p[r] - want) <= ref.round_probs_bound(want))
     assert err == 0
