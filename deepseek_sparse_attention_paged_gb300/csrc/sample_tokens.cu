@@ -676,7 +676,9 @@ __global__ void __launch_bounds__(NT, (kStaged ? 1024 : 2048) / NT) sample_token
         if (!counting) s.stage_count = 0;
         s.found = 0x7fffffff;
         const double r = 1024.0 * 1.4426950408889634074 / static_cast<double>(temperature);
-        s.rh = r < FLT_MAX ? static_cast<float>(r) : FLT_MAX;
+        // (an infinite temperature: the smallest number, as 0 times the -infinity of masked entries, and of the places beside
+        // the slice, would be NaN, whose bits say nothing of its size; weights of finite entries are 1 all the same)
+        s.rh = r < FLT_MAX ? fmaxf(static_cast<float>(r), 0x1p-149f) : FLT_MAX;
         s.rl = r < FLT_MAX ? static_cast<float>(r - static_cast<double>(s.rh)) : 0.0f;
     }
     // by one thread: the fp64 unit is slow (by all of them 5 us).  At an infinite temperature all weights are 1, which no

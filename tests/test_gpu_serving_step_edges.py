@@ -106,3 +106,20 @@ def test_sample_min_p_at_an_infinite_temperature(V, R, bf16):
         assert got[r] == kept[math.floor(float(np.float32(u[r])) * n)]
         assert np.all(np.abs(p[r] - want) <= ref.round_probs_bound(want))
     assert err == 0
+
+
+@pytest.mark.parametrize("V,R,bf16", [(7, 5, True), (701, 6, False), (3001, 6, False), (3002, 6, True), (40001, 5, False), (2501, 80, True),
+                                      (9001, 300, False)])
+def test_sample_masked_rows_at_an_infinite_temperature(V, R, bf16):
+    """Masked entries and the places beside a row, which lies on any alignment, have no weight; all others have the same."""
+    g = torch.Generator().manual_seed(V)
+    x = _logits(R, V, 70 + V, bf16, 2)
+    off = torch.rand(R, V + 2, generator=g) < torch.tensor([0.3, 0.99])[torch.arange(R) % 2][:, None]
+    off[:, 3] = False
+    x[off] = -math.inf
+    x[2, 4:6] = math.nan
+    u = torch.rand(R, generator=g).tolist()
+    hot = [math.inf] * R
+    for kw in ({}, {"top_k": [40] * R}, {"top_p": [0.9] * R}, {"top_k": [V // 2] * R, "top_p": [0.9] * R}, {"min_p": [0.1] * R}):
+        for at in (0, 1, 2):
+            _check_sample(x[:, at:], V, u, temperature=hot, **kw)
