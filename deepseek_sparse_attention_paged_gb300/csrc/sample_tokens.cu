@@ -1571,6 +1571,7 @@ extern "C" dsa_status dsa_sample_tokens(const void* logits, int64_t ld, int32_t 
         threads = 1024;
         ctas = a.ctas = 1;
         a.slice = (V + 7) / 8 * 8;
+        a.region = kList;
         smem = sizeof(SampleShared<1024>) + kValueBins * sizeof(uint64_t);
     }
     // (the same limit in every call: another thread's may come between this and the launch)

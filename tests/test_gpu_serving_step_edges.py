@@ -123,3 +123,20 @@ def test_sample_masked_rows_at_an_infinite_temperature(V, R, bf16):
     for kw in ({}, {"top_k": [40] * R}, {"top_p": [0.9] * R}, {"top_k": [V // 2] * R, "top_p": [0.9] * R}, {"min_p": [0.1] * R}):
         for at in (0, 1, 2):
             _check_sample(x[:, at:], V, u, temperature=hot, **kw)
+
+
+@pytest.mark.parametrize("n", [200, 1000, 1300, 2048, 2300])
+def test_sample_border_in_a_bin_of_many_entries(n):
+    """A CTA a row, the border among n numbers next to 0, or among n equal ones in a bin of the masses: up to 2048 come
+    into the list whole."""
+    R, V = 80, 20003
+    g = torch.Generator().manual_seed(n)
+    small = (torch.arange(n) % 250 + 1).float() * 2.0 ** -18 * (1 - 2 * (torch.arange(n) % 2))
+    x = torch.full((R, V), -60.0)
+    for r in range(R):
+        x[r, torch.randperm(V, generator=g)[:n]] = small
+    x[:, 11] = 3.0
+    x = x.to(torch.bfloat16)
+    u = torch.rand(R, generator=g).tolist()
+    _check_sample(x, V, u, top_p=[0.3, 0.7] * (R // 2), probs=False)
+    _check_sample(x + 150.0, V, u, top_p=[0.6] * R)              # past the values with bins of their own: masses
