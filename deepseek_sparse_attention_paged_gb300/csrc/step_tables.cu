@@ -190,7 +190,12 @@ __global__ void __launch_bounds__(kTabThreads) step_tables_kernel(const StepTabl
     for (uint32_t i = first; i < n_give; i += stride) {
         const int b = owner(given, i), c = mapped(s, b);
         const int64_t top = static_cast<int64_t>(have0) + i;
-        if (top < s.num_pages) s.free_pages[top] = s.table[static_cast<int64_t>(b) * s.max_pages + kept(s, b, c) + (i - given[b])];
+        int page = s.table[static_cast<int64_t>(b) * s.max_pages + kept(s, b, c) + (i - given[b])];
+        if (page < 0 || page >= s.num_pages) {   // no page: the entry keeps its place, which the sums have given it
+            bad |= DSA_DEVERR_PAGE_RANGE;
+            page = -1;
+        }
+        if (top < s.num_pages) s.free_pages[top] = page;
     }
     // ---- lengths and counts, a request a thread
     for (int b = blockIdx.x * kTabThreads + tid; b < s.B; b += gridDim.x * kTabThreads) {

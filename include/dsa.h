@@ -781,7 +781,8 @@ dsa_status dsa_sample_tokens(const void* logits, int64_t ld, int32_t V, int32_t 
  *   to [0, num_pages].
  *   dev_err          nullable; DSA_DEVERR_NO_PAGE when the stack runs out (table entries -1 that are not counted,
  *                    slots -1), DSA_DEVERR_PAGE_RANGE for a page id outside [0, num_pages) in the table or on the
- *                    stack (the entry -1, slots -1), DSA_DEVERR_INDEX_RANGE for rows that were cut, tokens past
+ *                    stack where the call reads it: for a new token (slot -1), taken (the table's entry -1, slots
+ *                    -1) or given back (the stack's entry -1), DSA_DEVERR_INDEX_RANGE for rows that were cut, tokens past
  *                    max_pages * 64 (slot -1) or a stack that would pass num_pages entries (cut).
  */
 dsa_status dsa_step_tables(const int32_t* cached_lens, const int32_t* q_lens, const int32_t* page_counts,

@@ -10,7 +10,7 @@ import dense_mla_ref
 import serving_step_ref as ref
 from deepseek_sparse_attention_paged_gb300 import capi
 from test_gpu_serving_step import (SCALE, _check_sample, _cum, _logits, _run_sample, _run_shared,
-                                   _shared_inputs)
+                                   _run_tables, _shared_inputs)
 
 pytestmark = pytest.mark.gpu
 
@@ -140,3 +140,25 @@ def test_sample_border_in_a_bin_of_many_entries(n):
     u = torch.rand(R, generator=g).tolist()
     _check_sample(x, V, u, top_p=[0.3, 0.7] * (R // 2), probs=False)
     _check_sample(x + 150.0, V, u, top_p=[0.6] * R)              # past the values with bins of their own: masses
+
+
+# ---------------------------------------------------------------- step tables
+
+def test_tables_report_bad_pages_that_are_given_back():
+    """Ids that are no pages in the rows of requests that end: said in that call, -1 on the stack; those that the request
+    does not own, or that are not mapped, are not looked at."""
+    table = [[3, 99, 5, 1000], [-1, 7, -5, 2], [0, 1, 4, 6]]
+    stack = [8, 9] + [-1] * 8
+    got = _run_tables([200, 140, 100], [-1, -1, 10], [3, 3, 2], [0, 1, 0], table, 10, stack, 2, 12)
+    assert got == ([0, 0, 110], [0, 0, 2], 7, [0, 0, 0, 10], list(range(100, 110)) + [0, 0],
+                   [64 + p % 64 for p in range(100, 110)] + [-1, -1], capi.DSA_DEVERR_PAGE_RANGE)
+    assert stack == [8, 9, 3, -1, 5, 7, -1, -1, -1, -1]
+    assert table == [[3, 99, 5, 1000], [-1, 7, -5, 2], [0, 1, 4, 6]]
+    # outside of what is given back: no error
+    stack = [8, 9] + [-1] * 8
+    got = _run_tables([200, 140, 100], [-1, -1, 10], [1, 2, 2], [0, 1, 0], table, 10, stack, 2, 10)
+    assert got[-1] == 0 and got[2] == 4 and stack[:4] == [8, 9, 3, 7]
+    # taken again in the same call: the request that gets the entry has no page there
+    table = [[99, 2], [0, -1]]
+    got = _run_tables([100, 64], [-1, 1], [2, 1], None, table, 10, [-1] * 10, 0, 1)
+    assert got == ([0, 65], [0, 2], 1, [0, 0, 1], [64], [2 * 64], capi.DSA_DEVERR_PAGE_RANGE) and table[1] == [0, 2]
