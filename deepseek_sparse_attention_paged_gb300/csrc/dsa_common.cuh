@@ -167,6 +167,12 @@ __device__ __forceinline__ void i8x4_to_f16x4(uint32_t w, uint32_t& lo, uint32_t
 
 inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
+// Two arrays (of na and nb bytes; NULL: none) have memory in common.
+inline bool overlap(const void* a, size_t na, const void* b, size_t nb) {
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+    return a != nullptr && b != nullptr && na > 0 && nb > 0 && x < y + nb && y < x + na;
+}
+
 // Multiprocessor count of the current device (the launch heuristics size grids by it); `fallback`
 // when no device can be queried (a size query made without a GPU).
 inline int device_sm_count(int fallback = 152) {

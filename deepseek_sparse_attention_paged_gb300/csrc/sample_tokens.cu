@@ -1517,12 +1517,15 @@ extern "C" dsa_status dsa_sample_tokens(const void* logits, int64_t ld, int32_t 
     if (!logits || !u || !tokens || ld < V || (probs != nullptr && ld_probs < V)) return DSA_ERR_INVALID_ARG;
     const uintptr_t align = bf16 ? 2 : 4;
     if (reinterpret_cast<uintptr_t>(logits) % align != 0 || reinterpret_cast<uintptr_t>(probs) % 4 != 0) return DSA_ERR_INVALID_ARG;
-    // the probabilities may not lie over the logits: a CTA writes its own while others still read
-    if (probs != nullptr) {
-        const uintptr_t x = reinterpret_cast<uintptr_t>(logits), y = reinterpret_cast<uintptr_t>(probs);
-        const uintptr_t nx = (static_cast<uintptr_t>(R - 1) * ld + V) * align, ny = (static_cast<uintptr_t>(R - 1) * ld_probs + V) * 4;
-        if (x < y + ny && y < x + nx) return DSA_ERR_INVALID_ARG;
-    }
+    // the outputs may not lie over the inputs or each other: a CTA writes its own while others still read (its row's settings
+    // too, which are loaded where they are used)
+    const size_t n_logits = (static_cast<size_t>(R - 1) * ld + V) * align, n_probs = (static_cast<size_t>(R - 1) * ld_probs + V) * 4;
+    const size_t n_row = static_cast<size_t>(R) * 4;
+    if (overlap(probs, n_probs, logits, n_logits) || overlap(tokens, n_row, logits, n_logits) || overlap(tokens, n_row, probs, n_probs))
+        return DSA_ERR_INVALID_ARG;
+    for (const void* in : {static_cast<const void*>(temperature), static_cast<const void*>(top_k), static_cast<const void*>(top_p),
+                           static_cast<const void*>(min_p), static_cast<const void*>(u)})
+        if (overlap(probs, n_probs, in, n_row) || overlap(tokens, n_row, in, n_row)) return DSA_ERR_INVALID_ARG;
     int ctas = 1;
     while (ctas < kMaxCtas && V > ctas * 2048) ctas *= 2;
     // many rows: not more CTAs than need be (a top-k of up to 1024 wants four), with 8192 entries or so each (k = 50: 512 rows of

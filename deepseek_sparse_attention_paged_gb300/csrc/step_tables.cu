@@ -218,11 +218,6 @@ __global__ void __launch_bounds__(kTabThreads) step_tables_kernel(const StepTabl
     ptx::griddep_launch_dependents();
 }
 
-bool overlap(const void* a, size_t na, const void* b, size_t nb) {
-    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
-    return a != nullptr && b != nullptr && na > 0 && nb > 0 && x < y + nb && y < x + na;
-}
-
 }  // namespace
 }  // namespace dsa
 

@@ -745,7 +745,8 @@ dsa_status dsa_verify_drafts(const float* target_probs, int64_t target_ld, const
  *   temperature    fp32 [R] (NULL: 1).   top_k int32 [R] (NULL, <= 0 or >= V: all).   top_p fp32 [R] (NULL, >= 1 or
  *                  NaN: all; <= 0: the first).   min_p fp32 [R] (NULL, <= 0 or NaN: all).
  *   u              fp32 [R]: uniform numbers in [0, 1).
- *   tokens         int32 [R].   probs nullable, fp32 rows of stride ld_probs >= V, apart from logits.
+ *   tokens         int32 [R].   probs nullable, fp32 rows of stride ld_probs >= V.  Both lie apart from every input
+ *                  and from one another (first row's start to last row's end).
  *   dev_err        nullable; DSA_DEVERR_PROB for a row without a finite logit (token -1, probs 0).
  */
 dsa_status dsa_sample_tokens(const void* logits, int64_t ld, int32_t V, int32_t R, uint32_t flags,

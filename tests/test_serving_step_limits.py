@@ -2,7 +2,7 @@
 import pytest
 
 from deepseek_sparse_attention_paged_gb300 import build, capi
-from test_serving_step_host import _shared
+from test_serving_step_host import _sample, _shared
 
 INVALID, UNSUPPORTED = 1, 2
 
@@ -23,3 +23,17 @@ def test_shared_refuses_units_whose_positions_pass_32_bits(lib, H):
     # in bounds: it gets to the next check
     for kw in ({"maxp": most}, {"b": n - 1}, {"t": n - 1}):
         assert _shared(lib, **{**too_many, **kw}, ws=None) == INVALID
+
+
+def test_sample_refuses_outputs_over_inputs_and_each_other(lib):
+    """Two rows of 1000: the first and the last bytes of each array."""
+    inputs = {"t": 0x51000, "k": 0x51100, "p": 0x51200, "m": 0x51300, "u": 0x51400}
+    for at in inputs.values():
+        for d in (-4, 0, 4):
+            assert _sample(lib, **inputs, tok=at + d) == INVALID
+        for d in (-7996, 0, 4):
+            assert _sample(lib, **inputs, pr=at + d, lg=0x900000) == INVALID
+    for d in (-4, 0, 7996):
+        assert _sample(lib, **inputs, tok=0x100000 + d) == INVALID          # logits
+        assert _sample(lib, **inputs, tok=0x900000 + d) == INVALID          # probabilities
+        assert _sample(lib, **inputs, tok=0x900000 + d, ld=1004, ldp=1004) == INVALID
