@@ -883,7 +883,8 @@ def dsa_step_tables(cached_lens: torch.Tensor, q_lens: torch.Tensor, page_counts
                     keep_pages: Optional[torch.Tensor] = None, dev_err: Optional[torch.Tensor] = None,
                     stream=None) -> None:
     """Lengths, row offsets, positions and slots of a step from cached_lens / q_lens [B] (q_lens < 0: the request
-    ends); block_table [B, max_pages] and the stack free_pages [num_pages] are updated in place."""
+    ends); block_table [B, max_pages] and the stack free_pages [num_pages] are updated in place.  B = 0 (and T = 0)
+    writes nothing, free_count_out neither: no buffers are swapped after it."""
     dev = _current_device()
     i32 = torch.int32
     ca = _arr(cached_lens, i32, dev, "cached_lens")

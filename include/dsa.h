@@ -777,6 +777,8 @@ dsa_status dsa_sample_tokens(const void* logits, int64_t ld, int32_t V, int32_t 
  *   seq_lens, page_counts_out int32 [B], cu_q int32 [B + 1], positions and slot_mapping int64 [T].
  *   Every output lies apart from every input and from the other outputs (a loop swaps cached_lens with seq_lens,
  *   page_counts with page_counts_out and free_count with free_count_out from step to step).
+ *   B = 0 (T = 0 then; other T are refused): nothing is written, not free_count_out and cu_q either, so a loop does
+ *   not swap its buffers after such a call.
  *   B at most 16384, B * max_pages < 2^31, num_pages < 2^25.
  *   Lengths below 0 count as 0; counts are cut to [0, max_pages], keep_pages to [0, page_counts], *free_count
  *   to [0, num_pages].

@@ -9,7 +9,7 @@ import torch
 import dense_mla_ref
 import serving_step_ref as ref
 from deepseek_sparse_attention_paged_gb300 import capi
-from test_gpu_serving_step import (SCALE, _check_sample, _cum, _logits, _run_sample, _run_shared,
+from test_gpu_serving_step import (SCALE, _check_sample, _cum, _i32, _logits, _run_sample, _run_shared,
                                    _run_tables, _shared_inputs)
 
 pytestmark = pytest.mark.gpu
@@ -162,3 +162,16 @@ def test_tables_report_bad_pages_that_are_given_back():
     table = [[99, 2], [0, -1]]
     got = _run_tables([100, 64], [-1, 1], [2, 1], None, table, 10, [-1] * 10, 0, 1)
     assert got == ([0, 65], [0, 2], 1, [0, 0, 1], [64], [2 * 64], capi.DSA_DEVERR_PAGE_RANGE) and table[1] == [0, 2]
+
+
+def test_tables_without_requests():
+    """An empty batch: nothing is written; rows without requests are refused."""
+    stack = [3, 1, -1, -1]
+    i64 = lambda n: torch.full((n,), 7, dtype=torch.int64, device="cuda")
+    bufs = lambda: (_i32([]), _i32([]), _i32([7]), _i32([7]), i64(0), i64(0))
+    st, seq, co, ho, cu, pos, slots = _i32(stack), *bufs()
+    none, table, err = _i32([]), torch.zeros(0, 5, dtype=torch.int32, device="cuda"), _i32([0])
+    capi.dsa_step_tables(none, none, none, table, 4, st, _i32([2]), seq, co, ho, cu, pos, slots, dev_err=err)
+    assert ho.item() == 7 and cu.tolist() == [7] and st.tolist() == stack and err.item() == 0
+    with pytest.raises(capi.DSAError):
+        capi.dsa_step_tables(none, none, none, table, 4, st, _i32([2]), seq, co, ho, cu, i64(3), i64(3))
