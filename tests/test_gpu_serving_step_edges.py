@@ -142,6 +142,37 @@ def test_sample_border_in_a_bin_of_many_entries(n):
     _check_sample(x + 150.0, V, u, top_p=[0.6] * R)              # past the values with bins of their own: masses
 
 
+@pytest.mark.parametrize("mode", ["usual", "mixed", "top_p", "all"])
+@pytest.mark.parametrize("V,R,bf16,masked", [(1000, 300, True, 0.0), (1049, 373, True, 0.99), (1601, 200, False, 0.5), (2808, 150, False, 0.0),
+                                             (4005, 120, True, 0.5)])
+def test_sample_short_vocabularies(V, R, bf16, masked, mode):
+    """Rows with their largest tokens at places of their own and masks in every other row: the definition's tokens, and a
+    second call's are the first one's."""
+    g = torch.Generator().manual_seed(V)
+    x = torch.randn(R, V + 3, generator=g) * 2.0
+    top = torch.rand(R, V, generator=g).argsort(1)[:, :24]
+    x.scatter_(1, top, 7.0 + 3.0 * torch.randn(R, 24, generator=g))
+    off = torch.rand(R, V + 3, generator=g) < masked
+    off[1::2] = False
+    off.scatter_(1, top[:, :1], False)
+    x = x.masked_fill(off, -math.inf)
+    x = x.to(torch.bfloat16) if bf16 else x
+    u = torch.rand(R, generator=g).tolist()
+    pick = lambda v: [v[i] for i in torch.randint(len(v), (R,), generator=g).tolist()]
+    kw = {"temperature": (0.6 + 0.7 * torch.rand(R, generator=g)).tolist()}
+    if mode == "usual":
+        kw.update(top_k=[50] * R, top_p=[0.95] * R)
+    elif mode == "top_p":
+        kw["top_p"] = pick([0.9, 0.95, 0.99])
+    elif mode == "mixed":
+        kw.update(top_k=pick([0, 1, 20, 50, 1000]), top_p=pick([0.5, 0.9, 0.99, 1.0]), min_p=pick([0.0, 0.02, 0.1]))
+        kw["temperature"][::4] = [0.0] * len(kw["temperature"][::4])
+    for probs in (False, True):
+        _check_sample(x, V, u, probs=probs, **kw)
+    a, b = _run_sample(x, V, u, **kw), _run_sample(x, V, u, **kw)
+    assert a[0] == b[0] and np.array_equal(a[1], b[1])
+
+
 # ---------------------------------------------------------------- step tables
 
 def test_tables_report_bad_pages_that_are_given_back():
