@@ -10,8 +10,8 @@
 // but the pieces of a unit that is split.  The products with a page behind the prefix go into the rows of that page's request
 // alone: the weights of the other rows are 0 there, but 0 times an infinite or NaN value is NaN.  (Compared with products into
 // all rows: 4 requests 24.9 -> 25.2 us, 32 of 128 heads 120.3 -> 121.0, 200 behind 131008 keys 662 -> 665, others the same.)
-// Requests outside all groups make up groups without a prefix.  The key
-// tiles (128 positions = two pages) of all units in one sequence are cut into equal shares, one per cluster.
+// Requests outside all groups make up groups without a prefix.  The key tiles (128 positions = two pages) of all units in one
+// sequence are cut into equal shares, one per cluster.
 //
 // Bound: the tensor cores, 2176 FLOP a row and key, once a prefix has about 6 rows of 16 heads.  A unit is a pipeline
 // over the four CTAs of a cluster: the pair of ranks 0 and 1 forms the scores of 2 x 128 rows and their softmax, the pair
@@ -26,12 +26,12 @@
 // Behind the prefix a tile costs the same for the few rows that see it.
 //
 // Measured (calls in a captured graph; in brackets the plain call on the same batch):
-//   200 requests of 16 heads behind 131008 common keys            640 us (3780)   1.44 PFLOP/s of what is needed, 75 % of
-//                                                                                 the measured rate
-//   64 of 16 heads behind 32768, with 64 to 4096 of their own     107 us (327)
+//   200 requests of 16 heads behind 131008 common keys     650 to 665 us (3780 to 4160), 1.38 to 1.41 PFLOP/s of what is
+//                                                                 needed, 72 to 74 % of the measured rate; power
+//   64 of 16 heads behind 32768, with 64 to 4096 of their own     106 us (328)
 //   60 of 32 heads, two rows each, behind 5 of 2K to 32K           97 us (99)
-//   32 of 128 heads behind 16384                                  118 us (116)    a request fills a tile by itself
-//   4 of 16 heads behind 1024                                      24 us (21)     a chain of about 20 steps
+//   32 of 128 heads behind 16384                                  120 us (119)    a request fills a tile by itself
+//   4 of 16 heads behind 1024                                      25 us (20)     a chain of about 20 steps
 // So it is for many requests of few heads behind one long prefix; prefixes that the L2 holds cost the plain call little where
 // its own row tiles are full.  144 of 152 SMs: clusters of four do not fill a GPC whose SMs are no multiple of four.
 //

@@ -24,7 +24,7 @@
 //   * where more entries than fit (2048) come together (ties, a temperature far above 1), or for a larger top-k:
 //     bisection over the 32 bits of z, a pass over the slices each.
 //
-// Measured (calls in a captured graph): one row of 32000 (bf16) with top-k 50 and top-p 8.5 us, 64 of 131072 (fp32) with
+// Measured (calls in a captured graph): one row of 32000 (bf16) with top-k 50 and top-p 8.8 us, 64 of 131072 (fp32) with
 // top-k, top-p and min-p, a setting each, 49 us, 300 of 100003 (bf16) with top-p alone 84 us, 256 of 131072 (fp32) with top-k 50
 // and the probabilities written 64 us: 268 MB at 4.2 TB/s.  Bound: a few rows by the cluster's exchanges (launch, maxima, list,
 // sums: about 1.2 us each) and by the slowest of eight CTAs; many rows with a top-k by the memory while all CTAs read and
